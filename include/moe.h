@@ -321,6 +321,149 @@ int32_t moe_selftest_timeout(void* workspace, int32_t timeout_us, void* stream);
 int32_t moe_route_noalloc(const moe_shape* shape, const float* router_logits, int32_t* ids,
                           float* weights, int32_t* offsets, int32_t* row_of, void* stream);
 
+/* ---------------------------------------------------------------------
+ * Operators that adapt and train beside the frozen layer.  They follow the
+ * conventions above (device pointers, caller-owned memory, asynchronous on
+ * `stream`, argument errors before any CUDA call, sm_103a only) and give the
+ * same result for the same arguments on every call.
+ * ------------------------------------------------------------------- */
+
+/* Element types. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F32 1
+
+/* Low-rank adapters of many requests beside a shared projection: token t
+ * uses adapter a = adapter_ids[t] and gets scale[a] * B_a (A_a x_t) beside
+ * what the shared projection gave it.
+ * Limits: num_tokens >= 0; 1 <= num_adapters <= 1024; rank a multiple of 8
+ * in [8, 128]; in_features and out_features positive multiples of 8
+ * up to 2^20 (smaller ranks are padded with zeros). */
+typedef struct {
+  int32_t num_tokens;     /* T */
+  int32_t num_adapters;   /* NA */
+  int32_t rank;           /* r */
+  int32_t in_features;    /* H */
+  int32_t out_features;   /* N */
+  int32_t out_dtype;      /* MOE_DTYPE_*: base, out and dout */
+} moe_adapter_shape;
+
+/* Workspace bytes of moe_adapter_forward (backward = 0) or
+ * moe_adapter_backward (1).  0 for an invalid shape. */
+size_t moe_adapter_workspace_size(const moe_adapter_shape* shape, int32_t backward);
+
+/* out = base + scale_a B_a A_a x, one token a row; for prompts and for
+ * batches of single tokens.
+ *   x            bf16  [T, H], rows ld_x elements apart
+ *   adapter_ids  int32 [T]; an id outside [0, NA) means no adapter: the
+ *                token's row of x is not read and out = base
+ *   a            bf16  [NA, r, H]     b  bf16 [NA, N, r]
+ *   scale        float [NA], or NULL for 1
+ *   base         [T, N] of out_dtype, rows ld_base apart; NULL for zero; may
+ *                be out itself
+ *   out          [T, N] of out_dtype, rows ld_out apart
+ * x, a, b, base and out 16-byte aligned, row strides multiples of 8 elements
+ * and at least the row's length.  The product A_a x is held in float and
+ * enters the second product as two bf16 terms (a relative error below
+ * 2^-17). */
+int32_t moe_adapter_forward(const moe_adapter_shape* shape, const void* x, int64_t ld_x,
+                            const int32_t* adapter_ids, const void* a, const void* b,
+                            const float* scale, const void* base, int64_t ld_base, void* out,
+                            int64_t ld_out, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Gradients of moe_adapter_forward for dout (out_dtype [T, N], rows ld_dout
+ * apart):
+ *   dx  bf16  [T, H] = dx_base + A_a^T (scale_a B_a^T dout); dx_base bf16 or
+ *             NULL for zero, may be dx itself; tokens without an adapter get
+ *             dx_base.  NULL: not computed.  Not the memory of x or dout.
+ *   da  float [NA, r, H] = sum over the adapter's tokens of u x^T
+ *   db  float [NA, N, r] = scale_a * sum of dout (A_a x)^T
+ * da and db are written in full (zero for an adapter without tokens); both or
+ * neither may be NULL. */
+int32_t moe_adapter_backward(const moe_adapter_shape* shape, const void* dout, int64_t ld_dout,
+                             const void* x, int64_t ld_x, const int32_t* adapter_ids,
+                             const void* a, const void* b, const float* scale,
+                             const void* dx_base, int64_t ld_dx_base, void* dx, int64_t ld_dx,
+                             float* da, float* db, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Limits: num_tokens >= 0; 1 <= num_experts <= 1024; 1 <= top_k <=
+ * min(num_experts, 32); 1 <= num_sequences <= 2^20; coef finite. */
+typedef struct {
+  int32_t num_tokens;      /* T */
+  int32_t num_experts;     /* E */
+  int32_t top_k;           /* k */
+  int32_t num_sequences;   /* S */
+  float coef;
+} moe_balance_shape;
+
+size_t moe_balance_workspace_size(const moe_balance_shape* shape);
+
+/* Load-balance loss of the router, per-expert counts and the gradient of the
+ * logits.  Over the n_s valid tokens of sequence s, with p the softmax of
+ * the logits over all experts:
+ *   f_se = E counts_se / (k n_s),  loss = coef * mean over the sequences with
+ *   n_s > 0 of sum_e f_se * mean_t p_te     (coef when perfectly balanced)
+ *   dlogits_te = coef / (S' n_s) p_te (f_se - sum_j f_sj p_tj)
+ *   logits       float [T, E]; -inf is allowed, and a row of nothing else
+ *                has p = 0; a NaN reaches the loss and its own row
+ *   ids          int32 [T, k] the routed experts; an id outside [0, E) (a
+ *                dropped slot) is not counted
+ *   token_mask   uint8 [T], zero for padding (its logits are not read); or
+ *                NULL
+ *   seq_offsets  int32 [S + 1], ascending within [0, T]: sequence s holds the
+ *                tokens [offsets[s], offsets[s + 1]), possibly none; NULL
+ *                with S = 1 for the whole batch
+ *   weights, dweights  float [T, k], both or neither: the routing weights
+ *                (softmax over the k selected logits) and the gradient that
+ *                reached them; adds w_j (dw_j - sum_i w_i dw_i) to dlogits at
+ *                ids_j, for every token
+ *   loss         float [1]     counts int32 [S, E]
+ *   dlogits      float [T, E] written in full, or NULL
+ * num_tokens == 0 writes a zero loss and zero counts.  Sums run in float in a
+ * fixed order. */
+int32_t moe_balance_loss(const moe_balance_shape* shape, const float* logits, const int32_t* ids,
+                         const uint8_t* token_mask, const int32_t* seq_offsets,
+                         const float* weights, const float* dweights, float* loss,
+                         int32_t* counts, float* dlogits, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/* Elements of a tensor that share one scale of its 8-bit moments. */
+#define MOE_ADAMW_BLOCK 256
+
+/* One tensor of an AdamW step; all updated in place. */
+typedef struct {
+  float* param;        /* [n] */
+  const void* grad;    /* [n] of grad_dtype */
+  void* m;             /* [n] first moment: float, or E4M3 codes */
+  void* v;             /* [n] second moment: float, or E4M3 codes of its root */
+  float* m_scale;      /* 8 bits: [ceil(n / MOE_ADAMW_BLOCK)], else unused */
+  float* v_scale;
+  void* param_bf16;    /* bf16 [n], receives the rounded parameter; or NULL */
+  int64_t n;
+} moe_adamw_tensor;
+
+typedef struct {
+  double lr, beta1, beta2, eps, weight_decay;
+  int32_t step;              /* 1 for the first step */
+  int32_t state_bits;        /* 32 or 8 */
+  int32_t grad_dtype;        /* MOE_DTYPE_* */
+  int32_t reserved[2];       /* must be zero */
+  const float* grad_scale;   /* device scalar every gradient is multiplied by, or NULL */
+} moe_adamw_options;
+
+/* One AdamW step (decoupled weight decay) over `count` tensors:
+ *   m <- beta1 m + (1 - beta1) g,  v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr wd) - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps)
+ * With state_bits = 8 each block of MOE_ADAMW_BLOCK elements of m, and of
+ * sqrt(v), is kept as E4M3 codes of x * (448 / amax) and the scale
+ * amax / 448 (a block below 2^-100: scale 1, codes 0); a positive root never
+ * rounds to zero.  New moments start as zero codes and any finite scale.  A
+ * NaN or infinite gradient makes its element NaN, and with 8 bits its block.
+ * `tensors` is host memory, read before the call returns. */
+int32_t moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count,
+                       const moe_adamw_options* options, void* stream);
+
 /* Message describing the last error returned on the calling thread. */
 const char* moe_last_error(void);
 

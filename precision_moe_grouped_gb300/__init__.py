@@ -4,7 +4,10 @@ The compute path is libmoe.so (csrc/, C ABI in include/moe.h): hand-written
 sm_103a CUDA kernels for routing, the expert-sorted scatter with per-token
 FP8 quantisation, two tcgen05 block-scaled grouped GEMMs (SwiGLU and the
 token scale fused in GEMM1's epilogue), the FP8 quantisation of h and the
-top-k combine.  This package only marshals torch tensors into that ABI.
+top-k combine.  Beside the forward: low-rank adapters of many requests
+(LowRankAdapters), the router's balance loss (BalanceLoss) and the AdamW step
+(AdamW), for adapting a frozen layer.  This package only marshals torch
+tensors into that ABI.
 """
 from __future__ import annotations
 
@@ -13,8 +16,9 @@ from ._lib import (MOE_W4A8_MXFP4_FP8, MOE_W4A16_MXFP4_BF16, MOE_W8A8_MXFP8, Moe
                    MoeOptions, MoeShape, WsLayout, forward, forward_host, forward_host_steps,
                    load, options, prepare_weights, read_device_status, selftest_timeout, shape,
                    steps_workspace_size, workspace_layout, workspace_size)
+from ._adapt import AdamW, BalanceLoss, LowRankAdapters
 
-__all__ = ["FusedMoE", "MoeError", "MoeOptions", "MoeShape", "WsLayout", "forward",
+__all__ = ["AdamW", "BalanceLoss", "FusedMoE", "LowRankAdapters", "MoeError", "MoeOptions", "MoeShape", "WsLayout", "forward",
            "forward_host", "forward_host_steps", "load", "options", "prepare_weights",
            "read_device_status", "selftest_timeout", "shape", "steps_workspace_size",
            "workspace_layout", "workspace_size",
@@ -64,6 +68,15 @@ class FusedMoE:
         forward(self.shape(T), x, logits, self.w1_p, self.w1_sf_p, self.w2_p, self.w2_sf_p, out,
                 ws, self.mode, opts)
         return out
+
+    def routing(self, T: int):
+        """(ids int32 [T, k], weights float32 [T, k]) of the last forward of T
+        tokens: views of the workspace, valid until the next forward."""
+        import torch
+        lay, n = workspace_layout(self.shape(T), self.mode), T * self.top_k * 4
+        ws = self.workspace(T)
+        ids = ws[lay.ids:lay.ids + n].view(torch.int32).view(T, self.top_k)
+        return ids, ws[lay.weights:lay.weights + n].view(torch.float32).view(T, self.top_k)
 
     def host_steps(self, xs, logits, outs=None, opts: MoeOptions | None = None):
         """Forwards of host (CPU) tensors xs[i] [T, H] bf16 and logits[i]

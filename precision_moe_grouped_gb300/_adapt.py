@@ -1,0 +1,319 @@
+"""Adapting a frozen layer: low-rank adapters, the router's balance loss and
+the AdamW step, over the C ABI (include/moe.h).
+
+As in _lib, every tensor is checked (placement, device, dtype, shape, layout)
+before the library sees its address, and a bad one raises MoeError.  Calls
+run on the current stream of the current device; a call's workspace comes
+from torch's allocator for that stream, so calls on different streams and
+calls captured into a CUDA graph do not share one.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import _lib
+from ._lib import (MOE_ADAMW_BLOCK, MOE_DTYPE_BF16, MOE_DTYPE_F32, AdamwOptions, AdamwTensor,
+                   AdapterShape, BalanceShape, _bad, _check_tensor, _current_device, _ptr, _stream,
+                   check, load)
+
+
+def _check_rows(t, name: str, dtype, shape, device) -> None:
+    """A [rows, cols] CUDA tensor with unit column stride; rows may be apart."""
+    if t is None:
+        _bad(f"{name} is None")
+    if not t.is_cuda or t.device.index != device:
+        _bad(f"{name} is on {t.device}, the current device is cuda:{device}")
+    if t.dtype != dtype:
+        _bad(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        _bad(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if shape[0] and t.stride(1) != 1 and shape[1] > 1:
+        _bad(f"{name} must have unit stride along its rows")
+
+
+def _ld(t, cols: int) -> int:
+    """Elements between rows (a single row's stride says nothing)."""
+    return t.stride(0) if t.shape[0] > 1 else cols
+
+
+class LowRankAdapters:
+    """Pools of low-rank adapters beside a shared projection: token t of a
+    call uses adapter a = ids[t] and gets scale[a] * b[a] @ (a[a] @ x[t])
+    beside the projection's own result.
+
+    a bf16 [NA, r, H], b bf16 [NA, N, r], scale float32 [NA] or None for 1;
+    r, H and N multiples of 8, r <= 128, NA <= 1024.  The pools are read at
+    every call, so that an update in place takes effect with the next one."""
+
+    def __init__(self, a, b, scale=None):
+        import torch
+        dev = _current_device()
+        _check_tensor(a, "a", cuda=True, dtype=torch.bfloat16, device=dev)
+        if a.dim() != 3:
+            _bad(f"a must be [adapters, rank, in_features], got {tuple(a.shape)}")
+        self.num_adapters, self.rank, self.in_features = a.shape
+        if b is None or b.dim() != 3:
+            _bad("b must be [adapters, out_features, rank]")
+        self.out_features = b.shape[1]
+        _check_tensor(b, "b", cuda=True, dtype=torch.bfloat16, device=dev,
+                      shape=(self.num_adapters, self.out_features, self.rank))
+        if scale is not None:
+            _check_tensor(scale, "scale", cuda=True, dtype=torch.float32, device=dev,
+                          shape=(self.num_adapters,))
+        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        for dt in (MOE_DTYPE_BF16, MOE_DTYPE_F32):   # rejects unsupported sizes here
+            self._workspace_size(0, dt, 0)
+
+    def _shape(self, T: int, out_dtype: int) -> AdapterShape:
+        return AdapterShape(T, self.num_adapters, self.rank, self.in_features, self.out_features,
+                            out_dtype)
+
+    def _workspace_size(self, T: int, out_dtype: int, backward: int) -> int:
+        n = load().moe_adapter_workspace_size(self._shape(T, out_dtype), backward)
+        if n == 0:
+            raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, load().moe_last_error().decode())
+        return n
+
+    def _check_ids(self, ids, T: int, dev) -> None:
+        import torch
+        _check_tensor(ids, "ids", cuda=True, dtype=torch.int32, shape=(T,), device=dev)
+
+    def _kind(self, t, name: str) -> int:
+        import torch
+        if t == torch.bfloat16:
+            return MOE_DTYPE_BF16
+        if t != torch.float32:
+            _bad(f"{name} must be bfloat16 or float32, got {t}")
+        return MOE_DTYPE_F32
+
+    def forward(self, x, ids, base=None, out=None, out_dtype=None):
+        """base + the adapters' products: [T, N] of base's dtype (without a
+        base: of `out`'s, of out_dtype's, or bfloat16).
+
+        x bf16 [T, H], ids int32 [T] (outside [0, NA): no adapter), base
+        [T, N] bf16 or float32; rows may be strided.  `out` may be `base`
+        itself."""
+        import torch
+        dev = _current_device()
+        T = x.shape[0]
+        _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
+        self._check_ids(ids, T, dev)
+        dtype = base.dtype if base is not None else out.dtype if out is not None else (
+            out_dtype or torch.bfloat16)
+        kind, shape = self._kind(dtype, "base"), (T, self.out_features)
+        if base is not None:
+            _check_rows(base, "base", dtype, shape, dev)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=x.device)
+        else:
+            _check_rows(out, "out", dtype, shape, dev)
+        s = self._shape(T, kind)
+        n = load().moe_adapter_workspace_size(s, 0)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+        check(load().moe_adapter_forward(
+            s, x.data_ptr(), _ld(x, self.in_features), ids.data_ptr(), self.a.data_ptr(),
+            self.b.data_ptr(), _ptr(self.scale), _ptr(base),
+            0 if base is None else _ld(base, self.out_features), out.data_ptr(),
+            _ld(out, self.out_features), ws.data_ptr(), n, _stream(None)))
+        return out
+
+    __call__ = forward
+
+    def backward(self, dout, x, ids, dx_base=None, dx=None, da=None, db=None,
+                 need_dx: bool = True, need_weights: bool = True):
+        """(dx, da, db) for dout [T, N] (bf16 or float32): dx bf16 [T, H] with
+        dx_base (the shared projection's) added, da float32 [NA, r, H], db
+        float32 [NA, N, r], zero for adapters without tokens.  What is not
+        needed comes back as None.  `dx` may be `dx_base`, not x or dout."""
+        import torch
+        dev = _current_device()
+        T = x.shape[0]
+        kind = self._kind(dout.dtype, "dout")
+        _check_rows(dout, "dout", dout.dtype, (T, self.out_features), dev)
+        _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
+        self._check_ids(ids, T, dev)
+        if not need_dx:
+            dx = dx_base = None
+        elif dx is None:
+            dx = torch.empty((T, self.in_features), dtype=torch.bfloat16, device=x.device)
+        else:
+            _check_rows(dx, "dx", torch.bfloat16, (T, self.in_features), dev)
+        if dx_base is not None:
+            _check_rows(dx_base, "dx_base", torch.bfloat16, (T, self.in_features), dev)
+        if not need_weights:
+            da = db = None
+        else:
+            if da is None:
+                da = torch.empty(self.a.shape, dtype=torch.float32, device=x.device)
+            else:
+                _check_tensor(da, "da", cuda=True, dtype=torch.float32, shape=self.a.shape, device=dev)
+            if db is None:
+                db = torch.empty(self.b.shape, dtype=torch.float32, device=x.device)
+            else:
+                _check_tensor(db, "db", cuda=True, dtype=torch.float32, shape=self.b.shape, device=dev)
+        s = self._shape(T, kind)
+        n = load().moe_adapter_workspace_size(s, 1)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
+        check(load().moe_adapter_backward(
+            s, dout.data_ptr(), _ld(dout, self.out_features), x.data_ptr(),
+            _ld(x, self.in_features), ids.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
+            _ptr(self.scale), _ptr(dx_base),
+            0 if dx_base is None else _ld(dx_base, self.in_features), _ptr(dx),
+            0 if dx is None else _ld(dx, self.in_features), _ptr(da), _ptr(db), ws.data_ptr(), n,
+            _stream(None)))
+        return dx, da, db
+
+
+class BalanceLoss:
+    """The router's load-balance loss over `num_experts` experts and top-k
+    routing, per-expert counts and the gradient of the logits (the formulas:
+    moe_balance_loss in include/moe.h)."""
+
+    def __init__(self, num_experts: int, top_k: int, coef: float = 1.0):
+        self.num_experts, self.top_k, self.coef = num_experts, top_k, coef
+        if load().moe_balance_workspace_size(BalanceShape(0, num_experts, top_k, 1, coef)) == 0:
+            raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, load().moe_last_error().decode())
+
+    def __call__(self, logits, ids, mask=None, seq_offsets=None, weights=None, dweights=None,
+                 need_grad: bool = True):
+        """(loss float32 [1], counts int32 [S, E], dlogits float32 [T, E] or
+        None).
+
+        logits float32 [T, E], ids int32 [T, k], mask bool or uint8 [T] (zero:
+        padding), seq_offsets int32 [S + 1] (None: the whole batch as one
+        sequence), weights and dweights float32 [T, k] (both or neither: adds
+        the gradient of the routing weights)."""
+        import torch
+        dev, E, k = _current_device(), self.num_experts, self.top_k
+        T = logits.shape[0]
+        _check_tensor(logits, "logits", cuda=True, dtype=torch.float32, shape=(T, E), device=dev)
+        _check_tensor(ids, "ids", cuda=True, dtype=torch.int32, shape=(T, k), device=dev)
+        if mask is not None:
+            if mask.dtype not in (torch.bool, torch.uint8):
+                _bad(f"mask must be bool or uint8, got {mask.dtype}")
+            _check_tensor(mask, "mask", cuda=True, shape=(T,), device=dev)
+        S = 1
+        if seq_offsets is not None:
+            _check_tensor(seq_offsets, "seq_offsets", cuda=True, dtype=torch.int32, device=dev)
+            if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+                _bad("seq_offsets must be [sequences + 1]")
+            S = seq_offsets.shape[0] - 1
+        if (weights is None) != (dweights is None):
+            _bad("weights and dweights go together")
+        if weights is not None:
+            for t, name in ((weights, "weights"), (dweights, "dweights")):
+                _check_tensor(t, name, cuda=True, dtype=torch.float32, shape=(T, k), device=dev)
+        s = BalanceShape(T, E, k, S, self.coef)
+        n = load().moe_balance_workspace_size(s)
+        ws = torch.empty(n, dtype=torch.uint8, device=logits.device)
+        loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+        counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
+        dlogits = torch.empty_like(logits) if need_grad else None
+        check(load().moe_balance_loss(s, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
+                                      _ptr(seq_offsets), _ptr(weights), _ptr(dweights),
+                                      loss.data_ptr(), counts.data_ptr(), _ptr(dlogits),
+                                      ws.data_ptr(), n, _stream(None)))
+        return loss, counts, dlogits
+
+
+class AdamW:
+    """AdamW over a list of tensors, one launch a step (400 tensors a launch).
+
+    params: contiguous float32 CUDA tensors, updated in place; grads: tensors
+    of the same sizes, all float32 or all bfloat16; copies: bfloat16 tensors
+    that receive the rounded parameters, or None.  state_bits 32 keeps float32
+    moments; 8 keeps E4M3 codes in blocks of 256 with a float32 scale each
+    (v holds the codes of the second moment's root).  `state`: {"m": [...],
+    "v": [...]} and, with 8 bits, "m_scale" and "v_scale", to resume from; by
+    default it starts at zero.  The tensors are bound here: after replacing a
+    parameter's or a gradient's memory, build a new AdamW (state=old.state) or
+    pass the new gradients to step()."""
+
+    def __init__(self, params, grads, copies=None, state_bits: int = 32, state=None,
+                 lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, steps_done: int = 0):
+        import torch
+        if state_bits not in (8, 32):
+            _bad(f"state_bits must be 8 or 32, got {state_bits}")
+        dev = _current_device()
+        # detached: keeps the bound memory alive whatever becomes of the originals
+        self.params = [t.detach() for t in params]
+        self.state_bits, self.lr, self.betas, self.eps = state_bits, lr, betas, eps
+        self.weight_decay, self.steps_done = weight_decay, steps_done
+        for i, p in enumerate(self.params):
+            _check_tensor(p, f"params[{i}]", cuda=True, dtype=torch.float32, device=dev)
+        sizes = [p.numel() for p in self.params]
+        blocks = [-(-n // MOE_ADAMW_BLOCK) for n in sizes]
+        if state is None:
+            kind = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+            state = {k: [torch.zeros(n, dtype=torch.uint8 if state_bits == 8 else kind,
+                                     device=p.device).view(kind)
+                         for n, p in zip(sizes, self.params)] for k in ("m", "v")}
+            if state_bits == 8:
+                state |= {k: [torch.ones(n, device=p.device) for n, p in zip(blocks, self.params)]
+                          for k in ("m_scale", "v_scale")}
+        keys = ("m", "v") if state_bits == 32 else ("m", "v", "m_scale", "v_scale")
+        self.state = {}
+        for key in keys:
+            self.state[key] = list(state.get(key) or ())
+            if len(self.state[key]) != len(sizes):
+                _bad(f"state[{key!r}] must hold {len(sizes)} tensors")
+            scales = key.endswith("scale")
+            for i, t in enumerate(self.state[key]):
+                n = blocks[i] if scales else sizes[i]
+                if scales or state_bits == 32:
+                    _check_tensor(t, f"state[{key!r}][{i}]", cuda=True, dtype=torch.float32, numel=n,
+                                  device=dev)
+                else:
+                    _check_tensor(t, f"state[{key!r}][{i}]", cuda=True, itemsize=1, numel=n,
+                                  device=dev)
+        self.copies = None if copies is None else [t.detach() for t in copies]
+        if self.copies is not None:
+            if len(self.copies) != len(sizes):
+                _bad(f"copies must hold {len(sizes)} tensors")
+            for i, t in enumerate(self.copies):
+                _check_tensor(t, f"copies[{i}]", cuda=True, dtype=torch.bfloat16, numel=sizes[i],
+                              device=dev)
+        self._table = (AdamwTensor * max(1, len(sizes)))()
+        for i, n in enumerate(sizes):
+            e = self._table[i]
+            e.param, e.n = self.params[i].data_ptr(), n
+            for key in keys:
+                setattr(e, key, self.state[key][i].data_ptr())
+            e.param_bf16 = None if self.copies is None else self.copies[i].data_ptr()
+        self._options = AdamwOptions(state_bits=state_bits)
+        self.bind_grads(grads)
+
+    def bind_grads(self, grads) -> None:
+        """Take the next steps' gradients from these tensors."""
+        import torch
+        grads = [t.detach() for t in grads]
+        if len(grads) != len(self.params):
+            _bad(f"grads must hold {len(self.params)} tensors")
+        kind = grads[0].dtype if grads else torch.float32
+        if kind not in (torch.float32, torch.bfloat16):
+            _bad(f"grads must be float32 or bfloat16, got {kind}")
+        dev = _current_device()
+        for i, (t, p) in enumerate(zip(grads, self.params)):
+            _check_tensor(t, f"grads[{i}]", cuda=True, dtype=kind, numel=p.numel(), device=dev)
+        self.grads = grads
+        for e, t in zip(self._table, grads):
+            e.grad = t.data_ptr()
+        self._options.grad_dtype = MOE_DTYPE_F32 if kind == torch.float32 else MOE_DTYPE_BF16
+
+    def step(self, grads=None, step: int | None = None, grad_scale=None) -> None:
+        """One step, in place.  `step` (from 1) overrides the count kept here;
+        grad_scale: float32 CUDA scalar every gradient is multiplied by."""
+        if grads is not None:
+            self.bind_grads(grads)
+        t = self.steps_done + 1 if step is None else step
+        o = self._options
+        if grad_scale is not None:
+            import torch
+            _check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
+                          device=_current_device())
+        o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
+        o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
+        o.weight_decay, o.step = self.weight_decay, t
+        check(load().moe_adamw_step(self._table, len(self.params), o, _stream(None)))
+        self.steps_done = t

@@ -32,7 +32,13 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_layout", "moe_prepare_weights", 
            "moe_forward_ex", "moe_forward_host", "moe_read_device_status",
            "moe_selftest_timeout", "moe_last_error", "moe_stage_name", "moe_status_string",
            "moe_version", "moe_route_noalloc", "moe_steps_workspace_size",
-           "moe_forward_host_steps")
+           "moe_forward_host_steps", "moe_adapter_workspace_size", "moe_adapter_forward",
+           "moe_adapter_backward", "moe_balance_workspace_size", "moe_balance_loss",
+           "moe_adamw_step")
+
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_F32 = 1
+MOE_ADAMW_BLOCK = 256
 
 MOE_NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -73,6 +79,27 @@ class WsLayout(ctypes.Structure):
         "tiles", "xq", "x_scale", "h", "hq", "h_scale", "y", "x_stage", "logits_stage",
         "out_stage", "tile_plan", "x_sf", "h_sf", "x_sf_tiled", "h_sf_tiled", "total")] + [("max_tiles", ctypes.c_int32), ("num_chunks", ctypes.c_int32),
                                   ("reserved", ctypes.c_int32 * 6)]
+
+
+class AdapterShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_adapters", "rank", "in_features",
+                                              "out_features", "out_dtype")]
+
+
+class BalanceShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "num_experts", "top_k",
+                                              "num_sequences")] + [("coef", ctypes.c_float)]
+
+
+class AdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "grad", "m", "v", "m_scale", "v_scale",
+                                               "param_bf16")] + [("n", ctypes.c_int64)]
+
+
+class AdamwOptions(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] +
+                [(n, ctypes.c_int32) for n in ("step", "state_bits", "grad_dtype")] +
+                [("reserved", ctypes.c_int32 * 2), ("grad_scale", ctypes.c_void_p)])
 
 
 class MoeError(RuntimeError):
@@ -125,6 +152,20 @@ def load() -> ctypes.CDLL:
     lib.moe_stage_name.restype = ctypes.c_char_p
     lib.moe_status_string.argtypes = [i32]
     lib.moe_status_string.restype = ctypes.c_char_p
+    i64, ash, bsh = ctypes.c_int64, ctypes.POINTER(AdapterShape), ctypes.POINTER(BalanceShape)
+    lib.moe_adapter_workspace_size.argtypes = [ash, i32]
+    lib.moe_adapter_workspace_size.restype = sz
+    lib.moe_adapter_forward.argtypes = [ash, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64, vp, sz, vp]
+    lib.moe_adapter_forward.restype = i32
+    lib.moe_adapter_backward.argtypes = ([ash, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, vp, i64] +
+                                         [vp] * 3 + [sz, vp])
+    lib.moe_adapter_backward.restype = i32
+    lib.moe_balance_workspace_size.argtypes = [bsh]
+    lib.moe_balance_workspace_size.restype = sz
+    lib.moe_balance_loss.argtypes = [bsh] + [vp] * 10 + [sz, vp]
+    lib.moe_balance_loss.restype = i32
+    lib.moe_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), i32, ctypes.POINTER(AdamwOptions), vp]
+    lib.moe_adamw_step.restype = i32
     _lib = lib
     return lib
 

@@ -1,0 +1,394 @@
+// balance.cu -- the router's load-balance loss, the per-expert counts and the
+// gradient of the router logits, in one pass over the logits.
+//
+// Over the valid tokens of sequence s (n_s of them), with c_se the slots that
+// went to expert e, p_t the softmax of the logits over all experts:
+//   f_se = E c_se / (k n_s)
+//   loss = coef / S' * sum_s 1/n_s sum_t sum_e f_se p_te      (S' sequences with n_s > 0)
+//   dloss/dz_te = coef / (S' n_s) * p_te (f_se - sum_j f_sj p_tj)
+// f is the usual non-differentiable factor.  The mean probability of an expert
+// appears only inside the sum over experts, so a token contributes one number,
+// d_t = sum_e f_se p_te, which its gradient needs anyway: no [E] sums of
+// probabilities are kept, and the gradient does not wait for the loss.  What
+// it does wait for are the counts, hence two kernels.
+//
+// Bound by HBM: logits are read once and the gradient is written once, 8 E
+// bytes a token; the counts read 4 k bytes a token.
+#include <cfloat>
+
+#include "cluster.cuh"
+#include "entry.h"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kCountCtas = 8;       // one cluster of CTAs counts a sequence
+constexpr int kCountThreads = 512;
+constexpr int kMainThreads = 256;
+
+// Sequence bounds, held inside [0, T] and in order whatever the offsets hold.
+__device__ __forceinline__ int2 seq_range(const int32_t* seq, int s, int T) {
+  if (!seq) return make_int2(0, T);
+  const int a = min(max(seq[s], 0), T);
+  return make_int2(a, max(a, min(max(seq[s + 1], 0), T)));
+}
+
+// Cluster s counts sequence s: the slots of its valid tokens by expert, and
+// its valid tokens.  Integer sums, so their order does not matter.  Each CTA
+// takes a contiguous eighth of the tokens and then writes an eighth of the
+// experts: counts, and f without the factors that main applies.
+__global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThreads)
+    balance_count_kernel(const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
+                         const int32_t* __restrict__ seq, int T, int E, int k,
+                         int32_t* __restrict__ counts, int32_t* __restrict__ n_valid,
+                         uint32_t* __restrict__ ticket) {
+  extern __shared__ int32_t hist[];   // [E] slots by expert, [E]: valid tokens
+  griddep_wait();
+  griddep_launch_dependents();
+  const int s = blockIdx.x / kCountCtas;
+  const int rank = static_cast<int>(cluster_rank());
+  for (int i = threadIdx.x; i <= E; i += kCountThreads) hist[i] = 0;
+  __syncthreads();
+  const int2 r = seq_range(seq, s, T);
+  const int64_t n = r.y - r.x;
+  const int a = r.x + static_cast<int>(n * rank / kCountCtas);
+  const int b = r.x + static_cast<int>(n * (rank + 1) / kCountCtas);
+  const int64_t i0 = static_cast<int64_t>(a) * k, i1 = static_cast<int64_t>(b) * k;
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += kCountThreads) {
+    const int e = ids[i];
+    if (static_cast<unsigned>(e) < static_cast<unsigned>(E) && (!mask || mask[i / k]))
+      atomicAdd(&hist[e], 1);
+  }
+  int valid = 0;
+  if (mask)
+    for (int t = a + threadIdx.x; t < b; t += kCountThreads) valid += mask[t] != 0;
+  else
+    valid = threadIdx.x == 0 ? b - a : 0;
+  valid = __reduce_add_sync(0xFFFFFFFFu, valid);
+  if ((threadIdx.x & 31) == 0 && valid) atomicAdd(&hist[E], valid);
+  cluster_sync();
+  const int e0 = E * rank / kCountCtas, e1 = E * (rank + 1) / kCountCtas;
+  for (int e = e0 + threadIdx.x; e < e1; e += kCountThreads) {
+    int sum = 0;
+    for (int c = 0; c < kCountCtas; ++c) sum += cluster_load(hist + e, c);
+    counts[static_cast<int64_t>(s) * E + e] = sum;
+  }
+  if (rank == 0 && threadIdx.x == 0) {
+    int sum = 0;
+    for (int c = 0; c < kCountCtas; ++c) sum += cluster_load(hist + E, c);
+    n_valid[s] = sum;
+    if (s == 0) *ticket = 0;
+  }
+  cluster_sync();   // no CTA leaves while another reads its shared memory
+}
+
+struct BalanceArgs {
+  const float* logits;
+  const int32_t* ids;
+  const uint8_t* mask;
+  const int32_t* seq;
+  const float* weights;
+  const float* dweights;
+  const int32_t* counts;
+  const int32_t* n_valid;
+  float* partial;        // one per CTA
+  uint32_t* ticket;
+  float* loss;
+  float* dlogits;
+  int32_t T, E, k, S;
+  float coef;
+  int32_t vec;           // logits and dlogits allow 16-byte accesses
+};
+
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, o, G));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = G / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o, G);
+  return v;
+}
+
+// G lanes hold one token's row: lane l the experts 4 (l + G i) .. + 3, i < V.
+// A CTA takes a contiguous range of tokens, its groups of lanes in turn.
+template <int G, int V>
+__global__ void __launch_bounds__(kMainThreads) balance_main_kernel(const BalanceArgs a) {
+  constexpr int kGroups = kMainThreads / G;
+  __shared__ float sums[kMainThreads / 32];
+  __shared__ int live_s;
+  __shared__ bool last;
+  const int lane = threadIdx.x % G, group = threadIdx.x / G;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) live_s = 0;
+  __syncthreads();
+  int live = 0;
+  for (int s = threadIdx.x; s < a.S; s += kMainThreads) live += a.n_valid[s] > 0;
+  if (live) atomicAdd(&live_s, live);
+  __syncthreads();
+  const float share = a.coef / static_cast<float>(max(live_s, 1));
+  const int64_t per = (static_cast<int64_t>(a.T) + gridDim.x - 1) / gridDim.x;
+  const int64_t t0 = per * blockIdx.x, t1 = min(t0 + per, static_cast<int64_t>(a.T));
+  float mine = 0.f;
+  int s = -1, s_end = -1;   // the sequence of the token in hand, and where it ends
+  float f[4 * V], c = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4 * V; ++i) f[i] = 0.f;
+  // every lane of a warp runs the same number of rounds (the shuffles)
+  for (int64_t tt = t0; tt < t1; tt += kGroups) {
+    const int64_t t = tt + group;
+    const bool in = t < t1;
+    if (in && t >= s_end) {
+      // the last sequence that begins at or before t
+      int lo = 0, hi = a.S;
+      if (a.seq)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (a.seq[mid] <= t) lo = mid;
+          else hi = mid;
+        }
+      const int2 r = seq_range(a.seq, lo, a.T);
+      const bool inside = t >= r.x && t < r.y;   // not: a token of no sequence
+      s = inside ? lo : -1;
+      s_end = inside ? r.y : static_cast<int>(t) + 1;
+      const int n = inside ? a.n_valid[s] : 0;
+      c = n > 0 ? share / static_cast<float>(n) : 0.f;
+      const float unit = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n)) : 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int e = 4 * (lane + G * i) + q;
+          f[4 * i + q] = inside && e < a.E
+                             ? unit * static_cast<float>(a.counts[static_cast<int64_t>(s) * a.E + e])
+                             : 0.f;
+        }
+    }
+    const bool valid = in && s >= 0 && (!a.mask || a.mask[t]);
+    const float* row = a.logits + (in ? t : 0) * a.E;
+    float z[4 * V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = 4 * (lane + G * i);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[4 * i + q] = -INFINITY;
+      if (valid) {
+        if (a.vec && e < a.E) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(row + e));
+          z[4 * i] = v.x, z[4 * i + 1] = v.y, z[4 * i + 2] = v.z, z[4 * i + 3] = v.w;
+        } else if (!a.vec) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (e + q < a.E) z[4 * i + q] = row[e + q];
+        }
+      }
+    }
+    float top = z[0];
+#pragma unroll
+    for (int i = 1; i < 4 * V; ++i) top = fmaxf(top, z[i]);
+    top = group_max<G>(top);
+    // a row without a finite or infinite logit has no probabilities: p = 0
+    // (a NaN beside it still shows: exp(NaN))
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * V; ++i) {
+      z[i] = expf(z[i] - base);
+      sum += z[i];
+      dot = fmaf(z[i], f[i], dot);
+    }
+    sum = group_sum<G>(sum);
+    dot = group_sum<G>(dot);
+    const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+    dot *= inv;
+    if (valid && lane == 0) mine = fmaf(c, dot, mine);
+    if (!a.dlogits || !in) continue;
+    const float scale = valid ? c * inv : 0.f;
+#pragma unroll
+    for (int i = 0; i < 4 * V; ++i) z[i] = valid ? scale * z[i] * (f[i] - dot) : 0.f;
+    if (a.weights) {
+      const int64_t r0 = t * a.k;
+      float inner = 0.f;
+      for (int j = 0; j < a.k; ++j)
+        if (static_cast<unsigned>(a.ids[r0 + j]) < static_cast<unsigned>(a.E))
+          inner = fmaf(a.weights[r0 + j], a.dweights[r0 + j], inner);
+      for (int j = 0; j < a.k; ++j) {
+        const int e = a.ids[r0 + j];
+        const float g = a.weights[r0 + j] * (a.dweights[r0 + j] - inner);
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (4 * (lane + G * i) + q == e) z[4 * i + q] += g;
+      }
+    }
+    float* out = a.dlogits + t * a.E;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = 4 * (lane + G * i);
+      if (a.vec) {
+        if (e < a.E)
+          __stcs(reinterpret_cast<float4*>(out + e),
+                 make_float4(z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]));
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (e + q < a.E) out[e + q] = z[4 * i + q];
+      }
+    }
+  }
+  // The loss: the CTAs' sums, added in CTA order by the last CTA to finish,
+  // so that it does not depend on which one that is.
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = mine;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v = 0.f;
+    for (int w = 0; w < kMainThreads / 32; ++w) v += sums[w];
+    __stcg(a.partial + blockIdx.x, v);
+    __threadfence();
+    last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (last && threadIdx.x < 32) {
+    __threadfence();
+    float v = 0.f;
+    for (unsigned b = threadIdx.x; b < gridDim.x; b += 32) v += __ldcg(a.partial + b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    if (threadIdx.x == 0) *a.loss = v;
+  }
+}
+
+__global__ void balance_empty_kernel(float* loss, int32_t* counts, int64_t n) {
+  griddep_wait();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (i == 0) *loss = 0.f;
+  if (i < n) counts[i] = 0;
+}
+
+constexpr int kMaxCtas = 152 * 8;
+
+struct BalanceWs {
+  size_t n_valid, partial, ticket, total;
+};
+
+BalanceWs balance_ws(const moe_balance_shape* s) {
+  BalanceWs w;
+  w.n_valid = 0;
+  w.partial = ws_up(static_cast<size_t>(s->num_sequences) * 4);
+  w.ticket = w.partial + ws_up(kMaxCtas * 4);
+  w.total = w.ticket + kWsAlign;
+  return w;
+}
+
+int32_t check_balance(const moe_balance_shape* s) {
+  if (!s) return entry_fail(MOE_ERR_INVALID_ARG, "shape is NULL");
+  if (s->num_tokens < 0 || s->num_experts < 1 || s->num_experts > 1024 || s->top_k < 1 ||
+      s->top_k > 32 || s->top_k > s->num_experts)
+    return entry_fail(MOE_ERR_INVALID_ARG, "need num_tokens >= 0, 1 <= num_experts <= 1024, "
+                                           "1 <= top_k <= min(num_experts, 32)");
+  if (s->num_sequences < 1 || s->num_sequences > (1 << 20))
+    return entry_fail(MOE_ERR_INVALID_ARG, "num_sequences must be in [1, 2^20]");
+  if (!(s->coef - s->coef == 0.f)) return entry_fail(MOE_ERR_INVALID_ARG, "coef must be finite");
+  return MOE_OK;
+}
+
+template <int G, int V>
+cudaError_t launch_main(const BalanceArgs& a, int grid, cudaStream_t st) {
+  return launch_pdl(balance_main_kernel<G, V>, dim3(grid), dim3(kMainThreads), 0, st, a);
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" size_t moe_balance_workspace_size(const moe_balance_shape* shape) {
+  if (moe::check_balance(shape) != MOE_OK) return 0;
+  return moe::balance_ws(shape).total;
+}
+
+extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float* logits,
+                                    const int32_t* ids, const uint8_t* token_mask,
+                                    const int32_t* seq_offsets, const float* weights,
+                                    const float* dweights, float* loss, int32_t* counts,
+                                    float* dlogits, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  using namespace moe;
+  int32_t rc = check_balance(shape);
+  if (rc != MOE_OK) return rc;
+  const int T = shape->num_tokens, E = shape->num_experts, S = shape->num_sequences;
+  if (!loss || !counts) return entry_fail(MOE_ERR_INVALID_ARG, "loss or counts is NULL");
+  if (T > 0 && (!logits || !ids || !workspace))
+    return entry_fail(MOE_ERR_INVALID_ARG, "logits, ids or workspace is NULL");
+  if (S > 1 && !seq_offsets)
+    return entry_fail(MOE_ERR_INVALID_ARG, "num_sequences > 1 needs seq_offsets");
+  if (!weights != !dweights)
+    return entry_fail(MOE_ERR_INVALID_ARG, "weights and dweights go together");
+  const void* ptrs[8] = {logits, ids, seq_offsets, weights, dweights, loss, counts, dlogits};
+  for (const void* p : ptrs)
+    if (!ptr_aligned(p, 4)) return entry_fail(MOE_ERR_MISALIGNED, "a pointer is not 4-byte aligned");
+  if (!ptr_aligned(workspace, kWsAlign))
+    return entry_fail(MOE_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  const BalanceWs w = balance_ws(shape);
+  if (T > 0 && workspace_bytes < w.total)
+    return entry_fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu",
+                      workspace_bytes, w.total);
+  int sms = 0;
+  if ((rc = check_device(&sms)) != MOE_OK) return rc;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0) {
+    const int64_t n = static_cast<int64_t>(S) * E;
+    return entry_launched(launch_pdl(balance_empty_kernel,
+                                     dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0,
+                                     st, loss, counts, n));
+  }
+  uint8_t* base = static_cast<uint8_t*>(workspace);
+  int32_t* n_valid = reinterpret_cast<int32_t*>(base + w.n_valid);
+  uint32_t* ticket = reinterpret_cast<uint32_t*>(base + w.ticket);
+  cudaError_t e = launch_pdl(balance_count_kernel, dim3(static_cast<unsigned>(S) * kCountCtas),
+                             dim3(kCountThreads), (E + 1) * sizeof(int32_t), st, ids, token_mask,
+                             seq_offsets, T, E, shape->top_k, counts, n_valid, ticket);
+  if (e != cudaSuccess) return entry_launched(e);
+  BalanceArgs a;
+  a.logits = logits;
+  a.ids = ids;
+  a.mask = token_mask;
+  a.seq = seq_offsets;
+  a.weights = weights;
+  a.dweights = dweights;
+  a.counts = counts;
+  a.n_valid = n_valid;
+  a.partial = reinterpret_cast<float*>(base + w.partial);
+  a.ticket = ticket;
+  a.loss = loss;
+  a.dlogits = dlogits;
+  a.T = T, a.E = E, a.k = shape->top_k, a.S = S;
+  a.coef = shape->coef;
+  a.vec = E % 4 == 0 && ptr_aligned(logits, 16) && ptr_aligned(dlogits, 16);
+  // lanes per token: as many as hold its experts by fours, up to a warp
+  const int lanes = E <= 8 ? 2 : E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : 32;
+  const int per_round = kMainThreads / lanes;
+  const int64_t rounds = (static_cast<int64_t>(T) + per_round - 1) / per_round;
+  int max_ctas = sms * 8;
+  if (max_ctas > kMaxCtas) max_ctas = kMaxCtas;
+  const int grid = static_cast<int>(rounds < max_ctas ? rounds : max_ctas);
+  switch (lanes) {
+    case 2: e = launch_main<2, 1>(a, grid, st); break;
+    case 4: e = launch_main<4, 1>(a, grid, st); break;
+    case 8: e = launch_main<8, 1>(a, grid, st); break;
+    case 16: e = launch_main<16, 1>(a, grid, st); break;
+    default:
+      e = E <= 128   ? launch_main<32, 1>(a, grid, st)
+          : E <= 256 ? launch_main<32, 2>(a, grid, st)
+          : E <= 384 ? launch_main<32, 3>(a, grid, st)
+          : E <= 512 ? launch_main<32, 4>(a, grid, st)
+                     : launch_main<32, 8>(a, grid, st);
+  }
+  return entry_launched(e);
+}
