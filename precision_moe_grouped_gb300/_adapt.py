@@ -13,27 +13,59 @@ import ctypes
 
 from . import _lib
 from ._lib import (MOE_ADAMW_BLOCK, MOE_DTYPE_BF16, MOE_DTYPE_F32, AdamwOptions, AdamwTensor,
-                   AdapterShape, BalanceShape, _bad, _check_tensor, _current_device, _ptr, _stream,
-                   check, load)
+                   AdapterShape, BalanceShape, _bad, _check_tensor, check, load)
+
+torch = None   # bound when the first object is made: the build imports this package without it
 
 
-def _check_rows(t, name: str, dtype, shape, device) -> None:
-    """A [rows, cols] CUDA tensor with unit column stride; rows may be apart."""
+def _bind_torch() -> None:
+    global torch
+    if torch is None:
+        import torch as module
+        torch = module
+
+
+def _device() -> int | None:
+    """The current CUDA device's index; None where there is none (every tensor
+    then fails its check)."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else _lib._current_device()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _check_rows(t, name: str, dtype, shape: tuple, device) -> int:
+    """A [rows, cols] CUDA tensor with unit column stride; rows may be apart.
+    Returns the elements between rows (a single row's stride says nothing)."""
     if t is None:
         _bad(f"{name} is None")
-    if not t.is_cuda or t.device.index != device:
+    if not t.is_cuda or t.get_device() != device:
         _bad(f"{name} is on {t.device}, the current device is cuda:{device}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         _bad(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
-        _bad(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if shape[0] and t.stride(1) != 1 and shape[1] > 1:
+        _bad(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    row, col = t.stride()
+    if col != 1 and shape[0] and shape[1] > 1:
         _bad(f"{name} must have unit stride along its rows")
+    return row if shape[0] > 1 else shape[1]
 
 
-def _ld(t, cols: int) -> int:
-    """Elements between rows (a single row's stride says nothing)."""
-    return t.stride(0) if t.shape[0] > 1 else cols
+def _check_flat(t, name: str, dtype, shape: tuple, device) -> None:
+    """A contiguous CUDA tensor (_check_tensor at a fraction of its time)."""
+    if not (t is not None and t.is_cuda and t.get_device() == device and t.dtype is dtype
+            and t.shape == shape and t.is_contiguous()):
+        _check_tensor(t, name, cuda=True, dtype=dtype, shape=shape, device=device)
+
+
+def _scratch(n: int, like):
+    """The call's workspace, from torch's allocator for the current stream."""
+    return torch.empty(n, dtype=torch.uint8, device=like.device)
+
+
+def _stream() -> int:
+    return torch.cuda.current_stream().cuda_stream
 
 
 class LowRankAdapters:
@@ -46,8 +78,8 @@ class LowRankAdapters:
     every call, so that an update in place takes effect with the next one."""
 
     def __init__(self, a, b, scale=None):
-        import torch
-        dev = _current_device()
+        _bind_torch()
+        dev = _device()
         _check_tensor(a, "a", cuda=True, dtype=torch.bfloat16, device=dev)
         if a.dim() != 3:
             _bad(f"a must be [adapters, rank, in_features], got {tuple(a.shape)}")
@@ -61,29 +93,31 @@ class LowRankAdapters:
             _check_tensor(scale, "scale", cuda=True, dtype=torch.float32, device=dev,
                           shape=(self.num_adapters,))
         self.a, self.b, self.scale, self.device = a, b, scale, a.device
-        for dt in (MOE_DTYPE_BF16, MOE_DTYPE_F32):   # rejects unsupported sizes here
-            self._workspace_size(0, dt, 0)
+        self._lib = load()
+        self._sizes = {}
+        for kind in (MOE_DTYPE_BF16, MOE_DTYPE_F32):   # rejects unsupported sizes here
+            self._call(0, kind, 0)
 
-    def _shape(self, T: int, out_dtype: int) -> AdapterShape:
-        return AdapterShape(T, self.num_adapters, self.rank, self.in_features, self.out_features,
-                            out_dtype)
+    def _call(self, T: int, kind: int, backward: int):
+        """(shape, workspace bytes) of a call with T tokens."""
+        got = self._sizes.get((T, kind, backward))
+        if got is None:
+            s = AdapterShape(T, self.num_adapters, self.rank, self.in_features, self.out_features,
+                             kind)
+            n = self._lib.moe_adapter_workspace_size(s, backward)
+            if n == 0:
+                raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, self._lib.moe_last_error().decode())
+            if len(self._sizes) > 4096:
+                self._sizes.clear()
+            got = self._sizes[(T, kind, backward)] = (s, n)
+        return got
 
-    def _workspace_size(self, T: int, out_dtype: int, backward: int) -> int:
-        n = load().moe_adapter_workspace_size(self._shape(T, out_dtype), backward)
-        if n == 0:
-            raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, load().moe_last_error().decode())
-        return n
-
-    def _check_ids(self, ids, T: int, dev) -> None:
-        import torch
-        _check_tensor(ids, "ids", cuda=True, dtype=torch.int32, shape=(T,), device=dev)
-
-    def _kind(self, t, name: str) -> int:
-        import torch
-        if t == torch.bfloat16:
+    @staticmethod
+    def _kind(dtype, name: str) -> int:
+        if dtype is torch.bfloat16:
             return MOE_DTYPE_BF16
-        if t != torch.float32:
-            _bad(f"{name} must be bfloat16 or float32, got {t}")
+        if dtype is not torch.float32:
+            _bad(f"{name} must be bfloat16 or float32, got {dtype}")
         return MOE_DTYPE_F32
 
     def forward(self, x, ids, base=None, out=None, out_dtype=None):
@@ -93,28 +127,26 @@ class LowRankAdapters:
         x bf16 [T, H], ids int32 [T] (outside [0, NA): no adapter), base
         [T, N] bf16 or float32; rows may be strided.  `out` may be `base`
         itself."""
-        import torch
-        dev = _current_device()
+        dev = _device()
         T = x.shape[0]
-        _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
-        self._check_ids(ids, T, dev)
+        ld_x = _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
+        _check_flat(ids, "ids", torch.int32, (T,), dev)
         dtype = base.dtype if base is not None else out.dtype if out is not None else (
             out_dtype or torch.bfloat16)
         kind, shape = self._kind(dtype, "base"), (T, self.out_features)
-        if base is not None:
-            _check_rows(base, "base", dtype, shape, dev)
+        ld_base = 0 if base is None else _check_rows(base, "base", dtype, shape, dev)
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=x.device)
+            out, ld_out = torch.empty(shape, dtype=dtype, device=self.device), self.out_features
         else:
-            _check_rows(out, "out", dtype, shape, dev)
-        s = self._shape(T, kind)
-        n = load().moe_adapter_workspace_size(s, 0)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-        check(load().moe_adapter_forward(
-            s, x.data_ptr(), _ld(x, self.in_features), ids.data_ptr(), self.a.data_ptr(),
-            self.b.data_ptr(), _ptr(self.scale), _ptr(base),
-            0 if base is None else _ld(base, self.out_features), out.data_ptr(),
-            _ld(out, self.out_features), ws.data_ptr(), n, _stream(None)))
+            ld_out = _check_rows(out, "out", dtype, shape, dev)
+        s, n = self._call(T, kind, 0)
+        ws = _scratch(n, x)
+        rc = self._lib.moe_adapter_forward(
+            s, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
+            _ptr(self.scale), _ptr(base), ld_base, out.data_ptr(), ld_out, ws.data_ptr(), n,
+            _stream())
+        if rc:
+            check(rc)
         return out
 
     __call__ = forward
@@ -125,42 +157,40 @@ class LowRankAdapters:
         dx_base (the shared projection's) added, da float32 [NA, r, H], db
         float32 [NA, N, r], zero for adapters without tokens.  What is not
         needed comes back as None.  `dx` may be `dx_base`, not x or dout."""
-        import torch
-        dev = _current_device()
+        dev = _device()
         T = x.shape[0]
-        kind = self._kind(dout.dtype, "dout")
-        _check_rows(dout, "dout", dout.dtype, (T, self.out_features), dev)
-        _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
-        self._check_ids(ids, T, dev)
+        kind, wide = self._kind(dout.dtype, "dout"), (T, self.in_features)
+        ld_dout = _check_rows(dout, "dout", dout.dtype, (T, self.out_features), dev)
+        ld_x = _check_rows(x, "x", torch.bfloat16, wide, dev)
+        _check_flat(ids, "ids", torch.int32, (T,), dev)
+        ld_dx = ld_base = 0
         if not need_dx:
             dx = dx_base = None
         elif dx is None:
-            dx = torch.empty((T, self.in_features), dtype=torch.bfloat16, device=x.device)
+            dx, ld_dx = torch.empty(wide, dtype=torch.bfloat16, device=self.device), wide[1]
         else:
-            _check_rows(dx, "dx", torch.bfloat16, (T, self.in_features), dev)
+            ld_dx = _check_rows(dx, "dx", torch.bfloat16, wide, dev)
         if dx_base is not None:
-            _check_rows(dx_base, "dx_base", torch.bfloat16, (T, self.in_features), dev)
+            ld_base = _check_rows(dx_base, "dx_base", torch.bfloat16, wide, dev)
         if not need_weights:
             da = db = None
         else:
             if da is None:
-                da = torch.empty(self.a.shape, dtype=torch.float32, device=x.device)
+                da = torch.empty(self.a.shape, dtype=torch.float32, device=self.device)
             else:
-                _check_tensor(da, "da", cuda=True, dtype=torch.float32, shape=self.a.shape, device=dev)
+                _check_flat(da, "da", torch.float32, self.a.shape, dev)
             if db is None:
-                db = torch.empty(self.b.shape, dtype=torch.float32, device=x.device)
+                db = torch.empty(self.b.shape, dtype=torch.float32, device=self.device)
             else:
-                _check_tensor(db, "db", cuda=True, dtype=torch.float32, shape=self.b.shape, device=dev)
-        s = self._shape(T, kind)
-        n = load().moe_adapter_workspace_size(s, 1)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device)
-        check(load().moe_adapter_backward(
-            s, dout.data_ptr(), _ld(dout, self.out_features), x.data_ptr(),
-            _ld(x, self.in_features), ids.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
-            _ptr(self.scale), _ptr(dx_base),
-            0 if dx_base is None else _ld(dx_base, self.in_features), _ptr(dx),
-            0 if dx is None else _ld(dx, self.in_features), _ptr(da), _ptr(db), ws.data_ptr(), n,
-            _stream(None)))
+                _check_flat(db, "db", torch.float32, self.b.shape, dev)
+        s, n = self._call(T, kind, 1)
+        ws = _scratch(n, x)
+        rc = self._lib.moe_adapter_backward(
+            s, dout.data_ptr(), ld_dout, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(),
+            self.b.data_ptr(), _ptr(self.scale), _ptr(dx_base), ld_base, _ptr(dx), ld_dx, _ptr(da),
+            _ptr(db), ws.data_ptr(), n, _stream())
+        if rc:
+            check(rc)
         return dx, da, db
 
 
@@ -170,9 +200,16 @@ class BalanceLoss:
     moe_balance_loss in include/moe.h)."""
 
     def __init__(self, num_experts: int, top_k: int, coef: float = 1.0):
+        _bind_torch()
         self.num_experts, self.top_k, self.coef = num_experts, top_k, coef
-        if load().moe_balance_workspace_size(BalanceShape(0, num_experts, top_k, 1, coef)) == 0:
-            raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, load().moe_last_error().decode())
+        self._lib, self._sizes = load(), {}
+        self._size(BalanceShape(0, num_experts, top_k, 1, coef))   # rejects bad sizes here
+
+    def _size(self, s: BalanceShape) -> int:
+        n = self._lib.moe_balance_workspace_size(s)
+        if n == 0:
+            raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, self._lib.moe_last_error().decode())
+        return n
 
     def __call__(self, logits, ids, mask=None, seq_offsets=None, weights=None, dweights=None,
                  need_grad: bool = True):
@@ -183,36 +220,39 @@ class BalanceLoss:
         padding), seq_offsets int32 [S + 1] (None: the whole batch as one
         sequence), weights and dweights float32 [T, k] (both or neither: adds
         the gradient of the routing weights)."""
-        import torch
-        dev, E, k = _current_device(), self.num_experts, self.top_k
+        dev, E, k = _device(), self.num_experts, self.top_k
         T = logits.shape[0]
-        _check_tensor(logits, "logits", cuda=True, dtype=torch.float32, shape=(T, E), device=dev)
-        _check_tensor(ids, "ids", cuda=True, dtype=torch.int32, shape=(T, k), device=dev)
+        _check_flat(logits, "logits", torch.float32, (T, E), dev)
+        _check_flat(ids, "ids", torch.int32, (T, k), dev)
         if mask is not None:
             if mask.dtype not in (torch.bool, torch.uint8):
                 _bad(f"mask must be bool or uint8, got {mask.dtype}")
-            _check_tensor(mask, "mask", cuda=True, shape=(T,), device=dev)
+            _check_flat(mask, "mask", mask.dtype, (T,), dev)
         S = 1
         if seq_offsets is not None:
-            _check_tensor(seq_offsets, "seq_offsets", cuda=True, dtype=torch.int32, device=dev)
             if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
                 _bad("seq_offsets must be [sequences + 1]")
             S = seq_offsets.shape[0] - 1
+            _check_flat(seq_offsets, "seq_offsets", torch.int32, (S + 1,), dev)
         if (weights is None) != (dweights is None):
             _bad("weights and dweights go together")
         if weights is not None:
-            for t, name in ((weights, "weights"), (dweights, "dweights")):
-                _check_tensor(t, name, cuda=True, dtype=torch.float32, shape=(T, k), device=dev)
+            _check_flat(weights, "weights", torch.float32, (T, k), dev)
+            _check_flat(dweights, "dweights", torch.float32, (T, k), dev)
         s = BalanceShape(T, E, k, S, self.coef)
-        n = load().moe_balance_workspace_size(s)
-        ws = torch.empty(n, dtype=torch.uint8, device=logits.device)
+        n = self._sizes.get(S)
+        if n is None:   # it depends on the sequences alone
+            n = self._sizes[S] = self._size(s)
+        ws = _scratch(n, logits)
         loss = torch.empty(1, dtype=torch.float32, device=logits.device)
         counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
         dlogits = torch.empty_like(logits) if need_grad else None
-        check(load().moe_balance_loss(s, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
-                                      _ptr(seq_offsets), _ptr(weights), _ptr(dweights),
-                                      loss.data_ptr(), counts.data_ptr(), _ptr(dlogits),
-                                      ws.data_ptr(), n, _stream(None)))
+        rc = self._lib.moe_balance_loss(s, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
+                                        _ptr(seq_offsets), _ptr(weights), _ptr(dweights),
+                                        loss.data_ptr(), counts.data_ptr(), _ptr(dlogits),
+                                        ws.data_ptr(), n, _stream())
+        if rc:
+            check(rc)
         return loss, counts, dlogits
 
 
@@ -232,10 +272,10 @@ class AdamW:
     def __init__(self, params, grads, copies=None, state_bits: int = 32, state=None,
                  lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, steps_done: int = 0):
-        import torch
+        _bind_torch()
         if state_bits not in (8, 32):
             _bad(f"state_bits must be 8 or 32, got {state_bits}")
-        dev = _current_device()
+        dev = _device()
         # detached: keeps the bound memory alive whatever becomes of the originals
         self.params = [t.detach() for t in params]
         self.state_bits, self.lr, self.betas, self.eps = state_bits, lr, betas, eps
@@ -286,14 +326,13 @@ class AdamW:
 
     def bind_grads(self, grads) -> None:
         """Take the next steps' gradients from these tensors."""
-        import torch
         grads = [t.detach() for t in grads]
         if len(grads) != len(self.params):
             _bad(f"grads must hold {len(self.params)} tensors")
         kind = grads[0].dtype if grads else torch.float32
         if kind not in (torch.float32, torch.bfloat16):
             _bad(f"grads must be float32 or bfloat16, got {kind}")
-        dev = _current_device()
+        dev = _device()
         for i, (t, p) in enumerate(zip(grads, self.params)):
             _check_tensor(t, f"grads[{i}]", cuda=True, dtype=kind, numel=p.numel(), device=dev)
         self.grads = grads
@@ -309,11 +348,10 @@ class AdamW:
         t = self.steps_done + 1 if step is None else step
         o = self._options
         if grad_scale is not None:
-            import torch
-            _check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
-                          device=_current_device())
+                _check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
+                          device=_device())
         o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
         o.weight_decay, o.step = self.weight_decay, t
-        check(load().moe_adamw_step(self._table, len(self.params), o, _stream(None)))
+        check(load().moe_adamw_step(self._table, len(self.params), o, _stream()))
         self.steps_done = t
