@@ -363,8 +363,8 @@ size_t moe_adapter_workspace_size(const moe_adapter_shape* shape, int32_t backwa
  *   out          [T, N] of out_dtype, rows ld_out apart
  * x, a, b, base and out 16-byte aligned, row strides multiples of 8 elements
  * and at least the row's length.  The product A_a x is held in float and
- * enters the second product as two bf16 terms (a relative error below
- * 2^-17). */
+ * enters the second product as bf16 terms: two for a bf16 out (an error
+ * below 2^-17 of it), three for a float one (2^-25). */
 int32_t moe_adapter_forward(const moe_adapter_shape* shape, const void* x, int64_t ld_x,
                             const int32_t* adapter_ids, const void* a, const void* b,
                             const float* scale, const void* base, int64_t ld_base, void* out,

@@ -16,12 +16,16 @@ from ._lib import (MOE_ADAMW_BLOCK, MOE_DTYPE_BF16, MOE_DTYPE_F32, AdamwOptions,
                    AdapterShape, BalanceShape, _bad, _check_tensor, check, load)
 
 torch = None   # bound when the first object is made: the build imports this package without it
+_raw_stream = None
 
 
 def _bind_torch() -> None:
-    global torch
+    global torch, _raw_stream
     if torch is None:
         import torch as module
+        # the handle alone: building torch's stream object takes 3 us
+        _raw_stream = getattr(module._C, "_cuda_getCurrentRawStream", None) or (
+            lambda device: module.cuda.current_stream(device).cuda_stream)
         torch = module
 
 
@@ -62,10 +66,6 @@ def _check_flat(t, name: str, dtype, shape: tuple, device) -> None:
 def _scratch(n: int, like):
     """The call's workspace, from torch's allocator for the current stream."""
     return torch.empty(n, dtype=torch.uint8, device=like.device)
-
-
-def _stream() -> int:
-    return torch.cuda.current_stream().cuda_stream
 
 
 class LowRankAdapters:
@@ -144,7 +144,7 @@ class LowRankAdapters:
         rc = self._lib.moe_adapter_forward(
             s, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
             _ptr(self.scale), _ptr(base), ld_base, out.data_ptr(), ld_out, ws.data_ptr(), n,
-            _stream())
+            _raw_stream(dev))
         if rc:
             check(rc)
         return out
@@ -188,7 +188,7 @@ class LowRankAdapters:
         rc = self._lib.moe_adapter_backward(
             s, dout.data_ptr(), ld_dout, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(),
             self.b.data_ptr(), _ptr(self.scale), _ptr(dx_base), ld_base, _ptr(dx), ld_dx, _ptr(da),
-            _ptr(db), ws.data_ptr(), n, _stream())
+            _ptr(db), ws.data_ptr(), n, _raw_stream(dev))
         if rc:
             check(rc)
         return dx, da, db
@@ -250,7 +250,7 @@ class BalanceLoss:
         rc = self._lib.moe_balance_loss(s, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
                                         _ptr(seq_offsets), _ptr(weights), _ptr(dweights),
                                         loss.data_ptr(), counts.data_ptr(), _ptr(dlogits),
-                                        ws.data_ptr(), n, _stream())
+                                        ws.data_ptr(), n, _raw_stream(dev))
         if rc:
             check(rc)
         return loss, counts, dlogits
@@ -346,12 +346,12 @@ class AdamW:
         if grads is not None:
             self.bind_grads(grads)
         t = self.steps_done + 1 if step is None else step
-        o = self._options
+        dev, o = _device(), self._options
         if grad_scale is not None:
                 _check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
-                          device=_device())
+                          device=dev)
         o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
         o.weight_decay, o.step = self.weight_decay, t
-        check(load().moe_adamw_step(self._table, len(self.params), o, _stream()))
+        check(load().moe_adamw_step(self._table, len(self.params), o, _raw_stream(dev)))
         self.steps_done = t

@@ -23,9 +23,9 @@
 //
 // u and w are computed in float and leave as bf16 planes that add up to them:
 // hi = bf16(v), then mid (and lo) the rounded rests.  Two planes (an error
-// below 2^-17) feed the products that are rounded to bf16 or added to a
-// float base, three (2^-25) the float sums dA and dB.  A float dout is split the
-// same way.  Ranks are padded with zeros to RP = 16, 32, 64 or 128.
+// below 2^-17) feed the products that are rounded to bf16, three (2^-25) a
+// float out and the float sums dA and dB.  A float dout is split in three as
+// well.  Ranks are padded with zeros to RP = 16, 32, 64 or 128.
 #include <cuda_bf16.h>
 
 #include "cluster.cuh"
@@ -51,10 +51,13 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The low (high) halves of two words: element 0 (1) of two rows.
-template <int ODD>
-__device__ __forceinline__ uint32_t pair(uint32_t a, uint32_t b) {
-  return __byte_perm(a, b, ODD ? 0x7632 : 0x5410);
+// Long sums run in short pieces: an MMA truncates its sum to the accumulator's
+// last place, always downwards in magnitude, and a chain of hundreds of them
+// would drift by that bias (measured: 1e-6 of the result after 256 steps); the
+// pieces are added with rounding.
+__device__ __forceinline__ void add(float (&d)[4], const float (&s)[4]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) d[q] += s[q];
 }
 
 __device__ __forceinline__ uint32_t word(__nv_bfloat16 a, __nv_bfloat16 b) {
@@ -72,31 +75,43 @@ __device__ __forceinline__ uint32_t peel(float& x, float& y) {
   return word(a, b);
 }
 
-// 16 bytes of a stream that no other warp of the SM wants.
-__device__ __forceinline__ uint4 ldg16_stream(const void* p) {
-  uint4 q;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-               : "l"(p));
-  return q;
-}
 __device__ __forceinline__ uint4 ldg16(const void* p) { return __ldg(static_cast<const uint4*>(p)); }
 
-// W words (2 W bf16) at p, 4 W-byte aligned (16 for W >= 4).
-template <int W>
-__device__ __forceinline__ void load_words(const __nv_bfloat16* p, uint32_t (&o)[W]) {
-  if constexpr (W == 1) {
-    o[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-  } else if constexpr (W == 2) {
-    const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
-    o[0] = q.x, o[1] = q.y;
-  } else {
-#pragma unroll
-    for (int i = 0; i < W / 4; ++i) {
-      const uint4 q = ldg16(p + 8 * i);
-      o[4 * i] = q.x, o[4 * i + 1] = q.y, o[4 * i + 2] = q.z, o[4 * i + 3] = q.w;
-    }
-  }
+// 16 bytes into shared memory, asynchronously; zeros where !some.
+__device__ __forceinline__ void cp16(void* dst, const void* src, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src),
+               "r"(some ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {   // all but the last N groups have landed
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Four 8x8 matrices of bf16: lane l gives the address of row l % 8 of matrix
+// l / 8.
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Byte offset of 16-byte piece `c` of row `row` in a staged tile of ROW-byte
+// rows: pieces are permuted so that the 8 rows one matrix of an ldmatrix reads
+// lie in distinct banks.
+template <int ROW>
+__device__ __forceinline__ uint32_t piece(int row, int c) {
+  constexpr int P = ROW / 16;
+  const int x = P >= 8 ? row & 7 : P == 4 ? (row >> 1) & 3 : (row >> 2) & 1;
+  return static_cast<uint32_t>(row * ROW + 16 * (c ^ x));
 }
 
 // ------------------------------------------------------------ grouping
@@ -118,7 +133,7 @@ __host__ __device__ inline int64_t max_tiles(int64_t T, int64_t NA) {
 // a warp hands out slots to its tokens in order.
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __restrict__ ids,
                                                               int T, int NA, Groups g) {
-  extern __shared__ __align__(16) uint8_t sm[];
+  extern __shared__ __align__(128) uint8_t sm[];
   const int C = NA + 1;                 // columns: the adapters and "none"
   int32_t* hist = reinterpret_cast<int32_t*>(sm);   // [32][C]
   int32_t* count = hist + 32 * C;       // [C + 1] tokens
@@ -222,8 +237,9 @@ struct TileSource {
 template <bool SMALL>
 __device__ __forceinline__ bool find_tile(const TileSource& src, int i, Tile* tile, int32_t* tok) {
   if constexpr (!SMALL) {
-    if (i >= *src.num_tiles) return false;
-    const int4 q = src.tiles[i];
+    const int n = *src.num_tiles;
+    const int4 q = src.tiles[i];   // (allocated for every CTA's i; both loads in flight)
+    if (i >= n) return false;
     tile->adapter = q.x;
     tile->n = q.y;
     tile->slot = static_cast<int64_t>(i) * kTile;
@@ -262,11 +278,12 @@ __device__ __forceinline__ bool find_tile(const TileSource& src, int i, Tile* ti
 }
 
 // ------------------------------------------- w = s A x, u = s B^T dout
-// Low-rank rows leave as planes: `row` two planes [slots, RP], `col` three
-// planes [tiles, RP, kTile] (each may be null); slots past a tile's tokens are
-// zero.
+// Low-rank rows leave as planes: `row` two or three planes [slots, RP], `col`
+// three planes [tiles, RP, kTile] (each may be null); slots past a tile's
+// tokens are zero.
 struct Planes {
   __nv_bfloat16* row;
+  int32_t rows;        // row planes
   __nv_bfloat16* col;
   int64_t size;        // elements of a plane
 };
@@ -281,43 +298,71 @@ struct ShrinkArgs {
   int32_t r, K;        // K: contracted length
 };
 
-// Sums the CTA's WK partial tiles [WK][NTOK][RP + 1] in warp order, then the
-// cluster's in rank order, and writes the planes.
+// The four floats at `p` of each CTA of the cluster, added in rank order; the
+// loads of all of them in flight at once.
+__device__ __forceinline__ float4 cluster_sum4(const float* p, int S) {
+  if (S == 1) return *reinterpret_cast<const float4*>(p);
+  float4 v[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c)
+    if (c < S) v[c] = cluster_load4(p, c);
+#pragma unroll
+  for (int c = 1; c < 8; ++c)
+    if (c < S) v[0].x += v[c].x, v[0].y += v[c].y, v[0].z += v[c].z, v[0].w += v[c].w;
+  return v[0];
+}
+
+// Row stride (floats) of a CTA's partial tile of RP ranks.
+constexpr int red_stride(int RP) { return RP + 4; }
+
+// Each CTA of the cluster takes a share of the tile's tokens: it sums their
+// WK partial rows [WK][NTOK][RP + 4] over warps and CTAs, in that order, and
+// writes the planes.
 template <int RP, int WK, int NTOK>
 __device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float scale,
                                             const Planes& dst) {
-  constexpr int RS = RP + 1;
-  __syncthreads();
-  if constexpr (WK > 1) {
-    for (int i = threadIdx.x; i < NTOK * RS; i += kThreads) {
-      float v = red[i];
+  constexpr int RS = red_stride(RP);
+  const int S = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  if constexpr (WK > 2) {   // the CTA's own first: one round over the cluster
+    __syncthreads();
+    for (int i = threadIdx.x; i < NTOK * RS / 4; i += kThreads) {
+      float4 v[WK];
 #pragma unroll
-      for (int w = 1; w < WK; ++w) v += red[w * NTOK * RS + i];
-      red[i] = v;
+      for (int w = 0; w < WK; ++w) v[w] = reinterpret_cast<const float4*>(red + w * NTOK * RS)[i];
+#pragma unroll
+      for (int w = 1; w < WK; ++w)
+        v[0].x += v[w].x, v[0].y += v[w].y, v[0].z += v[w].z, v[0].w += v[w].w;
+      reinterpret_cast<float4*>(red)[i] = v[0];
     }
   }
-  const int S = static_cast<int>(cluster_size());
   if (S > 1) cluster_sync();
   else __syncthreads();
-  const int step = S * kThreads, start = static_cast<int>(cluster_rank()) * kThreads + threadIdx.x;
-  auto value = [&](int t, int j) {
-    if (S == 1) return red[t * RS + j] * scale;
-    float v = 0.f;
-    for (int c = 0; c < S; ++c) v += cluster_load(red + t * RS + j, c);
-    return v * scale;
-  };
+  const int per = NTOK / S, t0 = rank * per;
+  for (int i = threadIdx.x; i < per * RP / 4; i += kThreads) {
+    float* p = red + (t0 + i / (RP / 4)) * RS + i % (RP / 4) * 4;
+    float4 v = cluster_sum4(p, S);
+#pragma unroll
+    for (int w = 1; w < (WK > 2 ? 1 : WK); ++w) {
+      const float4 u = cluster_sum4(p + w * NTOK * RS, S);
+      v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
+    }
+    // these rows of this CTA are read by no other
+    *reinterpret_cast<float4*>(p) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+  }
+  __syncthreads();
   if (dst.row)
-    for (int i = start; i < NTOK * RP / 2; i += step) {   // two ranks of a token
-      const int t = i / (RP / 2), j = 2 * (i % (RP / 2));
-      float x = value(t, j), y = value(t, j + 1);
+    for (int i = threadIdx.x; i < per * RP / 2; i += kThreads) {   // two ranks of a token
+      const int t = t0 + i / (RP / 2), j = 2 * (i % (RP / 2));
+      float x = red[t * RS + j], y = red[t * RS + j + 1];
       __nv_bfloat16* o = dst.row + (tile.slot + t) * RP + j;
       *reinterpret_cast<uint32_t*>(o) = peel(x, y);
       *reinterpret_cast<uint32_t*>(o + dst.size) = peel(x, y);
+      if (dst.rows > 2) *reinterpret_cast<uint32_t*>(o + 2 * dst.size) = peel(x, y);
     }
   if (dst.col)
-    for (int i = start; i < NTOK * RP / 2; i += step) {   // two tokens of a rank
-      const int j = i / (NTOK / 2), t = 2 * (i % (NTOK / 2));
-      float x = value(t, j), y = value(t + 1, j);
+    for (int i = threadIdx.x; i < per * RP / 2; i += kThreads) {   // two tokens of a rank
+      const int j = i / (per / 2), t = t0 + 2 * (i % (per / 2));
+      float x = red[t * RS + j], y = red[(t + 1) * RS + j];
       __nv_bfloat16* o = dst.col + tile.slot * RP + j * kTile + t;
       *reinterpret_cast<uint32_t*>(o) = peel(x, y);
       *reinterpret_cast<uint32_t*>(o + dst.size) = peel(x, y);
@@ -326,33 +371,34 @@ __device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float 
   if (S > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
-// The 32-element chunks of K a warp contracts: its share of the cluster's.
-__device__ __forceinline__ int2 chunk_range(int K, int wk, int WK) {
-  const int chunks = (K + 31) / 32, parts = static_cast<int>(cluster_size()) * WK;
-  const int part = static_cast<int>(cluster_rank()) * WK + wk;
-  return make_int2(static_cast<int>(static_cast<int64_t>(chunks) * part / parts),
-                   static_cast<int>(static_cast<int64_t>(chunks) * (part + 1) / parts));
+// Chunks of `chunk` elements of K that part `part` of `parts` contracts.
+__device__ __forceinline__ int2 chunk_range(int K, int chunk, int part, int parts) {
+  const int64_t n = (K + chunk - 1) / chunk;
+  return make_int2(static_cast<int>(n * part / parts), static_cast<int>(n * (part + 1) / parts));
 }
 
-// Shapes of shrink_x: 8-token columns of a warp, warps side by side.
-template <int RT, bool SMALL>
-struct ShrinkX {
-  static constexpr int NTOK = SMALL ? kSmallTile : kTile;
-  static constexpr int NT = SMALL ? 2 : RT == 1 ? 8 : RT == 8 ? 2 : 4;
-  static constexpr int WT = NTOK / (8 * NT), WK = kWarps / WT;
-  static constexpr int RP = 16 * RT;
-  static constexpr size_t smem = sizeof(float) * WK * NTOK * (RP + 1);
+// Small batches: the cluster's warps share out the 32-element chunks of K.  Rank is
+// MMA-M, tokens are MMA-N: lane (g, t) of a chunk loads the 8 elements at 8 t
+// of rank rows g and g + 8 and of token g, two MMAs deep, straight from
+// global memory: a warp has a few chunks, all in flight at once.
+template <int RT>
+struct ShrinkSmall {
+  static constexpr int NT = kSmallTile / 8, RP = 16 * RT;
+  static constexpr size_t smem = sizeof(float) * kWarps * kSmallTile * red_stride(RP);
 };
 
-// Rank is MMA-M, tokens are MMA-N: lane (g, t) of a chunk loads the 8
-// elements at 8 t of rank rows g and g + 8 and of token g, two MMAs deep.
-template <int RT, bool SMALL>
-__device__ __forceinline__ void shrink_x_tile(const ShrinkArgs& a, const Tile& tile,
-                                              const int32_t* tok, float* red) {
-  using C = ShrinkX<RT, SMALL>;
-  constexpr int NT = C::NT, WT = C::WT, WK = C::WK, RS = C::RP + 1;
+template <int RT>
+__global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2) shrink_small_kernel(const ShrinkArgs a) {
+  using C = ShrinkSmall<RT>;
+  constexpr int NT = C::NT, RS = red_stride(C::RP);
+  extern __shared__ __align__(128) uint8_t sm[];
+  float* red = reinterpret_cast<float*>(sm);
+  __shared__ int32_t tok[kSmallTile];
+  griddep_wait();
+  griddep_launch_dependents();
+  Tile tile;
+  if (!find_tile<true>(a.tiles, blockIdx.x / cluster_size(), &tile, tok) || tile.adapter < 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int wt = warp % WT, wk = warp / WT;
   float acc[RT][NT][4];
 #pragma unroll
   for (int i = 0; i < RT; ++i)
@@ -360,202 +406,213 @@ __device__ __forceinline__ void shrink_x_tile(const ShrinkArgs& a, const Tile& t
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.src);
   const __nv_bfloat16* row[NT];          // null: no such token
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int i = 8 * (wt * NT + j) + g;
-    const int64_t id = SMALL ? tok[i] : a.tiles.perm[tile.slot + i];
-    row[j] = id >= 0 ? src + id * a.ld + 8 * t : nullptr;
+    const int64_t id = tok[8 * j + g];
+    row[j] = id >= 0 ? static_cast<const __nv_bfloat16*>(a.src) + id * a.ld + 8 * t : nullptr;
   }
-  const int live = min(NT, (tile.n - 8 * wt * NT + 7) / 8);   // columns with a token
+  const int live = (tile.n + 7) / 8;     // columns with a token
   const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.K + 8 * t;
-  const int2 c = chunk_range(a.K, wk, WK);
-  if (live > 0)
-#pragma unroll(SMALL ? 4 : 1)
-    for (int k = 32 * c.x; k < 32 * c.y; k += 32) {
-      const bool in = k + 8 * t < a.K;
-      uint4 p[RT][2], x[NT];
+  const int2 c = chunk_range(a.K, 32, static_cast<int>(cluster_rank()) * kWarps + warp,
+                             static_cast<int>(cluster_size()) * kWarps);
+#pragma unroll(RT >= 4 ? 2 : 4)
+  for (int k = 32 * c.x; k < 32 * c.y; k += 32) {
+    const bool in = k + 8 * t < a.K;
+    uint4 p[RT][2], x[NT];
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        x[j] = in && row[j] ? ldg16_stream(row[j] + k) : make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < NT; ++j)
+      x[j] = in && row[j] ? ldg16(row[j] + k) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int rank = 16 * i + 8 * h + g;
-          p[i][h] = in && rank < a.r ? ldg16(pool + static_cast<int64_t>(rank) * a.K + k)
-                                     : make_uint4(0, 0, 0, 0);
+      for (int h = 0; h < 2; ++h) {
+        const int rank = 16 * i + 8 * h + g;
+        p[i][h] = in && rank < a.r ? ldg16(pool + static_cast<int64_t>(rank) * a.K + k)
+                                   : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      if (j < live)
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          mma(acc[i][j], p[i][0].x, p[i][1].x, p[i][0].y, p[i][1].y, x[j].x, x[j].y);
+          mma(acc[i][j], p[i][0].z, p[i][1].z, p[i][0].w, p[i][1].w, x[j].z, x[j].w);
         }
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (j < live)
-#pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            mma(acc[i][j], p[i][0].x, p[i][1].x, p[i][0].y, p[i][1].y, x[j].x, x[j].y);
-            mma(acc[i][j], p[i][0].z, p[i][1].z, p[i][0].w, p[i][1].w, x[j].z, x[j].w);
-          }
-    }
-  float* mine = red + wk * C::NTOK * RS;
+  }
+  float* mine = red + warp * kSmallTile * RS;
 #pragma unroll
   for (int i = 0; i < RT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        mine[(8 * (wt * NT + j) + 2 * t + (q & 1)) * RS + 16 * i + g + 8 * (q >> 1)] = acc[i][j][q];
+        mine[(8 * j + 2 * t + (q & 1)) * RS + 16 * i + g + 8 * (q >> 1)] = acc[i][j][q];
   const float scale = a.scale ? __ldg(a.scale + tile.adapter) : 1.0f;
-  finish_tile<C::RP, WK, C::NTOK>(red, tile, scale, a.dst);
+  finish_tile<C::RP, kWarps, kSmallTile>(red, tile, scale, a.dst);
 }
 
-// Cluster of S CTAs per tile, all their warps sharing out the chunks of K.
-template <int RT, bool SMALL>
-__global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2) shrink_x_kernel(const ShrinkArgs a) {
-  extern __shared__ __align__(16) uint8_t sm[];
-  __shared__ int32_t tok[kSmallTile];
+// Tiles of 64 tokens: the CTA's chunks of 64 elements of K come into shared
+// memory by asynchronous copies, kStages deep (gathered rows of src, and the
+// pool's rows), and feed ldmatrix.  Tokens are MMA-M, 16 to a warp; the two
+// warps that share 16 tokens split the ranks, or at RT = 1 the chunk.
+//   !ROWS (x):    pool [r, K], its rows are the fragments' columns
+//   ROWS (dout):  pool [K, r], read through the transposing ldmatrix
+// A float src is staged as it is and split when it is read.
+template <int RT, bool ROWS, bool F32>
+struct Shrink {
+  static constexpr int RP = 16 * RT, KC = 64;
+  static constexpr int WN = RT >= 2 ? 2 : 1, WK = 2 / WN;   // warps along ranks, along K
+  static constexpr int NT = 2 * RT / WN;                    // 8-rank columns of a warp
+  static constexpr int SROW = F32 ? 4 * KC + 32 : 2 * KC;   // bytes of a staged row of src
+  static constexpr int PROW = ROWS ? 2 * RP : 2 * KC;       // and of the pool
+  static constexpr int SRC = kTile * SROW, POOL = (ROWS ? KC : RP) * PROW;
+  static constexpr int STAGE = SRC + POOL;
+  static constexpr int STAGES = STAGE <= 10240 ? 5 : STAGE <= 12288 ? 4 : 3;   // 4 CTAs an SM
+  static constexpr size_t red = sizeof(float) * WK * kTile * red_stride(RP);
+  static constexpr size_t smem = STAGES * STAGE > red ? STAGES * STAGE : red;
+};
+
+template <int RT, bool ROWS, bool F32>
+__device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& tile, uint8_t* sm) {
+  using C = Shrink<RT, ROWS, F32>;
+  constexpr int NT = C::NT, RS = red_stride(C::RP), KC = C::KC;
+  constexpr int XP = F32 ? 3 : 1;                      // planes of src
+  constexpr int ES = F32 ? 4 : 2;
+  constexpr int PIECES = KC * ES / 16;                 // 16-byte pieces of a row of src
+  constexpr int MINE = kTile * PIECES / kThreads;      // and a thread's
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wm = warp & 3, wo = warp >> 2;             // 16 tokens; ranks or part of the chunk
+  const int wn = C::WN == 2 ? wo : 0, wk = C::WK == 2 ? wo : 0;
+  float acc[NT][4];
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+  const uint8_t* row[MINE];                            // null: no such token
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    const int64_t id = a.tiles.perm[tile.slot + (threadIdx.x + i * kThreads) / PIECES];
+    row[i] = id >= 0 ? static_cast<const uint8_t*>(a.src) + id * a.ld * ES : nullptr;
+  }
+  const int sc = threadIdx.x % PIECES;                 // the thread's piece of its rows
+  const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.K;
+  const int2 c = chunk_range(a.K, KC, static_cast<int>(cluster_rank()), static_cast<int>(cluster_size()));
+  auto fetch = [&](int chunk) {
+    if (chunk < c.y) {
+      uint8_t* s = sm + (chunk - c.x) % C::STAGES * C::STAGE;
+      const int k = chunk * KC;
+#pragma unroll
+      for (int i = 0; i < MINE; ++i) {
+        const int r = (threadIdx.x + i * kThreads) / PIECES, at = k + sc * (16 / ES);
+        const bool some = row[i] && at < a.K;
+        cp16(s + (F32 ? static_cast<uint32_t>(r * C::SROW + 16 * sc) : piece<2 * KC>(r, sc)),
+             some ? row[i] + static_cast<int64_t>(at) * ES : static_cast<const uint8_t*>(a.src), some);
+      }
+      uint8_t* p = s + C::SRC;
+      constexpr int PP = C::PROW / 16, ALL = C::POOL / 16;
+#pragma unroll
+      for (int i = 0; i < (ALL + kThreads - 1) / kThreads; ++i) {
+        const int x = threadIdx.x + i * kThreads;
+        if (ALL % kThreads && x >= ALL) break;
+        const int r = x / PP, q = x % PP;              // row and piece
+        const int rank = ROWS ? 8 * q : r, kk = ROWS ? k + r : k + 8 * q;
+        const bool some = rank < a.r && kk < a.K;
+        cp16(p + piece<C::PROW>(r, q),
+             some ? pool + (ROWS ? static_cast<int64_t>(kk) * a.r + rank
+                                 : static_cast<int64_t>(rank) * a.K + kk)
+                  : a.pool, some);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) fetch(c.x + i);
+  for (int chunk = c.x; chunk < c.y; ++chunk) {
+    cp_wait<C::STAGES - 2>();
+    __syncthreads();
+    fetch(chunk + C::STAGES - 1);   // into the stage that every warp has left
+    const uint8_t* s = sm + (chunk - c.x) % C::STAGES * C::STAGE;
+    const uint32_t sp = smem_u32(s), pp = sp + C::SRC;
+    float part[NT][4];   // of this chunk (see `add`)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) part[j][q] = 0.f;
+#pragma unroll
+    for (int kk = 0; kk < KC / 16 / C::WK; ++kk) {
+      const int k16 = wk * (KC / 16 / C::WK) + kk;
+      uint32_t x[XP][4];
+      if constexpr (F32) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {   // rows g, g + 8; columns 2 t, 2 t + 8
+          float2 v = *reinterpret_cast<const float2*>(
+              s + (16 * wm + g + 8 * (q & 1)) * C::SROW + 4 * (16 * k16 + 8 * (q >> 1) + 2 * t));
+#pragma unroll
+          for (int p = 0; p < XP; ++p) x[p][q] = peel(v.x, v.y);
+        }
+      } else {
+        ldm4(x[0], sp + piece<2 * KC>(16 * wm + (lane & 15), 2 * k16 + (lane >> 4)));
+      }
+#pragma unroll
+      for (int j = 0; j < NT; j += 2) {   // two columns of 8 ranks
+        const int n = wn * NT + j;
+        uint32_t b[4];
+        if constexpr (ROWS)
+          ldm4t(b, pp + piece<C::PROW>(16 * k16 + (lane & 15), n + (lane >> 4)));
+        else
+          ldm4(b, pp + piece<C::PROW>(8 * n + (lane & 7) + 8 * (lane >> 4), 2 * k16 + ((lane >> 3) & 1)));
+#pragma unroll
+        for (int p = 0; p < XP; ++p) {
+          mma(part[j], x[p][0], x[p][1], x[p][2], x[p][3], b[0], b[1]);
+          mma(part[j + 1], x[p][0], x[p][1], x[p][2], x[p][3], b[2], b[3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NT; ++j) add(acc[j], part[j]);
+  }
+  cp_wait<0>();
+  __syncthreads();   // the stages become the partial tiles
+  float* red = reinterpret_cast<float*>(sm);
+  float* mine = red + wk * kTile * RS;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      mine[(16 * wm + g + 8 * (q >> 1)) * RS + 8 * (wn * NT + j) + 2 * t + (q & 1)] = acc[j][q];
+  const float scale = a.scale ? __ldg(a.scale + tile.adapter) : 1.0f;
+  finish_tile<C::RP, C::WK, kTile>(red, tile, scale, a.dst);
+}
+
+// Cluster of S CTAs per tile, sharing out the chunks of K.
+template <int RT>
+__global__ void __launch_bounds__(kThreads) shrink_x_kernel(const ShrinkArgs a) {
+  extern __shared__ __align__(128) uint8_t sm[];
   griddep_wait();
   griddep_launch_dependents();
   Tile tile;
-  if (!find_tile<SMALL>(a.tiles, blockIdx.x / cluster_size(), &tile, tok) || tile.adapter < 0) return;
-  shrink_x_tile<RT, SMALL>(a, tile, tok, reinterpret_cast<float*>(sm));
-}
-
-// Eight values of dout at p as four words of two bf16 (and, from float, the
-// words of the rests).
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, uint32_t (&hi)[4], uint32_t (&lo)[4]) {
-  if constexpr (F32) {
-    const uint4 q[2] = {ldg16_stream(p), ldg16_stream(static_cast<const uint4*>(p) + 1)};
-    const uint32_t* w = &q[0].x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      float x = __uint_as_float(w[2 * i]), y = __uint_as_float(w[2 * i + 1]);
-      hi[i] = peel(x, y);
-      lo[i] = peel(x, y);
-    }
-  } else {
-    const uint4 a = ldg16_stream(p);
-    hi[0] = a.x, hi[1] = a.y, hi[2] = a.z, hi[3] = a.w;
-  }
-}
-
-template <int RT>
-struct ShrinkD {
-  static constexpr int MT = RT == 1 ? 4 : RT == 2 ? 2 : 1;   // 16-token rows of a warp
-  static constexpr int WT = kTile / (16 * MT), WK = kWarps / WT;
-  static constexpr int RP = 16 * RT;
-  static constexpr size_t smem = sizeof(float) * WK * kTile * (RP + 1);
-};
-
-// As shrink_x with the pool contracted over its rows (B [N, r]): tokens are
-// MMA-M, ranks MMA-N.  Lane (g, t) takes the 8 pool rows at 8 t of a chunk,
-// ranks 2 RT g .. + 2 RT - 1; column g of rank tile i is rank 2 RT g + i, so
-// that a lane's words of two rows pair up into fragments.
-template <int RT, bool F32>
-__device__ __forceinline__ void shrink_d_tile(const ShrinkArgs& a, const Tile& tile, float* red) {
-  using C = ShrinkD<RT>;
-  constexpr int MT = C::MT, WT = C::WT, WK = C::WK, RS = C::RP + 1;
-  constexpr size_t ES = F32 ? 4 : 2;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int wt = warp % WT, wk = warp / WT;
-  float acc[MT][2 * RT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < 2 * RT; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
-  const uint8_t* row[MT][2];
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int64_t id = a.tiles.perm[tile.slot + 16 * (wt * MT + m) + 8 * h + g];
-      row[m][h] = id >= 0 ? static_cast<const uint8_t*>(a.src) + (id * a.ld + 8 * t) * ES : nullptr;
-    }
-  const int live = min(MT, (tile.n - 16 * wt * MT + 15) / 16);
-  const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.K;
-  const int2 c = chunk_range(a.K, wk, WK);
-  const int rank0 = 2 * RT * g;   // the lane's ranks exist, by halves of 8 at RT = 8
-  if (live > 0)
-    for (int k = 32 * c.x; k < 32 * c.y; k += 32) {
-      const bool in = k + 8 * t < a.K;
-      uint32_t w[8][RT];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const __nv_bfloat16* p = pool + static_cast<int64_t>(k + 8 * t + q) * a.r + rank0;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) w[q][i] = 0;
-        if constexpr (RT == 8) {
-          uint32_t h[4];
-          if (in && rank0 < a.r) {
-            load_words<4>(p, h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[q][i] = h[i];
-          }
-          if (in && rank0 + 8 < a.r) {
-            load_words<4>(p + 8, h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[q][4 + i] = h[i];
-          }
-        } else {
-          if (in && rank0 < a.r) load_words<RT>(p, w[q]);
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        if (m >= live) continue;
-        uint32_t h0[4] = {0, 0, 0, 0}, h1[4] = {0, 0, 0, 0}, l0[4] = {0, 0, 0, 0}, l1[4] = {0, 0, 0, 0};
-        if (in && row[m][0]) load8<F32>(row[m][0] + k * ES, h0, l0);
-        if (in && row[m][1]) load8<F32>(row[m][1] + k * ES, h1, l1);
-#pragma unroll
-        for (int half = 0; half < 2; ++half)
-#pragma unroll
-          for (int j = 0; j < RT; ++j) {
-            const uint32_t* const w0 = w[4 * half];
-            const uint32_t r0 = w0[j], r1 = w[4 * half + 1][j], r2 = w[4 * half + 2][j],
-                           r3 = w[4 * half + 3][j];
-            const uint32_t b[2][2] = {{pair<0>(r0, r1), pair<0>(r2, r3)},
-                                      {pair<1>(r0, r1), pair<1>(r2, r3)}};
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-              float(&d)[4] = acc[m][2 * j + o];
-              mma(d, h0[2 * half], h1[2 * half], h0[2 * half + 1], h1[2 * half + 1], b[o][0], b[o][1]);
-              if constexpr (F32)
-                mma(d, l0[2 * half], l1[2 * half], l0[2 * half + 1], l1[2 * half + 1], b[o][0], b[o][1]);
-            }
-          }
-      }
-    }
-  float* mine = red + wk * kTile * RS;
-#pragma unroll
-  for (int m = 0; m < MT; ++m)
-#pragma unroll
-    for (int j = 0; j < 2 * RT; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        mine[(16 * (wt * MT + m) + g + 8 * (q >> 1)) * RS + 2 * RT * (2 * t + (q & 1)) + j] = acc[m][j][q];
-  const float scale = a.scale ? __ldg(a.scale + tile.adapter) : 1.0f;
-  finish_tile<C::RP, WK, kTile>(red, tile, scale, a.dst);
+  if (!find_tile<false>(a.tiles, blockIdx.x / cluster_size(), &tile, nullptr) || tile.adapter < 0) return;
+  shrink_tile<RT, false, false>(a, tile, sm);
 }
 
 // Both of the backward's, in one launch: the first `d_units` clusters take
 // dout, the others x.
 template <int RT, bool F32>
-__global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
-    shrink_both_kernel(const ShrinkArgs d, const ShrinkArgs x, int d_units) {
-  extern __shared__ __align__(16) uint8_t sm[];
+__global__ void __launch_bounds__(kThreads) shrink_both_kernel(const ShrinkArgs d, const ShrinkArgs x,
+                                                               int d_units) {
+  extern __shared__ __align__(128) uint8_t sm[];
   griddep_wait();
   griddep_launch_dependents();
   int unit = blockIdx.x / cluster_size();
   Tile tile;
   if (unit < d_units) {
     if (!find_tile<false>(d.tiles, unit, &tile, nullptr) || tile.adapter < 0) return;
-    shrink_d_tile<RT, F32>(d, tile, reinterpret_cast<float*>(sm));
+    shrink_tile<RT, true, F32>(d, tile, sm);
   } else {
     unit -= d_units;
     if (!find_tile<false>(x.tiles, unit, &tile, nullptr) || tile.adapter < 0) return;
-    shrink_x_tile<RT, false>(x, tile, nullptr, reinterpret_cast<float*>(sm));
+    shrink_tile<RT, false, false>(x, tile, sm);
   }
 }
 
@@ -569,182 +626,211 @@ struct ExpandArgs {
   void* out;
   int64_t ld_out;
   int32_t r, N;          // N: output features
+  int32_t units;         // tiles at most
+  int32_t cols, parts;   // blocks of features, CTAs they are split among
 };
 
-// Eight consecutive values of the base (zero without one).
-template <bool F32>
-struct Base8 {
-  uint4 q[F32 ? 2 : 1];
-  __device__ __forceinline__ void load(const void* p) {
-#pragma unroll
-    for (int i = 0; i < (F32 ? 2 : 1); ++i)
-      q[i] = p ? static_cast<const uint4*>(p)[i] : make_uint4(0, 0, 0, 0);
-  }
-  // out = base + d, rounded once
-  __device__ __forceinline__ void store(void* out, const float (&d)[8]) const {
-    uint4 o[F32 ? 2 : 1];
-    const uint32_t* w = &q[0].x;
-    uint32_t* p = &o[0].x;
-    if constexpr (F32) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) p[i] = __float_as_uint(__uint_as_float(w[i]) + d[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        p[i] = word(__float2bfloat16_rn(__uint_as_float(w[i] << 16) + d[2 * i]),
-                    __float2bfloat16_rn(__uint_as_float(w[i] & 0xFFFF0000u) + d[2 * i + 1]));
-    }
-#pragma unroll
-    for (int i = 0; i < (F32 ? 2 : 1); ++i) static_cast<uint4*>(out)[i] = o[i];
-  }
-};
-
-// Features of a warp: as many as hold its fragments (RT / 4 registers each)
-// beside the accumulators.
-template <int RT>
-constexpr int expand_width() { return RT >= 4 ? 32 : 64; }
-
-// A warp takes a group of features, holds the pool's fragments of it and runs
-// the tile's tokens, 16 at a time.  Tokens are MMA-M, features MMA-N.
-//   !ROWS: pool [N, r]: column n of feature tile j is feature
-//          32 (j / 4) + 8 (n / 2) + 2 (j % 4) + n % 2
-//   ROWS:  pool [r, N]: lane (g, t) of a 16-rank step loads FL = 8 (4)
-//          features of rank rows 4 t .. + 3; column n of tile j is FL n + j
-// so that a lane ends with 8 consecutive features of its two tokens, twice.
-// The pool's, the base's and the tile's loads do not depend on the kernel
-// before (inputs, and lists that were complete before that one began): they
-// are issued ahead of the grid wait.
+// A CTA takes a tile and a range of features, FB at a time: the tile's rows of
+// the base and the pool's rows come into shared memory by asynchronous copies,
+// STAGES deep; tokens are MMA-M (16 a warp, w's planes in registers
+// throughout), features MMA-N; the sums go back into the staged base, rounded
+// once, and leave as whole rows.
+//   !ROWS: pool [N, r], its rows are the fragments' columns
+//   ROWS:  pool [r, N], read through the transposing ldmatrix
 template <int RT, bool ROWS, bool F32, bool SMALL>
-__device__ __forceinline__ void expand_tile(const ExpandArgs& a, const Tile& tile, int f,
-                                            const int32_t* tok) {
-  constexpr int FW = expand_width<RT>();
-  constexpr int JT = FW / 8;                  // 8-feature tiles of a warp
-  constexpr int FL = FW / 8;                  // ROWS: features a lane loads
-  constexpr int RP = 16 * RT;
-  constexpr int NB = FW / 32;                 // runs of 8 features of a lane
-  constexpr size_t ES = F32 ? 4 : 2;
-  constexpr int MT = SMALL ? 1 : kTile / 16;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint32_t b[RT][JT][2];
-  const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.N;
-#pragma unroll
-  for (int i = 0; i < RT; ++i) {
-    if constexpr (ROWS) {
-      uint32_t w[4][FL / 2];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int rank = 16 * i + 4 * t + q;
-#pragma unroll
-        for (int c = 0; c < FL / 2; ++c) w[q][c] = 0;
-        if (rank < a.r && f + FL * g < a.N)
-          load_words<FL / 2>(pool + static_cast<int64_t>(rank) * a.N + f + FL * g, w[q]);
-      }
-#pragma unroll
-      for (int j = 0; j < JT / 2; ++j) {
-        b[i][2 * j][0] = pair<0>(w[0][j], w[1][j]);
-        b[i][2 * j][1] = pair<0>(w[2][j], w[3][j]);
-        b[i][2 * j + 1][0] = pair<1>(w[0][j], w[1][j]);
-        b[i][2 * j + 1][1] = pair<1>(w[2][j], w[3][j]);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < JT; ++j) {
-        const int n = f + 32 * (j / 4) + 8 * (g >> 1) + 2 * (j % 4) + (g & 1), rank = 16 * i + 4 * t;
-        uint32_t w[2] = {0, 0};
-        if (n < a.N && rank < a.r) load_words<2>(pool + static_cast<int64_t>(n) * a.r + rank, w);
-        b[i][j][0] = w[0];
-        b[i][j][1] = w[1];
-      }
-    }
-  }
-  // first feature of the lane's run c
-  auto run = [&](int c) { return ROWS && FL == 8 ? f + 16 * t + 8 * c : f + 32 * c + 8 * t; };
-  const int live = (tile.n + 15) / 16;
-  griddep_wait();   // (again in backward_out_kernel: returns at once)
-#pragma unroll(ROWS || F32 || RT > 2 ? 1 : 2)
-  for (int m = 0; m < MT; ++m) {
-    if (m >= live) break;
-    int64_t row[2];
-    Base8<F32> base[2][NB];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int i = 16 * m + 8 * h + g;
-      row[h] = SMALL ? tok[i] : a.tiles.perm[tile.slot + i];
-      const uint8_t* p = a.base && row[h] >= 0
-                             ? static_cast<const uint8_t*>(a.base) + row[h] * a.ld_base * ES
-                             : nullptr;
-#pragma unroll
-      for (int c = 0; c < NB; ++c) base[h][c].load(p && run(c) < a.N ? p + run(c) * ES : nullptr);
-    }
-    float acc[JT][4];
-#pragma unroll
-    for (int j = 0; j < JT; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
-    const __nv_bfloat16* v = a.v.row + (tile.slot + 16 * m + g) * RP + 4 * t;
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int plane = 0; plane < 2; ++plane) {
-        const uint2 v0 = *reinterpret_cast<const uint2*>(v + plane * a.v.size + 16 * i);
-        const uint2 v1 = *reinterpret_cast<const uint2*>(v + plane * a.v.size + 8 * RP + 16 * i);
-#pragma unroll
-        for (int j = 0; j < JT; ++j) mma(acc[j], v0.x, v1.x, v0.y, v1.y, b[i][j][0], b[i][j][1]);
-      }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (row[h] < 0) continue;
-      uint8_t* out = static_cast<uint8_t*>(a.out) + row[h] * a.ld_out * ES;
-#pragma unroll
-      for (int c = 0; c < NB; ++c) {
-        float d[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if constexpr (ROWS && FL == 8) d[j] = acc[j][2 * h + c];
-          else if constexpr (ROWS) d[j] = acc[j % 4][2 * h + j / 4];
-          else d[j] = acc[4 * c + j / 2][2 * h + j % 2];
-        }
-        if (run(c) < a.N) base[h][c].store(out + run(c) * ES, d);
-      }
-    }
-  }
+struct Expand {
+  static constexpr int RP = 16 * RT, FB = 128;
+  // CTAs that share a tile's tokens: two where the base outweighs the pool's
+  // rows, which each of them stages (8192 tokens, rank 16, 7168 features:
+  // 73.1 us for the forward against 76.2)
+  static constexpr int SUB = SMALL || ROWS || RT > 2 ? 1 : 2;
+  static constexpr int NTOK = SMALL ? kSmallTile : kTile / SUB;
+  static constexpr int WT = NTOK / 16, WF = kWarps / WT;      // warps along tokens, features
+  static constexpr int NT = FB / 8 / WF;                      // 8-feature columns of a warp
+  static constexpr int ES = F32 ? 4 : 2;
+  static constexpr int BROW = FB * ES + (F32 ? 32 : 16);      // bytes of a staged row of the base
+  static constexpr int PROW = ROWS ? 2 * FB : 2 * RP;         // and of the pool
+  static constexpr int BASE = NTOK * BROW, POOL = (ROWS ? RP : FB) * PROW, V = NTOK * 2 * RP;
+  static constexpr int VN = F32 ? 3 : 2;                      // planes of w
+  static constexpr int STAGE = BASE + POOL;
+  static constexpr int STAGES = 3 * STAGE + VN * V <= 40 * 1024 ? 3 : 2;
+  static constexpr size_t smem = STAGES * STAGE + VN * V;
+  // CTAs an SM, for the split of the features: what shared memory holds, times
+  // the waves that measured best (a few: ragged tiles even out)
+  static constexpr int WAVES = SMALL ? 1 : ROWS ? 2 : 4;
+  static constexpr int RESIDENT = WAVES * (smem <= 36 * 1024 ? 6 : smem <= 45 * 1024 ? 5 : smem <= 56 * 1024 ? 4
+                                            : smem <= 75 * 1024 ? 3 : smem <= 113 * 1024 ? 2 : 1);
+};
+
+// Share `sub` of a tile's tokens; false: it has none.
+template <typename C>
+__device__ __forceinline__ bool take_share(int sub, Tile* tile) {
+  tile->slot += sub * C::NTOK;
+  tile->n = min(tile->n - sub * C::NTOK, C::NTOK);
+  return tile->n > 0;
 }
 
 // Tokens without an adapter: out = base, bit for bit (nothing to do when they
-// are the same memory); the warp's features.
+// are the same memory).
 template <bool F32, bool SMALL>
 __device__ __forceinline__ void copy_rows(const ExpandArgs& a, const Tile& tile, int f, int width,
                                           const int32_t* tok) {
-  constexpr size_t ES = F32 ? 4 : 2;
+  constexpr int ES = F32 ? 4 : 2;
   if (a.base == a.out && a.ld_base == a.ld_out) return;
-  const int per = width / 8, lane = threadIdx.x & 31;
-  for (int i = lane; i < tile.n * per; i += 32) {
-    const int row = i / per, n = f + 8 * (i % per);
+  const int per = width * ES / 16;
+  for (int i = threadIdx.x; i < tile.n * per; i += kThreads) {
+    const int row = i / per, n = f + i % per * (16 / ES);
     if (n >= a.N) continue;
     const int64_t id = SMALL ? tok[row] : a.tiles.perm[tile.slot + row];
-    Base8<F32> q;
-    q.load(a.base ? static_cast<const uint8_t*>(a.base) + (id * a.ld_base + n) * ES : nullptr);
-    uint4* out = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (id * a.ld_out + n) * ES);
-#pragma unroll
-    for (int c = 0; c < (F32 ? 2 : 1); ++c) out[c] = q.q[c];
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (a.base)
+      q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.base) + (id * a.ld_base + n) * ES);
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (id * a.ld_out + n) * ES) = q;
   }
 }
 
-// One CTA per (tile, 8 groups of features).
+// Blocks [c0, c1) of FB features of a tile.  The inputs' first loads (base,
+// pool, and the tile's lists, which were complete before the kernel before
+// this one began) are issued ahead of the grid wait.
+template <int RT, bool ROWS, bool F32, bool SMALL>
+__device__ __forceinline__ void expand_tile(const ExpandArgs& a, const Tile& tile, int c0, int c1,
+                                            const int32_t* tok, uint8_t* sm) {
+  using C = Expand<RT, ROWS, F32, SMALL>;
+  constexpr int RP = C::RP, ES = C::ES, NT = C::NT, FB = C::FB;
+  constexpr int PIECES = FB * ES / 16, MINE = (C::NTOK * PIECES + kThreads - 1) / kThreads;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wt = warp % C::WT, wf = warp / C::WT;
+  uint8_t* v_s = sm + C::STAGES * C::STAGE;
+  const int bc = threadIdx.x % PIECES * (16 / ES);   // the thread's piece of its rows
+  int row[MINE];                                     // -1: no such token
+#pragma unroll
+  for (int i = 0; i < MINE; ++i) {
+    const int r = (threadIdx.x + i * kThreads) / PIECES;
+    row[i] = r >= C::NTOK ? -1 : SMALL ? tok[r] : a.tiles.perm[tile.slot + r];
+  }
+  const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.N;
+  auto fetch = [&](int c, int stage) {
+    if (c < c1) {
+      uint8_t* s = sm + stage * C::STAGE;
+      const int f = c * FB;
+      if (a.base) {
+        const bool in = f + bc < a.N;
+#pragma unroll
+        for (int i = 0; i < MINE; ++i)
+          if (row[i] >= 0)
+            cp16(s + (threadIdx.x + i * kThreads) / PIECES * C::BROW + bc * ES,
+                 static_cast<const uint8_t*>(a.base) + (in ? row[i] * a.ld_base + f + bc : 0) * ES, in);
+      }
+      constexpr int PP = C::PROW / 16, ALL = C::POOL / 16;
+#pragma unroll
+      for (int i = 0; i < (ALL + kThreads - 1) / kThreads; ++i) {
+        const int x = threadIdx.x + i * kThreads;
+        if (ALL % kThreads && x >= ALL) break;
+        const int r = x / PP, q = x % PP;
+        const int rank = ROWS ? r : 8 * q, n = ROWS ? f + 8 * q : f + r;
+        const bool some = rank < a.r && n < a.N;
+        cp16(s + C::BASE + piece<C::PROW>(r, q),
+             some ? pool + (ROWS ? static_cast<int64_t>(rank) * a.N + n : static_cast<int64_t>(n) * a.r + rank)
+                  : a.pool, some);
+      }
+    }
+    cp_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 2; ++i) fetch(c0 + i, i);
+  fetch(c0 + C::STAGES - 2, C::STAGES - 2);
+  griddep_wait();   // (again in backward_out_kernel: returns at once)
+  constexpr int VP = RP / 8, ALLV = C::VN * C::NTOK * VP;   // pieces of a row of a plane, of all planes
+#pragma unroll
+  for (int i = 0; i < (ALLV + kThreads - 1) / kThreads; ++i) {
+    const int x = threadIdx.x + i * kThreads;
+    if (ALLV % kThreads && x >= ALLV) break;
+    const int p = x / (C::NTOK * VP), r = x / VP % C::NTOK, q = x % VP;
+    cp16(v_s + p * C::V + piece<2 * RP>(r, q), a.v.row + p * a.v.size + (tile.slot + r) * RP + 8 * q, true);
+  }
+  cp_commit();
+  cp_wait<0>();
+  __syncthreads();
+  const uint32_t vp = smem_u32(v_s);
+  uint32_t v[RT][C::VN][4];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int p = 0; p < C::VN; ++p)
+      ldm4(v[i][p], vp + p * C::V + piece<2 * RP>(16 * wt + (lane & 15), 2 * i + (lane >> 4)));
+  int stage = 0;
+  for (int c = c0; c < c1; ++c) {
+    fetch(c + C::STAGES - 1, stage == 0 ? C::STAGES - 1 : stage - 1);
+    cp_wait<C::STAGES - 1>();
+    __syncthreads();
+    uint8_t* s = sm + stage * C::STAGE;
+    const uint32_t pp = smem_u32(s) + C::BASE;
+    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+    if (16 * wt < tile.n) {
+#pragma unroll(RT == 1 ? 4 : 1)
+      for (int j = 0; j < NT; j += 2) {
+        const int n = wf * NT + j;   // two columns of 8 features
+        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+          uint32_t b[4];
+          if constexpr (ROWS)
+            ldm4t(b, pp + piece<C::PROW>(16 * i + (lane & 15), n + (lane >> 4)));
+          else
+            ldm4(b, pp + piece<C::PROW>(8 * n + (lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int p = 0; p < C::VN; ++p) {
+            mma(acc[0], v[i][p][0], v[i][p][1], v[i][p][2], v[i][p][3], b[0], b[1]);
+            mma(acc[1], v[i][p][0], v[i][p][1], v[i][p][2], v[i][p][3], b[2], b[3]);
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint8_t* o = s + (16 * wt + 8 * h + g) * C::BROW + (8 * (n + e) + 2 * t) * ES;
+            const float x = acc[e][2 * h], y = acc[e][2 * h + 1];
+            if constexpr (F32) {
+              const float2 q = a.base ? *reinterpret_cast<const float2*>(o) : make_float2(0.f, 0.f);
+              *reinterpret_cast<float2*>(o) = make_float2(q.x + x, q.y + y);
+            } else {
+              const uint32_t q = a.base ? *reinterpret_cast<const uint32_t*>(o) : 0u;
+              *reinterpret_cast<uint32_t*>(o) =
+                  word(__float2bfloat16_rn(__uint_as_float(q << 16) + x),
+                       __float2bfloat16_rn(__uint_as_float(q & 0xFFFF0000u) + y));
+            }
+          }
+      }
+    }
+    __syncthreads();
+    if (c * FB + bc < a.N) {
+#pragma unroll
+      for (int i = 0; i < MINE; ++i)
+        if (row[i] >= 0)
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (row[i] * a.ld_out + c * FB + bc) * ES) =
+              *reinterpret_cast<const uint4*>(s + (threadIdx.x + i * kThreads) / PIECES * C::BROW + bc * ES);
+    }
+    __syncthreads();   // before the stage is filled again
+  }
+  cp_wait<0>();
+}
+
 template <int RT, bool ROWS, bool F32, bool SMALL>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const ExpandArgs a) {
-  constexpr int FW = expand_width<RT>();
+  using C = Expand<RT, ROWS, F32, SMALL>;
+  extern __shared__ __align__(128) uint8_t sm[];
   __shared__ int32_t tok[kSmallTile];
   griddep_launch_dependents();
   Tile tile;
-  const bool some = find_tile<SMALL>(a.tiles, blockIdx.x, &tile, tok);
-  const int f = (blockIdx.y * kWarps + (threadIdx.x >> 5)) * FW;
-  if (some && f < a.N && tile.adapter >= 0) {
-    expand_tile<RT, ROWS, F32, SMALL>(a, tile, f, tok);
+  const int part = blockIdx.x / (a.units * C::SUB), unit = blockIdx.x - part * a.units * C::SUB;
+  const int c0 = a.cols * part / a.parts, c1 = a.cols * (part + 1) / a.parts;
+  const bool some = find_tile<SMALL>(a.tiles, unit / C::SUB, &tile, tok) && take_share<C>(unit % C::SUB, &tile);
+  if (some && tile.adapter >= 0) {
+    expand_tile<RT, ROWS, F32, SMALL>(a, tile, c0, c1, tok, sm);
     return;
   }
   griddep_wait();   // every CTA: this kernel ends after the one before it
-  if (some && f < a.N) copy_rows<F32, SMALL>(a, tile, f, FW, tok);
+  if (some) copy_rows<F32, SMALL>(a, tile, c0 * C::FB, (c1 - c0) * C::FB, tok);
 }
 
 // ------------------------------------------------- dA = sum u x^T, dB
@@ -761,124 +847,167 @@ struct GradArgs {
   int32_t transposed;
 };
 
-// Features a lane loads: 8 while the accumulators (16 RT x 8 FL floats a warp)
-// leave room for two CTAs an SM.
+// A CTA's tile of the gradient: RP ranks x 128 features; warps 16 ranks x 128 / (8 / RT)
+// features each.  The adapter's tokens come TK slots at a time: the
+// col planes of u and the gathered rows of x, by asynchronous copies, STAGES
+// deep.
 template <int RT, bool F32>
-constexpr int grad_fl() { return RT == 1 || (RT == 2 && !F32) ? 8 : 4; }
-template <int RT, bool F32>
-constexpr size_t grad_smem() {
-  return sizeof(float) * kWarps * 16 * RT * (8 * grad_fl<RT, F32>() + 1);
-}
+struct Grad {
+  static constexpr int RP = 16 * RT, FB = 128;
+  static constexpr int TK = RT <= 2 ? kTile : kTile / 2;  // slots of a stage
+  static constexpr int WF = kWarps / RT;                 // warps along the features
+  static constexpr int NT = FB / 8 / WF;                 // 8-feature columns of a warp
+  static constexpr int XROW = F32 ? 4 * FB + 16 : 2 * FB;
+  static constexpr int X = TK * XROW, U = RP * 2 * TK;   // U: one plane
+  static constexpr int STAGE = X + 3 * U;
+  static constexpr int STAGES = 3 * STAGE <= 72 * 1024 ? 3 : 2;
+  static constexpr size_t red = sizeof(float) * RP * (FB + 4);
+  static constexpr size_t smem = STAGES * STAGE > red ? STAGES * STAGE : red;
+};
 
-// Cluster of C CTAs per (range of 8 FL features, adapter): the adapter's
-// tokens by 16, warp by warp over the cluster.  Ranks are MMA-M, features
-// MMA-N, tokens contracted: lane (g, t) loads FL features of the token rows
-// 4 t .. + 3, and ranks g and g + 8 of those tokens from the col planes.
+// Cluster of C CTAs per (128 features, adapter), sharing out the adapter's
+// stages.  Ranks are MMA-M, features MMA-N, tokens contracted.
 template <int RT, bool F32>
-__device__ __forceinline__ void grad_part(const GradArgs& a, int slab, int adapter, float* red) {
-  constexpr int FL = grad_fl<RT, F32>();
-  constexpr int FW = 8 * FL, RP = 16 * RT, RS = FW + 1;
-  constexpr int XP = F32 ? 3 : 1;   // planes of the features
-  constexpr size_t ES = F32 ? 4 : 2;
+__device__ __forceinline__ void grad_part(const GradArgs& a, int slab, int adapter, uint8_t* sm) {
+  using G = Grad<RT, F32>;
+  constexpr int NT = G::NT, RP = G::RP, FB = G::FB, RS = FB + 4, TK = G::TK;
+  constexpr int XP = F32 ? 3 : 1;                       // planes of the features
+  constexpr int ES = F32 ? 4 : 2;
+  constexpr int PIECES = FB * ES / 16, MINE = TK * PIECES / kThreads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int wf = warp % G::WF, wr = warp / G::WF;
   const int C = static_cast<int>(cluster_size()), rank_c = static_cast<int>(cluster_rank());
-  const int f = slab * FW;
-  const int steps = (a.counts[adapter] + 15) / 16;
+  const int f = slab * FB;
+  const int steps = (a.counts[adapter] + TK - 1) / TK;   // stages of TK slots
   const int64_t slot0 = static_cast<int64_t>(a.first[adapter]) * kTile;
-  float acc[RT][FL][4];
+  float acc[NT][4];
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < FL; ++j)
+    for (int q = 0; q < 4; ++q) acc[j][q] = 0.f;
+  const int xc = threadIdx.x % PIECES;                  // the thread's piece of its rows
+  const bool in = f + xc * (16 / ES) < a.N;
+  const uint8_t* src = static_cast<const uint8_t*>(a.src) + (f + xc * (16 / ES)) * static_cast<int64_t>(ES);
+  int ids[MINE];                                        // rows of the stage to fetch next
+  auto tokens = [&](int i) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
-  const bool in = f + FL * g < a.N;
-  const uint8_t* src = static_cast<const uint8_t*>(a.src) + (f + FL * g) * ES;
-  const int stride = C * kWarps;
-  int s = rank_c * kWarps + warp;
-  int4 id = make_int4(-1, -1, -1, -1);
-  if (s < steps) id = *reinterpret_cast<const int4*>(a.perm + slot0 + 16 * s + 4 * t);
-  for (; s < steps; s += stride) {
-    uint32_t w[XP][4][FL / 2];
-    const int ids[4] = {id.x, id.y, id.z, id.w};
+    for (int m = 0; m < MINE; ++m)
+      ids[m] = i < steps ? a.perm[slot0 + i * TK + (threadIdx.x + m * kThreads) / PIECES] : -1;
+  };
+  auto fetch = [&](int i, int stage) {
+    if (i < steps) {
+      uint8_t* s = sm + stage * G::STAGE;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+      for (int m = 0; m < MINE; ++m) {
+        const int r = (threadIdx.x + m * kThreads) / PIECES;
+        const bool some = in && ids[m] >= 0;
+        cp16(s + (F32 ? static_cast<uint32_t>(r * G::XROW + 16 * xc) : piece<2 * FB>(r, xc)),
+             some ? src + static_cast<int64_t>(ids[m]) * a.ld * ES : static_cast<const uint8_t*>(a.src), some);
+      }
+      const int64_t at = slot0 + i * TK;   // the planes are [tile, RP, kTile]
+      const __nv_bfloat16* u = a.left + at / kTile * (RP * kTile) + at % kTile;
+      constexpr int UP = TK / 8, ALL = 3 * RP * UP;
 #pragma unroll
-      for (int x = 0; x < XP; ++x)
-#pragma unroll
-        for (int c = 0; c < FL / 2; ++c) w[x][q][c] = 0;
-      if (in && ids[q] >= 0) {
-        const uint8_t* p = src + static_cast<int64_t>(ids[q]) * a.ld * ES;
-        if constexpr (F32) {
-#pragma unroll
-          for (int c = 0; c < FL / 4; ++c) {
-            const float4 v = __ldg(reinterpret_cast<const float4*>(p) + c);
-            float e[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-              w[x][q][2 * c] = peel(e[0], e[1]);
-              w[x][q][2 * c + 1] = peel(e[2], e[3]);
-            }
-          }
-        } else {
-          load_words<FL / 2>(reinterpret_cast<const __nv_bfloat16*>(p), w[0][q]);
-        }
+      for (int m = 0; m < (ALL + kThreads - 1) / kThreads; ++m) {
+        const int x = threadIdx.x + m * kThreads;
+        if (ALL % kThreads && x >= ALL) break;
+        const int plane = x / (RP * UP), r = x / UP % RP, q = x % UP;
+        cp16(s + G::X + plane * G::U + piece<2 * TK>(r, q), u + plane * a.plane + r * kTile + 8 * q, true);
       }
     }
-    // [tile, RP, kTile]: 16 consecutive slots of a rank row
-    const int64_t at = slot0 + 16 * s;
-    const __nv_bfloat16* u = a.left + at / kTile * (RP * kTile) + at % kTile + g * kTile + 4 * t;
-    if (s + stride < steps)
-      id = *reinterpret_cast<const int4*>(a.perm + at + 16 * stride + 4 * t);
+    cp_commit();
+  };
+  int next = rank_c;                                    // the stage whose rows ids names
+  tokens(next);
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+  for (int i = 0; i < G::STAGES - 1; ++i) {
+    fetch(next, i);
+    next += C;
+    tokens(next);
+  }
+  int stage = 0;
+  for (int i = rank_c; i < steps; i += C) {
+    cp_wait<G::STAGES - 2>();
+    __syncthreads();
+    fetch(next, stage == 0 ? G::STAGES - 1 : stage - 1);   // the stage that every warp has left
+    next += C;
+    tokens(next);
+    const uint8_t* s = sm + stage * G::STAGE;
+    const uint32_t xp = smem_u32(s), up = xp + G::X;
+    stage = stage + 1 == G::STAGES ? 0 : stage + 1;
+    uint32_t u[TK / 16][3][4];
 #pragma unroll
-      for (int plane = 0; plane < 3; ++plane) {
-        const __nv_bfloat16* up = u + plane * a.plane + 16 * i * kTile;
-        const uint2 u0 = *reinterpret_cast<const uint2*>(up);
-        const uint2 u1 = *reinterpret_cast<const uint2*>(up + 8 * kTile);
+    for (int k = 0; k < TK / 16; ++k)
 #pragma unroll
-        for (int x = 0; x < XP; ++x) {
-          if (plane + x > 2) continue;   // below the float sums' own rounding
+      for (int p = 0; p < 3; ++p)
+        ldm4(u[k][p], up + p * G::U + piece<2 * TK>(16 * wr + (lane & 15), 2 * k + (lane >> 4)));
 #pragma unroll
-          for (int j = 0; j < FL / 2; ++j) {
-            const uint32_t r0 = w[x][0][j], r1 = w[x][1][j], r2 = w[x][2][j], r3 = w[x][3][j];
-            mma(acc[i][2 * j], u0.x, u1.x, u0.y, u1.y, pair<0>(r0, r1), pair<0>(r2, r3));
-            mma(acc[i][2 * j + 1], u0.x, u1.x, u0.y, u1.y, pair<1>(r0, r1), pair<1>(r2, r3));
+    for (int j = 0; j < NT; j += 2) {
+      const int n = wf * NT + j;                        // two columns of 8 features
+      float part[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};   // of this stage (see `add`)
+#pragma unroll
+      for (int k = 0; k < TK / 16; ++k) {
+        uint32_t b[XP][4];
+        if constexpr (F32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {                 // token pairs 2 t, 2 t + 8; columns n, n + 1
+            const uint8_t* e = s + (16 * k + 2 * t + 8 * (q & 1)) * G::XROW + 4 * (8 * (n + (q >> 1)) + g);
+            float x = *reinterpret_cast<const float*>(e), y = *reinterpret_cast<const float*>(e + G::XROW);
+#pragma unroll
+            for (int p = 0; p < XP; ++p) b[p][q] = peel(x, y);
           }
+        } else {
+          ldm4t(b[0], xp + piece<2 * FB>(16 * k + (lane & 15), n + (lane >> 4)));
         }
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+#pragma unroll
+          for (int x = 0; x < XP; ++x) {
+            if (p + x > 2) continue;                    // below the float sums' own rounding
+            mma(part[0], u[k][p][0], u[k][p][1], u[k][p][2], u[k][p][3], b[x][0], b[x][1]);
+            mma(part[1], u[k][p][0], u[k][p][1], u[k][p][2], u[k][p][3], b[x][2], b[x][3]);
+          }
       }
+      add(acc[j], part[0]);
+      add(acc[j + 1], part[1]);
+    }
   }
-  // the warps' sums in warp order, then the cluster's in rank order
-  float* mine = red + warp * RP * RS;
+  cp_wait<0>();
+  __syncthreads();   // the stages become the CTA's tile
+  float* red = reinterpret_cast<float*>(sm);
 #pragma unroll
-  for (int i = 0; i < RT; ++i)
+  for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int j = 0; j < FL; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        mine[(16 * i + g + 8 * (q >> 1)) * RS + FL * (2 * t + (q & 1)) + j] = acc[i][j][q];
-  __syncthreads();
-  for (int i = threadIdx.x; i < RP * RS; i += kThreads) {
-    float v = red[i];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) v += red[w * RP * RS + i];
-    red[i] = v;
-  }
+    for (int q = 0; q < 4; ++q)
+      red[(16 * wr + g + 8 * (q >> 1)) * RS + 8 * (wf * NT + j) + 2 * t + (q & 1)] = acc[j][q];
   if (C > 1) cluster_sync();
   else __syncthreads();
-  const int cols = min(FW, a.N - f), total = a.r * cols;
+  // each CTA of the cluster sums and writes a share of the tile
   float* out = a.out + static_cast<int64_t>(adapter) * a.r * a.N;
-  for (int i = rank_c * kThreads + threadIdx.x; i < total; i += C * kThreads) {
-    int j, n;
-    if (a.transposed) n = i / a.r, j = i - n * a.r;
-    else j = i / cols, n = i - j * cols;
-    float v = 0.f;
-    if (C == 1) v = red[j * RS + n];
-    else
-      for (int c = 0; c < C; ++c) v += cluster_load(red + j * RS + n, c);
-    if (a.transposed) out[static_cast<int64_t>(f + n) * a.r + j] = v;
-    else out[static_cast<int64_t>(j) * a.N + f + n] = v;
+  if (!a.transposed) {   // of the ranks: rows of dA
+    const int per = RP / C, j0 = rank_c * per;
+    for (int i = threadIdx.x; i < per * FB / 4; i += kThreads) {
+      const int j = j0 + i / (FB / 4), n = i % (FB / 4) * 4;
+      if (j < a.r && f + n < a.N)
+        *reinterpret_cast<float4*>(out + static_cast<int64_t>(j) * a.N + f + n) =
+            cluster_sum4(red + j * RS + n, C);
+    }
+  } else {               // of the features: rows of dB
+    const int per = FB / C, n0 = rank_c * per;
+    if (C > 1) {
+      for (int i = threadIdx.x; i < RP * per / 4; i += kThreads) {
+        float* p = red + i / (per / 4) * RS + n0 + i % (per / 4) * 4;
+        *reinterpret_cast<float4*>(p) = cluster_sum4(p, C);   // read by no other CTA
+      }
+      __syncthreads();
+    }
+    const int quads = a.r / 4;
+    for (int i = threadIdx.x; i < per * quads; i += kThreads) {
+      const int n = n0 + i / quads, j = i % quads * 4;
+      if (f + n < a.N)
+        *reinterpret_cast<float4*>(out + static_cast<int64_t>(f + n) * a.r + j) =
+            make_float4(red[j * RS + n], red[(j + 1) * RS + n], red[(j + 2) * RS + n], red[(j + 3) * RS + n]);
+    }
   }
   if (C > 1) cluster_sync();
 }
@@ -889,32 +1018,32 @@ struct OutArgs {
   GradArgs da, db;
   ExpandArgs dx;
   int32_t da_slabs, db_slabs, NA;   // slabs 0: not wanted
-  int32_t dx_cols;
 };
 
 template <int RT, bool F32>
-__global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2) backward_out_kernel(const OutArgs a) {
-  extern __shared__ __align__(16) uint8_t sm[];
-  float* red = reinterpret_cast<float*>(sm);
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) backward_out_kernel(const OutArgs a) {
+  extern __shared__ __align__(128) uint8_t sm[];
   griddep_wait();
   griddep_launch_dependents();
   const int C = static_cast<int>(cluster_size());
   int unit = blockIdx.x / C;
   const int na = a.da_slabs * a.NA, nb = a.db_slabs * a.NA;
   if (unit < na) {
-    grad_part<RT, false>(a.da, unit % a.da_slabs, unit / a.da_slabs, red);
+    grad_part<RT, false>(a.da, unit % a.da_slabs, unit / a.da_slabs, sm);
   } else if (unit < na + nb) {
     unit -= na;
-    grad_part<RT, F32>(a.db, unit % a.db_slabs, unit / a.db_slabs, red);
+    grad_part<RT, F32>(a.db, unit % a.db_slabs, unit / a.db_slabs, sm);
   } else {
-    constexpr int FW = expand_width<RT>();
+    using E = Expand<RT, true, false, false>;
     const int cta = blockIdx.x - (na + nb) * C;
-    const int ti = cta / a.dx_cols;
-    const int f = ((cta - ti * a.dx_cols) * kWarps + (threadIdx.x >> 5)) * FW;
+    const int part = cta / (a.dx.units * E::SUB), ti = cta - part * a.dx.units * E::SUB;
+    const int c0 = a.dx.cols * part / a.dx.parts, c1 = a.dx.cols * (part + 1) / a.dx.parts;
     Tile tile;
-    if (!find_tile<false>(a.dx.tiles, ti, &tile, nullptr) || f >= a.dx.N) return;
-    if (tile.adapter < 0) copy_rows<false, false>(a.dx, tile, f, FW, nullptr);
-    else expand_tile<RT, true, false, false>(a.dx, tile, f, nullptr);
+    if (part >= a.dx.parts || !find_tile<false>(a.dx.tiles, ti / E::SUB, &tile, nullptr) ||
+        !take_share<E>(ti % E::SUB, &tile))
+      return;
+    if (tile.adapter < 0) copy_rows<false, false>(a.dx, tile, c0 * E::FB, (c1 - c0) * E::FB, nullptr);
+    else expand_tile<RT, true, false, false>(a.dx, tile, c0, c1, nullptr, sm);
   }
 }
 
@@ -947,8 +1076,8 @@ AdapterWs adapter_ws(const moe_adapter_shape* s, bool backward) {
     w.tiles = take(w.units * 16);
     w.num_tiles = take(4);
   }
-  // two row planes; backward: three col planes of u and of w as well
-  w.planes = take(w.plane * 2 * (backward ? 8 : 2));
+  // three row planes, or (backward) two of u and three col planes of u and of w
+  w.planes = take(w.plane * 2 * (backward ? 8 : 3));
   w.total = off > 0 ? off : kWsAlign;
   return w;
 }
@@ -1011,31 +1140,47 @@ cudaError_t launch_group(const int32_t* ids, int T, int NA, const Groups& g, cud
   return launch_pdl(group_kernel, dim3(1), dim3(kGroupThreads), smem, st, ids, T, NA, g);
 }
 
-// CTAs that share a tile: powers of two up to 8, while all clusters are
-// resident at once (two CTAs an SM) and every warp has a chunk of 32 to
-// contract.
-int shrink_cluster(int64_t units, int K, int warps_k, int sms) {
+// CTAs that share a tile: powers of two up to 8, while the clusters fill no
+// more than `resident` CTAs an SM and every CTA keeps `least` elements of K.
+int shrink_cluster(int64_t units, int K, int resident, int least, int sms) {
   int c = 1;
-  while (c < 8 && units * c <= sms && K >= 32 * 2 * c * warps_k) c *= 2;
+  while (c < 8 && 2 * units * c <= static_cast<int64_t>(resident) * sms && K >= 2 * c * least) c *= 2;
   return c;
 }
 
 template <int RT, bool SMALL>
 cudaError_t launch_shrink_x(const ShrinkArgs& a, int64_t units, int sms, cudaStream_t st) {
-  using S = ShrinkX<RT, SMALL>;
+  using S = Shrink<RT, false, false>;
   static DeviceOnce once;
-  const cudaError_t e = set_smem_limit_once(shrink_x_kernel<RT, SMALL>, S::smem, once);
+  auto kern = SMALL ? shrink_small_kernel<RT> : shrink_x_kernel<RT>;
+  constexpr size_t smem = SMALL ? ShrinkSmall<RT>::smem : S::smem;
+  const cudaError_t e = set_smem_limit_once(kern, smem, once);
   if (e != cudaSuccess) return e;
-  const int c = shrink_cluster(units, a.K, S::WK, sms);
-  return launch_cluster(shrink_x_kernel<RT, SMALL>, dim3(static_cast<unsigned>(units * c)), c, S::smem,
-                        st, a);
+  const int c = SMALL ? shrink_cluster(units, a.K, 2, 32 * kWarps, sms)
+                      : shrink_cluster(units, a.K, 4, 4 * S::KC, sms);
+  return launch_cluster(kern, dim3(static_cast<unsigned>(units * c)), c, smem, st, a);
+}
+
+// Splits the features of expand's tiles into C::RESIDENT CTAs an SM.
+template <typename C>
+void split_features(ExpandArgs* a, int sms) {
+  a->cols = (a->N + C::FB - 1) / C::FB;
+  int64_t want = static_cast<int64_t>(C::RESIDENT) * sms / (static_cast<int64_t>(a->units) * C::SUB);
+  if (want < 1) want = 1;
+  a->parts = static_cast<int32_t>(want < a->cols ? want : a->cols);
 }
 
 template <int RT, bool F32, bool SMALL>
-cudaError_t launch_expand(const ExpandArgs& a, int64_t units, cudaStream_t st) {
-  constexpr int unit = kWarps * expand_width<RT>();
-  const dim3 grid(static_cast<unsigned>(units), static_cast<unsigned>((a.N + unit - 1) / unit));
-  return launch_pdl(expand_kernel<RT, false, F32, SMALL>, grid, dim3(kThreads), 0, st, a);
+cudaError_t launch_expand(ExpandArgs a, int sms, cudaStream_t st) {
+  using C = Expand<RT, false, F32, SMALL>;
+  static DeviceOnce once;
+  const cudaError_t e = set_smem_limit_once(expand_kernel<RT, false, F32, SMALL>, C::smem, once);
+  if (e != cudaSuccess) return e;
+  split_features<C>(&a, sms);
+  const int64_t ctas = static_cast<int64_t>(a.units) * C::SUB * a.parts;
+  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
+  return launch_pdl(expand_kernel<RT, false, F32, SMALL>, dim3(static_cast<unsigned>(ctas)),
+                    dim3(kThreads), C::smem, st, a);
 }
 
 template <int RT, bool SMALL>
@@ -1043,8 +1188,8 @@ cudaError_t launch_forward(const ShrinkArgs& sa, const ExpandArgs& ea, bool f32,
                            int sms, cudaStream_t st) {
   const cudaError_t e = launch_shrink_x<RT, SMALL>(sa, units, sms, st);
   if (e != cudaSuccess) return e;
-  return f32 ? launch_expand<RT, true, SMALL>(ea, units, st)
-             : launch_expand<RT, false, SMALL>(ea, units, st);
+  return f32 ? launch_expand<RT, true, SMALL>(ea, sms, st)
+             : launch_expand<RT, false, SMALL>(ea, sms, st);
 }
 
 template <bool SMALL>
@@ -1070,32 +1215,33 @@ struct Backward {
 template <int RT, bool F32>
 cudaError_t launch_backward(const Backward& b, cudaStream_t st) {
   static DeviceOnce once_s, once_o;
-  constexpr size_t xs = ShrinkX<RT, false>::smem, ds = ShrinkD<RT>::smem;
+  constexpr size_t xs = Shrink<RT, false, false>::smem, ds = Shrink<RT, true, F32>::smem;
   constexpr size_t smem_s = xs > ds ? xs : ds;
   cudaError_t e = set_smem_limit_once(shrink_both_kernel<RT, F32>, smem_s, once_s);
   if (e != cudaSuccess) return e;
   const int64_t both = b.units * (b.want_x ? 2 : 1);
   // (the same split whichever outputs are wanted: their sums do not depend on it)
-  int c = shrink_cluster(2 * b.units, b.x.K > b.d.K ? b.x.K : b.d.K, ShrinkX<RT, false>::WK, b.sms);
+  int c = shrink_cluster(2 * b.units, b.x.K > b.d.K ? b.x.K : b.d.K, 4, 4 * 64, b.sms);
   e = launch_cluster(shrink_both_kernel<RT, F32>, dim3(static_cast<unsigned>(both * c)), c, smem_s, st,
                      b.d, b.x, static_cast<int>(b.units));
   if (e != cudaSuccess) return e;
-  constexpr size_t gx = grad_smem<RT, false>(), gd = grad_smem<RT, F32>();
-  constexpr size_t smem_o = gx > gd ? gx : gd;
+  constexpr size_t gx = Grad<RT, false>::smem, gd = Grad<RT, F32>::smem;
+  using E = Expand<RT, true, false, false>;
+  constexpr size_t gm = gx > gd ? gx : gd, smem_o = gm > E::smem ? gm : E::smem;
   e = set_smem_limit_once(backward_out_kernel<RT, F32>, smem_o, once_o);
   if (e != cudaSuccess) return e;
   OutArgs o = b.out;
-  const int fx = 8 * grad_fl<RT, false>(), fd = 8 * grad_fl<RT, F32>(), fe = kWarps * expand_width<RT>();
+  const int fb = Grad<RT, F32>::FB;
   o.NA = b.NA;
-  o.da_slabs = b.want_x ? (o.da.N + fx - 1) / fx : 0;
-  o.db_slabs = b.want_x ? (o.db.N + fd - 1) / fd : 0;
-  o.dx_cols = (o.dx.N + fe - 1) / fe;
+  o.da_slabs = b.want_x ? (o.da.N + fb - 1) / fb : 0;
+  o.db_slabs = b.want_x ? (o.db.N + fb - 1) / fb : 0;
+  split_features<E>(&o.dx, b.sms);
   const int64_t grads = static_cast<int64_t>(o.da_slabs + o.db_slabs) * b.NA;
   // CTAs that share an adapter's tokens: while the gradients' units leave SMs
-  // idle and each CTA has a round of 16 tokens a warp
+  // idle and each has a tile or two
   c = 1;
-  while (c < 8 && grads * c < 2 * b.sms && b.T >= 2 * c * 16 * kWarps) c *= 2;
-  int64_t ctas = b.want_dx ? b.units * o.dx_cols : 0;
+  while (c < 8 && grads * c < 2 * b.sms && b.T >= 2 * c * kTile) c *= 2;
+  int64_t ctas = b.want_dx ? b.units * E::SUB * o.dx.parts : 0;
   ctas = grads * c + (ctas + c - 1) / c * c;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
   return launch_cluster(backward_out_kernel<RT, F32>, dim3(static_cast<unsigned>(ctas)), c, smem_o, st, o);
@@ -1140,7 +1286,7 @@ AdapterCall adapter_call(const moe_adapter_shape* s, bool backward, const int32_
 
 // row / col: the plane each set of planes begins at, -1 for none.
 ShrinkArgs shrink_args(const AdapterCall& c, const void* src, int64_t ld, const void* pool,
-                       const float* scale, int row, int col, int r, int K) {
+                       const float* scale, int row, int rows, int col, int r, int K) {
   ShrinkArgs a;
   a.tiles = c.tiles;
   a.src = src;
@@ -1148,6 +1294,7 @@ ShrinkArgs shrink_args(const AdapterCall& c, const void* src, int64_t ld, const 
   a.pool = static_cast<const __nv_bfloat16*>(pool);
   a.scale = scale;
   a.dst.row = row < 0 ? nullptr : c.planes + row * c.w.plane;
+  a.dst.rows = rows;
   a.dst.col = col < 0 ? nullptr : c.planes + col * c.w.plane;
   a.dst.size = c.w.plane;
   a.r = r;
@@ -1160,6 +1307,7 @@ ExpandArgs expand_args(const AdapterCall& c, const void* pool, const void* base,
   ExpandArgs a;
   a.tiles = c.tiles;
   a.v.row = c.planes;
+  a.v.rows = 0;
   a.v.col = nullptr;
   a.v.size = c.w.plane;
   a.pool = static_cast<const __nv_bfloat16*>(pool);
@@ -1169,6 +1317,8 @@ ExpandArgs expand_args(const AdapterCall& c, const void* pool, const void* base,
   a.ld_out = ld_out;
   a.r = r;
   a.N = N;
+  a.cols = a.parts = 0;
+  a.units = static_cast<int32_t>(c.w.units);
   return a;
 }
 
@@ -1235,9 +1385,9 @@ extern "C" int32_t moe_adapter_forward(const moe_adapter_shape* s, const void* x
   if ((rc = check_device(&sms)) != MOE_OK) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const AdapterCall c = adapter_call(s, false, adapter_ids, workspace);
-  const ShrinkArgs sa = shrink_args(c, x, ld_x, a, scale, 0, -1, s->rank, s->in_features);
   const ExpandArgs ea = expand_args(c, b, base, ld_base, out, ld_out, s->rank, s->out_features);
   const bool f32 = s->out_dtype == MOE_DTYPE_F32;
+  const ShrinkArgs sa = shrink_args(c, x, ld_x, a, scale, 0, f32 ? 3 : 2, -1, s->rank, s->in_features);
   if (c.w.small) return entry_launched(forward_products<true>(sa, ea, f32, c.w.units, sms, st));
   cudaError_t e = launch_group(adapter_ids, s->num_tokens, s->num_adapters, c.g, st);
   if (e == cudaSuccess) e = forward_products<false>(sa, ea, f32, c.w.units, sms, st);
@@ -1284,8 +1434,8 @@ extern "C" int32_t moe_adapter_backward(const moe_adapter_shape* s, const void* 
   const AdapterCall c = adapter_call(s, true, adapter_ids, workspace);
   constexpr int kURow = 0, kUCol = 2, kWCol = 5;   // first planes
   Backward w;
-  w.d = shrink_args(c, dout, ld_dout, b, scale, dx ? kURow : -1, da ? kUCol : -1, r, N);
-  w.x = shrink_args(c, x, ld_x, a, scale, -1, kWCol, r, H);
+  w.d = shrink_args(c, dout, ld_dout, b, scale, dx ? kURow : -1, 2, da ? kUCol : -1, r, N);
+  w.x = shrink_args(c, x, ld_x, a, scale, -1, 0, kWCol, r, H);
   w.want_x = da != nullptr;
   w.out.da = grad_args(c, kUCol, x, ld_x, da, r, H, false);
   w.out.db = grad_args(c, kWCol, dout, ld_dout, db, r, N, true);

@@ -37,9 +37,13 @@ __device__ __forceinline__ int32_t cluster_load(const int32_t* p, uint32_t rank)
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
   return v;
 }
-__device__ __forceinline__ float cluster_load(const float* p, uint32_t rank) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(p, rank)) : "memory");
+// Volatile keeps these behind the barrier; without a memory clobber a run of
+// them stays in flight together.
+__device__ __forceinline__ float4 cluster_load4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr(p, rank)));
   return v;
 }
 
