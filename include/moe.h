@@ -347,6 +347,10 @@ typedef struct {
   int32_t out_dtype;      /* MOE_DTYPE_*: base, out and dout */
 } moe_adapter_shape;
 
+/* Forwards of at most this many tokens run as one kernel and use no
+ * workspace: it may be NULL then. */
+#define MOE_ADAPTER_SMALL_TOKENS 256
+
 /* Workspace bytes of moe_adapter_forward (backward = 0) or
  * moe_adapter_backward (1).  0 for an invalid shape. */
 size_t moe_adapter_workspace_size(const moe_adapter_shape* shape, int32_t backward);
@@ -388,7 +392,8 @@ int32_t moe_adapter_backward(const moe_adapter_shape* shape, const void* dout, i
                              void* stream);
 
 /* Limits: num_tokens >= 0; 1 <= num_experts <= 1024; 1 <= top_k <=
- * min(num_experts, 32); 1 <= num_sequences <= 2^20; coef finite. */
+ * min(num_experts, 32); num_tokens * top_k < 2^31; 1 <= num_sequences <= 2^20;
+ * coef finite. */
 typedef struct {
   int32_t num_tokens;      /* T */
   int32_t num_experts;     /* E */

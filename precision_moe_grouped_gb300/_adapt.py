@@ -12,8 +12,9 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from ._lib import (MOE_ADAMW_BLOCK, MOE_DTYPE_BF16, MOE_DTYPE_F32, AdamwOptions, AdamwTensor,
-                   AdapterShape, BalanceShape, _bad, _check_tensor, check, load)
+from ._lib import (MOE_ADAMW_BLOCK, MOE_ADAPTER_SMALL_TOKENS, MOE_DTYPE_BF16, MOE_DTYPE_F32,
+                   AdamwOptions, AdamwTensor, AdapterShape, BalanceShape, _bad, _check_tensor,
+                   check, load)
 
 torch = None   # bound when the first object is made: the build imports this package without it
 _raw_stream = None
@@ -140,10 +141,10 @@ class LowRankAdapters:
         else:
             ld_out = _check_rows(out, "out", dtype, shape, dev)
         s, n = self._call(T, kind, 0)
-        ws = _scratch(n, x)
+        ws = None if T <= MOE_ADAPTER_SMALL_TOKENS else _scratch(n, x)
         rc = self._lib.moe_adapter_forward(
             s, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
-            _ptr(self.scale), _ptr(base), ld_base, out.data_ptr(), ld_out, ws.data_ptr(), n,
+            _ptr(self.scale), _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(ws), n,
             _raw_stream(dev))
         if rc:
             check(rc)
@@ -243,14 +244,15 @@ class BalanceLoss:
         n = self._sizes.get(S)
         if n is None:   # it depends on the sequences alone
             n = self._sizes[S] = self._size(s)
-        ws = _scratch(n, logits)
-        loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+        # the loss and, 256 bytes on, the workspace
+        ws = torch.empty(64 + (n + 3) // 4, dtype=torch.float32, device=logits.device)
+        loss = ws.narrow(0, 0, 1)
         counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
         dlogits = torch.empty_like(logits) if need_grad else None
         rc = self._lib.moe_balance_loss(s, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
                                         _ptr(seq_offsets), _ptr(weights), _ptr(dweights),
                                         loss.data_ptr(), counts.data_ptr(), _ptr(dlogits),
-                                        ws.data_ptr(), n, _raw_stream(dev))
+                                        ws.data_ptr() + 256, n, _raw_stream(dev))
         if rc:
             check(rc)
         return loss, counts, dlogits

@@ -96,17 +96,35 @@ __device__ __forceinline__ void block_scale(uint32_t amax_bits, float* inv, floa
   *scale = some ? __fdiv_rn(amax, 448.0f) : 1.0f;
 }
 
-__device__ __forceinline__ uint32_t e4m3(float x, float inv) {
-  return __nv_cvt_float_to_fp8(__fmul_rn(x, inv), __NV_SATFINITE, __NV_E4M3);
+// Codes of four values times inv, first in the low byte; `least` (zero or the
+// least positive value) below which a positive value does not go.
+template <bool POSITIVE>
+__device__ __forceinline__ uint32_t encode4(const float* x, float inv, float least) {
+  float q[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    q[c] = __fmul_rn(x[c], inv);
+    if (POSITIVE && x[c] > 0.f) q[c] = fmaxf(q[c], least);
+  }
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
 }
 
-__device__ __forceinline__ float from_e4m3(uint32_t code) {
-  const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3);
-  return __half2float(__half(h));
+// Four codes times their scale.
+__device__ __forceinline__ void decode4(uint32_t codes, float scale, float* o) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(codes >> (16 * h)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(r));
+    o[2 * h] = __fmul_rn(f.x, scale);
+    o[2 * h + 1] = __fmul_rn(f.y, scale);
+  }
 }
 
 template <bool BF16G>
-__device__ __forceinline__ void load_grad4(const void* g, int64_t i, float (&o)[4]) {
+__device__ __forceinline__ void load_grad4(const void* g, int i, float* o) {
   if constexpr (BF16G) {
     const uint2 q = __ldcs(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(g) + i));
     o[0] = __uint_as_float(q.x << 16);
@@ -120,17 +138,153 @@ __device__ __forceinline__ void load_grad4(const void* g, int64_t i, float (&o)[
 }
 
 template <bool BF16G>
-__device__ __forceinline__ float load_grad(const void* g, int64_t i) {
+__device__ __forceinline__ float load_grad(const void* g, int i) {
   if constexpr (BF16G) return __bfloat162float(static_cast<const __nv_bfloat16*>(g)[i]);
   else return static_cast<const float*>(g)[i];
 }
 
-// One CTA per chunk of 2048 elements of one tensor; a warp holds 256
-// consecutive ones (an 8-bit block), lane l the groups of four at 4 l and
-// 128 + 4 l.
+// 256 consecutive elements from w0 (an 8-bit block) by one warp, lane l the
+// groups of four at 4 l and 128 + 4 l.  VEC: all of them exist, and every pointer
+// allows 4-element accesses.
+template <bool BITS8, bool BF16G, bool VEC>
+__device__ __forceinline__ void take_block(const Entry& t, int64_t w0, const Scalars& s, float gs) {
+  const int lane = threadIdx.x & 31;
+  const int64_t i0 = w0 + 4 * lane;
+  float* const tp = t.p + i0;
+  const void* const tg = BF16G ? static_cast<const void*>(static_cast<const __nv_bfloat16*>(t.g) + i0)
+                               : static_cast<const void*>(static_cast<const float*>(t.g) + i0);
+  float* const tm = static_cast<float*>(t.m) + i0;
+  float* const tv = static_cast<float*>(t.v) + i0;
+  uint8_t* const cm = static_cast<uint8_t*>(t.m) + i0;
+  uint8_t* const cv = static_cast<uint8_t*>(t.v) + i0;
+  __nv_bfloat16* const tc = t.copy ? t.copy + i0 : nullptr;
+  const int left = VEC ? 256 : static_cast<int>(min(t.n - i0, static_cast<int64_t>(256)));
+  auto has = [&](int k) { return k < left; };   // element i0 + k exists
+  float p[8], g[8], m[8], v[8];
+  float ms = 1.f, vs = 1.f;
+  if constexpr (BITS8) {
+    ms = t.m_scale[w0 / kBlock8];
+    vs = t.v_scale[w0 / kBlock8];
+  }
+  uint32_t mc[2] = {0, 0}, vc[2] = {0, 0};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if constexpr (VEC) {
+      load_grad4<BF16G>(tg, 128 * j, g + 4 * j);
+      const float4 q = __ldcs(reinterpret_cast<const float4*>(tp + 128 * j));
+      p[4 * j] = q.x, p[4 * j + 1] = q.y, p[4 * j + 2] = q.z, p[4 * j + 3] = q.w;
+      if constexpr (BITS8) {
+        mc[j] = __ldcs(reinterpret_cast<const uint32_t*>(cm + 128 * j));
+        vc[j] = __ldcs(reinterpret_cast<const uint32_t*>(cv + 128 * j));
+      } else {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(tm + 128 * j));
+        const float4 b = __ldcs(reinterpret_cast<const float4*>(tv + 128 * j));
+        m[4 * j] = a.x, m[4 * j + 1] = a.y, m[4 * j + 2] = a.z, m[4 * j + 3] = a.w;
+        v[4 * j] = b.x, v[4 * j + 1] = b.y, v[4 * j + 2] = b.z, v[4 * j + 3] = b.w;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {   // an element beyond the tensor's end is zero and stays zero
+        const int k = 128 * j + c, e = 4 * j + c;
+        p[e] = g[e] = m[e] = v[e] = 0.f;
+        if (has(k)) {
+          g[e] = load_grad<BF16G>(tg, k);
+          p[e] = tp[k];
+          if constexpr (BITS8) {
+            mc[j] |= static_cast<uint32_t>(cm[k]) << (8 * c);
+            vc[j] |= static_cast<uint32_t>(cv[k]) << (8 * c);
+          } else {
+            m[e] = tm[k];
+            v[e] = tv[k];
+          }
+        }
+      }
+    }
+  }
+  uint32_t ma = 0, ra = 0;
+  float r[8];
+  if constexpr (BITS8) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      decode4(mc[j], ms, m + 4 * j);
+      decode4(vc[j], vs, v + 4 * j);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    const float vo = BITS8 ? __fmul_rn(v[c], v[c]) : v[c];
+    const Moments o = update(p[c], s.grad_scale ? __fmul_rn(g[c], gs) : g[c], m[c], vo, s);
+    p[c] = o.p, m[c] = o.m, v[c] = o.v, r[c] = o.r;
+    if constexpr (BITS8) {
+      ma = max(ma, __float_as_uint(o.m) & 0x7FFFFFFFu);
+      ra = max(ra, __float_as_uint(o.r) & 0x7FFFFFFFu);
+    }
+  }
+  if constexpr (BITS8) {
+    float minv, rinv;
+    ma = __reduce_max_sync(0xFFFFFFFFu, ma);
+    ra = __reduce_max_sync(0xFFFFFFFFu, ra);
+    block_scale(ma, &minv, &ms);
+    block_scale(ra, &rinv, &vs);
+    if (lane == 0) {
+      t.m_scale[w0 / kBlock8] = ms;
+      t.v_scale[w0 / kBlock8] = vs;
+    }
+    const float least = rinv > 0.f ? 0.001953125f : 0.f;   // 2^-9, the least code's value
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      mc[j] = encode4<false>(m + 4 * j, minv, 0.f);
+      vc[j] = encode4<true>(r + 4 * j, rinv, least);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if constexpr (VEC) {
+      __stcs(reinterpret_cast<float4*>(tp + 128 * j),
+             make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]));
+      if (tc) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(p[4 * j], p[4 * j + 1]);
+        const __nv_bfloat162 b = __floats2bfloat162_rn(p[4 * j + 2], p[4 * j + 3]);
+        uint2 q;
+        memcpy(&q.x, &a, 4);
+        memcpy(&q.y, &b, 4);
+        __stcs(reinterpret_cast<uint2*>(tc + 128 * j), q);
+      }
+      if constexpr (BITS8) {
+        __stcs(reinterpret_cast<uint32_t*>(cm + 128 * j), mc[j]);
+        __stcs(reinterpret_cast<uint32_t*>(cv + 128 * j), vc[j]);
+      } else {
+        __stcs(reinterpret_cast<float4*>(tm + 128 * j),
+               make_float4(m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]));
+        __stcs(reinterpret_cast<float4*>(tv + 128 * j),
+               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int k = 128 * j + c, e = 4 * j + c;
+        if (!has(k)) continue;
+        tp[k] = p[e];
+        if (tc) tc[k] = __float2bfloat16_rn(p[e]);
+        if constexpr (BITS8) {
+          cm[k] = static_cast<uint8_t>(mc[j] >> (8 * c));
+          cv[k] = static_cast<uint8_t>(vc[j] >> (8 * c));
+        } else {
+          tm[k] = m[e];
+          tv[k] = v[e];
+        }
+      }
+    }
+  }
+}
+
+// One CTA per chunk of one tensor, a block of 256 a warp.  One block and no
+// more: the next CTA's loads then run under this one's arithmetic, about 70
+// instructions an element with 8-bit moments (200 M elements: 542 us at six
+// CTAs an SM; 720 with two blocks a warp in turn).
 template <bool BITS8, bool BF16G, int CAP>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ Table<CAP> tab,
-                                                         const Scalars s) {
+__global__ void __launch_bounds__(kThreads, BITS8 ? 6 : 4)
+    adamw_kernel(const __grid_constant__ Table<CAP> tab, const Scalars s) {
   const int chunk = blockIdx.x;
   int lo = 0, hi = tab.count;   // the last entry that begins at or before this chunk
   while (hi - lo > 1) {
@@ -140,140 +294,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   }
   const Entry& t = tab.e[lo];
   griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w0 = static_cast<int64_t>(chunk - t.first_chunk) * kChunk + (threadIdx.x >> 5) * 256;
-  const int64_t n = t.n;
-  if (w0 >= n) return;
-  const bool vec = t.vec && w0 + 256 <= n;
   const float gs = s.grad_scale ? __ldg(s.grad_scale) : 1.0f;
-  float p[8], g[8], m[8], v[8];
-  float ms = 1.f, vs = 1.f;
-  if constexpr (BITS8) {
-    ms = t.m_scale[w0 / kBlock8];
-    vs = t.v_scale[w0 / kBlock8];
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t i = w0 + 128 * j + 4 * lane;
-    float gg[4] = {0.f, 0.f, 0.f, 0.f}, pp[4] = {0.f, 0.f, 0.f, 0.f};
-    float mm[4] = {0.f, 0.f, 0.f, 0.f}, vv[4] = {0.f, 0.f, 0.f, 0.f};
-    if (vec) {
-      load_grad4<BF16G>(t.g, i, gg);
-      const float4 q = __ldcs(reinterpret_cast<const float4*>(t.p + i));
-      pp[0] = q.x, pp[1] = q.y, pp[2] = q.z, pp[3] = q.w;
-      if constexpr (BITS8) {
-        const uint32_t mc = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(t.m) + i));
-        const uint32_t vc = __ldcs(reinterpret_cast<const uint32_t*>(static_cast<uint8_t*>(t.v) + i));
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mm[c] = from_e4m3((mc >> (8 * c)) & 0xFF);
-          vv[c] = from_e4m3((vc >> (8 * c)) & 0xFF);
-        }
-      } else {
-        const float4 a = __ldcs(reinterpret_cast<const float4*>(static_cast<float*>(t.m) + i));
-        const float4 b = __ldcs(reinterpret_cast<const float4*>(static_cast<float*>(t.v) + i));
-        mm[0] = a.x, mm[1] = a.y, mm[2] = a.z, mm[3] = a.w;
-        vv[0] = b.x, vv[1] = b.y, vv[2] = b.z, vv[3] = b.w;
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (i + c < n) {
-          gg[c] = load_grad<BF16G>(t.g, i + c);
-          pp[c] = t.p[i + c];
-          if constexpr (BITS8) {
-            mm[c] = from_e4m3(static_cast<uint8_t*>(t.m)[i + c]);
-            vv[c] = from_e4m3(static_cast<uint8_t*>(t.v)[i + c]);
-          } else {
-            mm[c] = static_cast<float*>(t.m)[i + c];
-            vv[c] = static_cast<float*>(t.v)[i + c];
-          }
-        }
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      p[4 * j + c] = pp[c], g[4 * j + c] = gg[c], m[4 * j + c] = mm[c], v[4 * j + c] = vv[c];
-  }
-  uint32_t ma = 0, ra = 0;
-  float r[8];
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float mo = m[c], vo = v[c];
-    if constexpr (BITS8) {
-      mo = __fmul_rn(mo, ms);
-      vo = __fmul_rn(vo, vs);
-      vo = __fmul_rn(vo, vo);
-    }
-    const float gc = s.grad_scale ? __fmul_rn(g[c], gs) : g[c];
-    const Moments o = update(p[c], gc, mo, vo, s);
-    p[c] = o.p, m[c] = o.m, v[c] = o.v, r[c] = o.r;
-    if constexpr (BITS8) {
-      // an element beyond the tensor's end is zero and stays zero
-      ma = max(ma, __float_as_uint(o.m) & 0x7FFFFFFFu);
-      ra = max(ra, __float_as_uint(o.r) & 0x7FFFFFFFu);
-    }
-  }
-  float minv = 0.f, rinv = 0.f;
-  if constexpr (BITS8) {
-    ma = __reduce_max_sync(0xFFFFFFFFu, ma);
-    ra = __reduce_max_sync(0xFFFFFFFFu, ra);
-    block_scale(ma, &minv, &ms);
-    block_scale(ra, &rinv, &vs);
-    if (lane == 0) {
-      t.m_scale[w0 / kBlock8] = ms;
-      t.v_scale[w0 / kBlock8] = vs;
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t i = w0 + 128 * j + 4 * lane;
-    uint32_t mc[4], vc[4];
-    if constexpr (BITS8) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        mc[c] = e4m3(m[4 * j + c], minv);
-        vc[c] = e4m3(r[4 * j + c], rinv);
-        if (vc[c] == 0 && r[4 * j + c] > 0.f && rinv > 0.f) vc[c] = 1;
-      }
-    }
-    if (vec) {
-      __stcs(reinterpret_cast<float4*>(t.p + i),
-             make_float4(p[4 * j], p[4 * j + 1], p[4 * j + 2], p[4 * j + 3]));
-      if (t.copy) {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(p[4 * j], p[4 * j + 1]);
-        const __nv_bfloat162 b = __floats2bfloat162_rn(p[4 * j + 2], p[4 * j + 3]);
-        uint2 q;
-        memcpy(&q.x, &a, 4);
-        memcpy(&q.y, &b, 4);
-        __stcs(reinterpret_cast<uint2*>(t.copy + i), q);
-      }
-      if constexpr (BITS8) {
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.m) + i),
-               mc[0] | mc[1] << 8 | mc[2] << 16 | mc[3] << 24);
-        __stcs(reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(t.v) + i),
-               vc[0] | vc[1] << 8 | vc[2] << 16 | vc[3] << 24);
-      } else {
-        __stcs(reinterpret_cast<float4*>(static_cast<float*>(t.m) + i),
-               make_float4(m[4 * j], m[4 * j + 1], m[4 * j + 2], m[4 * j + 3]));
-        __stcs(reinterpret_cast<float4*>(static_cast<float*>(t.v) + i),
-               make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]));
-      }
-    } else {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (i + c < n) {
-          t.p[i + c] = p[4 * j + c];
-          if (t.copy) t.copy[i + c] = __float2bfloat16_rn(p[4 * j + c]);
-          if constexpr (BITS8) {
-            static_cast<uint8_t*>(t.m)[i + c] = static_cast<uint8_t>(mc[c]);
-            static_cast<uint8_t*>(t.v)[i + c] = static_cast<uint8_t>(vc[c]);
-          } else {
-            static_cast<float*>(t.m)[i + c] = m[4 * j + c];
-            static_cast<float*>(t.v)[i + c] = v[4 * j + c];
-          }
-        }
-    }
-  }
+  const int64_t w0 = static_cast<int64_t>(chunk - t.first_chunk) * kChunk + (threadIdx.x >> 5) * kBlock8;
+  if (w0 >= t.n) return;
+  if (t.vec && w0 + kBlock8 <= t.n) take_block<BITS8, BF16G, true>(t, w0, s, gs);
+  else take_block<BITS8, BF16G, false>(t, w0, s, gs);
 }
 
 template <int CAP>

@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kTile = 64;            // tokens of a tile
 constexpr int kSmallTile = 16;       // and of a small batch's
-constexpr int kSmallTokens = 256;
+constexpr int kSmallTokens = MOE_ADAPTER_SMALL_TOKENS;
 constexpr int kGroupThreads = 1024;
 constexpr int kWarps = 8;            // warps of the product kernels
 constexpr int kThreads = 32 * kWarps;
@@ -222,7 +222,7 @@ struct Tile {
   int64_t slot;
 };
 
-// Where the tiles come from: the group kernel's lists, or (SMALL) the ids.
+// Where the tiles come from: the group kernel's lists, or (small batches) the ids.
 struct TileSource {
   const int32_t* ids;
   int32_t T, NA;
@@ -231,51 +231,71 @@ struct TileSource {
   const int32_t* num_tiles;
 };
 
-// SMALL: CTA t of the grid leads the tile that begins with token t, if t is
-// the first, 17th, 33rd, ... token of its adapter: the token and the next 15
-// that share it.  False: no tile.  tok [kSmallTile] receives the tokens.
-template <bool SMALL>
-__device__ __forceinline__ bool find_tile(const TileSource& src, int i, Tile* tile, int32_t* tok) {
-  if constexpr (!SMALL) {
-    const int n = *src.num_tiles;
-    const int4 q = src.tiles[i];   // (allocated for every CTA's i; both loads in flight)
-    if (i >= n) return false;
-    tile->adapter = q.x;
-    tile->n = q.y;
-    tile->slot = static_cast<int64_t>(i) * kTile;
-    return true;
-  } else {
-    static_assert(kSmallTokens <= kThreads, "a thread per token");
-    __shared__ unsigned same[kThreads / 32];
-    const unsigned NA = static_cast<unsigned>(src.NA);
-    const int want = src.ids[i], mine = static_cast<int>(threadIdx.x) < src.T ? src.ids[threadIdx.x] : 0;
-    const bool none = static_cast<unsigned>(want) >= NA;
-    const bool eq = static_cast<int>(threadIdx.x) < src.T &&
-                    (none ? static_cast<unsigned>(mine) >= NA : mine == want);
-    const unsigned b = __ballot_sync(0xFFFFFFFFu, eq);
-    if ((threadIdx.x & 31) == 0) same[threadIdx.x >> 5] = b;
-    if (threadIdx.x < kSmallTile) tok[threadIdx.x] = -1;
-    __syncthreads();
-    int before_i = 0, before_me = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      const int n = __popc(same[w]);
-      total += n;
-      if (w < (i >> 5)) before_i += n;
-      if (w < static_cast<int>(threadIdx.x >> 5)) before_me += n;
-    }
-    before_i += __popc(same[i >> 5] & ((1u << (i & 31)) - 1));
-    before_me += __popc(b & ((1u << (threadIdx.x & 31)) - 1));
-    if (before_i % kSmallTile != 0) return false;
-    if (eq && before_me >= before_i && before_me < before_i + kSmallTile)
-      tok[before_me - before_i] = static_cast<int32_t>(threadIdx.x);
-    __syncthreads();
-    tile->adapter = none ? -1 : want;
-    tile->n = min(kSmallTile, total - before_i);
-    tile->slot = static_cast<int64_t>(i) * kSmallTile;
-    return true;
-  }
+__device__ __forceinline__ bool find_tile(const TileSource& src, int i, Tile* tile) {
+  const int n = *src.num_tiles;
+  const int4 q = src.tiles[i];   // (allocated for every CTA's i; both loads in flight)
+  if (i >= n) return false;
+  tile->adapter = q.x;
+  tile->n = q.y;
+  tile->slot = static_cast<int64_t>(i) * kTile;
+  return true;
 }
+
+// Small batches: the tiles of up to 16 tokens that share an adapter, found by
+// every CTA for itself.  Thread t holds token t: its adapter (NA: none, -1: no
+// such token), its rank among that adapter's tokens, and a bit of `leaders`
+// where a tile begins with it (ranks 0, 16, 32, ...).
+struct SmallTiles {
+  int id, rank, count;   // count: tiles
+
+  // ids [kThreads], leaders [kThreads / 32] in shared memory.
+  __device__ __forceinline__ void find(const TileSource& src, int32_t* ids, unsigned* leaders) {
+    static_assert(kSmallTokens <= kThreads, "a thread per token");
+    const int t = threadIdx.x;
+    id = -1;
+    if (t < src.T) {
+      const int v = src.ids[t];
+      id = static_cast<unsigned>(v) < static_cast<unsigned>(src.NA) ? v : src.NA;
+    }
+    ids[t] = id;
+    __syncthreads();
+    rank = 0;
+    const int end = min(t & ~3, src.T);   // whole groups of four before t
+#pragma unroll 4
+    for (int i = 0; i < end; i += 4) {
+      const int4 q = *reinterpret_cast<const int4*>(ids + i);
+      rank += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
+    }
+    for (int i = t & ~3; i < t; ++i) rank += ids[i] == id;
+    const unsigned b = __ballot_sync(0xFFFFFFFFu, id >= 0 && rank % kSmallTile == 0);
+    if ((t & 31) == 0) leaders[t >> 5] = b;
+    __syncthreads();
+    count = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) count += __popc(leaders[w]);
+  }
+
+  // Tile q: its tokens' numbers to tok [kSmallTile], -1 past the end.
+  __device__ __forceinline__ Tile take(int q, const TileSource& src, const int32_t* ids,
+                                       const unsigned* leaders, int32_t* tok, int32_t* head) const {
+    if (threadIdx.x < kSmallTile) tok[threadIdx.x] = -1;
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+      if (w < static_cast<int>(threadIdx.x >> 5)) before += __popc(leaders[w]);
+    const unsigned own = leaders[threadIdx.x >> 5], bit = 1u << (threadIdx.x & 31);
+    if ((own & bit) && before + __popc(own & (bit - 1)) == q) head[0] = id, head[1] = rank;
+    __syncthreads();
+    const int adapter = head[0], first = head[1];
+    const bool in = id == adapter && rank >= first && rank < first + kSmallTile;
+    if (in) tok[rank - first] = static_cast<int32_t>(threadIdx.x);
+    Tile tile;
+    tile.n = __syncthreads_count(in);
+    tile.adapter = adapter < src.NA ? adapter : -1;
+    tile.slot = 0;
+    return tile;
+  }
+};
 
 // ------------------------------------------- w = s A x, u = s B^T dout
 // Low-rank rows leave as planes: `row` two or three planes [slots, RP], `col`
@@ -323,18 +343,6 @@ __device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float 
                                             const Planes& dst) {
   constexpr int RS = red_stride(RP);
   const int S = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
-  if constexpr (WK > 2) {   // the CTA's own first: one round over the cluster
-    __syncthreads();
-    for (int i = threadIdx.x; i < NTOK * RS / 4; i += kThreads) {
-      float4 v[WK];
-#pragma unroll
-      for (int w = 0; w < WK; ++w) v[w] = reinterpret_cast<const float4*>(red + w * NTOK * RS)[i];
-#pragma unroll
-      for (int w = 1; w < WK; ++w)
-        v[0].x += v[w].x, v[0].y += v[w].y, v[0].z += v[w].z, v[0].w += v[w].w;
-      reinterpret_cast<float4*>(red)[i] = v[0];
-    }
-  }
   if (S > 1) cluster_sync();
   else __syncthreads();
   const int per = NTOK / S, t0 = rank * per;
@@ -342,7 +350,7 @@ __device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float 
     float* p = red + (t0 + i / (RP / 4)) * RS + i % (RP / 4) * 4;
     float4 v = cluster_sum4(p, S);
 #pragma unroll
-    for (int w = 1; w < (WK > 2 ? 1 : WK); ++w) {
+    for (int w = 1; w < WK; ++w) {
       const float4 u = cluster_sum4(p + w * NTOK * RS, S);
       v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
@@ -375,81 +383,6 @@ __device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float 
 __device__ __forceinline__ int2 chunk_range(int K, int chunk, int part, int parts) {
   const int64_t n = (K + chunk - 1) / chunk;
   return make_int2(static_cast<int>(n * part / parts), static_cast<int>(n * (part + 1) / parts));
-}
-
-// Small batches: the cluster's warps share out the 32-element chunks of K.  Rank is
-// MMA-M, tokens are MMA-N: lane (g, t) of a chunk loads the 8 elements at 8 t
-// of rank rows g and g + 8 and of token g, two MMAs deep, straight from
-// global memory: a warp has a few chunks, all in flight at once.
-template <int RT>
-struct ShrinkSmall {
-  static constexpr int NT = kSmallTile / 8, RP = 16 * RT;
-  static constexpr size_t smem = sizeof(float) * kWarps * kSmallTile * red_stride(RP);
-};
-
-template <int RT>
-__global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2) shrink_small_kernel(const ShrinkArgs a) {
-  using C = ShrinkSmall<RT>;
-  constexpr int NT = C::NT, RS = red_stride(C::RP);
-  extern __shared__ __align__(128) uint8_t sm[];
-  float* red = reinterpret_cast<float*>(sm);
-  __shared__ int32_t tok[kSmallTile];
-  griddep_wait();
-  griddep_launch_dependents();
-  Tile tile;
-  if (!find_tile<true>(a.tiles, blockIdx.x / cluster_size(), &tile, tok) || tile.adapter < 0) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  float acc[RT][NT][4];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
-  const __nv_bfloat16* row[NT];          // null: no such token
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int64_t id = tok[8 * j + g];
-    row[j] = id >= 0 ? static_cast<const __nv_bfloat16*>(a.src) + id * a.ld + 8 * t : nullptr;
-  }
-  const int live = (tile.n + 7) / 8;     // columns with a token
-  const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.K + 8 * t;
-  const int2 c = chunk_range(a.K, 32, static_cast<int>(cluster_rank()) * kWarps + warp,
-                             static_cast<int>(cluster_size()) * kWarps);
-#pragma unroll(RT >= 4 ? 2 : 4)
-  for (int k = 32 * c.x; k < 32 * c.y; k += 32) {
-    const bool in = k + 8 * t < a.K;
-    uint4 p[RT][2], x[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      x[j] = in && row[j] ? ldg16(row[j] + k) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int rank = 16 * i + 8 * h + g;
-        p[i][h] = in && rank < a.r ? ldg16(pool + static_cast<int64_t>(rank) * a.K + k)
-                                   : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      if (j < live)
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          mma(acc[i][j], p[i][0].x, p[i][1].x, p[i][0].y, p[i][1].y, x[j].x, x[j].y);
-          mma(acc[i][j], p[i][0].z, p[i][1].z, p[i][0].w, p[i][1].w, x[j].z, x[j].w);
-        }
-  }
-  float* mine = red + warp * kSmallTile * RS;
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        mine[(8 * j + 2 * t + (q & 1)) * RS + 16 * i + g + 8 * (q >> 1)] = acc[i][j][q];
-  const float scale = a.scale ? __ldg(a.scale + tile.adapter) : 1.0f;
-  finish_tile<C::RP, kWarps, kSmallTile>(red, tile, scale, a.dst);
 }
 
 // Tiles of 64 tokens: the CTA's chunks of 64 elements of K come into shared
@@ -592,7 +525,7 @@ __global__ void __launch_bounds__(kThreads) shrink_x_kernel(const ShrinkArgs a) 
   griddep_wait();
   griddep_launch_dependents();
   Tile tile;
-  if (!find_tile<false>(a.tiles, blockIdx.x / cluster_size(), &tile, nullptr) || tile.adapter < 0) return;
+  if (!find_tile(a.tiles, blockIdx.x / cluster_size(), &tile) || tile.adapter < 0) return;
   shrink_tile<RT, false, false>(a, tile, sm);
 }
 
@@ -607,11 +540,11 @@ __global__ void __launch_bounds__(kThreads) shrink_both_kernel(const ShrinkArgs 
   int unit = blockIdx.x / cluster_size();
   Tile tile;
   if (unit < d_units) {
-    if (!find_tile<false>(d.tiles, unit, &tile, nullptr) || tile.adapter < 0) return;
+    if (!find_tile(d.tiles, unit, &tile) || tile.adapter < 0) return;
     shrink_tile<RT, true, F32>(d, tile, sm);
   } else {
     unit -= d_units;
-    if (!find_tile<false>(x.tiles, unit, &tile, nullptr) || tile.adapter < 0) return;
+    if (!find_tile(x.tiles, unit, &tile) || tile.adapter < 0) return;
     shrink_tile<RT, false, false>(x, tile, sm);
   }
 }
@@ -639,7 +572,9 @@ struct ExpandArgs {
 //   ROWS:  pool [r, N], read through the transposing ldmatrix
 template <int RT, bool ROWS, bool F32, bool SMALL>
 struct Expand {
-  static constexpr int RP = 16 * RT, FB = 128;
+  static constexpr int RP = 16 * RT;
+  // features of a block: more where a block has few tokens, for fewer barriers
+  static constexpr int FB = SMALL && RT <= 2 ? 256 : 128;
   // CTAs that share a tile's tokens: two where the base outweighs the pool's
   // rows, which each of them stages (8192 tokens, rank 16, 7168 features:
   // 73.1 us for the forward against 76.2)
@@ -653,13 +588,9 @@ struct Expand {
   static constexpr int BASE = NTOK * BROW, POOL = (ROWS ? RP : FB) * PROW, V = NTOK * 2 * RP;
   static constexpr int VN = F32 ? 3 : 2;                      // planes of w
   static constexpr int STAGE = BASE + POOL;
-  static constexpr int STAGES = 3 * STAGE + VN * V <= 40 * 1024 ? 3 : 2;
+  static constexpr int FIT = 40 * 1024 / STAGE;   // stages that leave room for other CTAs
+  static constexpr int STAGES = SMALL && FIT > 2 ? (FIT < 4 ? FIT : 4) : 2;
   static constexpr size_t smem = STAGES * STAGE + VN * V;
-  // CTAs an SM, for the split of the features: what shared memory holds, times
-  // the waves that measured best (a few: ragged tiles even out)
-  static constexpr int WAVES = SMALL ? 1 : ROWS ? 2 : 4;
-  static constexpr int RESIDENT = WAVES * (smem <= 36 * 1024 ? 6 : smem <= 45 * 1024 ? 5 : smem <= 56 * 1024 ? 4
-                                            : smem <= 75 * 1024 ? 3 : smem <= 113 * 1024 ? 2 : 1);
 };
 
 // Share `sub` of a tile's tokens; false: it has none.
@@ -671,17 +602,17 @@ __device__ __forceinline__ bool take_share(int sub, Tile* tile) {
 }
 
 // Tokens without an adapter: out = base, bit for bit (nothing to do when they
-// are the same memory).
-template <bool F32, bool SMALL>
+// are the same memory).  token(i): the tile's i-th.
+template <bool F32, typename Token>
 __device__ __forceinline__ void copy_rows(const ExpandArgs& a, const Tile& tile, int f, int width,
-                                          const int32_t* tok) {
+                                          Token&& token) {
   constexpr int ES = F32 ? 4 : 2;
   if (a.base == a.out && a.ld_base == a.ld_out) return;
   const int per = width * ES / 16;
   for (int i = threadIdx.x; i < tile.n * per; i += kThreads) {
     const int row = i / per, n = f + i % per * (16 / ES);
     if (n >= a.N) continue;
-    const int64_t id = SMALL ? tok[row] : a.tiles.perm[tile.slot + row];
+    const int64_t id = token(row);
     uint4 q = make_uint4(0, 0, 0, 0);
     if (a.base)
       q = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.base) + (id * a.ld_base + n) * ES);
@@ -689,27 +620,33 @@ __device__ __forceinline__ void copy_rows(const ExpandArgs& a, const Tile& tile,
   }
 }
 
-// Blocks [c0, c1) of FB features of a tile.  The inputs' first loads (base,
-// pool, and the tile's lists, which were complete before the kernel before
-// this one began) are issued ahead of the grid wait.
+// A thread's part in a CTA's blocks of FB features up to c1: its pieces of the
+// tile's rows (whose tokens are `row`, -1: none) and of the pool.
 template <int RT, bool ROWS, bool F32, bool SMALL>
-__device__ __forceinline__ void expand_tile(const ExpandArgs& a, const Tile& tile, int c0, int c1,
-                                            const int32_t* tok, uint8_t* sm) {
+struct Blocks {
   using C = Expand<RT, ROWS, F32, SMALL>;
-  constexpr int RP = C::RP, ES = C::ES, NT = C::NT, FB = C::FB;
-  constexpr int PIECES = FB * ES / 16, MINE = (C::NTOK * PIECES + kThreads - 1) / kThreads;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int wt = warp % C::WT, wf = warp / C::WT;
-  uint8_t* v_s = sm + C::STAGES * C::STAGE;
-  const int bc = threadIdx.x % PIECES * (16 / ES);   // the thread's piece of its rows
-  int row[MINE];                                     // -1: no such token
+  static constexpr int ES = C::ES, NT = C::NT, FB = C::FB;
+  static constexpr int PIECES = FB * ES / 16, MINE = (C::NTOK * PIECES + kThreads - 1) / kThreads;
+  const ExpandArgs& a;
+  const __nv_bfloat16* pool;
+  uint8_t* sm;
+  int c1;
+  int bc;          // first feature of the thread's piece
+  int row[MINE];
+
+  template <typename Token>
+  __device__ __forceinline__ Blocks(const ExpandArgs& args, int adapter, int end, uint8_t* smem, Token&& token)
+      : a(args), pool(args.pool + static_cast<int64_t>(adapter) * args.r * args.N), sm(smem), c1(end),
+        bc(threadIdx.x % PIECES * (16 / ES)) {
 #pragma unroll
-  for (int i = 0; i < MINE; ++i) {
-    const int r = (threadIdx.x + i * kThreads) / PIECES;
-    row[i] = r >= C::NTOK ? -1 : SMALL ? tok[r] : a.tiles.perm[tile.slot + r];
+    for (int i = 0; i < MINE; ++i) {
+      const int r = (threadIdx.x + i * kThreads) / PIECES;
+      row[i] = r < C::NTOK ? token(r) : -1;
+    }
   }
-  const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.N;
-  auto fetch = [&](int c, int stage) {
+
+  // The copies of block c, as one group.
+  __device__ __forceinline__ void fetch(int c, int stage) const {
     if (c < c1) {
       uint8_t* s = sm + stage * C::STAGE;
       const int f = c * FB;
@@ -735,10 +672,91 @@ __device__ __forceinline__ void expand_tile(const ExpandArgs& a, const Tile& til
       }
     }
     cp_commit();
-  };
+  }
+
+  // Blocks c0 .. c1 - 1 for a tile of n tokens; blocks c0 .. c0 + STAGES - 2 are
+  // fetched already, and w's planes lie in v_s.
+  __device__ __forceinline__ void run(int c0, int n, const uint8_t* v_s) const {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int wt = warp % C::WT, wf = warp / C::WT;
+    const uint32_t vp = smem_u32(v_s);
+    uint32_t v[RT][C::VN][4];
 #pragma unroll
-  for (int i = 0; i < C::STAGES - 2; ++i) fetch(c0 + i, i);
-  fetch(c0 + C::STAGES - 2, C::STAGES - 2);
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int p = 0; p < C::VN; ++p)
+        ldm4(v[i][p], vp + p * C::V + piece<2 * C::RP>(16 * wt + (lane & 15), 2 * i + (lane >> 4)));
+    int stage = 0;
+    for (int c = c0; c < c1; ++c) {
+      fetch(c + C::STAGES - 1, stage == 0 ? C::STAGES - 1 : stage - 1);
+      cp_wait<C::STAGES - 1>();
+      __syncthreads();
+      uint8_t* s = sm + stage * C::STAGE;
+      const uint32_t pp = smem_u32(s) + C::BASE;
+      stage = stage + 1 == C::STAGES ? 0 : stage + 1;
+      if (16 * wt < n) {
+#pragma unroll(RT == 1 ? 4 : 1)
+        for (int j = 0; j < NT; j += 2) {
+          const int col = wf * NT + j;   // two columns of 8 features
+          float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            uint32_t b[4];
+            if constexpr (ROWS)
+              ldm4t(b, pp + piece<C::PROW>(16 * i + (lane & 15), col + (lane >> 4)));
+            else
+              ldm4(b, pp + piece<C::PROW>(8 * col + (lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
+#pragma unroll
+            for (int p = 0; p < C::VN; ++p) {
+              mma(acc[0], v[i][p][0], v[i][p][1], v[i][p][2], v[i][p][3], b[0], b[1]);
+              mma(acc[1], v[i][p][0], v[i][p][1], v[i][p][2], v[i][p][3], b[2], b[3]);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint8_t* o = s + (16 * wt + 8 * h + g) * C::BROW + (8 * (col + e) + 2 * t) * ES;
+              const float x = acc[e][2 * h], y = acc[e][2 * h + 1];
+              if constexpr (F32) {
+                const float2 q = a.base ? *reinterpret_cast<const float2*>(o) : make_float2(0.f, 0.f);
+                *reinterpret_cast<float2*>(o) = make_float2(q.x + x, q.y + y);
+              } else {
+                const uint32_t q = a.base ? *reinterpret_cast<const uint32_t*>(o) : 0u;
+                *reinterpret_cast<uint32_t*>(o) =
+                    word(__float2bfloat16_rn(__uint_as_float(q << 16) + x),
+                         __float2bfloat16_rn(__uint_as_float(q & 0xFFFF0000u) + y));
+              }
+            }
+        }
+      }
+      __syncthreads();
+      if (c * FB + bc < a.N) {
+#pragma unroll
+        for (int i = 0; i < MINE; ++i)
+          if (row[i] >= 0)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (row[i] * a.ld_out + c * FB + bc) * ES) =
+                *reinterpret_cast<const uint4*>(s + (threadIdx.x + i * kThreads) / PIECES * C::BROW + bc * ES);
+      }
+      __syncthreads();   // before the stage is filled again
+    }
+    cp_wait<0>();
+  }
+};
+
+// Blocks [c0, c1) of a tile.  The inputs' first loads (base, pool, and the
+// tile's lists, which were complete before the kernel before this one began)
+// are issued ahead of the grid wait.
+template <int RT, bool ROWS, bool F32>
+__device__ __forceinline__ void expand_tile(const ExpandArgs& a, const Tile& tile, int c0, int c1,
+                                            uint8_t* sm) {
+  using C = Expand<RT, ROWS, F32, false>;
+  constexpr int RP = C::RP;
+  uint8_t* v_s = sm + C::STAGES * C::STAGE;
+  const Blocks<RT, ROWS, F32, false> blocks(a, tile.adapter, c1, sm,
+                                            [&](int i) { return a.tiles.perm[tile.slot + i]; });
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) blocks.fetch(c0 + i, i);
   griddep_wait();   // (again in backward_out_kernel: returns at once)
   constexpr int VP = RP / 8, ALLV = C::VN * C::NTOK * VP;   // pieces of a row of a plane, of all planes
 #pragma unroll
@@ -751,86 +769,159 @@ __device__ __forceinline__ void expand_tile(const ExpandArgs& a, const Tile& til
   cp_commit();
   cp_wait<0>();
   __syncthreads();
-  const uint32_t vp = smem_u32(v_s);
-  uint32_t v[RT][C::VN][4];
-#pragma unroll
-  for (int i = 0; i < RT; ++i)
-#pragma unroll
-    for (int p = 0; p < C::VN; ++p)
-      ldm4(v[i][p], vp + p * C::V + piece<2 * RP>(16 * wt + (lane & 15), 2 * i + (lane >> 4)));
-  int stage = 0;
-  for (int c = c0; c < c1; ++c) {
-    fetch(c + C::STAGES - 1, stage == 0 ? C::STAGES - 1 : stage - 1);
-    cp_wait<C::STAGES - 1>();
-    __syncthreads();
-    uint8_t* s = sm + stage * C::STAGE;
-    const uint32_t pp = smem_u32(s) + C::BASE;
-    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
-    if (16 * wt < tile.n) {
-#pragma unroll(RT == 1 ? 4 : 1)
-      for (int j = 0; j < NT; j += 2) {
-        const int n = wf * NT + j;   // two columns of 8 features
-        float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-          uint32_t b[4];
-          if constexpr (ROWS)
-            ldm4t(b, pp + piece<C::PROW>(16 * i + (lane & 15), n + (lane >> 4)));
-          else
-            ldm4(b, pp + piece<C::PROW>(8 * n + (lane & 7) + 8 * (lane >> 4), 2 * i + ((lane >> 3) & 1)));
-#pragma unroll
-          for (int p = 0; p < C::VN; ++p) {
-            mma(acc[0], v[i][p][0], v[i][p][1], v[i][p][2], v[i][p][3], b[0], b[1]);
-            mma(acc[1], v[i][p][0], v[i][p][1], v[i][p][2], v[i][p][3], b[2], b[3]);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint8_t* o = s + (16 * wt + 8 * h + g) * C::BROW + (8 * (n + e) + 2 * t) * ES;
-            const float x = acc[e][2 * h], y = acc[e][2 * h + 1];
-            if constexpr (F32) {
-              const float2 q = a.base ? *reinterpret_cast<const float2*>(o) : make_float2(0.f, 0.f);
-              *reinterpret_cast<float2*>(o) = make_float2(q.x + x, q.y + y);
-            } else {
-              const uint32_t q = a.base ? *reinterpret_cast<const uint32_t*>(o) : 0u;
-              *reinterpret_cast<uint32_t*>(o) =
-                  word(__float2bfloat16_rn(__uint_as_float(q << 16) + x),
-                       __float2bfloat16_rn(__uint_as_float(q & 0xFFFF0000u) + y));
-            }
-          }
-      }
-    }
-    __syncthreads();
-    if (c * FB + bc < a.N) {
-#pragma unroll
-      for (int i = 0; i < MINE; ++i)
-        if (row[i] >= 0)
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out) + (row[i] * a.ld_out + c * FB + bc) * ES) =
-              *reinterpret_cast<const uint4*>(s + (threadIdx.x + i * kThreads) / PIECES * C::BROW + bc * ES);
-    }
-    __syncthreads();   // before the stage is filled again
-  }
-  cp_wait<0>();
+  blocks.run(c0, tile.n, v_s);
 }
 
-template <int RT, bool ROWS, bool F32, bool SMALL>
+template <int RT, bool F32>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const ExpandArgs a) {
-  using C = Expand<RT, ROWS, F32, SMALL>;
+  using C = Expand<RT, false, F32, false>;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ int32_t tok[kSmallTile];
   griddep_launch_dependents();
   Tile tile;
   const int part = blockIdx.x / (a.units * C::SUB), unit = blockIdx.x - part * a.units * C::SUB;
   const int c0 = a.cols * part / a.parts, c1 = a.cols * (part + 1) / a.parts;
-  const bool some = find_tile<SMALL>(a.tiles, unit / C::SUB, &tile, tok) && take_share<C>(unit % C::SUB, &tile);
+  const bool some = find_tile(a.tiles, unit / C::SUB, &tile) && take_share<C>(unit % C::SUB, &tile);
   if (some && tile.adapter >= 0) {
-    expand_tile<RT, ROWS, F32, SMALL>(a, tile, c0, c1, tok, sm);
+    expand_tile<RT, false, F32>(a, tile, c0, c1, sm);
     return;
   }
   griddep_wait();   // every CTA: this kernel ends after the one before it
-  if (some) copy_rows<F32, SMALL>(a, tile, c0 * C::FB, (c1 - c0) * C::FB, tok);
+  if (some)
+    copy_rows<F32>(a, tile, c0 * C::FB, (c1 - c0) * C::FB,
+                   [&](int i) { return a.tiles.perm[tile.slot + i]; });
+}
+
+// ------------------------------------------------------- small batches
+// The whole forward of a batch of up to kSmallTokens in one kernel: a
+// cluster takes a tile (16 tokens that share an adapter).  Its warps
+// share out the 32-element chunks of H (ranks are MMA-M, tokens MMA-N; lane (g, t)
+// of a chunk loads the 8 elements at 8 t of rank rows g and g + 8 and of token g
+// straight from global memory, a few chunks a warp and all in flight at
+// once), every CTA adds up the partial sums over distributed shared memory,
+// and the CTAs share out the output's blocks, whose first base and pool rows
+// have been on their way since the tile's start.  Bound by latency at one token
+// (two dependent trips to HBM and the cluster's barriers), by the touched
+// pools' bytes at many.
+template <int RT, bool F32>
+struct Small {
+  using E = Expand<RT, false, F32, true>;
+  static constexpr int NT = kSmallTile / 8, RP = 16 * RT, RS = red_stride(RP);
+  static constexpr size_t red = sizeof(float) * kWarps * kSmallTile * RS;
+  static constexpr size_t smem = E::smem + red;
+};
+
+template <int RT, bool F32>
+__global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
+    small_kernel(const ShrinkArgs a, const ExpandArgs e) {
+  using S = Small<RT, F32>;
+  using C = typename S::E;
+  constexpr int NT = S::NT, RS = S::RS, RP = S::RP;
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(16) int32_t ids[kThreads];
+  __shared__ unsigned leaders[kThreads / 32];
+  __shared__ int32_t tok[kSmallTile], head[2];
+  uint8_t* v_s = sm + C::STAGES * C::STAGE;
+  float* red = reinterpret_cast<float*>(sm + C::smem);
+  griddep_wait();
+  griddep_launch_dependents();
+  const int CS = static_cast<int>(cluster_size()), rank_c = static_cast<int>(cluster_rank());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int c0 = e.cols * rank_c / CS, c1 = e.cols * (rank_c + 1) / CS;
+  SmallTiles tiles;
+  tiles.find(a.tiles, ids, leaders);
+  const int q = blockIdx.x / CS;
+  if (q >= tiles.count) return;   // the whole cluster
+  const Tile tile = tiles.take(q, a.tiles, ids, leaders, tok, head);
+  if (tile.adapter < 0) {
+    copy_rows<F32>(e, tile, c0 * C::FB, (c1 - c0) * C::FB, [&](int i) { return tok[i]; });
+    return;
+  }
+  const Blocks<RT, false, F32, true> blocks(e, tile.adapter, c1, sm, [&](int i) { return tok[i]; });
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) blocks.fetch(c0 + i, i);
+  float acc[RT][NT][4];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) acc[i][j][q] = 0.f;
+  const __nv_bfloat16* row[NT];          // null: no such token
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int64_t id = tok[8 * j + g];
+    row[j] = id >= 0 ? static_cast<const __nv_bfloat16*>(a.src) + id * a.ld + 8 * t : nullptr;
+  }
+  const int live = (tile.n + 7) / 8;     // columns with a token
+  const __nv_bfloat16* pool = a.pool + static_cast<int64_t>(tile.adapter) * a.r * a.K + 8 * t;
+  const int2 c = chunk_range(a.K, 32, rank_c * kWarps + warp, CS * kWarps);
+  constexpr int U = RT == 1 ? 4 : RT == 2 ? 3 : RT == 4 ? 2 : 1;   // chunks in flight
+#pragma unroll 1
+  for (int k0 = 32 * c.x; k0 < 32 * c.y; k0 += 32 * U) {
+    uint4 p[U][RT][2], x[U][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = k0 + 32 * u;
+      const bool in = k < 32 * c.y && k + 8 * t < a.K;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        x[u][j] = in && row[j] ? ldg16(row[j] + k) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int rank = 16 * i + 8 * h + g;
+          p[u][i][h] = in && rank < a.r ? ldg16(pool + static_cast<int64_t>(rank) * a.K + k)
+                                        : make_uint4(0, 0, 0, 0);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        if (j < live)
+#pragma unroll
+          for (int i = 0; i < RT; ++i) {
+            mma(acc[i][j], p[u][i][0].x, p[u][i][1].x, p[u][i][0].y, p[u][i][1].y, x[u][j].x, x[u][j].y);
+            mma(acc[i][j], p[u][i][0].z, p[u][i][1].z, p[u][i][0].w, p[u][i][1].w, x[u][j].z, x[u][j].w);
+          }
+  }
+  float* mine = red + warp * kSmallTile * RS;
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        mine[(8 * j + 2 * t + (q & 1)) * RS + 16 * i + g + 8 * (q >> 1)] = acc[i][j][q];
+  __syncthreads();
+  // the CTA's own warps first: one round over the cluster
+  for (int i = threadIdx.x; i < kSmallTile * RS / 4; i += kThreads) {
+    float4 v[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v[w] = reinterpret_cast<const float4*>(red + w * kSmallTile * RS)[i];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w)
+      v[0].x += v[w].x, v[0].y += v[w].y, v[0].z += v[w].z, v[0].w += v[w].w;
+    reinterpret_cast<float4*>(red)[i] = v[0];
+  }
+  if (CS > 1) cluster_sync();
+  else __syncthreads();
+  const float scale = a.scale ? __ldg(a.scale + tile.adapter) : 1.0f;
+  for (int i = threadIdx.x; i < kSmallTile * RP / 4; i += kThreads) {   // four ranks of a token
+    const int r = i / (RP / 4), j = i % (RP / 4) * 4;
+    float4 v = cluster_sum4(red + r * RS + j, CS);
+    v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+    uint8_t* o = v_s + piece<2 * RP>(r, j / 8) + 2 * (j % 8);
+#pragma unroll
+    for (int p = 0; p < C::VN; ++p) {
+      const uint32_t lo = peel(v.x, v.y), hi = peel(v.z, v.w);
+      *reinterpret_cast<uint2*>(o + p * C::V) = make_uint2(lo, hi);
+    }
+  }
+  __syncthreads();
+  blocks.run(c0, tile.n, v_s);
+  if (CS > 1) cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
 // ------------------------------------------------- dA = sum u x^T, dB
@@ -1039,11 +1130,14 @@ __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) backward_out_kernel
     const int part = cta / (a.dx.units * E::SUB), ti = cta - part * a.dx.units * E::SUB;
     const int c0 = a.dx.cols * part / a.dx.parts, c1 = a.dx.cols * (part + 1) / a.dx.parts;
     Tile tile;
-    if (part >= a.dx.parts || !find_tile<false>(a.dx.tiles, ti / E::SUB, &tile, nullptr) ||
+    if (part >= a.dx.parts || !find_tile(a.dx.tiles, ti / E::SUB, &tile) ||
         !take_share<E>(ti % E::SUB, &tile))
       return;
-    if (tile.adapter < 0) copy_rows<false, false>(a.dx, tile, c0 * E::FB, (c1 - c0) * E::FB, nullptr);
-    else expand_tile<RT, true, false, false>(a.dx, tile, c0, c1, nullptr, sm);
+    if (tile.adapter < 0)
+      copy_rows<false>(a.dx, tile, c0 * E::FB, (c1 - c0) * E::FB,
+                       [&](int i) { return a.dx.tiles.perm[tile.slot + i]; });
+    else
+      expand_tile<RT, true, false>(a.dx, tile, c0, c1, sm);
   }
 }
 
@@ -1054,31 +1148,33 @@ struct AdapterWs {
   size_t perm, counts, first, tiles, num_tiles, planes, total;
   int64_t units;    // tiles at most
   int64_t plane;    // elements of a plane
-  bool small;
+  bool small;       // forward of a small batch: no workspace
 };
 
 AdapterWs adapter_ws(const moe_adapter_shape* s, bool backward) {
   const int64_t T = s->num_tokens, NA = s->num_adapters;
   AdapterWs w = {};
   w.small = !backward && T <= kSmallTokens;
-  w.units = w.small ? T : max_tiles(T, NA);
-  w.plane = w.units * (w.small ? kSmallTile : kTile) * 16 * rt_of(s->rank);
+  // an adapter with n tokens has at most n / 16 + 1 tiles
+  const int64_t small_units = T / kSmallTile + NA + 1;
+  w.units = w.small ? (small_units < T ? small_units : T) : max_tiles(T, NA);
+  w.total = kWsAlign;
+  if (w.small) return w;   // unused
+  w.plane = w.units * kTile * 16 * rt_of(s->rank);
   size_t off = 0;
   auto take = [&](int64_t bytes) {
     const size_t o = off;
     off += ws_up(static_cast<size_t>(bytes));
     return o;
   };
-  if (!w.small) {
-    w.perm = take(w.units * kTile * 4);
-    w.counts = take((NA + 1) * 4);
-    w.first = take((NA + 2) * 4);
-    w.tiles = take(w.units * 16);
-    w.num_tiles = take(4);
-  }
+  w.perm = take(w.units * kTile * 4);
+  w.counts = take((NA + 1) * 4);
+  w.first = take((NA + 2) * 4);
+  w.tiles = take(w.units * 16);
+  w.num_tiles = take(4);
   // three row planes, or (backward) two of u and three col planes of u and of w
   w.planes = take(w.plane * 2 * (backward ? 8 : 3));
-  w.total = off > 0 ? off : kWsAlign;
+  w.total = off;
   return w;
 }
 
@@ -1148,58 +1244,61 @@ int shrink_cluster(int64_t units, int K, int resident, int least, int sms) {
   return c;
 }
 
-template <int RT, bool SMALL>
-cudaError_t launch_shrink_x(const ShrinkArgs& a, int64_t units, int sms, cudaStream_t st) {
-  using S = Shrink<RT, false, false>;
-  static DeviceOnce once;
-  auto kern = SMALL ? shrink_small_kernel<RT> : shrink_x_kernel<RT>;
-  constexpr size_t smem = SMALL ? ShrinkSmall<RT>::smem : S::smem;
-  const cudaError_t e = set_smem_limit_once(kern, smem, once);
-  if (e != cudaSuccess) return e;
-  const int c = SMALL ? shrink_cluster(units, a.K, 2, 32 * kWarps, sms)
-                      : shrink_cluster(units, a.K, 4, 4 * S::KC, sms);
-  return launch_cluster(kern, dim3(static_cast<unsigned>(units * c)), c, smem, st, a);
-}
-
-// Splits the features of expand's tiles into C::RESIDENT CTAs an SM.
-template <typename C>
+// Splits the features of expand's tiles into WAVES times the CTAs that an SM
+// holds by shared memory: ragged tiles even out over a few waves, more lose to
+// each CTA's start (4 waves forward, 2 beside the backward's sums).
+template <typename C, int WAVES>
 void split_features(ExpandArgs* a, int sms) {
+  constexpr int resident = static_cast<int>(220 * 1024 / (C::smem + 1024));
   a->cols = (a->N + C::FB - 1) / C::FB;
-  int64_t want = static_cast<int64_t>(C::RESIDENT) * sms / (static_cast<int64_t>(a->units) * C::SUB);
+  int64_t want = static_cast<int64_t>(resident < 6 ? resident : 6) * WAVES * sms /
+                 (static_cast<int64_t>(a->units) * C::SUB);
   if (want < 1) want = 1;
   a->parts = static_cast<int32_t>(want < a->cols ? want : a->cols);
 }
 
-template <int RT, bool F32, bool SMALL>
-cudaError_t launch_expand(ExpandArgs a, int sms, cudaStream_t st) {
-  using C = Expand<RT, false, F32, SMALL>;
+template <int RT, bool F32>
+cudaError_t launch_small(const ShrinkArgs& sa, ExpandArgs e, int sms, cudaStream_t st) {
+  using S = Small<RT, F32>;
   static DeviceOnce once;
-  const cudaError_t e = set_smem_limit_once(expand_kernel<RT, false, F32, SMALL>, C::smem, once);
-  if (e != cudaSuccess) return e;
-  split_features<C>(&a, sms);
-  const int64_t ctas = static_cast<int64_t>(a.units) * C::SUB * a.parts;
+  const cudaError_t err = set_smem_limit_once(small_kernel<RT, F32>, S::smem, once);
+  if (err != cudaSuccess) return err;
+  e.cols = (e.N + S::E::FB - 1) / S::E::FB;
+  // a cluster per possible tile; the more CTAs in it, the shorter its chain of
+  // loads, while (about) all of them are resident, two an SM (64 tokens, 64
+  // adapters of rank 16: 11.6 us at four, 16.5 at eight, 13.4 at two)
+  const int64_t u = e.units;
+  const int c = 8 * u <= 2 * sms ? 8 : 4 * u <= 3 * sms ? 4 : 2 * u <= 4 * sms ? 2 : 1;
+  return launch_cluster(small_kernel<RT, F32>, dim3(static_cast<unsigned>(u * c)), c, S::smem, st, sa, e);
+}
+
+template <int RT, bool F32>
+cudaError_t launch_forward(const ShrinkArgs& sa, ExpandArgs e, int sms, cudaStream_t st) {
+  using S = Shrink<RT, false, false>;
+  static DeviceOnce once_s, once_e;
+  cudaError_t err = set_smem_limit_once(shrink_x_kernel<RT>, S::smem, once_s);
+  if (err != cudaSuccess) return err;
+  const int c = shrink_cluster(e.units, sa.K, 4, 4 * S::KC, sms);
+  err = launch_cluster(shrink_x_kernel<RT>, dim3(static_cast<unsigned>(e.units) * c), c, S::smem, st, sa);
+  if (err != cudaSuccess) return err;
+  using C = Expand<RT, false, F32, false>;
+  err = set_smem_limit_once(expand_kernel<RT, F32>, C::smem, once_e);
+  if (err != cudaSuccess) return err;
+  split_features<C, 4>(&e, sms);
+  const int64_t ctas = static_cast<int64_t>(e.units) * C::SUB * e.parts;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-  return launch_pdl(expand_kernel<RT, false, F32, SMALL>, dim3(static_cast<unsigned>(ctas)),
-                    dim3(kThreads), C::smem, st, a);
+  return launch_pdl(expand_kernel<RT, F32>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), C::smem,
+                    st, e);
 }
 
-template <int RT, bool SMALL>
-cudaError_t launch_forward(const ShrinkArgs& sa, const ExpandArgs& ea, bool f32, int64_t units,
-                           int sms, cudaStream_t st) {
-  const cudaError_t e = launch_shrink_x<RT, SMALL>(sa, units, sms, st);
-  if (e != cudaSuccess) return e;
-  return f32 ? launch_expand<RT, true, SMALL>(ea, sms, st)
-             : launch_expand<RT, false, SMALL>(ea, sms, st);
-}
-
-template <bool SMALL>
-cudaError_t forward_products(const ShrinkArgs& sa, const ExpandArgs& ea, bool f32, int64_t units,
-                             int sms, cudaStream_t st) {
+template <bool F32>
+cudaError_t forward_products(const ShrinkArgs& sa, const ExpandArgs& e, bool small, int sms,
+                             cudaStream_t st) {
   switch (rt_of(sa.r)) {
-    case 1: return launch_forward<1, SMALL>(sa, ea, f32, units, sms, st);
-    case 2: return launch_forward<2, SMALL>(sa, ea, f32, units, sms, st);
-    case 4: return launch_forward<4, SMALL>(sa, ea, f32, units, sms, st);
-    default: return launch_forward<8, SMALL>(sa, ea, f32, units, sms, st);
+    case 1: return small ? launch_small<1, F32>(sa, e, sms, st) : launch_forward<1, F32>(sa, e, sms, st);
+    case 2: return small ? launch_small<2, F32>(sa, e, sms, st) : launch_forward<2, F32>(sa, e, sms, st);
+    case 4: return small ? launch_small<4, F32>(sa, e, sms, st) : launch_forward<4, F32>(sa, e, sms, st);
+    default: return small ? launch_small<8, F32>(sa, e, sms, st) : launch_forward<8, F32>(sa, e, sms, st);
   }
 }
 
@@ -1235,7 +1334,7 @@ cudaError_t launch_backward(const Backward& b, cudaStream_t st) {
   o.NA = b.NA;
   o.da_slabs = b.want_x ? (o.da.N + fb - 1) / fb : 0;
   o.db_slabs = b.want_x ? (o.db.N + fb - 1) / fb : 0;
-  split_features<E>(&o.dx, b.sms);
+  split_features<E, 2>(&o.dx, b.sms);
   const int64_t grads = static_cast<int64_t>(o.da_slabs + o.db_slabs) * b.NA;
   // CTAs that share an adapter's tokens: while the gradients' units leave SMs
   // idle and each has a tile or two
@@ -1342,17 +1441,20 @@ GradArgs grad_args(const AdapterCall& c, int col, const void* src, int64_t ld, f
 int32_t check_common(const moe_adapter_shape* s, const void* x, int64_t ld_x, const int32_t* ids,
                      const void* a, const void* b, const float* scale, const void* workspace,
                      size_t workspace_bytes, bool backward) {
-  if (!x || !ids || !a || !b || !workspace)
-    return entry_fail(MOE_ERR_INVALID_ARG, "x, adapter_ids, a, b or workspace is NULL");
+  if (!x || !ids || !a || !b)
+    return entry_fail(MOE_ERR_INVALID_ARG, "x, adapter_ids, a or b is NULL");
   int32_t rc = check_rows("x", x, ld_x, s->in_features);
   if (rc != MOE_OK) return rc;
   if (!ptr_aligned(a, 16) || !ptr_aligned(b, 16))
     return entry_fail(MOE_ERR_MISALIGNED, "a and b must be 16-byte aligned");
   if (!ptr_aligned(ids, 4) || !ptr_aligned(scale, 4))
     return entry_fail(MOE_ERR_MISALIGNED, "adapter_ids and scale must be 4-byte aligned");
+  const AdapterWs w = adapter_ws(s, backward);
+  if (w.small) return MOE_OK;
+  if (!workspace) return entry_fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
   if (!ptr_aligned(workspace, kWsAlign))
     return entry_fail(MOE_ERR_MISALIGNED, "workspace must be 256-byte aligned");
-  const size_t need = adapter_ws(s, backward).total;
+  const size_t need = w.total;
   if (workspace_bytes < need)
     return entry_fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu",
                       workspace_bytes, need);
@@ -1388,9 +1490,11 @@ extern "C" int32_t moe_adapter_forward(const moe_adapter_shape* s, const void* x
   const ExpandArgs ea = expand_args(c, b, base, ld_base, out, ld_out, s->rank, s->out_features);
   const bool f32 = s->out_dtype == MOE_DTYPE_F32;
   const ShrinkArgs sa = shrink_args(c, x, ld_x, a, scale, 0, f32 ? 3 : 2, -1, s->rank, s->in_features);
-  if (c.w.small) return entry_launched(forward_products<true>(sa, ea, f32, c.w.units, sms, st));
-  cudaError_t e = launch_group(adapter_ids, s->num_tokens, s->num_adapters, c.g, st);
-  if (e == cudaSuccess) e = forward_products<false>(sa, ea, f32, c.w.units, sms, st);
+  cudaError_t e = cudaSuccess;
+  if (!c.w.small) e = launch_group(adapter_ids, s->num_tokens, s->num_adapters, c.g, st);
+  if (e == cudaSuccess)
+    e = f32 ? forward_products<true>(sa, ea, c.w.small, sms, st)
+            : forward_products<false>(sa, ea, c.w.small, sms, st);
   return entry_launched(e);
 }
 

@@ -24,7 +24,7 @@ namespace moe {
 namespace {
 
 constexpr int kCountCtas = 8;       // one cluster of CTAs counts a sequence
-constexpr int kCountThreads = 512;
+constexpr int kCountThreads = 1024;
 constexpr int kMainThreads = 256;
 
 // Sequence bounds, held inside [0, T] and in order whatever the offsets hold.
@@ -54,17 +54,22 @@ __global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThrea
   const int64_t n = r.y - r.x;
   const int a = r.x + static_cast<int>(n * rank / kCountCtas);
   const int b = r.x + static_cast<int>(n * (rank + 1) / kCountCtas);
-  const int64_t i0 = static_cast<int64_t>(a) * k, i1 = static_cast<int64_t>(b) * k;
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += kCountThreads) {
-    const int e = ids[i];
-    if (static_cast<unsigned>(e) < static_cast<unsigned>(E) && (!mask || mask[i / k]))
-      atomicAdd(&hist[e], 1);
-  }
+  // a token a thread; its slots in groups of 8 loads that do not wait for one
+  // another or for the mask
   int valid = 0;
-  if (mask)
-    for (int t = a + threadIdx.x; t < b; t += kCountThreads) valid += mask[t] != 0;
-  else
-    valid = threadIdx.x == 0 ? b - a : 0;
+  for (int t = a + static_cast<int>(threadIdx.x); t < b; t += kCountThreads) {
+    const bool ok = !mask || mask[t];
+    const int32_t* row = ids + static_cast<int64_t>(t) * k;
+    for (int j0 = 0; j0 < k; j0 += 8) {
+      int e[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) e[j] = j0 + j < k ? row[j0 + j] : -1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (ok && static_cast<unsigned>(e[j]) < static_cast<unsigned>(E)) atomicAdd(&hist[e[j]], 1);
+    }
+    valid += ok;
+  }
   valid = __reduce_add_sync(0xFFFFFFFFu, valid);
   if ((threadIdx.x & 31) == 0 && valid) atomicAdd(&hist[E], valid);
   cluster_sync();
@@ -114,35 +119,89 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
+// CTAs an SM, all resident (65,536 tokens of 256 experts: 31 us at four with
+// the registers they leave, 39 at two, 47 at five, which spill).
+constexpr int main_ctas(int V) { return V <= 4 ? 4 : 2; }
+
 // G lanes hold one token's row: lane l the experts 4 (l + G i) .. + 3, i < V.
 // A CTA takes a contiguous range of tokens, its groups of lanes in turn.
+// The gate gradient is scattered through shared memory: lane j writes slot j's
+// value at its expert, the lanes add what they find there.
 template <int G, int V>
-__global__ void __launch_bounds__(kMainThreads) balance_main_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kernel(const BalanceArgs a) {
   constexpr int kGroups = kMainThreads / G;
   __shared__ float sums[kMainThreads / 32];
+  __shared__ __align__(16) float gate_s[kGroups * G * 4 * V];
   __shared__ int live_s;
   __shared__ bool last;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  griddep_wait();
+  float* const gate = gate_s + group * (G * 4 * V);
   griddep_launch_dependents();
   if (threadIdx.x == 0) live_s = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    *reinterpret_cast<float4*>(gate + 4 * (lane + G * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
   __syncthreads();
-  int live = 0;
-  for (int s = threadIdx.x; s < a.S; s += kMainThreads) live += a.n_valid[s] > 0;
-  if (live) atomicAdd(&live_s, live);
-  __syncthreads();
-  const float share = a.coef / static_cast<float>(max(live_s, 1));
-  const int64_t per = (static_cast<int64_t>(a.T) + gridDim.x - 1) / gridDim.x;
-  const int64_t t0 = per * blockIdx.x, t1 = min(t0 + per, static_cast<int64_t>(a.T));
+  const int64_t t0 = static_cast<int64_t>(a.T) * blockIdx.x / gridDim.x;
+  const int64_t t1 = static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x;
+  // one slot a lane where the lanes are enough for them
+  const bool gates = a.weights && a.dlogits, slots = gates && a.k <= G;
+  struct Slot {
+    int id;
+    float w, dw;
+  };
+  auto is_on = [&](int64_t t) { return t < t1 && (!a.mask || a.mask[t]); };
+  auto load_row = [&](int64_t t, bool on, float (&z)[4 * V]) {
+    const float* row = a.logits + t * a.E;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = 4 * (lane + G * i);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) z[4 * i + q] = -INFINITY;
+      if (!on) continue;
+      if (a.vec) {
+        if (e < a.E) {
+          const float4 v = __ldcs(reinterpret_cast<const float4*>(row + e));
+          z[4 * i] = v.x, z[4 * i + 1] = v.y, z[4 * i + 2] = v.z, z[4 * i + 3] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (e + q < a.E) z[4 * i + q] = row[e + q];
+      }
+    }
+  };
+  auto load_slot = [&](int64_t t) {
+    Slot s = {-1, 0.f, 0.f};
+    if (slots && t < t1 && lane < a.k) {
+      const int64_t r = t * a.k + lane;
+      s.id = a.ids[r], s.w = a.weights[r], s.dw = a.dweights[r];
+    }
+    return s;
+  };
   float mine = 0.f;
   int s = -1, s_end = -1;   // the sequence of the token in hand, and where it ends
   float f[4 * V], c = 0.f;
 #pragma unroll
   for (int i = 0; i < 4 * V; ++i) f[i] = 0.f;
+  int64_t t = t0 + group;
+  bool on = is_on(t), on_next = is_on(t + kGroups);
+  // so far only the call's inputs; now the counts
+  griddep_wait();
+  int live = 0;
+  for (int i = threadIdx.x; i < a.S; i += kMainThreads) live += a.n_valid[i] > 0;
+  if (live) atomicAdd(&live_s, live);
+  __syncthreads();
+  const float share = a.coef / static_cast<float>(max(live_s, 1));
   // every lane of a warp runs the same number of rounds (the shuffles)
-  for (int64_t tt = t0; tt < t1; tt += kGroups) {
-    const int64_t t = tt + group;
+  for (int64_t tt = t0; tt < t1; tt += kGroups, t += kGroups) {
     const bool in = t < t1;
+    float z[4 * V];
+    const bool masked_in = on;
+    const Slot slot = load_slot(t);
+    load_row(t, on, z);
+    on = on_next;
+    on_next = is_on(t + 2 * kGroups);
     if (in && t >= s_end) {
       // the last sequence that begins at or before t
       int lo = 0, hi = a.S;
@@ -169,25 +228,7 @@ __global__ void __launch_bounds__(kMainThreads) balance_main_kernel(const Balanc
                              : 0.f;
         }
     }
-    const bool valid = in && s >= 0 && (!a.mask || a.mask[t]);
-    const float* row = a.logits + (in ? t : 0) * a.E;
-    float z[4 * V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = 4 * (lane + G * i);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) z[4 * i + q] = -INFINITY;
-      if (valid) {
-        if (a.vec && e < a.E) {
-          const float4 v = __ldcs(reinterpret_cast<const float4*>(row + e));
-          z[4 * i] = v.x, z[4 * i + 1] = v.y, z[4 * i + 2] = v.z, z[4 * i + 3] = v.w;
-        } else if (!a.vec) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (e + q < a.E) z[4 * i + q] = row[e + q];
-        }
-      }
-    }
+    const bool valid = masked_in && s >= 0;
     float top = z[0];
 #pragma unroll
     for (int i = 1; i < 4 * V; ++i) top = fmaxf(top, z[i]);
@@ -198,7 +239,7 @@ __global__ void __launch_bounds__(kMainThreads) balance_main_kernel(const Balanc
     float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * V; ++i) {
-      z[i] = expf(z[i] - base);
+      z[i] = __expf(z[i] - base);   // within 2 + 1.2 |z - base| units in the last place
       sum += z[i];
       dot = fmaf(z[i], f[i], dot);
     }
@@ -207,11 +248,34 @@ __global__ void __launch_bounds__(kMainThreads) balance_main_kernel(const Balanc
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     dot *= inv;
     if (valid && lane == 0) mine = fmaf(c, dot, mine);
-    if (!a.dlogits || !in) continue;
+    if (!a.dlogits) continue;
     const float scale = valid ? c * inv : 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * V; ++i) z[i] = valid ? scale * z[i] * (f[i] - dot) : 0.f;
-    if (a.weights) {
+    if (slots) {
+      const bool some = static_cast<unsigned>(slot.id) < static_cast<unsigned>(a.E);
+      const float inner = group_sum<G>(some ? slot.w * slot.dw : 0.f);
+      const float g = slot.w * (slot.dw - inner);
+      // an expert named twice (never by the router): its slots one after the other
+      const unsigned same = __match_any_sync(0xFFFFFFFFu, some ? slot.id + group * 1024 : -1 - static_cast<int>(threadIdx.x));
+      const unsigned earlier = same & ((1u << (threadIdx.x & 31)) - 1);
+      if (some && !earlier) gate[slot.id] = g;
+      __syncwarp();
+      if (__any_sync(0xFFFFFFFFu, earlier != 0)) {
+        for (int l = 0; l < 32; ++l) {
+          if (some && earlier && l == static_cast<int>(threadIdx.x & 31)) gate[slot.id] += g;
+          __syncwarp();
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float4 v = *reinterpret_cast<const float4*>(gate + 4 * (lane + G * i));
+        z[4 * i] += v.x, z[4 * i + 1] += v.y, z[4 * i + 2] += v.z, z[4 * i + 3] += v.w;
+      }
+      __syncwarp();
+      if (some) gate[slot.id] = 0.f;
+      __syncwarp();
+    } else if (gates && in) {   // more slots than lanes: few experts
       const int64_t r0 = t * a.k;
       float inner = 0.f;
       for (int j = 0; j < a.k; ++j)
@@ -224,9 +288,10 @@ __global__ void __launch_bounds__(kMainThreads) balance_main_kernel(const Balanc
         for (int i = 0; i < V; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (4 * (lane + G * i) + q == e) z[4 * i + q] += g;
+            if (4 * (lane + G * i) + q == e && e < a.E) z[4 * i + q] += g;
       }
     }
+    if (!in) continue;
     float* out = a.dlogits + t * a.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -256,13 +321,19 @@ __global__ void __launch_bounds__(kMainThreads) balance_main_kernel(const Balanc
     last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
   }
   __syncthreads();
-  if (last && threadIdx.x < 32) {
+  if (last) {
     __threadfence();
     float v = 0.f;
-    for (unsigned b = threadIdx.x; b < gridDim.x; b += 32) v += __ldcg(a.partial + b);
+    for (unsigned b = threadIdx.x; b < gridDim.x; b += kMainThreads) v += __ldcg(a.partial + b);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if (threadIdx.x == 0) *a.loss = v;
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      v = 0.f;
+      for (int w = 0; w < kMainThreads / 32; ++w) v += sums[w];
+      *a.loss = v;
+    }
   }
 }
 
@@ -273,7 +344,7 @@ __global__ void balance_empty_kernel(float* loss, int32_t* counts, int64_t n) {
   if (i < n) counts[i] = 0;
 }
 
-constexpr int kMaxCtas = 152 * 8;
+constexpr int kMaxCtas = 152 * 8;   // CTAs the partial sums have room for
 
 struct BalanceWs {
   size_t n_valid, partial, ticket, total;
@@ -294,6 +365,8 @@ int32_t check_balance(const moe_balance_shape* s) {
       s->top_k > 32 || s->top_k > s->num_experts)
     return entry_fail(MOE_ERR_INVALID_ARG, "need num_tokens >= 0, 1 <= num_experts <= 1024, "
                                            "1 <= top_k <= min(num_experts, 32)");
+  if (static_cast<int64_t>(s->num_tokens) * s->top_k >= (int64_t(1) << 31))
+    return entry_fail(MOE_ERR_INVALID_ARG, "num_tokens * top_k must be < 2^31");
   if (s->num_sequences < 1 || s->num_sequences > (1 << 20))
     return entry_fail(MOE_ERR_INVALID_ARG, "num_sequences must be in [1, 2^20]");
   if (!(s->coef - s->coef == 0.f)) return entry_fail(MOE_ERR_INVALID_ARG, "coef must be finite");
@@ -371,24 +444,29 @@ extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float*
   a.T = T, a.E = E, a.k = shape->top_k, a.S = S;
   a.coef = shape->coef;
   a.vec = E % 4 == 0 && ptr_aligned(logits, 16) && ptr_aligned(dlogits, 16);
-  // lanes per token: as many as hold its experts by fours, up to a warp
-  const int lanes = E <= 8 ? 2 : E <= 16 ? 4 : E <= 32 ? 8 : E <= 64 ? 16 : 32;
+  // lanes per token: as many as hold its experts by fours up to 64 experts, then
+  // half a warp (two tokens share the reductions' instructions) while four
+  // groups of four a lane do
+  const int lanes = E <= 8 ? 2 : E <= 16 ? 4 : E <= 32 ? 8 : E <= 256 ? 16 : 32;
   const int per_round = kMainThreads / lanes;
   const int64_t rounds = (static_cast<int64_t>(T) + per_round - 1) / per_round;
-  int max_ctas = sms * 8;
+  const int v = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 384 ? 3 : E <= 512 ? 4 : 8;
+  int max_ctas = sms * main_ctas(v);   // one wave
   if (max_ctas > kMaxCtas) max_ctas = kMaxCtas;
   const int grid = static_cast<int>(rounds < max_ctas ? rounds : max_ctas);
   switch (lanes) {
     case 2: e = launch_main<2, 1>(a, grid, st); break;
     case 4: e = launch_main<4, 1>(a, grid, st); break;
     case 8: e = launch_main<8, 1>(a, grid, st); break;
-    case 16: e = launch_main<16, 1>(a, grid, st); break;
+    case 16:
+      e = v == 1   ? launch_main<16, 1>(a, grid, st)
+          : v == 2 ? launch_main<16, 2>(a, grid, st)
+                   : launch_main<16, 4>(a, grid, st);
+      break;
     default:
-      e = E <= 128   ? launch_main<32, 1>(a, grid, st)
-          : E <= 256 ? launch_main<32, 2>(a, grid, st)
-          : E <= 384 ? launch_main<32, 3>(a, grid, st)
-          : E <= 512 ? launch_main<32, 4>(a, grid, st)
-                     : launch_main<32, 8>(a, grid, st);
+      e = v == 3   ? launch_main<32, 3>(a, grid, st)
+          : v == 4 ? launch_main<32, 4>(a, grid, st)
+                   : launch_main<32, 8>(a, grid, st);
   }
   return entry_launched(e);
 }
