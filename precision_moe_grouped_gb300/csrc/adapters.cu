@@ -11,15 +11,17 @@
 //              dA = sum u x^T, dB = sum dout w^T              (grad: contracts over
 //                                                              the adapter's tokens)
 // With ranks of 8 to 128 every one of these does r multiply-adds for each
-// element it moves, far below the ~290 operations a byte at which tensor
-// throughput would bind, so the layout serves the memory stream: operands
-// go straight from global memory into the fragments of mma.sync (16x8x16,
-// bf16, float accumulators), with no staging and no barrier in the loops.
-// The contraction index and the column index of a fragment are free to be
-// permuted as long as both operands (or the store) use the same order; each
-// kernel picks the order in which a lane's share is contiguous in memory.
-// (tcgen05 would need the gathered rows staged in shared memory through
-// another pass, for tiles whose N is r.)
+// element it moves, mostly far below the ~290 operations a byte at which tensor
+// throughput would bind, so the layout serves the memory stream: the long
+// operand is staged by asynchronous copies (small batches: loaded straight
+// into fragments) and multiplied by mma.sync (16x8x16, bf16, float
+// accumulators).  mma.sync rather than tcgen05: the gathered rows have no
+// tensor map to be staged by, N would be r, and only the gradients' sums at
+// rank 64 and more keep the tensor pipe busy (0.4 of it).
+//
+// A call's kernels overlap by programmatic dependent launch, but its last one
+// never lets a successor start early: the forward of the layer reads its
+// logits, which may come from here, ahead of its own grid wait.
 //
 // u and w are computed in float and leave as bf16 planes that add up to them:
 // hi = bf16(v), then mid (and lo) the rounded rests.  Two planes (an error
@@ -44,7 +46,7 @@ constexpr int kThreads = 32 * kWarps;
 
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                     uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(   // no side effect: free to be scheduled
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -90,18 +92,17 @@ __device__ __forceinline__ void cp_wait() {   // all but the last N groups have 
 }
 
 // Four 8x8 matrices of bf16: lane l gives the address of row l % 8 of matrix
-// l / 8.
+// l / 8.  (Volatile keeps them behind the barriers; nothing else writes what
+// they read in between.)
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 __device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
 }
 
 // Byte offset of 16-byte piece `c` of row `row` in a staged tile of ROW-byte
@@ -386,7 +387,7 @@ __device__ __forceinline__ int2 chunk_range(int K, int chunk, int part, int part
 }
 
 // Tiles of 64 tokens: the CTA's chunks of 64 elements of K come into shared
-// memory by asynchronous copies, kStages deep (gathered rows of src, and the
+// memory by asynchronous copies, STAGES deep (gathered rows of src, and the
 // pool's rows), and feed ldmatrix.  Tokens are MMA-M, 16 to a warp; the two
 // warps that share 16 tokens split the ranks, or at RT = 1 the chunk.
 //   !ROWS (x):    pool [r, K], its rows are the fragments' columns
@@ -776,7 +777,6 @@ template <int RT, bool F32>
 __global__ void __launch_bounds__(kThreads) expand_kernel(const ExpandArgs a) {
   using C = Expand<RT, false, F32, false>;
   extern __shared__ __align__(128) uint8_t sm[];
-  griddep_launch_dependents();
   Tile tile;
   const int part = blockIdx.x / (a.units * C::SUB), unit = blockIdx.x - part * a.units * C::SUB;
   const int c0 = a.cols * part / a.parts, c1 = a.cols * (part + 1) / a.parts;
@@ -823,7 +823,6 @@ __global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
   uint8_t* v_s = sm + C::STAGES * C::STAGE;
   float* red = reinterpret_cast<float*>(sm + C::smem);
   griddep_wait();
-  griddep_launch_dependents();
   const int CS = static_cast<int>(cluster_size()), rank_c = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int c0 = e.cols * rank_c / CS, c1 = e.cols * (rank_c + 1) / CS;
@@ -876,15 +875,18 @@ __global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
         }
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int j = 0; j < NT; ++j)
+      if (j < live)
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
-        if (j < live)
+        for (int i = 0; i < RT; ++i) {
+          float part[4] = {0.f, 0.f, 0.f, 0.f};   // of these chunks (see `add`)
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
-            mma(acc[i][j], p[u][i][0].x, p[u][i][1].x, p[u][i][0].y, p[u][i][1].y, x[u][j].x, x[u][j].y);
-            mma(acc[i][j], p[u][i][0].z, p[u][i][1].z, p[u][i][0].w, p[u][i][1].w, x[u][j].z, x[u][j].w);
+          for (int u = 0; u < U; ++u) {
+            mma(part, p[u][i][0].x, p[u][i][1].x, p[u][i][0].y, p[u][i][1].y, x[u][j].x, x[u][j].y);
+            mma(part, p[u][i][0].z, p[u][i][1].z, p[u][i][0].w, p[u][i][1].w, x[u][j].z, x[u][j].w);
           }
+          add(acc[i][j], part);
+        }
   }
   float* mine = red + warp * kSmallTile * RS;
 #pragma unroll
@@ -945,7 +947,7 @@ struct GradArgs {
 template <int RT, bool F32>
 struct Grad {
   static constexpr int RP = 16 * RT, FB = 128;
-  static constexpr int TK = RT <= 2 ? kTile : kTile / 2;  // slots of a stage
+  static constexpr int TK = RT <= 4 ? kTile : kTile / 2;  // slots of a stage
   static constexpr int WF = kWarps / RT;                 // warps along the features
   static constexpr int NT = FB / 8 / WF;                 // 8-feature columns of a warp
   static constexpr int XROW = F32 ? 4 * FB + 16 : 2 * FB;
@@ -1115,7 +1117,6 @@ template <int RT, bool F32>
 __global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) backward_out_kernel(const OutArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
   griddep_wait();
-  griddep_launch_dependents();
   const int C = static_cast<int>(cluster_size());
   int unit = blockIdx.x / C;
   const int na = a.da_slabs * a.NA, nb = a.db_slabs * a.NA;

@@ -136,7 +136,6 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
   __shared__ bool last;
   const int lane = threadIdx.x % G, group = threadIdx.x / G;
   float* const gate = gate_s + group * (G * 4 * V);
-  griddep_launch_dependents();
   if (threadIdx.x == 0) live_s = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i)
