@@ -402,6 +402,9 @@ typedef struct {
   float coef;
 } moe_balance_shape;
 
+/* Workspace bytes of moe_balance_loss; 0 for an invalid shape.  256: a small
+ * batch of one sequence, which runs as one kernel and uses none (the workspace
+ * may be NULL). */
 size_t moe_balance_workspace_size(const moe_balance_shape* shape);
 
 /* Load-balance loss of the router, per-expert counts and the gradient of the

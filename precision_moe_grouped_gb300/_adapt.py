@@ -203,7 +203,7 @@ class BalanceLoss:
     def __init__(self, num_experts: int, top_k: int, coef: float = 1.0):
         _bind_torch()
         self.num_experts, self.top_k, self.coef = num_experts, top_k, coef
-        self._lib, self._sizes = load(), {}
+        self._lib, self._calls = load(), {}
         self._size(BalanceShape(0, num_experts, top_k, 1, coef))   # rejects bad sizes here
 
     def _size(self, s: BalanceShape) -> int:
@@ -240,19 +240,21 @@ class BalanceLoss:
         if weights is not None:
             _check_flat(weights, "weights", torch.float32, (T, k), dev)
             _check_flat(dweights, "dweights", torch.float32, (T, k), dev)
-        s = BalanceShape(T, E, k, S, self.coef)
-        n = self._sizes.get(S)
-        if n is None:   # it depends on the sequences alone
-            n = self._sizes[S] = self._size(s)
-        # the loss and, 256 bytes on, the workspace
-        ws = torch.empty(64 + (n + 3) // 4, dtype=torch.float32, device=logits.device)
-        loss = ws.narrow(0, 0, 1)
+        got = self._calls.get((T, S))
+        if got is None:
+            s = BalanceShape(T, E, k, S, self.coef)
+            if len(self._calls) > 4096:
+                self._calls.clear()
+            got = self._calls[(T, S)] = (s, self._size(s))
+        s, n = got
+        ws = None if n <= 256 else _scratch(n, logits)   # small batches use none
+        loss = torch.empty(1, dtype=torch.float32, device=logits.device)
         counts = torch.empty((S, E), dtype=torch.int32, device=logits.device)
         dlogits = torch.empty_like(logits) if need_grad else None
         rc = self._lib.moe_balance_loss(s, logits.data_ptr(), ids.data_ptr(), _ptr(mask),
                                         _ptr(seq_offsets), _ptr(weights), _ptr(dweights),
                                         loss.data_ptr(), counts.data_ptr(), _ptr(dlogits),
-                                        ws.data_ptr() + 256, n, _raw_stream(dev))
+                                        _ptr(ws), n, _raw_stream(dev))
         if rc:
             check(rc)
         return loss, counts, dlogits

@@ -13,7 +13,8 @@
 // it does wait for are the counts, hence two kernels.
 //
 // Bound by HBM: logits are read once and the gradient is written once, 8 E
-// bytes a token; the counts read 4 k bytes a token.
+// bytes a token; the counts read 4 k bytes a token.  (A call's last kernel lets
+// no successor start early: others may read its results ahead of a grid wait.)
 #include <cfloat>
 
 #include "cluster.cuh"
@@ -119,42 +120,39 @@ __device__ __forceinline__ float group_sum(float v) {
   return v;
 }
 
-// CTAs an SM, all resident (65,536 tokens of 256 experts: 31 us at four with
-// the registers they leave, 39 at two, 47 at five, which spill).
-constexpr int main_ctas(int V) { return V <= 4 ? 4 : 2; }
+struct Slot {
+  int id;
+  float w, dw;
+};
 
-// G lanes hold one token's row: lane l the experts 4 (l + G i) .. + 3, i < V.
-// A CTA takes a contiguous range of tokens, its groups of lanes in turn.
+// Rows as G lanes hold them: lane l the experts 4 (l + G i) .. + 3, i < V.
 // The gate gradient is scattered through shared memory: lane j writes slot j's
 // value at its expert, the lanes add what they find there.
 template <int G, int V>
-__global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kernel(const BalanceArgs a) {
-  constexpr int kGroups = kMainThreads / G;
-  __shared__ float sums[kMainThreads / 32];
-  __shared__ __align__(16) float gate_s[kGroups * G * 4 * V];
-  __shared__ int live_s;
-  __shared__ bool last;
-  const int lane = threadIdx.x % G, group = threadIdx.x / G;
-  float* const gate = gate_s + group * (G * 4 * V);
-  if (threadIdx.x == 0) live_s = 0;
+struct Rows {
+  static constexpr int kGroups = kMainThreads / G;   // tokens a CTA has in hand
+  const BalanceArgs& a;
+  const int lane, group;
+  float* const gate;
+  const bool gates, slots;   // slots: one a lane, where the lanes are enough for them
+
+  // gate_s [kGroups * G * 4 V] in shared memory, visible after a barrier.
+  __device__ __forceinline__ Rows(const BalanceArgs& args, float* gate_s)
+      : a(args), lane(threadIdx.x % G), group(threadIdx.x / G), gate(gate_s + group * (G * 4 * V)),
+        gates(args.weights && args.dlogits), slots(gates && args.k <= G) {
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    *reinterpret_cast<float4*>(gate + 4 * (lane + G * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
-  __syncthreads();
-  const int64_t t0 = static_cast<int64_t>(a.T) * blockIdx.x / gridDim.x;
-  const int64_t t1 = static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x;
-  // one slot a lane where the lanes are enough for them
-  const bool gates = a.weights && a.dlogits, slots = gates && a.k <= G;
-  struct Slot {
-    int id;
-    float w, dw;
-  };
-  auto is_on = [&](int64_t t) { return t < t1 && (!a.mask || a.mask[t]); };
-  auto load_row = [&](int64_t t, bool on, float (&z)[4 * V]) {
+    for (int i = 0; i < V; ++i)
+      *reinterpret_cast<float4*>(gate + 4 * (lane + G * i)) = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+
+  __device__ __forceinline__ int expert(int i) const { return 4 * (lane + G * i); }
+
+  // Token t's logits; -inf where it is not `on` and past the experts.
+  __device__ __forceinline__ void load(int64_t t, bool on, float (&z)[4 * V]) const {
     const float* row = a.logits + t * a.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = 4 * (lane + G * i);
+      const int e = expert(i);
 #pragma unroll
       for (int q = 0; q < 4; ++q) z[4 * i + q] = -INFINITY;
       if (!on) continue;
@@ -169,65 +167,34 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
           if (e + q < a.E) z[4 * i + q] = row[e + q];
       }
     }
-  };
-  auto load_slot = [&](int64_t t) {
+  }
+
+  __device__ __forceinline__ Slot slot_of(int64_t t, bool in) const {
     Slot s = {-1, 0.f, 0.f};
-    if (slots && t < t1 && lane < a.k) {
+    if (slots && in && lane < a.k) {
       const int64_t r = t * a.k + lane;
       s.id = a.ids[r], s.w = a.weights[r], s.dw = a.dweights[r];
     }
     return s;
-  };
-  float mine = 0.f;
-  int s = -1, s_end = -1;   // the sequence of the token in hand, and where it ends
-  float f[4 * V], c = 0.f;
+  }
+
+  // f of a sequence with n valid tokens from its counts.
+  __device__ __forceinline__ void factors(const int32_t* counts, int n, float (&f)[4 * V]) const {
+    const float unit = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n)) : 0.f;
 #pragma unroll
-  for (int i = 0; i < 4 * V; ++i) f[i] = 0.f;
-  int64_t t = t0 + group;
-  bool on = is_on(t), on_next = is_on(t + kGroups);
-  // so far only the call's inputs; now the counts
-  griddep_wait();
-  int live = 0;
-  for (int i = threadIdx.x; i < a.S; i += kMainThreads) live += a.n_valid[i] > 0;
-  if (live) atomicAdd(&live_s, live);
-  __syncthreads();
-  const float share = a.coef / static_cast<float>(max(live_s, 1));
-  // every lane of a warp runs the same number of rounds (the shuffles)
-  for (int64_t tt = t0; tt < t1; tt += kGroups, t += kGroups) {
-    const bool in = t < t1;
-    float z[4 * V];
-    const bool masked_in = on;
-    const Slot slot = load_slot(t);
-    load_row(t, on, z);
-    on = on_next;
-    on_next = is_on(t + 2 * kGroups);
-    if (in && t >= s_end) {
-      // the last sequence that begins at or before t
-      int lo = 0, hi = a.S;
-      if (a.seq)
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (a.seq[mid] <= t) lo = mid;
-          else hi = mid;
-        }
-      const int2 r = seq_range(a.seq, lo, a.T);
-      const bool inside = t >= r.x && t < r.y;   // not: a token of no sequence
-      s = inside ? lo : -1;
-      s_end = inside ? r.y : static_cast<int>(t) + 1;
-      const int n = inside ? a.n_valid[s] : 0;
-      c = n > 0 ? share / static_cast<float>(n) : 0.f;
-      const float unit = n > 0 ? static_cast<float>(a.E) / (static_cast<float>(a.k) * static_cast<float>(n)) : 0.f;
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int e = 4 * (lane + G * i) + q;
-          f[4 * i + q] = inside && e < a.E
-                             ? unit * static_cast<float>(a.counts[static_cast<int64_t>(s) * a.E + e])
-                             : 0.f;
-        }
-    }
-    const bool valid = masked_in && s >= 0;
+      for (int q = 0; q < 4; ++q) {
+        const int e = expert(i) + q;
+        f[4 * i + q] = e < a.E ? unit * static_cast<float>(counts[e]) : 0.f;
+      }
+  }
+
+  // Token t (in: it exists; valid: it counts) with its sequence's f and weight
+  // c: writes its gradient, returns c d_t (on lane 0; 0 elsewhere).  All
+  // threads of the warp.
+  __device__ __forceinline__ float take(int64_t t, bool in, bool valid, float (&z)[4 * V], const Slot& slot,
+                                        const float (&f)[4 * V], float c) const {
     float top = z[0];
 #pragma unroll
     for (int i = 1; i < 4 * V; ++i) top = fmaxf(top, z[i]);
@@ -246,8 +213,8 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
     dot = group_sum<G>(dot);
     const float inv = sum == 0.f ? 0.f : 1.0f / sum;
     dot *= inv;
-    if (valid && lane == 0) mine = fmaf(c, dot, mine);
-    if (!a.dlogits) continue;
+    const float mine = valid && lane == 0 ? c * dot : 0.f;
+    if (!a.dlogits) return mine;
     const float scale = valid ? c * inv : 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * V; ++i) z[i] = valid ? scale * z[i] * (f[i] - dot) : 0.f;
@@ -256,7 +223,8 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
       const float inner = group_sum<G>(some ? slot.w * slot.dw : 0.f);
       const float g = slot.w * (slot.dw - inner);
       // an expert named twice (never by the router): its slots one after the other
-      const unsigned same = __match_any_sync(0xFFFFFFFFu, some ? slot.id + group * 1024 : -1 - static_cast<int>(threadIdx.x));
+      const unsigned same =
+          __match_any_sync(0xFFFFFFFFu, some ? slot.id + group * 1024 : -1 - static_cast<int>(threadIdx.x));
       const unsigned earlier = same & ((1u << (threadIdx.x & 31)) - 1);
       if (some && !earlier) gate[slot.id] = g;
       __syncwarp();
@@ -268,7 +236,7 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
       }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const float4 v = *reinterpret_cast<const float4*>(gate + 4 * (lane + G * i));
+        const float4 v = *reinterpret_cast<const float4*>(gate + expert(i));
         z[4 * i] += v.x, z[4 * i + 1] += v.y, z[4 * i + 2] += v.z, z[4 * i + 3] += v.w;
       }
       __syncwarp();
@@ -287,14 +255,14 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
         for (int i = 0; i < V; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            if (4 * (lane + G * i) + q == e && e < a.E) z[4 * i + q] += g;
+            if (expert(i) + q == e && e < a.E) z[4 * i + q] += g;
       }
     }
-    if (!in) continue;
+    if (!in) return mine;
     float* out = a.dlogits + t * a.E;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = 4 * (lane + G * i);
+      const int e = expert(i);
       if (a.vec) {
         if (e < a.E)
           __stcs(reinterpret_cast<float4*>(out + e),
@@ -305,17 +273,86 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
           if (e + q < a.E) out[e + q] = z[4 * i + q];
       }
     }
+    return mine;
+  }
+};
+
+// The CTA's threads' values, added in a fixed order; on thread 0.
+__device__ __forceinline__ float block_sum(float v, float* sums) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = 0.f;
+  if (threadIdx.x == 0)
+    for (int w = 0; w < kMainThreads / 32; ++w) v += sums[w];
+  return v;
+}
+
+// CTAs an SM, all resident (65,536 tokens of 256 experts: 31 us at four with
+// the registers they leave, 39 at two, 47 at five, which spill).
+constexpr int main_ctas(int V) { return V <= 4 ? 4 : 2; }
+
+// A CTA takes a contiguous range of tokens, its groups of lanes in turn.
+template <int G, int V>
+__global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kernel(const BalanceArgs a) {
+  constexpr int kGroups = Rows<G, V>::kGroups;
+  __shared__ float sums[kMainThreads / 32];
+  __shared__ __align__(16) float gate_s[kMainThreads * 4 * V];
+  __shared__ int live_s;
+  __shared__ bool last;
+  const Rows<G, V> rows(a, gate_s);
+  if (threadIdx.x == 0) live_s = 0;
+  __syncthreads();
+  const int64_t t0 = static_cast<int64_t>(a.T) * blockIdx.x / gridDim.x;
+  const int64_t t1 = static_cast<int64_t>(a.T) * (blockIdx.x + 1) / gridDim.x;
+  auto is_on = [&](int64_t t) { return t < t1 && (!a.mask || a.mask[t]); };
+  float mine = 0.f;
+  int s = -1, s_end = -1;   // the sequence of the token in hand, and where it ends
+  float f[4 * V], c = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4 * V; ++i) f[i] = 0.f;
+  int64_t t = t0 + rows.group;
+  bool on = is_on(t), on_next = is_on(t + kGroups);
+  // so far only the call's inputs; now the counts
+  griddep_wait();
+  int live = 0;
+  for (int i = threadIdx.x; i < a.S; i += kMainThreads) live += a.n_valid[i] > 0;
+  if (live) atomicAdd(&live_s, live);
+  __syncthreads();
+  const float share = a.coef / static_cast<float>(max(live_s, 1));
+  // every lane of a warp runs the same number of rounds (the shuffles)
+  for (int64_t tt = t0; tt < t1; tt += kGroups, t += kGroups) {
+    const bool in = t < t1, masked_in = on;
+    float z[4 * V];
+    const Slot slot = rows.slot_of(t, in);
+    rows.load(t, on, z);
+    on = on_next;
+    on_next = is_on(t + 2 * kGroups);
+    if (in && t >= s_end) {
+      // the last sequence that begins at or before t
+      int lo = 0, hi = a.S;
+      if (a.seq)
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (a.seq[mid] <= t) lo = mid;
+          else hi = mid;
+        }
+      const int2 r = seq_range(a.seq, lo, a.T);
+      const bool inside = t >= r.x && t < r.y;   // not: a token of no sequence
+      s = inside ? lo : -1;
+      s_end = inside ? r.y : static_cast<int>(t) + 1;
+      const int n = inside ? a.n_valid[s] : 0;
+      c = n > 0 ? share / static_cast<float>(n) : 0.f;
+      rows.factors(a.counts + static_cast<int64_t>(lo) * a.E, n, f);
+    }
+    mine += rows.take(t, in, masked_in && s >= 0, z, slot, f, c);
   }
   // The loss: the CTAs' sums, added in CTA order by the last CTA to finish,
   // so that it does not depend on which one that is.
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = mine;
-  __syncthreads();
+  mine = block_sum(mine, sums);
   if (threadIdx.x == 0) {
-    float v = 0.f;
-    for (int w = 0; w < kMainThreads / 32; ++w) v += sums[w];
-    __stcg(a.partial + blockIdx.x, v);
+    __stcg(a.partial + blockIdx.x, mine);
     __threadfence();
     last = atomicAdd(a.ticket, 1u) == gridDim.x - 1;
   }
@@ -324,16 +361,80 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
     __threadfence();
     float v = 0.f;
     for (unsigned b = threadIdx.x; b < gridDim.x; b += kMainThreads) v += __ldcg(a.partial + b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      v = 0.f;
-      for (int w = 0; w < kMainThreads / 32; ++w) v += sums[w];
-      *a.loss = v;
-    }
+    v = block_sum(v, sums);
+    if (threadIdx.x == 0) *a.loss = v;
   }
+}
+
+// A small batch of one sequence, whole, by one cluster: its CTAs count an
+// eighth of the tokens each, add the counts up over distributed shared
+// memory, and take their tokens' rows.  One launch and no workspace, for
+// batches whose time is that of a launch.
+constexpr int kSmallRounds = 2;   // tokens a group of lanes may have to take
+__host__ __device__ constexpr int small_tokens(int lanes) {
+  return kCountCtas * kSmallRounds * (kMainThreads / lanes);
+}
+
+template <int G, int V>
+__global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kMainThreads)
+    balance_small_kernel(const BalanceArgs a, int32_t* __restrict__ counts_out) {
+  constexpr int kGroups = Rows<G, V>::kGroups;
+  __shared__ float sums[kMainThreads / 32];
+  __shared__ __align__(16) float gate_s[kMainThreads * 4 * V];
+  __shared__ int32_t hist[1025], total[1025];   // [E] slots by expert, [E]: valid tokens
+  __shared__ __align__(16) float part[4];
+  const Rows<G, V> rows(a, gate_s);
+  const int rank = static_cast<int>(cluster_rank());
+  for (int i = threadIdx.x; i <= a.E; i += kMainThreads) hist[i] = 0;
+  __syncthreads();
+  griddep_wait();
+  const int t0 = static_cast<int>(static_cast<int64_t>(a.T) * rank / kCountCtas);
+  const int t1 = static_cast<int>(static_cast<int64_t>(a.T) * (rank + 1) / kCountCtas);
+  const int2 range = seq_range(a.seq, 0, a.T);
+  auto is_on = [&](int t) { return t >= range.x && t < range.y && (!a.mask || a.mask[t]); };
+  bool on[kSmallRounds];
+  float z[kSmallRounds][4 * V];
+#pragma unroll
+  for (int i = 0; i < kSmallRounds; ++i) {
+    const int t = t0 + i * kGroups + rows.group;
+    on[i] = t < t1 && is_on(t);
+    rows.load(t, on[i], z[i]);
+    if (rows.lane == 0 && on[i]) atomicAdd(&hist[a.E], 1);
+  }
+  for (int i = t0 * a.k + static_cast<int>(threadIdx.x); i < t1 * a.k; i += kMainThreads) {
+    const int e = a.ids[i];
+    if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E) && is_on(i / a.k))
+      atomicAdd(&hist[e], 1);
+  }
+  cluster_sync();
+  for (int e = threadIdx.x; e <= a.E; e += kMainThreads) {
+    int32_t n[kCountCtas];
+#pragma unroll
+    for (int c = 0; c < kCountCtas; ++c) n[c] = cluster_load(hist + e, c);
+#pragma unroll
+    for (int c = 1; c < kCountCtas; ++c) n[0] += n[c];
+    total[e] = n[0];
+    if (e < a.E && e % kCountCtas == rank) counts_out[e] = n[0];
+  }
+  __syncthreads();
+  const int n = total[a.E];
+  float f[4 * V], mine = 0.f;
+  const float c = n > 0 ? a.coef / static_cast<float>(n) : 0.f;
+  rows.factors(total, n, f);
+#pragma unroll
+  for (int i = 0; i < kSmallRounds; ++i) {
+    const int t = t0 + i * kGroups + rows.group;
+    mine += rows.take(t, t < t1, on[i], z[i], rows.slot_of(t, t < t1), f, c);
+  }
+  mine = block_sum(mine, sums);
+  if (threadIdx.x == 0) part[0] = mine;
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    float v = 0.f;
+    for (int r = 0; r < kCountCtas; ++r) v += cluster_load4(part, r).x;
+    *a.loss = v;
+  }
+  cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
 __global__ void balance_empty_kernel(float* loss, int32_t* counts, int64_t n) {
@@ -372,9 +473,53 @@ int32_t check_balance(const moe_balance_shape* s) {
   return MOE_OK;
 }
 
+// Lanes per token: as many as hold its experts by fours up to 64 experts, then
+// half a warp (two tokens share the reductions' instructions) while four groups
+// of four a lane do; and those groups.
+struct Split {
+  int lanes, v;
+};
+Split split_of(int E) {
+  if (E <= 8) return {2, 1};
+  if (E <= 16) return {4, 1};
+  if (E <= 32) return {8, 1};
+  if (E <= 64) return {16, 1};
+  if (E <= 128) return {16, 2};
+  if (E <= 256) return {16, 4};
+  return {32, E <= 384 ? 3 : E <= 512 ? 4 : 8};
+}
+
+bool is_small(const moe_balance_shape* s) {
+  return s->num_sequences == 1 && s->num_tokens <= small_tokens(split_of(s->num_experts).lanes);
+}
+
 template <int G, int V>
-cudaError_t launch_main(const BalanceArgs& a, int grid, cudaStream_t st) {
-  return launch_pdl(balance_main_kernel<G, V>, dim3(grid), dim3(kMainThreads), 0, st, a);
+cudaError_t launch_rows(const BalanceArgs& a, int32_t* counts, bool small, int sms, cudaStream_t st) {
+  if (small)
+    return launch_pdl(balance_small_kernel<G, V>, dim3(kCountCtas), dim3(kMainThreads), 0, st, a, counts);
+  const int per_round = kMainThreads / G;
+  const int64_t rounds = (static_cast<int64_t>(a.T) + per_round - 1) / per_round;
+  int ctas = sms * main_ctas(V);   // one wave
+  if (ctas > kMaxCtas) ctas = kMaxCtas;
+  return launch_pdl(balance_main_kernel<G, V>, dim3(static_cast<unsigned>(rounds < ctas ? rounds : ctas)),
+                    dim3(kMainThreads), 0, st, a);
+}
+
+cudaError_t launch_by_experts(const BalanceArgs& a, int32_t* counts, bool small, int sms, cudaStream_t st) {
+  const Split p = split_of(a.E);
+  switch (p.lanes) {
+    case 2: return launch_rows<2, 1>(a, counts, small, sms, st);
+    case 4: return launch_rows<4, 1>(a, counts, small, sms, st);
+    case 8: return launch_rows<8, 1>(a, counts, small, sms, st);
+    case 16:
+      return p.v == 1   ? launch_rows<16, 1>(a, counts, small, sms, st)
+             : p.v == 2 ? launch_rows<16, 2>(a, counts, small, sms, st)
+                        : launch_rows<16, 4>(a, counts, small, sms, st);
+    default:
+      return p.v == 3   ? launch_rows<32, 3>(a, counts, small, sms, st)
+             : p.v == 4 ? launch_rows<32, 4>(a, counts, small, sms, st)
+                        : launch_rows<32, 8>(a, counts, small, sms, st);
+  }
 }
 
 }  // namespace
@@ -382,7 +527,7 @@ cudaError_t launch_main(const BalanceArgs& a, int grid, cudaStream_t st) {
 
 extern "C" size_t moe_balance_workspace_size(const moe_balance_shape* shape) {
   if (moe::check_balance(shape) != MOE_OK) return 0;
-  return moe::balance_ws(shape).total;
+  return moe::is_small(shape) ? moe::kWsAlign : moe::balance_ws(shape).total;
 }
 
 extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float* logits,
@@ -396,8 +541,9 @@ extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float*
   if (rc != MOE_OK) return rc;
   const int T = shape->num_tokens, E = shape->num_experts, S = shape->num_sequences;
   if (!loss || !counts) return entry_fail(MOE_ERR_INVALID_ARG, "loss or counts is NULL");
-  if (T > 0 && (!logits || !ids || !workspace))
-    return entry_fail(MOE_ERR_INVALID_ARG, "logits, ids or workspace is NULL");
+  const bool small = is_small(shape), use_ws = T > 0 && !small;
+  if (T > 0 && (!logits || !ids)) return entry_fail(MOE_ERR_INVALID_ARG, "logits or ids is NULL");
+  if (use_ws && !workspace) return entry_fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
   if (S > 1 && !seq_offsets)
     return entry_fail(MOE_ERR_INVALID_ARG, "num_sequences > 1 needs seq_offsets");
   if (!weights != !dweights)
@@ -405,10 +551,10 @@ extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float*
   const void* ptrs[8] = {logits, ids, seq_offsets, weights, dweights, loss, counts, dlogits};
   for (const void* p : ptrs)
     if (!ptr_aligned(p, 4)) return entry_fail(MOE_ERR_MISALIGNED, "a pointer is not 4-byte aligned");
-  if (!ptr_aligned(workspace, kWsAlign))
+  if (use_ws && !ptr_aligned(workspace, kWsAlign))
     return entry_fail(MOE_ERR_MISALIGNED, "workspace must be 256-byte aligned");
   const BalanceWs w = balance_ws(shape);
-  if (T > 0 && workspace_bytes < w.total)
+  if (use_ws && workspace_bytes < w.total)
     return entry_fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu",
                       workspace_bytes, w.total);
   int sms = 0;
@@ -421,11 +567,13 @@ extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float*
                                      st, loss, counts, n));
   }
   uint8_t* base = static_cast<uint8_t*>(workspace);
-  int32_t* n_valid = reinterpret_cast<int32_t*>(base + w.n_valid);
-  uint32_t* ticket = reinterpret_cast<uint32_t*>(base + w.ticket);
-  cudaError_t e = launch_pdl(balance_count_kernel, dim3(static_cast<unsigned>(S) * kCountCtas),
-                             dim3(kCountThreads), (E + 1) * sizeof(int32_t), st, ids, token_mask,
-                             seq_offsets, T, E, shape->top_k, counts, n_valid, ticket);
+  int32_t* n_valid = small ? nullptr : reinterpret_cast<int32_t*>(base + w.n_valid);
+  uint32_t* ticket = small ? nullptr : reinterpret_cast<uint32_t*>(base + w.ticket);
+  cudaError_t e = cudaSuccess;
+  if (!small)
+    e = launch_pdl(balance_count_kernel, dim3(static_cast<unsigned>(S) * kCountCtas),
+                   dim3(kCountThreads), (E + 1) * sizeof(int32_t), st, ids, token_mask, seq_offsets, T,
+                   E, shape->top_k, counts, n_valid, ticket);
   if (e != cudaSuccess) return entry_launched(e);
   BalanceArgs a;
   a.logits = logits;
@@ -436,36 +584,12 @@ extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float*
   a.dweights = dweights;
   a.counts = counts;
   a.n_valid = n_valid;
-  a.partial = reinterpret_cast<float*>(base + w.partial);
+  a.partial = small ? nullptr : reinterpret_cast<float*>(base + w.partial);
   a.ticket = ticket;
   a.loss = loss;
   a.dlogits = dlogits;
   a.T = T, a.E = E, a.k = shape->top_k, a.S = S;
   a.coef = shape->coef;
   a.vec = E % 4 == 0 && ptr_aligned(logits, 16) && ptr_aligned(dlogits, 16);
-  // lanes per token: as many as hold its experts by fours up to 64 experts, then
-  // half a warp (two tokens share the reductions' instructions) while four
-  // groups of four a lane do
-  const int lanes = E <= 8 ? 2 : E <= 16 ? 4 : E <= 32 ? 8 : E <= 256 ? 16 : 32;
-  const int per_round = kMainThreads / lanes;
-  const int64_t rounds = (static_cast<int64_t>(T) + per_round - 1) / per_round;
-  const int v = E <= 64 ? 1 : E <= 128 ? 2 : E <= 256 ? 4 : E <= 384 ? 3 : E <= 512 ? 4 : 8;
-  int max_ctas = sms * main_ctas(v);   // one wave
-  if (max_ctas > kMaxCtas) max_ctas = kMaxCtas;
-  const int grid = static_cast<int>(rounds < max_ctas ? rounds : max_ctas);
-  switch (lanes) {
-    case 2: e = launch_main<2, 1>(a, grid, st); break;
-    case 4: e = launch_main<4, 1>(a, grid, st); break;
-    case 8: e = launch_main<8, 1>(a, grid, st); break;
-    case 16:
-      e = v == 1   ? launch_main<16, 1>(a, grid, st)
-          : v == 2 ? launch_main<16, 2>(a, grid, st)
-                   : launch_main<16, 4>(a, grid, st);
-      break;
-    default:
-      e = v == 3   ? launch_main<32, 3>(a, grid, st)
-          : v == 4 ? launch_main<32, 4>(a, grid, st)
-                   : launch_main<32, 8>(a, grid, st);
-  }
-  return entry_launched(e);
+  return entry_launched(launch_by_experts(a, counts, small, sms, st));
 }

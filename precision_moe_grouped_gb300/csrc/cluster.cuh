@@ -32,13 +32,13 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
-__device__ __forceinline__ int32_t cluster_load(const int32_t* p, uint32_t rank) {
-  int32_t v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
-  return v;
-}
 // Volatile keeps these behind the barrier; without a memory clobber a run of
 // them stays in flight together.
+__device__ __forceinline__ int32_t cluster_load(const int32_t* p, uint32_t rank) {
+  int32_t v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)));
+  return v;
+}
 __device__ __forceinline__ float4 cluster_load4(const float* p, uint32_t rank) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"

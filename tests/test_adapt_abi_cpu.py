@@ -93,7 +93,7 @@ def balance(lib, s, z=0x100000, ids=0x200000, mask=None, seq=None, w=None, dw=No
 
 
 def test_balance_refusals(lib):
-    good = dict(num_tokens=100, num_experts=16, top_k=2, num_sequences=1, coef=1.0)
+    good = dict(num_tokens=5000, num_experts=16, top_k=2, num_sequences=1, coef=1.0)
     for bad in (dict(num_tokens=-1), dict(num_experts=0), dict(num_experts=1025), dict(top_k=0),
                 dict(top_k=17), dict(num_sequences=0), dict(coef=float("inf")),
                 dict(num_tokens=(1 << 30), top_k=2)):
@@ -108,6 +108,7 @@ def test_balance_refusals(lib):
     assert balance(lib, s, w=0x100000) == L.MOE_ERR_INVALID_ARG
     assert balance(lib, s, ws=0x100010) == L.MOE_ERR_MISALIGNED
     assert balance(lib, s, n=lib.moe_balance_workspace_size(s) - 1) == L.MOE_ERR_WORKSPACE_TOO_SMALL
+    assert lib.moe_balance_workspace_size(L.BalanceShape(**(good | dict(num_tokens=100)))) == 256
     many = L.BalanceShape(**(good | dict(num_sequences=3)))
     assert balance(lib, many) == L.MOE_ERR_INVALID_ARG                     # no offsets
 

@@ -115,6 +115,19 @@ def test_sequences(seqs):
     check(make(100, 12, 2, seqs=seqs, masked=True, gates=True))
 
 
+@pytest.mark.parametrize("E,k", [(8, 2), (16, 2), (30, 4), (64, 8), (200, 8), (256, 8), (384, 6), (1024, 4)])
+def test_either_side_of_the_small_batches(E, k):
+    """The largest batch that one kernel takes and the next one, masked and not,
+    and one sequence that is a part of the batch."""
+    lib = P.load()
+    small = lambda T: lib.moe_balance_workspace_size(P._lib.BalanceShape(T, E, k, 1, 1.0)) == 256  # noqa: E731
+    T = max(t for t in range(1, 4000) if small(t))
+    for n in (T, T + 1):
+        check(make(n, E, k))
+        check(make(n, E, k, masked=True, gates=True, drop=True))
+        check(make(n, E, k, seqs=[3, n - 20], gates=True))
+
+
 def test_long_batches():
     check(make(20011, 256, 8, masked=True, seqs=[0, 7, 9000, 9000, 15000, 20011], gates=True))
     check(make(30000, 8, 2))
