@@ -395,14 +395,14 @@ __device__ __forceinline__ int2 chunk_range(int K, int chunk, int part, int part
 // A float src is staged as it is and split when it is read.
 template <int RT, bool ROWS, bool F32>
 struct Shrink {
-  static constexpr int RP = 16 * RT, KC = 64;
+  static constexpr int RP = 16 * RT, KC = F32 ? 64 : 128;
   static constexpr int WN = RT >= 2 ? 2 : 1, WK = 2 / WN;   // warps along ranks, along K
   static constexpr int NT = 2 * RT / WN;                    // 8-rank columns of a warp
   static constexpr int SROW = F32 ? 4 * KC + 32 : 2 * KC;   // bytes of a staged row of src
   static constexpr int PROW = ROWS ? 2 * RP : 2 * KC;       // and of the pool
   static constexpr int SRC = kTile * SROW, POOL = (ROWS ? KC : RP) * PROW;
   static constexpr int STAGE = SRC + POOL;
-  static constexpr int STAGES = STAGE <= 10240 ? 5 : STAGE <= 12288 ? 4 : 3;   // 4 CTAs an SM
+  static constexpr int STAGES = STAGE <= 24 * 1024 ? 3 : 2;
   static constexpr size_t red = sizeof(float) * WK * kTile * red_stride(RP);
   static constexpr size_t smem = STAGES * STAGE > red ? STAGES * STAGE : red;
 };
@@ -947,13 +947,13 @@ struct GradArgs {
 template <int RT, bool F32>
 struct Grad {
   static constexpr int RP = 16 * RT, FB = 128;
-  static constexpr int TK = RT <= 4 ? kTile : kTile / 2;  // slots of a stage
+  static constexpr int TK = RT <= 4 && !F32 ? kTile : kTile / 2;  // slots of a stage
   static constexpr int WF = kWarps / RT;                 // warps along the features
   static constexpr int NT = FB / 8 / WF;                 // 8-feature columns of a warp
   static constexpr int XROW = F32 ? 4 * FB + 16 : 2 * FB;
   static constexpr int X = TK * XROW, U = RP * 2 * TK;   // U: one plane
   static constexpr int STAGE = X + 3 * U;
-  static constexpr int STAGES = 3 * STAGE <= 72 * 1024 ? 3 : 2;
+  static constexpr int STAGES = 3 * STAGE <= 40 * 1024 ? 3 : 2;
   static constexpr size_t red = sizeof(float) * RP * (FB + 4);
   static constexpr size_t smem = STAGES * STAGE > red ? STAGES * STAGE : red;
 };
@@ -1114,7 +1114,7 @@ struct OutArgs {
 };
 
 template <int RT, bool F32>
-__global__ void __launch_bounds__(kThreads, RT == 1 ? 3 : 2) backward_out_kernel(const OutArgs a) {
+__global__ void __launch_bounds__(kThreads, RT == 1 ? 4 : 2) backward_out_kernel(const OutArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
   griddep_wait();
   const int C = static_cast<int>(cluster_size());
@@ -1279,7 +1279,7 @@ cudaError_t launch_forward(const ShrinkArgs& sa, ExpandArgs e, int sms, cudaStre
   static DeviceOnce once_s, once_e;
   cudaError_t err = set_smem_limit_once(shrink_x_kernel<RT>, S::smem, once_s);
   if (err != cudaSuccess) return err;
-  const int c = shrink_cluster(e.units, sa.K, 4, 4 * S::KC, sms);
+  const int c = shrink_cluster(e.units, sa.K, 4, 256, sms);
   err = launch_cluster(shrink_x_kernel<RT>, dim3(static_cast<unsigned>(e.units) * c), c, S::smem, st, sa);
   if (err != cudaSuccess) return err;
   using C = Expand<RT, false, F32, false>;
@@ -1321,7 +1321,7 @@ cudaError_t launch_backward(const Backward& b, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t both = b.units * (b.want_x ? 2 : 1);
   // (the same split whichever outputs are wanted: their sums do not depend on it)
-  int c = shrink_cluster(2 * b.units, b.x.K > b.d.K ? b.x.K : b.d.K, 4, 4 * 64, b.sms);
+  int c = shrink_cluster(2 * b.units, b.x.K > b.d.K ? b.x.K : b.d.K, 4, 256, b.sms);
   e = launch_cluster(shrink_both_kernel<RT, F32>, dim3(static_cast<unsigned>(both * c)), c, smem_s, st,
                      b.d, b.x, static_cast<int>(b.units));
   if (e != cudaSuccess) return e;
@@ -1344,7 +1344,8 @@ cudaError_t launch_backward(const Backward& b, cudaStream_t st) {
   int64_t ctas = b.want_dx ? b.units * E::SUB * o.dx.parts : 0;
   ctas = grads * c + (ctas + c - 1) / c * c;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
-  return launch_cluster(backward_out_kernel<RT, F32>, dim3(static_cast<unsigned>(ctas)), c, smem_o, st, o);
+  return launch_cluster(backward_out_kernel<RT, F32>, dim3(static_cast<unsigned>(ctas)), c,
+                        grads ? smem_o : E::smem, st, o);
 }
 
 template <bool F32>
