@@ -332,10 +332,12 @@ int32_t moe_route_noalloc(const moe_shape* shape, const float* router_logits, in
 #define MOE_DTYPE_BF16 0
 #define MOE_DTYPE_F32 1
 
+#define MOE_ADAPTER_MAX 1024
+
 /* Low-rank adapters of many requests beside a shared projection: token t
  * uses adapter a = adapter_ids[t] and gets scale[a] * B_a (A_a x_t) beside
  * what the shared projection gave it.
- * Limits: num_tokens >= 0; 1 <= num_adapters <= 1024; rank a multiple of 8
+ * Limits: num_tokens >= 0; 1 <= num_adapters <= MOE_ADAPTER_MAX; rank a multiple of 8
  * in [8, 128]; in_features and out_features positive multiples of 8
  * up to 2^20 (smaller ranks are padded with zeros). */
 typedef struct {
@@ -347,12 +349,9 @@ typedef struct {
   int32_t out_dtype;      /* MOE_DTYPE_*: base, out and dout */
 } moe_adapter_shape;
 
-/* Forwards of at most this many tokens run as one kernel and use no
- * workspace: it may be NULL then. */
-#define MOE_ADAPTER_SMALL_TOKENS 256
-
 /* Workspace bytes of moe_adapter_forward (backward = 0) or
- * moe_adapter_backward (1).  0 for an invalid shape. */
+ * moe_adapter_backward (1).  0 for an invalid shape.  256: a small batch, whose
+ * forward runs as one kernel and uses none (the workspace may be NULL). */
 size_t moe_adapter_workspace_size(const moe_adapter_shape* shape, int32_t backward);
 
 /* out = base + scale_a B_a A_a x, one token a row; for prompts and for

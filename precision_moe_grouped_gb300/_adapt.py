@@ -12,7 +12,7 @@ from __future__ import annotations
 import ctypes
 
 from . import _lib
-from ._lib import (MOE_ADAMW_BLOCK, MOE_ADAPTER_SMALL_TOKENS, MOE_DTYPE_BF16, MOE_DTYPE_F32,
+from ._lib import (MOE_ADAMW_BLOCK, MOE_DTYPE_BF16, MOE_DTYPE_F32,
                    AdamwOptions, AdamwTensor, AdapterShape, BalanceShape, _bad, _check_tensor,
                    check, load)
 
@@ -141,7 +141,7 @@ class LowRankAdapters:
         else:
             ld_out = _check_rows(out, "out", dtype, shape, dev)
         s, n = self._call(T, kind, 0)
-        ws = None if T <= MOE_ADAPTER_SMALL_TOKENS else _scratch(n, x)
+        ws = None if n <= 256 else _scratch(n, x)   # small batches use none
         rc = self._lib.moe_adapter_forward(
             s, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
             _ptr(self.scale), _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(ws), n,

@@ -39,7 +39,7 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_layout", "moe_prepare_weights", 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
 MOE_ADAMW_BLOCK = 256
-MOE_ADAPTER_SMALL_TOKENS = 256
+MOE_ADAPTER_MAX = 1024
 
 MOE_NOALLOC_SCRATCH_BYTES = 4 << 20
 

@@ -2,14 +2,15 @@
 // projection: out = base + scale_a B_a (A_a x), and its gradients.
 //
 // Tokens are grouped by adapter on the device into tiles of up to 64 tokens
-// (group_kernel; batches of up to kSmallTokens group inside the product
-// kernels, tiles of up to 16), then:
+// (group_kernel), then:
 //   forward:   w = s A x                contracts over H      (shrink_x)
 //              out = base + B w         contracts over r      (expand)
 //   backward:  w = s A x, u = s B^T dout                      (shrink_x, shrink_d)
 //              dx = dx_base + A^T u                           (expand)
 //              dA = sum u x^T, dB = sum dout w^T              (grad: contracts over
 //                                                              the adapter's tokens)
+// A small batch's forward is one kernel (small_kernel), which finds tiles of up
+// to 16 tokens by itself.
 // With ranks of 8 to 128 every one of these does r multiply-adds for each
 // element it moves, mostly far below the ~290 operations a byte at which tensor
 // throughput would bind, so the layout serves the memory stream: the long
@@ -39,7 +40,7 @@ namespace {
 
 constexpr int kTile = 64;            // tokens of a tile
 constexpr int kSmallTile = 16;       // and of a small batch's
-constexpr int kSmallTokens = MOE_ADAPTER_SMALL_TOKENS;
+constexpr int kSmallTokens = 1024;   // of a small batch at most
 constexpr int kGroupThreads = 1024;
 constexpr int kWarps = 8;            // warps of the product kernels
 constexpr int kThreads = 32 * kWarps;
@@ -243,55 +244,70 @@ __device__ __forceinline__ bool find_tile(const TileSource& src, int i, Tile* ti
 }
 
 // Small batches: the tiles of up to 16 tokens that share an adapter, found by
-// every CTA for itself.  Thread t holds token t: its adapter (NA: none, -1: no
-// such token), its rank among that adapter's tokens, and a bit of `leaders`
-// where a tile begins with it (ranks 0, 16, 32, ...).
+// every CTA for itself.  A tile begins with the tokens of rank 0, 16, 32, ...
+// among their adapter's; their bits are set in `leaders`.
 struct SmallTiles {
-  int id, rank, count;   // count: tiles
+  int32_t ids[kSmallTokens];                // adapter (NA: none, -1: no such token)
+  int32_t count[MOE_ADAPTER_MAX + 1];       // tokens seen of each adapter
+  uint16_t rank[kSmallTokens];
+  unsigned leaders[kSmallTokens / 32];
+  int32_t tok[kSmallTile];                  // the tile in hand: its tokens, -1 past the end
+  int32_t head[2];                          // its adapter and first rank
 
-  // ids [kThreads], leaders [kThreads / 32] in shared memory.
-  __device__ __forceinline__ void find(const TileSource& src, int32_t* ids, unsigned* leaders) {
-    static_assert(kSmallTokens <= kThreads, "a thread per token");
-    const int t = threadIdx.x;
-    id = -1;
-    if (t < src.T) {
-      const int v = src.ids[t];
-      id = static_cast<unsigned>(v) < static_cast<unsigned>(src.NA) ? v : src.NA;
+  // All threads; returns the number of tiles.
+  __device__ __forceinline__ int find(const TileSource& src) {
+    const int end = (src.T + 31) / 32 * 32;
+    for (int t = threadIdx.x; t < end; t += kThreads) {
+      int id = -1;
+      if (t < src.T) {
+        const int v = src.ids[t];
+        id = static_cast<unsigned>(v) < static_cast<unsigned>(src.NA) ? v : src.NA;
+      }
+      ids[t] = id;
     }
-    ids[t] = id;
+    for (int c = threadIdx.x; c <= src.NA; c += kThreads) count[c] = 0;
     __syncthreads();
-    rank = 0;
-    const int end = min(t & ~3, src.T);   // whole groups of four before t
-#pragma unroll 4
-    for (int i = 0; i < end; i += 4) {
-      const int4 q = *reinterpret_cast<const int4*>(ids + i);
-      rank += (q.x == id) + (q.y == id) + (q.z == id) + (q.w == id);
+    if (threadIdx.x < 32) {   // in token order, 32 at a time
+      const int lane = threadIdx.x;
+      int id = ids[lane];
+      for (int t = 0; t < end; t += 32) {
+        const int next = t + 32 < end ? ids[t + 32 + lane] : -1;
+        const unsigned same = __match_any_sync(0xFFFFFFFFu, id);
+        const int before = __popc(same & ((1u << lane) - 1));
+        const int seen = id >= 0 ? count[id] : 0;
+        __syncwarp();
+        if (id >= 0 && before == 0) count[id] = seen + __popc(same);
+        __syncwarp();
+        rank[t + lane] = static_cast<uint16_t>(seen + before);
+        const unsigned b = __ballot_sync(0xFFFFFFFFu, id >= 0 && (seen + before) % kSmallTile == 0);
+        if (lane == 0) leaders[t / 32] = b;
+        id = next;
+      }
     }
-    for (int i = t & ~3; i < t; ++i) rank += ids[i] == id;
-    const unsigned b = __ballot_sync(0xFFFFFFFFu, id >= 0 && rank % kSmallTile == 0);
-    if ((t & 31) == 0) leaders[t >> 5] = b;
     __syncthreads();
-    count = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) count += __popc(leaders[w]);
+    int tiles = 0;
+    for (int w = 0; w < end / 32; ++w) tiles += __popc(leaders[w]);
+    return tiles;
   }
 
-  // Tile q: its tokens' numbers to tok [kSmallTile], -1 past the end.
-  __device__ __forceinline__ Tile take(int q, const TileSource& src, const int32_t* ids,
-                                       const unsigned* leaders, int32_t* tok, int32_t* head) const {
+  // All threads: tile q, its tokens in tok.
+  __device__ __forceinline__ Tile take(int q, const TileSource& src) {
     if (threadIdx.x < kSmallTile) tok[threadIdx.x] = -1;
-    int before = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w)
-      if (w < static_cast<int>(threadIdx.x >> 5)) before += __popc(leaders[w]);
-    const unsigned own = leaders[threadIdx.x >> 5], bit = 1u << (threadIdx.x & 31);
-    if ((own & bit) && before + __popc(own & (bit - 1)) == q) head[0] = id, head[1] = rank;
+    if (threadIdx.x == 0) {
+      int w = 0, left = q;
+      while (left >= __popc(leaders[w])) left -= __popc(leaders[w++]);
+      const int t = 32 * w + static_cast<int>(__fns(leaders[w], 0, left + 1));
+      head[0] = ids[t], head[1] = rank[t];
+    }
     __syncthreads();
     const int adapter = head[0], first = head[1];
-    const bool in = id == adapter && rank >= first && rank < first + kSmallTile;
-    if (in) tok[rank - first] = static_cast<int32_t>(threadIdx.x);
+    for (int t = threadIdx.x; t < src.T; t += kThreads)
+      if (ids[t] == adapter && rank[t] >= first && rank[t] < first + kSmallTile)
+        tok[rank[t] - first] = t;
+    __syncthreads();
     Tile tile;
-    tile.n = __syncthreads_count(in);
+    const int lane = threadIdx.x & 31;
+    tile.n = __popc(__ballot_sync(0xFFFFFFFFu, lane < kSmallTile && tok[lane % kSmallTile] >= 0));
     tile.adapter = adapter < src.NA ? adapter : -1;
     tile.slot = 0;
     return tile;
@@ -792,7 +808,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(const ExpandArgs a) {
 }
 
 // ------------------------------------------------------- small batches
-// The whole forward of a batch of up to kSmallTokens in one kernel: a
+// The whole forward of a small batch in one kernel: a
 // cluster takes a tile (16 tokens that share an adapter).  Its warps
 // share out the 32-element chunks of H (ranks are MMA-M, tokens MMA-N; lane (g, t)
 // of a chunk loads the 8 elements at 8 t of rank rows g and g + 8 and of token g
@@ -817,25 +833,21 @@ __global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
   using C = typename S::E;
   constexpr int NT = S::NT, RS = S::RS, RP = S::RP;
   extern __shared__ __align__(128) uint8_t sm[];
-  __shared__ __align__(16) int32_t ids[kThreads];
-  __shared__ unsigned leaders[kThreads / 32];
-  __shared__ int32_t tok[kSmallTile], head[2];
+  __shared__ SmallTiles tiles;
   uint8_t* v_s = sm + C::STAGES * C::STAGE;
   float* red = reinterpret_cast<float*>(sm + C::smem);
   griddep_wait();
   const int CS = static_cast<int>(cluster_size()), rank_c = static_cast<int>(cluster_rank());
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int c0 = e.cols * rank_c / CS, c1 = e.cols * (rank_c + 1) / CS;
-  SmallTiles tiles;
-  tiles.find(a.tiles, ids, leaders);
   const int q = blockIdx.x / CS;
-  if (q >= tiles.count) return;   // the whole cluster
-  const Tile tile = tiles.take(q, a.tiles, ids, leaders, tok, head);
+  if (q >= tiles.find(a.tiles)) return;   // the whole cluster
+  const Tile tile = tiles.take(q, a.tiles);
   if (tile.adapter < 0) {
-    copy_rows<F32>(e, tile, c0 * C::FB, (c1 - c0) * C::FB, [&](int i) { return tok[i]; });
+    copy_rows<F32>(e, tile, c0 * C::FB, (c1 - c0) * C::FB, [&](int i) { return tiles.tok[i]; });
     return;
   }
-  const Blocks<RT, false, F32, true> blocks(e, tile.adapter, c1, sm, [&](int i) { return tok[i]; });
+  const Blocks<RT, false, F32, true> blocks(e, tile.adapter, c1, sm, [&](int i) { return tiles.tok[i]; });
 #pragma unroll
   for (int i = 0; i < C::STAGES - 1; ++i) blocks.fetch(c0 + i, i);
   float acc[RT][NT][4];
@@ -848,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
   const __nv_bfloat16* row[NT];          // null: no such token
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int64_t id = tok[8 * j + g];
+    const int64_t id = tiles.tok[8 * j + g];
     row[j] = id >= 0 ? static_cast<const __nv_bfloat16*>(a.src) + id * a.ld + 8 * t : nullptr;
   }
   const int live = (tile.n + 7) / 8;     // columns with a token
@@ -1155,7 +1167,11 @@ struct AdapterWs {
 AdapterWs adapter_ws(const moe_adapter_shape* s, bool backward) {
   const int64_t T = s->num_tokens, NA = s->num_adapters;
   AdapterWs w = {};
-  w.small = !backward && T <= kSmallTokens;
+  // One kernel where it is no slower than three (7168 x 7168, rank 16, 8
+  // adapters: 7.7 us against 12.4 at 64 tokens, 10.2 / 13.3 at 256, 16.8 / 19.0 at
+  // 1021; 64 adapters: 21.0 / 28.3).  At rank 128 its tiles of 16 tokens read the
+  // pools too often (2048 x 2048: 10.1 / 14.2 at 64 tokens, 20.2 / 14.6 at 256).
+  w.small = !backward && T <= (s->rank <= 64 ? kSmallTokens : 64);
   // an adapter with n tokens has at most n / 16 + 1 tiles
   const int64_t small_units = T / kSmallTile + NA + 1;
   w.units = w.small ? (small_units < T ? small_units : T) : max_tiles(T, NA);
@@ -1182,7 +1198,7 @@ AdapterWs adapter_ws(const moe_adapter_shape* s, bool backward) {
 int32_t check_adapter(const moe_adapter_shape* s) {
   if (!s) return entry_fail(MOE_ERR_INVALID_ARG, "shape is NULL");
   if (s->num_tokens < 0) return entry_fail(MOE_ERR_INVALID_ARG, "num_tokens < 0");
-  if (s->num_adapters < 1 || s->num_adapters > 1024)
+  if (s->num_adapters < 1 || s->num_adapters > MOE_ADAPTER_MAX)
     return entry_fail(MOE_ERR_INVALID_ARG, "num_adapters must be in [1, 1024]");
   if (s->rank < 1 || s->rank > 128)
     return entry_fail(MOE_ERR_INVALID_ARG, "rank must be in [8, 128]");
@@ -1232,7 +1248,7 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, size_
 cudaError_t launch_group(const int32_t* ids, int T, int NA, const Groups& g, cudaStream_t st) {
   static DeviceOnce once;
   const size_t smem = (32 * static_cast<size_t>(NA + 1) + 2 * (NA + 2)) * 4;
-  const cudaError_t e = set_smem_limit_once(group_kernel, (32 * 1025 + 2 * 1026) * 4, once);
+  const cudaError_t e = set_smem_limit_once(group_kernel, (32 * (MOE_ADAPTER_MAX + 1) + 2 * (MOE_ADAPTER_MAX + 2)) * 4, once);
   if (e != cudaSuccess) return e;
   return launch_pdl(group_kernel, dim3(1), dim3(kGroupThreads), smem, st, ids, T, NA, g);
 }

@@ -43,6 +43,9 @@ def test_adapter_shapes(lib, bad, code):
 
 def test_adapter_workspace(lib):
     assert lib.moe_adapter_workspace_size(ashape(), 0) == 256          # unused
+    assert lib.moe_adapter_workspace_size(ashape(T=1024), 0) == 256
+    assert lib.moe_adapter_workspace_size(ashape(T=1025), 0) > 256
+    assert lib.moe_adapter_workspace_size(ashape(T=65, r=72), 0) > 256
     big = lib.moe_adapter_workspace_size(ashape(T=5000), 0)
     assert big > 5000 * 16 * 2 * 3 and big % 256 == 0
     assert lib.moe_adapter_workspace_size(ashape(T=5000), 1) > big
@@ -62,7 +65,7 @@ def backward(lib, s, dout=0x100000, ld_dout=128, x=0x200000, ld_x=256, ids=0x300
 
 
 def test_adapter_refusals(lib):
-    s = ashape(T=500)
+    s = ashape(T=5000)
     for k in ("x", "ids", "a", "b", "out", "ws"):
         assert forward(lib, s, **{k: None}) == L.MOE_ERR_INVALID_ARG, k
     for k in ("x", "a", "b", "out", "base"):
@@ -147,7 +150,7 @@ def test_adamw_refusals(lib):
 def test_no_device_gives_cuda_error(lib):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present: these pointers must not reach it")
-    assert forward(lib, ashape(T=500)) == L.MOE_ERR_CUDA
+    assert forward(lib, ashape(T=5000)) == L.MOE_ERR_CUDA
     assert forward(lib, ashape()) == L.MOE_ERR_CUDA
     assert backward(lib, ashape(T=500)) == L.MOE_ERR_CUDA
     assert balance(lib, L.BalanceShape(100, 16, 2, 1, 1.0)) == L.MOE_ERR_CUDA

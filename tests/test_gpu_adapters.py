@@ -120,6 +120,13 @@ SHAPES = [
     (1100, 5, 16, 2048, 384, "runs"),
     (4099, 1, 64, 256, 520, "one"),
     (100, 4, 16, 128, 128, "none"),
+    # either side of the batches that one kernel takes
+    (1024, 1024, 16, 72, 136, "mixed"),
+    (1024, 3, 64, 264, 520, "runs"),
+    (1025, 1024, 16, 72, 136, "mixed"),
+    (1025, 2, 32, 1000, 264, "one"),
+    (64, 9, 128, 520, 264, "mixed"),
+    (65, 9, 128, 520, 264, "mixed"),
 ]
 
 
