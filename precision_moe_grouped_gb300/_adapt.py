@@ -64,6 +64,21 @@ def _check_flat(t, name: str, dtype, shape: tuple, device) -> None:
         _check_tensor(t, name, cuda=True, dtype=dtype, shape=shape, device=device)
 
 
+def _same_device(device, made_on) -> None:
+    if device != made_on:
+        _bad(f"the current device is cuda:{device}, this object's tensors are on cuda:{made_on}")
+
+
+def _check_numel(t, name: str, key, dtype, n: int, device) -> int:
+    """A contiguous CUDA tensor of n elements (dtype None: of one byte each);
+    returns its address."""
+    if not (t is not None and t.is_cuda and t.get_device() == device and t.numel() == n
+            and t.is_contiguous() and (t.dtype is dtype if dtype else t.element_size() == 1)):
+        _check_tensor(t, f"{name}[{key}]", cuda=True, dtype=dtype, numel=n, device=device,
+                      itemsize=None if dtype else 1)
+    return t.data_ptr()
+
+
 def _scratch(n: int, like):
     """The call's workspace, from torch's allocator for the current stream."""
     return torch.empty(n, dtype=torch.uint8, device=like.device)
@@ -93,7 +108,7 @@ class LowRankAdapters:
         if scale is not None:
             _check_tensor(scale, "scale", cuda=True, dtype=torch.float32, device=dev,
                           shape=(self.num_adapters,))
-        self.a, self.b, self.scale, self.device = a, b, scale, a.device
+        self.a, self.b, self.scale, self.device, self._dev = a, b, scale, a.device, dev
         self._lib = load()
         self._sizes = {}
         for kind in (MOE_DTYPE_BF16, MOE_DTYPE_F32):   # rejects unsupported sizes here
@@ -129,6 +144,8 @@ class LowRankAdapters:
         [T, N] bf16 or float32; rows may be strided.  `out` may be `base`
         itself."""
         dev = _device()
+        if dev != self._dev:
+            _same_device(dev, self._dev)
         T = x.shape[0]
         ld_x = _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
         _check_flat(ids, "ids", torch.int32, (T,), dev)
@@ -159,6 +176,8 @@ class LowRankAdapters:
         float32 [NA, N, r], zero for adapters without tokens.  What is not
         needed comes back as None.  `dx` may be `dx_base`, not x or dout."""
         dev = _device()
+        if dev != self._dev:
+            _same_device(dev, self._dev)
         T = x.shape[0]
         kind, wide = self._kind(dout.dtype, "dout"), (T, self.in_features)
         ld_dout = _check_rows(dout, "dout", dout.dtype, (T, self.out_features), dev)
@@ -279,13 +298,11 @@ class AdamW:
         _bind_torch()
         if state_bits not in (8, 32):
             _bad(f"state_bits must be 8 or 32, got {state_bits}")
-        dev = _device()
+        dev = self._dev = _device()
         # detached: keeps the bound memory alive whatever becomes of the originals
         self.params = [t.detach() for t in params]
         self.state_bits, self.lr, self.betas, self.eps = state_bits, lr, betas, eps
         self.weight_decay, self.steps_done = weight_decay, steps_done
-        for i, p in enumerate(self.params):
-            _check_tensor(p, f"params[{i}]", cuda=True, dtype=torch.float32, device=dev)
         sizes = [p.numel() for p in self.params]
         blocks = [-(-n // MOE_ADAMW_BLOCK) for n in sizes]
         if state is None:
@@ -298,33 +315,26 @@ class AdamW:
                           for k in ("m_scale", "v_scale")}
         keys = ("m", "v") if state_bits == 32 else ("m", "v", "m_scale", "v_scale")
         self.state = {}
+        self._table = (AdamwTensor * max(1, len(sizes)))()
+        f32 = torch.float32
+        for e, p, n, i in zip(self._table, self.params, sizes, range(len(sizes))):
+            e.param, e.n = _check_numel(p, "params", i, f32, n, dev), n
+        if len({p.data_ptr() for p in self.params if p.numel()}) < sum(n > 0 for n in sizes):
+            _bad("params must be distinct")   # updated in place, side by side
         for key in keys:
-            self.state[key] = list(state.get(key) or ())
-            if len(self.state[key]) != len(sizes):
+            held = self.state[key] = [t.detach() for t in state.get(key) or ()]
+            if len(held) != len(sizes):
                 _bad(f"state[{key!r}] must hold {len(sizes)} tensors")
             scales = key.endswith("scale")
-            for i, t in enumerate(self.state[key]):
-                n = blocks[i] if scales else sizes[i]
-                if scales or state_bits == 32:
-                    _check_tensor(t, f"state[{key!r}][{i}]", cuda=True, dtype=torch.float32, numel=n,
-                                  device=dev)
-                else:
-                    _check_tensor(t, f"state[{key!r}][{i}]", cuda=True, itemsize=1, numel=n,
-                                  device=dev)
+            kind = f32 if scales or state_bits == 32 else None   # None: one byte each
+            for e, t, n, i in zip(self._table, held, blocks if scales else sizes, range(len(held))):
+                setattr(e, key, _check_numel(t, f"state[{key!r}]", i, kind, n, dev))
         self.copies = None if copies is None else [t.detach() for t in copies]
         if self.copies is not None:
             if len(self.copies) != len(sizes):
                 _bad(f"copies must hold {len(sizes)} tensors")
-            for i, t in enumerate(self.copies):
-                _check_tensor(t, f"copies[{i}]", cuda=True, dtype=torch.bfloat16, numel=sizes[i],
-                              device=dev)
-        self._table = (AdamwTensor * max(1, len(sizes)))()
-        for i, n in enumerate(sizes):
-            e = self._table[i]
-            e.param, e.n = self.params[i].data_ptr(), n
-            for key in keys:
-                setattr(e, key, self.state[key][i].data_ptr())
-            e.param_bf16 = None if self.copies is None else self.copies[i].data_ptr()
+            for e, t, n, i in zip(self._table, self.copies, sizes, range(len(sizes))):
+                e.param_bf16 = _check_numel(t, "copies", i, torch.bfloat16, n, dev)
         self._options = AdamwOptions(state_bits=state_bits)
         self.bind_grads(grads)
 
@@ -337,11 +347,11 @@ class AdamW:
         if kind not in (torch.float32, torch.bfloat16):
             _bad(f"grads must be float32 or bfloat16, got {kind}")
         dev = _device()
-        for i, (t, p) in enumerate(zip(grads, self.params)):
-            _check_tensor(t, f"grads[{i}]", cuda=True, dtype=kind, numel=p.numel(), device=dev)
+        at = [_check_numel(t, "grads", i, kind, p.numel(), dev)
+              for i, (t, p) in enumerate(zip(grads, self.params))]
         self.grads = grads
-        for e, t in zip(self._table, grads):
-            e.grad = t.data_ptr()
+        for e, address in zip(self._table, at):
+            e.grad = address
         self._options.grad_dtype = MOE_DTYPE_F32 if kind == torch.float32 else MOE_DTYPE_BF16
 
     def step(self, grads=None, step: int | None = None, grad_scale=None) -> None:
@@ -351,8 +361,9 @@ class AdamW:
             self.bind_grads(grads)
         t = self.steps_done + 1 if step is None else step
         dev, o = _device(), self._options
+        _same_device(dev, self._dev)
         if grad_scale is not None:
-                _check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
+            _check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
                           device=dev)
         o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps

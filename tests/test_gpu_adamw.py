@@ -229,6 +229,7 @@ def test_refusals():
         lambda: P.AdamW(p, [t.half() for t in g]),
         lambda: P.AdamW([t.cpu() for t in p], g),
         lambda: P.AdamW(p, g, state_bits=16),
+        lambda: P.AdamW([p[0], p[0]], [g[0], g[0]]),
         lambda: P.AdamW(p, g, copies=[t.clone() for t in p]),
         lambda: P.AdamW(p, g, state={"m": p, "v": p[:1]}),
         lambda: P.AdamW(p, g, state_bits=8, state={"m": g, "v": g}),
