@@ -363,7 +363,8 @@ size_t moe_adapter_workspace_size(const moe_adapter_shape* shape, int32_t backwa
  *   scale        float [NA], or NULL for 1
  *   base         [T, N] of out_dtype, rows ld_base apart; NULL for zero; may
  *                be out itself
- *   out          [T, N] of out_dtype, rows ld_out apart
+ *   out          [T, N] of out_dtype, rows ld_out apart; may be x itself (H =
+ *                N, the same stride), otherwise no part of x
  * x, a, b, base and out 16-byte aligned, row strides multiples of 8 elements
  * and at least the row's length.  The product A_a x is held in float and
  * enters the second product as bf16 terms: two for a bf16 out (an error

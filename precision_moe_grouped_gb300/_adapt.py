@@ -40,6 +40,20 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _rows(t, name: str) -> int:
+    try:
+        return t.shape[0]
+    except (AttributeError, IndexError):
+        _bad(f"{name} must be a tensor of rows, got {t if t is None else type(t)}")
+
+
+def _detached(ts, name: str) -> list:
+    try:
+        return [t.detach() for t in ts]
+    except (AttributeError, TypeError):
+        _bad(f"{name} must be a list of tensors")
+
+
 def _check_rows(t, name: str, dtype, shape: tuple, device) -> int:
     """A [rows, cols] CUDA tensor with unit column stride; rows may be apart.
     Returns the elements between rows (a single row's stride says nothing)."""
@@ -142,11 +156,11 @@ class LowRankAdapters:
 
         x bf16 [T, H], ids int32 [T] (outside [0, NA): no adapter), base
         [T, N] bf16 or float32; rows may be strided.  `out` may be `base`
-        itself."""
+        itself, or x."""
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        T = x.shape[0]
+        T = _rows(x, "x")
         ld_x = _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
         _check_flat(ids, "ids", torch.int32, (T,), dev)
         dtype = base.dtype if base is not None else out.dtype if out is not None else (
@@ -178,7 +192,9 @@ class LowRankAdapters:
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        T = x.shape[0]
+        T = _rows(x, "x")
+        if dout is None:
+            _bad("dout is None")
         kind, wide = self._kind(dout.dtype, "dout"), (T, self.in_features)
         ld_dout = _check_rows(dout, "dout", dout.dtype, (T, self.out_features), dev)
         ld_x = _check_rows(x, "x", torch.bfloat16, wide, dev)
@@ -241,7 +257,7 @@ class BalanceLoss:
         sequence), weights and dweights float32 [T, k] (both or neither: adds
         the gradient of the routing weights)."""
         dev, E, k = _device(), self.num_experts, self.top_k
-        T = logits.shape[0]
+        T = _rows(logits, "logits")
         _check_flat(logits, "logits", torch.float32, (T, E), dev)
         _check_flat(ids, "ids", torch.int32, (T, k), dev)
         if mask is not None:
@@ -300,7 +316,7 @@ class AdamW:
             _bad(f"state_bits must be 8 or 32, got {state_bits}")
         dev = self._dev = _device()
         # detached: keeps the bound memory alive whatever becomes of the originals
-        self.params = [t.detach() for t in params]
+        self.params = _detached(params, "params")
         self.state_bits, self.lr, self.betas, self.eps = state_bits, lr, betas, eps
         self.weight_decay, self.steps_done = weight_decay, steps_done
         sizes = [p.numel() for p in self.params]
@@ -322,14 +338,14 @@ class AdamW:
         if len({p.data_ptr() for p in self.params if p.numel()}) < sum(n > 0 for n in sizes):
             _bad("params must be distinct")   # updated in place, side by side
         for key in keys:
-            held = self.state[key] = [t.detach() for t in state.get(key) or ()]
+            held = self.state[key] = _detached(state.get(key) or (), f"state[{key!r}]")
             if len(held) != len(sizes):
                 _bad(f"state[{key!r}] must hold {len(sizes)} tensors")
             scales = key.endswith("scale")
             kind = f32 if scales or state_bits == 32 else None   # None: one byte each
             for e, t, n, i in zip(self._table, held, blocks if scales else sizes, range(len(held))):
                 setattr(e, key, _check_numel(t, f"state[{key!r}]", i, kind, n, dev))
-        self.copies = None if copies is None else [t.detach() for t in copies]
+        self.copies = None if copies is None else _detached(copies, "copies")
         if self.copies is not None:
             if len(self.copies) != len(sizes):
                 _bad(f"copies must hold {len(sizes)} tensors")
@@ -340,7 +356,7 @@ class AdamW:
 
     def bind_grads(self, grads) -> None:
         """Take the next steps' gradients from these tensors."""
-        grads = [t.detach() for t in grads]
+        grads = _detached(grads, "grads")
         if len(grads) != len(self.params):
             _bad(f"grads must hold {len(self.params)} tensors")
         kind = grads[0].dtype if grads else torch.float32

@@ -876,7 +876,8 @@ __global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
       const bool in = k < 32 * c.y && k + 8 * t < a.K;
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        x[u][j] = in && row[j] ? ldg16(row[j] + k) : make_uint4(0, 0, 0, 0);
+        x[u][j] = in && row[j] ? *reinterpret_cast<const uint4*>(row[j] + k)   // (may be out's)
+                               : make_uint4(0, 0, 0, 0);
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll

@@ -169,6 +169,16 @@ def test_binding_refuses_host_tensors(lib):
         P.BalanceLoss(8, 9)
 
 
+def test_binding_refuses_what_is_no_tensor(lib):
+    ids = torch.zeros(4, 2, dtype=torch.int32)
+    for z in (None, 3.0, torch.zeros(())):
+        with pytest.raises(P.MoeError, match="logits"):
+            P.BalanceLoss(8, 2)(z, ids)
+    for params, grads in ((None, []), ([None], []), ([], None)):
+        with pytest.raises(P.MoeError, match="list of tensors"):
+            P.AdamW(params, grads)
+
+
 def test_structs_match_the_header(tmp_path):
     """The binding's structures have the sizes and offsets C gives them."""
     import shutil

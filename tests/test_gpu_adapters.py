@@ -295,6 +295,17 @@ def test_offsets_beyond_32_bits():
     assert all(torch.equal(p, q) for p, q in zip(ref, op.backward(c["dout"], x, c["ids"])))
 
 
+@pytest.mark.parametrize("T", [3, 200, 1500])
+def test_forward_over_its_input(T):
+    """x += the adapters' products of x: a tile's rows are read before any of
+    them is written."""
+    c = make(T, 4, 16, 512, 512, torch.bfloat16)
+    op = P.LowRankAdapters(c["a"], c["b"], c["scale"])
+    want = op.forward(c["x"], c["ids"], c["x"])
+    x = c["x"].clone()
+    assert op.forward(x, c["ids"], x, out=x) is x and torch.equal(x, want)
+
+
 def test_refusals():
     c = make(20, 3, 16, 64, 64, torch.bfloat16)
     op = P.LowRankAdapters(c["a"], c["b"], c["scale"])
