@@ -337,8 +337,8 @@ int32_t moe_route_noalloc(const moe_shape* shape, const float* router_logits, in
 /* Low-rank adapters of many requests beside a shared projection: token t
  * uses adapter a = adapter_ids[t] and gets scale[a] * B_a (A_a x_t) beside
  * what the shared projection gave it.
- * Limits: num_tokens >= 0; 1 <= num_adapters <= MOE_ADAPTER_MAX; rank a multiple of 8
- * in [8, 128]; in_features and out_features positive multiples of 8
+ * Limits: 0 <= num_tokens <= 2^30; 1 <= num_adapters <= MOE_ADAPTER_MAX; rank a
+ * multiple of 8 in [8, 128]; in_features and out_features positive multiples of 8
  * up to 2^20 (smaller ranks are padded with zeros). */
 typedef struct {
   int32_t num_tokens;     /* T */

@@ -41,7 +41,8 @@ namespace {
 constexpr int kTile = 64;            // tokens of a tile
 constexpr int kSmallTile = 16;       // and of a small batch's
 constexpr int kSmallTokens = 1024;   // of a small batch at most
-constexpr int kGroupThreads = 1024;
+constexpr int kGroupThreads = 512;
+constexpr int kGroupCtas = 8;
 constexpr int kWarps = 8;            // warps of the product kernels
 constexpr int kThreads = 32 * kWarps;
 
@@ -130,23 +131,34 @@ __host__ __device__ inline int64_t max_tiles(int64_t T, int64_t NA) {
 }
 
 // Slots of the tokens in the order (adapter 0 .. NA-1, none), stable in the
-// token.  One CTA: warp w owns the w-th contiguous 32nd of the tokens and a
-// histogram of it; the histograms' running sums give each warp its bases, and
-// a warp hands out slots to its tokens in order.
+// token.  One cluster: each of its warps owns a contiguous run of the tokens
+// and a histogram of it; the histograms' running sums, over the CTA's warps and
+// then over the CTAs, give each warp its bases, and it hands out slots to its
+// tokens in order.  Bound by the latency of its stages, and from some 10^4
+// tokens by the shared-memory atomics and matches of its SMs, hence eight
+// (a whole call at 64 x 64 features and rank 8, tokens of 200 adapters at
+// random: 12.4 us at 8192 tokens and 31 at 65,536, against 19 and 90 with one
+// CTA of 1024 threads).
 __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __restrict__ ids,
                                                               int T, int NA, Groups g) {
   extern __shared__ __align__(128) uint8_t sm[];
+  constexpr int kGroupWarps = kGroupThreads / 32;
   const int C = NA + 1;                 // columns: the adapters and "none"
-  int32_t* hist = reinterpret_cast<int32_t*>(sm);   // [32][C]
-  int32_t* count = hist + 32 * C;       // [C + 1] tokens
-  int32_t* tfirst = count + C + 1;      // [C + 1] first tile
+  int32_t* hist = reinterpret_cast<int32_t*>(sm);   // [warps][C]
+  int32_t* mine = hist + kGroupWarps * C;   // [C] this CTA's tokens
+  int32_t* count = mine + C;            // [C] all tokens
+  int32_t* start = count + C;           // [C] slots of the column before this CTA's
+  int32_t* tfirst = start + C;          // [C + 1] first tile
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int cta = static_cast<int>(cluster_rank());
+  constexpr int threads = kGroupCtas * kGroupThreads;
+  const int first = cta * kGroupThreads + static_cast<int>(threadIdx.x);   // in the cluster
   griddep_wait();
   griddep_launch_dependents();
-  for (int i = threadIdx.x; i < 32 * C; i += kGroupThreads) hist[i] = 0;
+  for (int i = threadIdx.x; i < kGroupWarps * C; i += kGroupThreads) hist[i] = 0;
   __syncthreads();
-  const int per = ((T + 31) / 32 + 31) / 32 * 32;   // tokens of a warp, whole rounds
-  const int64_t t0 = static_cast<int64_t>(per) * warp;
+  const int per = (T + threads - 1) / threads * 32;   // tokens of a warp, whole rounds
+  const int64_t t0 = static_cast<int64_t>(per) * (first / 32);
   const int t1 = static_cast<int>(min(t0 + per, static_cast<int64_t>(T)));
   for (int64_t t = t0 + lane; t < t1; t += 32) {
     const int id = ids[t];
@@ -155,13 +167,27 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
   __syncthreads();
   for (int c = threadIdx.x; c < C; c += kGroupThreads) {
     int sum = 0;
-    for (int w = 0; w < 32; ++w) {
+#pragma unroll
+    for (int w = 0; w < kGroupWarps; ++w) {
       const int n = hist[w * C + c];
       hist[w * C + c] = sum;            // tokens of this column in earlier warps
       sum += n;
     }
+    mine[c] = sum;
+  }
+  cluster_sync();
+  for (int c = threadIdx.x; c < C; c += kGroupThreads) {
+    int n[kGroupCtas], sum = 0, before = 0;
+#pragma unroll
+    for (int q = 0; q < kGroupCtas; ++q) n[q] = cluster_load(mine + c, q);
+#pragma unroll
+    for (int q = 0; q < kGroupCtas; ++q) {
+      if (q < cta) before += n[q];
+      sum += n[q];
+    }
     count[c] = sum;
-    g.counts[c] = sum;
+    start[c] = before;
+    if (cta == 0) g.counts[c] = sum;
   }
   __syncthreads();
   if (warp == 0) {   // exclusive sum of the columns' tiles
@@ -178,12 +204,15 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
       if (c < C) tfirst[c] = run + x - n;
       run += __shfl_sync(0xFFFFFFFFu, x, 31);
     }
-    if (lane == 0) tfirst[C] = run, *g.num_tiles = run;
+    if (lane == 0) {
+      tfirst[C] = run;
+      if (cta == 0) *g.num_tiles = run;
+    }
   }
   __syncthreads();
-  for (int c = threadIdx.x; c <= C; c += kGroupThreads) g.first[c] = tfirst[c];
+  for (int c = first; c <= C; c += threads) g.first[c] = tfirst[c];
   const int tiles = tfirst[C];
-  for (int i = threadIdx.x; i < tiles; i += kGroupThreads) {
+  for (int i = first; i < tiles; i += threads) {
     int lo = 0, hi = C;                 // the last column whose first tile is at or before i
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -192,7 +221,7 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
     }
     g.tiles[i] = make_int4(lo < NA ? lo : -1, min(kTile, count[lo] - (i - tfirst[lo]) * kTile), 0, 0);
   }
-  for (int i = threadIdx.x; i < C * kTile; i += kGroupThreads) {   // the ends of the last tiles
+  for (int i = first; i < C * kTile; i += threads) {   // the ends of the last tiles
     const int c = i / kTile, slot = count[c] + i % kTile;
     if (slot < (tfirst[c + 1] - tfirst[c]) * kTile)
       g.perm[static_cast<int64_t>(tfirst[c]) * kTile + slot] = -1;
@@ -210,11 +239,12 @@ __global__ void __launch_bounds__(kGroupThreads) group_kernel(const int32_t* __r
     if (c >= 0) base = hist[warp * C + c];
     __syncwarp();
     if (c >= 0) {
-      g.perm[static_cast<int64_t>(tfirst[c]) * kTile + base + rank] = static_cast<int32_t>(t);
+      g.perm[static_cast<int64_t>(tfirst[c]) * kTile + start[c] + base + rank] = static_cast<int32_t>(t);
       if (rank == 0) hist[warp * C + c] = base + __popc(same);
     }
     __syncwarp();
   }
+  cluster_sync();   // no CTA leaves while another reads its shared memory
 }
 
 // A tile as the product kernels see it: adapter (-1: none), tokens, first slot
@@ -1199,6 +1229,8 @@ AdapterWs adapter_ws(const moe_adapter_shape* s, bool backward) {
 int32_t check_adapter(const moe_adapter_shape* s) {
   if (!s) return entry_fail(MOE_ERR_INVALID_ARG, "shape is NULL");
   if (s->num_tokens < 0) return entry_fail(MOE_ERR_INVALID_ARG, "num_tokens < 0");
+  if (s->num_tokens > (1 << 30))   // the lists' counts stay inside 32 bits
+    return entry_fail(MOE_ERR_UNSUPPORTED, "num_tokens must be at most 2^30");
   if (s->num_adapters < 1 || s->num_adapters > MOE_ADAPTER_MAX)
     return entry_fail(MOE_ERR_INVALID_ARG, "num_adapters must be in [1, 1024]");
   if (s->rank < 1 || s->rank > 128)
@@ -1228,10 +1260,10 @@ int32_t check_rows(const char* name, const void* p, int64_t ld, int64_t len) {
 // Launches a kernel whose grid.x is a multiple of the cluster size, with PDL.
 template <typename... KArgs, typename... Args>
 cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, size_t smem,
-                           cudaStream_t st, Args&&... args) {
+                           cudaStream_t st, int threads, Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
@@ -1248,10 +1280,11 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), dim3 grid, int cluster, size_
 
 cudaError_t launch_group(const int32_t* ids, int T, int NA, const Groups& g, cudaStream_t st) {
   static DeviceOnce once;
-  const size_t smem = (32 * static_cast<size_t>(NA + 1) + 2 * (NA + 2)) * 4;
-  const cudaError_t e = set_smem_limit_once(group_kernel, (32 * (MOE_ADAPTER_MAX + 1) + 2 * (MOE_ADAPTER_MAX + 2)) * 4, once);
+  auto smem = [](int na) { return (kGroupThreads / 32 + 4) * (na + 2) * sizeof(int32_t); };
+  const cudaError_t e = set_smem_limit_once(group_kernel, smem(MOE_ADAPTER_MAX), once);
   if (e != cudaSuccess) return e;
-  return launch_pdl(group_kernel, dim3(1), dim3(kGroupThreads), smem, st, ids, T, NA, g);
+  return launch_cluster(group_kernel, dim3(kGroupCtas), kGroupCtas, smem(NA), st, kGroupThreads,
+                        ids, T, NA, g);
 }
 
 // CTAs that share a tile: powers of two up to 8, while the clusters fill no
@@ -1287,7 +1320,7 @@ cudaError_t launch_small(const ShrinkArgs& sa, ExpandArgs e, int sms, cudaStream
   // adapters of rank 16: 11.6 us at four, 16.5 at eight, 13.4 at two)
   const int64_t u = e.units;
   const int c = 8 * u <= 2 * sms ? 8 : 4 * u <= 3 * sms ? 4 : 2 * u <= 4 * sms ? 2 : 1;
-  return launch_cluster(small_kernel<RT, F32>, dim3(static_cast<unsigned>(u * c)), c, S::smem, st, sa, e);
+  return launch_cluster(small_kernel<RT, F32>, dim3(static_cast<unsigned>(u * c)), c, S::smem, st, kThreads, sa, e);
 }
 
 template <int RT, bool F32>
@@ -1297,7 +1330,8 @@ cudaError_t launch_forward(const ShrinkArgs& sa, ExpandArgs e, int sms, cudaStre
   cudaError_t err = set_smem_limit_once(shrink_x_kernel<RT>, S::smem, once_s);
   if (err != cudaSuccess) return err;
   const int c = shrink_cluster(e.units, sa.K, 4, 256, sms);
-  err = launch_cluster(shrink_x_kernel<RT>, dim3(static_cast<unsigned>(e.units) * c), c, S::smem, st, sa);
+  err = launch_cluster(shrink_x_kernel<RT>, dim3(static_cast<unsigned>(e.units) * c), c, S::smem, st, kThreads,
+                       sa);
   if (err != cudaSuccess) return err;
   using C = Expand<RT, false, F32, false>;
   err = set_smem_limit_once(expand_kernel<RT, F32>, C::smem, once_e);
@@ -1340,7 +1374,7 @@ cudaError_t launch_backward(const Backward& b, cudaStream_t st) {
   // (the same split whichever outputs are wanted: their sums do not depend on it)
   int c = shrink_cluster(2 * b.units, b.x.K > b.d.K ? b.x.K : b.d.K, 4, 256, b.sms);
   e = launch_cluster(shrink_both_kernel<RT, F32>, dim3(static_cast<unsigned>(both * c)), c, smem_s, st,
-                     b.d, b.x, static_cast<int>(b.units));
+                     kThreads, b.d, b.x, static_cast<int>(b.units));
   if (e != cudaSuccess) return e;
   constexpr size_t gx = Grad<RT, false>::smem, gd = Grad<RT, F32>::smem;
   using E = Expand<RT, true, false, false>;
@@ -1362,7 +1396,7 @@ cudaError_t launch_backward(const Backward& b, cudaStream_t st) {
   ctas = grads * c + (ctas + c - 1) / c * c;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidConfiguration;
   return launch_cluster(backward_out_kernel<RT, F32>, dim3(static_cast<unsigned>(ctas)), c,
-                        grads ? smem_o : E::smem, st, o);
+                        grads ? smem_o : E::smem, st, kThreads, o);
 }
 
 template <bool F32>

@@ -27,7 +27,8 @@ def ashape(T=64, NA=4, r=16, H=256, N=128, kind=L.MOE_DTYPE_BF16):
 
 
 @pytest.mark.parametrize("bad,code", [
-    (dict(T=-1), L.MOE_ERR_INVALID_ARG), (dict(NA=0), L.MOE_ERR_INVALID_ARG),
+    (dict(T=-1), L.MOE_ERR_INVALID_ARG), (dict(T=(1 << 30) + 1), L.MOE_ERR_UNSUPPORTED),
+    (dict(NA=0), L.MOE_ERR_INVALID_ARG),
     (dict(NA=1025), L.MOE_ERR_INVALID_ARG), (dict(r=0), L.MOE_ERR_INVALID_ARG),
     (dict(r=136), L.MOE_ERR_INVALID_ARG), (dict(r=12), L.MOE_ERR_MISALIGNED),
     (dict(H=0), L.MOE_ERR_INVALID_ARG), (dict(H=100), L.MOE_ERR_MISALIGNED),

@@ -295,6 +295,16 @@ def test_offsets_beyond_32_bits():
     assert all(torch.equal(p, q) for p, q in zip(ref, op.backward(c["dout"], x, c["ids"])))
 
 
+@pytest.mark.parametrize("T,NA,ids", [(4096, 2, "runs"), (4097, 1024, "mixed"), (20011, 200, "mixed"),
+                                      (70001, 3, "runs")])
+def test_long_batches(T, NA, ids):
+    """Token lists that each of the grouping's warps walks in several rounds."""
+    c = make(T, NA, 8, 64, 64, torch.float32, ids)
+    op = P.LowRankAdapters(c["a"], c["b"], c["scale"])
+    check_forward(c, op.forward(c["x"], c["ids"], c["base"]), torch.float32)
+    check_backward(c, *op.backward(c["dout"], c["x"], c["ids"], c["dx_base"]), torch.float32)
+
+
 @pytest.mark.parametrize("T", [3, 200, 1500])
 def test_forward_over_its_input(T):
     """x += the adapters' products of x: a tile's rows are read before any of
