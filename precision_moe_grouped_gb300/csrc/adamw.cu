@@ -24,7 +24,9 @@
 //
 // Bound by HBM: 26 or 28 bytes an element (32-bit moments, float or bf16
 // gradients, 2 more for a bf16 copy of the parameter), 14.06 or 16.06 with
-// 8-bit moments.
+// 8-bit moments.  200 M elements with bf16 gradients and copies: 787 us (7.1
+// TB/s, a little above a plain copy) with 32-bit moments, 543 us (5.9 TB/s, 0.83
+// of the issue slots) with 8-bit ones.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 

@@ -10,10 +10,14 @@
 // appears only inside the sum over experts, so a token contributes one number,
 // d_t = sum_e f_se p_te, which its gradient needs anyway: no [E] sums of
 // probabilities are kept, and the gradient does not wait for the loss.  What
-// it does wait for are the counts, hence two kernels.
+// it does wait for are the counts, hence two kernels, or one cluster's barrier
+// where a small batch is one kernel.
 //
 // Bound by HBM: logits are read once and the gradient is written once, 8 E
-// bytes a token; the counts read 4 k bytes a token.  (A call's last kernel lets
+// bytes a token; the counts read 4 k bytes a token.  65,536 tokens of 256
+// experts, top-8, with the gate's gradient: 31.5 us, 4.5 TB/s of those bytes
+// (the copy's rate would be 21 us), with 0.65 of the issue slots taken by the
+// softmax's arithmetic.  (A call's last kernel lets
 // no successor start early: others may read its results ahead of a grid wait.)
 #include <cfloat>
 
@@ -39,22 +43,24 @@ __device__ __forceinline__ int2 seq_range(const int32_t* seq, int s, int T) {
 // its valid tokens.  Integer sums, so their order does not matter.  Each CTA
 // takes a contiguous eighth of the tokens and then writes an eighth of the
 // experts: counts, and f without the factors that main applies.
+template <bool PARTS>
 __global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThreads)
     balance_count_kernel(const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
                          const int32_t* __restrict__ seq, int T, int E, int k,
-                         int32_t* __restrict__ counts, int32_t* __restrict__ n_valid,
+                         int parts, int32_t* __restrict__ counts, int32_t* __restrict__ n_valid,
                          uint32_t* __restrict__ ticket) {
   extern __shared__ int32_t hist[];   // [E] slots by expert, [E]: valid tokens
   griddep_wait();
   griddep_launch_dependents();
-  const int s = blockIdx.x / kCountCtas;
+  const int unit = blockIdx.x / kCountCtas, s = PARTS ? 0 : unit;
   const int rank = static_cast<int>(cluster_rank());
   for (int i = threadIdx.x; i <= E; i += kCountThreads) hist[i] = 0;
   __syncthreads();
   const int2 r = seq_range(seq, s, T);
   const int64_t n = r.y - r.x;
-  const int a = r.x + static_cast<int>(n * rank / kCountCtas);
-  const int b = r.x + static_cast<int>(n * (rank + 1) / kCountCtas);
+  const int nth = PARTS ? static_cast<int>(blockIdx.x) : rank, of = PARTS ? parts * kCountCtas : kCountCtas;
+  const int a = r.x + static_cast<int>(n * nth / of);
+  const int b = r.x + static_cast<int>(n * (nth + 1) / of);
   // a token a thread; its slots in groups of 8 loads that do not wait for one
   // another or for the mask
   int valid = 0;
@@ -78,13 +84,13 @@ __global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThrea
   for (int e = e0 + threadIdx.x; e < e1; e += kCountThreads) {
     int sum = 0;
     for (int c = 0; c < kCountCtas; ++c) sum += cluster_load(hist + e, c);
-    counts[static_cast<int64_t>(s) * E + e] = sum;
+    counts[static_cast<int64_t>(unit) * E + e] = sum;
   }
   if (rank == 0 && threadIdx.x == 0) {
     int sum = 0;
     for (int c = 0; c < kCountCtas; ++c) sum += cluster_load(hist + E, c);
-    n_valid[s] = sum;
-    if (s == 0) *ticket = 0;
+    n_valid[unit] = sum;
+    if (unit == 0) *ticket = 0;
   }
   cluster_sync();   // no CTA leaves while another reads its shared memory
 }
@@ -105,6 +111,13 @@ struct BalanceArgs {
   int32_t T, E, k, S;
   float coef;
   int32_t vec;           // logits and dlogits allow 16-byte accesses
+};
+
+// One sequence's counts in parts.
+struct Parts {
+  int32_t n;
+  const int32_t* counts;   // [n, E]
+  int32_t* sums;           // [E]
 };
 
 template <int G>
@@ -294,13 +307,21 @@ __device__ __forceinline__ float block_sum(float v, float* sums) {
 constexpr int main_ctas(int V) { return V <= 4 ? 4 : 2; }
 
 // A CTA takes a contiguous range of tokens, its groups of lanes in turn.
-template <int G, int V>
-__global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kernel(const BalanceArgs a) {
+// PARTS: one sequence, whose counts come in parts.  An own instantiation, with
+// a parameter of its own, leaves the others the registers they had (65,536
+// tokens of 256 experts in 24 sequences: 31.5 us; 33.8 with a condition).
+template <int G, int V, bool PARTS>
+__global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kernel(const BalanceArgs a, const Parts p) {
   constexpr int kGroups = Rows<G, V>::kGroups;
   __shared__ float sums[kMainThreads / 32];
   __shared__ __align__(16) float gate_s[kMainThreads * 4 * V];
   __shared__ int live_s;
   __shared__ bool last;
+  int* whole = nullptr;   // the parts' sums
+  if constexpr (PARTS) {
+    __shared__ int sums_of_parts[1024];
+    whole = sums_of_parts;
+  }
   const Rows<G, V> rows(a, gate_s);
   if (threadIdx.x == 0) live_s = 0;
   __syncthreads();
@@ -316,9 +337,21 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
   bool on = is_on(t), on_next = is_on(t + kGroups);
   // so far only the call's inputs; now the counts
   griddep_wait();
-  int live = 0;
-  for (int i = threadIdx.x; i < a.S; i += kMainThreads) live += a.n_valid[i] > 0;
-  if (live) atomicAdd(&live_s, live);
+  [[maybe_unused]] int n_whole = 0;
+  if constexpr (PARTS) {
+    for (int q = 0; q < p.n; ++q) n_whole += a.n_valid[q];
+    for (int e = threadIdx.x; e < a.E; e += kMainThreads) {
+      int sum = 0;
+#pragma unroll 8
+      for (int q = 0; q < p.n; ++q) sum += p.counts[q * a.E + e];
+      whole[e] = sum;
+      if (blockIdx.x == 0) p.sums[e] = sum;
+    }
+  } else {
+    int live = 0;
+    for (int i = threadIdx.x; i < a.S; i += kMainThreads) live += a.n_valid[i] > 0;
+    if (live) atomicAdd(&live_s, live);
+  }
   __syncthreads();
   const float share = a.coef / static_cast<float>(max(live_s, 1));
   // every lane of a warp runs the same number of rounds (the shuffles)
@@ -342,9 +375,10 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
       const bool inside = t >= r.x && t < r.y;   // not: a token of no sequence
       s = inside ? lo : -1;
       s_end = inside ? r.y : static_cast<int>(t) + 1;
-      const int n = inside ? a.n_valid[s] : 0;
+      const int n = !inside ? 0 : PARTS ? n_whole : a.n_valid[s];
       c = n > 0 ? share / static_cast<float>(n) : 0.f;
-      rows.factors(a.counts + static_cast<int64_t>(lo) * a.E, n, f);
+      if constexpr (PARTS) rows.factors(whole, n, f);
+      else rows.factors(a.counts + static_cast<int64_t>(lo) * a.E, n, f);
     }
     mine += rows.take(t, in, masked_in && s >= 0, z, slot, f, c);
   }
@@ -369,7 +403,8 @@ __global__ void __launch_bounds__(kMainThreads, main_ctas(V)) balance_main_kerne
 // A small batch of one sequence, whole, by one cluster: its CTAs count an
 // eighth of the tokens each, add the counts up over distributed shared
 // memory, and take their tokens' rows.  One launch and no workspace, for
-// batches whose time is that of a launch.
+// batches whose time is that of a launch (201 tokens of 8 experts: 4.1 us
+// against 6.1 in two kernels).
 constexpr int kSmallRounds = 2;   // tokens a group of lanes may have to take
 __host__ __device__ constexpr int small_tokens(int lanes) {
   return kCountCtas * kSmallRounds * (kMainThreads / lanes);
@@ -446,14 +481,26 @@ __global__ void balance_empty_kernel(float* loss, int32_t* counts, int64_t n) {
 
 constexpr int kMaxCtas = 152 * 8;   // CTAs the partial sums have room for
 
+// Clusters that count a batch of one sequence: one for each round of their
+// threads (32,768 tokens of 64 experts, top-8: 13 us against 16 with one, at
+// 131,072 of 256 53 against 73; more than eight gain nothing).  Several
+// sequences have as many clusters already.
+int count_parts(const moe_balance_shape* s) {
+  const int parts = s->num_sequences > 1 ? 1 : s->num_tokens / (kCountCtas * kCountThreads);
+  return parts < 1 ? 1 : parts < 8 ? parts : 8;
+}
+
 struct BalanceWs {
-  size_t n_valid, partial, ticket, total;
+  int32_t parts;
+  size_t n_valid, part_counts, partial, ticket, total;
 };
 
 BalanceWs balance_ws(const moe_balance_shape* s) {
   BalanceWs w;
+  w.parts = count_parts(s);
   w.n_valid = 0;
-  w.partial = ws_up(static_cast<size_t>(s->num_sequences) * 4);
+  w.part_counts = ws_up(static_cast<size_t>(s->num_sequences) * w.parts * 4);
+  w.partial = w.part_counts + (w.parts > 1 ? ws_up(static_cast<size_t>(w.parts) * s->num_experts * 4) : 0);
   w.ticket = w.partial + ws_up(kMaxCtas * 4);
   w.total = w.ticket + kWsAlign;
   return w;
@@ -494,31 +541,31 @@ bool is_small(const moe_balance_shape* s) {
 }
 
 template <int G, int V>
-cudaError_t launch_rows(const BalanceArgs& a, int32_t* counts, bool small, int sms, cudaStream_t st) {
+cudaError_t launch_rows(const BalanceArgs& a, const Parts& p, bool small, int sms, cudaStream_t st) {
   if (small)
-    return launch_pdl(balance_small_kernel<G, V>, dim3(kCountCtas), dim3(kMainThreads), 0, st, a, counts);
+    return launch_pdl(balance_small_kernel<G, V>, dim3(kCountCtas), dim3(kMainThreads), 0, st, a, p.sums);
   const int per_round = kMainThreads / G;
   const int64_t rounds = (static_cast<int64_t>(a.T) + per_round - 1) / per_round;
   int ctas = sms * main_ctas(V);   // one wave
   if (ctas > kMaxCtas) ctas = kMaxCtas;
-  return launch_pdl(balance_main_kernel<G, V>, dim3(static_cast<unsigned>(rounds < ctas ? rounds : ctas)),
-                    dim3(kMainThreads), 0, st, a);
+  return launch_pdl(p.n > 1 ? balance_main_kernel<G, V, true> : balance_main_kernel<G, V, false>,
+                    dim3(static_cast<unsigned>(rounds < ctas ? rounds : ctas)), dim3(kMainThreads), 0, st, a, p);
 }
 
-cudaError_t launch_by_experts(const BalanceArgs& a, int32_t* counts, bool small, int sms, cudaStream_t st) {
+cudaError_t launch_by_experts(const BalanceArgs& a, const Parts& parts, bool small, int sms, cudaStream_t st) {
   const Split p = split_of(a.E);
   switch (p.lanes) {
-    case 2: return launch_rows<2, 1>(a, counts, small, sms, st);
-    case 4: return launch_rows<4, 1>(a, counts, small, sms, st);
-    case 8: return launch_rows<8, 1>(a, counts, small, sms, st);
+    case 2: return launch_rows<2, 1>(a, parts, small, sms, st);
+    case 4: return launch_rows<4, 1>(a, parts, small, sms, st);
+    case 8: return launch_rows<8, 1>(a, parts, small, sms, st);
     case 16:
-      return p.v == 1   ? launch_rows<16, 1>(a, counts, small, sms, st)
-             : p.v == 2 ? launch_rows<16, 2>(a, counts, small, sms, st)
-                        : launch_rows<16, 4>(a, counts, small, sms, st);
+      return p.v == 1   ? launch_rows<16, 1>(a, parts, small, sms, st)
+             : p.v == 2 ? launch_rows<16, 2>(a, parts, small, sms, st)
+                        : launch_rows<16, 4>(a, parts, small, sms, st);
     default:
-      return p.v == 3   ? launch_rows<32, 3>(a, counts, small, sms, st)
-             : p.v == 4 ? launch_rows<32, 4>(a, counts, small, sms, st)
-                        : launch_rows<32, 8>(a, counts, small, sms, st);
+      return p.v == 3   ? launch_rows<32, 3>(a, parts, small, sms, st)
+             : p.v == 4 ? launch_rows<32, 4>(a, parts, small, sms, st)
+                        : launch_rows<32, 8>(a, parts, small, sms, st);
   }
 }
 
@@ -568,12 +615,14 @@ extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float*
   }
   uint8_t* base = static_cast<uint8_t*>(workspace);
   int32_t* n_valid = small ? nullptr : reinterpret_cast<int32_t*>(base + w.n_valid);
+  int32_t* part_counts = small ? nullptr : reinterpret_cast<int32_t*>(base + w.part_counts);
   uint32_t* ticket = small ? nullptr : reinterpret_cast<uint32_t*>(base + w.ticket);
   cudaError_t e = cudaSuccess;
   if (!small)
-    e = launch_pdl(balance_count_kernel, dim3(static_cast<unsigned>(S) * kCountCtas),
+    e = launch_pdl(w.parts > 1 ? balance_count_kernel<true> : balance_count_kernel<false>,
+                   dim3(static_cast<unsigned>(S) * w.parts * kCountCtas),
                    dim3(kCountThreads), (E + 1) * sizeof(int32_t), st, ids, token_mask, seq_offsets, T,
-                   E, shape->top_k, counts, n_valid, ticket);
+                   E, shape->top_k, w.parts, w.parts > 1 ? part_counts : counts, n_valid, ticket);
   if (e != cudaSuccess) return entry_launched(e);
   BalanceArgs a;
   a.logits = logits;
@@ -591,5 +640,5 @@ extern "C" int32_t moe_balance_loss(const moe_balance_shape* shape, const float*
   a.T = T, a.E = E, a.k = shape->top_k, a.S = S;
   a.coef = shape->coef;
   a.vec = E % 4 == 0 && ptr_aligned(logits, 16) && ptr_aligned(dlogits, 16);
-  return entry_launched(launch_by_experts(a, counts, small, sms, st));
+  return entry_launched(launch_by_experts(a, {w.parts, part_counts, counts}, small, sms, st));
 }

@@ -133,6 +133,15 @@ def test_long_batches():
     check(make(30000, 8, 2))
 
 
+@pytest.mark.parametrize("T,E,k", [(4096, 40, 4), (8195, 384, 6), (20011, 7, 3), (70001, 64, 8)])
+def test_one_long_sequence(T, E, k):
+    """One sequence counted by several clusters: whole, masked, a part of the
+    batch, and none of it."""
+    check(make(T, E, k))
+    check(make(T, E, k, masked=True, gates=True, drop=True, seqs=[11, T - 100]))
+    check(make(T, E, k, gates=True, seqs=[5, 5]))
+
+
 def test_masked_infinite_and_nan():
     c = make(50, 64, 4, masked=True)
     c["mask"][:10] = False
