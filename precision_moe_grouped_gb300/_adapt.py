@@ -168,7 +168,9 @@ class LowRankAdapters:
         kind, shape = self._kind(dtype, "base"), (T, self.out_features)
         ld_base = 0 if base is None else _check_rows(base, "base", dtype, shape, dev)
         if out is None:
-            out, ld_out = torch.empty(shape, dtype=dtype, device=self.device), self.out_features
+            ld_out = self.out_features
+            out = (torch.empty_like(base) if ld_base == ld_out else   # (quicker)
+                   torch.empty(shape, dtype=dtype, device=self.device))
         else:
             ld_out = _check_rows(out, "out", dtype, shape, dev)
         s, n = self._call(T, kind, 0)

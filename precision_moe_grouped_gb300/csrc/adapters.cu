@@ -434,8 +434,8 @@ __device__ __forceinline__ int2 chunk_range(int K, int chunk, int part, int part
 
 // Tiles of 64 tokens: the CTA's chunks of 64 elements of K come into shared
 // memory by asynchronous copies, STAGES deep (gathered rows of src, and the
-// pool's rows), and feed ldmatrix.  Bound by the copies' latency with three
-// CTAs of stages an SM (8192 tokens of 7168, rank 16: 21 us cold, 95 MB at 4.5
+// pool's rows), and feed ldmatrix.  Bound by the copies' latency with two
+// CTAs' stages an SM (8192 tokens of 7168, rank 16: 22 us cold, 95 MB at 4.2
 // TB/s).  Tokens are MMA-M, 16 to a warp; the two
 // warps that share 16 tokens split the ranks, or at RT = 1 the chunk.
 //   !ROWS (x):    pool [r, K], its rows are the fragments' columns
@@ -450,7 +450,9 @@ struct Shrink {
   static constexpr int PROW = ROWS ? 2 * RP : 2 * KC;       // and of the pool
   static constexpr int SRC = kTile * SROW, POOL = (ROWS ? KC : RP) * PROW;
   static constexpr int STAGE = SRC + POOL;
-  static constexpr int STAGES = STAGE <= 24 * 1024 ? 3 : 2;
+  // as many as leave room for a second CTA on the SM
+  static constexpr int FIT = 110 * 1024 / STAGE;
+  static constexpr int STAGES = FIT > 4 ? 4 : FIT < 2 ? 2 : FIT;
   static constexpr size_t red = sizeof(float) * WK * kTile * red_stride(RP);
   static constexpr size_t smem = STAGES * STAGE > red ? STAGES * STAGE : red;
 };
@@ -569,7 +571,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& til
 
 // Cluster of S CTAs per tile, sharing out the chunks of K.
 template <int RT>
-__global__ void __launch_bounds__(kThreads) shrink_x_kernel(const ShrinkArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) shrink_x_kernel(const ShrinkArgs a) {
   extern __shared__ __align__(128) uint8_t sm[];
   griddep_wait();
   griddep_launch_dependents();
@@ -581,7 +583,7 @@ __global__ void __launch_bounds__(kThreads) shrink_x_kernel(const ShrinkArgs a) 
 // Both of the backward's, in one launch: the first `d_units` clusters take
 // dout, the others x.
 template <int RT, bool F32>
-__global__ void __launch_bounds__(kThreads) shrink_both_kernel(const ShrinkArgs d, const ShrinkArgs x,
+__global__ void __launch_bounds__(kThreads, 2) shrink_both_kernel(const ShrinkArgs d, const ShrinkArgs x,
                                                                int d_units) {
   extern __shared__ __align__(128) uint8_t sm[];
   griddep_wait();
@@ -1295,12 +1297,21 @@ cudaError_t launch_group(const int32_t* ids, int T, int NA, const Groups& g, cud
                         ids, T, NA, g);
 }
 
-// CTAs that share a tile: powers of two up to 8, while the clusters fill no
-// more than `resident` CTAs an SM and every CTA keeps `least` elements of K.
-int shrink_cluster(int64_t units, int K, int resident, int least, int sms) {
+// CTAs that share a tile of `units` expected: powers of two up to 8, while all
+// of them are resident, two an SM (a tenth more for the first split, the most
+// worth), and every CTA keeps 256 elements of K.
+// (Two with four stages each and one wave: 4096 tokens, rank 16, 7168 x 7168 in
+// 45 us, 50 with three of three stages and more than a wave; rank 64: 64 and 76.
+// Only tiles of few tokens want more CTAs: 3000 tokens of 200 adapters 63 and 59.)
+int shrink_cluster(int64_t units, int K, int sms) {
   int c = 1;
-  while (c < 8 && 2 * units * c <= static_cast<int64_t>(resident) * sms && K >= 2 * c * least) c *= 2;
+  while (c < 8 && units * c <= sms + (c == 1 ? sms / 10 : 0) && K >= 2 * c * 256) c *= 2;
   return c;
+}
+// About as many tiles as T tokens of NA adapters make.
+int64_t likely_tiles(int64_t T, int NA) {
+  const int64_t filled = T / kTile + (NA + 1) / 2, one_each = T < NA ? T : NA;
+  return filled > one_each ? filled : one_each;
 }
 
 // Splits the features of expand's tiles into WAVES times the CTAs that an SM
@@ -1337,7 +1348,7 @@ cudaError_t launch_forward(const ShrinkArgs& sa, ExpandArgs e, int sms, cudaStre
   static DeviceOnce once_s, once_e;
   cudaError_t err = set_smem_limit_once(shrink_x_kernel<RT>, S::smem, once_s);
   if (err != cudaSuccess) return err;
-  const int c = shrink_cluster(e.units, sa.K, 4, 256, sms);
+  const int c = shrink_cluster(likely_tiles(sa.tiles.T, sa.tiles.NA), sa.K, sms);
   err = launch_cluster(shrink_x_kernel<RT>, dim3(static_cast<unsigned>(e.units) * c), c, S::smem, st, kThreads,
                        sa);
   if (err != cudaSuccess) return err;
@@ -1380,7 +1391,11 @@ cudaError_t launch_backward(const Backward& b, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const int64_t both = b.units * (b.want_x ? 2 : 1);
   // (the same split whichever outputs are wanted: their sums do not depend on it)
-  int c = shrink_cluster(2 * b.units, b.x.K > b.d.K ? b.x.K : b.d.K, 4, 256, b.sms);
+  // The shorter product's CTAs count as their share of the work, but for an
+  // eighth at least: what one costs beside its chunks.
+  const int longer = b.x.K > b.d.K ? b.x.K : b.d.K, shorter = b.x.K + b.d.K - longer;
+  const int64_t tiles = likely_tiles(b.T, b.NA);
+  int c = shrink_cluster(tiles + tiles * (8 * shorter > longer ? shorter : longer / 8) / longer, longer, b.sms);
   e = launch_cluster(shrink_both_kernel<RT, F32>, dim3(static_cast<unsigned>(both * c)), c, smem_s, st,
                      kThreads, b.d, b.x, static_cast<int>(b.units));
   if (e != cudaSuccess) return e;
