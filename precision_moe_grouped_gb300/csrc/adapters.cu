@@ -432,7 +432,7 @@ __device__ __forceinline__ int2 chunk_range(int K, int chunk, int part, int part
   return make_int2(static_cast<int>(n * part / parts), static_cast<int>(n * (part + 1) / parts));
 }
 
-// Tiles of 64 tokens: the CTA's chunks of 64 elements of K come into shared
+// Tiles of 64 tokens: the CTA's chunks of 128 elements of K (float: 64) come into shared
 // memory by asynchronous copies, STAGES deep (gathered rows of src, and the
 // pool's rows), and feed ldmatrix.  Bound by the copies' latency with two
 // CTAs' stages an SM (8192 tokens of 7168, rank 16: 22 us cold, 95 MB at 4.2
@@ -630,7 +630,7 @@ struct Expand {
   static constexpr int FB = SMALL && RT <= 2 ? 256 : 128;
   // CTAs that share a tile's tokens: two where the base outweighs the pool's
   // rows, which each of them stages (8192 tokens, rank 16, 7168 features:
-  // 73.1 us for the forward against 76.2)
+  // 73.3 us for the forward against 75.7)
   static constexpr int SUB = SMALL || ROWS || RT > 2 ? 1 : 2;
   static constexpr int NTOK = SMALL ? kSmallTile : kTile / SUB;
   static constexpr int WT = NTOK / 16, WF = kWarps / WT;      // warps along tokens, features
