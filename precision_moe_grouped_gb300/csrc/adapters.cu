@@ -1209,9 +1209,10 @@ AdapterWs adapter_ws(const moe_adapter_shape* s, bool backward) {
   const int64_t T = s->num_tokens, NA = s->num_adapters;
   AdapterWs w = {};
   // One kernel where it is no slower than three (7168 x 7168, rank 16, 8
-  // adapters: 7.7 us against 12.4 at 64 tokens, 10.2 / 13.3 at 256, 16.8 / 19.0 at
-  // 1021; 64 adapters: 21.0 / 28.3).  At rank 128 its tiles of 16 tokens read the
-  // pools too often (2048 x 2048: 10.1 / 14.2 at 64 tokens, 20.2 / 14.6 at 256).
+  // adapters: 8.3 us against 12.9 at 128 tokens, 9.9 / 13.8 at 256, 17.8 / 20.3 at
+  // 1021; 64 adapters: 24.2 / 28.6.  Rank 64 at 1021: 32.8 / 31.3, 46.5 / 56.0).  At
+  // rank 128 its tiles of 16 tokens read the pools too often (2048 x 2048: 10.1 /
+  // 14.2 at 64 tokens, 20.2 / 14.6 at 256).
   w.small = !backward && T <= (s->rank <= 64 ? kSmallTokens : 64);
   // an adapter with n tokens has at most n / 16 + 1 tiles
   const int64_t small_units = T / kSmallTile + NA + 1;
