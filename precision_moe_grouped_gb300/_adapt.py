@@ -235,7 +235,8 @@ class LowRankAdapters:
 class BalanceLoss:
     """The router's load-balance loss over `num_experts` experts and top-k
     routing, per-expert counts and the gradient of the logits (the formulas:
-    moe_balance_loss in include/moe.h)."""
+    moe_balance_loss in include/moe.h).  The attributes are read at every call, so
+    that coef may follow a schedule."""
 
     def __init__(self, num_experts: int, top_k: int, coef: float = 1.0):
         _bind_torch()
@@ -258,7 +259,7 @@ class BalanceLoss:
         padding), seq_offsets int32 [S + 1] (None: the whole batch as one
         sequence), weights and dweights float32 [T, k] (both or neither: adds
         the gradient of the routing weights)."""
-        dev, E, k = _device(), self.num_experts, self.top_k
+        dev, E, k, coef = _device(), self.num_experts, self.top_k, float(self.coef)
         T = _rows(logits, "logits")
         _check_flat(logits, "logits", torch.float32, (T, E), dev)
         _check_flat(ids, "ids", torch.int32, (T, k), dev)
@@ -277,12 +278,13 @@ class BalanceLoss:
         if weights is not None:
             _check_flat(weights, "weights", torch.float32, (T, k), dev)
             _check_flat(dweights, "dweights", torch.float32, (T, k), dev)
-        got = self._calls.get((T, S))
+        key = (T, E, k, S, coef)   # all that the shape holds
+        got = self._calls.get(key)
         if got is None:
-            s = BalanceShape(T, E, k, S, self.coef)
+            s = BalanceShape(*key)
             if len(self._calls) > 4096:
                 self._calls.clear()
-            got = self._calls[(T, S)] = (s, self._size(s))
+            got = self._calls[key] = (s, self._size(s))
         s, n = got
         ws = None if n <= 256 else _scratch(n, logits)   # small batches use none
         loss = torch.empty(1, dtype=torch.float32, device=logits.device)
