@@ -47,6 +47,7 @@ class FusedMoE:
         prepare_weights(self.shape(0), w1, w1_sf, w2, w2_sf, self.w1_p, self.w1_sf_p, self.w2_p,
                         self.w2_sf_p, mode)
         self._ws = None
+        self._routed = None   # tokens of the call whose routing the workspace holds
         self._steps_ws = None
 
     def shape(self, T: int) -> MoeShape:
@@ -57,6 +58,7 @@ class FusedMoE:
         need = workspace_size(self.shape(T), self.mode)
         if self._ws is None or self._ws.numel() < need:
             self._ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+            self._routed = None
         return self._ws
 
     def __call__(self, x, logits, out=None, opts: MoeOptions | None = None):
@@ -65,16 +67,24 @@ class FusedMoE:
         if out is None:
             out = torch.empty((T, self.H), dtype=torch.bfloat16, device=self.device)
         ws = self.workspace(T)
+        self._routed = None
         forward(self.shape(T), x, logits, self.w1_p, self.w1_sf_p, self.w2_p, self.w2_sf_p, out,
                 ws, self.mode, opts)
+        self._routed = T
         return out
 
     def routing(self, T: int):
-        """(ids int32 [T, k], weights float32 [T, k]) of the last forward of T
-        tokens: views of the workspace, valid until the next forward."""
+        """(ids int32 [T, k], weights float32 [T, k]) of this object's last call,
+        which had T tokens: views of the workspace, valid until the next call.
+        (Calls captured into a CUDA graph: take the views at the capture, a replay
+        fills them.)"""
         import torch
+        if self._routed != T:
+            _lib._bad(f"no routing of {T} tokens: " + (
+                "nothing was forwarded in this workspace" if self._routed is None else
+                f"the last call had {self._routed}"))
         lay, n = workspace_layout(self.shape(T), self.mode), T * self.top_k * 4
-        ws = self.workspace(T)
+        ws = self._ws
         ids = ws[lay.ids:lay.ids + n].view(torch.int32).view(T, self.top_k)
         return ids, ws[lay.weights:lay.weights + n].view(torch.float32).view(T, self.top_k)
 

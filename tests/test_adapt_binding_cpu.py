@@ -63,3 +63,40 @@ def test_balance_coefficient_is_read_at_every_call(lib):
     op.coef = float("nan")
     with pytest.raises(P.MoeError, match="coef"):
         op(z, ids)
+
+
+def test_routing_is_of_the_last_call(monkeypatch, lib):
+    """Views of a workspace that no call of so many tokens has filled are
+    refused, a replaced workspace's among them."""
+    monkeypatch.setattr(P, "prepare_weights", lambda *a, **k: None)
+    monkeypatch.setattr(P, "forward", lambda *a, **k: None)
+    E, H, I = 8, 256, 128
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)                # noqa: E731
+    moe = P.FusedMoE(u8(E, 2 * I, H // 2), u8(E, 2 * I, H // 32), u8(E, H, I // 2), u8(E, H, I // 32), 2)
+    x, z = torch.zeros(2000, H, dtype=torch.bfloat16), torch.zeros(2000, E)
+
+    def refused(T):
+        with pytest.raises(P.MoeError, match="no routing"):
+            moe.routing(T)
+
+    refused(5)                       # nothing forwarded yet
+    moe(x[:100], z[:100])
+    ids, w = moe.routing(100)
+    assert ids.shape == w.shape == (100, 2)
+    for T in (5, 101, 2000):         # smaller, and larger than the workspace
+        refused(T)
+    assert moe.routing(100)[0].data_ptr() == ids.data_ptr()    # the refusals left it as it was
+    moe(x[:5], z[:5])
+    moe.routing(5)
+    refused(100)                     # overwritten since
+    moe.workspace(2000)              # grows: a new one
+    refused(5)
+    moe(x, z)
+    assert moe.routing(2000)[0].shape == (2000, 2)
+
+    def fails(*a, **k):
+        raise P.MoeError(L.MOE_ERR_INVALID_ARG, "x")
+    monkeypatch.setattr(P, "forward", fails)
+    with pytest.raises(P.MoeError):
+        moe(x[:7], z[:7])
+    refused(7)
