@@ -105,35 +105,53 @@ class LowRankAdapters:
 
     a bf16 [NA, r, H], b bf16 [NA, N, r], scale float32 [NA] or None for 1;
     r, H and N multiples of 8, r <= 128, NA <= 1024.  The pools are read at
-    every call, so that an update in place takes effect with the next one."""
+    every call, so that an update in place takes effect with the next one.  So
+    does another tensor in their place, by assignment here or to a tensor's
+    .data: a call that finds other memory checks it, and refuses what is not as
+    at the start (a module moved to the host or to another type)."""
 
     def __init__(self, a, b, scale=None):
         _bind_torch()
         dev = _device()
-        _check_tensor(a, "a", cuda=True, dtype=torch.bfloat16, device=dev)
-        if a.dim() != 3:
-            _bad(f"a must be [adapters, rank, in_features], got {tuple(a.shape)}")
-        self.num_adapters, self.rank, self.in_features = a.shape
+        if a is None or a.dim() != 3:
+            _bad("a must be [adapters, rank, in_features]")
+        NA, r, H = self.num_adapters, self.rank, self.in_features = tuple(a.shape)
         if b is None or b.dim() != 3:
             _bad("b must be [adapters, out_features, rank]")
-        self.out_features = b.shape[1]
-        _check_tensor(b, "b", cuda=True, dtype=torch.bfloat16, device=dev,
-                      shape=(self.num_adapters, self.out_features, self.rank))
-        if scale is not None:
-            _check_tensor(scale, "scale", cuda=True, dtype=torch.float32, device=dev,
-                          shape=(self.num_adapters,))
+        N = self.out_features = b.shape[1]
+        self._dims = NA, r, H, N
+        self._shapes = (NA, r, H), (NA, N, r), (NA,)
         self.a, self.b, self.scale, self.device, self._dev = a, b, scale, a.device, dev
+        self._at = None
+        self._addresses()
         self._lib = load()
         self._sizes = {}
         for kind in (MOE_DTYPE_BF16, MOE_DTYPE_F32):   # rejects unsupported sizes here
             self._call(0, kind, 0)
 
+    def _addresses(self) -> tuple:
+        """Of a, b and scale, checked where they are not the last call's.  That
+        one's memory is held (detached), so that it cannot have become another
+        tensor's in the meantime."""
+        a, b, scale = self.a, self.b, self.scale
+        if a is None or b is None:
+            _bad("a or b is None")
+        at = a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr()
+        if at != self._at:
+            shapes = self._shapes
+            _check_flat(a, "a", torch.bfloat16, shapes[0], self._dev)
+            _check_flat(b, "b", torch.bfloat16, shapes[1], self._dev)
+            if scale is not None:
+                _check_flat(scale, "scale", torch.float32, shapes[2], self._dev)
+            self._held = [t.detach() for t in (a, b, scale) if t is not None]
+            self._at = at
+        return at
+
     def _call(self, T: int, kind: int, backward: int):
         """(shape, workspace bytes) of a call with T tokens."""
         got = self._sizes.get((T, kind, backward))
         if got is None:
-            s = AdapterShape(T, self.num_adapters, self.rank, self.in_features, self.out_features,
-                             kind)
+            s = AdapterShape(T, *self._dims, kind)
             n = self._lib.moe_adapter_workspace_size(s, backward)
             if n == 0:
                 raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, self._lib.moe_last_error().decode())
@@ -160,15 +178,16 @@ class LowRankAdapters:
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        T = _rows(x, "x")
-        ld_x = _check_rows(x, "x", torch.bfloat16, (T, self.in_features), dev)
+        at = self._addresses()
+        T, (_, _, H, N) = _rows(x, "x"), self._dims
+        ld_x = _check_rows(x, "x", torch.bfloat16, (T, H), dev)
         _check_flat(ids, "ids", torch.int32, (T,), dev)
         dtype = base.dtype if base is not None else out.dtype if out is not None else (
             out_dtype or torch.bfloat16)
-        kind, shape = self._kind(dtype, "base"), (T, self.out_features)
+        kind, shape = self._kind(dtype, "base"), (T, N)
         ld_base = 0 if base is None else _check_rows(base, "base", dtype, shape, dev)
         if out is None:
-            ld_out = self.out_features
+            ld_out = N
             out = (torch.empty_like(base) if ld_base == ld_out else   # (quicker)
                    torch.empty(shape, dtype=dtype, device=self.device))
         else:
@@ -176,9 +195,8 @@ class LowRankAdapters:
         s, n = self._call(T, kind, 0)
         ws = None if n <= 256 else _scratch(n, x)   # small batches use none
         rc = self._lib.moe_adapter_forward(
-            s, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(), self.b.data_ptr(),
-            _ptr(self.scale), _ptr(base), ld_base, out.data_ptr(), ld_out, _ptr(ws), n,
-            _raw_stream(dev))
+            s, x.data_ptr(), ld_x, ids.data_ptr(), *at, _ptr(base), ld_base, out.data_ptr(), ld_out,
+            _ptr(ws), n, _raw_stream(dev))
         if rc:
             check(rc)
         return out
@@ -194,11 +212,12 @@ class LowRankAdapters:
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        T = _rows(x, "x")
+        at = self._addresses()
+        T, (_, _, H, N) = _rows(x, "x"), self._dims
         if dout is None:
             _bad("dout is None")
-        kind, wide = self._kind(dout.dtype, "dout"), (T, self.in_features)
-        ld_dout = _check_rows(dout, "dout", dout.dtype, (T, self.out_features), dev)
+        kind, wide = self._kind(dout.dtype, "dout"), (T, H)
+        ld_dout = _check_rows(dout, "dout", dout.dtype, (T, N), dev)
         ld_x = _check_rows(x, "x", torch.bfloat16, wide, dev)
         _check_flat(ids, "ids", torch.int32, (T,), dev)
         ld_dx = ld_base = 0
@@ -213,20 +232,20 @@ class LowRankAdapters:
         if not need_weights:
             da = db = None
         else:
+            da_shape, db_shape, _ = self._shapes
             if da is None:
-                da = torch.empty(self.a.shape, dtype=torch.float32, device=self.device)
+                da = torch.empty(da_shape, dtype=torch.float32, device=self.device)
             else:
-                _check_flat(da, "da", torch.float32, self.a.shape, dev)
+                _check_flat(da, "da", torch.float32, da_shape, dev)
             if db is None:
-                db = torch.empty(self.b.shape, dtype=torch.float32, device=self.device)
+                db = torch.empty(db_shape, dtype=torch.float32, device=self.device)
             else:
-                _check_flat(db, "db", torch.float32, self.b.shape, dev)
+                _check_flat(db, "db", torch.float32, db_shape, dev)
         s, n = self._call(T, kind, 1)
         ws = _scratch(n, x)
         rc = self._lib.moe_adapter_backward(
-            s, dout.data_ptr(), ld_dout, x.data_ptr(), ld_x, ids.data_ptr(), self.a.data_ptr(),
-            self.b.data_ptr(), _ptr(self.scale), _ptr(dx_base), ld_base, _ptr(dx), ld_dx, _ptr(da),
-            _ptr(db), ws.data_ptr(), n, _raw_stream(dev))
+            s, dout.data_ptr(), ld_dout, x.data_ptr(), ld_x, ids.data_ptr(), *at, _ptr(dx_base),
+            ld_base, _ptr(dx), ld_dx, _ptr(da), _ptr(db), ws.data_ptr(), n, _raw_stream(dev))
         if rc:
             check(rc)
         return dx, da, db

@@ -100,3 +100,55 @@ def test_routing_is_of_the_last_call(monkeypatch, lib):
     with pytest.raises(P.MoeError):
         moe(x[:7], z[:7])
     refused(7)
+
+
+def adapters(NA=3, r=8, H=64, N=32):
+    a = on(torch.zeros(NA, r, H, dtype=torch.bfloat16))
+    b = on(torch.zeros(NA, N, r, dtype=torch.bfloat16))
+    return P.LowRankAdapters(a, b, on(torch.ones(NA)))
+
+
+def test_pools_are_checked_at_every_call(lib):
+    """A pool whose memory, type, size, layout or place changed after the
+    construction: the library sees the new one or the call is refused."""
+    x, ids = on(torch.zeros(4, 64, dtype=torch.bfloat16)), on(torch.zeros(4, dtype=torch.int32))
+    dout = on(torch.zeros(4, 32))
+    bf16 = torch.bfloat16
+
+    class Host(OnDevice):
+        is_cuda = property(lambda self: False)
+
+    changes = {
+        "a": [torch.zeros(3, 8, 32, dtype=bf16), torch.zeros(2, 8, 64, dtype=bf16), torch.zeros(3, 8, 64),
+              torch.zeros(3, 64, 8, dtype=bf16).transpose(1, 2), None],
+        "b": [torch.zeros(3, 32, 16, dtype=bf16), torch.zeros(3, 16, 8, dtype=bf16), torch.zeros(3, 32, 8), None],
+        "scale": [torch.zeros(2), torch.zeros(3, dtype=torch.float64), torch.zeros(6)[::2]],
+    }
+    for name, bad in changes.items():
+        bad.append(  # as its module moved to the host
+            getattr(adapters(), name).as_subclass(Host))
+        for t in bad:
+            op = adapters()
+            setattr(op, name, on(t) if t is not None and not isinstance(t, Host) else t)
+            for call in (lambda: op.forward(x, ids), lambda: op.backward(dout, x, ids)):
+                with pytest.raises(P.MoeError):
+                    call()
+                    pytest.fail(f"{name}: {t if t is None else (t.shape, t.dtype)}")
+    assert not lib.calls
+    # .data of the caller's own tensor
+    op = adapters()
+    op.forward(x, ids)
+    op.a.data = torch.zeros(1, dtype=bf16)
+    with pytest.raises(P.MoeError):
+        op.forward(x, ids)
+    assert len(lib.calls) == 1 and len(op._held) == 3      # the first call's memory is held
+    lib.calls.clear()
+    # good ones are followed, and the sizes of the construction stay
+    op = adapters()
+    op.a, op.b, op.scale = adapters().a, adapters().b, None
+    op.rank = op.in_features = 8
+    op.forward(x, ids)
+    op.backward(dout, x, ids)
+    (_, f), (_, b) = lib.calls
+    assert f[4:7] == (op.a.data_ptr(), op.b.data_ptr(), None) and b[6:9] == f[4:7]
+    assert f[0].rank == b[0].rank == 8 and f[0].in_features == b[0].in_features == 64
