@@ -386,6 +386,7 @@ class AdamW:
         if kind not in (torch.float32, torch.bfloat16):
             _bad(f"grads must be float32 or bfloat16, got {kind}")
         dev = _device()
+        _same_device(dev, self._dev)
         at = [_check_numel(t, "grads", i, kind, p.numel(), dev)
               for i, (t, p) in enumerate(zip(grads, self.params))]
         self.grads = grads

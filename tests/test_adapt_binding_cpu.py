@@ -152,3 +152,27 @@ def test_pools_are_checked_at_every_call(lib):
     (_, f), (_, b) = lib.calls
     assert f[4:7] == (op.a.data_ptr(), op.b.data_ptr(), None) and b[6:9] == f[4:7]
     assert f[0].rank == b[0].rank == 8 and f[0].in_features == b[0].in_features == 64
+
+
+def adamw(n=2, **kw):
+    zeros = lambda: [on(torch.zeros(8 + i)) for i in range(n)]        # noqa: E731
+    return P.AdamW(zeros(), zeros(), state={"m": zeros(), "v": zeros()}, **kw)
+
+
+def test_gradients_of_another_device_are_refused(lib, monkeypatch):
+    """Bound while their device is current, they would reach a step on the
+    parameters' device."""
+    class OnOther(OnDevice):
+        def get_device(self):
+            return 1
+
+    opt = adamw(1)
+    monkeypatch.setattr(_adapt, "_device", lambda: 1)
+    for call in (lambda: opt.bind_grads([torch.zeros(8).as_subclass(OnOther)]),
+                 lambda: opt.step(grads=[torch.zeros(8).as_subclass(OnOther)]), opt.step):
+        with pytest.raises(P.MoeError, match="current device is cuda:1"):
+            call()
+    monkeypatch.setattr(_adapt, "_device", lambda: 0)
+    opt.step()
+    (_, (table, count, options, stream)), = lib.calls
+    assert count == 1 and table[0].grad == opt.grads[0].data_ptr() and opt.steps_done == 1
