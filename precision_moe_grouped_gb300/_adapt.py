@@ -327,9 +327,10 @@ class AdamW:
     moments; 8 keeps E4M3 codes in blocks of 256 with a float32 scale each
     (v holds the codes of the second moment's root).  `state`: {"m": [...],
     "v": [...]} and, with 8 bits, "m_scale" and "v_scale", to resume from; by
-    default it starts at zero.  The tensors are bound here: after replacing a
-    parameter's or a gradient's memory, build a new AdamW (state=old.state) or
-    pass the new gradients to step()."""
+    default it starts at zero.  The tensors are bound and held here (params,
+    grads, copies and state name them and cannot be assigned): after replacing
+    a parameter's or a gradient's memory, build a new AdamW (state=old.state)
+    or pass the new gradients to step()."""
 
     def __init__(self, params, grads, copies=None, state_bits: int = 32, state=None,
                  lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -339,57 +340,73 @@ class AdamW:
             _bad(f"state_bits must be 8 or 32, got {state_bits}")
         dev = self._dev = _device()
         # detached: keeps the bound memory alive whatever becomes of the originals
-        self.params = _detached(params, "params")
+        bound = self._params = tuple(_detached(params, "params"))
         self.state_bits, self.lr, self.betas, self.eps = state_bits, lr, betas, eps
         self.weight_decay, self.steps_done = weight_decay, steps_done
-        sizes = [p.numel() for p in self.params]
+        sizes = [p.numel() for p in bound]
         blocks = [-(-n // MOE_ADAMW_BLOCK) for n in sizes]
         if state is None:
             kind = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
             state = {k: [torch.zeros(n, dtype=torch.uint8 if state_bits == 8 else kind,
                                      device=p.device).view(kind)
-                         for n, p in zip(sizes, self.params)] for k in ("m", "v")}
+                         for n, p in zip(sizes, bound)] for k in ("m", "v")}
             if state_bits == 8:
-                state |= {k: [torch.ones(n, device=p.device) for n, p in zip(blocks, self.params)]
+                state |= {k: [torch.ones(n, device=p.device) for n, p in zip(blocks, bound)]
                           for k in ("m_scale", "v_scale")}
         keys = ("m", "v") if state_bits == 32 else ("m", "v", "m_scale", "v_scale")
-        self.state = {}
+        self._state = {}
         self._table = (AdamwTensor * max(1, len(sizes)))()
         f32 = torch.float32
-        for e, p, n, i in zip(self._table, self.params, sizes, range(len(sizes))):
+        for e, p, n, i in zip(self._table, bound, sizes, range(len(sizes))):
             e.param, e.n = _check_numel(p, "params", i, f32, n, dev), n
-        if len({p.data_ptr() for p in self.params if p.numel()}) < sum(n > 0 for n in sizes):
+        if len({p.data_ptr() for p in bound if p.numel()}) < sum(n > 0 for n in sizes):
             _bad("params must be distinct")   # updated in place, side by side
         for key in keys:
-            held = self.state[key] = _detached(state.get(key) or (), f"state[{key!r}]")
+            held = self._state[key] = tuple(_detached(state.get(key) or (), f"state[{key!r}]"))
             if len(held) != len(sizes):
                 _bad(f"state[{key!r}] must hold {len(sizes)} tensors")
             scales = key.endswith("scale")
             kind = f32 if scales or state_bits == 32 else None   # None: one byte each
             for e, t, n, i in zip(self._table, held, blocks if scales else sizes, range(len(held))):
                 setattr(e, key, _check_numel(t, f"state[{key!r}]", i, kind, n, dev))
-        self.copies = None if copies is None else _detached(copies, "copies")
-        if self.copies is not None:
-            if len(self.copies) != len(sizes):
+        self._copies = None if copies is None else tuple(_detached(copies, "copies"))
+        if self._copies is not None:
+            if len(self._copies) != len(sizes):
                 _bad(f"copies must hold {len(sizes)} tensors")
-            for e, t, n, i in zip(self._table, self.copies, sizes, range(len(sizes))):
+            for e, t, n, i in zip(self._table, self._copies, sizes, range(len(sizes))):
                 e.param_bf16 = _check_numel(t, "copies", i, torch.bfloat16, n, dev)
         self._options = AdamwOptions(state_bits=state_bits)
         self.bind_grads(grads)
 
+    @property
+    def params(self) -> tuple:
+        return self._params
+
+    @property
+    def grads(self) -> tuple:
+        return self._grads
+
+    @property
+    def copies(self) -> tuple | None:
+        return self._copies
+
+    @property
+    def state(self) -> dict:
+        return dict(self._state)
+
     def bind_grads(self, grads) -> None:
         """Take the next steps' gradients from these tensors."""
-        grads = _detached(grads, "grads")
-        if len(grads) != len(self.params):
-            _bad(f"grads must hold {len(self.params)} tensors")
+        grads = tuple(_detached(grads, "grads"))
+        if len(grads) != len(self._params):
+            _bad(f"grads must hold {len(self._params)} tensors")
         kind = grads[0].dtype if grads else torch.float32
         if kind not in (torch.float32, torch.bfloat16):
             _bad(f"grads must be float32 or bfloat16, got {kind}")
         dev = _device()
         _same_device(dev, self._dev)
         at = [_check_numel(t, "grads", i, kind, p.numel(), dev)
-              for i, (t, p) in enumerate(zip(grads, self.params))]
-        self.grads = grads
+              for i, (t, p) in enumerate(zip(grads, self._params))]
+        self._grads = grads
         for e, address in zip(self._table, at):
             e.grad = address
         self._options.grad_dtype = MOE_DTYPE_F32 if kind == torch.float32 else MOE_DTYPE_BF16
@@ -408,5 +425,5 @@ class AdamW:
         o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
         o.weight_decay, o.step = self.weight_decay, t
-        check(load().moe_adamw_step(self._table, len(self.params), o, _raw_stream(dev)))
+        check(load().moe_adamw_step(self._table, len(self._params), o, _raw_stream(dev)))
         self.steps_done = t

@@ -176,3 +176,36 @@ def test_gradients_of_another_device_are_refused(lib, monkeypatch):
     opt.step()
     (_, (table, count, options, stream)), = lib.calls
     assert count == 1 and table[0].grad == opt.grads[0].data_ptr() and opt.steps_done == 1
+
+
+def test_bound_tensors_stay_alive_and_counted(lib):
+    """What a caller does to the lists and tensors it gave or reads back changes
+    neither the table's memory nor its length."""
+    import gc
+    zeros = lambda: [on(torch.zeros(8 + i)) for i in range(2)]        # noqa: E731
+    params, grads, moments = zeros(), zeros(), {"m": zeros(), "v": zeros()}
+    opt = P.AdamW(params, grads, state=moments)
+    opt.step()
+    table = lib.calls[-1][1][0]
+    addresses = [[getattr(e, f) for e in table] for f in ("param", "grad", "m", "v")]
+    for name in ("params", "grads", "copies", "state"):
+        with pytest.raises(AttributeError):
+            setattr(opt, name, None)
+    for read in (opt.params, opt.grads, opt.state["m"]):
+        with pytest.raises((TypeError, AttributeError)):
+            read[0] = on(torch.zeros(8))
+        with pytest.raises(AttributeError):
+            read.append(on(torch.zeros(8)))
+    opt.state["m"] = zeros()                       # of a copy
+    for held in (params, grads, moments["m"], moments["v"]):
+        held[0].data = torch.zeros(8)
+        held.pop()
+    moments.clear()
+    gc.collect()
+    opt.step()
+    table, count = lib.calls[-1][1][:2]
+    assert count == 2 and [[getattr(e, f) for e in table] for f in ("param", "grad", "m", "v")] == addresses
+    held = opt.params + opt.grads + opt.state["m"] + opt.state["v"]
+    assert [t.data_ptr() for t in held] == sum(addresses, [])
+    again = P.AdamW(opt.params, opt.grads, state=opt.state, steps_done=opt.steps_done)
+    assert again.params[1].data_ptr() == addresses[0][1] and again.copies is None
