@@ -468,7 +468,11 @@ typedef struct {
  * amax / 448 (a block below 2^-100: scale 1, codes 0); a positive root never
  * rounds to zero.  New moments start as zero codes and any finite scale.  A
  * NaN or infinite gradient makes its element NaN, and with 8 bits its block.
- * `tensors` is host memory, read before the call returns. */
+ * `tensors` and `options` are host memory, read before the call returns: step,
+ * lr and the other scalars become part of the launch, and a step captured into
+ * a CUDA graph repeats them (the bias corrections of `step` among them) at every
+ * replay.  Only the gradients, the moments, the parameters and *grad_scale are
+ * read when it runs. */
 int32_t moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count,
                        const moe_adamw_options* options, void* stream);
 

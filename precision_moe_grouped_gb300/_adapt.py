@@ -36,6 +36,11 @@ def _device() -> int | None:
     return torch.cuda.current_device() if torch.cuda.is_initialized() else _lib._current_device()
 
 
+def _capturing() -> bool:
+    """Whether the current stream is captured into a CUDA graph."""
+    return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -330,7 +335,14 @@ class AdamW:
     default it starts at zero.  The tensors are bound and held here (params,
     grads, copies and state name them and cannot be assigned): after replacing
     a parameter's or a gradient's memory, build a new AdamW (state=old.state)
-    or pass the new gradients to step()."""
+    or pass the new gradients to step().
+
+    The step number and lr, betas, eps and weight_decay are the host's: they go
+    into the launch.  A step captured into a CUDA graph keeps the capture's at
+    every replay, so that the graph is good for that step number only (a
+    training loop captures forward and backward and calls step() after the
+    replay).  Under a capture step() therefore wants its number named, and
+    steps_done is left as it is: nothing has run yet."""
 
     def __init__(self, params, grads, copies=None, state_bits: int = 32, state=None,
                  lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
@@ -414,6 +426,10 @@ class AdamW:
     def step(self, grads=None, step: int | None = None, grad_scale=None) -> None:
         """One step, in place.  `step` (from 1) overrides the count kept here;
         grad_scale: float32 CUDA scalar every gradient is multiplied by."""
+        captured = _capturing()
+        if captured and step is None:
+            _bad("a captured step keeps its number at every replay: name it (step=...), or "
+                 "call step() outside the graph")
         if grads is not None:
             self.bind_grads(grads)
         t = self.steps_done + 1 if step is None else step
@@ -426,4 +442,5 @@ class AdamW:
         o.lr, (o.beta1, o.beta2), o.eps = self.lr, self.betas, self.eps
         o.weight_decay, o.step = self.weight_decay, t
         check(load().moe_adamw_step(self._table, len(self._params), o, _raw_stream(dev)))
-        self.steps_done = t
+        if not captured:
+            self.steps_done = t

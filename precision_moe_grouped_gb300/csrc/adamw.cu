@@ -58,9 +58,9 @@ struct Entry {
 };
 
 // The tensors of one launch travel as a kernel parameter (at most 32,764
-// bytes), so that a step copies nothing to the device and can be captured
-// into a graph.  The table comes in three sizes because its bytes are copied
-// at each launch.
+// bytes), so that a step copies nothing to the device.  Captured into a graph it
+// repeats its table and its scalars, so one step number, at every replay.  The
+// table comes in three sizes because its bytes are copied at each launch.
 template <int CAP>
 struct Table {
   int32_t count;

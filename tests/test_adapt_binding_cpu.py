@@ -209,3 +209,19 @@ def test_bound_tensors_stay_alive_and_counted(lib):
     assert [t.data_ptr() for t in held] == sum(addresses, [])
     again = P.AdamW(opt.params, opt.grads, state=opt.state, steps_done=opt.steps_done)
     assert again.params[1].data_ptr() == addresses[0][1] and again.copies is None
+
+
+def test_captured_step_wants_its_number(lib, monkeypatch):
+    """A graph repeats the step number it was captured with, so that one counted
+    here would be wrong from the second replay on."""
+    opt = adamw()
+    opt.step()
+    monkeypatch.setattr(_adapt, "_capturing", lambda: True, raising=False)
+    with pytest.raises(P.MoeError, match="captured step"):
+        opt.step()
+    assert len(lib.calls) == 1 and opt.steps_done == 1
+    opt.step(step=7)
+    assert lib.calls[-1][1][2].step == 7 and opt.steps_done == 1     # nothing has run
+    monkeypatch.setattr(_adapt, "_capturing", lambda: False)
+    opt.step()
+    assert lib.calls[-1][1][2].step == 2 and opt.steps_done == 2

@@ -30,3 +30,25 @@ def test_balance_coefficient_changes(T):
     fresh = P.BalanceLoss(16, 2, coef=0.25)(z, ids)
     assert all(torch.equal(p, q) for p, q in zip(quarter, fresh))
     assert torch.equal(quarter[0], one[0] * 0.25) and torch.equal(quarter[2], one[2] * 0.25)
+
+
+def test_captured_step_repeats_its_number():
+    """Replays of a captured step are eager steps of its number, whatever the
+    gradients; a step whose number is only counted is refused under a capture."""
+    g = torch.Generator(device=DEV).manual_seed(1)
+    p = torch.randn(5000, generator=g, device=DEV)
+    q, grad = p.clone(), torch.randn(5000, generator=g, device=DEV)
+    a, b = P.AdamW([p], [grad], lr=1e-2), P.AdamW([q], [grad], lr=1e-2)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(P.MoeError, match="captured step"):
+            b.step()
+        b.step(step=3)
+    b.lr = 1.0                       # no part of the graph any more
+    assert b.steps_done == 0
+    for _ in range(4):
+        grad.copy_(torch.randn(5000, generator=g, device=DEV))
+        graph.replay()
+        a.step(step=3)
+    torch.cuda.synchronize()
+    assert torch.equal(p, q) and torch.equal(a.state["v"][0], b.state["v"][0])
