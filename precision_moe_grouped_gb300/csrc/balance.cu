@@ -61,12 +61,12 @@ __global__ void __cluster_dims__(kCountCtas, 1, 1) __launch_bounds__(kCountThrea
   const int nth = PARTS ? static_cast<int>(blockIdx.x) : rank, of = PARTS ? parts * kCountCtas : kCountCtas;
   const int a = r.x + static_cast<int>(n * nth / of);
   const int b = r.x + static_cast<int>(n * (nth + 1) / of);
-  // a token a thread; its slots in groups of 8 loads that do not wait for one
-  // another or for the mask
+  // a token a thread (64 bits: the step past the last one may pass 2^31); its
+  // slots in groups of 8 loads that do not wait for one another or for the mask
   int valid = 0;
-  for (int t = a + static_cast<int>(threadIdx.x); t < b; t += kCountThreads) {
+  for (int64_t t = static_cast<int64_t>(a) + threadIdx.x; t < b; t += kCountThreads) {
     const bool ok = !mask || mask[t];
-    const int32_t* row = ids + static_cast<int64_t>(t) * k;
+    const int32_t* row = ids + t * k;
     for (int j0 = 0; j0 < k; j0 += 8) {
       int e[8];
 #pragma unroll

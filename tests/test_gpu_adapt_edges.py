@@ -52,3 +52,22 @@ def test_captured_step_repeats_its_number():
         a.step(step=3)
     torch.cuda.synchronize()
     assert torch.equal(p, q) and torch.equal(a.state["v"][0], b.state["v"][0])
+
+
+def test_balance_of_the_most_tokens():
+    """2^31 - 1 tokens, the most that the entry point takes: token indices that
+    step past 2^31 and byte offsets beyond 2^33.  With one expert p = 1, so loss
+    = coef * counted / valid and the gradient is 0.  A thread of the row kernel
+    adds some 2^31 / (608 * 128) terms in float, each sum off by 2^-24."""
+    T = 2 ** 31 - 1
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    z, ids = torch.zeros(T, 1, device=DEV), torch.zeros(T, 1, dtype=torch.int32, device=DEV)
+    mask = torch.ones(T, dtype=torch.uint8, device=DEV)
+    mask[-3000::2] = 0               # 1500 of the last ones: padding
+    ids[-2999:-999:2] = -1           # 1000 valid ones: no expert
+    loss, counts, dz = P.BalanceLoss(1, 1, coef=2.0)(z, ids, mask=mask)
+    valid = T - 1500
+    assert counts.tolist() == [[valid - 1000]]
+    assert not bool(dz.any())
+    assert abs(float(loss) - 2 * (valid - 1000) / valid) <= 2 * (T / (608 * 128) + 100) * 2.0 ** -24
