@@ -41,6 +41,13 @@ def _capturing() -> bool:
     return torch.cuda.is_initialized() and torch.cuda.is_current_stream_capturing()
 
 
+def _int32(name: str, *values: int) -> None:
+    """The structures' integers have 32 bits, and ctypes drops the rest."""
+    for n in values:
+        if not -1 << 31 <= n < 1 << 31:
+            _bad(f"{name} must be below 2^31, got {n}")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -156,6 +163,7 @@ class LowRankAdapters:
         """(shape, workspace bytes) of a call with T tokens."""
         got = self._sizes.get((T, kind, backward))
         if got is None:
+            _int32("tokens, adapters and features", T, *self._dims)
             s = AdapterShape(T, *self._dims, kind)
             n = self._lib.moe_adapter_workspace_size(s, backward)
             if n == 0:
@@ -266,6 +274,7 @@ class BalanceLoss:
         _bind_torch()
         self.num_experts, self.top_k, self.coef = num_experts, top_k, coef
         self._lib, self._calls = load(), {}
+        _int32("num_experts and top_k", num_experts, top_k)
         self._size(BalanceShape(0, num_experts, top_k, 1, coef))   # rejects bad sizes here
 
     def _size(self, s: BalanceShape) -> int:
@@ -305,6 +314,7 @@ class BalanceLoss:
         key = (T, E, k, S, coef)   # all that the shape holds
         got = self._calls.get(key)
         if got is None:
+            _int32("tokens, experts, top_k and sequences", *key[:4])
             s = BalanceShape(*key)
             if len(self._calls) > 4096:
                 self._calls.clear()
@@ -433,6 +443,7 @@ class AdamW:
         if grads is not None:
             self.bind_grads(grads)
         t = self.steps_done + 1 if step is None else step
+        _int32("step", t)
         dev, o = _device(), self._options
         _same_device(dev, self._dev)
         if grad_scale is not None:

@@ -225,3 +225,32 @@ def test_captured_step_wants_its_number(lib, monkeypatch):
     monkeypatch.setattr(_adapt, "_capturing", lambda: False)
     opt.step()
     assert lib.calls[-1][1][2].step == 2 and opt.steps_done == 2
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """Not taken modulo 2^32 (of views that repeat a row, which cost no memory)."""
+    n = 2 ** 32 + 4
+
+    class Dense(OnDevice):
+        def is_contiguous(self):
+            return True
+
+        def stride(self):
+            return 64, 1
+
+    def long(*shape, dtype):
+        return torch.zeros(1, dtype=dtype).expand(n, *shape).as_subclass(Dense)
+
+    op = adapters()
+    x, ids = long(64, dtype=torch.bfloat16), long(dtype=torch.int32)
+    out = long(32, dtype=torch.bfloat16)
+    calls = [lambda: op.forward(x, ids, out=out),
+             lambda: op.backward(long(32, dtype=torch.float32), x, ids, need_dx=False),
+             lambda: P.BalanceLoss(1, 1)(long(1, dtype=torch.float32), long(1, dtype=torch.int32), need_grad=False),
+             lambda: P.BalanceLoss(2 ** 32 + 8, 2), lambda: P.BalanceLoss(8, 2 ** 32 + 2),
+             lambda: adamw().step(step=2 ** 32 + 1)]
+    for i, call in enumerate(calls):
+        with pytest.raises(P.MoeError, match="2\\^31"):
+            call()
+            pytest.fail(f"refusal {i} did not come")
+    assert not lib.calls
