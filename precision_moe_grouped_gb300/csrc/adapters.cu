@@ -20,9 +20,8 @@
 // tensor map to be staged by, N would be r, and only the gradients' sums at
 // rank 64 and more keep the tensor pipe busy (0.4 of it).
 //
-// A call's kernels overlap by programmatic dependent launch, but its last one
-// never lets a successor start early: the forward of the layer reads its
-// logits, which may come from here, ahead of its own grid wait.
+// A call's kernels overlap by programmatic dependent launch; its last one lets
+// no successor start early (it would only wait, on SMs that this call fills).
 //
 // u and w are computed in float and leave as bf16 planes that add up to them:
 // hi = bf16(v), then mid (and lo) the rounded rests.  Two planes (an error

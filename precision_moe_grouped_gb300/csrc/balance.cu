@@ -17,8 +17,8 @@
 // bytes a token; the counts read 4 k bytes a token.  65,536 tokens of 256
 // experts, top-8, with the gate's gradient: 31.5 us, 4.5 TB/s of those bytes
 // (the copy's rate would be 21 us), with 0.65 of the issue slots taken by the
-// softmax's arithmetic.  (A call's last kernel lets
-// no successor start early: others may read its results ahead of a grid wait.)
+// softmax's arithmetic.  (A call's last kernel lets no successor start early:
+// it would only wait, on SMs that this call fills.)
 #include <cfloat>
 
 #include "cluster.cuh"

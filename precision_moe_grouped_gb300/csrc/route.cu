@@ -97,13 +97,10 @@ __device__ __forceinline__ void route_token_warp(const float* __restrict__ row, 
 }
 
 // One warp per token (32 warps = one chunk per CTA): route_token_warp, then
-// the chunk's per-expert histogram.  The logits are the forward's input,
-// complete before the previous kernel on the stream passed its own grid
-// wait (every kernel here signals its dependents only after that wait), so
-// the routing and the shared-memory histogram run before this kernel's
-// wait, overlapping the previous forward's last kernel; every global write
-// (which that kernel's reads of the workspace may still precede) follows
-// the wait.
+// the chunk's per-expert histogram.  Only the histogram's zeroing precedes the
+// grid wait: the logits may come from the kernel just before this one on the
+// stream, and that kernel may let its successors start before it has written
+// them (a library's GEMM for the router, for one).
 template <int NV>
 __global__ void __launch_bounds__(1024) route_kernel(const float* __restrict__ logits, int T,
                                                     int E, int k, int32_t* __restrict__ ids,
@@ -114,6 +111,8 @@ __global__ void __launch_bounds__(1024) route_kernel(const float* __restrict__ l
   static_assert(kRouteChunk == 32, "one warp per token of the chunk");
   extern __shared__ int32_t hist[];
   for (int i = threadIdx.x; i < E; i += blockDim.x) hist[i] = 0;
+  griddep_wait();
+  griddep_launch_dependents();
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int t = blockIdx.x * kRouteChunk + warp;
@@ -124,8 +123,6 @@ __global__ void __launch_bounds__(1024) route_kernel(const float* __restrict__ l
     if (lane < k) atomicAdd(&hist[my_id], 1);
   }
   __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();
   // the forward's first kernel clears the device status word
   if (status && blockIdx.x == 0 && threadIdx.x == 0) {
     status[0] = 0;
@@ -736,12 +733,11 @@ __global__ void __launch_bounds__(1024, 2) expand_small_kernel(
 // one kernel of T CTAs (1024 threads each), so the routed rows need no
 // second launch and each token row is fetched while the routing runs.
 // CTA t:
-//   1. prefetches token t's row into L2; warp w routes token w (every CTA
-//      routes all T tokens -- the same selection and softmax as
-//      route_kernel; the logits are L2-resident after the first CTA) and
-//      counts its experts (shared atomics) -- all before the grid wait, as
-//      in route_kernel: logits and x are the forward's inputs;
-//   2. after the wait: offsets (block scan), the tile plan and the stable
+//   1. prefetches token t's row into L2 and waits for the grid before;
+//      warp w routes token w (every CTA routes all T tokens -- the same
+//      selection and softmax as route_kernel; the logits are L2-resident
+//      after the first CTA) and counts its experts (shared atomics);
+//   2. offsets (block scan), the tile plan and the stable
 //      rank of token t's slots (earlier tokens routed to the same expert);
 //      CTA 0 writes counts, offsets and the tile list;
 //   3. quantises token t into its k rows (quantize_token).
@@ -767,10 +763,10 @@ __global__ void __launch_bounds__(1024) route_expand_tiny_kernel(
     // Route the T tokens like the CTAs below, plan the tiles without
     // writing them, and ask L2 for the first weight boxes (and their scale
     // blocks) of the GEMM1 items that run first: items 0 .. first_items-1,
-    // item i = tile i / MT, M-tile i % MT.  Only inputs are read and
-    // nothing is written, so these CTAs never wait for the previous grid:
-    // the weight stream starts while the front end (and the previous
-    // forward's last kernel) runs.
+    // item i = tile i / MT, M-tile i % MT.  These CTAs write nothing and
+    // never wait for the previous grid: the weight stream starts while it
+    // runs.  Logits that it has yet to write only spoil the guess (whatever
+    // they hold, k experts in range come out).
     for (int i = threadIdx.x; i < E; i += blockDim.x) cnt[i] = 0;
     __syncthreads();
     if (warp < T) {
@@ -808,6 +804,8 @@ __global__ void __launch_bounds__(1024) route_expand_tiny_kernel(
       asm volatile("prefetch.global.L2 [%0];" ::"l"(base + static_cast<size_t>(i) * 128));
   }
   for (int i = threadIdx.x; i < E; i += blockDim.x) cnt[i] = 0;
+  griddep_wait();   // logits and x may come from the kernel before this one
+  griddep_launch_dependents();
   __syncthreads();
   int my_id = 0;
   float my_w = 0.f;
@@ -819,8 +817,6 @@ __global__ void __launch_bounds__(1024) route_expand_tiny_kernel(
     }
   }
   __syncthreads();
-  griddep_wait();
-  griddep_launch_dependents();
   if (t == 0 && threadIdx.x == 0) {   // first kernel of the forward
     status[0] = 0;
     if (kChecks) {
