@@ -368,7 +368,9 @@ size_t moe_adapter_workspace_size(const moe_adapter_shape* shape, int32_t backwa
  * x, a, b, base and out 16-byte aligned, row strides multiples of 8 elements
  * and at least the row's length.  The product A_a x is held in float and
  * enters the second product as bf16 terms: two for a bf16 out (an error
- * below 2^-17 of it), three for a float one (2^-25). */
+ * below 2^-17 of it), three for a float one (2^-25).  An infinite x gives what
+ * the formula does; an infinite element of a pool makes what it enters infinite
+ * or NaN. */
 int32_t moe_adapter_forward(const moe_adapter_shape* shape, const void* x, int64_t ld_x,
                             const int32_t* adapter_ids, const void* a, const void* b,
                             const float* scale, const void* base, int64_t ld_base, void* out,
@@ -383,7 +385,8 @@ int32_t moe_adapter_forward(const moe_adapter_shape* shape, const void* x, int64
  *   da  float [NA, r, H] = sum over the adapter's tokens of u x^T
  *   db  float [NA, N, r] = scale_a * sum of dout (A_a x)^T
  * da and db are written in full (zero for an adapter without tokens); both or
- * neither may be NULL. */
+ * neither may be NULL.  An infinite dout or x gives dx as the formula does, and
+ * makes the elements of da and db that it enters infinite or NaN. */
 int32_t moe_adapter_backward(const moe_adapter_shape* shape, const void* dout, int64_t ld_dout,
                              const void* x, int64_t ld_x, const int32_t* adapter_ids,
                              const void* a, const void* b, const float* scale,

@@ -383,9 +383,10 @@ constexpr int red_stride(int RP) { return RP + 4; }
 
 // Each CTA of the cluster takes a share of the tile's tokens: it sums their
 // WK partial rows [WK][NTOK][RP + 4] over warps and CTAs, in that order, and
-// writes the planes.
+// writes the planes; zeros from rank r on, where an infinite row of the source
+// has left NaN (0 * inf).
 template <int RP, int WK, int NTOK>
-__device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float scale,
+__device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float scale, int r,
                                             const Planes& dst) {
   constexpr int RS = red_stride(RP);
   const int S = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
@@ -401,7 +402,8 @@ __device__ __forceinline__ void finish_tile(float* red, const Tile& tile, float 
       v.x += u.x, v.y += u.y, v.z += u.z, v.w += u.w;
     }
     // these rows of this CTA are read by no other
-    *reinterpret_cast<float4*>(p) = make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale);
+    *reinterpret_cast<float4*>(p) = i % (RP / 4) * 4 < r
+        ? make_float4(v.x * scale, v.y * scale, v.z * scale, v.w * scale) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
   if (dst.row)
@@ -565,7 +567,7 @@ __device__ __forceinline__ void shrink_tile(const ShrinkArgs& a, const Tile& til
     for (int q = 0; q < 4; ++q)
       mine[(16 * wm + g + 8 * (q >> 1)) * RS + 8 * (wn * NT + j) + 2 * t + (q & 1)] = acc[j][q];
   const float scale = a.scale ? __ldg(a.scale + tile.adapter) : 1.0f;
-  finish_tile<C::RP, C::WK, kTile>(red, tile, scale, a.dst);
+  finish_tile<C::RP, C::WK, kTile>(red, tile, scale, a.r, a.dst);
 }
 
 // Cluster of S CTAs per tile, sharing out the chunks of K.
@@ -963,6 +965,7 @@ __global__ void __launch_bounds__(kThreads, RT == 8 ? 1 : 2)
     const int r = i / (RP / 4), j = i % (RP / 4) * 4;
     float4 v = cluster_sum4(red + r * RS + j, CS);
     v.x *= scale, v.y *= scale, v.z *= scale, v.w *= scale;
+    if (j >= a.r) v = make_float4(0.f, 0.f, 0.f, 0.f);   // (as in finish_tile)
     uint8_t* o = v_s + piece<2 * RP>(r, j / 8) + 2 * (j % 8);
 #pragma unroll
     for (int p = 0; p < C::VN; ++p) {

@@ -71,3 +71,49 @@ def test_balance_of_the_most_tokens():
     assert counts.tolist() == [[valid - 1000]]
     assert not bool(dz.any())
     assert abs(float(loss) - 2 * (valid - 1000) / valid) <= 2 * (T / (608 * 128) + 100) * 2.0 ** -24
+
+
+def formula(x, ids, a, b, scale, dout):
+    """out (without a base), dx, da, db in 64 bits."""
+    x, a, b, dout = x.double(), a.double(), b.double(), dout.double()
+    out, dx = torch.zeros_like(dout), torch.zeros_like(x)
+    da, db = torch.zeros_like(a), torch.zeros_like(b)
+    for i in range(a.shape[0]):
+        rows = torch.nonzero(ids == i).reshape(-1)
+        s = scale[i].double()
+        v, u = x[rows] @ a[i].T, s * (dout[rows] @ b[i])
+        out[rows], dx[rows] = s * (v @ b[i].T), u @ a[i]
+        da[i], db[i] = u.T @ x[rows], s * dout[rows].T @ v
+    return out, dx, da, db
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,r", [(20, 8), (20, 24), (20, 16), (60, 72), (1100, 8), (1100, 40), (80, 72), (1100, 128)])
+def test_infinities(T, r, kind):
+    """An infinite x or dout: out and dx are infinite, with the formula's sign, or
+    NaN where the formula's are (ranks that a kernel pads with zeros must not
+    make NaN of them), da and db not finite where the formula's are not, and all
+    else is what it was."""
+    H, N, NA = 72, 64, 3
+    g = torch.Generator(device=DEV).manual_seed(T + r)
+    rnd = lambda *s: torch.randn(*s, generator=g, device=DEV)        # noqa: E731
+    x, dout, ids = rnd(T, H).bfloat16(), rnd(T, N).to(kind), (torch.arange(T, device=DEV) % NA).to(torch.int32)
+    a, b, scale = rnd(NA, r, H).bfloat16(), rnd(NA, N, r).bfloat16(), torch.rand(NA, generator=g, device=DEV) + 0.5
+    # one sign throughout for some outputs, so that the formula gives infinities beside NaN
+    a[:, :, 5], b[:, 1::2] = a[:, :, 5].abs(), b[:, 1::2].abs()
+    b[:, 7], a[:, :, 2::3] = b[:, 7].abs(), a[:, :, 2::3].abs()
+    op = P.LowRankAdapters(a, b, scale)
+    clean = (op.forward(x, ids, out_dtype=kind),) + op.backward(dout, x, ids)
+    for sign in (1, -1):
+        xi, di = x.clone(), dout.clone()
+        xi[4, 5], di[7, 7] = sign * float("inf"), sign * float("inf")
+        out, dx, da, db = (op.forward(xi, ids, out_dtype=kind),) + op.backward(di, xi, ids)
+        ref = formula(xi, ids, a, b, scale, di)
+        assert bool(ref[0].isinf().any()) and bool(ref[1].isinf().any())
+        for name, got, want, old in zip(("out", "dx"), (out, dx), ref, clean):
+            assert torch.equal(got.isnan(), want.isnan()), name
+            assert torch.equal(got.double()[want.isinf()], want[want.isinf()]), name
+            assert torch.equal(got[want.isfinite()], old[want.isfinite()]), name
+        for name, got, want, old in zip(("da", "db"), (da, db), ref[2:], clean[2:]):
+            assert torch.equal(got.isfinite(), want.isfinite()), name
+            assert torch.equal(got[want.isfinite()], old[want.isfinite()]), name
