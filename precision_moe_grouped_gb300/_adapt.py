@@ -131,33 +131,26 @@ class LowRankAdapters:
         if b is None or b.dim() != 3:
             _bad("b must be [adapters, out_features, rank]")
         N = self.out_features = b.shape[1]
-        self._dims = NA, r, H, N
+        self._dims, self._H, self._N = (NA, r, H, N), H, N
         self._shapes = (NA, r, H), (NA, N, r), (NA,)
         self.a, self.b, self.scale, self.device, self._dev = a, b, scale, a.device, dev
-        self._at = None
-        self._addresses()
+        self._check_pools(a.data_ptr(), b.data_ptr(), _ptr(scale))
         self._lib = load()
         self._sizes = {}
         for kind in (MOE_DTYPE_BF16, MOE_DTYPE_F32):   # rejects unsupported sizes here
             self._call(0, kind, 0)
 
-    def _addresses(self) -> tuple:
-        """Of a, b and scale, checked where they are not the last call's.  That
-        one's memory is held (detached), so that it cannot have become another
-        tensor's in the meantime."""
-        a, b, scale = self.a, self.b, self.scale
-        if a is None or b is None:
-            _bad("a or b is None")
-        at = a.data_ptr(), b.data_ptr(), None if scale is None else scale.data_ptr()
-        if at != self._at:
-            shapes = self._shapes
-            _check_flat(a, "a", torch.bfloat16, shapes[0], self._dev)
-            _check_flat(b, "b", torch.bfloat16, shapes[1], self._dev)
-            if scale is not None:
-                _check_flat(scale, "scale", torch.float32, shapes[2], self._dev)
-            self._held = [t.detach() for t in (a, b, scale) if t is not None]
-            self._at = at
-        return at
+    def _check_pools(self, *at) -> None:
+        """Checks a, b and scale, whose addresses are not the last call's.  That
+        one's memory is held (detached): while it was the last call's, no other
+        tensor could get its addresses."""
+        shapes = self._shapes
+        _check_flat(self.a, "a", torch.bfloat16, shapes[0], self._dev)
+        _check_flat(self.b, "b", torch.bfloat16, shapes[1], self._dev)
+        if self.scale is not None:
+            _check_flat(self.scale, "scale", torch.float32, shapes[2], self._dev)
+        self._held = [t.detach() for t in (self.a, self.b, self.scale) if t is not None]
+        self._at_a, self._at_b, self._at_scale = at
 
     def _call(self, T: int, kind: int, backward: int):
         """(shape, workspace bytes) of a call with T tokens."""
@@ -191,8 +184,10 @@ class LowRankAdapters:
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        at = self._addresses()
-        T, (_, _, H, N) = _rows(x, "x"), self._dims
+        a, b, scale = _ptr(self.a), _ptr(self.b), _ptr(self.scale)
+        if a != self._at_a or b != self._at_b or scale != self._at_scale:
+            self._check_pools(a, b, scale)
+        T, H, N = _rows(x, "x"), self._H, self._N
         ld_x = _check_rows(x, "x", torch.bfloat16, (T, H), dev)
         _check_flat(ids, "ids", torch.int32, (T,), dev)
         dtype = base.dtype if base is not None else out.dtype if out is not None else (
@@ -208,8 +203,8 @@ class LowRankAdapters:
         s, n = self._call(T, kind, 0)
         ws = None if n <= 256 else _scratch(n, x)   # small batches use none
         rc = self._lib.moe_adapter_forward(
-            s, x.data_ptr(), ld_x, ids.data_ptr(), *at, _ptr(base), ld_base, out.data_ptr(), ld_out,
-            _ptr(ws), n, _raw_stream(dev))
+            s, x.data_ptr(), ld_x, ids.data_ptr(), a, b, scale, _ptr(base), ld_base, out.data_ptr(),
+            ld_out, _ptr(ws), n, _raw_stream(dev))
         if rc:
             check(rc)
         return out
@@ -225,8 +220,10 @@ class LowRankAdapters:
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        at = self._addresses()
-        T, (_, _, H, N) = _rows(x, "x"), self._dims
+        a, b, scale = _ptr(self.a), _ptr(self.b), _ptr(self.scale)
+        if a != self._at_a or b != self._at_b or scale != self._at_scale:
+            self._check_pools(a, b, scale)
+        T, H, N = _rows(x, "x"), self._H, self._N
         if dout is None:
             _bad("dout is None")
         kind, wide = self._kind(dout.dtype, "dout"), (T, H)
@@ -257,8 +254,9 @@ class LowRankAdapters:
         s, n = self._call(T, kind, 1)
         ws = _scratch(n, x)
         rc = self._lib.moe_adapter_backward(
-            s, dout.data_ptr(), ld_dout, x.data_ptr(), ld_x, ids.data_ptr(), *at, _ptr(dx_base),
-            ld_base, _ptr(dx), ld_dx, _ptr(da), _ptr(db), ws.data_ptr(), n, _raw_stream(dev))
+            s, dout.data_ptr(), ld_dout, x.data_ptr(), ld_x, ids.data_ptr(), a, b, scale,
+            _ptr(dx_base), ld_base, _ptr(dx), ld_dx, _ptr(da), _ptr(db), ws.data_ptr(), n,
+            _raw_stream(dev))
         if rc:
             check(rc)
         return dx, da, db
