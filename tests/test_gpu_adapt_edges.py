@@ -117,3 +117,23 @@ def test_infinities(T, r, kind):
         for name, got, want, old in zip(("da", "db"), (da, db), ref[2:], clean[2:]):
             assert torch.equal(got.isfinite(), want.isfinite()), name
             assert torch.equal(got[want.isfinite()], old[want.isfinite()]), name
+
+
+@pytest.mark.parametrize("E,T", [(64, 40), (256, 3000)])
+def test_rare_experts(E, T):
+    """Logits up to 80 below their row's largest: an exponential is within 2 +
+    1.2 |z - max| units (2^-23) of it, its argument is rounded once (|z - max|
+    2^-24), and 70 roundings of 2^-24 hold the sums over the experts and the
+    products after them."""
+    g = torch.Generator(device=DEV).manual_seed(E)
+    z = -80 * torch.rand(T, E, generator=g, device=DEV)
+    z[:, 0] = 0
+    ids = torch.randint(0, E, (T, 2), generator=g, device=DEV).to(torch.int32)
+    _, counts, dz = P.BalanceLoss(E, 2, coef=1.0)(z, ids)
+    p = z.double().softmax(1)
+    f = counts[0].double() * (E / (2 * T))
+    dot = p @ f
+    ref = p / T * (f - dot[:, None])
+    tol = p / T * (f + dot[:, None]) * ((2 - 1.2 * z.double()) * 2.0 ** -23 + (70 - z.double()) * 2.0 ** -24)
+    bad = (dz.double() - ref).abs() > tol + 1e-37
+    assert not bool(bad.any()), int(bad.sum())
