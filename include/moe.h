@@ -432,7 +432,8 @@ size_t moe_balance_workspace_size(const moe_balance_shape* shape);
  *   loss         float [1]     counts int32 [S, E]
  *   dlogits      float [T, E] written in full, or NULL
  * num_tokens == 0 writes a zero loss and zero counts.  Sums run in float in a
- * fixed order. */
+ * fixed order; an exponential is within 2 + 1.2 |z - max| units in the last place
+ * (3e-6 of it for a logit 20 below its row's largest). */
 int32_t moe_balance_loss(const moe_balance_shape* shape, const float* logits, const int32_t* ids,
                          const uint8_t* token_mask, const int32_t* seq_offsets,
                          const float* weights, const float* dweights, float* loss,

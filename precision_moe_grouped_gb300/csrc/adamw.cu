@@ -283,7 +283,9 @@ __device__ __forceinline__ void take_block(const Entry& t, int64_t w0, const Sca
 // One CTA per chunk of one tensor, a block of 256 a warp.  One block and no
 // more: the next CTA's loads then run under this one's arithmetic, about 70
 // instructions an element with 8-bit moments (200 M elements: 542 us at six
-// CTAs an SM; 720 with two blocks a warp in turn).
+// CTAs an SM; 720 with two blocks a warp in turn).  Six CTAs leave the 8-bit form
+// 40 registers, and it spills: 120 bytes of stores and 152 of loads a thread, some
+// 8 of those instructions.
 template <bool BITS8, bool BF16G, int CAP>
 __global__ void __launch_bounds__(kThreads, BITS8 ? 6 : 4)
     adamw_kernel(const __grid_constant__ Table<CAP> tab, const Scalars s) {

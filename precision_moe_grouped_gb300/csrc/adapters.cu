@@ -16,9 +16,12 @@
 // throughput would bind, so the layout serves the memory stream: the long
 // operand is staged by asynchronous copies (small batches: loaded straight
 // into fragments) and multiplied by mma.sync (16x8x16, bf16, float
-// accumulators).  mma.sync rather than tcgen05: the gathered rows have no
-// tensor map to be staged by, N would be r, and only the gradients' sums at
-// rank 64 and more keep the tensor pipe busy (0.4 of it).
+// accumulators).  Only the gradients' sums at rank 64 and more are held up by
+// it (the tensor pipe 0.4 busy): there tcgen05, which reads its operands from
+// shared memory whoever staged them, would lift the limit.  It is not built.
+// (Registers: the contractions at rank 128, both of them at rank 32 with a float
+// dout, and small batches at rank 64 are held to 128 for two CTAs an SM and spill up
+// to 72 bytes a thread; the others 16 at most.)
 //
 // A call's kernels overlap by programmatic dependent launch; its last one lets
 // no successor start early (it would only wait, on SMs that this call fills).
@@ -1210,11 +1213,13 @@ struct AdapterWs {
 AdapterWs adapter_ws(const moe_adapter_shape* s, bool backward) {
   const int64_t T = s->num_tokens, NA = s->num_adapters;
   AdapterWs w = {};
-  // One kernel where it is no slower than three (7168 x 7168, rank 16, 8
-  // adapters: 8.3 us against 12.9 at 128 tokens, 9.9 / 13.8 at 256, 17.8 / 20.3 at
-  // 1021; 64 adapters: 24.2 / 28.6.  Rank 64 at 1021: 32.8 / 31.3, 46.5 / 56.0).  At
-  // rank 128 its tiles of 16 tokens read the pools too often (2048 x 2048: 10.1 /
-  // 14.2 at 64 tokens, 20.2 / 14.6 at 256).
+  // One kernel up to where three catch up (7168 x 7168, rank 16, 8 adapters:
+  // 8.3 us against 12.9 at 128 tokens, 9.9 / 13.8 at 256, 17.8 / 20.3 at 1021; 64
+  // adapters: 24.2 / 28.6).  At rank 64 the two meet near 1024 tokens: with 8 adapters
+  // 32.8 / 31.3 at 1021, with 64 46.5 / 56.0.  At rank 128 its tiles of 16 tokens read
+  // the pools too often (2048 x 2048: 10.1 / 14.2 at 64 tokens, 20.2 / 14.6 at 256).
+  // What it costs is the pools' rows times the tiles, so that the rule, which sees
+  // neither the features nor the adapters, is a little off near its edge.
   w.small = !backward && T <= (s->rank <= 64 ? kSmallTokens : 64);
   // an adapter with n tokens has at most n / 16 + 1 tiles
   const int64_t small_units = T / kSmallTile + NA + 1;

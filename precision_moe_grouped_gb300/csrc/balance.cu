@@ -218,7 +218,9 @@ struct Rows {
     float sum = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < 4 * V; ++i) {
-      z[i] = __expf(z[i] - base);   // within 2 + 1.2 |z - base| units in the last place
+      // within 2 + 1.2 |z - base| units in the last place: in proportion to how
+      // rare the expert is (the issue slots, not the precision, bound this kernel)
+      z[i] = __expf(z[i] - base);
       sum += z[i];
       dot = fmaf(z[i], f[i], dot);
     }
@@ -483,8 +485,9 @@ constexpr int kMaxCtas = 152 * 8;   // CTAs the partial sums have room for
 
 // Clusters that count a batch of one sequence: one for each round of their
 // threads (32,768 tokens of 64 experts, top-8: 13 us against 16 with one, at
-// 131,072 of 256 53 against 73; more than eight gain nothing).  Several
-// sequences have as many clusters already.
+// 131,072 of 256 54 against 73; more than eight gain nothing).  Several sequences
+// have a cluster each: as good from eight on (131,072 tokens in eight: 54 us), not
+// below (in two: 62.5).
 int count_parts(const moe_balance_shape* s) {
   const int parts = s->num_sequences > 1 ? 1 : s->num_tokens / (kCountCtas * kCountThreads);
   return parts < 1 ? 1 : parts < 8 ? parts : 8;
