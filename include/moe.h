@@ -480,6 +480,59 @@ typedef struct {
 int32_t moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count,
                        const moe_adamw_options* options, void* stream);
 
+/* Limits of the gated feed-forward block. */
+#define MOE_FFN_MAX_TOKENS (1 << 24)
+#define MOE_FFN_MAX_FEATURES (1 << 17)
+
+/* A gated feed-forward block in bf16 (a shared expert, or a dense layer, beside
+ * the routed experts).  Limits: 0 <= num_tokens <= MOE_FFN_MAX_TOKENS; hidden
+ * and inter positive multiples of 8 up to MOE_FFN_MAX_FEATURES. */
+typedef struct {
+  int32_t num_tokens;   /* T */
+  int32_t hidden;       /* H */
+  int32_t inter;        /* I */
+} moe_ffn_shape;
+
+/* Workspace bytes of moe_ffn_forward (backward = 0) or moe_ffn_backward (1); 0
+ * for an invalid shape. */
+size_t moe_ffn_workspace_size(const moe_ffn_shape* shape, int32_t backward);
+
+/* out = base + (silu(x Wg^T) * (x Wu^T)) Wd^T, one token a row.
+ *   x          bf16 [T, H], rows ld_x elements apart
+ *   w_gate_up  bf16 [2 I, H]: rows 0 .. I - 1 Wg, I .. 2 I - 1 Wu
+ *   w_down     bf16 [H, I]
+ *   base       bf16 [T, H], rows ld_base apart; NULL for zero; may be out itself
+ *   out        bf16 [T, H], rows ld_out apart; may be x itself (the same
+ *              stride), otherwise no part of x or of the weights
+ *   status     device int32, zeroed by the caller when it is made: the first
+ *              device-side error (MOE_ERR_DEVICE_TIMEOUT: a bounded wait ran
+ *              out) is recorded there, and stays; the results are then undefined
+ * x, base, out and the weights 16-byte aligned, row strides multiples of 8
+ * elements and at least the row's length.  Sums are float; silu(g) u is
+ * rounded to bf16 once, between the two products.  Up to 32 tokens stream the
+ * weights once from HBM; larger batches run on the tensor cores. */
+int32_t moe_ffn_forward(const moe_ffn_shape* shape, const void* x, int64_t ld_x,
+                        const void* w_gate_up, const void* w_down, const void* base,
+                        int64_t ld_base, void* out, int64_t ld_out, void* workspace,
+                        size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Gradients of moe_ffn_forward for dout (bf16 [T, H], rows ld_dout apart).  The
+ * activations are computed again from x, so that nothing of the forward is kept:
+ *   dh = dout Wd, s = sigmoid(g): du = dh g s, dg = dh u s (1 + g (1 - s))
+ *   dx          bf16 [T, H] = dx_base + dg Wg + du Wu; dx_base bf16 or NULL for
+ *               zero, may be dx itself; NULL: not computed.  Not the memory of
+ *               x or dout
+ *   dw_gate_up  bf16 [2 I, H] = [dg^T x; du^T x]
+ *   dw_down     bf16 [H, I] = dout^T (silu(g) u)
+ * The weights' gradients are written in full (zero without tokens); both or
+ * neither may be NULL.  Sums are float and rounded once; dg, du and silu(g) u
+ * are rounded to bf16 once, ahead of the products that they enter. */
+int32_t moe_ffn_backward(const moe_ffn_shape* shape, const void* dout, int64_t ld_dout,
+                         const void* x, int64_t ld_x, const void* w_gate_up, const void* w_down,
+                         const void* dx_base, int64_t ld_dx_base, void* dx, int64_t ld_dx,
+                         void* dw_gate_up, void* dw_down, void* workspace,
+                         size_t workspace_bytes, int32_t* status, void* stream);
+
 /* Message describing the last error returned on the calling thread. */
 const char* moe_last_error(void);
 

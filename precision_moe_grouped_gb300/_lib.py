@@ -34,7 +34,7 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_layout", "moe_prepare_weights", 
            "moe_version", "moe_route_noalloc", "moe_steps_workspace_size",
            "moe_forward_host_steps", "moe_adapter_workspace_size", "moe_adapter_forward",
            "moe_adapter_backward", "moe_balance_workspace_size", "moe_balance_loss",
-           "moe_adamw_step")
+           "moe_adamw_step", "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward")
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
@@ -103,6 +103,10 @@ class AdamwOptions(ctypes.Structure):
                 [("reserved", ctypes.c_int32 * 2), ("grad_scale", ctypes.c_void_p)])
 
 
+class FfnShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "hidden", "inter")]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"moe error {code}: {msg}")
@@ -167,6 +171,14 @@ def load() -> ctypes.CDLL:
     lib.moe_balance_loss.restype = i32
     lib.moe_adamw_step.argtypes = [ctypes.POINTER(AdamwTensor), i32, ctypes.POINTER(AdamwOptions), vp]
     lib.moe_adamw_step.restype = i32
+    fsh = ctypes.POINTER(FfnShape)
+    lib.moe_ffn_workspace_size.argtypes = [fsh, i32]
+    lib.moe_ffn_workspace_size.restype = sz
+    lib.moe_ffn_forward.argtypes = [fsh, vp, i64, vp, vp, vp, i64, vp, i64, vp, sz, vp, vp]
+    lib.moe_ffn_forward.restype = i32
+    lib.moe_ffn_backward.argtypes = ([fsh, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64] + [vp] * 3 +
+                                     [sz, vp, vp])
+    lib.moe_ffn_backward.restype = i32
     _lib = lib
     return lib
 

@@ -1,5 +1,5 @@
 // cluster.cuh -- distributed shared memory of a thread-block cluster: rank,
-// barrier and loads from another CTA's shared memory.
+// barriers and loads from another CTA's shared memory.
 #pragma once
 
 #include <cstdint>
@@ -45,6 +45,12 @@ __device__ __forceinline__ float4 cluster_load4(const float* p, uint32_t rank) {
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
                : "r"(cluster_addr(p, rank)));
   return v;
+}
+
+// Arrives on the mbarrier at a shared::cluster address (cluster_addr's).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
+               : "memory");
 }
 
 }  // namespace moe

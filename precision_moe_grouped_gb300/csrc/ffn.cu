@@ -1,0 +1,801 @@
+// ffn.cu -- a gated feed-forward block in bf16 and its gradients: the shared
+// expert, or a dense layer, beside the routed experts.
+//
+//   g = x Wg^T, u = x Wu^T, h = silu(g) u, out = base + h Wd^T
+//   dh = dout Wd, s = sigmoid(g): du = dh g s, dg = dh u s (1 + g (1 - s))
+//   dx = dx_base + dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dout^T h
+//
+// Sums are float; h, dg and du enter the second products as bf16, each
+// rounded once (half a step of 2^-8), as the outputs are: an output's error is
+// then about sqrt(2) of its own rounding's.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "dense.cuh"
+#include "entry.h"
+
+namespace moe {
+namespace {
+
+using dense::Elem;
+using dense::EpiWarp;
+using dense::Maps;
+using dense::Problem;
+using dense::Tile;
+
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr int kDecodeTokens = 32;   // at most: the products that stream the weights once
+
+// ------------------------------------------------------------- activation
+// silu(g) = g / (1 + e^-g), its factor s = 1 / (1 + e^-g): fast exponential and
+// division (relative error about 1e-6, far below the bf16 rounding that follows).
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.0f, 1.0f + __expf(-g)); }
+__device__ __forceinline__ float swiglu(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+struct Grads {
+  float h, dg, du;
+};
+__device__ __forceinline__ Grads swiglu_grads(float g, float u, float dh) {
+  const float s = sigmoid(g), a = g * s;
+  return {a * u, dh * u * (s * (1.0f + g * (1.0f - s))), dh * a};
+}
+
+// -------------------------------------------------------------- epilogues
+// bf16 out = base + D.
+struct EpiOut {
+  struct Args {
+    const __nv_bfloat16* base;   // or null
+    int64_t ld_base;
+    int32_t map, rows, cols;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
+                                             const EpiWarp& w, const Maps& maps) {
+    if (w.row >= a.rows) return;
+    const int c0 = w.half * (p.bn >> 1);
+    const bool mine = w.row + w.lane < a.rows;
+    for (int c = c0; c < c0 + (p.bn >> 1); c += 64) {
+      const int col = o.j * p.bn + c;
+      if (col >= a.cols) return;
+      uint32_t lo[32], hi[32];
+      dense::tmem_ld_x32(w.tmem + c, lo);
+      dense::tmem_ld_x32(w.tmem + c + 32, hi);
+      uint4 b[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        b[i] = make_uint4(0, 0, 0, 0);
+        if (a.base && mine && col + 8 * i < a.cols)
+          b[i] = *reinterpret_cast<const uint4*>(a.base + (w.row + w.lane) * a.ld_base + col + 8 * i);
+      }
+      dense::tmem_wait(lo);
+      dense::tmem_wait(hi);
+      if (w.lane == 0) dense::box_wait_read();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t* v = i < 4 ? lo + 8 * i : hi + 8 * (i - 4);
+        uint32_t r[4];
+        const uint32_t bb[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = dense::unpack_bf16(bb[k]);
+          r[k] = dense::pack_bf16(__uint_as_float(v[2 * k]) + f.x, __uint_as_float(v[2 * k + 1]) + f.y);
+        }
+        *dense::box_piece(w.box, w.lane, i) = make_uint4(r[0], r[1], r[2], r[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0) dense::box_store(&maps.m[a.map], w.box, col, w.row);
+    }
+  }
+};
+
+// Float sums as they are: shares of K, or what a later kernel's epilogue reads.
+// Row r of share s goes to row s rows_pad + r, rows_pad a multiple of 32.
+struct EpiSum {
+  struct Args {
+    int32_t map, rows_pad, cols;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
+                                             const EpiWarp& w, const Maps& maps) {
+    if (w.row >= a.rows_pad) return;
+    const int c0 = w.half * (p.bn >> 1);
+    for (int c = c0; c < c0 + (p.bn >> 1); c += 32) {
+      const int col = o.j * p.bn + c;
+      if (col >= a.cols) return;
+      uint32_t v[32];
+      dense::tmem_ld_x32(w.tmem + c, v);
+      dense::tmem_wait(v);
+      if (w.lane == 0) dense::box_wait_read();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *dense::box_piece(w.box, w.lane, i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0) dense::box_store(&maps.m[a.map], w.box, col, o.s * a.rows_pad + w.row);
+    }
+  }
+};
+
+// A warp's 32 features [f, f + 32) as bf16 through its box, at the box's
+// column 32 * part; the store follows when the box's last part is written
+// (64 features), or at once (alone: one part of 32).
+__device__ __forceinline__ void put_features(const uint32_t (&v)[16], const EpiWarp& w, int part) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *dense::box_piece(w.box, w.lane, 4 * part + i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+__device__ __forceinline__ void row_features(const uint32_t (&v)[16], __nv_bfloat16* row, int f, int I) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (f + 8 * i < I)
+      *reinterpret_cast<uint4*>(row + f + 8 * i) = make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+}
+
+// h = silu(g) u; D's columns: bn / 2 of the gate's, then the same features' up.
+struct EpiGate {
+  struct Args {
+    __nv_bfloat16* h;   // [T, I]
+    int32_t map, rows, inter;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
+                                             const EpiWarp& w, const Maps& maps) {
+    if (w.row >= a.rows) return;
+    const int n = p.bn >> 2;   // 64 or 32 features of this warp's half
+    const int f0 = o.j * p.b_step + w.half * n;
+    if (f0 >= a.inter) return;
+    const bool mine = w.row + w.lane < a.rows;
+    for (int part = 0; part < n / 32; ++part) {
+      uint32_t g[32], u[32], r[16];
+      dense::tmem_ld_x32(w.tmem + w.half * n + 32 * part, g);
+      dense::tmem_ld_x32(w.tmem + (p.bn >> 1) + w.half * n + 32 * part, u);
+      dense::tmem_wait(g);
+      dense::tmem_wait(u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        r[i] = dense::pack_bf16(swiglu(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i])),
+                                swiglu(__uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i + 1])));
+      if (n == 64) {
+        if (part == 0) {
+          if (w.lane == 0) dense::box_wait_read();
+          __syncwarp();
+        }
+        put_features(r, w, part);
+      } else if (mine) {
+        row_features(r, a.h + static_cast<int64_t>(w.row + w.lane) * a.inter, f0, a.inter);
+      }
+    }
+    if (n == 64) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0) dense::box_store(&maps.m[a.map], w.box, f0, w.row);
+    }
+  }
+};
+
+// h, dg and du from D (as EpiGate's) and dh.
+struct EpiGateGrad {
+  struct Args {
+    __nv_bfloat16 *h, *dgu;   // [T, I], [T, 2 I]
+    const float* dh;          // [rows rounded up to 32, ld_dh]
+    int64_t ld_dh;
+    int32_t map_h, map_dg, map_du, rows, inter;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
+                                             const EpiWarp& w, const Maps& maps) {
+    if (w.row >= a.rows) return;
+    const int n = p.bn >> 2;
+    const int f0 = o.j * p.b_step + w.half * n;
+    const bool mine = w.row + w.lane < a.rows;
+    const int64_t row = w.row + w.lane;
+    for (int part = 0; part < n / 32; ++part) {
+      const int f = f0 + 32 * part;
+      if (f >= a.inter) return;
+      uint32_t g[32], u[32], rh[16], rg[16], ru[16];
+      dense::tmem_ld_x32(w.tmem + w.half * n + 32 * part, g);
+      dense::tmem_ld_x32(w.tmem + (p.bn >> 1) + w.half * n + 32 * part, u);
+      float4 d[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        d[i] = mine && f + 4 * i < a.inter ? *reinterpret_cast<const float4*>(a.dh + row * a.ld_dh + f + 4 * i)
+                                           : make_float4(0, 0, 0, 0);
+      dense::tmem_wait(g);
+      dense::tmem_wait(u);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float d0 = i & 1 ? d[i >> 1].z : d[i >> 1].x, d1 = i & 1 ? d[i >> 1].w : d[i >> 1].y;
+        const Grads x = swiglu_grads(__uint_as_float(g[2 * i]), __uint_as_float(u[2 * i]), d0);
+        const Grads y = swiglu_grads(__uint_as_float(g[2 * i + 1]), __uint_as_float(u[2 * i + 1]), d1);
+        rh[i] = dense::pack_bf16(x.h, y.h);
+        rg[i] = dense::pack_bf16(x.dg, y.dg);
+        ru[i] = dense::pack_bf16(x.du, y.du);
+      }
+      if (mine) {
+        row_features(rh, a.h + row * a.inter, f, a.inter);
+        row_features(rg, a.dgu + row * 2 * a.inter, f, a.inter);
+        row_features(ru, a.dgu + row * 2 * a.inter + a.inter, f, a.inter);
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------- joining K's shares
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+// Four columns from column c of row r, summed over the shares in order.
+__device__ __forceinline__ float4 joined(const float* sums, int splits, int64_t share, int64_t at) {
+  float4 v = *reinterpret_cast<const float4*>(sums + at);
+  for (int s = 1; s < splits; ++s) v = add4(v, *reinterpret_cast<const float4*>(sums + s * share + at));
+  return v;
+}
+__device__ __forceinline__ uint2 pack4(float4 v) {
+  return make_uint2(dense::pack_bf16(v.x, v.y), dense::pack_bf16(v.z, v.w));
+}
+
+constexpr int kJoinThreads = 256;
+
+// h from the shares of x [Wg; Wu]^T, [splits][rows_pad][2 I].
+__global__ void __launch_bounds__(kJoinThreads)
+    join_gate_kernel(const float* sums, int splits, int64_t rows_pad, int64_t rows, int inter,
+                     __nv_bfloat16* h) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int per = inter >> 2;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t r = i / per, ld = 2 * static_cast<int64_t>(inter);
+  const int c = static_cast<int>(i - r * per) * 4;
+  const float4 g = joined(sums, splits, rows_pad * ld, r * ld + c);
+  const float4 u = joined(sums, splits, rows_pad * ld, r * ld + inter + c);
+  *reinterpret_cast<uint2*>(h + r * inter + c) =
+      pack4(make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z), swiglu(g.w, u.w)));
+}
+
+// out = base + the shares of [splits][rows_pad][cols].
+__global__ void __launch_bounds__(kJoinThreads)
+    join_out_kernel(const float* sums, int splits, int64_t rows_pad, int64_t rows, int cols,
+                    const __nv_bfloat16* base, int64_t ld_base, __nv_bfloat16* out, int64_t ld_out) {
+  griddep_wait();
+  const int per = cols >> 2;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t r = i / per;
+  const int c = static_cast<int>(i - r * per) * 4;
+  float4 v = joined(sums, splits, rows_pad * cols, r * cols + c);
+  if (base) {
+    const uint2 b = *reinterpret_cast<const uint2*>(base + r * ld_base + c);
+    const float2 lo = dense::unpack_bf16(b.x), hi = dense::unpack_bf16(b.y);
+    v = add4(v, make_float4(lo.x, lo.y, hi.x, hi.y));
+  }
+  *reinterpret_cast<uint2*>(out + r * ld_out + c) = pack4(v);
+}
+
+// h, dg, du from the shares of x [Wg; Wu]^T and of dout Wd.
+__global__ void __launch_bounds__(kJoinThreads)
+    join_grad_kernel(const float* gu, int splits_gu, const float* dh, int splits_dh, int64_t rows_pad,
+                     int64_t rows, int inter, __nv_bfloat16* h, __nv_bfloat16* dgu) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int per = inter >> 2;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+  if (i >= rows * per) return;
+  const int64_t r = i / per, ld = 2 * static_cast<int64_t>(inter);
+  const int c = static_cast<int>(i - r * per) * 4;
+  const float4 g = joined(gu, splits_gu, rows_pad * ld, r * ld + c);
+  const float4 u = joined(gu, splits_gu, rows_pad * ld, r * ld + inter + c);
+  const float4 d = joined(dh, splits_dh, rows_pad * inter, r * inter + c);
+  const Grads a = swiglu_grads(g.x, u.x, d.x), b = swiglu_grads(g.y, u.y, d.y);
+  const Grads e = swiglu_grads(g.z, u.z, d.z), f = swiglu_grads(g.w, u.w, d.w);
+  *reinterpret_cast<uint2*>(h + r * inter + c) = pack4(make_float4(a.h, b.h, e.h, f.h));
+  *reinterpret_cast<uint2*>(dgu + r * ld + c) = pack4(make_float4(a.dg, b.dg, e.dg, f.dg));
+  *reinterpret_cast<uint2*>(dgu + r * ld + inter + c) = pack4(make_float4(a.du, b.du, e.du, f.du));
+}
+
+// ------------------------------------------------------ batches of few tokens
+// Up to 32 tokens: a product is the weights streamed once from HBM.  A CTA
+// takes an equal share of the output rows, its eight warps share K; a lane
+// loads 16 bytes of a weight row (K order is free as long as both operands
+// use the same: lane t of a quad holds elements 8 t .. 8 t + 7 of each 32), and
+// mma.sync.m16n8k16 takes 16 weight rows against eight tokens, straight from
+// the registers.  The warps' sums are joined in shared memory in warp order.
+constexpr int kDecodeThreads = 256, kDecodeWarps = 8;
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 load_once(const __nv_bfloat16* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+
+struct DecodeArgs {
+  const __nv_bfloat16* w;      // [rows, K]
+  const __nv_bfloat16* in;     // [T, K], rows ld_in apart
+  const __nv_bfloat16* base;   // DOWN: added, or null
+  __nv_bfloat16* out;
+  int64_t ld_in, ld_base, ld_out;
+  int32_t tokens, units, k;    // units: features (two weight rows each), or rows
+};
+
+// MT: tiles of 16 weight rows at once; NT: of eight tokens; U: K steps of 32
+// whose loads are in flight together.
+template <bool DOWN, int MT, int NT, int U>
+__global__ void __launch_bounds__(kDecodeThreads)
+    decode_kernel(const DecodeArgs a) {
+  __shared__ float sums[kDecodeWarps][MT * NT * 4][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int K = a.k, steps = (K + 31) >> 5;
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * warp / kDecodeWarps);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (warp + 1) / kDecodeWarps);
+  const int u0 = static_cast<int>(static_cast<int64_t>(a.units) * blockIdx.x / gridDim.x);
+  const int u1 = static_cast<int>(static_cast<int64_t>(a.units) * (blockIdx.x + 1) / gridDim.x);
+  constexpr int kPer = DOWN ? 16 : 8;   // units of a tile
+  if constexpr (!DOWN) {
+    griddep_wait();
+    griddep_launch_dependents();
+  }
+  bool waited = !DOWN;
+  for (int u = u0; u < u1; u += MT * kPer) {
+    float acc[MT][NT][4] = {};
+    // lane's two weight rows of each tile (g and g + 8 of the MMA's 16)
+    const __nv_bfloat16* rows[MT][2];
+    bool on[MT][2];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int lo = u + m * kPer + g, hi = DOWN ? lo + 8 : lo;
+      on[m][0] = lo < u1;
+      on[m][1] = hi < u1;
+      rows[m][0] = a.w + static_cast<int64_t>(on[m][0] ? lo : u0) * K + 8 * t;
+      rows[m][1] = a.w + static_cast<int64_t>(on[m][1] ? (DOWN ? hi : a.units + hi) : u0) * K + 8 * t;
+    }
+    for (int s = s0; s < s1; s += U) {
+      uint4 wv[U][MT][2], xv[U][NT];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t k = static_cast<int64_t>(s + i) * 32;
+        const bool in = s + i < s1 && k + 8 * t < K;
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            wv[i][m][j] = in && on[m][j] ? load_once(rows[m][j] + k) : make_uint4(0, 0, 0, 0);
+      }
+      if (DOWN && !waited) {   // the weights are the call's inputs, h is the kernel before's
+        griddep_wait();
+        waited = true;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int64_t k = static_cast<int64_t>(s + i) * 32;
+        const bool in = s + i < s1 && k + 8 * t < K;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+          xv[i][n] = in && 8 * n + g < a.tokens
+                         ? *reinterpret_cast<const uint4*>(a.in + (8 * n + g) * a.ld_in + k + 8 * t)
+                         : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const uint4 &p = wv[i][m][0], &q = wv[i][m][1], &x = xv[i][n];
+            mma_bf16(acc[m][n], p.x, q.x, p.y, q.y, x.x, x.y);
+            mma_bf16(acc[m][n], p.z, q.z, p.w, q.w, x.z, x.w);
+          }
+    }
+    if (DOWN && !waited) {
+      griddep_wait();
+      waited = true;
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sums[warp][(m * NT + n) * 4 + i][lane] = acc[m][n][i];
+    __syncthreads();
+    // value i of (tile m, token tile n): row g + 8 (i >> 1), token 2 t + (i & 1)
+    for (int at = threadIdx.x; at < MT * NT * (DOWN ? 4 : 2) * 32; at += kDecodeThreads) {
+      const int l = at & 31, v = at >> 5;
+      const int i = DOWN ? v & 3 : v & 1, mn = DOWN ? v >> 2 : v >> 1;
+      const int n = mn % NT, m = mn / NT;
+      const int token = 8 * n + 2 * (l & 3) + (i & 1);
+      const int unit = u + m * kPer + (l >> 2) + (DOWN ? 8 * (i >> 1) : 0);
+      if (token >= a.tokens || unit >= u1) continue;
+      float x = 0.f, y = 0.f;
+#pragma unroll
+      for (int j = 0; j < kDecodeWarps; ++j) {
+        x += sums[j][mn * 4 + i][l];
+        if constexpr (!DOWN) y += sums[j][mn * 4 + i + 2][l];
+      }
+      if constexpr (DOWN) {
+        if (a.base) x += __bfloat162float(a.base[token * a.ld_base + unit]);
+        a.out[token * a.ld_out + unit] = __float2bfloat16_rn(x);
+      } else {
+        a.out[token * a.ld_out + unit] = __float2bfloat16_rn(swiglu(x, y));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <bool DOWN, int NT>
+cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
+  constexpr int MT = DOWN ? 3 : 2, U = NT == 1 ? 4 : 2;
+  const int grid = static_cast<int>(std::min<int64_t>(sms, (a.units + 7) / 8));
+  return launch_pdl(decode_kernel<DOWN, MT, NT, U>, dim3(static_cast<unsigned>(grid)),
+                    dim3(kDecodeThreads), 0, s, a);
+}
+template <bool DOWN>
+cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
+  const int nt = (a.tokens + 7) / 8;
+  return nt <= 1   ? launch_decode<DOWN, 1>(a, sms, s)
+         : nt == 2 ? launch_decode<DOWN, 2>(a, sms, s)
+                   : launch_decode<DOWN, 4>(a, sms, s);
+}
+
+// ------------------------------------------------------------------- plans
+constexpr int64_t up32(int64_t v) { return (v + 31) / 32 * 32; }
+
+struct FfnWs {
+  dense::Plan gate, down;   // forward; gate also in the backward pass
+  dense::Plan dh, dx;
+  bool split;               // gate's (and dh's) sums go through joining kernels
+  size_t h, dgu, sums, sums2, total;
+};
+
+FfnWs ffn_ws(const moe_ffn_shape* s, bool backward) {
+  const int64_t T = s->num_tokens, H = s->hidden, I = s->inter;
+  const int64_t tm = dense::cdiv(T, dense::kTile), rp = up32(T);
+  FfnWs w = {};
+  size_t at = 0;
+  auto take = [&](int64_t bytes) {
+    const size_t o = at;
+    at += ws_up(static_cast<size_t>(bytes));
+    return o;
+  };
+  w.h = take(2 * T * I);
+  if (!backward && T <= kDecodeTokens) {
+    w.total = at;
+    return w;
+  }
+  const int64_t kh = dense::cdiv(H, dense::kBK), ki = dense::cdiv(I, dense::kBK);
+  w.gate = dense::make_plan(tm, 2 * I, kh, true);
+  w.split = w.gate.splits > 1;
+  if (!backward) {
+    w.down = dense::make_plan(tm, H, ki, true);
+    const int64_t a = w.split ? 4 * w.gate.splits * rp * 2 * I : 0;
+    const int64_t b = w.down.splits > 1 ? 4 * w.down.splits * rp * H : 0;
+    w.sums = take(std::max<int64_t>(a, 0));
+    w.sums2 = take(b);
+  } else {
+    w.dgu = take(4 * T * I);
+    w.dh = dense::make_plan(tm, I, kh, w.split);
+    w.sums = take(4 * w.dh.splits * rp * I);
+    w.sums2 = take(w.split ? 4 * w.gate.splits * rp * 2 * I : 0);
+    w.dx = dense::make_plan(tm, H, dense::cdiv(2 * I, dense::kBK), false);
+  }
+  w.total = at;
+  return w;
+}
+
+int32_t check_shape(const moe_ffn_shape* s) {
+  if (!s) return entry_fail(MOE_ERR_INVALID_ARG, "shape is NULL");
+  if (s->num_tokens < 0 || s->hidden <= 0 || s->inter <= 0)
+    return entry_fail(MOE_ERR_INVALID_ARG, "num_tokens, hidden and inter must be positive, got %d, %d, %d",
+                      s->num_tokens, s->hidden, s->inter);
+  if (s->hidden % 8 || s->inter % 8)
+    return entry_fail(MOE_ERR_MISALIGNED, "hidden and inter must be multiples of 8, got %d and %d", s->hidden,
+                      s->inter);
+  if (s->num_tokens > MOE_FFN_MAX_TOKENS || s->hidden > MOE_FFN_MAX_FEATURES ||
+      s->inter > MOE_FFN_MAX_FEATURES)
+    return entry_fail(MOE_ERR_UNSUPPORTED, "at most %d tokens and %d features", MOE_FFN_MAX_TOKENS,
+                      MOE_FFN_MAX_FEATURES);
+  return MOE_OK;
+}
+
+int32_t check_matrix(const void* p, const char* name, int64_t ld, int64_t cols) {
+  if (!p) return entry_fail(MOE_ERR_INVALID_ARG, "%s is NULL", name);
+  if (ld < cols || ld >= (int64_t(1) << 31))
+    return entry_fail(MOE_ERR_INVALID_ARG, "%s: rows of %lld elements, %lld apart", name,
+                      static_cast<long long>(cols), static_cast<long long>(ld));
+  if (!ptr_aligned(p, 16) || ld % 8)
+    return entry_fail(MOE_ERR_MISALIGNED, "%s must be 16-byte aligned, its row stride a multiple of 8", name);
+  return MOE_OK;
+}
+
+int32_t check_weights(const void* w_gate_up, const void* w_down, const void* ws, size_t have, size_t need,
+                      const int32_t* status) {
+  if (!w_gate_up || !w_down) return entry_fail(MOE_ERR_INVALID_ARG, "w_gate_up or w_down is NULL");
+  if (!ptr_aligned(w_gate_up, 16) || !ptr_aligned(w_down, 16))
+    return entry_fail(MOE_ERR_MISALIGNED, "w_gate_up and w_down must be 16-byte aligned");
+  if (!status) return entry_fail(MOE_ERR_INVALID_ARG, "status is NULL");
+  if (!ptr_aligned(status, 4)) return entry_fail(MOE_ERR_MISALIGNED, "status must be 4-byte aligned");
+  if (!ws) return entry_fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  if (!ptr_aligned(ws, kWsAlign)) return entry_fail(MOE_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  if (have < need)
+    return entry_fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", have, need);
+  return MOE_OK;
+}
+
+#define MOE_TRY(call)                    \
+  do {                                   \
+    const int32_t rc_ = (call);          \
+    if (rc_ != MOE_OK) return rc_;       \
+  } while (0)
+#define MOE_CUDA(call)                                     \
+  do {                                                     \
+    const cudaError_t e_ = (call);                         \
+    if (e_ != cudaSuccess) return entry_launched(e_);      \
+  } while (0)
+
+template <class Epi>
+dense::Launch<typename Epi::Args> new_launch(int32_t* status) {
+  dense::Launch<typename Epi::Args> l = {};
+  l.status = status;
+  l.timeout_ns = kTimeoutNs;
+  return l;
+}
+
+unsigned join_blocks(int64_t rows, int64_t cols) {
+  return static_cast<unsigned>(dense::cdiv(rows * (cols / 4), kJoinThreads));
+}
+
+// Boxes of the operands: K-major rows of a tile (128 of A, bn / 2 of B), and
+// MN-major squares of 64.
+constexpr int kSquare = dense::kBK;
+
+int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const void* wgu, const void* wd,
+                    const void* base, int64_t ld_base, void* out, int64_t ld_out, uint8_t* ws,
+                    int32_t* status, int sms, cudaStream_t st) {
+  const int64_t T = s->num_tokens, H = s->hidden, I = s->inter;
+  const FfnWs w = ffn_ws(s, false);
+  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(ws + w.h);
+  if (T <= kDecodeTokens) {
+    DecodeArgs a = {static_cast<const __nv_bfloat16*>(wgu), static_cast<const __nv_bfloat16*>(x), nullptr, h,
+                    ld_x, 0, I, s->num_tokens, s->inter, s->hidden};
+    MOE_CUDA(launch_decode<false>(a, sms, st));
+    DecodeArgs b = {static_cast<const __nv_bfloat16*>(wd), h, static_cast<const __nv_bfloat16*>(base),
+                    static_cast<__nv_bfloat16*>(out), I, ld_base, ld_out, s->num_tokens, s->hidden, s->inter};
+    MOE_CUDA(launch_decode<true>(b, sms, st));
+    return MOE_OK;
+  }
+  const int64_t rp = up32(T), kh = dense::cdiv(H, dense::kBK), ki = dense::cdiv(I, dense::kBK);
+  {
+    Maps m;
+    MOE_TRY(dense::make_map(&m.m[0], x, Elem::kBf16, T, H, ld_x, dense::kBK, 128));
+    MOE_TRY(dense::make_map(&m.m[1], wgu, Elem::kBf16, 2 * I, H, H, dense::kBK, w.gate.bn / 2));
+    int pairs;
+    if (w.split) {
+      auto l = new_launch<EpiSum>(status);
+      float* sums = reinterpret_cast<float*>(ws + w.sums);
+      MOE_TRY(dense::make_map(&m.m[2], sums, Elem::kF32, w.gate.splits * rp, 2 * I, 2 * I, 32, 32));
+      l.problems = 1;
+      l.maps = 3;
+      l.p[0] = dense::make_problem(w.gate, T, 2 * I, kh, 0, false, 1, false, true);
+      l.e[0] = {2, static_cast<int32_t>(rp), static_cast<int32_t>(2 * I)};
+      MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
+      MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
+      MOE_CUDA(launch_pdl(join_gate_kernel, dim3(join_blocks(T, I)), dim3(kJoinThreads), 0, st,
+                          static_cast<const float*>(sums), static_cast<int>(w.gate.splits), rp, T,
+                          static_cast<int>(I), h));
+    } else {
+      auto l = new_launch<EpiGate>(status);
+      MOE_TRY(dense::make_map(&m.m[2], h, Elem::kBf16, T, I, I, 64, 32));
+      l.problems = 1;
+      l.maps = 3;
+      l.p[0] = dense::make_problem(w.gate, T, 2 * I, kh, 0, false, 1, false, true);
+      l.p[0].b_step = w.gate.bn / 2;   // features of a tile: gate rows of rank 0, up rows of rank 1
+      l.p[0].b_rank = static_cast<int32_t>(I);
+      l.p[0].tiles_n = static_cast<int32_t>(dense::cdiv(I, w.gate.bn / 2));
+      l.p[0].per_matrix = l.p[0].tiles_m * l.p[0].tiles_n;
+      l.e[0] = {h, 2, static_cast<int32_t>(T), static_cast<int32_t>(I)};
+      MOE_CUDA(dense::resident_pairs<EpiGate>(sms, &pairs));
+      MOE_CUDA(dense::launch<EpiGate>(m, l, pairs, st));
+    }
+  }
+  Maps m;
+  int pairs;
+  MOE_TRY(dense::make_map(&m.m[0], h, Elem::kBf16, T, I, I, dense::kBK, 128));
+  MOE_TRY(dense::make_map(&m.m[1], wd, Elem::kBf16, H, I, I, dense::kBK, w.down.bn / 2));
+  const Problem p = dense::make_problem(w.down, T, H, ki, 0, false, 1, false, true);
+  if (w.down.splits > 1) {
+    auto l = new_launch<EpiSum>(status);
+    float* sums = reinterpret_cast<float*>(ws + w.sums2);
+    MOE_TRY(dense::make_map(&m.m[2], sums, Elem::kF32, w.down.splits * rp, H, H, 32, 32));
+    l.problems = 1;
+    l.maps = 3;
+    l.p[0] = p;
+    l.e[0] = {2, static_cast<int32_t>(rp), static_cast<int32_t>(H)};
+    MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
+    MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
+    MOE_CUDA(launch_pdl(join_out_kernel, dim3(join_blocks(T, H)), dim3(kJoinThreads), 0, st,
+                        static_cast<const float*>(sums), static_cast<int>(w.down.splits), rp, T,
+                        static_cast<int>(H), static_cast<const __nv_bfloat16*>(base), ld_base,
+                        static_cast<__nv_bfloat16*>(out), ld_out));
+    return MOE_OK;
+  }
+  auto l = new_launch<EpiOut>(status);
+  MOE_TRY(dense::make_map(&m.m[2], out, Elem::kBf16, T, H, ld_out, 64, 32));
+  l.problems = 1;
+  l.maps = 3;
+  l.last = 1;
+  l.p[0] = p;
+  l.e[0] = {static_cast<const __nv_bfloat16*>(base), ld_base, 2, static_cast<int32_t>(T), static_cast<int32_t>(H)};
+  MOE_CUDA(dense::resident_pairs<EpiOut>(sms, &pairs));
+  MOE_CUDA(dense::launch<EpiOut>(m, l, pairs, st));
+  return MOE_OK;
+}
+
+int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, const void* x, int64_t ld_x,
+                     const void* wgu, const void* wd, const void* dx_base, int64_t ld_base, void* dx,
+                     int64_t ld_dx, void* dw_gate_up, void* dw_down, uint8_t* ws, int32_t* status, int sms,
+                     cudaStream_t st) {
+  const int64_t T = s->num_tokens, H = s->hidden, I = s->inter;
+  const FfnWs w = ffn_ws(s, true);
+  const int64_t rp = up32(T), kh = dense::cdiv(H, dense::kBK), ki2 = dense::cdiv(2 * I, dense::kBK);
+  const int64_t kt = dense::cdiv(T, dense::kBK);
+  __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(ws + w.h);
+  __nv_bfloat16* dgu = reinterpret_cast<__nv_bfloat16*>(ws + w.dgu);
+  float* dh = reinterpret_cast<float*>(ws + w.sums);
+  float* gu = reinterpret_cast<float*>(ws + w.sums2);
+  int pairs;
+  {
+    // dh = dout Wd (Wd [H, I] is MN-major there); with few tokens the shares of
+    // x [Wg; Wu]^T in the same launch
+    Maps m;
+    auto l = new_launch<EpiSum>(status);
+    MOE_TRY(dense::make_map(&m.m[0], dout, Elem::kBf16, T, H, ld_dout, dense::kBK, 128));
+    MOE_TRY(dense::make_map(&m.m[1], wd, Elem::kBf16, H, I, I, kSquare, kSquare));
+    MOE_TRY(dense::make_map(&m.m[2], dh, Elem::kF32, w.dh.splits * rp, I, I, 32, 32));
+    l.maps = 3;
+    l.p[0] = dense::make_problem(w.dh, T, I, kh, 0, false, 1, true, true);
+    l.e[0] = {2, static_cast<int32_t>(rp), static_cast<int32_t>(I)};
+    l.problems = 1;
+    if (w.split) {
+      MOE_TRY(dense::make_map(&m.m[3], x, Elem::kBf16, T, H, ld_x, dense::kBK, 128));
+      MOE_TRY(dense::make_map(&m.m[4], wgu, Elem::kBf16, 2 * I, H, H, dense::kBK, w.gate.bn / 2));
+      MOE_TRY(dense::make_map(&m.m[5], gu, Elem::kF32, w.gate.splits * rp, 2 * I, 2 * I, 32, 32));
+      l.maps = 6;
+      l.p[1] = dense::make_problem(w.gate, T, 2 * I, kh, 3, false, 4, false, true);
+      l.e[1] = {5, static_cast<int32_t>(rp), static_cast<int32_t>(2 * I)};
+      l.problems = 2;
+    }
+    MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
+    MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
+  }
+  if (w.split) {
+    MOE_CUDA(launch_pdl(join_grad_kernel, dim3(join_blocks(T, I)), dim3(kJoinThreads), 0, st,
+                        static_cast<const float*>(gu), static_cast<int>(w.gate.splits),
+                        static_cast<const float*>(dh), static_cast<int>(w.dh.splits), rp, T,
+                        static_cast<int>(I), h, dgu));
+  } else {
+    Maps m;
+    auto l = new_launch<EpiGateGrad>(status);
+    MOE_TRY(dense::make_map(&m.m[0], x, Elem::kBf16, T, H, ld_x, dense::kBK, 128));
+    MOE_TRY(dense::make_map(&m.m[1], wgu, Elem::kBf16, 2 * I, H, H, dense::kBK, w.gate.bn / 2));
+    l.maps = 2;
+    l.problems = 1;
+    l.p[0] = dense::make_problem(w.gate, T, 2 * I, kh, 0, false, 1, false, true);
+    l.p[0].b_step = w.gate.bn / 2;
+    l.p[0].b_rank = static_cast<int32_t>(I);
+    l.p[0].tiles_n = static_cast<int32_t>(dense::cdiv(I, w.gate.bn / 2));
+    l.p[0].per_matrix = l.p[0].tiles_m * l.p[0].tiles_n;
+    l.e[0] = {h, dgu, dh, I, 0, 0, 0, static_cast<int32_t>(T), static_cast<int32_t>(I)};
+    MOE_CUDA(dense::resident_pairs<EpiGateGrad>(sms, &pairs));
+    MOE_CUDA(dense::launch<EpiGateGrad>(m, l, pairs, st));
+  }
+  // dx = [dg du] [Wg; Wu] (the weights MN-major), and the weights' gradients,
+  // sums over the tokens (both operands MN-major), in one launch
+  Maps m;
+  auto l = new_launch<EpiOut>(status);
+  l.last = 1;
+  if (dx) {
+    const int i = l.problems++, k = l.maps;
+    l.maps += 3;
+    MOE_TRY(dense::make_map(&m.m[k], dgu, Elem::kBf16, T, 2 * I, 2 * I, dense::kBK, 128));
+    MOE_TRY(dense::make_map(&m.m[k + 1], wgu, Elem::kBf16, 2 * I, H, H, kSquare, kSquare));
+    MOE_TRY(dense::make_map(&m.m[k + 2], dx, Elem::kBf16, T, H, ld_dx, 64, 32));
+    l.p[i] = dense::make_problem(w.dx, T, H, ki2, k, false, k + 1, true, true);
+    l.e[i] = {static_cast<const __nv_bfloat16*>(dx_base), ld_base, k + 2, static_cast<int32_t>(T),
+              static_cast<int32_t>(H)};
+  }
+  if (dw_gate_up) {
+    const dense::Plan g = dense::make_plan(dense::cdiv(2 * I, dense::kTile), H, kt, false);
+    const dense::Plan d = dense::make_plan(dense::cdiv(H, dense::kTile), I, kt, false);
+    int i = l.problems++, k = l.maps;
+    l.maps += 3;
+    MOE_TRY(dense::make_map(&m.m[k], dgu, Elem::kBf16, T, 2 * I, 2 * I, kSquare, kSquare));
+    MOE_TRY(dense::make_map(&m.m[k + 1], x, Elem::kBf16, T, H, ld_x, kSquare, kSquare));
+    MOE_TRY(dense::make_map(&m.m[k + 2], dw_gate_up, Elem::kBf16, 2 * I, H, H, 64, 32));
+    l.p[i] = dense::make_problem(g, 2 * I, H, kt, k, true, k + 1, true, true);
+    l.e[i] = {nullptr, 0, k + 2, static_cast<int32_t>(2 * I), static_cast<int32_t>(H)};
+    i = l.problems++, k = l.maps;
+    l.maps += 3;
+    MOE_TRY(dense::make_map(&m.m[k], dout, Elem::kBf16, T, H, ld_dout, kSquare, kSquare));
+    MOE_TRY(dense::make_map(&m.m[k + 1], h, Elem::kBf16, T, I, I, kSquare, kSquare));
+    MOE_TRY(dense::make_map(&m.m[k + 2], dw_down, Elem::kBf16, H, I, I, 64, 32));
+    l.p[i] = dense::make_problem(d, H, I, kt, k, true, k + 1, true, true);
+    l.e[i] = {nullptr, 0, k + 2, static_cast<int32_t>(H), static_cast<int32_t>(I)};
+  }
+  MOE_CUDA(dense::resident_pairs<EpiOut>(sms, &pairs));
+  MOE_CUDA(dense::launch<EpiOut>(m, l, pairs, st));
+  return MOE_OK;
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" size_t moe_ffn_workspace_size(const moe_ffn_shape* shape, int32_t backward) {
+  using namespace moe;
+  if (check_shape(shape) != MOE_OK) return 0;
+  return std::max(ffn_ws(shape, backward != 0).total, kWsAlign);
+}
+
+extern "C" int32_t moe_ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x,
+                                   const void* w_gate_up, const void* w_down, const void* base,
+                                   int64_t ld_base, void* out, int64_t ld_out, void* workspace,
+                                   size_t workspace_bytes, int32_t* status, void* stream) {
+  using namespace moe;
+  MOE_TRY(check_shape(s));
+  if (s->num_tokens == 0) return MOE_OK;
+  MOE_TRY(check_matrix(x, "x", ld_x, s->hidden));
+  if (base) MOE_TRY(check_matrix(base, "base", ld_base, s->hidden));
+  MOE_TRY(check_matrix(out, "out", ld_out, s->hidden));
+  MOE_TRY(check_weights(w_gate_up, w_down, workspace, workspace_bytes, ffn_ws(s, false).total, status));
+  int sms = 0;
+  MOE_TRY(check_device(&sms));
+  return ffn_forward(s, x, ld_x, w_gate_up, w_down, base, ld_base, out, ld_out,
+                     static_cast<uint8_t*>(workspace), status, sms, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" int32_t moe_ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout,
+                                    const void* x, int64_t ld_x, const void* w_gate_up,
+                                    const void* w_down, const void* dx_base, int64_t ld_dx_base, void* dx,
+                                    int64_t ld_dx, void* dw_gate_up, void* dw_down, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, void* stream) {
+  using namespace moe;
+  MOE_TRY(check_shape(s));
+  if (!dw_gate_up != !dw_down)
+    return entry_fail(MOE_ERR_INVALID_ARG, "dw_gate_up and dw_down go together");
+  if (!ptr_aligned(dw_gate_up, 16) || !ptr_aligned(dw_down, 16))
+    return entry_fail(MOE_ERR_MISALIGNED, "dw_gate_up and dw_down must be 16-byte aligned");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (s->num_tokens == 0) {   // sums over no tokens
+    if (!dw_gate_up) return MOE_OK;
+    MOE_TRY(check_device(nullptr));
+    const size_t n = static_cast<size_t>(s->hidden) * s->inter * 2;
+    MOE_CUDA(cudaMemsetAsync(dw_gate_up, 0, 2 * n, st));
+    MOE_CUDA(cudaMemsetAsync(dw_down, 0, n, st));
+    return MOE_OK;
+  }
+  MOE_TRY(check_matrix(dout, "dout", ld_dout, s->hidden));
+  MOE_TRY(check_matrix(x, "x", ld_x, s->hidden));
+  if (dx_base) MOE_TRY(check_matrix(dx_base, "dx_base", ld_dx_base, s->hidden));
+  if (dx) {
+    MOE_TRY(check_matrix(dx, "dx", ld_dx, s->hidden));
+    if (dx == x || dx == dout)
+      return entry_fail(MOE_ERR_INVALID_ARG, "dx must not be the memory of x or dout");
+  }
+  MOE_TRY(check_weights(w_gate_up, w_down, workspace, workspace_bytes, ffn_ws(s, true).total, status));
+  if (!dx && !dw_gate_up) return MOE_OK;
+  int sms = 0;
+  MOE_TRY(check_device(&sms));
+  return ffn_backward(s, dout, ld_dout, x, ld_x, w_gate_up, w_down, dx_base, ld_dx_base, dx, ld_dx,
+                      dw_gate_up, dw_down, static_cast<uint8_t*>(workspace), status, sms, st);
+}

@@ -13,6 +13,7 @@
 
 #include <cuda_bf16.h>
 
+#include "cluster.cuh"
 #include "moe_internal.h"
 #include "ptx.cuh"
 
@@ -99,11 +100,6 @@ struct EpiSched {
   int item0, item_step, items_per_tile, mt_mul, mt_add;
   uint32_t release_cluster;
 };
-
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr)
-               : "memory");
-}
 
 // Top-k combine formed in GEMM2's epilogue (moe_options.fuse_combine; null
 // cnt = off).  After a warp has stored its 32 columns of y for a chunk of
