@@ -533,6 +533,57 @@ int32_t moe_ffn_backward(const moe_ffn_shape* shape, const void* dout, int64_t l
                          void* dw_gate_up, void* dw_down, void* workspace,
                          size_t workspace_bytes, int32_t* status, void* stream);
 
+/* Limits of the orthogonalised step's matrices: a side, the shorter side. */
+#define MOE_MUON_MAX_SIDE (1 << 20)
+#define MOE_MUON_MAX_SHORT 32768
+
+/* How large an orthogonalised update is made, s below: */
+#define MOE_MUON_RMS 0        /* 0.2 sqrt(max(rows, cols)): a root mean square of about 0.2 */
+#define MOE_MUON_SPECTRAL 1   /* sqrt(max(1, rows / cols)) */
+
+/* `count` matrices [rows, cols] one after another; all updated in place. */
+typedef struct {
+  float* param;        /* [count, rows, cols] */
+  const void* grad;    /* the same, of grad_dtype */
+  float* momentum;     /* the same */
+  void* param_bf16;    /* the same in bf16, receives the rounded parameters; or NULL */
+  int32_t count, rows, cols;
+  int32_t reserved;    /* must be zero */
+} moe_muon_tensor;
+
+typedef struct {
+  double lr, momentum, weight_decay, eps;
+  double coefficients[3];    /* a, b, c */
+  int32_t ns_steps;          /* 1 .. 12 */
+  int32_t nesterov;          /* 0 or 1 */
+  int32_t grad_dtype;        /* MOE_DTYPE_* */
+  int32_t update_scale;      /* MOE_MUON_* */
+  int32_t reserved[2];       /* must be zero */
+  const float* grad_scale;   /* device scalar every gradient is multiplied by, or NULL */
+} moe_muon_options;
+
+/* Workspace bytes of moe_muon_step for these tensors; 0 for invalid arguments. */
+size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count,
+                               const moe_muon_options* options);
+
+/* One step over weight matrices whose update is orthogonalised, with mu =
+ * momentum and (a, b, c) = coefficients:
+ *   m <- mu m + (1 - mu) g,  u = nesterov ? mu m + (1 - mu) g : m
+ *   X = u / (|u|_F + eps);  ns_steps times: G = X X^T, X <- a X + (b G + c G^2) X
+ *   p <- p (1 - lr wd) - lr s X,  s by update_scale
+ * each matrix by itself.  Products run on the tensor cores with numbers held as
+ * two fp16 terms (22 bits) and float sums: X is as near to the formula as 32-bit
+ * arithmetic brings it, to a small factor.  The sum of u^2 is float: |u|_F
+ * between 1e-18 and 1e18.  A NaN or infinite gradient makes its matrix NaN.
+ * Coefficients whose steps leave every bound are refused with
+ * MOE_ERR_UNSUPPORTED.
+ * `tensors` and `options` are host memory, read before the call returns: lr and
+ * the other scalars become part of the launches, and a step captured into a
+ * CUDA graph repeats them at every replay.  `status` as in moe_ffn_forward. */
+int32_t moe_muon_step(const moe_muon_tensor* tensors, int32_t count,
+                      const moe_muon_options* options, void* workspace, size_t workspace_bytes,
+                      int32_t* status, void* stream);
+
 /* Message describing the last error returned on the calling thread. */
 const char* moe_last_error(void);
 

@@ -17,9 +17,9 @@ from ._lib import (MOE_W4A8_MXFP4_FP8, MOE_W4A16_MXFP4_BF16, MOE_W8A8_MXFP8, Moe
                    load, options, prepare_weights, read_device_status, selftest_timeout, shape,
                    steps_workspace_size, workspace_layout, workspace_size)
 from ._adapt import AdamW, BalanceLoss, LowRankAdapters
-from ._dense import GatedFFN
+from ._dense import GatedFFN, Muon
 
-__all__ = ["AdamW", "BalanceLoss", "FusedMoE", "GatedFFN", "LowRankAdapters", "MoeError", "MoeOptions", "MoeShape", "WsLayout", "forward",
+__all__ = ["AdamW", "BalanceLoss", "FusedMoE", "GatedFFN", "LowRankAdapters", "MoeError", "MoeOptions", "MoeShape", "Muon", "WsLayout", "forward",
            "forward_host", "forward_host_steps", "load", "options", "prepare_weights",
            "read_device_status", "selftest_timeout", "shape", "steps_workspace_size",
            "workspace_layout", "workspace_size",

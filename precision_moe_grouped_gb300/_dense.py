@@ -157,3 +157,133 @@ class GatedFFN(_Status):
         if rc:
             check(rc)
         return dx, dw_gate_up, dw_down
+
+
+class Muon(_Status):
+    """Steps over weight matrices whose update is made (nearly) orthogonal by
+    Newton-Schulz steps on the momentum (the formulas: moe_muon_step in
+    include/moe.h).
+
+    params: contiguous float32 CUDA tensors [rows, cols], or [n, rows, cols] for
+    n matrices (a pool of adapters; a gate and an up projection as two), updated
+    in place; grads: tensors of the same shapes, all float32 or all bfloat16;
+    copies: bfloat16 tensors of the same shapes that receive the rounded
+    parameters, or None.  `state`: the momenta, float32 of the same shapes, to
+    resume from; by default they start at zero.  update_scale "rms" makes an
+    update's root mean square about 0.2 whatever the shape, "spectral" its
+    largest singular value about sqrt(max(1, rows / cols)).  The tensors are
+    bound and held here (params, grads, copies and state name them and cannot be
+    assigned): after replacing a parameter's or a gradient's memory, build a new
+    Muon (state=old.state) or pass the new gradients to step().
+
+    lr, momentum, weight_decay, eps, nesterov, ns_steps, ns_coefficients and
+    update_scale are read at every step.  They are the host's: a step captured
+    into a CUDA graph repeats the capture's at every replay."""
+
+    def __init__(self, params, grads, copies=None, state=None, lr: float = 1e-3,
+                 momentum: float = 0.95, nesterov: bool = True, weight_decay: float = 0.1,
+                 eps: float = 1e-7, ns_steps: int = 5, ns_coefficients=(3.4445, -4.7750, 2.0315),
+                 update_scale: str = "rms"):
+        _bind_torch()
+        dev = self._dev = A._device()
+        # detached: keeps the bound memory alive whatever becomes of the originals
+        bound = self._params = tuple(A._detached(params, "params"))
+        self.lr, self.momentum, self.nesterov, self.weight_decay = lr, momentum, nesterov, weight_decay
+        self.eps, self.ns_steps, self.ns_coefficients = eps, ns_steps, ns_coefficients
+        self.update_scale = update_scale
+        for i, p in enumerate(bound):
+            if p.dim() not in (2, 3):
+                _bad(f"params[{i}] must be [rows, cols] or [n, rows, cols], got {tuple(p.shape)}")
+            _int32(f"params[{i}]'s sizes", *p.shape)
+            _check_flat(p, f"params[{i}]", torch.float32, p.shape, dev)
+        if state is None:
+            state = [torch.zeros_like(p) for p in bound]
+        self._state = self._bound(state, "state", torch.float32)
+        self._copies = None if copies is None else self._bound(copies, "copies", torch.bfloat16)
+        written = [t for t in (*bound, *self._state, *(self._copies or ())) if t.numel()]
+        if len({t.data_ptr() for t in written}) < len(written):
+            _bad("params, state and copies must be distinct")   # all written, side by side
+        self._table = (_lib.MuonTensor * max(1, len(bound)))()
+        for i, (e, p, m) in enumerate(zip(self._table, bound, self._state)):
+            e.param, e.momentum = p.data_ptr(), m.data_ptr()
+            e.count = p.shape[0] if p.dim() == 3 else 1
+            e.rows, e.cols = p.shape[-2:]
+            e.param_bf16 = None if self._copies is None else self._copies[i].data_ptr()
+        self._options = _lib.MuonOptions()
+        self._lib = A.load()
+        self.bind_grads(grads)
+        self._sized = None
+        self._workspace_size()   # rejects unsupported sizes here
+        self._new_status(torch.device("cuda", dev) if dev is not None else None)
+
+    def _bound(self, tensors, name: str, dtype) -> tuple:
+        held = tuple(A._detached(tensors, name))
+        if len(held) != len(self._params):
+            _bad(f"{name} must hold {len(self._params)} tensors")
+        for i, (t, p) in enumerate(zip(held, self._params)):
+            _check_flat(t, f"{name}[{i}]", dtype, p.shape, self._dev)
+        return held
+
+    @property
+    def params(self) -> tuple:
+        return self._params
+
+    @property
+    def grads(self) -> tuple:
+        return self._grads
+
+    @property
+    def copies(self) -> tuple | None:
+        return self._copies
+
+    @property
+    def state(self) -> tuple:
+        return self._state
+
+    def bind_grads(self, grads) -> None:
+        """Take the next steps' gradients from these tensors."""
+        grads = tuple(A._detached(grads, "grads"))
+        _same_device(A._device(), self._dev)
+        kind = grads[0].dtype if grads else torch.float32
+        if kind not in (torch.float32, torch.bfloat16):
+            _bad(f"grads must be float32 or bfloat16, got {kind}")
+        self._grads = self._bound(grads, "grads", kind)
+        for e, t in zip(self._table, self._grads):
+            e.grad = t.data_ptr()
+        self._options.grad_dtype = _lib.MOE_DTYPE_F32 if kind == torch.float32 else _lib.MOE_DTYPE_BF16
+
+    def _workspace_size(self) -> int:
+        o = self._options
+        if self.update_scale not in ("rms", "spectral"):
+            _bad(f"update_scale must be 'rms' or 'spectral', got {self.update_scale!r}")
+        if len(self.ns_coefficients) != 3:
+            _bad("ns_coefficients must be three numbers")
+        _int32("ns_steps", self.ns_steps)
+        o.lr, o.momentum, o.weight_decay, o.eps = self.lr, self.momentum, self.weight_decay, self.eps
+        o.coefficients[:] = self.ns_coefficients
+        o.ns_steps, o.nesterov = self.ns_steps, bool(self.nesterov)
+        o.update_scale = _lib.MOE_MUON_RMS if self.update_scale == "rms" else _lib.MOE_MUON_SPECTRAL
+        # the sizes are bound: only what the schedule of the steps depends on can change the need
+        key = o.ns_steps, tuple(o.coefficients), o.lr, o.momentum, o.weight_decay, o.eps
+        if key != self._sized:
+            n = self._lib.moe_muon_workspace_size(self._table, len(self._params), o)
+            if n == 0:
+                raise _lib.MoeError(_lib.MOE_ERR_INVALID_ARG, self._lib.moe_last_error().decode())
+            self._sized, self._need = key, n
+        return self._need
+
+    def step(self, grads=None, grad_scale=None) -> None:
+        """One step, in place.  grad_scale: float32 CUDA scalar every gradient is
+        multiplied by."""
+        if grads is not None:
+            self.bind_grads(grads)
+        dev, o = A._device(), self._options
+        _same_device(dev, self._dev)
+        if grad_scale is not None:
+            _lib._check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
+                               device=dev)
+        o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
+        n = self._workspace_size()
+        ws = _scratch(n, self._status)
+        check(self._lib.moe_muon_step(self._table, len(self._params), o, ws.data_ptr(), n,
+                                      self._at_status, A._raw_stream(dev)))

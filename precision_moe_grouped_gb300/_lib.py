@@ -34,12 +34,15 @@ EXPORTS = ("moe_workspace_size", "moe_workspace_layout", "moe_prepare_weights", 
            "moe_version", "moe_route_noalloc", "moe_steps_workspace_size",
            "moe_forward_host_steps", "moe_adapter_workspace_size", "moe_adapter_forward",
            "moe_adapter_backward", "moe_balance_workspace_size", "moe_balance_loss",
-           "moe_adamw_step", "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward")
+           "moe_adamw_step", "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_backward",
+           "moe_muon_workspace_size", "moe_muon_step")
 
 MOE_DTYPE_BF16 = 0
 MOE_DTYPE_F32 = 1
 MOE_ADAMW_BLOCK = 256
 MOE_ADAPTER_MAX = 1024
+MOE_MUON_RMS = 0
+MOE_MUON_SPECTRAL = 1
 
 MOE_NOALLOC_SCRATCH_BYTES = 4 << 20
 
@@ -105,6 +108,18 @@ class AdamwOptions(ctypes.Structure):
 
 class FfnShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("num_tokens", "hidden", "inter")]
+
+
+class MuonTensor(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("param", "grad", "momentum", "param_bf16")] +
+                [(n, ctypes.c_int32) for n in ("count", "rows", "cols", "reserved")])
+
+
+class MuonOptions(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_double) for n in ("lr", "momentum", "weight_decay", "eps")] +
+                [("coefficients", ctypes.c_double * 3)] +
+                [(n, ctypes.c_int32) for n in ("ns_steps", "nesterov", "grad_dtype", "update_scale")] +
+                [("reserved", ctypes.c_int32 * 2), ("grad_scale", ctypes.c_void_p)])
 
 
 class MoeError(RuntimeError):
@@ -179,6 +194,11 @@ def load() -> ctypes.CDLL:
     lib.moe_ffn_backward.argtypes = ([fsh, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64] + [vp] * 3 +
                                      [sz, vp, vp])
     lib.moe_ffn_backward.restype = i32
+    mts, mop = ctypes.POINTER(MuonTensor), ctypes.POINTER(MuonOptions)
+    lib.moe_muon_workspace_size.argtypes = [mts, i32, mop]
+    lib.moe_muon_workspace_size.restype = sz
+    lib.moe_muon_step.argtypes = [mts, i32, mop, vp, sz, vp, vp]
+    lib.moe_muon_step.restype = i32
     _lib = lib
     return lib
 

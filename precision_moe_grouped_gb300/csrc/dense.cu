@@ -26,7 +26,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encoder() {
 }  // namespace
 
 int32_t make_map(CUtensorMap* m, const void* base, Elem type, int64_t rows, int64_t cols, int64_t ld,
-                 int box_cols, int box_rows) {
+                 int box_cols, int box_rows, Swizzle swizzle) {
   auto fn = encoder();
   if (!fn) return entry_fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled entry point unavailable");
   const int64_t bytes = type == Elem::kF32 ? 4 : 2;
@@ -39,7 +39,8 @@ int32_t make_map(CUtensorMap* m, const void* base, Elem type, int64_t rows, int6
                         : type == Elem::kF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                              : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                         2, const_cast<void*>(base), dims, strides, box, estr,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        swizzle == Swizzle::k128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return entry_fail(MOE_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d) rows=%lld cols=%lld ld=%lld",

@@ -151,6 +151,23 @@ __device__ __forceinline__ void mma_stage_warp(uint32_t d, uint64_t a, uint64_t 
       : "memory");
 }
 
+// The same four without a commit: one product of a stage that holds several.
+__device__ __forceinline__ void mma_quad_warp(uint32_t d, uint64_t a, uint64_t b, uint64_t a_step,
+                                              uint64_t b_step, uint32_t idesc, uint32_t acc0) {
+  asm volatile(
+      "{\n\t.reg .pred e, p, q;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, %4, %4;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %5, %6, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %7, %8, %3, q;\n\t"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %9, %10, %3, q;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc0), "l"(a + a_step), "l"(b + b_step), "l"(a + 2 * a_step),
+      "l"(b + 2 * b_step), "l"(a + 3 * a_step), "l"(b + 3 * b_step)
+      : "memory");
+}
+
 // 32 lanes x 32 columns: thread i receives lane (quarter * 32 + i).  The
 // registers hold the values only after tmem_wait().
 __device__ __forceinline__ void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
@@ -200,6 +217,14 @@ __device__ __forceinline__ void box_wait_read() {
 }
 __device__ __forceinline__ void box_wait_all() {
   asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t v) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
 }
 
 // What an epilogue warp works on: its 32 rows (first one `row`, this lane's
@@ -402,8 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Row-major [rows, cols] matrix of 2- or 4-byte elements, rows ld elements
 // apart; the box is box_cols x box_rows in the 128-byte swizzle.
 enum class Elem { kBf16, kF16, kF32 };
+enum class Swizzle { k128, k64 };
 int32_t make_map(CUtensorMap* m, const void* base, Elem type, int64_t rows, int64_t cols, int64_t ld,
-                 int box_cols, int box_rows);
+                 int box_cols, int box_rows, Swizzle swizzle = Swizzle::k128);
 
 // How a product is cut: columns of a tile, and shares of K where there are too
 // few tiles for the pairs.
@@ -459,24 +485,21 @@ inline Problem make_problem(const Plan& plan, int64_t rows, int64_t cols, int64_
   return p;
 }
 
-// Launch grid: as many CTA pairs as can be resident.  Cached per kernel and
-// device.
-template <class Epi>
-cudaError_t resident_pairs(int num_sms, int* pairs) {
-  static DeviceOnce cache;
+// Launch grid: as many CTA pairs as can be resident.  `cache` is the kernel's,
+// by device.
+template <class Kernel>
+cudaError_t resident_pairs(Kernel kern, int smem, DeviceOnce& cache, int num_sms, int* pairs) {
   cudaError_t e;
   std::atomic<int>* at = device_entry(cache, &e);
   if (!at) return e;
   int n = at->load(std::memory_order_acquire);
   if (n == 0) {
-    auto kern = dense_kernel<Epi>;
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes)) !=
-        cudaSuccess)
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess)
       return e;
     cudaLaunchConfig_t q = {};
     q.gridDim = dim3(static_cast<unsigned>(num_sms & ~1));
     q.blockDim = dim3(kThreads);
-    q.dynamicSmemBytes = kSmemBytes;
+    q.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -493,7 +516,13 @@ cudaError_t resident_pairs(int num_sms, int* pairs) {
 }
 
 template <class Epi>
-cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, cudaStream_t s) {
+cudaError_t resident_pairs(int num_sms, int* pairs) {
+  static DeviceOnce cache;
+  return resident_pairs(dense_kernel<Epi>, kSmemBytes, cache, num_sms, pairs);
+}
+
+template <class Kernel, class Args>
+cudaError_t launch(Kernel kern, int smem, const Maps& maps, Launch<Args>& l, int pairs, cudaStream_t s) {
   int tiles = 0;
   for (int i = 0; i < l.problems; ++i) {
     l.p[i].first_tile = tiles;
@@ -504,7 +533,7 @@ cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -514,7 +543,11 @@ cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, c
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, dense_kernel<Epi>, maps, l);
+  return cudaLaunchKernelEx(&cfg, kern, maps, l);
+}
+template <class Epi>
+cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, cudaStream_t s) {
+  return launch(dense_kernel<Epi>, kSmemBytes, maps, l, pairs, s);
 }
 
 }  // namespace dense

@@ -1,5 +1,5 @@
 // entry.h -- argument checking shared by the C ABI entry points that have
-// their own translation unit (adapters.cu, balance.cu, adamw.cu).
+// their own translation unit (adapters.cu, balance.cu, adamw.cu, ffn.cu, muon.cu).
 #pragma once
 
 #include <cstdarg>
@@ -33,6 +33,18 @@ inline int32_t entry_launched(cudaError_t e) {
   if (e == cudaSuccess) return MOE_OK;
   return entry_fail(MOE_ERR_CUDA, "kernel launch failed: %s", cudaGetErrorString(e));
 }
+
+// Leave an entry point with the first error.
+#define MOE_TRY(call)                    \
+  do {                                   \
+    const int32_t rc_ = (call);          \
+    if (rc_ != MOE_OK) return rc_;       \
+  } while (0)
+#define MOE_CUDA(call)                                     \
+  do {                                                     \
+    const cudaError_t e_ = (call);                         \
+    if (e_ != cudaSuccess) return entry_launched(e_);      \
+  } while (0)
 
 constexpr size_t kWsAlign = 256;
 constexpr size_t ws_up(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }

@@ -533,17 +533,6 @@ int32_t check_weights(const void* w_gate_up, const void* w_down, const void* ws,
   return MOE_OK;
 }
 
-#define MOE_TRY(call)                    \
-  do {                                   \
-    const int32_t rc_ = (call);          \
-    if (rc_ != MOE_OK) return rc_;       \
-  } while (0)
-#define MOE_CUDA(call)                                     \
-  do {                                                     \
-    const cudaError_t e_ = (call);                         \
-    if (e_ != cudaSuccess) return entry_launched(e_);      \
-  } while (0)
-
 template <class Epi>
 dense::Launch<typename Epi::Args> new_launch(int32_t* status) {
   dense::Launch<typename Epi::Args> l = {};

@@ -1,0 +1,758 @@
+// muon.cu -- one step over weight matrices whose update is made (nearly)
+// orthogonal by Newton-Schulz steps.
+//
+//   m <- mu m + (1 - mu) g,  u = mu m + (1 - mu) g (nesterov) or m
+//   X0 = u / (|u|_F + eps);  X <- a X + (b G + c G^2) X with G = X X^T, `steps` times
+//   p <- p (1 - lr wd) - lr s X
+//
+// X is taken with its short side m as rows.  All the steps' polynomials of G
+// commute, so they are carried out on m x m matrices: with P = a I + b G + c G^2
+// a step is X <- P X, G <- P G P, and three of them are X <- Q X with Q <- P Q.
+// The long side is then met twice in three steps (G = X X^T, Q X) instead of
+// twice in each, and every m x m product is symmetric and computed by half.
+// After three steps X is formed and G taken from it anew: a small singular value
+// s of X enters G as s^2 beside 1 and the steps multiply its errors by up to a^2
+// each; three of them lose as little as the plain form in 32 bits does (five
+// in one go lose up to 50 times as much for a decaying spectrum).
+//
+// Numbers between the products are two fp16 terms, hi + lo, of the value times
+// a power of two (22 bits; the powers follow from the coefficients, which
+// bound every matrix), and a product is lo hi + hi lo + hi hi (terms.cuh).
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "dense.cuh"
+#include "entry.h"
+#include "terms.cuh"
+
+namespace moe {
+namespace {
+
+using dense::Elem;
+using dense::EpiWarp;
+using dense::Maps;
+using dense::Problem;
+using dense::Tile;
+
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr int kPartSteps = 3;         // steps between two Gram matrices
+
+// ------------------------------------------------------------ elementwise
+constexpr int kThreads = 256;
+constexpr int kChunk = 16384;         // elements of a block's share
+
+struct Momentum {
+  const void* grad;
+  float* m;
+  const float* grad_scale;
+  float mu, rest;                     // mu, 1 - mu
+  int32_t bf16, nesterov;
+};
+
+__device__ __forceinline__ float grad_at(const Momentum& a, int64_t i, float gs) {
+  return gs * (a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.grad)[i])
+                      : static_cast<const float*>(a.grad)[i]);
+}
+__device__ __forceinline__ float update_of(const Momentum& a, float m, float g) {
+  return a.nesterov ? fmaf(a.mu, m, a.rest * g) : m;
+}
+
+// Sum over the block in a fixed order; every thread gets it.
+__device__ __forceinline__ float block_sum(float v, float* warp_sums) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kThreads / 32; ++i) s += warp_sums[i];
+  __syncthreads();
+  return s;
+}
+
+// The new momentum, and each chunk's sum of u^2 (matrix z, chunk c at
+// sums[z chunks + c]).
+__global__ void __launch_bounds__(kThreads)
+    muon_momentum_kernel(const Momentum a, int64_t size, int vec, float* sums) {
+  __shared__ float warp_sums[kThreads / 32];
+  griddep_wait();
+  griddep_launch_dependents();
+  const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
+  const int64_t base = static_cast<int64_t>(blockIdx.y) * size;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kChunk;
+  const int64_t i1 = i0 + kChunk < size ? i0 + kChunk : size;
+  float s = 0.f;
+  if (vec) {
+#pragma unroll 4
+    for (int64_t i = i0 + 4 * threadIdx.x; i < i1; i += 4 * kThreads) {
+      float4 m = *reinterpret_cast<const float4*>(a.m + base + i);
+      float g[4];
+      if (a.bf16) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.grad) + base + i);
+        const float2 lo = dense::unpack_bf16(v.x), hi = dense::unpack_bf16(v.y);
+        g[0] = lo.x, g[1] = lo.y, g[2] = hi.x, g[3] = hi.y;
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + base + i);
+        g[0] = v.x, g[1] = v.y, g[2] = v.z, g[3] = v.w;
+      }
+      float* e = &m.x;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float gk = gs * g[k];
+        e[k] = fmaf(a.mu, e[k], a.rest * gk);
+        const float u = update_of(a, e[k], gk);
+        s = fmaf(u, u, s);
+      }
+      *reinterpret_cast<float4*>(a.m + base + i) = m;
+    }
+  } else {
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
+      const float g = grad_at(a, base + i, gs);
+      const float m = fmaf(a.mu, a.m[base + i], a.rest * g);
+      a.m[base + i] = m;
+      const float u = update_of(a, m, g);
+      s = fmaf(u, u, s);
+    }
+  }
+  s = block_sum(s, warp_sums);
+  if (threadIdx.x == 0) sums[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = s;
+}
+
+// X0's planes: hi and lo fp16 terms of scale * u / (|u| + eps), [mp][np] per
+// matrix with zeros beyond m x n; a tall matrix [n, m] is turned on the way.
+constexpr int kSide = 64;
+__global__ void __launch_bounds__(kThreads)
+    muon_planes_kernel(const Momentum a, int rows, int cols, const float* sums, int chunks, float eps,
+                       float scale, __half* planes, int64_t lo_off, int mp, int np) {
+  __shared__ float warp_sums[kThreads / 32];
+  __shared__ float tile[kSide][kSide + 1];
+  griddep_wait();
+  griddep_launch_dependents();
+  const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
+  const int z = blockIdx.z;
+  float s = 0.f;
+  for (int i = threadIdx.x; i < chunks; i += kThreads) s += sums[static_cast<int64_t>(z) * chunks + i];
+  s = block_sum(s, warp_sums);
+  const float mul = scale / (sqrtf(s) + eps);
+  const bool tall = rows > cols;
+  const int64_t base = static_cast<int64_t>(z) * rows * cols;
+  // the source's square: rows r0.., columns c0..
+  const int r0 = (tall ? blockIdx.x : blockIdx.y) * kSide, c0 = (tall ? blockIdx.y : blockIdx.x) * kSide;
+  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
+#pragma unroll 4
+  for (int i = ty; i < kSide; i += 4) {
+    float v = 0.f;
+    if (r0 + i < rows && c0 + tx < cols) {
+      const int64_t at = base + static_cast<int64_t>(r0 + i) * cols + c0 + tx;
+      v = update_of(a, a.m[at], grad_at(a, at, gs)) * mul;
+    }
+    if (tall) tile[tx][i] = v;
+    else tile[i][tx] = v;
+  }
+  __syncthreads();
+  const int64_t out = (static_cast<int64_t>(z) * mp + blockIdx.y * kSide) * np + blockIdx.x * kSide;
+  const int px = (threadIdx.x & 31) * 2, py = threadIdx.x >> 5;
+#pragma unroll 4
+  for (int i = py; i < kSide; i += 8) {
+    const float x = tile[i][px], y = tile[i][px + 1];
+    const __half2 hi = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(hi);
+    *reinterpret_cast<__half2*>(planes + out + static_cast<int64_t>(i) * np + px) = hi;
+    *reinterpret_cast<__half2*>(planes + lo_off + out + static_cast<int64_t>(i) * np + px) =
+        __floats2half2_rn(x - f.x, y - f.y);
+  }
+}
+
+// -------------------------------------------------------------- epilogues
+// A matrix as planes: v = c D + b G + a I, times `scale`, as hi and lo terms.
+// Symmetric ones (upper): squares of 64 above the diagonal are stored twice, the
+// ones below not at all, so that every element has one writer.
+struct EpiPlanes {
+  struct Args {
+    const __half* g;       // G's planes, or null
+    __half* out;           // [2][batch][rows][cols]
+    int64_t lo;            // elements from a hi plane to its lo plane (G's and out's)
+    float c, b, a, scale;  // b includes 1 / G's scale, c that of D
+    int32_t map;           // stores of 32 x 32
+    int32_t lo_rows;       // rows from the hi to the lo plane
+    int32_t m, rows, cols; // rows of I; stored rows (a multiple of 64) and columns
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
+                                             const EpiWarp& w, const Maps& maps, float (&d)[128]) {
+    if (w.row >= a.rows) return;
+    const int r = w.row + w.lane;
+    const int64_t matrix = static_cast<int64_t>(o.z) * a.rows;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      const int col = o.j * p.bn + w.half * (p.bn >> 1) + c;
+      const int side = p.upper ? (col >> 6) - (w.row >> 6) : 0;
+      if (c >= (p.bn >> 1) || col >= a.cols || side < 0) continue;
+      const int64_t at = (matrix + r) * a.cols + col;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (a.g) {
+          const uint4 h = *reinterpret_cast<const uint4*>(a.g + at + 8 * i);
+          const uint4 l = *reinterpret_cast<const uint4*>(a.g + a.lo + at + 8 * i);
+          const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = dense::unpack_f16(hh[k]), y = dense::unpack_f16(ll[k]);
+            d[c + 8 * i + 2 * k] = fmaf(a.c, d[c + 8 * i + 2 * k], a.b * (x.x + y.x));
+            d[c + 8 * i + 2 * k + 1] = fmaf(a.c, d[c + 8 * i + 2 * k + 1], a.b * (x.y + y.y));
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) d[c + 8 * i + k] *= a.c;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (r == col + 8 * i + k && r < a.m) d[c + 8 * i + k] += a.a;
+          d[c + 8 * i + k] *= a.scale;
+        }
+      }
+      if (w.lane == 0) dense::box_wait_read();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float x = d[c + 8 * i + 2 * k], y = d[c + 8 * i + 2 * k + 1];
+          hi[k] = dense::pack_f16(x, y);
+          const float2 f = dense::unpack_f16(hi[k]);
+          lo[k] = dense::pack_f16(x - f.x, y - f.y);
+          if (side > 0) {   // turned: a warp writes 64 bytes of each of its columns
+            __half* to = a.out + (matrix + col + 8 * i + 2 * k) * a.cols + r;
+            const __half2 h2 = *reinterpret_cast<const __half2*>(&hi[k]);
+            const __half2 l2 = *reinterpret_cast<const __half2*>(&lo[k]);
+            to[0] = __low2half(h2);
+            to[a.cols] = __high2half(h2);
+            to[a.lo] = __low2half(l2);
+            to[a.lo + a.cols] = __high2half(l2);
+          }
+        }
+        *piece(w.box, w.lane, i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *piece(w.box + kHalfBox, w.lane, i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0) {
+        const int row = static_cast<int>(matrix) + w.row;
+        dense::box_store(&maps.m[a.map], w.box, col, row);
+        dense::box_store(&maps.m[a.map], w.box + kHalfBox, col, row + a.lo_rows);
+      }
+    }
+  }
+  // 32 rows of 64 bytes in the 64-byte swizzle
+  static constexpr int kHalfBox = dense::kStageBox / 2;
+  static __device__ __forceinline__ uint4* piece(uint8_t* box, int row, int i) {
+    return reinterpret_cast<uint4*>(box + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
+  }
+};
+
+// p <- decay p - step D, and the copy.  D's rows run along p's contiguous side
+// (element (r, c) of D at p[c rows + r]), so that a warp's 32 rows are 128 bytes.
+struct EpiUpdate {
+  struct Args {
+    float* p;
+    __nv_bfloat16* copy;   // or null
+    float decay, step;
+    int32_t rows, cols;
+  };
+  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
+                                             const EpiWarp& w, const Maps&, float (&d)[128]) {
+    const int r = w.row + w.lane;
+    if (r >= a.rows) return;
+    const int64_t base = static_cast<int64_t>(o.z) * a.rows * a.cols + r;
+#pragma unroll
+    for (int c = 0; c < 128; c += 16) {
+      const int col = o.j * p.bn + w.half * (p.bn >> 1) + c;
+      if (c >= (p.bn >> 1) || col >= a.cols) continue;
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        v[i] = col + i < a.cols ? a.p[base + static_cast<int64_t>(col + i) * a.rows] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        if (col + i < a.cols) {
+          const int64_t at = base + static_cast<int64_t>(col + i) * a.rows;
+          const float x = fmaf(-a.step, d[c + i], a.decay * v[i]);
+          a.p[at] = x;
+          if (a.copy) a.copy[at] = __float2bfloat16_rn(x);
+        }
+      }
+    }
+  }
+};
+
+// ------------------------------------------------------------------- plans
+// Bounds of every matrix of a schedule, from the polynomials on a grid over the
+// singular values (all at most 1 at first, as |X0|_F is), and the powers of two
+// that bring each to at most 2^14: fp16 then holds it with room for the grid's
+// and the arithmetic's errors.
+constexpr int kMaxSteps = 12;
+struct StepScales {
+  float g, p, q, s;   // of G and P of the step, of Q after it, of S = P G
+};
+struct Scales {
+  StepScales step[kMaxSteps];
+  float x[kMaxSteps + 1];   // of X before each part, [parts]: after the last (unused)
+};
+
+bool power_for(double bound, float* out) {
+  if (!(bound < 1e6)) return false;   // NaN too
+  int e;
+  std::frexp(std::max(bound, 1e-6), &e);   // bound < 2^e
+  *out = std::ldexp(1.0f, 14 - e);
+  return true;
+}
+
+bool make_scales(const moe_muon_options* o, Scales* out) {
+  constexpr int kGrid = 512;
+  const double a = o->coefficients[0], b = o->coefficients[1], c = o->coefficients[2];
+  double top = 1.0;
+  int part = 0;
+  for (int done = 0; done < o->ns_steps; done += kPartSteps, ++part) {
+    const int n = std::min(kPartSteps, o->ns_steps - done);
+    double mg[kPartSteps] = {}, mp[kPartSteps] = {}, mq[kPartSteps] = {}, ms[kPartSteps] = {}, mx = 0;
+    for (int i = 0; i <= kGrid; ++i) {
+      const double s = top * i / kGrid;
+      double g = s * s, q = 1;
+      for (int k = 0; k < n; ++k) {
+        const double p = a + b * g + c * g * g;
+        q *= p;
+        mg[k] = std::max(mg[k], std::fabs(g));
+        mp[k] = std::max(mp[k], std::fabs(p));
+        mq[k] = std::max(mq[k], std::fabs(q));
+        ms[k] = std::max(ms[k], std::fabs(p * g));
+        g = p * p * g;
+      }
+      mx = std::max(mx, std::fabs(q * s));
+    }
+    if (!power_for(top, &out->x[part])) return false;
+    for (int k = 0; k < n; ++k) {
+      StepScales& t = out->step[done + k];
+      if (!power_for(mg[k], &t.g) || !power_for(mp[k], &t.p) || !power_for(mq[k], &t.q) ||
+          !power_for(ms[k], &t.s))
+        return false;
+    }
+    if (!(mx < 1e3)) return false;
+    top = std::max(mx, 1e-3);
+  }
+  return true;
+}
+
+// One group: the tensors whose matrices are m x n (or n x m).
+struct Shape {
+  int32_t m, n, mp, np;
+  int64_t batch;
+};
+Shape shape_of(const moe_muon_tensor& t) {
+  Shape s;
+  s.m = std::min(t.rows, t.cols);
+  s.n = std::max(t.rows, t.cols);
+  s.mp = (s.m + 63) / 64 * 64;
+  s.np = (s.n + 63) / 64 * 64;
+  s.batch = 0;
+  return s;
+}
+bool empty(const moe_muon_tensor& t) { return t.count == 0 || t.rows == 0 || t.cols == 0; }
+bool same(const moe_muon_tensor& t, const Shape& s) {
+  return !empty(t) && std::min(t.rows, t.cols) == s.m && std::max(t.rows, t.cols) == s.n;
+}
+int chunks_of(const Shape& s) {
+  return static_cast<int>(dense::cdiv(static_cast<int64_t>(s.m) * s.n, kChunk));
+}
+
+struct GroupWs {
+  size_t sums, x, x1, g, s, p, qa, qb, total;
+};
+GroupWs group_ws(const Shape& s) {
+  GroupWs w = {};
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += ws_up(bytes);
+    return o;
+  };
+  const size_t big = 4ull * s.batch * s.mp * s.np, small = 4ull * s.batch * s.mp * s.mp;
+  w.sums = take(4ull * s.batch * chunks_of(s));
+  w.x = take(big);
+  w.x1 = take(big);
+  w.g = take(small);
+  w.s = take(small);
+  w.p = take(small);
+  w.qa = take(small);
+  w.qb = take(small);
+  w.total = at;
+  return w;
+}
+
+// What the launches of one group share.
+struct Group {
+  const moe_muon_tensor* t;
+  int32_t count;
+  const moe_muon_options* o;
+  Shape s;
+  uint8_t* ws;
+  GroupWs w;
+  Scales sc;
+  int32_t* status;
+  cudaStream_t st;
+  int pairs_planes, pairs_update;
+};
+
+// A symmetric-operand product of m x m planes: D = A B, both [mp, mp] and read
+// K-major (either is its own transpose).
+struct Planes {
+  __half* at;
+  float scale;
+};
+
+dense::Plan square_plan(const Shape& s, int64_t tiles_of_256, int64_t tiles_of_128) {
+  dense::Plan p;
+  p.bn = 2 * dense::cdiv(tiles_of_256 * s.batch, dense::kPlanPairs) <=
+                 dense::cdiv(tiles_of_128 * s.batch, dense::kPlanPairs)
+             ? 256
+             : 128;
+  p.splits = 1;
+  p.kb_split = 0;
+  return p;
+}
+
+// Tiles of the upper triangle (row i from column i * 256 / bn on).
+int64_t upper_tiles(int64_t mp, int bn) {
+  const int64_t rows = dense::cdiv(mp, dense::kTile), cols = dense::cdiv(mp, bn), per = dense::kTile / bn;
+  int64_t n = 0;
+  for (int64_t i = 0; i < rows; ++i) n += std::max<int64_t>(0, cols - i * per);
+  return n;
+}
+
+// Where the second terms are, beside the first ones' rows.
+void two_terms(Problem& p, int64_t lo_rows) {
+  p.a_off[1] = static_cast<int32_t>(p.a_off[0] + lo_rows);
+  p.b_off[1] = static_cast<int32_t>(p.b_off[0] + lo_rows);
+}
+
+// Adds out = c A B^T + b G + a I (symmetric, planes [mp][mp]) to a launch; A and
+// B are [mp][ld] K-major planes over k columns.
+int32_t add_symmetric(const Group& gr, Maps* m, dense::Launch<EpiPlanes::Args>* l, Planes a, Planes b,
+                      int64_t ld, Planes out, float c, const Planes* g, float gb, float ga) {
+  const Shape& s = gr.s;
+  const int64_t lo_rows = s.batch * s.mp;
+  const dense::Plan plan = square_plan(s, upper_tiles(s.mp, 256), upper_tiles(s.mp, 128));
+  const int i = l->problems++, k = l->maps;
+  l->maps += 3;
+  MOE_TRY(dense::make_map(&m->m[k], a.at, Elem::kF16, 2 * lo_rows, ld, ld, dense::kBK, 128));
+  MOE_TRY(dense::make_map(&m->m[k + 1], b.at, Elem::kF16, 2 * lo_rows, ld, ld, dense::kBK, plan.bn / 2));
+  MOE_TRY(dense::make_map(&m->m[k + 2], out.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, 32, 32,
+                          dense::Swizzle::k64));
+  Problem& p = l->p[i];
+  p = dense::make_problem(plan, s.mp, s.mp, ld / dense::kBK, k, false, k + 1, false, false);
+  p.kb_split = p.kb;
+  p.upper = 1;
+  p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp, plan.bn));
+  p.batch = static_cast<int32_t>(s.batch);
+  p.a_batch = p.b_batch = s.mp;
+  two_terms(p, lo_rows);
+  EpiPlanes::Args& e = l->e[i];
+  e.g = g ? g->at : nullptr;
+  e.out = out.at;
+  e.lo = lo_rows * s.mp;
+  e.c = c / (a.scale * b.scale);
+  e.b = g ? gb / g->scale : 0.f;
+  e.a = ga;
+  e.scale = out.scale;
+  e.map = k + 2;
+  e.lo_rows = static_cast<int32_t>(lo_rows);
+  e.m = s.m;
+  e.rows = e.cols = s.mp;
+  return MOE_OK;
+}
+
+template <class Epi>
+dense::Launch<typename Epi::Args> new_launch(const Group& g) {
+  dense::Launch<typename Epi::Args> l = {};
+  l.status = g.status;
+  l.timeout_ns = kTimeoutNs;
+  return l;
+}
+
+int32_t symmetric(const Group& gr, Planes a, Planes b, int64_t ld, Planes out, float c, const Planes* g,
+                  float gb, float ga) {
+  Maps m;
+  auto l = new_launch<EpiPlanes>(gr);
+  MOE_TRY(add_symmetric(gr, &m, &l, a, b, ld, out, c, g, gb, ga));
+  MOE_CUDA(terms::launch<EpiPlanes>(m, l, gr.pairs_planes, gr.st));
+  return MOE_OK;
+}
+
+// X1 = Q X as planes.
+int32_t apply(const Group& gr, Planes q, Planes x, Planes out) {
+  const Shape& s = gr.s;
+  const int64_t lo_rows = s.batch * s.mp;
+  dense::Plan plan = dense::make_plan(dense::cdiv(s.mp, dense::kTile) * s.batch, s.np, 1, false);
+  plan.kb_split = s.mp / dense::kBK;
+  Maps m;
+  auto l = new_launch<EpiPlanes>(gr);
+  MOE_TRY(dense::make_map(&m.m[0], q.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, dense::kBK, 128));
+  MOE_TRY(dense::make_map(&m.m[1], x.at, Elem::kF16, 2 * lo_rows, s.np, s.np, dense::kBK, dense::kBK));
+  MOE_TRY(dense::make_map(&m.m[2], out.at, Elem::kF16, 2 * lo_rows, s.np, s.np, 32, 32,
+                          dense::Swizzle::k64));
+  l.maps = 3;
+  l.problems = 1;
+  Problem& p = l.p[0];
+  p = dense::make_problem(plan, s.mp, s.np, s.mp / dense::kBK, 0, false, 1, true, false);
+  p.batch = static_cast<int32_t>(s.batch);
+  p.a_batch = p.b_batch = s.mp;
+  two_terms(p, lo_rows);
+  EpiPlanes::Args& e = l.e[0];
+  e = {};
+  e.c = 1.0f / (q.scale * x.scale);
+  e.scale = out.scale;
+  e.out = out.at;
+  e.lo = lo_rows * s.np;
+  e.map = 2;
+  e.lo_rows = static_cast<int32_t>(lo_rows);
+  e.rows = s.mp;
+  e.cols = s.np;
+  MOE_CUDA(terms::launch<EpiPlanes>(m, l, gr.pairs_planes, gr.st));
+  return MOE_OK;
+}
+
+// p <- decay p - lr s Q X for the group's tensors, up to four a launch.
+int32_t update(const Group& gr, Planes q, Planes x) {
+  const Shape& s = gr.s;
+  const int64_t lo_rows = s.batch * s.mp;
+  const dense::Plan by_n = dense::make_plan(dense::cdiv(s.n, dense::kTile) * s.batch, s.m, 1, false);
+  const dense::Plan by_m = dense::make_plan(dense::cdiv(s.m, dense::kTile) * s.batch, s.n, 1, false);
+  Maps m;
+  auto l = new_launch<EpiUpdate>(gr);
+  // Q as A and as B, X likewise: all K = m long, X MN-major
+  MOE_TRY(dense::make_map(&m.m[0], q.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, dense::kBK, 128));
+  MOE_TRY(dense::make_map(&m.m[1], q.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, dense::kBK, by_n.bn / 2));
+  MOE_TRY(dense::make_map(&m.m[2], x.at, Elem::kF16, 2 * lo_rows, s.np, s.np, dense::kBK, dense::kBK));
+  l.maps = 3;
+  int64_t z = 0;
+  for (int i = 0; i < gr.count; ++i) {
+    const moe_muon_tensor& t = gr.t[i];
+    if (!same(t, s)) continue;
+    const bool tall = t.rows > t.cols;
+    dense::Plan plan = tall ? by_m : by_n;
+    plan.kb_split = s.mp / dense::kBK;
+    Problem& p = l.p[l.problems];
+    EpiUpdate::Args& e = l.e[l.problems];
+    if (tall) p = dense::make_problem(plan, s.m, s.n, s.mp / dense::kBK, 0, false, 2, true, false);
+    else p = dense::make_problem(plan, s.n, s.m, s.mp / dense::kBK, 2, true, 1, false, false);
+    p.batch = t.count;
+    p.a_batch = p.b_batch = s.mp;
+    p.a_off[0] = p.b_off[0] = static_cast<int32_t>(z * s.mp);
+    two_terms(p, lo_rows);
+    const double size = gr.o->update_scale == MOE_MUON_RMS
+                            ? 0.2 * std::sqrt(static_cast<double>(std::max(t.rows, t.cols)))
+                            : std::sqrt(std::max(1.0, static_cast<double>(t.rows) / t.cols));
+    e.p = t.param;
+    e.copy = static_cast<__nv_bfloat16*>(t.param_bf16);
+    e.decay = static_cast<float>(1.0 - gr.o->lr * gr.o->weight_decay);
+    e.step = static_cast<float>(gr.o->lr * size / (static_cast<double>(q.scale) * x.scale));
+    e.rows = tall ? s.m : s.n;
+    e.cols = tall ? s.n : s.m;
+    z += t.count;
+    if (++l.problems == dense::kMaxProblems) {
+      MOE_CUDA(terms::launch<EpiUpdate>(m, l, gr.pairs_update, gr.st));
+      l.problems = 0;
+    }
+  }
+  if (l.problems) MOE_CUDA(terms::launch<EpiUpdate>(m, l, gr.pairs_update, gr.st));
+  return MOE_OK;
+}
+
+int32_t run_group(const Group& gr) {
+  const Shape& s = gr.s;
+  const int64_t lo = s.batch * s.mp;
+  float* sums = reinterpret_cast<float*>(gr.ws + gr.w.sums);
+  auto planes = [&](size_t off) { return reinterpret_cast<__half*>(gr.ws + off); };
+  const int chunks = chunks_of(s);
+  const int64_t size = static_cast<int64_t>(s.m) * s.n;
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t z = 0;
+    for (int i = 0; i < gr.count; ++i) {
+      const moe_muon_tensor& t = gr.t[i];
+      if (!same(t, s)) continue;
+      const bool bf16 = gr.o->grad_dtype == MOE_DTYPE_BF16;
+      const Momentum a = {t.grad, t.momentum, gr.o->grad_scale, static_cast<float>(gr.o->momentum),
+                          static_cast<float>(1.0 - gr.o->momentum), bf16, gr.o->nesterov};
+      const int vec = size % 4 == 0 && ptr_aligned(t.momentum, 16) && ptr_aligned(t.grad, bf16 ? 8 : 16);
+      // a launch's matrices are at most 65535 blocks in y or z
+      for (int at = 0; at < t.count; at += 65535) {
+        const int n = std::min(t.count - at, 65535);
+        Momentum b = a;
+        b.m += at * size;
+        b.grad = static_cast<const uint8_t*>(a.grad) + at * size * (bf16 ? 2 : 4);
+        if (pass == 0) {
+          MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, gr.st, b, size, vec,
+                              sums + (z + at) * chunks));
+        } else {
+          MOE_CUDA(launch_pdl(muon_planes_kernel, dim3(s.np / kSide, s.mp / kSide, n), dim3(kThreads), 0, gr.st,
+                              b, t.rows, t.cols, static_cast<const float*>(sums + (z + at) * chunks), chunks,
+                              static_cast<float>(gr.o->eps), gr.sc.x[0],
+                              planes(gr.w.x) + (z + at) * s.mp * s.np, lo * s.np, s.mp, s.np));
+        }
+      }
+      z += t.count;
+    }
+  }
+  const float ca = static_cast<float>(gr.o->coefficients[0]), cb = static_cast<float>(gr.o->coefficients[1]),
+              cc = static_cast<float>(gr.o->coefficients[2]);
+  Planes x = {planes(gr.w.x), gr.sc.x[0]};
+  int part = 0;
+  for (int done = 0; done < gr.o->ns_steps; done += kPartSteps, ++part) {
+    const int n = std::min(kPartSteps, gr.o->ns_steps - done);
+    const StepScales* sc = gr.sc.step + done;
+    Planes g = {planes(gr.w.g), sc[0].g}, q = {nullptr, 0};
+    MOE_TRY(symmetric(gr, x, x, s.np, g, 1.0f, nullptr, 0.f, 0.f));
+    for (int k = 0; k < n; ++k) {
+      const bool last = k == n - 1;
+      const Planes p = {planes(k == 0 ? gr.w.qa : gr.w.p), sc[k].p};
+      MOE_TRY(symmetric(gr, g, g, s.mp, p, cc, &g, cb, ca));
+      const Planes sp = {planes(gr.w.s), sc[k].s};
+      Maps m;
+      auto l = new_launch<EpiPlanes>(gr);
+      if (!last) MOE_TRY(add_symmetric(gr, &m, &l, p, g, s.mp, sp, 1.0f, nullptr, 0.f, 0.f));
+      if (k == 0) {
+        q = p;
+      } else {
+        const Planes next = {planes(k & 1 ? gr.w.qb : gr.w.qa), sc[k].q};
+        MOE_TRY(add_symmetric(gr, &m, &l, p, q, s.mp, next, 1.0f, nullptr, 0.f, 0.f));
+        q = next;
+      }
+      if (l.problems) MOE_CUDA(terms::launch<EpiPlanes>(m, l, gr.pairs_planes, gr.st));
+      if (!last) {
+        g.scale = sc[k + 1].g;
+        MOE_TRY(symmetric(gr, sp, p, s.mp, g, 1.0f, nullptr, 0.f, 0.f));
+      }
+    }
+    if (done + n < gr.o->ns_steps) {
+      const Planes next = {planes(x.at == planes(gr.w.x) ? gr.w.x1 : gr.w.x), gr.sc.x[part + 1]};
+      MOE_TRY(apply(gr, q, x, next));
+      x = next;
+    } else {
+      MOE_TRY(update(gr, q, x));
+    }
+  }
+  return MOE_OK;
+}
+
+int32_t check_tensor(const moe_muon_tensor& t, int i, bool bf16) {
+  if (t.count < 0 || t.rows < 0 || t.cols < 0)
+    return entry_fail(MOE_ERR_INVALID_ARG, "tensor %d: a negative size", i);
+  if (t.reserved) return entry_fail(MOE_ERR_INVALID_ARG, "tensor %d: reserved must be zero", i);
+  if (empty(t)) return MOE_OK;
+  if (!t.param || !t.grad || !t.momentum)
+    return entry_fail(MOE_ERR_INVALID_ARG, "tensor %d: param, grad or momentum is NULL", i);
+  if (t.rows > MOE_MUON_MAX_SIDE || t.cols > MOE_MUON_MAX_SIDE || std::min(t.rows, t.cols) > MOE_MUON_MAX_SHORT)
+    return entry_fail(MOE_ERR_UNSUPPORTED, "tensor %d: sides of at most %d, the shorter at most %d", i,
+                      MOE_MUON_MAX_SIDE, MOE_MUON_MAX_SHORT);
+  if (!ptr_aligned(t.param, 4) || !ptr_aligned(t.grad, bf16 ? 2 : 4) || !ptr_aligned(t.momentum, 4) ||
+      !ptr_aligned(t.param_bf16, 2))
+    return entry_fail(MOE_ERR_MISALIGNED, "tensor %d: a pointer is not aligned to its type", i);
+  return MOE_OK;
+}
+
+int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_options* o, Scales* sc) {
+  if (!o) return entry_fail(MOE_ERR_INVALID_ARG, "options is NULL");
+  if (count < 0) return entry_fail(MOE_ERR_INVALID_ARG, "count < 0");
+  if (count > 0 && !t) return entry_fail(MOE_ERR_INVALID_ARG, "tensors is NULL");
+  if (o->grad_dtype != MOE_DTYPE_F32 && o->grad_dtype != MOE_DTYPE_BF16)
+    return entry_fail(MOE_ERR_INVALID_ARG, "grad_dtype %d unknown", o->grad_dtype);
+  if (o->update_scale != MOE_MUON_RMS && o->update_scale != MOE_MUON_SPECTRAL)
+    return entry_fail(MOE_ERR_INVALID_ARG, "update_scale %d unknown", o->update_scale);
+  if (!(o->momentum >= 0 && o->momentum < 1))
+    return entry_fail(MOE_ERR_INVALID_ARG, "momentum must be in [0, 1)");
+  if (!(o->eps > 0) || !std::isfinite(o->eps) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay))
+    return entry_fail(MOE_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite, eps > 0");
+  if (o->ns_steps < 1 || o->ns_steps > kMaxSteps)
+    return entry_fail(MOE_ERR_INVALID_ARG, "ns_steps must be in [1, %d]", kMaxSteps);
+  if (o->reserved[0] || o->reserved[1]) return entry_fail(MOE_ERR_INVALID_ARG, "reserved must be zero");
+  if (!ptr_aligned(o->grad_scale, 4))
+    return entry_fail(MOE_ERR_MISALIGNED, "grad_scale must be 4-byte aligned");
+  if (!make_scales(o, sc))
+    return entry_fail(MOE_ERR_UNSUPPORTED, "the Newton-Schulz steps of these coefficients grow without bound");
+  for (int i = 0; i < count; ++i) MOE_TRY(check_tensor(t[i], i, o->grad_dtype == MOE_DTYPE_BF16));
+  return MOE_OK;
+}
+
+// Calls f with the shape (and matrices) of each group, in the order of their
+// first tensors; stops at the first error.
+template <class F>
+int32_t each_group(const moe_muon_tensor* t, int32_t count, F f) {
+  for (int i = 0; i < count; ++i) {
+    if (empty(t[i])) continue;
+    Shape s = shape_of(t[i]);
+    bool seen = false;
+    for (int j = 0; j < i && !seen; ++j) seen = same(t[j], s);
+    if (seen) continue;
+    for (int j = i; j < count; ++j)
+      if (same(t[j], s)) s.batch += t[j].count;
+    MOE_TRY(f(s));
+  }
+  return MOE_OK;
+}
+
+int32_t total_ws(const moe_muon_tensor* t, int32_t count, size_t* need) {
+  *need = kWsAlign;
+  return each_group(t, count, [&](const Shape& s) -> int32_t {
+    if (2 * s.batch * s.mp >= (int64_t(1) << 31) || s.batch * dense::cdiv(s.mp, 128) * dense::cdiv(s.np, 128) >= (int64_t(1) << 31))
+      return entry_fail(MOE_ERR_UNSUPPORTED, "too many matrices of %d x %d", s.m, s.n);
+    *need = std::max(*need, group_ws(s).total);
+    return MOE_OK;
+  });
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count,
+                                          const moe_muon_options* options) {
+  using namespace moe;
+  Scales sc;
+  size_t need;
+  if (check_call(tensors, count, options, &sc) != MOE_OK || total_ws(tensors, count, &need) != MOE_OK) return 0;
+  return need;
+}
+
+extern "C" int32_t moe_muon_step(const moe_muon_tensor* tensors, int32_t count, const moe_muon_options* o,
+                                 void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
+  using namespace moe;
+  Group g = {};
+  size_t need;
+  MOE_TRY(check_call(tensors, count, o, &g.sc));
+  MOE_TRY(total_ws(tensors, count, &need));
+  bool any = false;
+  for (int i = 0; i < count; ++i) any = any || !empty(tensors[i]);
+  if (!any) return MOE_OK;
+  if (!status) return entry_fail(MOE_ERR_INVALID_ARG, "status is NULL");
+  if (!ptr_aligned(status, 4)) return entry_fail(MOE_ERR_MISALIGNED, "status must be 4-byte aligned");
+  if (!workspace) return entry_fail(MOE_ERR_INVALID_ARG, "workspace is NULL");
+  if (!ptr_aligned(workspace, kWsAlign))
+    return entry_fail(MOE_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  if (workspace_bytes < need)
+    return entry_fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+  int sms = 0;
+  MOE_TRY(check_device(&sms));
+  MOE_CUDA(terms::resident_pairs<EpiPlanes>(sms, &g.pairs_planes));
+  MOE_CUDA(terms::resident_pairs<EpiUpdate>(sms, &g.pairs_update));
+  g.t = tensors;
+  g.count = count;
+  g.o = o;
+  g.ws = static_cast<uint8_t*>(workspace);
+  g.status = status;
+  g.st = static_cast<cudaStream_t>(stream);
+  return each_group(tensors, count, [&](const Shape& s) -> int32_t {
+    g.s = s;
+    g.w = group_ws(s);
+    return run_group(g);
+  });
+}

@@ -1,0 +1,264 @@
+// terms.cuh -- dense products of matrices held as two fp16 terms, on CTA pairs:
+// D = (A_hi + A_lo)(B_hi + B_lo) without A_lo B_lo, in float.
+//
+// dense.cuh's tiles, tile list and operand majors; what differs:
+// - A stage holds both terms of both operands for a K block of 64 (64 KB a CTA
+//   at BN = 256, three stages) and feeds three products, so that each term
+//   is loaded once.
+// - An MMA aligns its 16 products and the accumulator to the largest of them
+//   and cuts each off at 24 bits: a long sum of squares shrinks by about n 2^-25
+//   of itself.  So sums run in pieces of two K blocks, which alternate between
+//   the two accumulators; the epilogue warps add the pieces up in registers
+//   (rounded to nearest) while the next one runs.
+//   Noise of 333 x 1001 through five steps is 1.7e-5 off (4.2e-5 without
+//   pieces), 16 x 7168 1.0e-6 (3.9e-5); plain 32-bit arithmetic 2.6e-6, 0.8e-6.
+#pragma once
+
+#include "dense.cuh"
+
+namespace moe {
+namespace terms {
+
+using dense::EpiWarp;
+using dense::kABytes;
+using dense::kBBytes;
+using dense::kBK;
+using dense::kEpiWarp0;
+using dense::kNumEpiWarps;
+using dense::kStageBox;
+using dense::kThreads;
+using dense::kTile;
+using dense::Launch;
+using dense::Maps;
+using dense::Problem;
+using dense::Tile;
+
+constexpr int kStages = 3;
+constexpr int kPiece = 2;     // K blocks of a piece
+constexpr int kStageBytes = 2 * (kABytes + kBBytes);   // A hi, A lo, B hi, B lo
+constexpr int kOffStage = kStages * kStageBytes;
+constexpr int kOffBar = kOffStage + kNumEpiWarps * kStageBox;
+constexpr int kOffMisc = kOffBar + 8 * (2 * kStages + 4 + 1);
+constexpr int kSmemBytes = kOffMisc + 16 + 1024;
+static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
+
+// Epi: struct Args; static run(args, problem, tile, warp, maps, sums): the
+// warp's row (lane) and its half of the tile's columns, bn / 2 of sums[128].
+// Problem: one segment, a_off[0] and a_off[1] the rows of the hi and lo terms.
+template <class Epi>
+__global__ void __launch_bounds__(kThreads, 1)
+    terms_kernel(const __grid_constant__ Maps maps,
+                 const __grid_constant__ Launch<typename Epi::Args> l) {
+  extern __shared__ uint8_t smem_raw[];
+  // the same offset in both CTAs, which the pair's descriptors rely on
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
+  uint64_t* empty = full + kStages;
+  uint64_t* tfull = empty + kStages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
+  volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc + 4);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full + s, 1);
+      mbar_init(empty + s, 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(tfull + a, 1);
+      mbar_init(tempty + a, 2 * kNumEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  if (warp == 2 && lane < l.maps) prefetch_tmap(&maps.m[lane]);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_wait();
+  if (!l.last) griddep_launch_dependents();
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ producer
+    const uint32_t full0 = cluster_addr(full, 0);
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+    uint32_t stage = 0, phase = 0;
+    bool ok = true, issued = false;
+    for (int t = pair; ok && t < l.tiles; t += pairs) {
+      const Tile o = dense::find_tile(l, t);
+      const Problem& p = l.p[o.p];
+      const CUtensorMap *am = &maps.m[p.a_map[0]], *bm = &maps.m[p.b_map[0]];
+      const int a_mn0 = o.i * kTile + static_cast<int>(rank) * 128;
+      const int b_mn0 = o.j * p.b_step + static_cast<int>(rank) * p.b_rank;
+      const uint32_t bytes = 4u * static_cast<uint32_t>(kABytes + p.bn * 64);
+      for (int kb = 0; kb < p.kb; ++kb) {
+        if (!mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          uint8_t* as = smem + stage * kStageBytes;
+          uint8_t* bs = as + 2 * kABytes;
+          const uint32_t bar = full0 + 8 * stage;
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int ar = p.a_off[h] + o.z * p.a_batch, br = p.b_off[h] + o.z * p.b_batch;
+            if (p.a_mn) {
+              tma_load_2d_pair(as, am, a_mn0, kb * kBK + ar, bar);
+              tma_load_2d_pair(as + 8192, am, a_mn0 + 64, kb * kBK + ar, bar);
+            } else {
+              tma_load_2d_pair(as, am, kb * kBK, a_mn0 + ar, bar);
+            }
+            if (p.b_mn) {
+              tma_load_2d_pair(bs, bm, b_mn0, kb * kBK + br, bar);
+              if (p.bn == 256) tma_load_2d_pair(bs + 8192, bm, b_mn0 + 64, kb * kBK + br, bar);
+            } else {
+              tma_load_2d_pair(bs, bm, kb * kBK, b_mn0 + br, bar);
+            }
+            as += kABytes;
+            bs += kBBytes;
+          }
+        }
+        issued = true;
+        if (++stage == kStages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    // rank 0: every copy of both CTAs has landed before either may leave
+    if (rank == 0 && issued) {
+      int32_t none = 0;
+      for (int s = 0; s < kStages; ++s) {
+        const uint32_t par = s < static_cast<int>(stage) ? phase : phase ^ 1u;
+        mbar_wait_warp(full + s, par, l.timeout_ns, l.status, kDevTimeout, &none);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (rank == 0) {
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      int piece = 0;
+      for (int t = pair; ok && t < l.tiles; t += pairs) {
+        const Tile o = dense::find_tile(l, t);
+        const Problem& p = l.p[o.p];
+        const uint64_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
+        const uint64_t ad0 = smem_desc(smem_u32(smem), p.a_mn ? 8192 : 0, 1024, 2);
+        const uint64_t bd0 = smem_desc(smem_u32(smem) + 2 * kABytes, p.b_mn ? 8192 : 0, 1024, 2);
+        const uint32_t idesc = static_cast<uint32_t>(p.idesc);
+        for (int kb = 0; ok && kb < p.kb; kb += kPiece, ++piece) {
+          const int acc = piece & 1, n = min(kPiece, p.kb - kb);
+          if (!mbar_wait_warp(tempty + acc, static_cast<uint32_t>((piece >> 1) & 1) ^ 1u, l.timeout_ns,
+                              l.status, kDevTimeout, abort_flag)) {
+            ok = false;
+            break;
+          }
+          asm volatile("fence.acq_rel.cluster;" ::: "memory");
+          tc_fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+          for (int k = 0; k < n; ++k) {
+            if (!mbar_wait_warp(full + stage, phase, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t a = ad0 + stage * (kStageBytes >> 4), b = bd0 + stage * (kStageBytes >> 4);
+            // the small products first: they lose nothing to a sum that is still small
+            dense::mma_quad_warp(d, a + (kABytes >> 4), b, a_step, b_step, idesc, k > 0 ? 1u : 0u);
+            dense::mma_quad_warp(d, a, b + (kBBytes >> 4), a_step, b_step, idesc, 1u);
+            dense::mma_quad_warp(d, a, b, a_step, b_step, idesc, 1u);
+            tc2_commit_both_warp(empty + stage);
+            if (++stage == kStages) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+          if (ok) tc2_commit_both_warp(tfull + acc);
+        }
+      }
+      tc2_commit_local_warp(drain);
+      int32_t none = 0;
+      mbar_wait_warp(drain, 0, l.timeout_ns, l.status, kDevTimeout, &none);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ------------------------------------------------------------ epilogue
+    const int e = warp - kEpiWarp0, quarter = warp & 3;
+    const uint32_t release = cluster_addr(tempty, 0);
+    EpiWarp w;
+    w.box = smem + kOffStage + e * kStageBox;
+    w.half = e >> 2;
+    w.lane = lane;
+    w.tmem = 0;
+    int piece = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < l.tiles; t += pairs) {
+      const Tile o = dense::find_tile(l, t);
+      const Problem& p = l.p[o.p];
+      float sums[128];
+#pragma unroll
+      for (int i = 0; i < 128; ++i) sums[i] = 0.f;
+      for (int kb = 0; kb < p.kb; kb += kPiece, ++piece) {
+        const int acc = piece & 1;
+        if (!mbar_wait_warp(tfull + acc, static_cast<uint32_t>((piece >> 1) & 1), l.timeout_ns, l.status,
+                            kDevTimeout, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t at = tmem + static_cast<uint32_t>(acc * 256 + w.half * (p.bn >> 1)) +
+                            (static_cast<uint32_t>(32 * quarter) << 16);
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          if (c < (p.bn >> 1)) {
+            uint32_t v[32];
+            dense::tmem_ld_x32(at + c, v);
+            dense::tmem_wait(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sums[c + i] += __uint_as_float(v[i]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(release + static_cast<uint32_t>(8 * acc));
+      }
+      if (!ok) break;
+      w.row = o.i * kTile + static_cast<int>(rank) * 128 + 32 * quarter;
+      Epi::run(l.e[o.p], p, o, w, maps, sums);
+    }
+    if (lane == 0) dense::box_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // Neither CTA leaves while the other may still use its memory: rank 0 has
+  // drained its MMAs and every copy of both CTAs.
+  cluster_sync_all();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <class Epi>
+cudaError_t resident_pairs(int num_sms, int* pairs) {
+  static DeviceOnce cache;
+  return dense::resident_pairs(terms_kernel<Epi>, kSmemBytes, cache, num_sms, pairs);
+}
+template <class Epi>
+cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, cudaStream_t s) {
+  return dense::launch(terms_kernel<Epi>, kSmemBytes, maps, l, pairs, s);
+}
+
+}  // namespace terms
+}  // namespace moe
