@@ -33,7 +33,7 @@ namespace dense {
 constexpr int kTile = 256;     // rows of a tile (128 per CTA)
 constexpr int kBK = 64;        // K elements of a stage: one 128-byte swizzle row
 constexpr int kStages = 6;
-constexpr int kMaxMaps = 10;
+constexpr int kMaxMaps = 16;
 constexpr int kMaxProblems = 4;
 constexpr int kMaxSegments = 3;
 constexpr int kThreads = 384;
@@ -96,7 +96,7 @@ __device__ __forceinline__ Tile find_tile(const L& l, int t) {
 #pragma unroll
   for (int q = 1; q < kMaxProblems; ++q)
     if (q < l.problems && t >= l.p[q].first_tile) o.p = q;
-  const Problem& p = l.p[o.p];
+  const auto& p = l.p[o.p];
   t -= p.first_tile;
   const int zs = t / p.per_matrix;
   t -= zs * p.per_matrix;
@@ -521,8 +521,8 @@ cudaError_t resident_pairs(int num_sms, int* pairs) {
   return resident_pairs(dense_kernel<Epi>, kSmemBytes, cache, num_sms, pairs);
 }
 
-template <class Kernel, class Args>
-cudaError_t launch(Kernel kern, int smem, const Maps& maps, Launch<Args>& l, int pairs, cudaStream_t s) {
+template <class Kernel, class L>
+cudaError_t launch(Kernel kern, int smem, const Maps& maps, L& l, int pairs, cudaStream_t s) {
   int tiles = 0;
   for (int i = 0; i < l.problems; ++i) {
     l.p[i].first_tile = tiles;

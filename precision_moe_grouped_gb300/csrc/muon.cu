@@ -8,6 +8,8 @@
 // X is taken with its short side m as rows.  All the steps' polynomials of G
 // commute, so they are carried out on m x m matrices: with P = a I + b G + c G^2
 // a step is X <- P X, G <- P G P, and three of them are X <- Q X with Q <- P Q.
+// (P is formed as c G (G + (b / c) I) + a I: the sum in brackets differs from G
+// on the diagonal alone, so G's diagonal blocks are kept a second time.)
 // The long side is then met twice in three steps (G = X X^T, Q X) instead of
 // twice in each, and every m x m product is symmetric and computed by half.
 // After three steps X is formed and G taken from it anew: a small singular value
@@ -33,7 +35,6 @@ namespace {
 using dense::Elem;
 using dense::EpiWarp;
 using dense::Maps;
-using dense::Problem;
 using dense::Tile;
 
 constexpr uint64_t kTimeoutNs = 1000000000ull;
@@ -166,89 +167,70 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // -------------------------------------------------------------- epilogues
-// A matrix as planes: v = c D + b G + a I, times `scale`, as hi and lo terms.
-// Symmetric ones (upper): squares of 64 above the diagonal are stored twice, the
-// ones below not at all, so that every element has one writer.
+// A matrix as planes, hi and lo terms of v = c D + a I.  A symmetric one is
+// computed and stored by its 256 x 256 blocks on and above the diagonal; with
+// map_diag the diagonal blocks go there a second time, as v + h I.
 struct EpiPlanes {
   struct Args {
-    const __half* g;       // G's planes, or null
-    __half* out;           // [2][batch][rows][cols]
-    int64_t lo;            // elements from a hi plane to its lo plane (G's and out's)
-    float c, b, a, scale;  // b includes 1 / G's scale, c that of D
-    int32_t map;           // stores of 32 x 32
-    int32_t lo_rows;       // rows from the hi to the lo plane
-    int32_t m, rows, cols; // rows of I; stored rows (a multiple of 64) and columns
+    float c, a, h;
+    int32_t map, map_diag;   // stores of 32 x 32; 0: none
+    int32_t lo_rows;         // rows from the hi to the lo plane
+    int32_t m, rows, cols;   // rows of I; stored rows (a multiple of 64) and columns
   };
-  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
-                                             const EpiWarp& w, const Maps& maps, float (&d)[128]) {
+  static __device__ __forceinline__ void ahead(const Args&, const Tile&, int, int, const EpiWarp&) {}
+  static __device__ __forceinline__ void run(const Args& a, int bn, const Tile& o, const EpiWarp& w,
+                                             const Maps& maps, float (&d)[128]) {
     if (w.row >= a.rows) return;
-    const int r = w.row + w.lane;
-    const int64_t matrix = static_cast<int64_t>(o.z) * a.rows;
+    const int row = o.z * a.rows + w.row;
 #pragma unroll
     for (int c = 0; c < 128; c += 32) {
-      const int col = o.j * p.bn + w.half * (p.bn >> 1) + c;
-      const int side = p.upper ? (col >> 6) - (w.row >> 6) : 0;
-      if (c >= (p.bn >> 1) || col >= a.cols || side < 0) continue;
-      const int64_t at = (matrix + r) * a.cols + col;
+      const int col = o.j * bn + w.half * (bn >> 1) + c;
+      if (c >= (bn >> 1) || col >= a.cols) continue;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (a.g) {
-          const uint4 h = *reinterpret_cast<const uint4*>(a.g + at + 8 * i);
-          const uint4 l = *reinterpret_cast<const uint4*>(a.g + a.lo + at + 8 * i);
-          const uint32_t hh[4] = {h.x, h.y, h.z, h.w}, ll[4] = {l.x, l.y, l.z, l.w};
+      for (int i = 0; i < 32; ++i) d[c + i] *= a.c;
+      const int on = w.row + w.lane - col;   // this row's place on the diagonal
+      const bool diag = col == w.row;        // (both are multiples of 32)
+      if (diag && w.row + w.lane < a.m) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 x = dense::unpack_f16(hh[k]), y = dense::unpack_f16(ll[k]);
-            d[c + 8 * i + 2 * k] = fmaf(a.c, d[c + 8 * i + 2 * k], a.b * (x.x + y.x));
-            d[c + 8 * i + 2 * k + 1] = fmaf(a.c, d[c + 8 * i + 2 * k + 1], a.b * (x.y + y.y));
-          }
-        } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) d[c + 8 * i + k] *= a.c;
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (r == col + 8 * i + k && r < a.m) d[c + 8 * i + k] += a.a;
-          d[c + 8 * i + k] *= a.scale;
-        }
+        for (int i = 0; i < 32; ++i) d[c + i] += on == i ? a.a : 0.f;
       }
-      if (w.lane == 0) dense::box_wait_read();
-      __syncwarp();
+      store(d, c, w, maps.m[a.map], col, row, a.lo_rows);
+      if (a.map_diag && (col >> 8) == o.i) {
+        if (diag && w.row + w.lane < a.m) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t hi[4], lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float x = d[c + 8 * i + 2 * k], y = d[c + 8 * i + 2 * k + 1];
-          hi[k] = dense::pack_f16(x, y);
-          const float2 f = dense::unpack_f16(hi[k]);
-          lo[k] = dense::pack_f16(x - f.x, y - f.y);
-          if (side > 0) {   // turned: a warp writes 64 bytes of each of its columns
-            __half* to = a.out + (matrix + col + 8 * i + 2 * k) * a.cols + r;
-            const __half2 h2 = *reinterpret_cast<const __half2*>(&hi[k]);
-            const __half2 l2 = *reinterpret_cast<const __half2*>(&lo[k]);
-            to[0] = __low2half(h2);
-            to[a.cols] = __high2half(h2);
-            to[a.lo] = __low2half(l2);
-            to[a.lo + a.cols] = __high2half(l2);
-          }
+          for (int i = 0; i < 32; ++i) d[c + i] += on == i ? a.h : 0.f;
         }
-        *piece(w.box, w.lane, i) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        *piece(w.box + kHalfBox, w.lane, i) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (w.lane == 0) {
-        const int row = static_cast<int>(matrix) + w.row;
-        dense::box_store(&maps.m[a.map], w.box, col, row);
-        dense::box_store(&maps.m[a.map], w.box + kHalfBox, col, row + a.lo_rows);
+        store(d, c, w, maps.m[a.map_diag], col & 255, row, a.lo_rows);
       }
     }
   }
-  // 32 rows of 64 bytes in the 64-byte swizzle
-  static constexpr int kHalfBox = dense::kStageBox / 2;
-  static __device__ __forceinline__ uint4* piece(uint8_t* box, int row, int i) {
-    return reinterpret_cast<uint4*>(box + row * 64 + ((i ^ ((row >> 1) & 3)) << 4));
+  // 32 columns through the warp's box: two halves of 32 rows of 64 bytes, in the
+  // 64-byte swizzle
+  static __device__ __forceinline__ void store(const float (&d)[128], int c, const EpiWarp& w,
+                                               const CUtensorMap& m, int col, int row, int lo_rows) {
+    constexpr int kHalf = dense::kStageBox / 2;
+    if (w.lane == 0) dense::box_wait_read();
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float x = d[c + 8 * i + 2 * k], y = d[c + 8 * i + 2 * k + 1];
+        hi[k] = dense::pack_f16(x, y);
+        const float2 f = dense::unpack_f16(hi[k]);
+        lo[k] = dense::pack_f16(x - f.x, y - f.y);
+      }
+      uint8_t* at = w.box + w.lane * 64 + ((i ^ ((w.lane >> 1) & 3)) << 4);
+      *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(at + kHalf) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (w.lane == 0) {
+      dense::box_store(&m, w.box, col, row);
+      dense::box_store(&m, w.box + kHalf, col, row + lo_rows);
+    }
   }
 };
 
@@ -261,15 +243,26 @@ struct EpiUpdate {
     float decay, step;
     int32_t rows, cols;
   };
-  static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
-                                             const EpiWarp& w, const Maps&, float (&d)[128]) {
+  // p's lines into L2 while the products run: a lane's are 128 bytes apart
+  static __device__ __forceinline__ void ahead(const Args& a, const Tile& o, int bn, int row,
+                                               const EpiWarp& w) {
+    if (row >= a.rows) return;
+    const int64_t base = static_cast<int64_t>(o.z) * a.rows * a.cols + row;
+    for (int c = w.lane; c < (bn >> 1); c += 32) {
+      const int col = o.j * bn + w.half * (bn >> 1) + c;
+      if (col < a.cols)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.p + base + static_cast<int64_t>(col) * a.rows));
+    }
+  }
+  static __device__ __forceinline__ void run(const Args& a, int bn, const Tile& o, const EpiWarp& w,
+                                             const Maps&, float (&d)[128]) {
     const int r = w.row + w.lane;
     if (r >= a.rows) return;
     const int64_t base = static_cast<int64_t>(o.z) * a.rows * a.cols + r;
 #pragma unroll
     for (int c = 0; c < 128; c += 16) {
-      const int col = o.j * p.bn + w.half * (p.bn >> 1) + c;
-      if (c >= (p.bn >> 1) || col >= a.cols) continue;
+      const int col = o.j * bn + w.half * (bn >> 1) + c;
+      if (c >= (bn >> 1) || col >= a.cols) continue;
       float v[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i)
@@ -334,7 +327,7 @@ bool make_scales(const moe_muon_options* o, Scales* out) {
     if (!power_for(top, &out->x[part])) return false;
     for (int k = 0; k < n; ++k) {
       StepScales& t = out->step[done + k];
-      if (!power_for(mg[k], &t.g) || !power_for(mp[k], &t.p) || !power_for(mq[k], &t.q) ||
+      if (!power_for(mg[k] + std::fabs(b / c), &t.g) || !power_for(mp[k], &t.p) || !power_for(mq[k], &t.q) ||
           !power_for(ms[k], &t.s))
         return false;
     }
@@ -367,7 +360,7 @@ int chunks_of(const Shape& s) {
 }
 
 struct GroupWs {
-  size_t sums, x, x1, g, s, p, qa, qb, total;
+  size_t sums, x, x1, g, h, s, p, qa, qb, total;
 };
 GroupWs group_ws(const Shape& s) {
   GroupWs w = {};
@@ -382,6 +375,7 @@ GroupWs group_ws(const Shape& s) {
   w.x = take(big);
   w.x1 = take(big);
   w.g = take(small);
+  w.h = take(4ull * s.batch * s.mp * dense::kTile);
   w.s = take(small);
   w.p = take(small);
   w.qa = take(small);
@@ -404,25 +398,16 @@ struct Group {
   int pairs_planes, pairs_update;
 };
 
-// A symmetric-operand product of m x m planes: D = A B, both [mp, mp] and read
-// K-major (either is its own transpose).
+// A matrix [rows of the batch][ld] as planes, times `scale`.
 struct Planes {
   __half* at;
   float scale;
+  int32_t ld;
+  bool sym;
+  __half* diag;   // G's diagonal blocks + (b / c) I, or null
 };
 
-dense::Plan square_plan(const Shape& s, int64_t tiles_of_256, int64_t tiles_of_128) {
-  dense::Plan p;
-  p.bn = 2 * dense::cdiv(tiles_of_256 * s.batch, dense::kPlanPairs) <=
-                 dense::cdiv(tiles_of_128 * s.batch, dense::kPlanPairs)
-             ? 256
-             : 128;
-  p.splits = 1;
-  p.kb_split = 0;
-  return p;
-}
-
-// Tiles of the upper triangle (row i from column i * 256 / bn on).
+// Tiles on and above the diagonal's 256 x 256 blocks.
 int64_t upper_tiles(int64_t mp, int bn) {
   const int64_t rows = dense::cdiv(mp, dense::kTile), cols = dense::cdiv(mp, bn), per = dense::kTile / bn;
   int64_t n = 0;
@@ -430,142 +415,153 @@ int64_t upper_tiles(int64_t mp, int bn) {
   return n;
 }
 
-// Where the second terms are, beside the first ones' rows.
-void two_terms(Problem& p, int64_t lo_rows) {
-  p.a_off[1] = static_cast<int32_t>(p.a_off[0] + lo_rows);
-  p.b_off[1] = static_cast<int32_t>(p.b_off[0] + lo_rows);
+// 128 columns a tile take about 0.7 of the time of 256.
+int pick_bn(int64_t tiles_of_256, int64_t tiles_of_128) {
+  return 10 * dense::cdiv(tiles_of_256, dense::kPlanPairs) <= 7 * dense::cdiv(tiles_of_128, dense::kPlanPairs) ? 256
+                                                                                                         : 128;
 }
 
-// Adds out = c A B^T + b G + a I (symmetric, planes [mp][mp]) to a launch; A and
-// B are [mp][ld] K-major planes over k columns.
-int32_t add_symmetric(const Group& gr, Maps* m, dense::Launch<EpiPlanes::Args>* l, Planes a, Planes b,
-                      int64_t ld, Planes out, float c, const Planes* g, float gb, float ga) {
-  const Shape& s = gr.s;
-  const int64_t lo_rows = s.batch * s.mp;
-  const dense::Plan plan = square_plan(s, upper_tiles(s.mp, 256), upper_tiles(s.mp, 128));
-  const int i = l->problems++, k = l->maps;
-  l->maps += 3;
-  MOE_TRY(dense::make_map(&m->m[k], a.at, Elem::kF16, 2 * lo_rows, ld, ld, dense::kBK, 128));
-  MOE_TRY(dense::make_map(&m->m[k + 1], b.at, Elem::kF16, 2 * lo_rows, ld, ld, dense::kBK, plan.bn / 2));
-  MOE_TRY(dense::make_map(&m->m[k + 2], out.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, 32, 32,
-                          dense::Swizzle::k64));
-  Problem& p = l->p[i];
-  p = dense::make_problem(plan, s.mp, s.mp, ld / dense::kBK, k, false, k + 1, false, false);
-  p.kb_split = p.kb;
+// A launch in the making: problems of one bn.
+template <class Epi>
+struct Build {
+  const Group& g;
+  Maps m;
+  terms::Launch<typename Epi::Args> l;
+  int bn;
+
+  Build(const Group& gr, int n) : g(gr), l{}, bn(n) {
+    l.status = gr.status;
+    l.timeout_ns = kTimeoutNs;
+    l.maps = 1;   // map 0 stands for none
+    m.m[0] = CUtensorMap{};
+  }
+  int64_t rows() const { return g.s.batch * g.s.mp; }
+
+  int32_t map(const __half* at, int64_t cols, int box_cols, int box_rows, dense::Swizzle sw, int32_t* index) {
+    *index = l.maps++;
+    return dense::make_map(&m.m[*index], at, Elem::kF16, 2 * rows(), cols, cols, box_cols, box_rows, sw);
+  }
+  // The operand as rows of a tile (half_rows of them in each CTA), or, with mn,
+  // as its transpose; from matrix z on.
+  int32_t operand(const Planes& p, int half_rows, bool mn, int64_t z, terms::Operand* o) {
+    *o = {};
+    o->hi = static_cast<int32_t>(z * g.s.mp);
+    o->lo = static_cast<int32_t>(rows() + z * g.s.mp);
+    o->batch = g.s.mp;
+    o->mn = mn;
+    o->sym = p.sym;
+    if (!mn) MOE_TRY(map(p.at, p.ld, dense::kBK, half_rows, dense::Swizzle::k128, &o->map));
+    if (mn || p.sym) MOE_TRY(map(p.at, p.ld, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->map_mn));
+    if (p.diag) MOE_TRY(map(p.diag, dense::kTile, dense::kBK, half_rows, dense::Swizzle::k128, &o->diag));
+    return MOE_OK;
+  }
+  terms::Problem& problem(int64_t tile_rows, int64_t tile_cols, int64_t batch, int64_t kb) {
+    terms::Problem& p = l.p[l.problems++];
+    p.bn = bn;
+    p.tiles_m = static_cast<int32_t>(dense::cdiv(tile_rows, dense::kTile));
+    p.tiles_n = static_cast<int32_t>(dense::cdiv(tile_cols, bn));
+    p.per_matrix = p.tiles_m * p.tiles_n;
+    p.batch = static_cast<int32_t>(batch);
+    p.splits = 1;
+    p.kb = p.kb_split = static_cast<int32_t>(kb);
+    return p;
+  }
+};
+
+using BuildPlanes = Build<EpiPlanes>;
+
+int square_bn(const Group& g) {
+  return pick_bn(upper_tiles(g.s.mp, 256) * g.s.batch, upper_tiles(g.s.mp, 128) * g.s.batch);
+}
+
+// out = c A B^T + a I, symmetric [mp, mp]; A and B [mp, k], B's second copy of the
+// diagonal blocks used when use_diag.
+int32_t add_symmetric(BuildPlanes& b, const Planes& x, Planes y, bool use_diag, const Planes& out, float c,
+                      float a, float ratio) {
+  const Shape& s = b.g.s;
+  if (!use_diag) y.diag = nullptr;
+  Planes left = x;
+  left.diag = nullptr;
+  terms::Problem& p = b.problem(s.mp, s.mp, s.batch, x.ld / dense::kBK);
   p.upper = 1;
-  p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp, plan.bn));
-  p.batch = static_cast<int32_t>(s.batch);
-  p.a_batch = p.b_batch = s.mp;
-  two_terms(p, lo_rows);
-  EpiPlanes::Args& e = l->e[i];
-  e.g = g ? g->at : nullptr;
-  e.out = out.at;
-  e.lo = lo_rows * s.mp;
-  e.c = c / (a.scale * b.scale);
-  e.b = g ? gb / g->scale : 0.f;
-  e.a = ga;
-  e.scale = out.scale;
-  e.map = k + 2;
-  e.lo_rows = static_cast<int32_t>(lo_rows);
+  p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp, b.bn));
+  MOE_TRY(b.operand(left, 128, false, 0, &p.a));
+  MOE_TRY(b.operand(y, b.bn / 2, false, 0, &p.b));
+  EpiPlanes::Args& e = b.l.e[b.l.problems - 1];
+  e = {};
+  e.c = c * out.scale / (x.scale * y.scale);
+  e.a = a * out.scale;
+  MOE_TRY(b.map(out.at, s.mp, 32, 32, dense::Swizzle::k64, &e.map));
+  if (out.diag) {
+    MOE_TRY(b.map(out.diag, dense::kTile, 32, 32, dense::Swizzle::k64, &e.map_diag));
+    e.h = ratio * out.scale;
+  }
+  e.lo_rows = static_cast<int32_t>(b.rows());
   e.m = s.m;
   e.rows = e.cols = s.mp;
   return MOE_OK;
 }
 
-template <class Epi>
-dense::Launch<typename Epi::Args> new_launch(const Group& g) {
-  dense::Launch<typename Epi::Args> l = {};
-  l.status = g.status;
-  l.timeout_ns = kTimeoutNs;
-  return l;
+int32_t run(BuildPlanes& b) {
+  MOE_CUDA(terms::launch<EpiPlanes>(b.m, b.l, b.g.pairs_planes, b.g.st));
+  return MOE_OK;
 }
 
-int32_t symmetric(const Group& gr, Planes a, Planes b, int64_t ld, Planes out, float c, const Planes* g,
-                  float gb, float ga) {
-  Maps m;
-  auto l = new_launch<EpiPlanes>(gr);
-  MOE_TRY(add_symmetric(gr, &m, &l, a, b, ld, out, c, g, gb, ga));
-  MOE_CUDA(terms::launch<EpiPlanes>(m, l, gr.pairs_planes, gr.st));
-  return MOE_OK;
+int32_t symmetric(const Group& gr, const Planes& x, const Planes& y, bool use_diag, const Planes& out, float c,
+                  float a, float ratio) {
+  BuildPlanes b(gr, square_bn(gr));
+  MOE_TRY(add_symmetric(b, x, y, use_diag, out, c, a, ratio));
+  return run(b);
 }
 
 // X1 = Q X as planes.
-int32_t apply(const Group& gr, Planes q, Planes x, Planes out) {
+int32_t apply(const Group& gr, const Planes& q, const Planes& x, const Planes& out) {
   const Shape& s = gr.s;
-  const int64_t lo_rows = s.batch * s.mp;
-  dense::Plan plan = dense::make_plan(dense::cdiv(s.mp, dense::kTile) * s.batch, s.np, 1, false);
-  plan.kb_split = s.mp / dense::kBK;
-  Maps m;
-  auto l = new_launch<EpiPlanes>(gr);
-  MOE_TRY(dense::make_map(&m.m[0], q.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, dense::kBK, 128));
-  MOE_TRY(dense::make_map(&m.m[1], x.at, Elem::kF16, 2 * lo_rows, s.np, s.np, dense::kBK, dense::kBK));
-  MOE_TRY(dense::make_map(&m.m[2], out.at, Elem::kF16, 2 * lo_rows, s.np, s.np, 32, 32,
-                          dense::Swizzle::k64));
-  l.maps = 3;
-  l.problems = 1;
-  Problem& p = l.p[0];
-  p = dense::make_problem(plan, s.mp, s.np, s.mp / dense::kBK, 0, false, 1, true, false);
-  p.batch = static_cast<int32_t>(s.batch);
-  p.a_batch = p.b_batch = s.mp;
-  two_terms(p, lo_rows);
-  EpiPlanes::Args& e = l.e[0];
+  const int64_t tm = dense::cdiv(s.mp, dense::kTile) * s.batch;
+  BuildPlanes b(gr, pick_bn(tm * dense::cdiv(s.np, 256), tm * dense::cdiv(s.np, 128)));
+  terms::Problem& p = b.problem(s.mp, s.np, s.batch, s.mp / dense::kBK);
+  MOE_TRY(b.operand(q, 128, false, 0, &p.a));
+  MOE_TRY(b.operand(x, b.bn / 2, true, 0, &p.b));
+  EpiPlanes::Args& e = b.l.e[0];
   e = {};
-  e.c = 1.0f / (q.scale * x.scale);
-  e.scale = out.scale;
-  e.out = out.at;
-  e.lo = lo_rows * s.np;
-  e.map = 2;
-  e.lo_rows = static_cast<int32_t>(lo_rows);
+  e.c = out.scale / (q.scale * x.scale);
+  MOE_TRY(b.map(out.at, s.np, 32, 32, dense::Swizzle::k64, &e.map));
+  e.lo_rows = static_cast<int32_t>(b.rows());
   e.rows = s.mp;
   e.cols = s.np;
-  MOE_CUDA(terms::launch<EpiPlanes>(m, l, gr.pairs_planes, gr.st));
-  return MOE_OK;
+  return run(b);
 }
 
-// p <- decay p - lr s Q X for the group's tensors, up to four a launch.
-int32_t update(const Group& gr, Planes q, Planes x) {
+// p <- decay p - lr s Q X for the group's tensors, as many in a launch as it
+// holds.
+int32_t update(const Group& gr, const Planes& q, const Planes& x) {
   const Shape& s = gr.s;
-  const int64_t lo_rows = s.batch * s.mp;
-  const dense::Plan by_n = dense::make_plan(dense::cdiv(s.n, dense::kTile) * s.batch, s.m, 1, false);
-  const dense::Plan by_m = dense::make_plan(dense::cdiv(s.m, dense::kTile) * s.batch, s.n, 1, false);
-  Maps m;
-  auto l = new_launch<EpiUpdate>(gr);
-  // Q as A and as B, X likewise: all K = m long, X MN-major
-  MOE_TRY(dense::make_map(&m.m[0], q.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, dense::kBK, 128));
-  MOE_TRY(dense::make_map(&m.m[1], q.at, Elem::kF16, 2 * lo_rows, s.mp, s.mp, dense::kBK, by_n.bn / 2));
-  MOE_TRY(dense::make_map(&m.m[2], x.at, Elem::kF16, 2 * lo_rows, s.np, s.np, dense::kBK, dense::kBK));
-  l.maps = 3;
+  const int64_t tn = dense::cdiv(s.n, dense::kTile) * s.batch;
+  const int bn = pick_bn(tn * dense::cdiv(s.m, 256), tn * dense::cdiv(s.m, 128));
   int64_t z = 0;
-  for (int i = 0; i < gr.count; ++i) {
-    const moe_muon_tensor& t = gr.t[i];
-    if (!same(t, s)) continue;
-    const bool tall = t.rows > t.cols;
-    dense::Plan plan = tall ? by_m : by_n;
-    plan.kb_split = s.mp / dense::kBK;
-    Problem& p = l.p[l.problems];
-    EpiUpdate::Args& e = l.e[l.problems];
-    if (tall) p = dense::make_problem(plan, s.m, s.n, s.mp / dense::kBK, 0, false, 2, true, false);
-    else p = dense::make_problem(plan, s.n, s.m, s.mp / dense::kBK, 2, true, 1, false, false);
-    p.batch = t.count;
-    p.a_batch = p.b_batch = s.mp;
-    p.a_off[0] = p.b_off[0] = static_cast<int32_t>(z * s.mp);
-    two_terms(p, lo_rows);
-    const double size = gr.o->update_scale == MOE_MUON_RMS
-                            ? 0.2 * std::sqrt(static_cast<double>(std::max(t.rows, t.cols)))
-                            : std::sqrt(std::max(1.0, static_cast<double>(t.rows) / t.cols));
-    e.p = t.param;
-    e.copy = static_cast<__nv_bfloat16*>(t.param_bf16);
-    e.decay = static_cast<float>(1.0 - gr.o->lr * gr.o->weight_decay);
-    e.step = static_cast<float>(gr.o->lr * size / (static_cast<double>(q.scale) * x.scale));
-    e.rows = tall ? s.m : s.n;
-    e.cols = tall ? s.n : s.m;
-    z += t.count;
-    if (++l.problems == dense::kMaxProblems) {
-      MOE_CUDA(terms::launch<EpiUpdate>(m, l, gr.pairs_update, gr.st));
-      l.problems = 0;
+  for (int i = 0; i < gr.count;) {
+    Build<EpiUpdate> b(gr, bn);
+    for (; i < gr.count && b.l.problems < dense::kMaxProblems; ++i) {
+      const moe_muon_tensor& t = gr.t[i];
+      if (!same(t, s)) continue;
+      const bool tall = t.rows > t.cols;
+      EpiUpdate::Args& e = b.l.e[b.l.problems];
+      terms::Problem& p = b.problem(tall ? s.m : s.n, tall ? s.n : s.m, t.count, s.mp / dense::kBK);
+      MOE_TRY(b.operand(tall ? q : x, 128, !tall, z, &p.a));
+      MOE_TRY(b.operand(tall ? x : q, bn / 2, tall, z, &p.b));
+      const double size = gr.o->update_scale == MOE_MUON_RMS
+                              ? 0.2 * std::sqrt(static_cast<double>(std::max(t.rows, t.cols)))
+                              : std::sqrt(std::max(1.0, static_cast<double>(t.rows) / t.cols));
+      e.p = t.param;
+      e.copy = static_cast<__nv_bfloat16*>(t.param_bf16);
+      e.decay = static_cast<float>(1.0 - gr.o->lr * gr.o->weight_decay);
+      e.step = static_cast<float>(gr.o->lr * size / (static_cast<double>(q.scale) * x.scale));
+      e.rows = tall ? s.m : s.n;
+      e.cols = tall ? s.n : s.m;
+      z += t.count;
     }
+    if (b.l.problems) MOE_CUDA(terms::launch<EpiUpdate>(b.m, b.l, gr.pairs_update, gr.st));
   }
-  if (l.problems) MOE_CUDA(terms::launch<EpiUpdate>(m, l, gr.pairs_update, gr.st));
   return MOE_OK;
 }
 
@@ -604,38 +600,41 @@ int32_t run_group(const Group& gr) {
       z += t.count;
     }
   }
-  const float ca = static_cast<float>(gr.o->coefficients[0]), cb = static_cast<float>(gr.o->coefficients[1]),
-              cc = static_cast<float>(gr.o->coefficients[2]);
-  Planes x = {planes(gr.w.x), gr.sc.x[0]};
+  const double ca = gr.o->coefficients[0], cb = gr.o->coefficients[1], cc = gr.o->coefficients[2];
+  const float fa = static_cast<float>(ca), fc = static_cast<float>(cc), ratio = static_cast<float>(cb / cc);
+  auto square = [&](size_t off, float scale) { return Planes{planes(off), scale, s.mp, true, nullptr}; };
+  Planes x = {planes(gr.w.x), gr.sc.x[0], s.np, false, nullptr};
   int part = 0;
   for (int done = 0; done < gr.o->ns_steps; done += kPartSteps, ++part) {
     const int n = std::min(kPartSteps, gr.o->ns_steps - done);
     const StepScales* sc = gr.sc.step + done;
-    Planes g = {planes(gr.w.g), sc[0].g}, q = {nullptr, 0};
-    MOE_TRY(symmetric(gr, x, x, s.np, g, 1.0f, nullptr, 0.f, 0.f));
+    Planes g = square(gr.w.g, sc[0].g), q = {};
+    g.diag = planes(gr.w.h);
+    MOE_TRY(symmetric(gr, x, x, false, g, 1.0f, 0.f, ratio));
     for (int k = 0; k < n; ++k) {
       const bool last = k == n - 1;
-      const Planes p = {planes(k == 0 ? gr.w.qa : gr.w.p), sc[k].p};
-      MOE_TRY(symmetric(gr, g, g, s.mp, p, cc, &g, cb, ca));
-      const Planes sp = {planes(gr.w.s), sc[k].s};
-      Maps m;
-      auto l = new_launch<EpiPlanes>(gr);
-      if (!last) MOE_TRY(add_symmetric(gr, &m, &l, p, g, s.mp, sp, 1.0f, nullptr, 0.f, 0.f));
+      // P = c G (G + (b / c) I) + a I
+      const Planes p = square(k == 0 ? gr.w.qa : gr.w.p, sc[k].p);
+      MOE_TRY(symmetric(gr, g, g, true, p, fc, fa, 0.f));
+      const Planes sp = square(gr.w.s, sc[k].s);
+      BuildPlanes b(gr, square_bn(gr));
+      if (!last) MOE_TRY(add_symmetric(b, p, g, false, sp, 1.0f, 0.f, 0.f));
       if (k == 0) {
         q = p;
       } else {
-        const Planes next = {planes(k & 1 ? gr.w.qb : gr.w.qa), sc[k].q};
-        MOE_TRY(add_symmetric(gr, &m, &l, p, q, s.mp, next, 1.0f, nullptr, 0.f, 0.f));
+        const Planes next = square(k & 1 ? gr.w.qb : gr.w.qa, sc[k].q);
+        MOE_TRY(add_symmetric(b, p, q, false, next, 1.0f, 0.f, 0.f));
         q = next;
       }
-      if (l.problems) MOE_CUDA(terms::launch<EpiPlanes>(m, l, gr.pairs_planes, gr.st));
+      if (b.l.problems) MOE_TRY(run(b));
       if (!last) {
         g.scale = sc[k + 1].g;
-        MOE_TRY(symmetric(gr, sp, p, s.mp, g, 1.0f, nullptr, 0.f, 0.f));
+        MOE_TRY(symmetric(gr, sp, p, false, g, 1.0f, 0.f, ratio));
       }
     }
     if (done + n < gr.o->ns_steps) {
-      const Planes next = {planes(x.at == planes(gr.w.x) ? gr.w.x1 : gr.w.x), gr.sc.x[part + 1]};
+      const Planes next = {planes(x.at == planes(gr.w.x) ? gr.w.x1 : gr.w.x), gr.sc.x[part + 1], s.np, false,
+                           nullptr};
       MOE_TRY(apply(gr, q, x, next));
       x = next;
     } else {
@@ -678,6 +677,9 @@ int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_optio
   if (o->reserved[0] || o->reserved[1]) return entry_fail(MOE_ERR_INVALID_ARG, "reserved must be zero");
   if (!ptr_aligned(o->grad_scale, 4))
     return entry_fail(MOE_ERR_MISALIGNED, "grad_scale must be 4-byte aligned");
+  if (!(std::fabs(o->coefficients[1]) <= 64 * std::fabs(o->coefficients[2])))
+    return entry_fail(MOE_ERR_UNSUPPORTED, "coefficients (%g, %g, %g): c must be at least |b| / 64", o->coefficients[0],
+                      o->coefficients[1], o->coefficients[2]);
   if (!make_scales(o, sc))
     return entry_fail(MOE_ERR_UNSUPPORTED, "the Newton-Schulz steps of these coefficients grow without bound");
   for (int i = 0; i < count; ++i) MOE_TRY(check_tensor(t[i], i, o->grad_dtype == MOE_DTYPE_BF16));

@@ -59,4 +59,40 @@ __device__ __forceinline__ void tc2_commit_local_warp(uint64_t* bar) {
       : "memory");
 }
 
+// mbar_wait_warp for waits that end within a microsecond and for arrivals from
+// the other CTA of the pair (acquire at cluster scope): polls without sleeping,
+// since a sleeping warp wakes up late; bounded as the others are.
+__device__ __forceinline__ bool mbar_poll_warp(uint64_t* bar, uint32_t parity, uint64_t timeout_ns,
+                                               int32_t* status, int32_t code,
+                                               volatile int32_t* abort) {
+  const uint32_t a = smem_u32(bar);
+  uint64_t t0 = 0;
+  bool ok = false;
+  for (uint32_t n = 1;; ++n) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (done) {
+      ok = true;
+      break;
+    }
+    if ((n & 63) == 0) {
+      if (*abort) break;
+      const uint64_t t = globaltimer_ns();
+      if (t0 == 0) t0 = t;
+      if (t - t0 > timeout_ns) {
+        atomicCAS(status, 0, code);
+        *abort = 1;
+        break;
+      }
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+
 }  // namespace moe

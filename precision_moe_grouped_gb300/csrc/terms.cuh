@@ -7,8 +7,8 @@
 //   is loaded once.
 // - An MMA aligns its 16 products and the accumulator to the largest of them
 //   and cuts each off at 24 bits: a long sum of squares shrinks by about n 2^-25
-//   of itself.  So sums run in pieces of two K blocks, which alternate between
-//   the two accumulators; the epilogue warps add the pieces up in registers
+//   of itself.  So sums run in pieces of two K blocks, which go round the
+//   accumulators (two of 256 columns or four of 128); the epilogue warps add the pieces up in registers
 //   (rounded to nearest) while the next one runs.
 //   Noise of 333 x 1001 through five steps is 1.7e-5 off (4.2e-5 without
 //   pieces), 16 x 7168 1.0e-6 (3.9e-5); plain 32-bit arithmetic 2.6e-6, 0.8e-6.
@@ -28,9 +28,7 @@ using dense::kNumEpiWarps;
 using dense::kStageBox;
 using dense::kThreads;
 using dense::kTile;
-using dense::Launch;
 using dense::Maps;
-using dense::Problem;
 using dense::Tile;
 
 constexpr int kStages = 3;
@@ -38,13 +36,67 @@ constexpr int kPiece = 2;     // K blocks of a piece
 constexpr int kStageBytes = 2 * (kABytes + kBBytes);   // A hi, A lo, B hi, B lo
 constexpr int kOffStage = kStages * kStageBytes;
 constexpr int kOffBar = kOffStage + kNumEpiWarps * kStageBox;
-constexpr int kOffMisc = kOffBar + 8 * (2 * kStages + 4 + 1);
+constexpr int kMaxBufs = 4;   // accumulators: 512 columns of TMEM / bn
+constexpr int kOffMisc = kOffBar + 8 * (2 * kStages + 2 * kMaxBufs + 1);
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
 
-// Epi: struct Args; static run(args, problem, tile, warp, maps, sums): the
-// warp's row (lane) and its half of the tile's columns, bn / 2 of sums[128].
-// Problem: one segment, a_off[0] and a_off[1] the rows of the hi and lo terms.
+// An operand of a product.  A symmetric matrix is stored by its 256 x 256 blocks
+// on and above the diagonal only: a K block right of its rows' block is read
+// K-major, one left of it MN-major from the block across the diagonal.  With
+// `diag` the diagonal blocks come from a matrix of their own ([rows][256], block
+// by block).
+struct Operand {
+  int32_t map, map_mn;    // maps of K-major and MN-major boxes (either may be unused)
+  int32_t hi, lo;         // rows of the first matrix's terms
+  int32_t batch;          // rows between matrices
+  int32_t mn, sym, diag;  // MN-major throughout; symmetric; map of the diagonal blocks, or 0 for none
+};
+struct Problem {
+  Operand a, b;
+  int32_t bn;             // 256 or 128, one for all problems of a launch
+  int32_t tiles_m, tiles_n;
+  int32_t upper;          // symmetric D: only tiles on and above the diagonal's blocks
+  int32_t per_matrix, batch, splits;
+  int32_t kb, kb_split;
+  int32_t first_tile;
+};
+template <typename Args>
+struct Launch {
+  Problem p[dense::kMaxProblems];
+  Args e[dense::kMaxProblems];
+  int32_t problems, tiles, maps, last;
+  int32_t* status;
+  uint64_t timeout_ns;
+};
+
+// Whether operand o's K block kb is read MN-major by a tile at row block tr.
+__device__ __forceinline__ bool mn_at(const Operand& o, int tr, int kb) {
+  return o.mn || (o.sym && (kb >> 2) < tr);
+}
+
+// Both terms of one operand: `rows` rows (or columns) from `at`, K block kb.
+__device__ __forceinline__ void load_terms(const Maps& maps, const Operand& o, int z, int at, int rows, int tr,
+                                           int kb, uint8_t* dst, int slot, uint32_t bar) {
+  const bool mn = mn_at(o, tr, kb), diag = o.diag && (kb >> 2) == tr;
+  const CUtensorMap* m = &maps.m[diag ? o.diag : mn ? o.map_mn : o.map];
+  const int k0 = diag ? (kb & 3) * kBK : kb * kBK;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int row = (h ? o.lo : o.hi) + z * o.batch;
+    if (mn) {
+      tma_load_2d_pair(dst, m, at, k0 + row, bar);
+      if (rows > 64) tma_load_2d_pair(dst + 8192, m, at + 64, k0 + row, bar);
+    } else {
+      tma_load_2d_pair(dst, m, k0, at + row, bar);
+    }
+    dst += slot;
+  }
+}
+
+// Epi: struct Args; static run(args, bn, tile, warp, maps, sums): the
+// warp's row (lane) and its half of the tile's columns, bn / 2 of sums[128]; and
+// static ahead(args, tile, bn, row, warp), called before the tile's products.
 template <class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
     terms_kernel(const __grid_constant__ Maps maps,
@@ -56,12 +108,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* drain = tempty + 2;
+  uint64_t* tempty = tfull + kMaxBufs;
+  uint64_t* drain = tempty + kMaxBufs;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
+  const int bn = l.p[0].bn, bufs = 512 / bn;   // of every problem of the launch
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
@@ -69,7 +122,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < kMaxBufs; ++a) {
       mbar_init(tfull + a, 1);
       mbar_init(tempty + a, 2 * kNumEpiWarps);
     }
@@ -78,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
-  if (warp == 2 && lane < l.maps) prefetch_tmap(&maps.m[lane]);
+  if (warp == 2 && lane > 0 && lane < l.maps) prefetch_tmap(&maps.m[lane]);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
@@ -96,38 +149,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int t = pair; ok && t < l.tiles; t += pairs) {
       const Tile o = dense::find_tile(l, t);
       const Problem& p = l.p[o.p];
-      const CUtensorMap *am = &maps.m[p.a_map[0]], *bm = &maps.m[p.b_map[0]];
-      const int a_mn0 = o.i * kTile + static_cast<int>(rank) * 128;
-      const int b_mn0 = o.j * p.b_step + static_cast<int>(rank) * p.b_rank;
-      const uint32_t bytes = 4u * static_cast<uint32_t>(kABytes + p.bn * 64);
-      for (int kb = 0; kb < p.kb; ++kb) {
-        if (!mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+      const int a0 = o.i * kTile + static_cast<int>(rank) * 128;
+      const int b0 = o.j * bn + static_cast<int>(rank) * (bn >> 1), tb = (o.j * bn) >> 8;
+      const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
+      const uint32_t bytes = 4u * static_cast<uint32_t>(kABytes + bn * 64);
+      for (int kb = k0; kb < k1; ++kb) {
+        if (!mbar_poll_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
           ok = false;
           break;
         }
         if (lane == 0) {
           uint8_t* as = smem + stage * kStageBytes;
-          uint8_t* bs = as + 2 * kABytes;
           const uint32_t bar = full0 + 8 * stage;
           if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int ar = p.a_off[h] + o.z * p.a_batch, br = p.b_off[h] + o.z * p.b_batch;
-            if (p.a_mn) {
-              tma_load_2d_pair(as, am, a_mn0, kb * kBK + ar, bar);
-              tma_load_2d_pair(as + 8192, am, a_mn0 + 64, kb * kBK + ar, bar);
-            } else {
-              tma_load_2d_pair(as, am, kb * kBK, a_mn0 + ar, bar);
-            }
-            if (p.b_mn) {
-              tma_load_2d_pair(bs, bm, b_mn0, kb * kBK + br, bar);
-              if (p.bn == 256) tma_load_2d_pair(bs + 8192, bm, b_mn0 + 64, kb * kBK + br, bar);
-            } else {
-              tma_load_2d_pair(bs, bm, kb * kBK, b_mn0 + br, bar);
-            }
-            as += kABytes;
-            bs += kBBytes;
-          }
+          load_terms(maps, p.a, o.z, a0, 128, o.i, kb, as, kABytes, bar);
+          load_terms(maps, p.b, o.z, b0, bn >> 1, tb, kb, as + 2 * kABytes, kBBytes, bar);
         }
         issued = true;
         if (++stage == kStages) {
@@ -149,31 +185,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (rank == 0) {
       uint32_t stage = 0, phase = 0;
       bool ok = true;
-      int piece = 0;
+      int acc = 0;
+      uint32_t round = 0;
       for (int t = pair; ok && t < l.tiles; t += pairs) {
         const Tile o = dense::find_tile(l, t);
         const Problem& p = l.p[o.p];
-        const uint64_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
-        const uint64_t ad0 = smem_desc(smem_u32(smem), p.a_mn ? 8192 : 0, 1024, 2);
-        const uint64_t bd0 = smem_desc(smem_u32(smem) + 2 * kABytes, p.b_mn ? 8192 : 0, 1024, 2);
-        const uint32_t idesc = static_cast<uint32_t>(p.idesc);
-        for (int kb = 0; ok && kb < p.kb; kb += kPiece, ++piece) {
-          const int acc = piece & 1, n = min(kPiece, p.kb - kb);
-          if (!mbar_wait_warp(tempty + acc, static_cast<uint32_t>((piece >> 1) & 1) ^ 1u, l.timeout_ns,
-                              l.status, kDevTimeout, abort_flag)) {
+        const int tb = (o.j * bn) >> 8;
+        const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
+        for (int kb = k0; ok && kb < k1; kb += kPiece) {
+          const int n = min(kPiece, k1 - kb);
+          if (!mbar_poll_warp(tempty + acc, round ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
             ok = false;
             break;
           }
-          asm volatile("fence.acq_rel.cluster;" ::: "memory");
           tc_fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * bn);
           for (int k = 0; k < n; ++k) {
-            if (!mbar_wait_warp(full + stage, phase, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+            if (!mbar_poll_warp(full + stage, phase, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t a = ad0 + stage * (kStageBytes >> 4), b = bd0 + stage * (kStageBytes >> 4);
+            const bool amn = mn_at(p.a, o.i, kb + k), bmn = mn_at(p.b, tb, kb + k);
+            const uint64_t a_step = amn ? 2048 >> 4 : 32 >> 4, b_step = bmn ? 2048 >> 4 : 32 >> 4;
+            const uint32_t at = smem_u32(smem + stage * kStageBytes);
+            const uint64_t a = smem_desc(at, amn ? 8192 : 0, 1024, 2);
+            const uint64_t b = smem_desc(at + 2 * kABytes, bmn ? 8192 : 0, 1024, 2);
+            const uint32_t idesc = dense::idesc_f16(false, amn, bmn, bn);
             // the small products first: they lose nothing to a sum that is still small
             dense::mma_quad_warp(d, a + (kABytes >> 4), b, a_step, b_step, idesc, k > 0 ? 1u : 0u);
             dense::mma_quad_warp(d, a, b + (kBBytes >> 4), a_step, b_step, idesc, 1u);
@@ -185,6 +223,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (ok) tc2_commit_both_warp(tfull + acc);
+          if (++acc == bufs) {
+            acc = 0;
+            round ^= 1u;
+          }
         }
       }
       tc2_commit_local_warp(drain);
@@ -200,7 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.half = e >> 2;
     w.lane = lane;
     w.tmem = 0;
-    int piece = 0;
+    int acc = 0;
+    uint32_t round = 0;
     bool ok = true;
     for (int t = pair; ok && t < l.tiles; t += pairs) {
       const Tile o = dense::find_tile(l, t);
@@ -208,19 +251,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sums[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sums[i] = 0.f;
-      for (int kb = 0; kb < p.kb; kb += kPiece, ++piece) {
-        const int acc = piece & 1;
-        if (!mbar_wait_warp(tfull + acc, static_cast<uint32_t>((piece >> 1) & 1), l.timeout_ns, l.status,
-                            kDevTimeout, abort_flag)) {
+      const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
+      Epi::ahead(l.e[o.p], o, bn, o.i * kTile + static_cast<int>(rank) * 128 + 32 * quarter, w);
+      for (int kb = k0; kb < k1; kb += kPiece) {
+        if (!mbar_poll_warp(tfull + acc, round, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = tmem + static_cast<uint32_t>(acc * 256 + w.half * (p.bn >> 1)) +
+        const uint32_t at = tmem + static_cast<uint32_t>(acc * bn + w.half * (bn >> 1)) +
                             (static_cast<uint32_t>(32 * quarter) << 16);
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
-          if (c < (p.bn >> 1)) {
+          if (c < (bn >> 1)) {
             uint32_t v[32];
             dense::tmem_ld_x32(at + c, v);
             dense::tmem_wait(v);
@@ -231,10 +274,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(release + static_cast<uint32_t>(8 * acc));
+        if (++acc == bufs) {
+          acc = 0;
+          round ^= 1u;
+        }
       }
       if (!ok) break;
       w.row = o.i * kTile + static_cast<int>(rank) * 128 + 32 * quarter;
-      Epi::run(l.e[o.p], p, o, w, maps, sums);
+      Epi::run(l.e[o.p], bn, o, w, maps, sums);
     }
     if (lane == 0) dense::box_wait_all();
   }
