@@ -63,7 +63,7 @@ struct Problem {
   int32_t b_step;              // columns of D between tiles (bn, or bn / 2 for two halves)
   int32_t b_rank;              // where rank 1's half of B begins, from rank 0's
   int32_t tiles_m, tiles_n;
-  int32_t upper;               // symmetric D: only tiles that meet the upper triangle
+  int32_t upper;               // symmetric D: only tiles on and above the diagonal
   int32_t per_matrix;          // tiles of one matrix
   int32_t batch, splits;
   int32_t kb, kb_split;        // K blocks of a segment, of a split's share
@@ -103,15 +103,13 @@ __device__ __forceinline__ Tile find_tile(const L& l, int t) {
   o.z = zs / p.splits;
   o.s = zs - o.z * p.splits;
   if (p.upper) {
-    // row i begins at column i * (256 / bn)
-    const int per = kTile / p.bn;
     int i = 0;
-    while (t >= p.tiles_n - i * per) {
-      t -= p.tiles_n - i * per;
+    while (t >= p.tiles_n - i) {
+      t -= p.tiles_n - i;
       ++i;
     }
     o.i = i;
-    o.j = i * per + t;
+    o.j = i + t;
   } else {
     const int g = t / (kRasterRows * p.tiles_n);
     t -= g * kRasterRows * p.tiles_n;
@@ -522,7 +520,7 @@ cudaError_t resident_pairs(int num_sms, int* pairs) {
 }
 
 template <class Kernel, class L>
-cudaError_t launch(Kernel kern, int smem, const Maps& maps, L& l, int pairs, cudaStream_t s) {
+cudaError_t launch(Kernel kern, int smem, const Maps& maps, L& l, int pairs, cudaStream_t s, int units = 0) {
   int tiles = 0;
   for (int i = 0; i < l.problems; ++i) {
     l.p[i].first_tile = tiles;
@@ -531,7 +529,8 @@ cudaError_t launch(Kernel kern, int smem, const Maps& maps, L& l, int pairs, cud
   l.tiles = tiles;
   if (tiles == 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
+  if (units < tiles) units = tiles;
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * (units < pairs ? units : pairs)));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;

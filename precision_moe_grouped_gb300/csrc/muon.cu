@@ -43,6 +43,7 @@ constexpr int kPartSteps = 3;         // steps between two Gram matrices
 // ------------------------------------------------------------ elementwise
 constexpr int kThreads = 256;
 constexpr int kChunk = 16384;         // elements of a block's share
+constexpr int64_t kL2Bytes = 100 << 20;   // of the 129 MB, what two readings in turn may count on
 
 struct Momentum {
   const void* grad;
@@ -122,10 +123,11 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // X0's planes: hi and lo fp16 terms of scale * u / (|u| + eps), [mp][np] per
-// matrix with zeros beyond m x n; a tall matrix [n, m] is turned on the way.
+// matrix with zeros beyond m x n; a tall matrix [n, m] is turned on the way.  A
+// block takes a square of 64, a thread four neighbours in each of four rows.
 constexpr int kSide = 64;
 __global__ void __launch_bounds__(kThreads)
-    muon_planes_kernel(const Momentum a, int rows, int cols, const float* sums, int chunks, float eps,
+    muon_planes_kernel(const Momentum a, int rows, int cols, int vec, const float* sums, int chunks, float eps,
                        float scale, __half* planes, int64_t lo_off, int mp, int np) {
   __shared__ float warp_sums[kThreads / 32];
   __shared__ float tile[kSide][kSide + 1];
@@ -133,36 +135,72 @@ __global__ void __launch_bounds__(kThreads)
   griddep_launch_dependents();
   const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
   const int z = blockIdx.z;
-  float s = 0.f;
-  for (int i = threadIdx.x; i < chunks; i += kThreads) s += sums[static_cast<int64_t>(z) * chunks + i];
-  s = block_sum(s, warp_sums);
-  const float mul = scale / (sqrtf(s) + eps);
   const bool tall = rows > cols;
   const int64_t base = static_cast<int64_t>(z) * rows * cols;
   // the source's square: rows r0.., columns c0..
   const int r0 = (tall ? blockIdx.x : blockIdx.y) * kSide, c0 = (tall ? blockIdx.y : blockIdx.x) * kSide;
-  const int tx = threadIdx.x & 63, ty = threadIdx.x >> 6;
-#pragma unroll 4
-  for (int i = ty; i < kSide; i += 4) {
-    float v = 0.f;
-    if (r0 + i < rows && c0 + tx < cols) {
-      const int64_t at = base + static_cast<int64_t>(r0 + i) * cols + c0 + tx;
-      v = update_of(a, a.m[at], grad_at(a, at, gs)) * mul;
+  const int tx = (threadIdx.x & 15) * 4, ty = threadIdx.x >> 4;
+  float mv[4][4], gv[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + ty + 16 * i, c = c0 + tx;
+    const int64_t at = base + static_cast<int64_t>(r) * cols + c;
+    if (vec && r < rows && c + 4 <= cols) {
+      const float4 m = *reinterpret_cast<const float4*>(a.m + at);
+      mv[i][0] = m.x, mv[i][1] = m.y, mv[i][2] = m.z, mv[i][3] = m.w;
+      if (a.bf16) {
+        const uint2 v = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.grad) + at);
+        const float2 lo = dense::unpack_bf16(v.x), hi = dense::unpack_bf16(v.y);
+        gv[i][0] = lo.x, gv[i][1] = lo.y, gv[i][2] = hi.x, gv[i][3] = hi.y;
+      } else {
+        const float4 v = *reinterpret_cast<const float4*>(static_cast<const float*>(a.grad) + at);
+        gv[i][0] = v.x, gv[i][1] = v.y, gv[i][2] = v.z, gv[i][3] = v.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) gv[i][k] *= gs;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const bool in = r < rows && c + k < cols;
+        mv[i][k] = in ? a.m[at + k] : 0.f;
+        gv[i][k] = in ? grad_at(a, at + k, gs) : 0.f;
+      }
     }
-    if (tall) tile[tx][i] = v;
-    else tile[i][tx] = v;
   }
-  __syncthreads();
-  const int64_t out = (static_cast<int64_t>(z) * mp + blockIdx.y * kSide) * np + blockIdx.x * kSide;
-  const int px = (threadIdx.x & 31) * 2, py = threadIdx.x >> 5;
-#pragma unroll 4
-  for (int i = py; i < kSide; i += 8) {
-    const float x = tile[i][px], y = tile[i][px + 1];
-    const __half2 hi = __floats2half2_rn(x, y);
-    const float2 f = __half22float2(hi);
-    *reinterpret_cast<__half2*>(planes + out + static_cast<int64_t>(i) * np + px) = hi;
-    *reinterpret_cast<__half2*>(planes + lo_off + out + static_cast<int64_t>(i) * np + px) =
-        __floats2half2_rn(x - f.x, y - f.y);
+  float s = 0.f;
+  for (int i = threadIdx.x; i < chunks; i += kThreads) s += sums[static_cast<int64_t>(z) * chunks + i];
+  s = block_sum(s, warp_sums);
+  const float mul = scale / (sqrtf(s) + eps);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool in = r0 + ty + 16 * i < rows && c0 + tx + k < cols;
+      mv[i][k] = in ? update_of(a, mv[i][k], gv[i][k]) * mul : 0.f;   // (0 stays 0 beside a NaN norm)
+    }
+  if (tall) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) tile[tx + k][ty + 16 * i] = mv[i][k];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mv[i][k] = tile[ty + 16 * i][tx + k];
+  }
+  const int64_t out = (static_cast<int64_t>(z) * mp + blockIdx.y * kSide + ty) * np + blockIdx.x * kSide + tx;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint2 hi, lo;
+    hi.x = dense::pack_f16(mv[i][0], mv[i][1]);
+    hi.y = dense::pack_f16(mv[i][2], mv[i][3]);
+    const float2 p = dense::unpack_f16(hi.x), q = dense::unpack_f16(hi.y);
+    lo.x = dense::pack_f16(mv[i][0] - p.x, mv[i][1] - p.y);
+    lo.y = dense::pack_f16(mv[i][2] - q.x, mv[i][3] - q.y);
+    __half* to = planes + out + static_cast<int64_t>(16 * i) * np;
+    *reinterpret_cast<uint2*>(to) = hi;
+    *reinterpret_cast<uint2*>(to + lo_off) = lo;
   }
 }
 
@@ -177,15 +215,15 @@ struct EpiPlanes {
     int32_t lo_rows;         // rows from the hi to the lo plane
     int32_t m, rows, cols;   // rows of I; stored rows (a multiple of 64) and columns
   };
-  static __device__ __forceinline__ void ahead(const Args&, const Tile&, int, int, const EpiWarp&) {}
-  static __device__ __forceinline__ void run(const Args& a, int bn, const Tile& o, const EpiWarp& w,
+  static __device__ __forceinline__ void ahead(const Args&, const Tile&, const EpiWarp&, int, int) {}
+  static __device__ __forceinline__ void run(const Args& a, const Tile& o, const EpiWarp& w, int col0, int n,
                                              const Maps& maps, float (&d)[128]) {
     if (w.row >= a.rows) return;
     const int row = o.z * a.rows + w.row;
 #pragma unroll
     for (int c = 0; c < 128; c += 32) {
-      const int col = o.j * bn + w.half * (bn >> 1) + c;
-      if (c >= (bn >> 1) || col >= a.cols) continue;
+      const int col = col0 + c;
+      if (c >= n || col >= a.cols) continue;
 #pragma unroll
       for (int i = 0; i < 32; ++i) d[c + i] *= a.c;
       const int on = w.row + w.lane - col;   // this row's place on the diagonal
@@ -243,37 +281,43 @@ struct EpiUpdate {
     float decay, step;
     int32_t rows, cols;
   };
-  // p's lines into L2 while the products run: a lane's are 128 bytes apart
-  static __device__ __forceinline__ void ahead(const Args& a, const Tile& o, int bn, int row,
-                                               const EpiWarp& w) {
-    if (row >= a.rows) return;
-    const int64_t base = static_cast<int64_t>(o.z) * a.rows * a.cols + row;
-    for (int c = w.lane; c < (bn >> 1); c += 32) {
-      const int col = o.j * bn + w.half * (bn >> 1) + c;
-      if (col < a.cols)
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(a.p + base + static_cast<int64_t>(col) * a.rows));
-    }
+  // p's lines into L2 while the products run
+  static __device__ __forceinline__ void ahead(const Args& a, const Tile& o, const EpiWarp& w, int col, int n) {
+    if (w.row >= a.rows) return;
+    const int64_t base = static_cast<int64_t>(o.z) * a.rows * a.cols + w.row;
+    for (int c = col + w.lane; c < col + n && c < a.cols; c += 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(a.p + base + static_cast<int64_t>(c) * a.rows));
   }
-  static __device__ __forceinline__ void run(const Args& a, int bn, const Tile& o, const EpiWarp& w,
+  static __device__ __forceinline__ void run(const Args& a, const Tile& o, const EpiWarp& w, int col0, int n,
                                              const Maps&, float (&d)[128]) {
     const int r = w.row + w.lane;
     if (r >= a.rows) return;
-    const int64_t base = static_cast<int64_t>(o.z) * a.rows * a.cols + r;
+    const int64_t base = (static_cast<int64_t>(o.z) * a.cols + col0) * a.rows + r;
+    float* p = a.p + base;
+    __nv_bfloat16* copy = a.copy + base;
+    const int end = a.cols - col0 < n ? a.cols - col0 : n;
 #pragma unroll
     for (int c = 0; c < 128; c += 16) {
-      const int col = o.j * bn + w.half * (bn >> 1) + c;
-      if (c >= (bn >> 1) || col >= a.cols) continue;
-      float v[16];
+      if (c + 16 <= end) {   // the loads of 16 columns are in flight together
+        float v[16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        v[i] = col + i < a.cols ? a.p[base + static_cast<int64_t>(col + i) * a.rows] : 0.f;
+        for (int i = 0; i < 16; ++i) v[i] = p[static_cast<int64_t>(c + i) * a.rows];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        if (col + i < a.cols) {
-          const int64_t at = base + static_cast<int64_t>(col + i) * a.rows;
+        for (int i = 0; i < 16; ++i) {
+          const int64_t at = static_cast<int64_t>(c + i) * a.rows;
           const float x = fmaf(-a.step, d[c + i], a.decay * v[i]);
-          a.p[at] = x;
-          if (a.copy) a.copy[at] = __float2bfloat16_rn(x);
+          p[at] = x;
+          if (a.copy) copy[at] = __float2bfloat16_rn(x);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          if (c + i < end) {
+            const int64_t at = static_cast<int64_t>(c + i) * a.rows;
+            const float x = fmaf(-a.step, d[c + i], a.decay * p[at]);
+            p[at] = x;
+            if (a.copy) copy[at] = __float2bfloat16_rn(x);
+          }
         }
       }
     }
@@ -407,29 +451,20 @@ struct Planes {
   __half* diag;   // G's diagonal blocks + (b / c) I, or null
 };
 
-// Tiles on and above the diagonal's 256 x 256 blocks.
-int64_t upper_tiles(int64_t mp, int bn) {
-  const int64_t rows = dense::cdiv(mp, dense::kTile), cols = dense::cdiv(mp, bn), per = dense::kTile / bn;
-  int64_t n = 0;
-  for (int64_t i = 0; i < rows; ++i) n += std::max<int64_t>(0, cols - i * per);
-  return n;
+// Tiles on and above the diagonal.
+int64_t upper_tiles(int64_t mp) {
+  const int64_t n = dense::cdiv(mp, dense::kTile);
+  return n * (n + 1) / 2;
 }
 
-// 128 columns a tile take about 0.7 of the time of 256.
-int pick_bn(int64_t tiles_of_256, int64_t tiles_of_128) {
-  return 10 * dense::cdiv(tiles_of_256, dense::kPlanPairs) <= 7 * dense::cdiv(tiles_of_128, dense::kPlanPairs) ? 256
-                                                                                                         : 128;
-}
-
-// A launch in the making: problems of one bn.
+// A launch in the making.
 template <class Epi>
 struct Build {
   const Group& g;
   Maps m;
   terms::Launch<typename Epi::Args> l;
-  int bn;
 
-  Build(const Group& gr, int n) : g(gr), l{}, bn(n) {
+  explicit Build(const Group& gr) : g(gr), l{} {
     l.status = gr.status;
     l.timeout_ns = kTimeoutNs;
     l.maps = 1;   // map 0 stands for none
@@ -441,25 +476,22 @@ struct Build {
     *index = l.maps++;
     return dense::make_map(&m.m[*index], at, Elem::kF16, 2 * rows(), cols, cols, box_cols, box_rows, sw);
   }
-  // The operand as rows of a tile (half_rows of them in each CTA), or, with mn,
-  // as its transpose; from matrix z on.
-  int32_t operand(const Planes& p, int half_rows, bool mn, int64_t z, terms::Operand* o) {
+  // The operand as rows of a tile or, with mn, its transpose; from matrix z on.
+  int32_t operand(const Planes& p, bool mn, int64_t z, terms::Operand* o) {
     *o = {};
     o->hi = static_cast<int32_t>(z * g.s.mp);
     o->lo = static_cast<int32_t>(rows() + z * g.s.mp);
     o->batch = g.s.mp;
     o->mn = mn;
     o->sym = p.sym;
-    if (!mn) MOE_TRY(map(p.at, p.ld, dense::kBK, half_rows, dense::Swizzle::k128, &o->map));
-    if (mn || p.sym) MOE_TRY(map(p.at, p.ld, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->map_mn));
-    if (p.diag) MOE_TRY(map(p.diag, dense::kTile, dense::kBK, half_rows, dense::Swizzle::k128, &o->diag));
+    MOE_TRY(map(p.at, p.ld, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->map));
+    if (p.diag) MOE_TRY(map(p.diag, dense::kTile, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->diag));
     return MOE_OK;
   }
   terms::Problem& problem(int64_t tile_rows, int64_t tile_cols, int64_t batch, int64_t kb) {
     terms::Problem& p = l.p[l.problems++];
-    p.bn = bn;
     p.tiles_m = static_cast<int32_t>(dense::cdiv(tile_rows, dense::kTile));
-    p.tiles_n = static_cast<int32_t>(dense::cdiv(tile_cols, bn));
+    p.tiles_n = static_cast<int32_t>(dense::cdiv(tile_cols, dense::kTile));
     p.per_matrix = p.tiles_m * p.tiles_n;
     p.batch = static_cast<int32_t>(batch);
     p.splits = 1;
@@ -469,10 +501,6 @@ struct Build {
 };
 
 using BuildPlanes = Build<EpiPlanes>;
-
-int square_bn(const Group& g) {
-  return pick_bn(upper_tiles(g.s.mp, 256) * g.s.batch, upper_tiles(g.s.mp, 128) * g.s.batch);
-}
 
 // out = c A B^T + a I, symmetric [mp, mp]; A and B [mp, k], B's second copy of the
 // diagonal blocks used when use_diag.
@@ -484,9 +512,9 @@ int32_t add_symmetric(BuildPlanes& b, const Planes& x, Planes y, bool use_diag, 
   left.diag = nullptr;
   terms::Problem& p = b.problem(s.mp, s.mp, s.batch, x.ld / dense::kBK);
   p.upper = 1;
-  p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp, b.bn));
-  MOE_TRY(b.operand(left, 128, false, 0, &p.a));
-  MOE_TRY(b.operand(y, b.bn / 2, false, 0, &p.b));
+  p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp));
+  MOE_TRY(b.operand(left, false, 0, &p.a));
+  MOE_TRY(b.operand(y, false, 0, &p.b));
   EpiPlanes::Args& e = b.l.e[b.l.problems - 1];
   e = {};
   e.c = c * out.scale / (x.scale * y.scale);
@@ -509,7 +537,7 @@ int32_t run(BuildPlanes& b) {
 
 int32_t symmetric(const Group& gr, const Planes& x, const Planes& y, bool use_diag, const Planes& out, float c,
                   float a, float ratio) {
-  BuildPlanes b(gr, square_bn(gr));
+  BuildPlanes b(gr);
   MOE_TRY(add_symmetric(b, x, y, use_diag, out, c, a, ratio));
   return run(b);
 }
@@ -517,11 +545,10 @@ int32_t symmetric(const Group& gr, const Planes& x, const Planes& y, bool use_di
 // X1 = Q X as planes.
 int32_t apply(const Group& gr, const Planes& q, const Planes& x, const Planes& out) {
   const Shape& s = gr.s;
-  const int64_t tm = dense::cdiv(s.mp, dense::kTile) * s.batch;
-  BuildPlanes b(gr, pick_bn(tm * dense::cdiv(s.np, 256), tm * dense::cdiv(s.np, 128)));
+  BuildPlanes b(gr);
   terms::Problem& p = b.problem(s.mp, s.np, s.batch, s.mp / dense::kBK);
-  MOE_TRY(b.operand(q, 128, false, 0, &p.a));
-  MOE_TRY(b.operand(x, b.bn / 2, true, 0, &p.b));
+  MOE_TRY(b.operand(q, false, 0, &p.a));
+  MOE_TRY(b.operand(x, true, 0, &p.b));
   EpiPlanes::Args& e = b.l.e[0];
   e = {};
   e.c = out.scale / (q.scale * x.scale);
@@ -536,19 +563,17 @@ int32_t apply(const Group& gr, const Planes& q, const Planes& x, const Planes& o
 // holds.
 int32_t update(const Group& gr, const Planes& q, const Planes& x) {
   const Shape& s = gr.s;
-  const int64_t tn = dense::cdiv(s.n, dense::kTile) * s.batch;
-  const int bn = pick_bn(tn * dense::cdiv(s.m, 256), tn * dense::cdiv(s.m, 128));
   int64_t z = 0;
   for (int i = 0; i < gr.count;) {
-    Build<EpiUpdate> b(gr, bn);
+    Build<EpiUpdate> b(gr);
     for (; i < gr.count && b.l.problems < dense::kMaxProblems; ++i) {
       const moe_muon_tensor& t = gr.t[i];
       if (!same(t, s)) continue;
       const bool tall = t.rows > t.cols;
       EpiUpdate::Args& e = b.l.e[b.l.problems];
       terms::Problem& p = b.problem(tall ? s.m : s.n, tall ? s.n : s.m, t.count, s.mp / dense::kBK);
-      MOE_TRY(b.operand(tall ? q : x, 128, !tall, z, &p.a));
-      MOE_TRY(b.operand(tall ? x : q, bn / 2, tall, z, &p.b));
+      MOE_TRY(b.operand(tall ? q : x, !tall, z, &p.a));
+      MOE_TRY(b.operand(tall ? x : q, tall, z, &p.b));
       const double size = gr.o->update_scale == MOE_MUON_RMS
                               ? 0.2 * std::sqrt(static_cast<double>(std::max(t.rows, t.cols)))
                               : std::sqrt(std::max(1.0, static_cast<double>(t.rows) / t.cols));
@@ -572,33 +597,30 @@ int32_t run_group(const Group& gr) {
   auto planes = [&](size_t off) { return reinterpret_cast<__half*>(gr.ws + off); };
   const int chunks = chunks_of(s);
   const int64_t size = static_cast<int64_t>(s.m) * s.n;
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t z = 0;
-    for (int i = 0; i < gr.count; ++i) {
-      const moe_muon_tensor& t = gr.t[i];
-      if (!same(t, s)) continue;
-      const bool bf16 = gr.o->grad_dtype == MOE_DTYPE_BF16;
-      const Momentum a = {t.grad, t.momentum, gr.o->grad_scale, static_cast<float>(gr.o->momentum),
-                          static_cast<float>(1.0 - gr.o->momentum), bf16, gr.o->nesterov};
-      const int vec = size % 4 == 0 && ptr_aligned(t.momentum, 16) && ptr_aligned(t.grad, bf16 ? 8 : 16);
-      // a launch's matrices are at most 65535 blocks in y or z
-      for (int at = 0; at < t.count; at += 65535) {
-        const int n = std::min(t.count - at, 65535);
-        Momentum b = a;
-        b.m += at * size;
-        b.grad = static_cast<const uint8_t*>(a.grad) + at * size * (bf16 ? 2 : 4);
-        if (pass == 0) {
-          MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, gr.st, b, size, vec,
-                              sums + (z + at) * chunks));
-        } else {
-          MOE_CUDA(launch_pdl(muon_planes_kernel, dim3(s.np / kSide, s.mp / kSide, n), dim3(kThreads), 0, gr.st,
-                              b, t.rows, t.cols, static_cast<const float*>(sums + (z + at) * chunks), chunks,
-                              static_cast<float>(gr.o->eps), gr.sc.x[0],
-                              planes(gr.w.x) + (z + at) * s.mp * s.np, lo * s.np, s.mp, s.np));
-        }
-      }
-      z += t.count;
+  const bool bf16 = gr.o->grad_dtype == MOE_DTYPE_BF16;
+  // Matrices whose momentum and gradient stay in L2 go one after another, so
+  // that the second reading finds them there; as many small ones at once as do.
+  const int64_t at_once = std::min<int64_t>(65535, std::max<int64_t>(1, kL2Bytes / (size * (bf16 ? 6 : 8))));
+  int64_t z = 0;
+  for (int i = 0; i < gr.count; ++i) {
+    const moe_muon_tensor& t = gr.t[i];
+    if (!same(t, s)) continue;
+    Momentum a = {t.grad, t.momentum, gr.o->grad_scale, static_cast<float>(gr.o->momentum),
+                  static_cast<float>(1.0 - gr.o->momentum), bf16, gr.o->nesterov};
+    const int vec = size % 4 == 0 && ptr_aligned(t.momentum, 16) && ptr_aligned(t.grad, bf16 ? 8 : 16);
+    const int vec_rows = vec && t.cols % 4 == 0;
+    for (int64_t at = 0; at < t.count; at += at_once) {
+      const unsigned n = static_cast<unsigned>(std::min<int64_t>(t.count - at, at_once));
+      a.m = t.momentum + at * size;
+      a.grad = static_cast<const uint8_t*>(t.grad) + at * size * (bf16 ? 2 : 4);
+      float* part = sums + (z + at) * chunks;
+      MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, gr.st, a, size, vec, part));
+      MOE_CUDA(launch_pdl(muon_planes_kernel, dim3(s.np / kSide, s.mp / kSide, n), dim3(kThreads), 0, gr.st, a,
+                          t.rows, t.cols, vec_rows, static_cast<const float*>(part), chunks,
+                          static_cast<float>(gr.o->eps), gr.sc.x[0], planes(gr.w.x) + (z + at) * s.mp * s.np,
+                          lo * s.np, s.mp, s.np));
     }
+    z += t.count;
   }
   const double ca = gr.o->coefficients[0], cb = gr.o->coefficients[1], cc = gr.o->coefficients[2];
   const float fa = static_cast<float>(ca), fc = static_cast<float>(cc), ratio = static_cast<float>(cb / cc);
@@ -617,7 +639,7 @@ int32_t run_group(const Group& gr) {
       const Planes p = square(k == 0 ? gr.w.qa : gr.w.p, sc[k].p);
       MOE_TRY(symmetric(gr, g, g, true, p, fc, fa, 0.f));
       const Planes sp = square(gr.w.s, sc[k].s);
-      BuildPlanes b(gr, square_bn(gr));
+      BuildPlanes b(gr);
       if (!last) MOE_TRY(add_symmetric(b, p, g, false, sp, 1.0f, 0.f, 0.f));
       if (k == 0) {
         q = p;

@@ -7,8 +7,8 @@
 //   is loaded once.
 // - An MMA aligns its 16 products and the accumulator to the largest of them
 //   and cuts each off at 24 bits: a long sum of squares shrinks by about n 2^-25
-//   of itself.  So sums run in pieces of two K blocks, which go round the
-//   accumulators (two of 256 columns or four of 128); the epilogue warps add the pieces up in registers
+//   of itself.  So sums run in pieces of two K blocks, which alternate between
+//   the two accumulators; the epilogue warps add the pieces up in registers
 //   (rounded to nearest) while the next one runs.
 //   Noise of 333 x 1001 through five steps is 1.7e-5 off (4.2e-5 without
 //   pieces), 16 x 7168 1.0e-6 (3.9e-5); plain 32-bit arithmetic 2.6e-6, 0.8e-6.
@@ -36,8 +36,7 @@ constexpr int kPiece = 2;     // K blocks of a piece
 constexpr int kStageBytes = 2 * (kABytes + kBBytes);   // A hi, A lo, B hi, B lo
 constexpr int kOffStage = kStages * kStageBytes;
 constexpr int kOffBar = kOffStage + kNumEpiWarps * kStageBox;
-constexpr int kMaxBufs = 4;   // accumulators: 512 columns of TMEM / bn
-constexpr int kOffMisc = kOffBar + 8 * (2 * kStages + 2 * kMaxBufs + 1);
+constexpr int kOffMisc = kOffBar + 8 * (2 * kStages + 4 + 1);
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
 
@@ -46,57 +45,74 @@ static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
 // K-major, one left of it MN-major from the block across the diagonal.  With
 // `diag` the diagonal blocks come from a matrix of their own ([rows][256], block
 // by block).
+// Boxes are 64 x 64 for either major.
 struct Operand {
-  int32_t map, map_mn;    // maps of K-major and MN-major boxes (either may be unused)
+  int32_t map;
   int32_t hi, lo;         // rows of the first matrix's terms
   int32_t batch;          // rows between matrices
   int32_t mn, sym, diag;  // MN-major throughout; symmetric; map of the diagonal blocks, or 0 for none
 };
 struct Problem {
   Operand a, b;
-  int32_t bn;             // 256 or 128, one for all problems of a launch
-  int32_t tiles_m, tiles_n;
-  int32_t upper;          // symmetric D: only tiles on and above the diagonal's blocks
+  int32_t tiles_m, tiles_n;   // of 256 x 256
+  int32_t upper;              // symmetric D: only tiles on and above the diagonal
   int32_t per_matrix, batch, splits;
   int32_t kb, kb_split;
   int32_t first_tile;
 };
+// The launch's tiles of 256 x 256 are taken whole up to `whole`; each of the rest
+// is two units of 128 columns, where that fills the last round of the pairs.
 template <typename Args>
 struct Launch {
   Problem p[dense::kMaxProblems];
   Args e[dense::kMaxProblems];
-  int32_t problems, tiles, maps, last;
+  int32_t problems, tiles, whole, maps, last;
   int32_t* status;
   uint64_t timeout_ns;
 };
+
+// A unit: tile o, columns [col, col + bn).
+struct Unit {
+  Tile o;
+  int32_t bn, col;
+};
+template <typename L>
+__device__ __forceinline__ int num_units(const L& l) {
+  return l.whole + 2 * (l.tiles - l.whole);
+}
+template <typename L>
+__device__ __forceinline__ Unit find_unit(const L& l, int u) {
+  const int rest = u - l.whole;
+  Unit x;
+  x.bn = rest < 0 ? 256 : 128;
+  x.o = dense::find_tile(l, rest < 0 ? u : l.whole + (rest >> 1));
+  x.col = x.o.j * 256 + (rest < 0 ? 0 : (rest & 1) * 128);
+  return x;
+}
 
 // Whether operand o's K block kb is read MN-major by a tile at row block tr.
 __device__ __forceinline__ bool mn_at(const Operand& o, int tr, int kb) {
   return o.mn || (o.sym && (kb >> 2) < tr);
 }
 
-// Both terms of one operand: `rows` rows (or columns) from `at`, K block kb.
+// Both terms of one operand: 64 or 128 rows (or columns) from `at`, K block kb.
 __device__ __forceinline__ void load_terms(const Maps& maps, const Operand& o, int z, int at, int rows, int tr,
                                            int kb, uint8_t* dst, int slot, uint32_t bar) {
   const bool mn = mn_at(o, tr, kb), diag = o.diag && (kb >> 2) == tr;
-  const CUtensorMap* m = &maps.m[diag ? o.diag : mn ? o.map_mn : o.map];
+  const CUtensorMap* m = &maps.m[diag ? o.diag : o.map];
   const int k0 = diag ? (kb & 3) * kBK : kb * kBK;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const int row = (h ? o.lo : o.hi) + z * o.batch;
-    if (mn) {
-      tma_load_2d_pair(dst, m, at, k0 + row, bar);
-      if (rows > 64) tma_load_2d_pair(dst + 8192, m, at + 64, k0 + row, bar);
-    } else {
-      tma_load_2d_pair(dst, m, k0, at + row, bar);
-    }
+    for (int r = 0; r < rows; r += 64)
+      tma_load_2d_pair(dst + r * 128, m, mn ? at + r : k0, (mn ? k0 : at + r) + row, bar);
     dst += slot;
   }
 }
 
-// Epi: struct Args; static run(args, bn, tile, warp, maps, sums): the
-// warp's row (lane) and its half of the tile's columns, bn / 2 of sums[128]; and
-// static ahead(args, tile, bn, row, warp), called before the tile's products.
+// Epi: struct Args; static run(args, tile, warp, col, n, maps, sums): the warp's
+// row (lane), columns [col, col + n) in sums[0 .. n), n 128 or 64; and static
+// ahead(args, tile, warp, col, n), called before the unit's products.
 template <class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
     terms_kernel(const __grid_constant__ Maps maps,
@@ -108,13 +124,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
-  uint64_t* tempty = tfull + kMaxBufs;
-  uint64_t* drain = tempty + kMaxBufs;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile int32_t* abort_flag = reinterpret_cast<volatile int32_t*>(smem + kOffMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int bn = l.p[0].bn, bufs = 512 / bn;   // of every problem of the launch
+  const int units = num_units(l);
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
 
   if (threadIdx.x == 0) {
@@ -122,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(full + s, 1);
       mbar_init(empty + s, 1);
     }
-    for (int a = 0; a < kMaxBufs; ++a) {
+    for (int a = 0; a < 2; ++a) {
       mbar_init(tfull + a, 1);
       mbar_init(tempty + a, 2 * kNumEpiWarps);
     }
@@ -146,11 +162,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("fence.proxy.async.global;" ::: "memory");
     uint32_t stage = 0, phase = 0;
     bool ok = true, issued = false;
-    for (int t = pair; ok && t < l.tiles; t += pairs) {
-      const Tile o = dense::find_tile(l, t);
+    for (int t = pair; ok && t < units; t += pairs) {
+      const Unit x = find_unit(l, t);
+      const Tile& o = x.o;
       const Problem& p = l.p[o.p];
-      const int a0 = o.i * kTile + static_cast<int>(rank) * 128;
-      const int b0 = o.j * bn + static_cast<int>(rank) * (bn >> 1), tb = (o.j * bn) >> 8;
+      const int bn = x.bn;
+      const int a0 = o.i * kTile + static_cast<int>(rank) * 128, b0 = x.col + static_cast<int>(rank) * (bn >> 1);
       const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
       const uint32_t bytes = 4u * static_cast<uint32_t>(kABytes + bn * 64);
       for (int kb = k0; kb < k1; ++kb) {
@@ -163,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t bar = full0 + 8 * stage;
           if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
           load_terms(maps, p.a, o.z, a0, 128, o.i, kb, as, kABytes, bar);
-          load_terms(maps, p.b, o.z, b0, bn >> 1, tb, kb, as + 2 * kABytes, kBBytes, bar);
+          load_terms(maps, p.b, o.z, b0, bn >> 1, o.j, kb, as + 2 * kABytes, kBBytes, bar);
         }
         issued = true;
         if (++stage == kStages) {
@@ -187,10 +204,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       int acc = 0;
       uint32_t round = 0;
-      for (int t = pair; ok && t < l.tiles; t += pairs) {
-        const Tile o = dense::find_tile(l, t);
+      for (int t = pair; ok && t < units; t += pairs) {
+        const Unit x = find_unit(l, t);
+        const Tile& o = x.o;
         const Problem& p = l.p[o.p];
-        const int tb = (o.j * bn) >> 8;
         const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
         for (int kb = k0; ok && kb < k1; kb += kPiece) {
           const int n = min(kPiece, k1 - kb);
@@ -199,19 +216,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>(acc * bn);
+          const uint32_t d = tmem + static_cast<uint32_t>(acc * 256);
           for (int k = 0; k < n; ++k) {
             if (!mbar_poll_warp(full + stage, phase, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const bool amn = mn_at(p.a, o.i, kb + k), bmn = mn_at(p.b, tb, kb + k);
+            const bool amn = mn_at(p.a, o.i, kb + k), bmn = mn_at(p.b, o.j, kb + k);
             const uint64_t a_step = amn ? 2048 >> 4 : 32 >> 4, b_step = bmn ? 2048 >> 4 : 32 >> 4;
             const uint32_t at = smem_u32(smem + stage * kStageBytes);
             const uint64_t a = smem_desc(at, amn ? 8192 : 0, 1024, 2);
             const uint64_t b = smem_desc(at + 2 * kABytes, bmn ? 8192 : 0, 1024, 2);
-            const uint32_t idesc = dense::idesc_f16(false, amn, bmn, bn);
+            const uint32_t idesc = dense::idesc_f16(false, amn, bmn, x.bn);
             // the small products first: they lose nothing to a sum that is still small
             dense::mma_quad_warp(d, a + (kABytes >> 4), b, a_step, b_step, idesc, k > 0 ? 1u : 0u);
             dense::mma_quad_warp(d, a, b + (kBBytes >> 4), a_step, b_step, idesc, 1u);
@@ -223,10 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
           if (ok) tc2_commit_both_warp(tfull + acc);
-          if (++acc == bufs) {
-            acc = 0;
-            round ^= 1u;
-          }
+          round ^= static_cast<uint32_t>(acc);
+          acc ^= 1;
         }
       }
       tc2_commit_local_warp(drain);
@@ -245,25 +260,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     int acc = 0;
     uint32_t round = 0;
     bool ok = true;
-    for (int t = pair; ok && t < l.tiles; t += pairs) {
-      const Tile o = dense::find_tile(l, t);
+    for (int t = pair; ok && t < units; t += pairs) {
+      const Unit x = find_unit(l, t);
+      const Tile& o = x.o;
       const Problem& p = l.p[o.p];
+      const int half = x.bn >> 1, col = x.col + w.half * half;
+      w.row = o.i * kTile + static_cast<int>(rank) * 128 + 32 * quarter;
       float sums[128];
 #pragma unroll
       for (int i = 0; i < 128; ++i) sums[i] = 0.f;
       const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
-      Epi::ahead(l.e[o.p], o, bn, o.i * kTile + static_cast<int>(rank) * 128 + 32 * quarter, w);
+      Epi::ahead(l.e[o.p], o, w, col, half);
       for (int kb = k0; kb < k1; kb += kPiece) {
         if (!mbar_poll_warp(tfull + acc, round, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t at = tmem + static_cast<uint32_t>(acc * bn + w.half * (bn >> 1)) +
+        const uint32_t at = tmem + static_cast<uint32_t>(acc * 256 + w.half * half) +
                             (static_cast<uint32_t>(32 * quarter) << 16);
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
-          if (c < (bn >> 1)) {
+          if (c < half) {
             uint32_t v[32];
             dense::tmem_ld_x32(at + c, v);
             dense::tmem_wait(v);
@@ -274,14 +292,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(release + static_cast<uint32_t>(8 * acc));
-        if (++acc == bufs) {
-          acc = 0;
-          round ^= 1u;
-        }
+        round ^= static_cast<uint32_t>(acc);
+        acc ^= 1;
       }
       if (!ok) break;
-      w.row = o.i * kTile + static_cast<int>(rank) * 128 + 32 * quarter;
-      Epi::run(l.e[o.p], bn, o, w, maps, sums);
+      Epi::run(l.e[o.p], o, w, col, half, maps, sums);
     }
     if (lane == 0) dense::box_wait_all();
   }
@@ -302,9 +317,15 @@ cudaError_t resident_pairs(int num_sms, int* pairs) {
   static DeviceOnce cache;
   return dense::resident_pairs(terms_kernel<Epi>, kSmemBytes, cache, num_sms, pairs);
 }
+// A unit of 128 columns takes about 0.7 of the time of a whole tile: the last
+// round is cut in halves where they all fit into one.
 template <class Epi>
 cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, cudaStream_t s) {
-  return dense::launch(terms_kernel<Epi>, kSmemBytes, maps, l, pairs, s);
+  int tiles = 0;
+  for (int i = 0; i < l.problems; ++i) tiles += l.p[i].per_matrix * l.p[i].batch * l.p[i].splits;
+  const int rest = tiles % pairs;
+  l.whole = 2 * rest <= pairs ? tiles - rest : tiles;
+  return dense::launch(terms_kernel<Epi>, kSmemBytes, maps, l, pairs, s, 2 * tiles - l.whole);
 }
 
 }  // namespace terms
