@@ -27,6 +27,7 @@
 
 #include "dense.cuh"
 #include "entry.h"
+#include "muon.cuh"
 #include "terms.cuh"
 
 namespace moe {
@@ -38,41 +39,12 @@ using dense::Maps;
 using dense::Tile;
 
 constexpr uint64_t kTimeoutNs = 1000000000ull;
-constexpr int kPartSteps = 3;         // steps between two Gram matrices
+constexpr int kPartSteps = kMuonPartSteps;
+constexpr int kThreads = 256;
 
 // ------------------------------------------------------------ elementwise
-constexpr int kThreads = 256;
 constexpr int kChunk = 16384;         // elements of a block's share
 constexpr int64_t kL2Bytes = 100 << 20;   // of the 129 MB, what two readings in turn may count on
-
-struct Momentum {
-  const void* grad;
-  float* m;
-  const float* grad_scale;
-  float mu, rest;                     // mu, 1 - mu
-  int32_t bf16, nesterov;
-};
-
-__device__ __forceinline__ float grad_at(const Momentum& a, int64_t i, float gs) {
-  return gs * (a.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.grad)[i])
-                      : static_cast<const float*>(a.grad)[i]);
-}
-__device__ __forceinline__ float update_of(const Momentum& a, float m, float g) {
-  return a.nesterov ? fmaf(a.mu, m, a.rest * g) : m;
-}
-
-// Sum over the block in a fixed order; every thread gets it.
-__device__ __forceinline__ float block_sum(float v, float* warp_sums) {
-#pragma unroll
-  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-  if ((threadIdx.x & 31) == 0) warp_sums[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < kThreads / 32; ++i) s += warp_sums[i];
-  __syncthreads();
-  return s;
-}
 
 // The new momentum, and each chunk's sum of u^2 (matrix z, chunk c at
 // sums[z chunks + c]).
@@ -118,7 +90,7 @@ __global__ void __launch_bounds__(kThreads)
       s = fmaf(u, u, s);
     }
   }
-  s = block_sum(s, warp_sums);
+  s = block_sum<kThreads>(s, warp_sums);
   if (threadIdx.x == 0) sums[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = s;
 }
 
@@ -169,7 +141,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   float s = 0.f;
   for (int i = threadIdx.x; i < chunks; i += kThreads) s += sums[static_cast<int64_t>(z) * chunks + i];
-  s = block_sum(s, warp_sums);
+  s = block_sum<kThreads>(s, warp_sums);
   const float mul = scale / (sqrtf(s) + eps);
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -395,9 +367,8 @@ Shape shape_of(const moe_muon_tensor& t) {
   s.batch = 0;
   return s;
 }
-bool empty(const moe_muon_tensor& t) { return t.count == 0 || t.rows == 0 || t.cols == 0; }
 bool same(const moe_muon_tensor& t, const Shape& s) {
-  return !empty(t) && std::min(t.rows, t.cols) == s.m && std::max(t.rows, t.cols) == s.n;
+  return !muon_empty(t) && std::min(t.rows, t.cols) == s.m && std::max(t.rows, t.cols) == s.n;
 }
 int chunks_of(const Shape& s) {
   return static_cast<int>(dense::cdiv(static_cast<int64_t>(s.m) * s.n, kChunk));
@@ -574,13 +545,10 @@ int32_t update(const Group& gr, const Planes& q, const Planes& x) {
       terms::Problem& p = b.problem(tall ? s.m : s.n, tall ? s.n : s.m, t.count, s.mp / dense::kBK);
       MOE_TRY(b.operand(tall ? q : x, !tall, z, &p.a));
       MOE_TRY(b.operand(tall ? x : q, tall, z, &p.b));
-      const double size = gr.o->update_scale == MOE_MUON_RMS
-                              ? 0.2 * std::sqrt(static_cast<double>(std::max(t.rows, t.cols)))
-                              : std::sqrt(std::max(1.0, static_cast<double>(t.rows) / t.cols));
       e.p = t.param;
       e.copy = static_cast<__nv_bfloat16*>(t.param_bf16);
-      e.decay = static_cast<float>(1.0 - gr.o->lr * gr.o->weight_decay);
-      e.step = static_cast<float>(gr.o->lr * size / (static_cast<double>(q.scale) * x.scale));
+      e.decay = muon_decay(gr.o);
+      e.step = static_cast<float>(muon_step(gr.o, t) / (static_cast<double>(q.scale) * x.scale));
       e.rows = tall ? s.m : s.n;
       e.cols = tall ? s.n : s.m;
       z += t.count;
@@ -646,6 +614,9 @@ int32_t run_group(const Group& gr) {
       } else {
         const Planes next = square(k & 1 ? gr.w.qb : gr.w.qa, sc[k].q);
         MOE_TRY(add_symmetric(b, p, q, false, next, 1.0f, 0.f, 0.f));
+        // P Q and not P Q^T: what is left of Q's asymmetry belongs to the X that the
+        // next Gram matrix is taken of
+        b.l.p[b.l.problems - 1].b.turned = 1;
         q = next;
       }
       if (b.l.problems) MOE_TRY(run(b));
@@ -670,7 +641,7 @@ int32_t check_tensor(const moe_muon_tensor& t, int i, bool bf16) {
   if (t.count < 0 || t.rows < 0 || t.cols < 0)
     return entry_fail(MOE_ERR_INVALID_ARG, "tensor %d: a negative size", i);
   if (t.reserved) return entry_fail(MOE_ERR_INVALID_ARG, "tensor %d: reserved must be zero", i);
-  if (empty(t)) return MOE_OK;
+  if (muon_empty(t)) return MOE_OK;
   if (!t.param || !t.grad || !t.momentum)
     return entry_fail(MOE_ERR_INVALID_ARG, "tensor %d: param, grad or momentum is NULL", i);
   if (t.rows > MOE_MUON_MAX_SIDE || t.cols > MOE_MUON_MAX_SIDE || std::min(t.rows, t.cols) > MOE_MUON_MAX_SHORT)
@@ -692,8 +663,8 @@ int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_optio
     return entry_fail(MOE_ERR_INVALID_ARG, "update_scale %d unknown", o->update_scale);
   if (!(o->momentum >= 0 && o->momentum < 1))
     return entry_fail(MOE_ERR_INVALID_ARG, "momentum must be in [0, 1)");
-  if (!(o->eps > 0) || !std::isfinite(o->eps) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay))
-    return entry_fail(MOE_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite, eps > 0");
+  if (!(o->eps >= 1e-30) || !std::isfinite(o->eps) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay))
+    return entry_fail(MOE_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite, eps at least 1e-30");
   if (o->ns_steps < 1 || o->ns_steps > kMaxSteps)
     return entry_fail(MOE_ERR_INVALID_ARG, "ns_steps must be in [1, %d]", kMaxSteps);
   if (o->reserved[0] || o->reserved[1]) return entry_fail(MOE_ERR_INVALID_ARG, "reserved must be zero");
@@ -713,7 +684,7 @@ int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_optio
 template <class F>
 int32_t each_group(const moe_muon_tensor* t, int32_t count, F f) {
   for (int i = 0; i < count; ++i) {
-    if (empty(t[i])) continue;
+    if (muon_empty(t[i]) || muon_is_small(t[i])) continue;
     Shape s = shape_of(t[i]);
     bool seen = false;
     for (int j = 0; j < i && !seen; ++j) seen = same(t[j], s);
@@ -726,9 +697,9 @@ int32_t each_group(const moe_muon_tensor* t, int32_t count, F f) {
 }
 
 int32_t total_ws(const moe_muon_tensor* t, int32_t count, size_t* need) {
-  *need = kWsAlign;
+  *need = std::max(kWsAlign, muon_small_ws(t, count));
   return each_group(t, count, [&](const Shape& s) -> int32_t {
-    if (2 * s.batch * s.mp >= (int64_t(1) << 31) || s.batch * dense::cdiv(s.mp, 128) * dense::cdiv(s.np, 128) >= (int64_t(1) << 31))
+    if (2 * s.batch * s.mp >= (int64_t(1) << 31) || s.batch * chunks_of(s) >= (int64_t(1) << 31) || s.batch * dense::cdiv(s.mp, 128) * dense::cdiv(s.np, 128) >= (int64_t(1) << 31))
       return entry_fail(MOE_ERR_UNSUPPORTED, "too many matrices of %d x %d", s.m, s.n);
     *need = std::max(*need, group_ws(s).total);
     return MOE_OK;
@@ -736,6 +707,15 @@ int32_t total_ws(const moe_muon_tensor* t, int32_t count, size_t* need) {
 }
 
 }  // namespace
+
+bool muon_empty(const moe_muon_tensor& t) { return t.count == 0 || t.rows == 0 || t.cols == 0; }
+float muon_decay(const moe_muon_options* o) { return static_cast<float>(1.0 - o->lr * o->weight_decay); }
+double muon_step(const moe_muon_options* o, const moe_muon_tensor& t) {
+  const double rows = t.rows, cols = t.cols;
+  return o->lr * (o->update_scale == MOE_MUON_RMS ? 0.2 * std::sqrt(std::max(rows, cols))
+                                                  : std::sqrt(std::max(1.0, rows / cols)));
+}
+
 }  // namespace moe
 
 extern "C" size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count,
@@ -755,7 +735,7 @@ extern "C" int32_t moe_muon_step(const moe_muon_tensor* tensors, int32_t count, 
   MOE_TRY(check_call(tensors, count, o, &g.sc));
   MOE_TRY(total_ws(tensors, count, &need));
   bool any = false;
-  for (int i = 0; i < count; ++i) any = any || !empty(tensors[i]);
+  for (int i = 0; i < count; ++i) any = any || !muon_empty(tensors[i]);
   if (!any) return MOE_OK;
   if (!status) return entry_fail(MOE_ERR_INVALID_ARG, "status is NULL");
   if (!ptr_aligned(status, 4)) return entry_fail(MOE_ERR_MISALIGNED, "status must be 4-byte aligned");
@@ -774,6 +754,7 @@ extern "C" int32_t moe_muon_step(const moe_muon_tensor* tensors, int32_t count, 
   g.ws = static_cast<uint8_t*>(workspace);
   g.status = status;
   g.st = static_cast<cudaStream_t>(stream);
+  MOE_TRY(muon_small_step(tensors, count, o, g.ws, g.st));
   return each_group(tensors, count, [&](const Shape& s) -> int32_t {
     g.s = s;
     g.w = group_ws(s);

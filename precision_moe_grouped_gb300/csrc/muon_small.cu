@@ -1,0 +1,544 @@
+// muon_small.cu -- the orthogonalised step for matrices with a short side m of up
+// to 64 (pools of adapters, small heads): muon.cu's steps on m x m matrices, in
+// float on the CUDA cores.
+//
+// Tensor cores would compute tiles of 128 x 256 for matrices of 16 x 16.  Here a
+// matrix is a stream: a block takes a run of its columns (its long side), tile
+// by tile through shared memory, and m multiply-adds an element (m / 2 for a
+// Gram matrix) keep below the stream's time for m up to about 32.
+//   gram:  m <- mu m + (1 - mu) g, u; or u again and Y = Q u; each block's
+//          share of u u^T (whose trace is |u|^2) or Y Y^T
+//   steps: one block a matrix joins the shares in order and carries out up to
+//          three steps; Q <- P Q.  Q is kept transposed, as the products here are
+//          A B^T: with P Q^T instead, what rounding leaves of Q's asymmetry would
+//          not be that of the X whose Gram matrix follows (errors 6 to 20 times
+//          larger where a singular value is small)
+//   apply: p <- decay p - step Q u
+// All tensors of a size class go in one launch of each kernel.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "entry.h"
+#include "muon.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCap = 40;           // tensors of a launch: its kernel parameter stays below 4 KB
+constexpr int kTargetBlocks = 304; // two blocks an SM, all resident at once
+
+struct Entry {
+  Momentum mo;
+  float* p;
+  __nv_bfloat16* copy;
+  float step;
+  int32_t m, n, tall;
+  int32_t blocks;       // of a matrix
+  int32_t first_block;  // of the launch
+  int32_t first_matrix;
+};
+struct Table {
+  Entry e[kCap];
+  int32_t count, matrices;
+  float decay;
+};
+
+// MP: m rounded up to 16, 32 or 64.  A tile is MP x NC (4096 elements, 16 a
+// thread); in products with a tile a thread computes 4 x 4 elements, which
+// keeps shared memory's reads at two floats for four multiply-adds.
+template <int MP>
+struct Cfg {
+  static constexpr int NC = 4096 / MP;
+  static constexpr int TR = MP / 16;   // m x m products: TR x TR elements a thread
+  static constexpr int LD = NC + 4;    // rows 16 bytes apart modulo the banks
+  static constexpr int LDM = MP + 4;
+  static constexpr int PER = 16;
+  static constexpr int kGroup = MP * MP / 16;          // threads that hold one MP x MP sum
+  static constexpr int kGroups = kThreads / kGroup;    // each over its own columns
+  static_assert(kGroups * MP * MP <= MP * LD || kGroups == 1, "the groups' sums are joined in the tile's memory");
+};
+
+template <int MP>
+__device__ __forceinline__ void zero(float (&c)[Cfg<MP>::TR][Cfg<MP>::TR]) {
+#pragma unroll
+  for (int r = 0; r < Cfg<MP>::TR; ++r)
+#pragma unroll
+    for (int s = 0; s < Cfg<MP>::TR; ++s) c[r][s] = 0.f;
+}
+// This thread's rows i = (tid / 16) + 16 r and columns j = (tid % 16) + 16 s.
+__device__ __forceinline__ int ti() { return threadIdx.x >> 4; }
+__device__ __forceinline__ int tj() { return threadIdx.x & 15; }
+
+// c[i][j] += sum over k of a[i][k] b[j][k], k < K, rows ld apart.
+template <int MP, int K, int LD>
+__device__ __forceinline__ void dot_rows(const float* a, const float* b, float (&c)[Cfg<MP>::TR][Cfg<MP>::TR]) {
+  constexpr int TR = Cfg<MP>::TR;
+#pragma unroll 4
+  for (int k = 0; k < K; k += 4) {
+    float4 x[TR], y[TR];
+#pragma unroll
+    for (int r = 0; r < TR; ++r) {
+      x[r] = *reinterpret_cast<const float4*>(a + (ti() + 16 * r) * LD + k);
+      y[r] = *reinterpret_cast<const float4*>(b + (tj() + 16 * r) * LD + k);
+    }
+#pragma unroll
+    for (int r = 0; r < TR; ++r)
+#pragma unroll
+      for (int s = 0; s < TR; ++s)
+        c[r][s] = fmaf(x[r].x, y[s].x, fmaf(x[r].y, y[s].y, fmaf(x[r].z, y[s].z, fmaf(x[r].w, y[s].w, c[r][s]))));
+  }
+}
+template <int MP>
+__device__ __forceinline__ void put(float* to, const float (&c)[Cfg<MP>::TR][Cfg<MP>::TR]) {
+#pragma unroll
+  for (int r = 0; r < Cfg<MP>::TR; ++r)
+#pragma unroll
+    for (int s = 0; s < Cfg<MP>::TR; ++s) to[(ti() + 16 * r) * Cfg<MP>::LDM + tj() + 16 * s] = c[r][s];
+}
+
+// What a block works on.
+struct Work {
+  int32_t e, z, part;
+};
+__device__ __forceinline__ Work find_block(const Table& t, int b) {
+  Work w;
+  w.e = 0;
+  while (w.e + 1 < t.count && b >= t.e[w.e + 1].first_block) ++w.e;
+  b -= t.e[w.e].first_block;
+  w.z = b / t.e[w.e].blocks;
+  w.part = b - w.z * t.e[w.e].blocks;
+  return w;
+}
+
+// This thread's 16 elements of the tile at column n0: element k at row i + k di
+// and column j + k dj of X, `at + k step` in the matrix.  Elements outside of the
+// matrix read its first one: loads without branches stay in flight together.
+template <int MP>
+struct Elements {
+  int i, j, di, dj, m, cols;
+  int at, step;   // below 2^26: m <= 64, n <= 2^20
+
+  __device__ __forceinline__ Elements(const Entry& e, int n0, int n1) : m(e.m), cols(n1 - n0) {
+    constexpr int NC = Cfg<MP>::NC;
+    const int t = threadIdx.x;
+    if (e.tall) {
+      i = t % MP, j = t / MP, di = 0, dj = kThreads / MP;
+      at = (n0 + j) * e.m + i;
+      step = dj * e.m;
+    } else {
+      i = t / NC, j = t % NC, di = kThreads / NC, dj = 0;
+      at = i * e.n + n0 + j;
+      step = di * e.n;
+    }
+  }
+  __device__ __forceinline__ bool in(int k) const { return i + k * di < m && j + k * dj < cols; }
+  __device__ __forceinline__ int where(int k) const { return in(k) ? at + k * step : 0; }
+  __device__ __forceinline__ int in_tile(int k) const { return (i + k * di) * Cfg<MP>::LD + j + k * dj; }
+};
+
+template <bool BF16>
+using Grad = typename std::conditional<BF16, __nv_bfloat16, float>::type;
+
+// A tile's momentum and gradient, from memory to registers ...
+template <int MP, bool BF16>
+struct Fetched {
+  float m[Cfg<MP>::PER];
+  Grad<BF16> g[Cfg<MP>::PER];
+
+  __device__ __forceinline__ void fetch(const Elements<MP>& x, const float* mp, const Grad<BF16>* gp, bool need_g) {
+#pragma unroll
+    for (int k = 0; k < Cfg<MP>::PER; ++k) m[k] = mp[x.where(k)];
+    if (need_g) {
+#pragma unroll
+      for (int k = 0; k < Cfg<MP>::PER; ++k) g[k] = gp[x.where(k)];
+    }
+  }
+  // ... and u from there to shared memory, zero outside of the matrix; FIRST:
+  // with the momentum's update.
+  template <bool FIRST>
+  __device__ __forceinline__ void put(const Elements<MP>& x, const Momentum& mo, float* mp, float gs, float* u) const {
+#pragma unroll
+    for (int k = 0; k < Cfg<MP>::PER; ++k) {
+      float mv = m[k];
+      const float gv = FIRST || mo.nesterov ? static_cast<float>(g[k]) * gs : 0.f;
+      if (FIRST) {
+        mv = fmaf(mo.mu, mv, mo.rest * gv);
+        if (x.in(k)) mp[x.where(k)] = mv;
+      }
+      u[x.in_tile(k)] = x.in(k) ? update_of(mo, mv, gv) : 0.f;
+    }
+  }
+};
+
+// c[r][s] += sum over this group's columns of u[i][k] u[j][k] for the thread's
+// rows i = ti + MP/4 r and j = tj + MP/4 s.
+template <int MP>
+__device__ __forceinline__ void gram_tile(const float* u, float (&c)[4][4]) {
+  using C = Cfg<MP>;
+  const int t = threadIdx.x % C::kGroup, g = threadIdx.x / C::kGroup;
+  const float* a = u + (t / (MP / 4)) * C::LD + g * (C::NC / C::kGroups);
+  const float* b = u + (t % (MP / 4)) * C::LD + g * (C::NC / C::kGroups);
+#pragma unroll 4
+  for (int k = 0; k < C::NC / C::kGroups; k += 4) {
+    float4 x[4], y[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      x[r] = *reinterpret_cast<const float4*>(a + r * (MP / 4) * C::LD + k);
+      y[r] = *reinterpret_cast<const float4*>(b + r * (MP / 4) * C::LD + k);
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        c[r][s] = fmaf(x[r].x, y[s].x, fmaf(x[r].y, y[s].y, fmaf(x[r].z, y[s].z, fmaf(x[r].w, y[s].w, c[r][s]))));
+  }
+}
+// The groups' sums joined in order, through the tile's memory, to `to`.
+template <int MP>
+__device__ __forceinline__ void put_gram(float (&c)[4][4], float* u, float* to) {
+  using C = Cfg<MP>;
+  const int t = threadIdx.x % C::kGroup, g = threadIdx.x / C::kGroup;
+  float* at = C::kGroups == 1 ? to : u + g * MP * MP;
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+#pragma unroll
+    for (int s = 0; s < 4; ++s) at[(t / (MP / 4) + MP / 4 * r) * MP + t % (MP / 4) + MP / 4 * s] = c[r][s];
+  if (C::kGroups == 1) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < MP * MP; i += kThreads) {
+    float v = 0.f;
+#pragma unroll
+    for (int j = 0; j < C::kGroups; ++j) v += u[j * MP * MP + i];
+    to[i] = v;
+  }
+}
+
+// u <- Q u for the tile, four rows and columns a thread; q holds Q^T.
+template <int MP>
+__device__ __forceinline__ void mul_tile(const float* q, float* u) {
+  using C = Cfg<MP>;
+  const int j = (threadIdx.x % (C::NC / 4)) * 4, i = (threadIdx.x / (C::NC / 4)) * 4;
+  float4 y[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) y[r] = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int k = 0; k < MP; ++k) {
+    const float4 v = *reinterpret_cast<const float4*>(u + k * C::LD + j);
+    const float4 w4 = *reinterpret_cast<const float4*>(q + k * C::LDM + i);
+    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      y[r].x = fmaf(w[r], v.x, y[r].x);
+      y[r].y = fmaf(w[r], v.y, y[r].y);
+      y[r].z = fmaf(w[r], v.z, y[r].z);
+      y[r].w = fmaf(w[r], v.w, y[r].w);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(u + (i + r) * C::LD + j) = y[r];
+  __syncthreads();
+}
+template <int MP>
+__device__ __forceinline__ void load_q(const float* from, float* q) {
+  for (int k = threadIdx.x; k < MP * MP; k += kThreads) q[(k / MP) * Cfg<MP>::LDM + k % MP] = from[k];
+}
+
+template <int MP>
+__device__ __forceinline__ void columns_of(const Entry& e, int part, int* n0, int* n1) {
+  const int tiles = (e.n + Cfg<MP>::NC - 1) / Cfg<MP>::NC;
+  *n0 = static_cast<int>(static_cast<int64_t>(tiles) * part / e.blocks) * Cfg<MP>::NC;
+  *n1 = min(e.n, static_cast<int>(static_cast<int64_t>(tiles) * (part + 1) / e.blocks) * Cfg<MP>::NC);
+}
+
+// Each block's share of u u^T (FIRST) or of Y Y^T, Y = Q u.
+template <int MP, bool FIRST, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
+    muon_small_gram_kernel(const __grid_constant__ Table t, const float* qs, float* shares) {
+  using C = Cfg<MP>;
+  __shared__ __align__(16) float u[MP * C::LD];
+  __shared__ __align__(16) float q[FIRST ? 4 : MP * C::LDM];
+  griddep_wait();
+  griddep_launch_dependents();
+  const Work w = find_block(t, blockIdx.x);
+  const Entry& e = t.e[w.e];
+  const float gs = e.mo.grad_scale ? __ldg(e.mo.grad_scale) : 1.0f;
+  const int64_t base = static_cast<int64_t>(w.z) * e.m * e.n;
+  if (!FIRST) load_q<MP>(qs + static_cast<int64_t>(e.first_matrix + w.z) * MP * MP, q);
+  float* mp = e.mo.m + base;
+  const Grad<BF16>* gp = static_cast<const Grad<BF16>*>(e.mo.grad) + base;
+  const bool need_g = FIRST || e.mo.nesterov;
+  int n0, n1;
+  columns_of<MP>(e, w.part, &n0, &n1);
+  float c[4][4] = {};
+  Fetched<MP, BF16> f;
+  f.fetch(Elements<MP>(e, n0, n1), mp, gp, need_g);
+  for (; n0 < n1; n0 += C::NC) {
+    f.template put<FIRST>(Elements<MP>(e, n0, n1), e.mo, mp, gs, u);
+    __syncthreads();
+    if (n0 + C::NC < n1) f.fetch(Elements<MP>(e, n0 + C::NC, n1), mp, gp, need_g);   // under the products
+    if (!FIRST) mul_tile<MP>(q, u);
+    gram_tile<MP>(u, c);
+    __syncthreads();
+  }
+  put_gram<MP>(c, u, shares + static_cast<int64_t>(blockIdx.x) * MP * MP);
+}
+
+// One matrix a block: `n` steps from G, the sum of its shares.
+template <int MP, bool FIRST>
+__global__ void __launch_bounds__(kThreads)
+    muon_small_steps_kernel(const __grid_constant__ Table t, const float* shares, float* qs, int n, float ca,
+                            float cb, float cc, float eps) {
+  using C = Cfg<MP>;
+  extern __shared__ __align__(16) float mem[];
+  float *g = mem, *p = g + MP * C::LDM, *q = p + MP * C::LDM;
+  griddep_wait();
+  griddep_launch_dependents();
+  int k = 0;
+  while (k + 1 < t.count && static_cast<int>(blockIdx.x) >= t.e[k + 1].first_matrix) ++k;
+  const Entry& e = t.e[k];
+  const int z = static_cast<int>(blockIdx.x) - e.first_matrix;
+  const float* from = shares + (static_cast<int64_t>(e.first_block) + static_cast<int64_t>(z) * e.blocks) * MP * MP;
+  float* to = qs + static_cast<int64_t>(blockIdx.x) * MP * MP;
+  if (!FIRST) load_q<MP>(to, q);
+  float c[C::TR][C::TR];
+  zero<MP>(c);
+#pragma unroll 4
+  for (int b = 0; b < e.blocks; ++b)
+#pragma unroll
+    for (int r = 0; r < C::TR; ++r)
+#pragma unroll
+      for (int s = 0; s < C::TR; ++s)
+        c[r][s] += from[static_cast<int64_t>(b) * MP * MP + (ti() + 16 * r) * MP + tj() + 16 * s];
+  put<MP>(g, c);
+  __syncthreads();
+  float inv = 1.0f;
+  if (FIRST) {   // |u|^2 is the trace
+    float s = 0.f;
+    for (int i = 0; i < e.m; ++i) s += g[i * C::LDM + i];
+    inv = 1.0f / (sqrtf(s) + eps);
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < C::TR; ++r)
+#pragma unroll
+      for (int v = 0; v < C::TR; ++v) c[r][v] = (c[r][v] * inv) * inv;
+    put<MP>(g, c);
+    __syncthreads();
+  }
+  for (int step = 0; step < n; ++step) {
+    zero<MP>(c);
+    dot_rows<MP, MP, C::LDM>(g, g, c);
+#pragma unroll
+    for (int r = 0; r < C::TR; ++r)
+#pragma unroll
+      for (int s = 0; s < C::TR; ++s) {
+        const int i = ti() + 16 * r, j = tj() + 16 * s;
+        c[r][s] = fmaf(cc, c[r][s], cb * g[i * C::LDM + j]) + (i == j && i < e.m ? ca : 0.f);
+      }
+    put<MP>(p, c);
+    __syncthreads();
+    if (FIRST && step == 0) {   // Q = P / (|u| + eps)
+#pragma unroll
+      for (int r = 0; r < C::TR; ++r)
+#pragma unroll
+        for (int s = 0; s < C::TR; ++s) c[r][s] *= inv;
+    } else {
+      zero<MP>(c);
+      dot_rows<MP, MP, C::LDM>(q, p, c);   // Q^T P^T
+      __syncthreads();
+    }
+    put<MP>(q, c);
+    if (step + 1 < n) {   // G <- (P G) P
+      zero<MP>(c);
+      dot_rows<MP, MP, C::LDM>(p, g, c);
+      __syncthreads();
+      put<MP>(g, c);
+      __syncthreads();
+      zero<MP>(c);
+      dot_rows<MP, MP, C::LDM>(g, p, c);
+      __syncthreads();
+      put<MP>(g, c);
+    }
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < MP * MP; i += kThreads) to[i] = q[(i / MP) * C::LDM + i % MP];
+}
+
+// p <- decay p - step Q u, and the copy.
+template <int MP, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
+    muon_small_apply_kernel(const __grid_constant__ Table t, const float* qs) {
+  using C = Cfg<MP>;
+  __shared__ __align__(16) float u[MP * C::LD];
+  __shared__ __align__(16) float q[MP * C::LDM];
+  griddep_wait();
+  const Work w = find_block(t, blockIdx.x);
+  const Entry& e = t.e[w.e];
+  const float gs = e.mo.grad_scale ? __ldg(e.mo.grad_scale) : 1.0f;
+  const int64_t base = static_cast<int64_t>(w.z) * e.m * e.n;
+  load_q<MP>(qs + static_cast<int64_t>(e.first_matrix + w.z) * MP * MP, q);
+  float *mp = e.mo.m + base, *p = e.p + base;
+  const Grad<BF16>* gp = static_cast<const Grad<BF16>*>(e.mo.grad) + base;
+  __nv_bfloat16* copy = e.copy + base;
+  int n0, n1;
+  columns_of<MP>(e, w.part, &n0, &n1);
+  Fetched<MP, BF16> f;
+  f.fetch(Elements<MP>(e, n0, n1), mp, gp, e.mo.nesterov);
+  for (; n0 < n1; n0 += C::NC) {
+    const Elements<MP> x(e, n0, n1);
+    f.template put<false>(x, e.mo, mp, gs, u);
+    float pv[C::PER];
+#pragma unroll
+    for (int k = 0; k < C::PER; ++k) pv[k] = p[x.where(k)];
+    __syncthreads();
+    mul_tile<MP>(q, u);
+    if (n0 + C::NC < n1) f.fetch(Elements<MP>(e, n0 + C::NC, n1), mp, gp, e.mo.nesterov);
+#pragma unroll
+    for (int k = 0; k < C::PER; ++k) {
+      const float v = fmaf(-e.step, u[x.in_tile(k)], t.decay * pv[k]);
+      if (x.in(k)) {
+        p[x.where(k)] = v;
+        if (e.copy) copy[x.where(k)] = __float2bfloat16_rn(v);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+int size_class(const moe_muon_tensor& t) {
+  const int m = std::min(t.rows, t.cols);
+  return m <= 16 ? 16 : m <= 32 ? 32 : 64;
+}
+
+// A launch's tensors: those of one class from `at` on, as many as fit.  Returns
+// the blocks.
+constexpr int64_t kMaxBlocks = int64_t(1) << 22;
+int64_t tiles_of(const moe_muon_tensor& t) {
+  const int nc = 4096 / size_class(t);
+  return (std::max(t.rows, t.cols) + nc - 1) / nc;
+}
+
+struct Batch {
+  int32_t index[kCap];
+  int32_t count;
+  int64_t matrices, blocks;
+  int64_t tiles;   // of a block, at most
+};
+int64_t blocks_of(const moe_muon_tensor& t, const Batch& b) { return (tiles_of(t) + b.tiles - 1) / b.tiles; }
+
+// The next batch of class mp at or after *at (a tensor's index); false: none.
+// Its blocks take as few tiles each as leaves all of them resident at once.
+bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Batch* b) {
+  b->count = 0;
+  b->matrices = 0;
+  int64_t all = 0, most = 1;
+  for (; *at < count && b->count < kCap; ++*at) {
+    if (muon_empty(t[*at]) || !muon_is_small(t[*at]) || size_class(t[*at]) != mp) continue;
+    if (b->count && b->matrices + t[*at].count > kMaxBlocks) break;
+    b->index[b->count++] = *at;
+    b->matrices += t[*at].count;
+    all += t[*at].count * tiles_of(t[*at]);
+    most = std::max(most, tiles_of(t[*at]));
+  }
+  for (b->tiles = std::min(most, std::max<int64_t>(1, (all + kTargetBlocks - 1) / kTargetBlocks));; ++b->tiles) {
+    b->blocks = 0;
+    for (int i = 0; i < b->count; ++i) b->blocks += t[b->index[i]].count * blocks_of(t[b->index[i]], *b);
+    if (b->blocks <= kTargetBlocks || b->tiles >= most) break;
+  }
+  return b->count > 0;
+}
+
+struct SmallWs {
+  size_t shares, q, total;
+};
+SmallWs small_ws(const Batch& b, int mp) {
+  SmallWs w;
+  w.shares = 0;
+  w.q = ws_up(4ull * b.blocks * mp * mp);
+  w.total = w.q + ws_up(4ull * b.matrices * mp * mp);
+  return w;
+}
+
+template <int MP, bool BF16>
+int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_options* o, uint8_t* ws,
+                  cudaStream_t st) {
+  const SmallWs w = small_ws(b, MP);
+  float* shares = reinterpret_cast<float*>(ws + w.shares);
+  float* qs = reinterpret_cast<float*>(ws + w.q);
+  Table tab = {};
+  tab.count = b.count;
+  tab.matrices = static_cast<int32_t>(b.matrices);
+  tab.decay = muon_decay(o);
+  int64_t blocks = 0, matrices = 0;
+  for (int i = 0; i < b.count; ++i) {
+    const moe_muon_tensor& x = t[b.index[i]];
+    Entry& e = tab.e[i];
+    e.mo = {x.grad, x.momentum, o->grad_scale, static_cast<float>(o->momentum),
+            static_cast<float>(1.0 - o->momentum), o->grad_dtype == MOE_DTYPE_BF16, o->nesterov};
+    e.p = x.param;
+    e.copy = static_cast<__nv_bfloat16*>(x.param_bf16);
+    e.step = static_cast<float>(muon_step(o, x));
+    e.m = std::min(x.rows, x.cols);
+    e.n = std::max(x.rows, x.cols);
+    e.tall = x.rows > x.cols;
+    e.blocks = static_cast<int32_t>(blocks_of(x, b));
+    e.first_block = static_cast<int32_t>(blocks);
+    e.first_matrix = static_cast<int32_t>(matrices);
+    blocks += x.count * static_cast<int64_t>(e.blocks);
+    matrices += x.count;
+  }
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+  constexpr int kSteps = 3 * MP * Cfg<MP>::LDM * 4;
+  static DeviceOnce once_first, once_next;
+  MOE_CUDA(set_smem_limit_once(muon_small_steps_kernel<MP, true>, kSteps, once_first));
+  MOE_CUDA(set_smem_limit_once(muon_small_steps_kernel<MP, false>, kSteps, once_next));
+  const float a = static_cast<float>(o->coefficients[0]), c1 = static_cast<float>(o->coefficients[1]),
+              c2 = static_cast<float>(o->coefficients[2]), eps = static_cast<float>(o->eps);
+  for (int done = 0; done < o->ns_steps; done += kMuonPartSteps) {
+    const int n = std::min(kMuonPartSteps, o->ns_steps - done);
+    const dim3 each(static_cast<unsigned>(matrices));
+    if (done == 0) {
+      MOE_CUDA(launch_pdl(muon_small_gram_kernel<MP, true, BF16>, grid, block, 0, st, tab,
+                          static_cast<const float*>(qs), shares));
+      MOE_CUDA(launch_pdl(muon_small_steps_kernel<MP, true>, each, block, kSteps, st, tab,
+                          static_cast<const float*>(shares), qs, n, a, c1, c2, eps));
+    } else {
+      MOE_CUDA(launch_pdl(muon_small_gram_kernel<MP, false, BF16>, grid, block, 0, st, tab,
+                          static_cast<const float*>(qs), shares));
+      MOE_CUDA(launch_pdl(muon_small_steps_kernel<MP, false>, each, block, kSteps, st, tab,
+                          static_cast<const float*>(shares), qs, n, a, c1, c2, eps));
+    }
+  }
+  MOE_CUDA(launch_pdl(muon_small_apply_kernel<MP, BF16>, grid, block, 0, st, tab, static_cast<const float*>(qs)));
+  return MOE_OK;
+}
+
+}  // namespace
+
+bool muon_is_small(const moe_muon_tensor& t) { return std::min(t.rows, t.cols) <= kMuonSmall; }
+
+size_t muon_small_ws(const moe_muon_tensor* t, int32_t count) {
+  size_t need = 0;
+  Batch b;
+  for (int mp : {16, 32, 64})
+    for (int32_t at = 0; next_batch(t, count, mp, &at, &b);) need = std::max(need, small_ws(b, mp).total);
+  return need;
+}
+
+int32_t muon_small_step(const moe_muon_tensor* t, int32_t count, const moe_muon_options* o, uint8_t* ws,
+                        cudaStream_t st) {
+  Batch b;
+  const bool bf16 = o->grad_dtype == MOE_DTYPE_BF16;
+  auto run = [&](auto f, auto g) { return bf16 ? g(t, b, o, ws, st) : f(t, b, o, ws, st); };
+  for (int mp : {16, 32, 64})
+    for (int32_t at = 0; next_batch(t, count, mp, &at, &b);)
+      MOE_TRY(mp == 16   ? run(run_batch<16, false>, run_batch<16, true>)
+              : mp == 32 ? run(run_batch<32, false>, run_batch<32, true>)
+                         : run(run_batch<64, false>, run_batch<64, true>));
+  return MOE_OK;
+}
+
+}  // namespace moe

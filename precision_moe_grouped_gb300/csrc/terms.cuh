@@ -51,6 +51,7 @@ struct Operand {
   int32_t hi, lo;         // rows of the first matrix's terms
   int32_t batch;          // rows between matrices
   int32_t mn, sym, diag;  // MN-major throughout; symmetric; map of the diagonal blocks, or 0 for none
+  int32_t turned;         // symmetric, diagonal blocks read transposed (they are symmetric but for roundings)
 };
 struct Problem {
   Operand a, b;
@@ -92,7 +93,7 @@ __device__ __forceinline__ Unit find_unit(const L& l, int u) {
 
 // Whether operand o's K block kb is read MN-major by a tile at row block tr.
 __device__ __forceinline__ bool mn_at(const Operand& o, int tr, int kb) {
-  return o.mn || (o.sym && (kb >> 2) < tr);
+  return o.mn || (o.sym && (kb >> 2) < tr + o.turned);
 }
 
 // Both terms of one operand: 64 or 128 rows (or columns) from `at`, K block kb.
