@@ -43,20 +43,20 @@ constexpr int kPartSteps = kMuonPartSteps;
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------ elementwise
-constexpr int kChunk = 16384;         // elements of a block's share
+constexpr int kChunk = 16384, kChunkSmall = 2048;   // elements of a block's share
 constexpr int64_t kL2Bytes = 100 << 20;   // of the 129 MB, what two readings in turn may count on
 
 // The new momentum, and each chunk's sum of u^2 (matrix z, chunk c at
 // sums[z chunks + c]).
 __global__ void __launch_bounds__(kThreads)
-    muon_momentum_kernel(const Momentum a, int64_t size, int vec, float* sums) {
+    muon_momentum_kernel(const Momentum a, int64_t size, int chunk, int vec, float* sums) {
   __shared__ float warp_sums[kThreads / 32];
   griddep_wait();
   griddep_launch_dependents();
   const float gs = a.grad_scale ? __ldg(a.grad_scale) : 1.0f;
   const int64_t base = static_cast<int64_t>(blockIdx.y) * size;
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * kChunk;
-  const int64_t i1 = i0 + kChunk < size ? i0 + kChunk : size;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x) * chunk;
+  const int64_t i1 = i0 + chunk < size ? i0 + chunk : size;
   float s = 0.f;
   if (vec) {
 #pragma unroll 4
@@ -82,16 +82,40 @@ __global__ void __launch_bounds__(kThreads)
       *reinterpret_cast<float4*>(a.m + base + i) = m;
     }
   } else {
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-      const float g = grad_at(a, base + i, gs);
-      const float m = fmaf(a.mu, a.m[base + i], a.rest * g);
-      a.m[base + i] = m;
-      const float u = update_of(a, m, g);
-      s = fmaf(u, u, s);
+    // eight loads of each in flight; beyond the end the last element, unused
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += 8 * kThreads) {
+      float g[8], m[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int64_t at = base + (i + k * kThreads < i1 ? i + k * kThreads : i1 - 1);
+        m[k] = a.m[at];
+        g[k] = grad_at(a, at, gs);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (i + k * kThreads < i1) {
+          m[k] = fmaf(a.mu, m[k], a.rest * g[k]);
+          a.m[base + i + k * kThreads] = m[k];
+          const float u = update_of(a, m[k], g[k]);
+          s = fmaf(u, u, s);
+        }
+      }
     }
   }
   s = block_sum<kThreads>(s, warp_sums);
   if (threadIdx.x == 0) sums[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = s;
+}
+
+// Four neighbours as hi and lo terms.
+__device__ __forceinline__ void put_terms(const float (&v)[4], __half* to, int64_t lo_off) {
+  uint2 hi, lo;
+  hi.x = dense::pack_f16(v[0], v[1]);
+  hi.y = dense::pack_f16(v[2], v[3]);
+  const float2 p = dense::unpack_f16(hi.x), q = dense::unpack_f16(hi.y);
+  lo.x = dense::pack_f16(v[0] - p.x, v[1] - p.y);
+  lo.y = dense::pack_f16(v[2] - q.x, v[3] - q.y);
+  *reinterpret_cast<uint2*>(to) = hi;
+  *reinterpret_cast<uint2*>(to + lo_off) = lo;
 }
 
 // X0's planes: hi and lo fp16 terms of scale * u / (|u| + eps), [mp][np] per
@@ -163,17 +187,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int64_t out = (static_cast<int64_t>(z) * mp + blockIdx.y * kSide + ty) * np + blockIdx.x * kSide + tx;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint2 hi, lo;
-    hi.x = dense::pack_f16(mv[i][0], mv[i][1]);
-    hi.y = dense::pack_f16(mv[i][2], mv[i][3]);
-    const float2 p = dense::unpack_f16(hi.x), q = dense::unpack_f16(hi.y);
-    lo.x = dense::pack_f16(mv[i][0] - p.x, mv[i][1] - p.y);
-    lo.y = dense::pack_f16(mv[i][2] - q.x, mv[i][3] - q.y);
-    __half* to = planes + out + static_cast<int64_t>(16 * i) * np;
-    *reinterpret_cast<uint2*>(to) = hi;
-    *reinterpret_cast<uint2*>(to + lo_off) = lo;
-  }
+  for (int i = 0; i < 4; ++i) put_terms(mv[i], planes + out + static_cast<int64_t>(16 * i) * np, lo_off);
 }
 
 // -------------------------------------------------------------- epilogues
@@ -243,6 +257,63 @@ struct EpiPlanes {
     }
   }
 };
+
+// A share of a long sum, in float: row r of share s of matrix z at row
+// (s batch + z) rows + r.
+struct EpiShare {
+  struct Args {
+    int32_t map, rows, batch;   // rows: a multiple of 64
+  };
+  static __device__ __forceinline__ void ahead(const Args&, const Tile&, const EpiWarp&, int, int) {}
+  static __device__ __forceinline__ void run(const Args& a, const Tile& o, const EpiWarp& w, int col0, int n,
+                                             const Maps& maps, float (&d)[128]) {
+    if (w.row >= a.rows) return;
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      if (c >= n || col0 + c >= a.rows) continue;
+      if (w.lane == 0) dense::box_wait_read();
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *dense::box_piece(w.box, w.lane, i) =
+            make_uint4(__float_as_uint(d[c + 4 * i]), __float_as_uint(d[c + 4 * i + 1]),
+                       __float_as_uint(d[c + 4 * i + 2]), __float_as_uint(d[c + 4 * i + 3]));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (w.lane == 0)
+        dense::box_store(&maps.m[a.map], w.box, col0 + c, (o.s * a.batch + o.z) * a.rows + w.row);
+    }
+  }
+};
+
+// The shares joined in order: G's planes (and its diagonal blocks + h I), as
+// EpiPlanes stores them.  Four columns a thread.
+__global__ void __launch_bounds__(kThreads)
+    muon_join_kernel(const float* shares, int splits, int64_t batch, int mp, int m, float c, float h, __half* g,
+                     __half* diag) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t row = i / (mp / 4);   // of all matrices
+  if (row >= batch * mp) return;
+  const int col = static_cast<int>(i - row * (mp / 4)) * 4, r = static_cast<int>(row % mp);
+  const int side = (col >> 8) - (r >> 8);
+  if (side < 0) return;
+  float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(shares + (s * batch * mp + row) * mp + col);
+    v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+  }
+  float d[4] = {v.x * c, v.y * c, v.z * c, v.w * c};
+  put_terms(d, g + row * mp + col, batch * mp * mp);
+  if (side == 0) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (col + k == r && r < m) d[k] += h;
+    put_terms(d, diag + row * dense::kTile + (col & 255), batch * mp * dense::kTile);
+  }
+}
 
 // p <- decay p - step D, and the copy.  D's rows run along p's contiguous side
 // (element (r, c) of D at p[c rows + r]), so that a warp's 32 rows are 128 bytes.
@@ -370,12 +441,28 @@ Shape shape_of(const moe_muon_tensor& t) {
 bool same(const moe_muon_tensor& t, const Shape& s) {
   return !muon_empty(t) && std::min(t.rows, t.cols) == s.m && std::max(t.rows, t.cols) == s.n;
 }
+// Blocks' shares: long ones, unless they would leave SMs idle.
+int chunk_of(const Shape& s) {
+  return static_cast<int64_t>(s.m) * s.n * s.batch >= int64_t(600) * kChunk ? kChunk : kChunkSmall;
+}
 int chunks_of(const Shape& s) {
-  return static_cast<int>(dense::cdiv(static_cast<int64_t>(s.m) * s.n, kChunk));
+  return static_cast<int>(dense::cdiv(static_cast<int64_t>(s.m) * s.n, chunk_of(s)));
+}
+
+// Tiles on and above the diagonal.
+int64_t upper_tiles(int64_t mp) {
+  const int64_t n = dense::cdiv(mp, dense::kTile);
+  return n * (n + 1) / 2;
+}
+// Shares of the sum over the long side, of at least four K blocks, where the
+// halves of X X^T's tiles leave half of the pairs without one.
+int gram_splits(const Shape& s) {
+  const int64_t units = 2 * upper_tiles(s.mp) * s.batch, kb = s.np / dense::kBK;
+  return static_cast<int>(std::max<int64_t>(1, std::min(dense::kPlanPairs / units, kb / 4)));
 }
 
 struct GroupWs {
-  size_t sums, x, x1, g, h, s, p, qa, qb, total;
+  size_t sums, x, x1, g, h, s, p, qa, qb, shares, total;
 };
 GroupWs group_ws(const Shape& s) {
   GroupWs w = {};
@@ -395,6 +482,8 @@ GroupWs group_ws(const Shape& s) {
   w.p = take(small);
   w.qa = take(small);
   w.qb = take(small);
+  const int splits = gram_splits(s);
+  w.shares = take(splits > 1 ? static_cast<size_t>(splits) * small : 0);
   w.total = at;
   return w;
 }
@@ -410,7 +499,7 @@ struct Group {
   Scales sc;
   int32_t* status;
   cudaStream_t st;
-  int pairs_planes, pairs_update;
+  int pairs_planes, pairs_update, pairs_share;
 };
 
 // A matrix [rows of the batch][ld] as planes, times `scale`.
@@ -421,12 +510,6 @@ struct Planes {
   bool sym;
   __half* diag;   // G's diagonal blocks + (b / c) I, or null
 };
-
-// Tiles on and above the diagonal.
-int64_t upper_tiles(int64_t mp) {
-  const int64_t n = dense::cdiv(mp, dense::kTile);
-  return n * (n + 1) / 2;
-}
 
 // A launch in the making.
 template <class Epi>
@@ -513,6 +596,33 @@ int32_t symmetric(const Group& gr, const Planes& x, const Planes& y, bool use_di
   return run(b);
 }
 
+// G = X X^T with its second diagonal blocks (+ ratio I), by shares of the long
+// side where there are few tiles.
+int32_t gram(const Group& gr, const Planes& x, const Planes& g, float ratio) {
+  const Shape& s = gr.s;
+  const int splits = gram_splits(s);
+  if (splits == 1) return symmetric(gr, x, x, false, g, 1.0f, 0.f, ratio);
+  Build<EpiShare> b(gr);
+  float* shares = reinterpret_cast<float*>(gr.ws + gr.w.shares);
+  terms::Problem& p = b.problem(s.mp, s.mp, s.batch, s.np / dense::kBK);
+  p.upper = 1;
+  p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp));
+  p.kb_split = static_cast<int32_t>(dense::cdiv(p.kb, splits));
+  p.splits = static_cast<int32_t>(dense::cdiv(p.kb, p.kb_split));
+  MOE_TRY(b.operand(x, false, 0, &p.a));
+  p.b = p.a;
+  EpiShare::Args& e = b.l.e[0];
+  e.map = b.l.maps++;
+  e.rows = s.mp;
+  e.batch = static_cast<int32_t>(s.batch);
+  MOE_TRY(dense::make_map(&b.m.m[e.map], shares, Elem::kF32, p.splits * b.rows(), s.mp, s.mp, 32, 32));
+  MOE_CUDA(terms::launch<EpiShare>(b.m, b.l, gr.pairs_share, gr.st));
+  MOE_CUDA(launch_pdl(muon_join_kernel, dim3(static_cast<unsigned>(dense::cdiv(b.rows() * (s.mp / 4), kThreads))),
+                      dim3(kThreads), 0, gr.st, static_cast<const float*>(shares), static_cast<int>(p.splits),
+                      s.batch, s.mp, s.m, g.scale / (x.scale * x.scale), ratio * g.scale, g.at, g.diag));
+  return MOE_OK;
+}
+
 // X1 = Q X as planes.
 int32_t apply(const Group& gr, const Planes& q, const Planes& x, const Planes& out) {
   const Shape& s = gr.s;
@@ -582,7 +692,8 @@ int32_t run_group(const Group& gr) {
       a.m = t.momentum + at * size;
       a.grad = static_cast<const uint8_t*>(t.grad) + at * size * (bf16 ? 2 : 4);
       float* part = sums + (z + at) * chunks;
-      MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, gr.st, a, size, vec, part));
+      MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, gr.st, a, size,
+                          chunk_of(s), vec, part));
       MOE_CUDA(launch_pdl(muon_planes_kernel, dim3(s.np / kSide, s.mp / kSide, n), dim3(kThreads), 0, gr.st, a,
                           t.rows, t.cols, vec_rows, static_cast<const float*>(part), chunks,
                           static_cast<float>(gr.o->eps), gr.sc.x[0], planes(gr.w.x) + (z + at) * s.mp * s.np,
@@ -600,7 +711,7 @@ int32_t run_group(const Group& gr) {
     const StepScales* sc = gr.sc.step + done;
     Planes g = square(gr.w.g, sc[0].g), q = {};
     g.diag = planes(gr.w.h);
-    MOE_TRY(symmetric(gr, x, x, false, g, 1.0f, 0.f, ratio));
+    MOE_TRY(gram(gr, x, g, ratio));
     for (int k = 0; k < n; ++k) {
       const bool last = k == n - 1;
       // P = c G (G + (b / c) I) + a I
@@ -748,6 +859,7 @@ extern "C" int32_t moe_muon_step(const moe_muon_tensor* tensors, int32_t count, 
   MOE_TRY(check_device(&sms));
   MOE_CUDA(terms::resident_pairs<EpiPlanes>(sms, &g.pairs_planes));
   MOE_CUDA(terms::resident_pairs<EpiUpdate>(sms, &g.pairs_update));
+  MOE_CUDA(terms::resident_pairs<EpiShare>(sms, &g.pairs_share));
   g.t = tensors;
   g.count = count;
   g.o = o;
