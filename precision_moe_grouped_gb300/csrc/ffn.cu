@@ -300,7 +300,12 @@ __global__ void __launch_bounds__(kJoinThreads)
 // loads 16 bytes of a weight row (K order is free as long as both operands
 // use the same: lane t of a quad holds elements 8 t .. 8 t + 7 of each 32), and
 // mma.sync.m16n8k16 takes 16 weight rows against eight tokens, straight from
-// the registers.  The warps' sums are joined in shared memory in warp order.
+// the registers.  The next steps' loads are issued ahead of a step's products
+// (64 KB an SM in flight); none hangs on a condition, as rows and tokens beyond
+// the end read a valid one and are not stored.  The warps' sums are joined in
+// shared memory in warp order.  The first product's CTAs ask L2 for the second
+// one's weights when their own are loaded, so that HBM works through the change
+// of kernels.
 constexpr int kDecodeThreads = 256, kDecodeWarps = 8;
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -327,10 +332,60 @@ struct DecodeArgs {
   __nv_bfloat16* out;
   int64_t ld_in, ld_base, ld_out;
   int32_t tokens, units, k;    // units: features (two weight rows each), or rows
+  const uint8_t* next;         // the next product's weights
+  int64_t next_bytes;          // a multiple of 16
 };
 
 // MT: tiles of 16 weight rows at once; NT: of eight tokens; U: K steps of 32
-// whose loads are in flight together.
+// that are loaded together.
+template <bool DOWN, int MT, int NT, int U>
+struct DecodeStep {
+  uint4 w[U][MT][2], x[U][NT];
+
+  __device__ __forceinline__ static int column(int s, int i, int t, int K) {
+    const int k = (s + i) * 32 + 8 * t;
+    return k < K ? k : 0;
+  }
+  __device__ __forceinline__ void load_w(const __nv_bfloat16* const (&rows)[MT][2], int s, int t, int K) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int k = column(s, i, t, K);
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[i][m][j] = load_once(rows[m][j] + k);
+    }
+  }
+  __device__ __forceinline__ void load_x(const __nv_bfloat16* const (&rows)[NT], int s, int t, int K) {
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) x[i][n] = *reinterpret_cast<const uint4*>(rows[n] + column(s, i, t, K));
+  }
+  __device__ __forceinline__ void multiply(float (&acc)[MT][NT][4], int s, int s1, int t, int K) {
+    if (s + U > s1 || (s + U) * 32 > K) {   // nothing beyond the warp's share or the end of K
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        if (s + i < s1 && (s + i) * 32 + 8 * t < K) continue;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) w[i][m][0] = w[i][m][1] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[i][n] = make_uint4(0, 0, 0, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint4 &p = w[i][m][0], &q = w[i][m][1], &v = x[i][n];
+          mma_bf16(acc[m][n], p.x, q.x, p.y, q.y, v.x, v.y);
+          mma_bf16(acc[m][n], p.z, q.z, p.w, q.w, v.z, v.w);
+        }
+  }
+};
+
 template <bool DOWN, int MT, int NT, int U>
 __global__ void __launch_bounds__(kDecodeThreads)
     decode_kernel(const DecodeArgs a) {
@@ -343,6 +398,9 @@ __global__ void __launch_bounds__(kDecodeThreads)
   const int u0 = static_cast<int>(static_cast<int64_t>(a.units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<int64_t>(a.units) * (blockIdx.x + 1) / gridDim.x);
   constexpr int kPer = DOWN ? 16 : 8;   // units of a tile
+  const __nv_bfloat16* xr[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) xr[n] = a.in + (8 * n + g < a.tokens ? 8 * n + g : 0) * a.ld_in;
   if constexpr (!DOWN) {
     griddep_wait();
     griddep_launch_dependents();
@@ -350,57 +408,39 @@ __global__ void __launch_bounds__(kDecodeThreads)
   bool waited = !DOWN;
   for (int u = u0; u < u1; u += MT * kPer) {
     float acc[MT][NT][4] = {};
-    // lane's two weight rows of each tile (g and g + 8 of the MMA's 16)
+    // the lane's two weight rows of each tile (g and g + 8 of the MMA's 16)
     const __nv_bfloat16* rows[MT][2];
-    bool on[MT][2];
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
       const int lo = u + m * kPer + g, hi = DOWN ? lo + 8 : lo;
-      on[m][0] = lo < u1;
-      on[m][1] = hi < u1;
-      rows[m][0] = a.w + static_cast<int64_t>(on[m][0] ? lo : u0) * K + 8 * t;
-      rows[m][1] = a.w + static_cast<int64_t>(on[m][1] ? (DOWN ? hi : a.units + hi) : u0) * K + 8 * t;
+      rows[m][0] = a.w + static_cast<int64_t>(lo < u1 ? lo : u0) * K;
+      rows[m][1] = a.w + static_cast<int64_t>((hi < u1 ? hi : u0) + (DOWN ? 0 : a.units)) * K;
     }
-    for (int s = s0; s < s1; s += U) {
-      uint4 wv[U][MT][2], xv[U][NT];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t k = static_cast<int64_t>(s + i) * 32;
-        const bool in = s + i < s1 && k + 8 * t < K;
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            wv[i][m][j] = in && on[m][j] ? load_once(rows[m][j] + k) : make_uint4(0, 0, 0, 0);
-      }
-      if (DOWN && !waited) {   // the weights are the call's inputs, h is the kernel before's
-        griddep_wait();
-        waited = true;
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int64_t k = static_cast<int64_t>(s + i) * 32;
-        const bool in = s + i < s1 && k + 8 * t < K;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-          xv[i][n] = in && 8 * n + g < a.tokens
-                         ? *reinterpret_cast<const uint4*>(a.in + (8 * n + g) * a.ld_in + k + 8 * t)
-                         : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            const uint4 &p = wv[i][m][0], &q = wv[i][m][1], &x = xv[i][n];
-            mma_bf16(acc[m][n], p.x, q.x, p.y, q.y, x.x, x.y);
-            mma_bf16(acc[m][n], p.z, q.z, p.w, q.w, x.z, x.w);
-          }
-    }
-    if (DOWN && !waited) {
+    DecodeStep<DOWN, MT, NT, U> even, odd;
+    if (s0 < s1) even.load_w(rows, s0, t, K);
+    if (!waited) {   // the weights are the call's inputs, h is the kernel before's
       griddep_wait();
       waited = true;
+    }
+    if (s0 < s1) even.load_x(xr, s0, t, K);
+    for (int s = s0; s < s1; s += 2 * U) {
+      if (s + U < s1) {
+        odd.load_w(rows, s + U, t, K);
+        odd.load_x(xr, s + U, t, K);
+      }
+      even.multiply(acc, s, s1, t, K);
+      if (s + 2 * U < s1) {
+        even.load_w(rows, s + 2 * U, t, K);
+        even.load_x(xr, s + 2 * U, t, K);
+      }
+      if (s + U < s1) odd.multiply(acc, s + U, s1, t, K);
+    }
+    if (!DOWN && u + MT * kPer >= u1) {
+      // this CTA's share of the next weights, 4 KB a request
+      const int64_t n0 = a.next_bytes / 16 * blockIdx.x / gridDim.x * 16;
+      const int64_t n1 = a.next_bytes / 16 * (blockIdx.x + 1) / gridDim.x * 16;
+      for (int64_t at = n0 + 4096 * threadIdx.x; at < n1; at += 4096 * kDecodeThreads)
+        bulk_prefetch_l2(a.next + at, static_cast<uint32_t>(n1 - at < 4096 ? n1 - at : 4096));
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m)
@@ -432,6 +472,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
     }
     __syncthreads();
   }
+  if (DOWN && !waited) griddep_wait();
 }
 
 template <bool DOWN, int NT>
@@ -557,10 +598,10 @@ int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const v
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(ws + w.h);
   if (T <= kDecodeTokens) {
     DecodeArgs a = {static_cast<const __nv_bfloat16*>(wgu), static_cast<const __nv_bfloat16*>(x), nullptr, h,
-                    ld_x, 0, I, s->num_tokens, s->inter, s->hidden};
+                    ld_x, 0, I, s->num_tokens, s->inter, s->hidden, static_cast<const uint8_t*>(wd), 2 * H * I};
     MOE_CUDA(launch_decode<false>(a, sms, st));
     DecodeArgs b = {static_cast<const __nv_bfloat16*>(wd), h, static_cast<const __nv_bfloat16*>(base),
-                    static_cast<__nv_bfloat16*>(out), I, ld_base, ld_out, s->num_tokens, s->hidden, s->inter};
+                    static_cast<__nv_bfloat16*>(out), I, ld_base, ld_out, s->num_tokens, s->hidden, s->inter, nullptr, 0};
     MOE_CUDA(launch_decode<true>(b, sms, st));
     return MOE_OK;
   }
