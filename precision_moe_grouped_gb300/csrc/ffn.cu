@@ -487,6 +487,7 @@ cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
   const int nt = (a.tokens + 7) / 8;
   return nt <= 1   ? launch_decode<DOWN, 1>(a, sms, s)
          : nt == 2 ? launch_decode<DOWN, 2>(a, sms, s)
+         : nt == 3 ? launch_decode<DOWN, 3>(a, sms, s)
                    : launch_decode<DOWN, 4>(a, sms, s);
 }
 
