@@ -33,8 +33,12 @@ namespace dense {
 constexpr int kTile = 256;     // rows of a tile (128 per CTA)
 constexpr int kBK = 64;        // K elements of a stage: one 128-byte swizzle row
 constexpr int kStages = 6;
-constexpr int kMaxMaps = 16;
+constexpr int kMaxMaps = 12;
 constexpr int kMaxProblems = 4;
+template <int N>
+struct MapList {
+  CUtensorMap m[N];
+};
 constexpr int kMaxSegments = 3;
 constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4, kNumEpiWarps = 8;
@@ -48,9 +52,7 @@ constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
 
-struct Maps {
-  CUtensorMap m[kMaxMaps];
-};
+using Maps = MapList<kMaxMaps>;
 
 // Tile t of a problem -> (batch z, split s, tile row i, tile column j).
 struct Problem {
@@ -77,6 +79,7 @@ struct Tile {
 
 template <typename Args>
 struct Launch {
+  static constexpr int kMost = kMaxProblems;
   Problem p[kMaxProblems];
   Args e[kMaxProblems];        // the epilogue's arguments
   int32_t problems, tiles, maps;
@@ -94,7 +97,7 @@ __device__ __forceinline__ Tile find_tile(const L& l, int t) {
   Tile o;
   o.p = 0;
 #pragma unroll
-  for (int q = 1; q < kMaxProblems; ++q)
+  for (int q = 1; q < L::kMost; ++q)
     if (q < l.problems && t >= l.p[q].first_tile) o.p = q;
   const auto& p = l.p[o.p];
   t -= p.first_tile;
@@ -519,8 +522,8 @@ cudaError_t resident_pairs(int num_sms, int* pairs) {
   return resident_pairs(dense_kernel<Epi>, kSmemBytes, cache, num_sms, pairs);
 }
 
-template <class Kernel, class L>
-cudaError_t launch(Kernel kern, int smem, const Maps& maps, L& l, int pairs, cudaStream_t s, int units = 0) {
+template <class Kernel, class M, class L>
+cudaError_t launch(Kernel kern, int smem, const M& maps, L& l, int pairs, cudaStream_t s, int units = 0) {
   int tiles = 0;
   for (int i = 0; i < l.problems; ++i) {
     l.p[i].first_tile = tiles;

@@ -35,7 +35,7 @@ namespace {
 
 using dense::Elem;
 using dense::EpiWarp;
-using dense::Maps;
+using terms::Maps;
 using dense::Tile;
 
 constexpr uint64_t kTimeoutNs = 1000000000ull;
@@ -488,20 +488,16 @@ GroupWs group_ws(const Shape& s) {
   return w;
 }
 
-// What the launches of one group share.
-struct Group {
+// What the launches of a call share.
+struct Call {
   const moe_muon_tensor* t;
   int32_t count;
   const moe_muon_options* o;
-  Shape s;
-  uint8_t* ws;
-  GroupWs w;
   Scales sc;
   int32_t* status;
   cudaStream_t st;
   int pairs_planes, pairs_update, pairs_share;
 };
-
 // A matrix [rows of the batch][ld] as planes, times `scale`.
 struct Planes {
   __half* at;
@@ -511,35 +507,44 @@ struct Planes {
   __half* diag;   // G's diagonal blocks + (b / c) I, or null
 };
 
+struct Group {
+  Shape s;
+  GroupWs w;
+  uint8_t* ws;
+  Planes x, g, p, q;
+  __half* planes(size_t off) const { return reinterpret_cast<__half*>(ws + off); }
+  Planes square(size_t off, float scale) const { return {planes(off), scale, s.mp, true, nullptr}; }
+};
+constexpr int kMostGroups = 4;   // that share their launches: two products each in terms::Launch
+int64_t rows_of(const Shape& s) { return s.batch * s.mp; }
+
 // A launch in the making.
 template <class Epi>
 struct Build {
-  const Group& g;
   Maps m;
   terms::Launch<typename Epi::Args> l;
 
-  explicit Build(const Group& gr) : g(gr), l{} {
-    l.status = gr.status;
+  explicit Build(const Call& c) : l{} {
+    l.status = c.status;
     l.timeout_ns = kTimeoutNs;
     l.maps = 1;   // map 0 stands for none
     m.m[0] = CUtensorMap{};
   }
-  int64_t rows() const { return g.s.batch * g.s.mp; }
-
-  int32_t map(const __half* at, int64_t cols, int box_cols, int box_rows, dense::Swizzle sw, int32_t* index) {
+  int32_t map(const Shape& s, const __half* at, int64_t cols, int box_cols, int box_rows, dense::Swizzle sw,
+              int32_t* index) {
     *index = l.maps++;
-    return dense::make_map(&m.m[*index], at, Elem::kF16, 2 * rows(), cols, cols, box_cols, box_rows, sw);
+    return dense::make_map(&m.m[*index], at, Elem::kF16, 2 * rows_of(s), cols, cols, box_cols, box_rows, sw);
   }
   // The operand as rows of a tile or, with mn, its transpose; from matrix z on.
-  int32_t operand(const Planes& p, bool mn, int64_t z, terms::Operand* o) {
+  int32_t operand(const Shape& s, const Planes& p, bool mn, int64_t z, terms::Operand* o) {
     *o = {};
-    o->hi = static_cast<int32_t>(z * g.s.mp);
-    o->lo = static_cast<int32_t>(rows() + z * g.s.mp);
-    o->batch = g.s.mp;
+    o->hi = static_cast<int32_t>(z * s.mp);
+    o->lo = static_cast<int32_t>(rows_of(s) + z * s.mp);
+    o->batch = s.mp;
     o->mn = mn;
     o->sym = p.sym;
-    MOE_TRY(map(p.at, p.ld, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->map));
-    if (p.diag) MOE_TRY(map(p.diag, dense::kTile, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->diag));
+    MOE_TRY(map(s, p.at, p.ld, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->map));
+    if (p.diag) MOE_TRY(map(s, p.diag, dense::kTile, dense::kBK, dense::kBK, dense::Swizzle::k128, &o->diag));
     return MOE_OK;
   }
   terms::Problem& problem(int64_t tile_rows, int64_t tile_cols, int64_t batch, int64_t kb) {
@@ -558,133 +563,149 @@ using BuildPlanes = Build<EpiPlanes>;
 
 // out = c A B^T + a I, symmetric [mp, mp]; A and B [mp, k], B's second copy of the
 // diagonal blocks used when use_diag.
-int32_t add_symmetric(BuildPlanes& b, const Planes& x, Planes y, bool use_diag, const Planes& out, float c,
+int32_t add_symmetric(BuildPlanes& b, const Shape& s, const Planes& x, Planes y, bool use_diag, const Planes& out, float c,
                       float a, float ratio) {
-  const Shape& s = b.g.s;
   if (!use_diag) y.diag = nullptr;
   Planes left = x;
   left.diag = nullptr;
   terms::Problem& p = b.problem(s.mp, s.mp, s.batch, x.ld / dense::kBK);
   p.upper = 1;
   p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp));
-  MOE_TRY(b.operand(left, false, 0, &p.a));
-  MOE_TRY(b.operand(y, false, 0, &p.b));
+  MOE_TRY(b.operand(s, left, false, 0, &p.a));
+  MOE_TRY(b.operand(s, y, false, 0, &p.b));
   EpiPlanes::Args& e = b.l.e[b.l.problems - 1];
   e = {};
   e.c = c * out.scale / (x.scale * y.scale);
   e.a = a * out.scale;
-  MOE_TRY(b.map(out.at, s.mp, 32, 32, dense::Swizzle::k64, &e.map));
+  MOE_TRY(b.map(s, out.at, s.mp, 32, 32, dense::Swizzle::k64, &e.map));
   if (out.diag) {
-    MOE_TRY(b.map(out.diag, dense::kTile, 32, 32, dense::Swizzle::k64, &e.map_diag));
+    MOE_TRY(b.map(s, out.diag, dense::kTile, 32, 32, dense::Swizzle::k64, &e.map_diag));
     e.h = ratio * out.scale;
   }
-  e.lo_rows = static_cast<int32_t>(b.rows());
+  e.lo_rows = static_cast<int32_t>(rows_of(s));
   e.m = s.m;
   e.rows = e.cols = s.mp;
   return MOE_OK;
 }
 
-int32_t run(BuildPlanes& b) {
-  MOE_CUDA(terms::launch<EpiPlanes>(b.m, b.l, b.g.pairs_planes, b.g.st));
+int32_t run(const Call& c, BuildPlanes& b) {
+  if (b.l.problems) MOE_CUDA(terms::launch<EpiPlanes>(b.m, b.l, c.pairs_planes, c.st));
   return MOE_OK;
-}
-
-int32_t symmetric(const Group& gr, const Planes& x, const Planes& y, bool use_diag, const Planes& out, float c,
-                  float a, float ratio) {
-  BuildPlanes b(gr);
-  MOE_TRY(add_symmetric(b, x, y, use_diag, out, c, a, ratio));
-  return run(b);
 }
 
 // G = X X^T with its second diagonal blocks (+ ratio I), by shares of the long
 // side where there are few tiles.
-int32_t gram(const Group& gr, const Planes& x, const Planes& g, float ratio) {
-  const Shape& s = gr.s;
-  const int splits = gram_splits(s);
-  if (splits == 1) return symmetric(gr, x, x, false, g, 1.0f, 0.f, ratio);
-  Build<EpiShare> b(gr);
-  float* shares = reinterpret_cast<float*>(gr.ws + gr.w.shares);
-  terms::Problem& p = b.problem(s.mp, s.mp, s.batch, s.np / dense::kBK);
-  p.upper = 1;
-  p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp));
-  p.kb_split = static_cast<int32_t>(dense::cdiv(p.kb, splits));
-  p.splits = static_cast<int32_t>(dense::cdiv(p.kb, p.kb_split));
-  MOE_TRY(b.operand(x, false, 0, &p.a));
-  p.b = p.a;
-  EpiShare::Args& e = b.l.e[0];
-  e.map = b.l.maps++;
-  e.rows = s.mp;
-  e.batch = static_cast<int32_t>(s.batch);
-  MOE_TRY(dense::make_map(&b.m.m[e.map], shares, Elem::kF32, p.splits * b.rows(), s.mp, s.mp, 32, 32));
-  MOE_CUDA(terms::launch<EpiShare>(b.m, b.l, gr.pairs_share, gr.st));
-  MOE_CUDA(launch_pdl(muon_join_kernel, dim3(static_cast<unsigned>(dense::cdiv(b.rows() * (s.mp / 4), kThreads))),
-                      dim3(kThreads), 0, gr.st, static_cast<const float*>(shares), static_cast<int>(p.splits),
-                      s.batch, s.mp, s.m, g.scale / (x.scale * x.scale), ratio * g.scale, g.at, g.diag));
-  return MOE_OK;
-}
-
-// X1 = Q X as planes.
-int32_t apply(const Group& gr, const Planes& q, const Planes& x, const Planes& out) {
-  const Shape& s = gr.s;
-  BuildPlanes b(gr);
-  terms::Problem& p = b.problem(s.mp, s.np, s.batch, s.mp / dense::kBK);
-  MOE_TRY(b.operand(q, false, 0, &p.a));
-  MOE_TRY(b.operand(x, true, 0, &p.b));
-  EpiPlanes::Args& e = b.l.e[0];
-  e = {};
-  e.c = out.scale / (q.scale * x.scale);
-  MOE_TRY(b.map(out.at, s.np, 32, 32, dense::Swizzle::k64, &e.map));
-  e.lo_rows = static_cast<int32_t>(b.rows());
-  e.rows = s.mp;
-  e.cols = s.np;
-  return run(b);
-}
-
-// p <- decay p - lr s Q X for the group's tensors, as many in a launch as it
-// holds.
-int32_t update(const Group& gr, const Planes& q, const Planes& x) {
-  const Shape& s = gr.s;
-  int64_t z = 0;
-  for (int i = 0; i < gr.count;) {
-    Build<EpiUpdate> b(gr);
-    for (; i < gr.count && b.l.problems < dense::kMaxProblems; ++i) {
-      const moe_muon_tensor& t = gr.t[i];
-      if (!same(t, s)) continue;
-      const bool tall = t.rows > t.cols;
-      EpiUpdate::Args& e = b.l.e[b.l.problems];
-      terms::Problem& p = b.problem(tall ? s.m : s.n, tall ? s.n : s.m, t.count, s.mp / dense::kBK);
-      MOE_TRY(b.operand(tall ? q : x, !tall, z, &p.a));
-      MOE_TRY(b.operand(tall ? x : q, tall, z, &p.b));
-      e.p = t.param;
-      e.copy = static_cast<__nv_bfloat16*>(t.param_bf16);
-      e.decay = muon_decay(gr.o);
-      e.step = static_cast<float>(muon_step(gr.o, t) / (static_cast<double>(q.scale) * x.scale));
-      e.rows = tall ? s.m : s.n;
-      e.cols = tall ? s.n : s.m;
-      z += t.count;
+int32_t gram(const Call& c, Group* gs, int n, float ratio) {
+  BuildPlanes whole(c);
+  Build<EpiShare> b(c);
+  for (Group* g = gs; g < gs + n; ++g) {
+    const Shape& s = g->s;
+    const int splits = gram_splits(s);
+    if (splits == 1) {
+      MOE_TRY(add_symmetric(whole, s, g->x, g->x, false, g->g, 1.0f, 0.f, ratio));
+      continue;
     }
-    if (b.l.problems) MOE_CUDA(terms::launch<EpiUpdate>(b.m, b.l, gr.pairs_update, gr.st));
+    terms::Problem& p = b.problem(s.mp, s.mp, s.batch, s.np / dense::kBK);
+    EpiShare::Args& e = b.l.e[b.l.problems - 1];
+    p.upper = 1;
+    p.per_matrix = static_cast<int32_t>(upper_tiles(s.mp));
+    p.kb_split = static_cast<int32_t>(dense::cdiv(p.kb, splits));
+    p.splits = static_cast<int32_t>(dense::cdiv(p.kb, p.kb_split));
+    MOE_TRY(b.operand(s, g->x, false, 0, &p.a));
+    p.b = p.a;
+    e.map = b.l.maps++;
+    e.rows = s.mp;
+    e.batch = static_cast<int32_t>(s.batch);
+    MOE_TRY(dense::make_map(&b.m.m[e.map], g->ws + g->w.shares, Elem::kF32, p.splits * rows_of(s), s.mp, s.mp, 32,
+                            32));
+  }
+  MOE_TRY(run(c, whole));
+  if (b.l.problems) MOE_CUDA(terms::launch<EpiShare>(b.m, b.l, c.pairs_share, c.st));
+  int i = 0;
+  for (Group* g = gs; g < gs + n; ++g) {
+    const Shape& s = g->s;
+    if (gram_splits(s) == 1) continue;
+    const int64_t blocks = dense::cdiv(rows_of(s) * (s.mp / 4), kThreads);
+    MOE_CUDA(launch_pdl(muon_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, c.st,
+                        reinterpret_cast<const float*>(g->ws + g->w.shares), static_cast<int>(b.l.p[i++].splits),
+                        s.batch, s.mp, s.m, g->g.scale / (g->x.scale * g->x.scale), ratio * g->g.scale, g->g.at,
+                        g->g.diag));
   }
   return MOE_OK;
 }
 
-int32_t run_group(const Group& gr) {
-  const Shape& s = gr.s;
-  const int64_t lo = s.batch * s.mp;
-  float* sums = reinterpret_cast<float*>(gr.ws + gr.w.sums);
-  auto planes = [&](size_t off) { return reinterpret_cast<__half*>(gr.ws + off); };
+// X <- Q X as planes, in the other one of two places.
+int32_t apply(const Call& c, Group* gs, int n, float scale) {
+  BuildPlanes b(c);
+  for (Group* g = gs; g < gs + n; ++g) {
+    const Shape& s = g->s;
+    Planes out = g->x;
+    out.at = g->planes(g->x.at == g->planes(g->w.x) ? g->w.x1 : g->w.x);
+    out.scale = scale;
+    terms::Problem& p = b.problem(s.mp, s.np, s.batch, s.mp / dense::kBK);
+    EpiPlanes::Args& e = b.l.e[b.l.problems - 1];
+    MOE_TRY(b.operand(s, g->q, false, 0, &p.a));
+    MOE_TRY(b.operand(s, g->x, true, 0, &p.b));
+    e = {};
+    e.c = out.scale / (g->q.scale * g->x.scale);
+    MOE_TRY(b.map(s, out.at, s.np, 32, 32, dense::Swizzle::k64, &e.map));
+    e.lo_rows = static_cast<int32_t>(rows_of(s));
+    e.rows = s.mp;
+    e.cols = s.np;
+    g->x = out;
+  }
+  return run(c, b);
+}
+
+// p <- decay p - lr s Q X for the groups' tensors, as many in a launch as it
+// holds.
+int32_t update(const Call& c, Group* gs, int n) {
+  Build<EpiUpdate> b(c);
+  auto send = [&]() -> int32_t {
+    if (b.l.problems) MOE_CUDA(terms::launch<EpiUpdate>(b.m, b.l, c.pairs_update, c.st));
+    b = Build<EpiUpdate>(c);
+    return MOE_OK;
+  };
+  for (Group* g = gs; g < gs + n; ++g) {
+    const Shape& s = g->s;
+    int64_t z = 0;
+    for (int i = 0; i < c.count; ++i) {
+      const moe_muon_tensor& t = c.t[i];
+      if (!same(t, s)) continue;
+      const bool tall = t.rows > t.cols;
+      EpiUpdate::Args& e = b.l.e[b.l.problems];
+      terms::Problem& p = b.problem(tall ? s.m : s.n, tall ? s.n : s.m, t.count, s.mp / dense::kBK);
+      MOE_TRY(b.operand(s, tall ? g->q : g->x, !tall, z, &p.a));
+      MOE_TRY(b.operand(s, tall ? g->x : g->q, tall, z, &p.b));
+      e.p = t.param;
+      e.copy = static_cast<__nv_bfloat16*>(t.param_bf16);
+      e.decay = muon_decay(c.o);
+      e.step = static_cast<float>(muon_step(c.o, t) / (static_cast<double>(g->q.scale) * g->x.scale));
+      e.rows = tall ? s.m : s.n;
+      e.cols = tall ? s.n : s.m;
+      z += t.count;
+      if (b.l.problems == terms::kMaxProblems) MOE_TRY(send());
+    }
+  }
+  return send();
+}
+
+// The momenta and X0's planes of one group.
+int32_t first_planes(const Call& c, const Group& g) {
+  const Shape& s = g.s;
+  float* sums = reinterpret_cast<float*>(g.ws + g.w.sums);
   const int chunks = chunks_of(s);
   const int64_t size = static_cast<int64_t>(s.m) * s.n;
-  const bool bf16 = gr.o->grad_dtype == MOE_DTYPE_BF16;
+  const bool bf16 = c.o->grad_dtype == MOE_DTYPE_BF16;
   // Matrices whose momentum and gradient stay in L2 go one after another, so
   // that the second reading finds them there; as many small ones at once as do.
   const int64_t at_once = std::min<int64_t>(65535, std::max<int64_t>(1, kL2Bytes / (size * (bf16 ? 6 : 8))));
   int64_t z = 0;
-  for (int i = 0; i < gr.count; ++i) {
-    const moe_muon_tensor& t = gr.t[i];
+  for (int i = 0; i < c.count; ++i) {
+    const moe_muon_tensor& t = c.t[i];
     if (!same(t, s)) continue;
-    Momentum a = {t.grad, t.momentum, gr.o->grad_scale, static_cast<float>(gr.o->momentum),
-                  static_cast<float>(1.0 - gr.o->momentum), bf16, gr.o->nesterov};
+    Momentum a = {t.grad, t.momentum, c.o->grad_scale, static_cast<float>(c.o->momentum),
+                  static_cast<float>(1.0 - c.o->momentum), bf16, c.o->nesterov};
     const int vec = size % 4 == 0 && ptr_aligned(t.momentum, 16) && ptr_aligned(t.grad, bf16 ? 8 : 16);
     const int vec_rows = vec && t.cols % 4 == 0;
     for (int64_t at = 0; at < t.count; at += at_once) {
@@ -692,60 +713,71 @@ int32_t run_group(const Group& gr) {
       a.m = t.momentum + at * size;
       a.grad = static_cast<const uint8_t*>(t.grad) + at * size * (bf16 ? 2 : 4);
       float* part = sums + (z + at) * chunks;
-      MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, gr.st, a, size,
-                          chunk_of(s), vec, part));
-      MOE_CUDA(launch_pdl(muon_planes_kernel, dim3(s.np / kSide, s.mp / kSide, n), dim3(kThreads), 0, gr.st, a,
+      MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, c.st, a, size, chunk_of(s), vec,
+                          part));
+      MOE_CUDA(launch_pdl(muon_planes_kernel, dim3(s.np / kSide, s.mp / kSide, n), dim3(kThreads), 0, c.st, a,
                           t.rows, t.cols, vec_rows, static_cast<const float*>(part), chunks,
-                          static_cast<float>(gr.o->eps), gr.sc.x[0], planes(gr.w.x) + (z + at) * s.mp * s.np,
-                          lo * s.np, s.mp, s.np));
+                          static_cast<float>(c.o->eps), c.sc.x[0], g.planes(g.w.x) + (z + at) * s.mp * s.np,
+                          rows_of(s) * s.np, s.mp, s.np));
     }
     z += t.count;
   }
-  const double ca = gr.o->coefficients[0], cb = gr.o->coefficients[1], cc = gr.o->coefficients[2];
-  const float fa = static_cast<float>(ca), fc = static_cast<float>(cc), ratio = static_cast<float>(cb / cc);
-  auto square = [&](size_t off, float scale) { return Planes{planes(off), scale, s.mp, true, nullptr}; };
-  Planes x = {planes(gr.w.x), gr.sc.x[0], s.np, false, nullptr};
-  int part = 0;
-  for (int done = 0; done < gr.o->ns_steps; done += kPartSteps, ++part) {
-    const int n = std::min(kPartSteps, gr.o->ns_steps - done);
-    const StepScales* sc = gr.sc.step + done;
-    Planes g = square(gr.w.g, sc[0].g), q = {};
-    g.diag = planes(gr.w.h);
-    MOE_TRY(gram(gr, x, g, ratio));
-    for (int k = 0; k < n; ++k) {
-      const bool last = k == n - 1;
-      // P = c G (G + (b / c) I) + a I
-      const Planes p = square(k == 0 ? gr.w.qa : gr.w.p, sc[k].p);
-      MOE_TRY(symmetric(gr, g, g, true, p, fc, fa, 0.f));
-      const Planes sp = square(gr.w.s, sc[k].s);
-      BuildPlanes b(gr);
-      if (!last) MOE_TRY(add_symmetric(b, p, g, false, sp, 1.0f, 0.f, 0.f));
-      if (k == 0) {
-        q = p;
-      } else {
-        const Planes next = square(k & 1 ? gr.w.qb : gr.w.qa, sc[k].q);
-        MOE_TRY(add_symmetric(b, p, q, false, next, 1.0f, 0.f, 0.f));
-        // P Q and not P Q^T: what is left of Q's asymmetry belongs to the X that the
-        // next Gram matrix is taken of
-        b.l.p[b.l.problems - 1].b.turned = 1;
-        q = next;
-      }
-      if (b.l.problems) MOE_TRY(run(b));
-      if (!last) {
-        g.scale = sc[k + 1].g;
-        MOE_TRY(symmetric(gr, sp, p, false, g, 1.0f, 0.f, ratio));
-      }
-    }
-    if (done + n < gr.o->ns_steps) {
-      const Planes next = {planes(x.at == planes(gr.w.x) ? gr.w.x1 : gr.w.x), gr.sc.x[part + 1], s.np, false,
-                           nullptr};
-      MOE_TRY(apply(gr, q, x, next));
-      x = next;
-    } else {
-      MOE_TRY(update(gr, q, x));
-    }
-  }
   return MOE_OK;
+}
+
+// All steps of up to kMostGroups groups, whose products share their launches.
+int32_t run_groups(const Call& c, Group* gs, int n) {
+  const double ca = c.o->coefficients[0], cb = c.o->coefficients[1], cc = c.o->coefficients[2];
+  const float fa = static_cast<float>(ca), fc = static_cast<float>(cc), ratio = static_cast<float>(cb / cc);
+  Group* const end = gs + n;
+  for (Group* g = gs; g < end; ++g) {
+    MOE_TRY(first_planes(c, *g));
+    g->x = {g->planes(g->w.x), c.sc.x[0], g->s.np, false, nullptr};
+  }
+  int part = 0;
+  for (int done = 0; done < c.o->ns_steps; done += kPartSteps, ++part) {
+    const int steps = std::min(kPartSteps, c.o->ns_steps - done);
+    const StepScales* sc = c.sc.step + done;
+    for (Group* g = gs; g < end; ++g) {
+      g->g = g->square(g->w.g, sc[0].g);
+      g->g.diag = g->planes(g->w.h);
+    }
+    MOE_TRY(gram(c, gs, n, ratio));
+    for (int k = 0; k < steps; ++k) {
+      const bool last = k == steps - 1;
+      BuildPlanes poly(c);   // P = c G (G + (b / c) I) + a I
+      for (Group* g = gs; g < end; ++g) {
+        g->p = g->square(k == 0 ? g->w.qa : g->w.p, sc[k].p);
+        MOE_TRY(add_symmetric(poly, g->s, g->g, g->g, true, g->p, fc, fa, 0.f));
+      }
+      MOE_TRY(run(c, poly));
+      BuildPlanes both(c);   // S = P G, Q <- P Q
+      for (Group* g = gs; g < end; ++g) {
+        if (!last)
+          MOE_TRY(add_symmetric(both, g->s, g->p, g->g, false, g->square(g->w.s, sc[k].s), 1.0f, 0.f, 0.f));
+        if (k == 0) {
+          g->q = g->p;
+        } else {
+          const Planes next = g->square(k & 1 ? g->w.qb : g->w.qa, sc[k].q);
+          MOE_TRY(add_symmetric(both, g->s, g->p, g->q, false, next, 1.0f, 0.f, 0.f));
+          // P Q and not P Q^T: what is left of Q's asymmetry belongs to the X that the
+          // next Gram matrix is taken of
+          both.l.p[both.l.problems - 1].b.turned = 1;
+          g->q = next;
+        }
+      }
+      MOE_TRY(run(c, both));
+      if (last) break;
+      BuildPlanes next(c);   // G <- S P
+      for (Group* g = gs; g < end; ++g) {
+        g->g.scale = sc[k + 1].g;
+        MOE_TRY(add_symmetric(next, g->s, g->square(g->w.s, sc[k].s), g->p, false, g->g, 1.0f, 0.f, ratio));
+      }
+      MOE_TRY(run(c, next));
+    }
+    if (done + steps < c.o->ns_steps) MOE_TRY(apply(c, gs, n, c.sc.x[part + 1]));
+  }
+  return update(c, gs, n);
 }
 
 int32_t check_tensor(const moe_muon_tensor& t, int i, bool bf16) {
@@ -790,29 +822,63 @@ int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_optio
   return MOE_OK;
 }
 
-// Calls f with the shape (and matrices) of each group, in the order of their
-// first tensors; stops at the first error.
-template <class F>
-int32_t each_group(const moe_muon_tensor* t, int32_t count, F f) {
-  for (int i = 0; i < count; ++i) {
-    if (muon_empty(t[i]) || muon_is_small(t[i])) continue;
-    Shape s = shape_of(t[i]);
-    bool seen = false;
-    for (int j = 0; j < i && !seen; ++j) seen = same(t[j], s);
-    if (seen) continue;
-    for (int j = i; j < count; ++j)
-      if (same(t[j], s)) s.batch += t[j].count;
-    MOE_TRY(f(s));
-  }
+int32_t check_group(const Shape& s) {
+  if (2 * s.batch * s.mp >= (int64_t(1) << 31) || s.batch * chunks_of(s) >= (int64_t(1) << 31) ||
+      s.batch * dense::cdiv(s.mp, 128) * dense::cdiv(s.np, 128) >= (int64_t(1) << 31))
+    return entry_fail(MOE_ERR_UNSUPPORTED, "too many matrices of %d x %d", s.m, s.n);
   return MOE_OK;
+}
+
+// The next group at or after tensor *i, whose first tensor it is; false: none.
+bool next_shape(const moe_muon_tensor* t, int32_t count, int32_t* i, Shape* s) {
+  for (; *i < count; ++*i) {
+    if (muon_empty(t[*i]) || muon_is_small(t[*i])) continue;
+    *s = shape_of(t[*i]);
+    bool seen = false;
+    for (int j = 0; j < *i && !seen; ++j) seen = same(t[j], *s);
+    if (seen) continue;
+    for (int j = *i; j < count; ++j)
+      if (same(t[j], *s)) s->batch += t[j].count;
+    ++*i;
+    return true;
+  }
+  return false;
+}
+
+// Calls f with each set of groups that share their launches (and the bytes that
+// they need), in the order of their first tensors: as many as kMostGroups and
+// the memory of the largest group, or kSharedBytes, hold.  Stops at the first
+// error.
+constexpr size_t kSharedBytes = size_t(256) << 20;
+template <class F>
+int32_t each_set(const moe_muon_tensor* t, int32_t count, F f) {
+  size_t most = kSharedBytes;
+  Shape s;
+  for (int32_t i = 0; next_shape(t, count, &i, &s);) {
+    MOE_TRY(check_group(s));
+    most = std::max(most, group_ws(s).total);
+  }
+  Group set[kMostGroups] = {};
+  int n = 0;
+  size_t bytes = 0;
+  for (int32_t i = 0; next_shape(t, count, &i, &s);) {
+    const GroupWs w = group_ws(s);
+    if (n == kMostGroups || (n && bytes + w.total > most)) {
+      MOE_TRY(f(set, n, bytes));
+      n = 0;
+      bytes = 0;
+    }
+    set[n].s = s;
+    set[n++].w = w;
+    bytes += w.total;
+  }
+  return n ? f(set, n, bytes) : MOE_OK;
 }
 
 int32_t total_ws(const moe_muon_tensor* t, int32_t count, size_t* need) {
   *need = std::max(kWsAlign, muon_small_ws(t, count));
-  return each_group(t, count, [&](const Shape& s) -> int32_t {
-    if (2 * s.batch * s.mp >= (int64_t(1) << 31) || s.batch * chunks_of(s) >= (int64_t(1) << 31) || s.batch * dense::cdiv(s.mp, 128) * dense::cdiv(s.np, 128) >= (int64_t(1) << 31))
-      return entry_fail(MOE_ERR_UNSUPPORTED, "too many matrices of %d x %d", s.m, s.n);
-    *need = std::max(*need, group_ws(s).total);
+  return each_set(t, count, [&](Group*, int, size_t bytes) -> int32_t {
+    *need = std::max(*need, bytes);
     return MOE_OK;
   });
 }
@@ -841,7 +907,7 @@ extern "C" size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_
 extern "C" int32_t moe_muon_step(const moe_muon_tensor* tensors, int32_t count, const moe_muon_options* o,
                                  void* workspace, size_t workspace_bytes, int32_t* status, void* stream) {
   using namespace moe;
-  Group g = {};
+  Call g = {};
   size_t need;
   MOE_TRY(check_call(tensors, count, o, &g.sc));
   MOE_TRY(total_ws(tensors, count, &need));
@@ -863,13 +929,16 @@ extern "C" int32_t moe_muon_step(const moe_muon_tensor* tensors, int32_t count, 
   g.t = tensors;
   g.count = count;
   g.o = o;
-  g.ws = static_cast<uint8_t*>(workspace);
   g.status = status;
   g.st = static_cast<cudaStream_t>(stream);
-  MOE_TRY(muon_small_step(tensors, count, o, g.ws, g.st));
-  return each_group(tensors, count, [&](const Shape& s) -> int32_t {
-    g.s = s;
-    g.w = group_ws(s);
-    return run_group(g);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  MOE_TRY(muon_small_step(tensors, count, o, ws, g.st));
+  return each_set(tensors, count, [&](Group* set, int n, size_t) -> int32_t {
+    size_t at = 0;
+    for (int i = 0; i < n; ++i) {
+      set[i].ws = ws + at;
+      at += set[i].w.total;
+    }
+    return run_groups(g, set, n);
   });
 }

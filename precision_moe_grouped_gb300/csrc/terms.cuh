@@ -28,9 +28,10 @@ using dense::kNumEpiWarps;
 using dense::kStageBox;
 using dense::kThreads;
 using dense::kTile;
-using dense::Maps;
 using dense::Tile;
 
+constexpr int kMaxMaps = 32, kMaxProblems = 8;
+using Maps = dense::MapList<kMaxMaps>;
 constexpr int kStages = 3;
 constexpr int kPiece = 2;     // K blocks of a piece
 constexpr int kStageBytes = 2 * (kABytes + kBBytes);   // A hi, A lo, B hi, B lo
@@ -65,8 +66,9 @@ struct Problem {
 // is two units of 128 columns, where that fills the last round of the pairs.
 template <typename Args>
 struct Launch {
-  Problem p[dense::kMaxProblems];
-  Args e[dense::kMaxProblems];
+  static constexpr int kMost = kMaxProblems;
+  Problem p[kMaxProblems];
+  Args e[kMaxProblems];
   int32_t problems, tiles, whole, maps, last;
   int32_t* status;
   uint64_t timeout_ns;
