@@ -3,7 +3,7 @@
 // (muon.cu).
 //
 // One persistent launch runs a list of problems D = sum over segments of
-// A_s B_s, each D cut into tiles of 256 x BN (BN = 256 or 128): a CTA pair
+// A_s B_s, each D cut into tiles of 256 x BN (BN = 64 to 256): a CTA pair
 // takes a tile, rank r holds its rows 128 r .. 128 r + 127 in its tensor
 // memory (tcgen05.mma.cta_group::2, M = 256, both operands from shared
 // memory, float accumulators).  A segment is one pair of operands; products
@@ -13,10 +13,11 @@
 // no operand is ever transposed in memory.
 //
 // Per K block of 64 a CTA stages its 128 rows of A and its half of B (16 +
-// 16 KB at BN = 256); six stages keep 192 KB in flight.  Two accumulators of
+// 16 KB at BN = 256); six stages, or up to nine smaller ones, keep 192 KB in
+// flight.  Two accumulators of
 // 256 columns let the epilogue of a tile run under the next one's products.
-//   warp 0: TMA producer   warp 1: MMA issuer (rank 0), TMEM   warps 4-11:
-//   epilogue, two per lane quarter, each with half of the columns
+//   warps 0, 2: TMA producers of A, B   warp 1: MMA issuer (rank 0), TMEM
+//   warps 4-11: epilogue, two per lane quarter, each with half of the columns
 // All waits are bounded (ptx.cuh).
 #pragma once
 
@@ -32,7 +33,7 @@ namespace dense {
 
 constexpr int kTile = 256;     // rows of a tile (128 per CTA)
 constexpr int kBK = 64;        // K elements of a stage: one 128-byte swizzle row
-constexpr int kStages = 6;
+constexpr int kMaxStages = 9;
 constexpr int kMaxMaps = 12;
 constexpr int kMaxProblems = 4;
 template <int N>
@@ -42,12 +43,12 @@ struct MapList {
 constexpr int kMaxSegments = 3;
 constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4, kNumEpiWarps = 8;
-constexpr int kABytes = 128 * 128, kBBytes = 128 * 128;   // slots
+constexpr int kABytes = 128 * 128, kBBytes = 128 * 128;   // of a stage, B's at most
+constexpr int kOperandBytes = 6 * (kABytes + kBBytes);    // all stages
 constexpr int kStageBox = 4096;                           // an epilogue warp's: 32 rows x 128 bytes
-constexpr int kOffA = 0, kOffB = kOffA + kStages * kABytes;
-constexpr int kOffStage = kOffB + kStages * kBBytes;
+constexpr int kOffStage = kOperandBytes;
 constexpr int kOffBar = kOffStage + kNumEpiWarps * kStageBox;
-constexpr int kNumBars = 2 * kStages + 4 + 1;
+constexpr int kNumBars = 2 * kMaxStages + 4 + 1;
 constexpr int kOffMisc = kOffBar + 8 * kNumBars;
 constexpr int kSmemBytes = kOffMisc + 16 + 1024;
 static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
@@ -61,7 +62,7 @@ struct Problem {
   int32_t a_off[kMaxSegments], b_off[kMaxSegments];   // added to the operand's row coordinate
   int32_t a_mn, b_mn;          // 1: the operand is MN-major
   int32_t a_batch, b_batch;    // row coordinates between matrices of the batch
-  int32_t bn;                  // 256 or 128
+  int32_t bn;                  // 64, 128, 192 or 256
   int32_t b_step;              // columns of D between tiles (bn, or bn / 2 for two halves)
   int32_t b_rank;              // where rank 1's half of B begins, from rank 0's
   int32_t tiles_m, tiles_n;
@@ -77,13 +78,20 @@ struct Tile {
   int32_t p, z, s, i, j;
 };
 
+// An operand that no kernel of the call writes is copied ahead of the grid wait,
+// as far as the slots go: the kernel before has passed its own, behind which the
+// call's inputs are complete.
+constexpr int kEarlyA = 1, kEarlyB = 2;
+
 template <typename Args>
 struct Launch {
   static constexpr int kMost = kMaxProblems;
   Problem p[kMaxProblems];
   Args e[kMaxProblems];        // the epilogue's arguments
   int32_t problems, tiles, maps;
+  int32_t stages, slot;        // slots of the operands, bytes of one
   int32_t last;                // the call's last kernel: lets no successor start early
+  int32_t early;               // kEarlyA, kEarlyB: that operand is the call's input, and this not its first kernel
   int32_t* status;
   uint64_t timeout_ns;
 };
@@ -238,6 +246,65 @@ struct EpiWarp {
   int32_t lane;
 };
 
+// A slot ring's producer: one warp copies A's share of every stage, another one
+// B's, so that neither's instructions stand between a freed slot and its
+// refill.  The whole warp runs the loop, one lane issues; a tile's last slot is
+// followed by the next tile's first without a pause.
+template <bool IS_A, class L>
+__device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* smem, uint64_t* full, uint64_t* empty,
+                                        uint32_t rank, int pair, int pairs, volatile int32_t* abort_flag) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t full0 = cluster_addr(full, 0), stages = static_cast<uint32_t>(l.stages);
+  uint8_t* const slots = smem + (IS_A ? 0 : kABytes);
+  asm volatile("fence.proxy.async.global;" ::: "memory");   // the kernel before used plain stores
+  uint32_t stage = 0, phase = 0;
+  bool ok = true, issued = false;
+  for (int t = pair; ok && t < l.tiles; t += pairs) {
+    const Tile o = find_tile(l, t);
+    const Problem& p = l.p[o.p];
+    const int k0 = o.s * p.kb_split, n = min(p.kb, k0 + p.kb_split) - k0;
+    const bool mn = IS_A ? p.a_mn : p.b_mn;
+    const int at = IS_A ? o.i * kTile + static_cast<int>(rank) * 128
+                        : o.j * p.b_step + static_cast<int>(rank) * p.b_rank;
+    const int dx = mn ? 0 : kBK, dy = mn ? kBK : 0;
+    const bool two = mn && (IS_A || p.bn == 256);   // boxes of 64 columns
+    const uint32_t bytes = IS_A ? 2u * kABytes : 128u * static_cast<uint32_t>(p.bn);   // both CTAs'
+    for (int s = 0; ok && s < p.segs; ++s) {
+      const CUtensorMap* m = &maps.m[IS_A ? p.a_map[s] : p.b_map[s]];
+      const int row = IS_A ? p.a_off[s] + o.z * p.a_batch : p.b_off[s] + o.z * p.b_batch;
+      int x = mn ? at : k0 * kBK, y = (mn ? k0 * kBK : at) + row;
+      for (int k = 0; k < n; ++k, x += dx, y += dy) {
+        if (!mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          uint8_t* dst = slots + stage * static_cast<uint32_t>(l.slot);
+          if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
+          tma_load_2d_pair(dst, m, x, y, full0 + 8 * stage);
+          if (two) tma_load_2d_pair(dst + 8192, m, x + 64, y, full0 + 8 * stage);
+        }
+        issued = true;
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  }
+  // Rank 0: every copy of both CTAs has landed before either may leave
+  // (bounded, whatever the abort flag says): the last fill of each slot.
+  if (rank == 0 && issued) {
+    int32_t none = 0;
+    for (uint32_t s = 0; s < stages; ++s) {
+      // slots below `stage` were last filled in this round of the ring, the others in the one before
+      // (a slot never filled has its fresh barrier pass at once)
+      const uint32_t par = s < stage ? phase : phase ^ 1u;
+      mbar_wait_warp(full + s, par, l.timeout_ns, l.status, kDevTimeout, &none);
+    }
+  }
+}
+
 // Epi: struct Args; static run(args, problem, tile, warp, maps).
 template <class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -248,8 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + kOffBar);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;
+  uint64_t* empty = full + kMaxStages;
+  uint64_t* tfull = empty + kMaxStages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
@@ -257,10 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = static_cast<int>(blockIdx.x >> 1), pairs = static_cast<int>(gridDim.x >> 1);
+  const uint32_t stages = static_cast<uint32_t>(l.stages), slot = static_cast<uint32_t>(l.slot);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);    // rank 0's producer, plus the bytes of both CTAs
+    for (uint32_t s = 0; s < stages; ++s) {
+      mbar_init(full + s, 2);    // rank 0's producers, plus the bytes of both CTAs
       mbar_init(empty + s, 1);   // the MMA commit
     }
     for (int a = 0; a < 2; ++a) {
@@ -272,80 +340,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
-  if (warp == 2 && lane < l.maps) prefetch_tmap(&maps.m[lane]);
+  if (warp == 3 && lane < l.maps) prefetch_tmap(&maps.m[lane]);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  griddep_wait();
-  if (!l.last) griddep_launch_dependents();
+  // (a producer of an early operand reads nothing that a kernel of the call writes)
+  if (!(warp == 0 && l.early == kEarlyA) && !(warp == 2 && l.early == kEarlyB)) {
+    griddep_wait();
+    if (!l.last) griddep_launch_dependents();
+  }
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    // The whole warp runs the loop, one lane issues.  A tile's last slot is
-    // followed by the next tile's first without a pause.
-    const uint32_t full0 = cluster_addr(full, 0);
-    asm volatile("fence.proxy.async.global;" ::: "memory");   // the planes' writers used plain stores
-    uint32_t stage = 0, phase = 0;
-    bool ok = true, issued = false;
-    for (int t = pair; ok && t < l.tiles; t += pairs) {
-      const Tile o = find_tile(l, t);
-      const Problem& p = l.p[o.p];
-      const int a_mn0 = o.i * kTile + static_cast<int>(rank) * 128;
-      const int b_mn0 = o.j * p.b_step + static_cast<int>(rank) * p.b_rank;
-      const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
-      const uint32_t bytes = 2u * static_cast<uint32_t>(kABytes + p.bn * 64);
-      for (int s = 0; ok && s < p.segs; ++s) {
-        const CUtensorMap *am = &maps.m[p.a_map[s]], *bm = &maps.m[p.b_map[s]];
-        const int ar = p.a_off[s] + o.z * p.a_batch, br = p.b_off[s] + o.z * p.b_batch;
-        for (int kb = k0; kb < k1; ++kb) {
-          if (!mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout,
-                              abort_flag)) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            uint8_t* as = smem + kOffA + stage * kABytes;
-            uint8_t* bs = smem + kOffB + stage * kBBytes;
-            const uint32_t bar = full0 + 8 * stage;
-            if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
-            if (p.a_mn) {
-              tma_load_2d_pair(as, am, a_mn0, kb * kBK + ar, bar);
-              tma_load_2d_pair(as + 8192, am, a_mn0 + 64, kb * kBK + ar, bar);
-            } else {
-              tma_load_2d_pair(as, am, kb * kBK, a_mn0 + ar, bar);
-            }
-            if (p.b_mn) {
-              tma_load_2d_pair(bs, bm, b_mn0, kb * kBK + br, bar);
-              if (p.bn == 256) tma_load_2d_pair(bs + 8192, bm, b_mn0 + 64, kb * kBK + br, bar);
-            } else {
-              tma_load_2d_pair(bs, bm, kb * kBK, b_mn0 + br, bar);
-            }
-          }
-          issued = true;
-          if (++stage == kStages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
-      }
-    }
-    // Rank 0: every copy of both CTAs has landed before either may leave
-    // (bounded, whatever the abort flag says): the last fill of each slot.
-    if (rank == 0 && issued) {
-      int32_t none = 0;
-      for (int s = 0; s < kStages; ++s) {
-        // slots below `stage` were last filled in this round of the ring, the others in the one before
-        // (a slot never filled has its fresh barrier pass at once)
-        const uint32_t par = s < static_cast<int>(stage) ? phase : phase ^ 1u;
-        mbar_wait_warp(full + s, par, l.timeout_ns, l.status, kDevTimeout, &none);
-      }
-    }
+    produce<true>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
+  } else if (warp == 2) {
+    produce<false>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
-      const uint32_t a0 = smem_u32(smem + kOffA), b0 = smem_u32(smem + kOffB);
+      const uint32_t a0 = smem_u32(smem), b0 = smem_u32(smem + kABytes);
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       int it = 0;
@@ -372,9 +386,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          mma_stage_warp(d, ad0 + stage * (kABytes >> 4), bd0 + stage * (kBBytes >> 4), a_step, b_step,
+          mma_stage_warp(d, ad0 + stage * (slot >> 4), bd0 + stage * (slot >> 4), a_step, b_step,
                          static_cast<uint32_t>(p.idesc), k > 0 ? 1u : 0u, empty + stage);
-          if (++stage == kStages) {
+          if (++stage == stages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -444,23 +458,10 @@ constexpr int kPlanPairs = 76;
 inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Tiles of 128 columns, which take about 0.7 of the time of 256, where they fill
-// the last wave better; shares of K of at least eight blocks where even they
-// leave half of the pairs without one.
-inline Plan make_plan(int64_t tiles_m, int64_t cols, int64_t kb, bool may_split) {
-  Plan p;
+// the last wave better.
+inline Plan make_plan(int64_t tiles_m, int64_t cols, int64_t kb) {
   const int64_t t256 = tiles_m * cdiv(cols, 256), t128 = tiles_m * cdiv(cols, 128);
-  p.bn = 10 * cdiv(t256, kPlanPairs) <= 7 * cdiv(t128, kPlanPairs) ? 256 : 128;
-  p.splits = 1;
-  p.kb_split = static_cast<int32_t>(kb);
-  if (may_split && 2 * t128 <= kPlanPairs) {
-    int64_t s = kPlanPairs / t128;
-    if (s > kb / 8) s = kb / 8;
-    if (s > 1) {
-      p.kb_split = static_cast<int32_t>(cdiv(kb, s));
-      p.splits = static_cast<int32_t>(cdiv(kb, p.kb_split));
-    }
-  }
-  return p;
+  return {10 * cdiv(t256, kPlanPairs) <= 7 * cdiv(t128, kPlanPairs) ? 256 : 128, 1, static_cast<int32_t>(kb)};
 }
 
 // One operand pair, tiles over rows x cols (cols counts D's columns, or the
@@ -549,6 +550,10 @@ cudaError_t launch(Kernel kern, int smem, const M& maps, L& l, int pairs, cudaSt
 }
 template <class Epi>
 cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, cudaStream_t s) {
+  int bn = 64;
+  for (int i = 0; i < l.problems; ++i) bn = l.p[i].bn > bn ? l.p[i].bn : bn;
+  l.slot = kABytes + bn * 64;
+  l.stages = kOperandBytes / l.slot < kMaxStages ? kOperandBytes / l.slot : kMaxStages;
   return launch(dense_kernel<Epi>, kSmemBytes, maps, l, pairs, s);
 }
 

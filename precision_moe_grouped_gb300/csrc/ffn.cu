@@ -181,7 +181,7 @@ struct EpiGateGrad {
     __nv_bfloat16 *h, *dgu;   // [T, I], [T, 2 I]
     const float* dh;          // [rows rounded up to 32, ld_dh]
     int64_t ld_dh;
-    int32_t map_h, map_dg, map_du, rows, inter;
+    int32_t rows, inter;
   };
   static __device__ __forceinline__ void run(const Args& a, const Problem& p, const Tile& o,
                                              const EpiWarp& w, const Maps& maps) {
@@ -222,76 +222,121 @@ struct EpiGateGrad {
 };
 
 // ------------------------------------------------------- joining K's shares
-__device__ __forceinline__ float4 add4(float4 a, float4 b) {
-  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-// Four columns from column c of row r, summed over the shares in order.
-__device__ __forceinline__ float4 joined(const float* sums, int splits, int64_t share, int64_t at) {
-  float4 v = *reinterpret_cast<const float4*>(sums + at);
-  for (int s = 1; s < splits; ++s) v = add4(v, *reinterpret_cast<const float4*>(sums + s * share + at));
-  return v;
-}
-__device__ __forceinline__ uint2 pack4(float4 v) {
-  return make_uint2(dense::pack_bf16(v.x, v.y), dense::pack_bf16(v.z, v.w));
-}
+// Batches of up to 256 tokens: the weights are the 256 rows of a tile, the
+// tokens its columns, and K is shared out until the pairs are busy.  Sums are
+// [shares][rows][tp], the tokens side by side; a block joins 16 features of 64
+// tokens, four tokens of a feature a thread, and turns them through shared
+// memory, so that both sides are met in long runs.
+constexpr int kJoinThreads = 256, kJoinFeatures = 16, kJoinTokens = 64;
 
-constexpr int kJoinThreads = 256;
+struct Sums {
+  const float* at;
+  int32_t shares, rows, tp;
 
-// h from the shares of x [Wg; Wu]^T, [splits][rows_pad][2 I].
-__global__ void __launch_bounds__(kJoinThreads)
-    join_gate_kernel(const float* sums, int splits, int64_t rows_pad, int64_t rows, int inter,
-                     __nv_bfloat16* h) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const int per = inter >> 2;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
-  if (i >= rows * per) return;
-  const int64_t r = i / per, ld = 2 * static_cast<int64_t>(inter);
-  const int c = static_cast<int>(i - r * per) * 4;
-  const float4 g = joined(sums, splits, rows_pad * ld, r * ld + c);
-  const float4 u = joined(sums, splits, rows_pad * ld, r * ld + inter + c);
-  *reinterpret_cast<uint2*>(h + r * inter + c) =
-      pack4(make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z), swiglu(g.w, u.w)));
-}
-
-// out = base + the shares of [splits][rows_pad][cols].
-__global__ void __launch_bounds__(kJoinThreads)
-    join_out_kernel(const float* sums, int splits, int64_t rows_pad, int64_t rows, int cols,
-                    const __nv_bfloat16* base, int64_t ld_base, __nv_bfloat16* out, int64_t ld_out) {
-  griddep_wait();
-  const int per = cols >> 2;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
-  if (i >= rows * per) return;
-  const int64_t r = i / per;
-  const int c = static_cast<int>(i - r * per) * 4;
-  float4 v = joined(sums, splits, rows_pad * cols, r * cols + c);
-  if (base) {
-    const uint2 b = *reinterpret_cast<const uint2*>(base + r * ld_base + c);
-    const float2 lo = dense::unpack_bf16(b.x), hi = dense::unpack_bf16(b.y);
-    v = add4(v, make_float4(lo.x, lo.y, hi.x, hi.y));
+  // four tokens from t on of row r, over the shares in order
+  __device__ __forceinline__ float4 joined(int r, int t) const {
+    const float* p = at + static_cast<int64_t>(r) * tp + t;
+    const int64_t step = static_cast<int64_t>(rows) * tp;
+    float4 v = *reinterpret_cast<const float4*>(p);
+#pragma unroll 4
+    for (int s = 1; s < shares; ++s) {
+      const float4 x = *reinterpret_cast<const float4*>(p + s * step);
+      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+    }
+    return v;
   }
-  *reinterpret_cast<uint2*>(out + r * ld_out + c) = pack4(v);
-}
+};
 
-// h, dg, du from the shares of x [Wg; Wu]^T and of dout Wd.
+struct Turned {
+  __nv_bfloat16 v[kJoinTokens][kJoinFeatures + 8];   // rows 48 bytes apart
+
+  __device__ __forceinline__ void put(int f, int t, float4 x) {
+    v[t][f] = __float2bfloat16_rn(x.x);
+    v[t + 1][f] = __float2bfloat16_rn(x.y);
+    v[t + 2][f] = __float2bfloat16_rn(x.z);
+    v[t + 3][f] = __float2bfloat16_rn(x.w);
+  }
+  // this thread's eight features of one token
+  __device__ __forceinline__ void send(__nv_bfloat16* to, int64_t ld, int f0, int t0, int features, int tokens) const {
+    const int t = threadIdx.x >> 1, f = (threadIdx.x & 1) * 8;
+    if (t < kJoinTokens && t0 + t < tokens && f0 + f < features)
+      *reinterpret_cast<uint4*>(to + static_cast<int64_t>(t0 + t) * ld + f0 + f) =
+          *reinterpret_cast<const uint4*>(&v[t][f]);
+  }
+};
+
+// h from x [Wg; Wu]^T.
 __global__ void __launch_bounds__(kJoinThreads)
-    join_grad_kernel(const float* gu, int splits_gu, const float* dh, int splits_dh, int64_t rows_pad,
-                     int64_t rows, int inter, __nv_bfloat16* h, __nv_bfloat16* dgu) {
+    join_gate_kernel(const Sums s, int tokens, int inter, __nv_bfloat16* h) {
+  __shared__ __align__(16) Turned turned;
   griddep_wait();
   griddep_launch_dependents();
-  const int per = inter >> 2;
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
-  if (i >= rows * per) return;
-  const int64_t r = i / per, ld = 2 * static_cast<int64_t>(inter);
-  const int c = static_cast<int>(i - r * per) * 4;
-  const float4 g = joined(gu, splits_gu, rows_pad * ld, r * ld + c);
-  const float4 u = joined(gu, splits_gu, rows_pad * ld, r * ld + inter + c);
-  const float4 d = joined(dh, splits_dh, rows_pad * inter, r * inter + c);
-  const Grads a = swiglu_grads(g.x, u.x, d.x), b = swiglu_grads(g.y, u.y, d.y);
-  const Grads e = swiglu_grads(g.z, u.z, d.z), f = swiglu_grads(g.w, u.w, d.w);
-  *reinterpret_cast<uint2*>(h + r * inter + c) = pack4(make_float4(a.h, b.h, e.h, f.h));
-  *reinterpret_cast<uint2*>(dgu + r * ld + c) = pack4(make_float4(a.dg, b.dg, e.dg, f.dg));
-  *reinterpret_cast<uint2*>(dgu + r * ld + inter + c) = pack4(make_float4(a.du, b.du, e.du, f.du));
+  const int f0 = blockIdx.x * kJoinFeatures, t0 = blockIdx.y * kJoinTokens;
+  const int t = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int f = threadIdx.x >> 4; f < kJoinFeatures; f += 16) {
+    if (f0 + f >= inter) continue;
+    const float4 g = s.joined(f0 + f, t0 + t), u = s.joined(inter + f0 + f, t0 + t);
+    turned.put(f, t, make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z), swiglu(g.w, u.w)));
+  }
+  __syncthreads();
+  turned.send(h, inter, f0, t0, inter, tokens);
+}
+
+// out = base + the sums: added in float, rounded once.
+__global__ void __launch_bounds__(kJoinThreads)
+    join_out_kernel(const Sums s, int tokens, int cols, const __nv_bfloat16* base, int64_t ld_base,
+                    __nv_bfloat16* out, int64_t ld_out) {
+  __shared__ __align__(16) float turned[kJoinTokens][kJoinFeatures + 4];
+  griddep_wait();
+  const int f0 = blockIdx.x * kJoinFeatures, t0 = blockIdx.y * kJoinTokens;
+  const int t = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int f = threadIdx.x >> 4; f < kJoinFeatures; f += 16) {
+    if (f0 + f >= cols) continue;
+    const float4 v = s.joined(f0 + f, t0 + t);
+    turned[t][f] = v.x;
+    turned[t + 1][f] = v.y;
+    turned[t + 2][f] = v.z;
+    turned[t + 3][f] = v.w;
+  }
+  __syncthreads();
+  const int tt = threadIdx.x >> 1, f = (threadIdx.x & 1) * 8;
+  if (tt >= kJoinTokens || t0 + tt >= tokens || f0 + f >= cols) return;
+  uint4 b = make_uint4(0, 0, 0, 0);
+  if (base) b = *reinterpret_cast<const uint4*>(base + (t0 + tt) * ld_base + f0 + f);
+  const uint32_t bb[4] = {b.x, b.y, b.z, b.w};
+  uint32_t r[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 x = dense::unpack_bf16(bb[k]);
+    r[k] = dense::pack_bf16(turned[tt][f + 2 * k] + x.x, turned[tt][f + 2 * k + 1] + x.y);
+  }
+  *reinterpret_cast<uint4*>(out + (t0 + tt) * ld_out + f0 + f) = make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// h, dg, du from x [Wg; Wu]^T and dout Wd.
+__global__ void __launch_bounds__(kJoinThreads)
+    join_grad_kernel(const Sums gu, const Sums dh, int tokens, int inter, __nv_bfloat16* h, __nv_bfloat16* dgu) {
+  __shared__ __align__(16) Turned th, tg, tu;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int f0 = blockIdx.x * kJoinFeatures, t0 = blockIdx.y * kJoinTokens;
+  const int t = (threadIdx.x & 15) * 4;
+#pragma unroll
+  for (int f = threadIdx.x >> 4; f < kJoinFeatures; f += 16) {
+    if (f0 + f >= inter) continue;
+    const float4 g = gu.joined(f0 + f, t0 + t), u = gu.joined(inter + f0 + f, t0 + t), d = dh.joined(f0 + f, t0 + t);
+    const Grads a = swiglu_grads(g.x, u.x, d.x), b = swiglu_grads(g.y, u.y, d.y);
+    const Grads c = swiglu_grads(g.z, u.z, d.z), e = swiglu_grads(g.w, u.w, d.w);
+    th.put(f, t, make_float4(a.h, b.h, c.h, e.h));
+    tg.put(f, t, make_float4(a.dg, b.dg, c.dg, e.dg));
+    tu.put(f, t, make_float4(a.du, b.du, c.du, e.du));
+  }
+  __syncthreads();
+  th.send(h, inter, f0, t0, inter, tokens);
+  tg.send(dgu, 2 * static_cast<int64_t>(inter), f0, t0, inter, tokens);
+  tu.send(dgu + inter, 2 * static_cast<int64_t>(inter), f0, t0, inter, tokens);
 }
 
 // ------------------------------------------------------ batches of few tokens
@@ -494,10 +539,24 @@ cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
 // ------------------------------------------------------------------- plans
 constexpr int64_t up32(int64_t v) { return (v + 31) / 32 * 32; }
 
+// A product whose tokens are the columns of one tile: weights [rows, K], K
+// shared out over the pairs, at least four blocks a share.
+constexpr int kTurnTokens = 256;   // at most
+dense::Plan turned_plan(int64_t tokens, int64_t rows, int64_t kb, int64_t pairs) {
+  dense::Plan p;
+  p.bn = static_cast<int32_t>((tokens + 63) / 64 * 64);
+  const int64_t tiles = dense::cdiv(rows, dense::kTile);
+  const int64_t s = std::max<int64_t>(1, std::min(pairs / tiles, kb / 4));
+  p.kb_split = static_cast<int32_t>(dense::cdiv(kb, s));
+  p.splits = static_cast<int32_t>(dense::cdiv(kb, p.kb_split));
+  return p;
+}
+int64_t sums_bytes(const dense::Plan& p, int64_t rows) { return 4 * p.splits * up32(rows) * p.bn; }
+
 struct FfnWs {
   dense::Plan gate, down;   // forward; gate also in the backward pass
   dense::Plan dh, dx;
-  bool split;               // gate's (and dh's) sums go through joining kernels
+  bool turned;              // gate, down and dh as turned_plan's
   size_t h, dgu, sums, sums2, total;
 };
 
@@ -517,20 +576,26 @@ FfnWs ffn_ws(const moe_ffn_shape* s, bool backward) {
     return w;
   }
   const int64_t kh = dense::cdiv(H, dense::kBK), ki = dense::cdiv(I, dense::kBK);
-  w.gate = dense::make_plan(tm, 2 * I, kh, true);
-  w.split = w.gate.splits > 1;
-  if (!backward) {
-    w.down = dense::make_plan(tm, H, ki, true);
-    const int64_t a = w.split ? 4 * w.gate.splits * rp * 2 * I : 0;
-    const int64_t b = w.down.splits > 1 ? 4 * w.down.splits * rp * H : 0;
-    w.sums = take(std::max<int64_t>(a, 0));
-    w.sums2 = take(b);
+  w.turned = T <= kTurnTokens;
+  if (w.turned && !backward) {
+    w.gate = turned_plan(T, 2 * I, kh, dense::kPlanPairs);
+    w.down = turned_plan(T, H, ki, dense::kPlanPairs);
+    w.sums = take(sums_bytes(w.gate, 2 * I));
+    w.sums2 = take(sums_bytes(w.down, H));
+  } else if (w.turned) {   // x [Wg; Wu]^T and dout Wd in one launch: two and one of three parts
+    w.gate = turned_plan(T, 2 * I, kh, dense::kPlanPairs * 2 / 3);
+    w.dh = turned_plan(T, I, kh, dense::kPlanPairs / 3);
+    w.sums = take(sums_bytes(w.dh, I));
+    w.sums2 = take(sums_bytes(w.gate, 2 * I));
   } else {
+    w.gate = dense::make_plan(tm, 2 * I, kh);
+    w.down = dense::make_plan(tm, H, ki);
+    w.dh = dense::make_plan(tm, I, kh);
+    w.sums = take(backward ? 4 * rp * I : 0);
+  }
+  if (backward) {
     w.dgu = take(4 * T * I);
-    w.dh = dense::make_plan(tm, I, kh, w.split);
-    w.sums = take(4 * w.dh.splits * rp * I);
-    w.sums2 = take(w.split ? 4 * w.gate.splits * rp * 2 * I : 0);
-    w.dx = dense::make_plan(tm, H, dense::cdiv(2 * I, dense::kBK), false);
+    w.dx = dense::make_plan(tm, H, dense::cdiv(2 * I, dense::kBK));
   }
   w.total = at;
   return w;
@@ -583,13 +648,41 @@ dense::Launch<typename Epi::Args> new_launch(int32_t* status) {
   return l;
 }
 
-unsigned join_blocks(int64_t rows, int64_t cols) {
-  return static_cast<unsigned>(dense::cdiv(rows * (cols / 4), kJoinThreads));
+dim3 join_grid(int64_t tokens, int64_t features) {
+  return dim3(static_cast<unsigned>(dense::cdiv(features, kJoinFeatures)),
+              static_cast<unsigned>(dense::cdiv(tokens, kJoinTokens)));
 }
 
 // Boxes of the operands: K-major rows of a tile (128 of A, bn / 2 of B), and
 // MN-major squares of 64.
 constexpr int kSquare = dense::kBK;
+
+// Adds the sums of W x^T (turned_plan): weights w [rows, K], or [K, rows] with
+// mn, against tokens x [T, K].
+int32_t add_turned(Maps* m, dense::Launch<EpiSum::Args>* l, const dense::Plan& plan, const void* w, int64_t rows,
+                   int64_t k, bool mn, const void* x, int64_t ld_x, int64_t tokens, float* sums, Sums* out) {
+  const int i = l->problems++, at = l->maps;
+  l->maps += 3;
+  if (mn) MOE_TRY(dense::make_map(&m->m[at], w, Elem::kBf16, k, rows, rows, kSquare, kSquare));
+  else MOE_TRY(dense::make_map(&m->m[at], w, Elem::kBf16, rows, k, k, dense::kBK, 128));
+  MOE_TRY(dense::make_map(&m->m[at + 1], x, Elem::kBf16, tokens, k, ld_x, dense::kBK, plan.bn / 2));
+  MOE_TRY(dense::make_map(&m->m[at + 2], sums, Elem::kF32, plan.splits * up32(rows), plan.bn, plan.bn, 32, 32));
+  l->p[i] = dense::make_problem(plan, rows, tokens, dense::cdiv(k, dense::kBK), at, mn, at + 1, false, true);
+  l->e[i] = {at + 2, static_cast<int32_t>(up32(rows)), plan.bn};
+  *out = {sums, plan.splits, static_cast<int32_t>(up32(rows)), plan.bn};
+  return MOE_OK;
+}
+
+// The launch of D = x [Wg; Wu]^T whose tiles hold both projections of a feature:
+// gate rows in rank 0's half of B, up rows in rank 1's.
+Problem gate_problem(const dense::Plan& plan, int64_t tokens, int64_t inter, int64_t kb) {
+  Problem p = dense::make_problem(plan, tokens, 2 * inter, kb, 0, false, 1, false, true);
+  p.b_step = plan.bn / 2;
+  p.b_rank = static_cast<int32_t>(inter);
+  p.tiles_n = static_cast<int32_t>(dense::cdiv(inter, plan.bn / 2));
+  p.per_matrix = p.tiles_m * p.tiles_n;
+  return p;
+}
 
 int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const void* wgu, const void* wd,
                     const void* base, int64_t ld_base, void* out, int64_t ld_out, uint8_t* ws,
@@ -597,77 +690,57 @@ int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const v
   const int64_t T = s->num_tokens, H = s->hidden, I = s->inter;
   const FfnWs w = ffn_ws(s, false);
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(ws + w.h);
+  const __nv_bfloat16* add = static_cast<const __nv_bfloat16*>(base);
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(out);
   if (T <= kDecodeTokens) {
     DecodeArgs a = {static_cast<const __nv_bfloat16*>(wgu), static_cast<const __nv_bfloat16*>(x), nullptr, h,
                     ld_x, 0, I, s->num_tokens, s->inter, s->hidden, static_cast<const uint8_t*>(wd), 2 * H * I};
     MOE_CUDA(launch_decode<false>(a, sms, st));
-    DecodeArgs b = {static_cast<const __nv_bfloat16*>(wd), h, static_cast<const __nv_bfloat16*>(base),
-                    static_cast<__nv_bfloat16*>(out), I, ld_base, ld_out, s->num_tokens, s->hidden, s->inter, nullptr, 0};
+    DecodeArgs b = {static_cast<const __nv_bfloat16*>(wd), h, add, to, I, ld_base, ld_out, s->num_tokens, s->hidden,
+                    s->inter, nullptr, 0};
     MOE_CUDA(launch_decode<true>(b, sms, st));
     return MOE_OK;
   }
-  const int64_t rp = up32(T), kh = dense::cdiv(H, dense::kBK), ki = dense::cdiv(I, dense::kBK);
-  {
-    Maps m;
-    MOE_TRY(dense::make_map(&m.m[0], x, Elem::kBf16, T, H, ld_x, dense::kBK, 128));
-    MOE_TRY(dense::make_map(&m.m[1], wgu, Elem::kBf16, 2 * I, H, H, dense::kBK, w.gate.bn / 2));
-    int pairs;
-    if (w.split) {
-      auto l = new_launch<EpiSum>(status);
-      float* sums = reinterpret_cast<float*>(ws + w.sums);
-      MOE_TRY(dense::make_map(&m.m[2], sums, Elem::kF32, w.gate.splits * rp, 2 * I, 2 * I, 32, 32));
-      l.problems = 1;
-      l.maps = 3;
-      l.p[0] = dense::make_problem(w.gate, T, 2 * I, kh, 0, false, 1, false, true);
-      l.e[0] = {2, static_cast<int32_t>(rp), static_cast<int32_t>(2 * I)};
-      MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
-      MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
-      MOE_CUDA(launch_pdl(join_gate_kernel, dim3(join_blocks(T, I)), dim3(kJoinThreads), 0, st,
-                          static_cast<const float*>(sums), static_cast<int>(w.gate.splits), rp, T,
-                          static_cast<int>(I), h));
-    } else {
-      auto l = new_launch<EpiGate>(status);
-      MOE_TRY(dense::make_map(&m.m[2], h, Elem::kBf16, T, I, I, 64, 32));
-      l.problems = 1;
-      l.maps = 3;
-      l.p[0] = dense::make_problem(w.gate, T, 2 * I, kh, 0, false, 1, false, true);
-      l.p[0].b_step = w.gate.bn / 2;   // features of a tile: gate rows of rank 0, up rows of rank 1
-      l.p[0].b_rank = static_cast<int32_t>(I);
-      l.p[0].tiles_n = static_cast<int32_t>(dense::cdiv(I, w.gate.bn / 2));
-      l.p[0].per_matrix = l.p[0].tiles_m * l.p[0].tiles_n;
-      l.e[0] = {h, 2, static_cast<int32_t>(T), static_cast<int32_t>(I)};
-      MOE_CUDA(dense::resident_pairs<EpiGate>(sms, &pairs));
-      MOE_CUDA(dense::launch<EpiGate>(m, l, pairs, st));
-    }
-  }
-  Maps m;
   int pairs;
-  MOE_TRY(dense::make_map(&m.m[0], h, Elem::kBf16, T, I, I, dense::kBK, 128));
-  MOE_TRY(dense::make_map(&m.m[1], wd, Elem::kBf16, H, I, I, dense::kBK, w.down.bn / 2));
-  const Problem p = dense::make_problem(w.down, T, H, ki, 0, false, 1, false, true);
-  if (w.down.splits > 1) {
-    auto l = new_launch<EpiSum>(status);
-    float* sums = reinterpret_cast<float*>(ws + w.sums2);
-    MOE_TRY(dense::make_map(&m.m[2], sums, Elem::kF32, w.down.splits * rp, H, H, 32, 32));
-    l.problems = 1;
-    l.maps = 3;
-    l.p[0] = p;
-    l.e[0] = {2, static_cast<int32_t>(rp), static_cast<int32_t>(H)};
+  Maps m;
+  if (w.turned) {
     MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
+    Sums sums;
+    auto l = new_launch<EpiSum>(status);
+    MOE_TRY(add_turned(&m, &l, w.gate, wgu, 2 * I, H, false, x, ld_x, T, reinterpret_cast<float*>(ws + w.sums), &sums));
     MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
-    MOE_CUDA(launch_pdl(join_out_kernel, dim3(join_blocks(T, H)), dim3(kJoinThreads), 0, st,
-                        static_cast<const float*>(sums), static_cast<int>(w.down.splits), rp, T,
-                        static_cast<int>(H), static_cast<const __nv_bfloat16*>(base), ld_base,
-                        static_cast<__nv_bfloat16*>(out), ld_out));
+    MOE_CUDA(launch_pdl(join_gate_kernel, join_grid(T, I), dim3(kJoinThreads), 0, st, sums, s->num_tokens, s->inter,
+                        h));
+    l = new_launch<EpiSum>(status);
+    l.early = dense::kEarlyA;
+    MOE_TRY(add_turned(&m, &l, w.down, wd, H, I, false, h, I, T, reinterpret_cast<float*>(ws + w.sums2), &sums));
+    MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
+    MOE_CUDA(launch_pdl(join_out_kernel, join_grid(T, H), dim3(kJoinThreads), 0, st, sums, s->num_tokens, s->hidden,
+                        add, ld_base, to, ld_out));
     return MOE_OK;
   }
+  {
+    auto l = new_launch<EpiGate>(status);
+    MOE_TRY(dense::make_map(&m.m[0], x, Elem::kBf16, T, H, ld_x, dense::kBK, 128));
+    MOE_TRY(dense::make_map(&m.m[1], wgu, Elem::kBf16, 2 * I, H, H, dense::kBK, w.gate.bn / 2));
+    MOE_TRY(dense::make_map(&m.m[2], h, Elem::kBf16, T, I, I, 64, 32));
+    l.problems = 1;
+    l.maps = 3;
+    l.p[0] = gate_problem(w.gate, T, I, dense::cdiv(H, dense::kBK));
+    l.e[0] = {h, 2, s->num_tokens, s->inter};
+    MOE_CUDA(dense::resident_pairs<EpiGate>(sms, &pairs));
+    MOE_CUDA(dense::launch<EpiGate>(m, l, pairs, st));
+  }
   auto l = new_launch<EpiOut>(status);
+  MOE_TRY(dense::make_map(&m.m[0], h, Elem::kBf16, T, I, I, dense::kBK, 128));
+  MOE_TRY(dense::make_map(&m.m[1], wd, Elem::kBf16, H, I, I, dense::kBK, w.down.bn / 2));
   MOE_TRY(dense::make_map(&m.m[2], out, Elem::kBf16, T, H, ld_out, 64, 32));
   l.problems = 1;
   l.maps = 3;
   l.last = 1;
-  l.p[0] = p;
-  l.e[0] = {static_cast<const __nv_bfloat16*>(base), ld_base, 2, static_cast<int32_t>(T), static_cast<int32_t>(H)};
+  l.early = dense::kEarlyB;
+  l.p[0] = dense::make_problem(w.down, T, H, dense::cdiv(I, dense::kBK), 0, false, 1, false, true);
+  l.e[0] = {add, ld_base, 2, s->num_tokens, s->hidden};
   MOE_CUDA(dense::resident_pairs<EpiOut>(sms, &pairs));
   MOE_CUDA(dense::launch<EpiOut>(m, l, pairs, st));
   return MOE_OK;
@@ -684,56 +757,42 @@ int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, 
   __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(ws + w.h);
   __nv_bfloat16* dgu = reinterpret_cast<__nv_bfloat16*>(ws + w.dgu);
   float* dh = reinterpret_cast<float*>(ws + w.sums);
-  float* gu = reinterpret_cast<float*>(ws + w.sums2);
   int pairs;
-  {
-    // dh = dout Wd (Wd [H, I] is MN-major there); with few tokens the shares of
-    // x [Wg; Wu]^T in the same launch
-    Maps m;
+  Maps m;
+  MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
+  if (w.turned) {
+    Sums sums_gu, sums_dh;
     auto l = new_launch<EpiSum>(status);
-    MOE_TRY(dense::make_map(&m.m[0], dout, Elem::kBf16, T, H, ld_dout, dense::kBK, 128));
-    MOE_TRY(dense::make_map(&m.m[1], wd, Elem::kBf16, H, I, I, kSquare, kSquare));
-    MOE_TRY(dense::make_map(&m.m[2], dh, Elem::kF32, w.dh.splits * rp, I, I, 32, 32));
-    l.maps = 3;
-    l.p[0] = dense::make_problem(w.dh, T, I, kh, 0, false, 1, true, true);
-    l.e[0] = {2, static_cast<int32_t>(rp), static_cast<int32_t>(I)};
-    l.problems = 1;
-    if (w.split) {
-      MOE_TRY(dense::make_map(&m.m[3], x, Elem::kBf16, T, H, ld_x, dense::kBK, 128));
-      MOE_TRY(dense::make_map(&m.m[4], wgu, Elem::kBf16, 2 * I, H, H, dense::kBK, w.gate.bn / 2));
-      MOE_TRY(dense::make_map(&m.m[5], gu, Elem::kF32, w.gate.splits * rp, 2 * I, 2 * I, 32, 32));
-      l.maps = 6;
-      l.p[1] = dense::make_problem(w.gate, T, 2 * I, kh, 3, false, 4, false, true);
-      l.e[1] = {5, static_cast<int32_t>(rp), static_cast<int32_t>(2 * I)};
-      l.problems = 2;
-    }
-    MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
+    MOE_TRY(add_turned(&m, &l, w.gate, wgu, 2 * I, H, false, x, ld_x, T, reinterpret_cast<float*>(ws + w.sums2),
+                       &sums_gu));
+    MOE_TRY(add_turned(&m, &l, w.dh, wd, I, H, true, dout, ld_dout, T, dh, &sums_dh));
     MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
-  }
-  if (w.split) {
-    MOE_CUDA(launch_pdl(join_grad_kernel, dim3(join_blocks(T, I)), dim3(kJoinThreads), 0, st,
-                        static_cast<const float*>(gu), static_cast<int>(w.gate.splits),
-                        static_cast<const float*>(dh), static_cast<int>(w.dh.splits), rp, T,
-                        static_cast<int>(I), h, dgu));
+    MOE_CUDA(launch_pdl(join_grad_kernel, join_grid(T, I), dim3(kJoinThreads), 0, st, sums_gu, sums_dh,
+                        s->num_tokens, s->inter, h, dgu));
   } else {
-    Maps m;
+    {   // dh = dout Wd (Wd [H, I] is MN-major there), in float for the next epilogue
+      auto l = new_launch<EpiSum>(status);
+      MOE_TRY(dense::make_map(&m.m[0], dout, Elem::kBf16, T, H, ld_dout, dense::kBK, 128));
+      MOE_TRY(dense::make_map(&m.m[1], wd, Elem::kBf16, H, I, I, kSquare, kSquare));
+      MOE_TRY(dense::make_map(&m.m[2], dh, Elem::kF32, rp, I, I, 32, 32));
+      l.maps = 3;
+      l.p[0] = dense::make_problem(w.dh, T, I, kh, 0, false, 1, true, true);
+      l.e[0] = {2, static_cast<int32_t>(rp), s->inter};
+      l.problems = 1;
+      MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
+    }
     auto l = new_launch<EpiGateGrad>(status);
     MOE_TRY(dense::make_map(&m.m[0], x, Elem::kBf16, T, H, ld_x, dense::kBK, 128));
     MOE_TRY(dense::make_map(&m.m[1], wgu, Elem::kBf16, 2 * I, H, H, dense::kBK, w.gate.bn / 2));
     l.maps = 2;
     l.problems = 1;
-    l.p[0] = dense::make_problem(w.gate, T, 2 * I, kh, 0, false, 1, false, true);
-    l.p[0].b_step = w.gate.bn / 2;
-    l.p[0].b_rank = static_cast<int32_t>(I);
-    l.p[0].tiles_n = static_cast<int32_t>(dense::cdiv(I, w.gate.bn / 2));
-    l.p[0].per_matrix = l.p[0].tiles_m * l.p[0].tiles_n;
-    l.e[0] = {h, dgu, dh, I, 0, 0, 0, static_cast<int32_t>(T), static_cast<int32_t>(I)};
+    l.p[0] = gate_problem(w.gate, T, I, kh);
+    l.e[0] = {h, dgu, dh, I, s->num_tokens, s->inter};
     MOE_CUDA(dense::resident_pairs<EpiGateGrad>(sms, &pairs));
     MOE_CUDA(dense::launch<EpiGateGrad>(m, l, pairs, st));
   }
   // dx = [dg du] [Wg; Wu] (the weights MN-major), and the weights' gradients,
   // sums over the tokens (both operands MN-major), in one launch
-  Maps m;
   auto l = new_launch<EpiOut>(status);
   l.last = 1;
   if (dx) {
@@ -747,8 +806,8 @@ int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, 
               static_cast<int32_t>(H)};
   }
   if (dw_gate_up) {
-    const dense::Plan g = dense::make_plan(dense::cdiv(2 * I, dense::kTile), H, kt, false);
-    const dense::Plan d = dense::make_plan(dense::cdiv(H, dense::kTile), I, kt, false);
+    const dense::Plan g = dense::make_plan(dense::cdiv(2 * I, dense::kTile), H, kt);
+    const dense::Plan d = dense::make_plan(dense::cdiv(H, dense::kTile), I, kt);
     int i = l.problems++, k = l.maps;
     l.maps += 3;
     MOE_TRY(dense::make_map(&m.m[k], dgu, Elem::kBf16, T, 2 * I, 2 * I, kSquare, kSquare));

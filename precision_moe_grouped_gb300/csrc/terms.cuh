@@ -98,18 +98,61 @@ __device__ __forceinline__ bool mn_at(const Operand& o, int tr, int kb) {
   return o.mn || (o.sym && (kb >> 2) < tr + o.turned);
 }
 
-// Both terms of one operand: 64 or 128 rows (or columns) from `at`, K block kb.
-__device__ __forceinline__ void load_terms(const Maps& maps, const Operand& o, int z, int at, int rows, int tr,
-                                           int kb, uint8_t* dst, int slot, uint32_t bar) {
-  const bool mn = mn_at(o, tr, kb), diag = o.diag && (kb >> 2) == tr;
-  const CUtensorMap* m = &maps.m[diag ? o.diag : o.map];
-  const int k0 = diag ? (kb & 3) * kBK : kb * kBK;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int row = (h ? o.lo : o.hi) + z * o.batch;
-    for (int r = 0; r < rows; r += 64)
-      tma_load_2d_pair(dst + r * 128, m, mn ? at + r : k0, (mn ? k0 : at + r) + row, bar);
-    dst += slot;
+// The producer of one operand (see dense::produce): both terms of a stage.
+template <bool IS_A, class L>
+__device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* smem, uint64_t* full, uint64_t* empty,
+                                        uint32_t rank, int pair, int pairs, volatile int32_t* abort_flag) {
+  constexpr int kSlot = IS_A ? kABytes : kBBytes;   // of one term
+  const int lane = threadIdx.x & 31, units = num_units(l);
+  const uint32_t full0 = cluster_addr(full, 0);
+  uint8_t* const slots = smem + (IS_A ? 0 : 2 * kABytes);
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+  uint32_t stage = 0, phase = 0;
+  bool ok = true, issued = false;
+  for (int t = pair; ok && t < units; t += pairs) {
+    const Unit x = find_unit(l, t);
+    const Problem& p = l.p[x.o.p];
+    const Operand& o = IS_A ? p.a : p.b;
+    const int at = IS_A ? x.o.i * kTile + static_cast<int>(rank) * 128
+                        : x.col + static_cast<int>(rank) * (x.bn >> 1);
+    const int tr = IS_A ? x.o.i : x.o.j, rows = IS_A ? 128 : x.bn >> 1;
+    const uint32_t bytes = 4u * static_cast<uint32_t>(rows) * 128u;   // both terms, both CTAs
+    const int hi = o.hi + x.o.z * o.batch, lo = o.lo + x.o.z * o.batch;
+    const int k0 = x.o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
+    for (int kb = k0; kb < k1; ++kb) {
+      const bool mn = mn_at(o, tr, kb), diag = o.diag && (kb >> 2) == tr;
+      const CUtensorMap* m = &maps.m[diag ? o.diag : o.map];
+      const int k = (diag ? kb & 3 : kb) * kBK;
+      const int cx = mn ? at : k, cy = mn ? k : at, dx = mn ? 64 : 0, dy = mn ? 0 : 64;
+      if (!mbar_poll_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        uint8_t* dst = slots + stage * kStageBytes;
+        const uint32_t bar = full0 + 8 * stage;
+        if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
+        tma_load_2d_pair(dst, m, cx, cy + hi, bar);
+        tma_load_2d_pair(dst + kSlot, m, cx, cy + lo, bar);
+        if (rows == 128) {
+          tma_load_2d_pair(dst + 8192, m, cx + dx, cy + dy + hi, bar);
+          tma_load_2d_pair(dst + kSlot + 8192, m, cx + dx, cy + dy + lo, bar);
+        }
+      }
+      issued = true;
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  // rank 0: every copy of both CTAs has landed before either may leave
+  if (rank == 0 && issued) {
+    int32_t none = 0;
+    for (int s = 0; s < kStages; ++s) {
+      const uint32_t par = s < static_cast<int>(stage) ? phase : phase ^ 1u;
+      mbar_wait_warp(full + s, par, l.timeout_ns, l.status, kDevTimeout, &none);
+    }
   }
 }
 
@@ -138,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
-      mbar_init(full + s, 1);
+      mbar_init(full + s, 2);   // rank 0's producers, plus the bytes of both CTAs
       mbar_init(empty + s, 1);
     }
     for (int a = 0; a < 2; ++a) {
@@ -150,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
-  if (warp == 2 && lane > 0 && lane < l.maps) prefetch_tmap(&maps.m[lane]);
+  if (warp == 3 && lane > 0 && lane < l.maps) prefetch_tmap(&maps.m[lane]);
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();
@@ -160,46 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (!l.last) griddep_launch_dependents();
 
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    const uint32_t full0 = cluster_addr(full, 0);
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-    uint32_t stage = 0, phase = 0;
-    bool ok = true, issued = false;
-    for (int t = pair; ok && t < units; t += pairs) {
-      const Unit x = find_unit(l, t);
-      const Tile& o = x.o;
-      const Problem& p = l.p[o.p];
-      const int bn = x.bn;
-      const int a0 = o.i * kTile + static_cast<int>(rank) * 128, b0 = x.col + static_cast<int>(rank) * (bn >> 1);
-      const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
-      const uint32_t bytes = 4u * static_cast<uint32_t>(kABytes + bn * 64);
-      for (int kb = k0; kb < k1; ++kb) {
-        if (!mbar_poll_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          uint8_t* as = smem + stage * kStageBytes;
-          const uint32_t bar = full0 + 8 * stage;
-          if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
-          load_terms(maps, p.a, o.z, a0, 128, o.i, kb, as, kABytes, bar);
-          load_terms(maps, p.b, o.z, b0, bn >> 1, o.j, kb, as + 2 * kABytes, kBBytes, bar);
-        }
-        issued = true;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    // rank 0: every copy of both CTAs has landed before either may leave
-    if (rank == 0 && issued) {
-      int32_t none = 0;
-      for (int s = 0; s < kStages; ++s) {
-        const uint32_t par = s < static_cast<int>(stage) ? phase : phase ^ 1u;
-        mbar_wait_warp(full + s, par, l.timeout_ns, l.status, kDevTimeout, &none);
-      }
-    }
+    produce<true>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
+  } else if (warp == 2) {
+    produce<false>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
