@@ -14,11 +14,14 @@
 //          not be that of the X whose Gram matrix follows (errors 6 to 20 times
 //          larger where a singular value is small)
 //   apply: p <- decay p - step Q u
-// All tensors of a size class go in one launch of each kernel.
+// All tensors of a size class go in one launch of each kernel.  Matrices that fit
+// into the shared memory of a cluster go through all of it in one kernel, which
+// reads and writes every tensor once; the three kernels are for longer ones.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "entry.h"
 #include "muon.cuh"
 #include "ptx.cuh"
@@ -136,7 +139,7 @@ struct Elements {
   }
   __device__ __forceinline__ bool in(int k) const { return i + k * di < m && j + k * dj < cols; }
   __device__ __forceinline__ int where(int k) const { return in(k) ? at + k * step : 0; }
-  __device__ __forceinline__ int in_tile(int k) const { return (i + k * di) * Cfg<MP>::LD + j + k * dj; }
+  __device__ __forceinline__ int in_tile(int k, int ld = Cfg<MP>::LD) const { return (i + k * di) * ld + j + k * dj; }
 };
 
 template <bool BF16>
@@ -159,7 +162,8 @@ struct Fetched {
   // ... and u from there to shared memory, zero outside of the matrix; FIRST:
   // with the momentum's update.
   template <bool FIRST>
-  __device__ __forceinline__ void put(const Elements<MP>& x, const Momentum& mo, float* mp, float gs, float* u) const {
+  __device__ __forceinline__ void put(const Elements<MP>& x, const Momentum& mo, float* mp, float gs, float* u,
+                                      int ld = Cfg<MP>::LD) const {
 #pragma unroll
     for (int k = 0; k < Cfg<MP>::PER; ++k) {
       float mv = m[k];
@@ -168,7 +172,7 @@ struct Fetched {
         mv = fmaf(mo.mu, mv, mo.rest * gv);
         if (x.in(k)) mp[x.where(k)] = mv;
       }
-      u[x.in_tile(k)] = x.in(k) ? update_of(mo, mv, gv) : 0.f;
+      u[x.in_tile(k, ld)] = x.in(k) ? update_of(mo, mv, gv) : 0.f;
     }
   }
 };
@@ -176,18 +180,18 @@ struct Fetched {
 // c[r][s] += sum over this group's columns of u[i][k] u[j][k] for the thread's
 // rows i = ti + MP/4 r and j = tj + MP/4 s.
 template <int MP>
-__device__ __forceinline__ void gram_tile(const float* u, float (&c)[4][4]) {
+__device__ __forceinline__ void gram_tile(const float* u, int ld, float (&c)[4][4]) {
   using C = Cfg<MP>;
   const int t = threadIdx.x % C::kGroup, g = threadIdx.x / C::kGroup;
-  const float* a = u + (t / (MP / 4)) * C::LD + g * (C::NC / C::kGroups);
-  const float* b = u + (t % (MP / 4)) * C::LD + g * (C::NC / C::kGroups);
+  const float* a = u + (t / (MP / 4)) * ld + g * (C::NC / C::kGroups);
+  const float* b = u + (t % (MP / 4)) * ld + g * (C::NC / C::kGroups);
 #pragma unroll 4
   for (int k = 0; k < C::NC / C::kGroups; k += 4) {
     float4 x[4], y[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      x[r] = *reinterpret_cast<const float4*>(a + r * (MP / 4) * C::LD + k);
-      y[r] = *reinterpret_cast<const float4*>(b + r * (MP / 4) * C::LD + k);
+      x[r] = *reinterpret_cast<const float4*>(a + r * (MP / 4) * ld + k);
+      y[r] = *reinterpret_cast<const float4*>(b + r * (MP / 4) * ld + k);
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -218,7 +222,7 @@ __device__ __forceinline__ void put_gram(float (&c)[4][4], float* u, float* to) 
 
 // u <- Q u for the tile, four rows and columns a thread; q holds Q^T.
 template <int MP>
-__device__ __forceinline__ void mul_tile(const float* q, float* u) {
+__device__ __forceinline__ void mul_tile(const float* q, float* u, int ld) {
   using C = Cfg<MP>;
   const int j = (threadIdx.x % (C::NC / 4)) * 4, i = (threadIdx.x / (C::NC / 4)) * 4;
   float4 y[4];
@@ -226,7 +230,7 @@ __device__ __forceinline__ void mul_tile(const float* q, float* u) {
   for (int r = 0; r < 4; ++r) y[r] = make_float4(0, 0, 0, 0);
 #pragma unroll 4
   for (int k = 0; k < MP; ++k) {
-    const float4 v = *reinterpret_cast<const float4*>(u + k * C::LD + j);
+    const float4 v = *reinterpret_cast<const float4*>(u + k * ld + j);
     const float4 w4 = *reinterpret_cast<const float4*>(q + k * C::LDM + i);
     const float w[4] = {w4.x, w4.y, w4.z, w4.w};
 #pragma unroll
@@ -239,7 +243,7 @@ __device__ __forceinline__ void mul_tile(const float* q, float* u) {
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(u + (i + r) * C::LD + j) = y[r];
+  for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(u + (i + r) * ld + j) = y[r];
   __syncthreads();
 }
 template <int MP>
@@ -280,11 +284,56 @@ __global__ void __launch_bounds__(kThreads, 2)
     f.template put<FIRST>(Elements<MP>(e, n0, n1), e.mo, mp, gs, u);
     __syncthreads();
     if (n0 + C::NC < n1) f.fetch(Elements<MP>(e, n0 + C::NC, n1), mp, gp, need_g);   // under the products
-    if (!FIRST) mul_tile<MP>(q, u);
-    gram_tile<MP>(u, c);
+    if (!FIRST) mul_tile<MP>(q, u, C::LD);
+    gram_tile<MP>(u, C::LD, c);
     __syncthreads();
   }
   put_gram<MP>(c, u, shares + static_cast<int64_t>(blockIdx.x) * MP * MP);
+}
+
+// `n` steps on G, all three [MP][LDM] in shared memory: Q <- P Q, or, `fresh`, Q
+// begins as `first` I.  q holds Q^T.
+template <int MP>
+__device__ __forceinline__ void newton_schulz(float* g, float* p, float* q, int n, bool fresh, float first, int m,
+                                              float ca, float cb, float cc) {
+  using C = Cfg<MP>;
+  float c[C::TR][C::TR];
+  for (int step = 0; step < n; ++step) {
+    zero<MP>(c);
+    dot_rows<MP, MP, C::LDM>(g, g, c);
+#pragma unroll
+    for (int r = 0; r < C::TR; ++r)
+#pragma unroll
+      for (int s = 0; s < C::TR; ++s) {
+        const int i = ti() + 16 * r, j = tj() + 16 * s;
+        c[r][s] = fmaf(cc, c[r][s], cb * g[i * C::LDM + j]) + (i == j && i < m ? ca : 0.f);
+      }
+    put<MP>(p, c);
+    __syncthreads();
+    if (fresh && step == 0) {
+#pragma unroll
+      for (int r = 0; r < C::TR; ++r)
+#pragma unroll
+        for (int s = 0; s < C::TR; ++s) c[r][s] *= first;
+    } else {
+      zero<MP>(c);
+      dot_rows<MP, MP, C::LDM>(q, p, c);   // Q^T P^T
+      __syncthreads();
+    }
+    put<MP>(q, c);
+    if (step + 1 < n) {   // G <- (P G) P
+      zero<MP>(c);
+      dot_rows<MP, MP, C::LDM>(p, g, c);
+      __syncthreads();
+      put<MP>(g, c);
+      __syncthreads();
+      zero<MP>(c);
+      dot_rows<MP, MP, C::LDM>(g, p, c);
+      __syncthreads();
+      put<MP>(g, c);
+    }
+    __syncthreads();
+  }
 }
 
 // One matrix a block: `n` steps from G, the sum of its shares.
@@ -328,42 +377,7 @@ __global__ void __launch_bounds__(kThreads)
     put<MP>(g, c);
     __syncthreads();
   }
-  for (int step = 0; step < n; ++step) {
-    zero<MP>(c);
-    dot_rows<MP, MP, C::LDM>(g, g, c);
-#pragma unroll
-    for (int r = 0; r < C::TR; ++r)
-#pragma unroll
-      for (int s = 0; s < C::TR; ++s) {
-        const int i = ti() + 16 * r, j = tj() + 16 * s;
-        c[r][s] = fmaf(cc, c[r][s], cb * g[i * C::LDM + j]) + (i == j && i < e.m ? ca : 0.f);
-      }
-    put<MP>(p, c);
-    __syncthreads();
-    if (FIRST && step == 0) {   // Q = P / (|u| + eps)
-#pragma unroll
-      for (int r = 0; r < C::TR; ++r)
-#pragma unroll
-        for (int s = 0; s < C::TR; ++s) c[r][s] *= inv;
-    } else {
-      zero<MP>(c);
-      dot_rows<MP, MP, C::LDM>(q, p, c);   // Q^T P^T
-      __syncthreads();
-    }
-    put<MP>(q, c);
-    if (step + 1 < n) {   // G <- (P G) P
-      zero<MP>(c);
-      dot_rows<MP, MP, C::LDM>(p, g, c);
-      __syncthreads();
-      put<MP>(g, c);
-      __syncthreads();
-      zero<MP>(c);
-      dot_rows<MP, MP, C::LDM>(g, p, c);
-      __syncthreads();
-      put<MP>(g, c);
-    }
-    __syncthreads();
-  }
+  newton_schulz<MP>(g, p, q, n, FIRST, inv, e.m, ca, cb, cc);
   for (int i = threadIdx.x; i < MP * MP; i += kThreads) to[i] = q[(i / MP) * C::LDM + i % MP];
 }
 
@@ -394,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
     for (int k = 0; k < C::PER; ++k) pv[k] = p[x.where(k)];
     __syncthreads();
-    mul_tile<MP>(q, u);
+    mul_tile<MP>(q, u, C::LD);
     if (n0 + C::NC < n1) f.fetch(Elements<MP>(e, n0 + C::NC, n1), mp, gp, e.mo.nesterov);
 #pragma unroll
     for (int k = 0; k < C::PER; ++k) {
@@ -406,6 +420,101 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncthreads();
   }
+}
+
+// The whole step of a matrix in one cluster: u stays in the shared memory of its
+// CTAs, each with an equal run of columns, from the momentum's update to the
+// parameter's, so that every tensor is met once.  Shares of a Gram matrix are
+// read from all CTAs in rank order, and every CTA carries out the m x m steps for
+// itself.
+struct Schedule {
+  int32_t steps;
+  float a, b, c, eps;
+};
+template <int MP>
+__host__ __device__ constexpr int cluster_scratch() {   // floats beside u: G, P, Q, this CTA's share, the groups' sums
+  return 3 * MP * Cfg<MP>::LDM + MP * MP + (Cfg<MP>::kGroups > 1 ? Cfg<MP>::kGroups * MP * MP : 0);
+}
+
+template <int MP, bool BF16>
+__global__ void __launch_bounds__(kThreads, 2)
+    muon_cluster_kernel(const __grid_constant__ Table t, const Schedule sc) {
+  using C = Cfg<MP>;
+  extern __shared__ __align__(16) float mem[];
+  float *g = mem, *p = g + MP * C::LDM, *q = p + MP * C::LDM, *share = q + MP * C::LDM;
+  float* groups = share + MP * MP;
+  float* u = mem + cluster_scratch<MP>();
+  griddep_wait();
+  const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
+  const int matrix = static_cast<int>(blockIdx.x) / ranks;
+  int at = 0;
+  while (at + 1 < t.count && matrix >= t.e[at + 1].first_matrix) ++at;
+  const Entry& e = t.e[at];
+  const float gs = e.mo.grad_scale ? __ldg(e.mo.grad_scale) : 1.0f;
+  const int64_t base = static_cast<int64_t>(matrix - e.first_matrix) * e.m * e.n;
+  float *mp = e.mo.m + base, *pp = e.p + base;
+  const Grad<BF16>* gp = static_cast<const Grad<BF16>*>(e.mo.grad) + base;
+  __nv_bfloat16* copy = e.copy + base;
+  const int tiles = (e.n + C::NC - 1) / C::NC;
+  const int first = tiles * rank / ranks * C::NC, last = tiles * (rank + 1) / ranks * C::NC;
+  const int end = min(e.n, last), ld = (tiles + ranks - 1) / ranks * C::NC + 4;
+  for (int n0 = first; n0 < last; n0 += C::NC) {
+    Fetched<MP, BF16> f;
+    const Elements<MP> x(e, n0, end);
+    f.fetch(x, mp, gp, true);
+    f.template put<true>(x, e.mo, mp, gs, u + (n0 - first), ld);
+  }
+  __syncthreads();
+  for (int done = 0; done < sc.steps; done += kMuonPartSteps) {
+    float c[4][4] = {};
+    for (int n0 = first; n0 < last; n0 += C::NC) gram_tile<MP>(u + (n0 - first), ld, c);
+    if (done) cluster_sync();   // the others have read the last share
+    put_gram<MP>(c, groups, share);
+    cluster_sync();
+    for (int i = threadIdx.x; i < MP * MP / 4; i += kThreads) {
+      float4 v = make_float4(0, 0, 0, 0);
+      for (int r = 0; r < ranks; ++r) {
+        const float4 s = cluster_load4(share + 4 * i, r);
+        v = make_float4(v.x + s.x, v.y + s.y, v.z + s.z, v.w + s.w);
+      }
+      *reinterpret_cast<float4*>(g + (4 * i / MP) * C::LDM + 4 * i % MP) = v;
+    }
+    __syncthreads();
+    float inv = 1.0f;
+    if (done == 0) {   // |u|^2 is the trace
+      float s = 0.f;
+      for (int i = 0; i < e.m; ++i) s += g[i * C::LDM + i];
+      inv = 1.0f / (sqrtf(s) + sc.eps);
+      __syncthreads();
+      for (int i = threadIdx.x; i < MP * MP; i += kThreads) {
+        float& v = g[(i / MP) * C::LDM + i % MP];
+        v = (v * inv) * inv;
+      }
+      __syncthreads();
+    }
+    const int n = min(kMuonPartSteps, sc.steps - done);
+    newton_schulz<MP>(g, p, q, n, true, inv, e.m, sc.a, sc.b, sc.c);
+    if (done + n < sc.steps) {
+      for (int n0 = first; n0 < last; n0 += C::NC) mul_tile<MP>(q, u + (n0 - first), ld);
+    } else {
+      for (int n0 = first; n0 < last; n0 += C::NC) {
+        const Elements<MP> x(e, n0, end);
+        float pv[C::PER];
+#pragma unroll
+        for (int k = 0; k < C::PER; ++k) pv[k] = pp[x.where(k)];
+        mul_tile<MP>(q, u + (n0 - first), ld);
+#pragma unroll
+        for (int k = 0; k < C::PER; ++k) {
+          const float v = fmaf(-e.step, u[x.in_tile(k, ld) + n0 - first], t.decay * pv[k]);
+          if (x.in(k)) {
+            pp[x.where(k)] = v;
+            if (e.copy) copy[x.where(k)] = __float2bfloat16_rn(v);
+          }
+        }
+      }
+    }
+  }
+  cluster_sync();   // no CTA leaves while another may read its share
 }
 
 int size_class(const moe_muon_tensor& t) {
@@ -451,6 +560,25 @@ bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Ba
   return b->count > 0;
 }
 
+// CTAs of a cluster, and their shared memory: as few as leave two CTAs an SM
+// (or one, where eight need more), more where there are few matrices.  0: u does
+// not fit into eight CTAs.
+struct ClusterPlan {
+  int ranks, smem;
+};
+template <int MP>
+ClusterPlan cluster_plan(const Batch& b, int64_t most_tiles) {
+  auto smem = [&](int ranks) {
+    const int64_t ld = (most_tiles + ranks - 1) / ranks * Cfg<MP>::NC + 4;
+    return 4 * (cluster_scratch<MP>() + MP * ld);
+  };
+  if (smem(8) > 227 * 1024) return {0, 0};
+  int ranks = 1;
+  while (ranks < 8 && smem(ranks) > 113 * 1024) ranks *= 2;
+  while (ranks < 8 && b.matrices * ranks * 2 <= kTargetBlocks && 2 * ranks <= most_tiles) ranks *= 2;
+  return {ranks, static_cast<int>(smem(ranks))};
+}
+
 struct SmallWs {
   size_t shares, q, total;
 };
@@ -490,13 +618,36 @@ int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_optio
     blocks += x.count * static_cast<int64_t>(e.blocks);
     matrices += x.count;
   }
+  int64_t most_tiles = 1;
+  for (int i = 0; i < b.count; ++i) most_tiles = std::max(most_tiles, tiles_of(t[b.index[i]]));
+  const ClusterPlan plan = cluster_plan<MP>(b, most_tiles);
+  const float a = static_cast<float>(o->coefficients[0]), c1 = static_cast<float>(o->coefficients[1]),
+              c2 = static_cast<float>(o->coefficients[2]), eps = static_cast<float>(o->eps);
+  if (plan.ranks) {
+    static DeviceOnce once;
+    MOE_CUDA(set_smem_limit_once(muon_cluster_kernel<MP, BF16>, 227 * 1024, once));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(b.matrices * plan.ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = plan.smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(plan.ranks);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const Schedule sc = {o->ns_steps, a, c1, c2, eps};
+    MOE_CUDA(cudaLaunchKernelEx(&cfg, muon_cluster_kernel<MP, BF16>, tab, sc));
+    return MOE_OK;
+  }
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   constexpr int kSteps = 3 * MP * Cfg<MP>::LDM * 4;
   static DeviceOnce once_first, once_next;
   MOE_CUDA(set_smem_limit_once(muon_small_steps_kernel<MP, true>, kSteps, once_first));
   MOE_CUDA(set_smem_limit_once(muon_small_steps_kernel<MP, false>, kSteps, once_next));
-  const float a = static_cast<float>(o->coefficients[0]), c1 = static_cast<float>(o->coefficients[1]),
-              c2 = static_cast<float>(o->coefficients[2]), eps = static_cast<float>(o->eps);
   for (int done = 0; done < o->ns_steps; done += kMuonPartSteps) {
     const int n = std::min(kMuonPartSteps, o->ns_steps - done);
     const dim3 each(static_cast<unsigned>(matrices));

@@ -56,7 +56,7 @@ def relative(x, ref):
 
 
 SHAPES = [(1, 1), (1, 7), (5, 3), (2, 16, 7168), (16, 33), (3, 64, 64), (4, 65, 200), (333, 1001), (2, 777, 129),
-          (256, 7168), (3, 300, 256), (640, 640), (2, 129, 1024), (1000, 520)]
+          (256, 7168), (3, 300, 256), (640, 640), (2, 129, 1024), (1000, 520), (16, 30001), (60, 7168), (2, 9000, 40)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
