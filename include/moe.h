@@ -552,7 +552,8 @@ typedef struct {
 } moe_muon_tensor;
 
 typedef struct {
-  double lr, momentum, weight_decay, eps;
+  double lr, momentum, weight_decay;
+  double eps;                /* at least 1e-30 */
   double coefficients[3];    /* a, b, c */
   int32_t ns_steps;          /* 1 .. 12 */
   int32_t nesterov;          /* 0 or 1 */
@@ -575,8 +576,8 @@ size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count,
  * two fp16 terms (22 bits) and float sums: X is as near to the formula as 32-bit
  * arithmetic brings it, to a small factor.  The sum of u^2 is float: |u|_F
  * between 1e-18 and 1e18.  A NaN or infinite gradient makes its matrix NaN.
- * Coefficients whose steps leave every bound, or with |b| > 64 |c|, are refused
- * with MOE_ERR_UNSUPPORTED.
+ * Coefficients that are not finite, whose steps leave every bound, or with c = 0 or
+ * |b| > 64 |c|, are refused with MOE_ERR_UNSUPPORTED.
  * `tensors` and `options` are host memory, read before the call returns: lr and
  * the other scalars become part of the launches, and a step captured into a
  * CUDA graph repeats them at every replay.  `status` as in moe_ffn_forward. */

@@ -279,10 +279,8 @@ class Muon(_Status):
             self.bind_grads(grads)
         dev, o = A._device(), self._options
         _same_device(dev, self._dev)
-        if grad_scale is not None:
-            _lib._check_tensor(grad_scale, "grad_scale", cuda=True, dtype=torch.float32, numel=1,
-                               device=dev)
-        o.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
+        o.grad_scale = None if grad_scale is None else A._check_numel(
+            grad_scale, "grad_scale", 0, torch.float32, 1, dev)
         n = self._workspace_size()
         ws = _scratch(n, self._status)
         check(self._lib.moe_muon_step(self._table, len(self._params), o, ws.data_ptr(), n,

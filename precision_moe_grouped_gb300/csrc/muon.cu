@@ -813,7 +813,9 @@ int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_optio
   if (o->reserved[0] || o->reserved[1]) return entry_fail(MOE_ERR_INVALID_ARG, "reserved must be zero");
   if (!ptr_aligned(o->grad_scale, 4))
     return entry_fail(MOE_ERR_MISALIGNED, "grad_scale must be 4-byte aligned");
-  if (!(std::fabs(o->coefficients[1]) <= 64 * std::fabs(o->coefficients[2])))
+  if (!std::isfinite(o->coefficients[0]) || !std::isfinite(o->coefficients[2]) ||
+      o->coefficients[2] == 0 ||
+      !(std::fabs(o->coefficients[1]) <= 64 * std::fabs(o->coefficients[2])))
     return entry_fail(MOE_ERR_UNSUPPORTED, "coefficients (%g, %g, %g): c must be at least |b| / 64", o->coefficients[0],
                       o->coefficients[1], o->coefficients[2]);
   if (!make_scales(o, sc))
