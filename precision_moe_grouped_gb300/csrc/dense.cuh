@@ -90,7 +90,6 @@ struct Launch {
   Args e[kMaxProblems];        // the epilogue's arguments
   int32_t problems, tiles, maps;
   int32_t stages, slot;        // slots of the operands, bytes of one
-  int32_t last;                // the call's last kernel: lets no successor start early
   int32_t early;               // kEarlyA, kEarlyB: that operand is the call's input, and this not its first kernel
   int32_t* status;
   uint64_t timeout_ns;
@@ -224,9 +223,6 @@ __device__ __forceinline__ void box_store(const CUtensorMap* m, const uint8_t* b
 __device__ __forceinline__ void box_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
 }
-__device__ __forceinline__ void box_wait_all() {
-  asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
@@ -349,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // (a producer of an early operand reads nothing that a kernel of the call writes)
   if (!(warp == 0 && l.early == kEarlyA) && !(warp == 2 && l.early == kEarlyB)) {
     griddep_wait();
-    if (!l.last) griddep_launch_dependents();
+    griddep_launch_dependents();
   }
 
   if (warp == 0) {
@@ -423,7 +419,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(release + static_cast<uint32_t>(8 * acc));
     }
-    if (lane == 0) box_wait_all();
+    if (lane == 0) box_wait_read();   // the kernel's end waits for the writes
   }
 
   tc_fence_before();

@@ -227,23 +227,35 @@ struct EpiGateGrad {
 // [shares][rows][tp], the tokens side by side; a block joins 16 features of 64
 // tokens, four tokens of a feature a thread, and turns them through shared
 // memory, so that both sides are met in long runs.
-constexpr int kJoinThreads = 256, kJoinFeatures = 16, kJoinTokens = 64;
+constexpr int kJoinThreads = 256, kJoinFeatures = 16, kJoinTokens = 64;   // a feature's four tokens a thread
 
 struct Sums {
   const float* at;
   int32_t shares, rows, tp;
+};
+// Four tokens from t on of row r, over the shares in order; the loads of up to
+// eight shares are in flight together.
+struct Joined {
+  float4 v[8];
 
-  // four tokens from t on of row r, over the shares in order
-  __device__ __forceinline__ float4 joined(int r, int t) const {
-    const float* p = at + static_cast<int64_t>(r) * tp + t;
-    const int64_t step = static_cast<int64_t>(rows) * tp;
-    float4 v = *reinterpret_cast<const float4*>(p);
-#pragma unroll 4
-    for (int s = 1; s < shares; ++s) {
-      const float4 x = *reinterpret_cast<const float4*>(p + s * step);
-      v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+  __device__ __forceinline__ void load(const Sums& s, int r, int t, int first) {
+    const float* p = s.at + static_cast<int64_t>(r) * s.tp + t;
+    const int64_t step = static_cast<int64_t>(s.rows) * s.tp;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (first + i < s.shares) v[i] = *reinterpret_cast<const float4*>(p + (first + i) * step);
+  }
+  __device__ __forceinline__ float4 sum(const Sums& s, int r, int t) {
+    float4 x = v[0];
+    for (int first = 0;;) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (first + i < s.shares && first + i > 0)
+          x = make_float4(x.x + v[i].x, x.y + v[i].y, x.z + v[i].z, x.w + v[i].w);
+      }
+      if ((first += 8) >= s.shares) return x;
+      load(s, r, t, first);
     }
-    return v;
   }
 };
 
@@ -273,10 +285,12 @@ __global__ void __launch_bounds__(kJoinThreads)
   griddep_launch_dependents();
   const int f0 = blockIdx.x * kJoinFeatures, t0 = blockIdx.y * kJoinTokens;
   const int t = (threadIdx.x & 15) * 4;
-#pragma unroll
-  for (int f = threadIdx.x >> 4; f < kJoinFeatures; f += 16) {
-    if (f0 + f >= inter) continue;
-    const float4 g = s.joined(f0 + f, t0 + t), u = s.joined(inter + f0 + f, t0 + t);
+  const int f = threadIdx.x >> 4;
+  if (f0 + f < inter) {
+    Joined jg, ju;
+    jg.load(s, f0 + f, t0 + t, 0);
+    ju.load(s, inter + f0 + f, t0 + t, 0);
+    const float4 g = jg.sum(s, f0 + f, t0 + t), u = ju.sum(s, inter + f0 + f, t0 + t);
     turned.put(f, t, make_float4(swiglu(g.x, u.x), swiglu(g.y, u.y), swiglu(g.z, u.z), swiglu(g.w, u.w)));
   }
   __syncthreads();
@@ -289,16 +303,18 @@ __global__ void __launch_bounds__(kJoinThreads)
                     __nv_bfloat16* out, int64_t ld_out) {
   __shared__ __align__(16) float turned[kJoinTokens][kJoinFeatures + 4];
   griddep_wait();
+  griddep_launch_dependents();
   const int f0 = blockIdx.x * kJoinFeatures, t0 = blockIdx.y * kJoinTokens;
   const int t = (threadIdx.x & 15) * 4;
-#pragma unroll
-  for (int f = threadIdx.x >> 4; f < kJoinFeatures; f += 16) {
-    if (f0 + f >= cols) continue;
-    const float4 v = s.joined(f0 + f, t0 + t);
-    turned[t][f] = v.x;
-    turned[t + 1][f] = v.y;
-    turned[t + 2][f] = v.z;
-    turned[t + 3][f] = v.w;
+  const int feature = threadIdx.x >> 4;
+  if (f0 + feature < cols) {
+    Joined j;
+    j.load(s, f0 + feature, t0 + t, 0);
+    const float4 v = j.sum(s, f0 + feature, t0 + t);
+    turned[t][feature] = v.x;
+    turned[t + 1][feature] = v.y;
+    turned[t + 2][feature] = v.z;
+    turned[t + 3][feature] = v.w;
   }
   __syncthreads();
   const int tt = threadIdx.x >> 1, f = (threadIdx.x & 1) * 8;
@@ -323,10 +339,14 @@ __global__ void __launch_bounds__(kJoinThreads)
   griddep_launch_dependents();
   const int f0 = blockIdx.x * kJoinFeatures, t0 = blockIdx.y * kJoinTokens;
   const int t = (threadIdx.x & 15) * 4;
-#pragma unroll
-  for (int f = threadIdx.x >> 4; f < kJoinFeatures; f += 16) {
-    if (f0 + f >= inter) continue;
-    const float4 g = gu.joined(f0 + f, t0 + t), u = gu.joined(inter + f0 + f, t0 + t), d = dh.joined(f0 + f, t0 + t);
+  const int f = threadIdx.x >> 4;
+  if (f0 + f < inter) {
+    Joined jg, ju, jd;
+    jg.load(gu, f0 + f, t0 + t, 0);
+    ju.load(gu, inter + f0 + f, t0 + t, 0);
+    jd.load(dh, f0 + f, t0 + t, 0);
+    const float4 g = jg.sum(gu, f0 + f, t0 + t), u = ju.sum(gu, inter + f0 + f, t0 + t);
+    const float4 d = jd.sum(dh, f0 + f, t0 + t);
     const Grads a = swiglu_grads(g.x, u.x, d.x), b = swiglu_grads(g.y, u.y, d.y);
     const Grads c = swiglu_grads(g.z, u.z, d.z), e = swiglu_grads(g.w, u.w, d.w);
     th.put(f, t, make_float4(a.h, b.h, c.h, e.h));
@@ -465,6 +485,7 @@ __global__ void __launch_bounds__(kDecodeThreads)
     if (s0 < s1) even.load_w(rows, s0, t, K);
     if (!waited) {   // the weights are the call's inputs, h is the kernel before's
       griddep_wait();
+      griddep_launch_dependents();
       waited = true;
     }
     if (s0 < s1) even.load_x(xr, s0, t, K);
@@ -737,7 +758,6 @@ int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const v
   MOE_TRY(dense::make_map(&m.m[2], out, Elem::kBf16, T, H, ld_out, 64, 32));
   l.problems = 1;
   l.maps = 3;
-  l.last = 1;
   l.early = dense::kEarlyB;
   l.p[0] = dense::make_problem(w.down, T, H, dense::cdiv(I, dense::kBK), 0, false, 1, false, true);
   l.e[0] = {add, ld_base, 2, s->num_tokens, s->hidden};
@@ -794,7 +814,6 @@ int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, 
   // dx = [dg du] [Wg; Wu] (the weights MN-major), and the weights' gradients,
   // sums over the tokens (both operands MN-major), in one launch
   auto l = new_launch<EpiOut>(status);
-  l.last = 1;
   if (dx) {
     const int i = l.problems++, k = l.maps;
     l.maps += 3;

@@ -389,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   __shared__ __align__(16) float u[MP * C::LD];
   __shared__ __align__(16) float q[MP * C::LDM];
   griddep_wait();
+  griddep_launch_dependents();
   const Work w = find_block(t, blockIdx.x);
   const Entry& e = t.e[w.e];
   const float gs = e.mo.grad_scale ? __ldg(e.mo.grad_scale) : 1.0f;
@@ -445,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* groups = share + MP * MP;
   float* u = mem + cluster_scratch<MP>();
   griddep_wait();
+  griddep_launch_dependents();
   const int ranks = static_cast<int>(cluster_size()), rank = static_cast<int>(cluster_rank());
   const int matrix = static_cast<int>(blockIdx.x) / ranks;
   int at = 0;

@@ -69,7 +69,7 @@ struct Launch {
   static constexpr int kMost = kMaxProblems;
   Problem p[kMaxProblems];
   Args e[kMaxProblems];
-  int32_t problems, tiles, whole, maps, last;
+  int32_t problems, tiles, whole, maps;
   int32_t* status;
   uint64_t timeout_ns;
 };
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   griddep_wait();
-  if (!l.last) griddep_launch_dependents();
+  griddep_launch_dependents();
 
   if (warp == 0) {
     produce<true>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       Epi::run(l.e[o.p], o, w, col, half, maps, sums);
     }
-    if (lane == 0) dense::box_wait_all();
+    if (lane == 0) dense::box_wait_read();
   }
 
   tc_fence_before();
