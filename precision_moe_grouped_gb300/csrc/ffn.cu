@@ -222,7 +222,7 @@ struct EpiGateGrad {
 };
 
 // ------------------------------------------------------- joining K's shares
-// Batches of up to 256 tokens: the weights are the 256 rows of a tile, the
+// Batches of few hundred tokens: the weights are the 256 rows of a tile, the
 // tokens its columns, and K is shared out until the pairs are busy.  Sums are
 // [shares][rows][tp], the tokens side by side; a block joins 16 features of 64
 // tokens, four tokens of a feature a thread, and turns them through shared
@@ -560,23 +560,44 @@ cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
 // ------------------------------------------------------------------- plans
 constexpr int64_t up32(int64_t v) { return (v + 31) / 32 * 32; }
 
-// A product whose tokens are the columns of one tile: weights [rows, K], K
-// shared out over the pairs, at least four blocks a share.
-constexpr int kTurnTokens = 256;   // at most
-dense::Plan turned_plan(int64_t tokens, int64_t rows, int64_t kb, int64_t pairs) {
-  dense::Plan p;
-  p.bn = static_cast<int32_t>((tokens + 63) / 64 * 64);
-  const int64_t tiles = dense::cdiv(rows, dense::kTile);
+// A product whose tokens are the columns of a tile (of two or more equal ones above
+// 256): weights [rows, K], K shared out over the pairs, at least four blocks a
+// share.
+struct TurnPlan : dense::Plan {
+  int32_t tp;   // tokens of all tiles
+};
+TurnPlan turned_plan(int64_t tokens, int64_t rows, int64_t kb, int64_t pairs) {
+  TurnPlan p;
+  const int64_t tn = std::max<int64_t>(1, dense::cdiv(tokens, 256));
+  p.bn = static_cast<int32_t>((dense::cdiv(tokens, tn) + 63) / 64 * 64);
+  p.tp = static_cast<int32_t>(tn * p.bn);
+  const int64_t tiles = dense::cdiv(rows, dense::kTile) * tn;
   const int64_t s = std::max<int64_t>(1, std::min(pairs / tiles, kb / 4));
   p.kb_split = static_cast<int32_t>(dense::cdiv(kb, s));
   p.splits = static_cast<int32_t>(dense::cdiv(kb, p.kb_split));
   return p;
 }
-int64_t sums_bytes(const dense::Plan& p, int64_t rows) { return 4 * p.splits * up32(rows) * p.bn; }
+int64_t sums_bytes(const TurnPlan& p, int64_t rows) { return 4 * p.splits * up32(rows) * p.tp; }
+
+// Where that is the faster way (measured at 7168 x 2048, 4096 x 1800, 2048 x 1024,
+// 7168 x 256 and 512 x 256).  Forward: both ways are two products, and shares of K cost two joins of
+// some 3 us, more with the tokens; they pay where the products are long (64
+// tokens: 7168 x 2048 27.9 against 38 us, 512 x 256 12.5 against 10.9; 131 tokens:
+// 7168 x 256 22.6 against 32.2, 2048 x 1024 19.1 against 18.3; 256 tokens level or
+// behind but for the narrow block).  Backward: one join for two products
+// (300 tokens: 98.8 against 111.9, 30.8 against 42.1, 14.8 against 21.3; 700:
+// 133 against 148, 39.9 against 46.6; 1024: 191 against 173, 48.6 against 49.9).
+constexpr int kTurnForward = 256, kTurnBackward = 768;   // tokens, at most
+bool turned(const moe_ffn_shape* s, bool backward) {
+  const int64_t blocks = dense::cdiv(s->hidden, dense::kBK) + dense::cdiv(s->inter, dense::kBK);
+  if (backward) return s->num_tokens <= kTurnBackward;
+  return s->num_tokens <= kTurnForward && blocks >= 16 + s->num_tokens / 4;
+}
 
 struct FfnWs {
   dense::Plan gate, down;   // forward; gate also in the backward pass
   dense::Plan dh, dx;
+  TurnPlan t_gate, t_down, t_dh;   // those of them whose tokens are columns
   bool turned;              // gate, down and dh as turned_plan's
   size_t h, dgu, sums, sums2, total;
 };
@@ -597,17 +618,17 @@ FfnWs ffn_ws(const moe_ffn_shape* s, bool backward) {
     return w;
   }
   const int64_t kh = dense::cdiv(H, dense::kBK), ki = dense::cdiv(I, dense::kBK);
-  w.turned = T <= kTurnTokens;
+  w.turned = turned(s, backward);
   if (w.turned && !backward) {
-    w.gate = turned_plan(T, 2 * I, kh, dense::kPlanPairs);
-    w.down = turned_plan(T, H, ki, dense::kPlanPairs);
-    w.sums = take(sums_bytes(w.gate, 2 * I));
-    w.sums2 = take(sums_bytes(w.down, H));
+    w.t_gate = turned_plan(T, 2 * I, kh, dense::kPlanPairs);
+    w.t_down = turned_plan(T, H, ki, dense::kPlanPairs);
+    w.sums = take(sums_bytes(w.t_gate, 2 * I));
+    w.sums2 = take(sums_bytes(w.t_down, H));
   } else if (w.turned) {   // x [Wg; Wu]^T and dout Wd in one launch: two and one of three parts
-    w.gate = turned_plan(T, 2 * I, kh, dense::kPlanPairs * 2 / 3);
-    w.dh = turned_plan(T, I, kh, dense::kPlanPairs / 3);
-    w.sums = take(sums_bytes(w.dh, I));
-    w.sums2 = take(sums_bytes(w.gate, 2 * I));
+    w.t_gate = turned_plan(T, 2 * I, kh, dense::kPlanPairs * 2 / 3);
+    w.t_dh = turned_plan(T, I, kh, dense::kPlanPairs / 3);
+    w.sums = take(sums_bytes(w.t_dh, I));
+    w.sums2 = take(sums_bytes(w.t_gate, 2 * I));
   } else {
     w.gate = dense::make_plan(tm, 2 * I, kh);
     w.down = dense::make_plan(tm, H, ki);
@@ -680,17 +701,17 @@ constexpr int kSquare = dense::kBK;
 
 // Adds the sums of W x^T (turned_plan): weights w [rows, K], or [K, rows] with
 // mn, against tokens x [T, K].
-int32_t add_turned(Maps* m, dense::Launch<EpiSum::Args>* l, const dense::Plan& plan, const void* w, int64_t rows,
+int32_t add_turned(Maps* m, dense::Launch<EpiSum::Args>* l, const TurnPlan& plan, const void* w, int64_t rows,
                    int64_t k, bool mn, const void* x, int64_t ld_x, int64_t tokens, float* sums, Sums* out) {
   const int i = l->problems++, at = l->maps;
   l->maps += 3;
   if (mn) MOE_TRY(dense::make_map(&m->m[at], w, Elem::kBf16, k, rows, rows, kSquare, kSquare));
   else MOE_TRY(dense::make_map(&m->m[at], w, Elem::kBf16, rows, k, k, dense::kBK, 128));
   MOE_TRY(dense::make_map(&m->m[at + 1], x, Elem::kBf16, tokens, k, ld_x, dense::kBK, plan.bn / 2));
-  MOE_TRY(dense::make_map(&m->m[at + 2], sums, Elem::kF32, plan.splits * up32(rows), plan.bn, plan.bn, 32, 32));
-  l->p[i] = dense::make_problem(plan, rows, tokens, dense::cdiv(k, dense::kBK), at, mn, at + 1, false, true);
-  l->e[i] = {at + 2, static_cast<int32_t>(up32(rows)), plan.bn};
-  *out = {sums, plan.splits, static_cast<int32_t>(up32(rows)), plan.bn};
+  MOE_TRY(dense::make_map(&m->m[at + 2], sums, Elem::kF32, plan.splits * up32(rows), plan.tp, plan.tp, 32, 32));
+  l->p[i] = dense::make_problem(plan, rows, plan.tp, dense::cdiv(k, dense::kBK), at, mn, at + 1, false, true);
+  l->e[i] = {at + 2, static_cast<int32_t>(up32(rows)), plan.tp};
+  *out = {sums, plan.splits, static_cast<int32_t>(up32(rows)), plan.tp};
   return MOE_OK;
 }
 
@@ -728,13 +749,13 @@ int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const v
     MOE_CUDA(dense::resident_pairs<EpiSum>(sms, &pairs));
     Sums sums;
     auto l = new_launch<EpiSum>(status);
-    MOE_TRY(add_turned(&m, &l, w.gate, wgu, 2 * I, H, false, x, ld_x, T, reinterpret_cast<float*>(ws + w.sums), &sums));
+    MOE_TRY(add_turned(&m, &l, w.t_gate, wgu, 2 * I, H, false, x, ld_x, T, reinterpret_cast<float*>(ws + w.sums), &sums));
     MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
     MOE_CUDA(launch_pdl(join_gate_kernel, join_grid(T, I), dim3(kJoinThreads), 0, st, sums, s->num_tokens, s->inter,
                         h));
     l = new_launch<EpiSum>(status);
     l.early = dense::kEarlyA;
-    MOE_TRY(add_turned(&m, &l, w.down, wd, H, I, false, h, I, T, reinterpret_cast<float*>(ws + w.sums2), &sums));
+    MOE_TRY(add_turned(&m, &l, w.t_down, wd, H, I, false, h, I, T, reinterpret_cast<float*>(ws + w.sums2), &sums));
     MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
     MOE_CUDA(launch_pdl(join_out_kernel, join_grid(T, H), dim3(kJoinThreads), 0, st, sums, s->num_tokens, s->hidden,
                         add, ld_base, to, ld_out));
@@ -783,9 +804,9 @@ int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, 
   if (w.turned) {
     Sums sums_gu, sums_dh;
     auto l = new_launch<EpiSum>(status);
-    MOE_TRY(add_turned(&m, &l, w.gate, wgu, 2 * I, H, false, x, ld_x, T, reinterpret_cast<float*>(ws + w.sums2),
+    MOE_TRY(add_turned(&m, &l, w.t_gate, wgu, 2 * I, H, false, x, ld_x, T, reinterpret_cast<float*>(ws + w.sums2),
                        &sums_gu));
-    MOE_TRY(add_turned(&m, &l, w.dh, wd, I, H, true, dout, ld_dout, T, dh, &sums_dh));
+    MOE_TRY(add_turned(&m, &l, w.t_dh, wd, I, H, true, dout, ld_dout, T, dh, &sums_dh));
     MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
     MOE_CUDA(launch_pdl(join_grad_kernel, join_grid(T, I), dim3(kJoinThreads), 0, st, sums_gu, sums_dh,
                         s->num_tokens, s->inter, h, dgu));

@@ -27,7 +27,7 @@ BF16 = torch.bfloat16
 TOKENS = [1, 24, 33, 200, 256, 257, 700]       # every path: streamed weights, shares of K, tiles
 
 
-def block(T, H=520, I=264, seed=1):
+def block(T, H=4104, I=264, seed=1):
     s = F.make(T, H, I, seed=seed)
     return s, P.GatedFFN(s["wgu"], s["wd"])
 
@@ -38,7 +38,7 @@ def test_strides_and_neighbours(cuda_ok, T):
     """Strided inputs and outputs give the same bits, and what lies between and
     behind the rows stays as it was."""
     s, op = block(T)
-    H = 520
+    H = 4104
     wide = {k: torch.full((T + 5, H + 40), 7.0, device="cuda", dtype=BF16) for k in ("x", "base", "dout", "dx_base")}
     for k, t in wide.items():
         t[:T, 16:16 + H] = s[k]
@@ -81,11 +81,11 @@ def test_in_place_and_parts(cuda_ok, T):
 
 def test_without_tokens(cuda_ok):
     _, op = block(1)
-    x = torch.empty((0, 520), device="cuda", dtype=BF16)
-    assert op(x).shape == (0, 520)
-    dw = [torch.ones((2 * 264, 520), device="cuda", dtype=BF16), torch.ones((520, 264), device="cuda", dtype=BF16)]
+    x = torch.empty((0, 4104), device="cuda", dtype=BF16)
+    assert op(x).shape == (0, 4104)
+    dw = [torch.ones((2 * 264, 4104), device="cuda", dtype=BF16), torch.ones((4104, 264), device="cuda", dtype=BF16)]
     dx, a, b = op.backward(x, x, dw_gate_up=dw[0], dw_down=dw[1])
-    assert dx.shape == (0, 520) and not a.any() and not b.any()
+    assert dx.shape == (0, 4104) and not a.any() and not b.any()
 
 
 @pytest.mark.parametrize("T", TOKENS[1:])
@@ -168,7 +168,7 @@ def test_streams(cuda_ok, T):
 def test_graph(cuda_ok, T):
     """Forward and backward captured (the first call of this size, so nothing is set up
     outside) and replayed with new inputs and weights, beside another graph."""
-    a, b = F.make(T, 520, 264, seed=1), F.make(T, 520, 264, seed=2)
+    a, b = F.make(T, 4104, 264, seed=1), F.make(T, 4104, 264, seed=2)
     op = P.GatedFFN(a["wgu"].clone(), a["wd"].clone())
     held = {k: a[k].clone() for k in ("x", "base", "dout")}
     graphs, outs = [], []

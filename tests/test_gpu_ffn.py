@@ -63,7 +63,8 @@ def close(got, want, name, few=False):
 
 SIZES = [(1, 256, 128), (1, 8, 8), (3, 2048, 1000), (8, 7168, 2048), (9, 520, 264), (17, 1024, 512),
          (32, 2048, 1024), (33, 2048, 1024), (64, 256, 128), (77, 2048, 1000), (131, 7168, 2048),
-         (255, 512, 256), (256, 512, 256), (257, 520, 264), (513, 2048, 1024), (1021, 904, 8),
+         (64, 2048, 2048), (100, 4096, 136), (255, 512, 256), (255, 4096, 1024), (256, 512, 256), (256, 7168, 256),
+         (257, 520, 264), (513, 2048, 1024), (768, 264, 520), (769, 264, 520), (1021, 904, 8),
          (1021, 8, 360), (2500, 2048, 1024)]
 
 
