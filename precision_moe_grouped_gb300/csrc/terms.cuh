@@ -63,13 +63,14 @@ struct Problem {
   int32_t first_tile;
 };
 // The launch's tiles of 256 x 256 are taken whole up to `whole`; each of the rest
-// is two units of 128 columns, where that fills the last round of the pairs.
+// is `cut` units of 256 / cut columns, where those all fit into the last round of
+// the pairs.
 template <typename Args>
 struct Launch {
   static constexpr int kMost = kMaxProblems;
   Problem p[kMaxProblems];
   Args e[kMaxProblems];
-  int32_t problems, tiles, whole, maps;
+  int32_t problems, tiles, whole, cut, maps;
   int32_t* status;
   uint64_t timeout_ns;
 };
@@ -81,15 +82,16 @@ struct Unit {
 };
 template <typename L>
 __device__ __forceinline__ int num_units(const L& l) {
-  return l.whole + 2 * (l.tiles - l.whole);
+  return l.whole + l.cut * (l.tiles - l.whole);
 }
 template <typename L>
 __device__ __forceinline__ Unit find_unit(const L& l, int u) {
   const int rest = u - l.whole;
   Unit x;
-  x.bn = rest < 0 ? 256 : 128;
-  x.o = dense::find_tile(l, rest < 0 ? u : l.whole + (rest >> 1));
-  x.col = x.o.j * 256 + (rest < 0 ? 0 : (rest & 1) * 128);
+  const int tile = rest < 0 ? u : l.whole + rest / l.cut;
+  x.bn = rest < 0 ? 256 : 256 / l.cut;
+  x.o = dense::find_tile(l, tile);
+  x.col = x.o.j * 256 + (rest < 0 ? 0 : (rest - (tile - l.whole) * l.cut) * x.bn);
   return x;
 }
 
@@ -115,7 +117,8 @@ __device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* s
     const Operand& o = IS_A ? p.a : p.b;
     const int at = IS_A ? x.o.i * kTile + static_cast<int>(rank) * 128
                         : x.col + static_cast<int>(rank) * (x.bn >> 1);
-    const int tr = IS_A ? x.o.i : x.o.j, rows = IS_A ? 128 : x.bn >> 1;
+    // (of a box's 64 rows, units of 64 columns use 32)
+    const int tr = IS_A ? x.o.i : x.o.j, rows = IS_A || x.bn == 256 ? 128 : 64;
     const uint32_t bytes = 4u * static_cast<uint32_t>(rows) * 128u;   // both terms, both CTAs
     const int hi = o.hi + x.o.z * o.batch, lo = o.lo + x.o.z * o.batch;
     const int k0 = x.o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
@@ -157,7 +160,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* s
 }
 
 // Epi: struct Args; static run(args, tile, warp, col, n, maps, sums): the warp's
-// row (lane), columns [col, col + n) in sums[0 .. n), n 128 or 64; and static
+// row (lane), columns [col, col + n) in sums[0 .. n), n 128, 64 or 32; and static
 // ahead(args, tile, warp, col, n), called before the unit's products.
 template <class Epi>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -326,15 +329,16 @@ cudaError_t resident_pairs(int num_sms, int* pairs) {
   static DeviceOnce cache;
   return dense::resident_pairs(terms_kernel<Epi>, kSmemBytes, cache, num_sms, pairs);
 }
-// A unit of 128 columns takes about 0.7 of the time of a whole tile: the last
-// round is cut in halves where they all fit into one.
+// The last round is cut where all of its parts fit into one: a unit of 128 columns
+// takes about 0.7 of the time of a whole tile, one of 64 about half.
 template <class Epi>
 cudaError_t launch(const Maps& maps, Launch<typename Epi::Args>& l, int pairs, cudaStream_t s) {
   int tiles = 0;
   for (int i = 0; i < l.problems; ++i) tiles += l.p[i].per_matrix * l.p[i].batch * l.p[i].splits;
   const int rest = tiles % pairs;
+  l.cut = 4 * rest <= pairs ? 4 : 2;
   l.whole = 2 * rest <= pairs ? tiles - rest : tiles;
-  return dense::launch(terms_kernel<Epi>, kSmemBytes, maps, l, pairs, s, 2 * tiles - l.whole);
+  return dense::launch(terms_kernel<Epi>, kSmemBytes, maps, l, pairs, s, l.whole + l.cut * (tiles - l.whole));
 }
 
 }  // namespace terms
