@@ -474,11 +474,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     put_gram<MP>(c, groups, share);
     cluster_sync();
     for (int i = threadIdx.x; i < MP * MP / 4; i += kThreads) {
+      float4 x[8];   // all ranks' loads in flight together
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < ranks) x[r] = cluster_load4(share + 4 * i, r);
       float4 v = make_float4(0, 0, 0, 0);
-      for (int r = 0; r < ranks; ++r) {
-        const float4 s = cluster_load4(share + 4 * i, r);
-        v = make_float4(v.x + s.x, v.y + s.y, v.z + s.z, v.w + s.w);
-      }
+#pragma unroll
+      for (int r = 0; r < 8; ++r)
+        if (r < ranks) v = make_float4(v.x + x[r].x, v.y + x[r].y, v.z + x[r].z, v.w + x[r].w);
       *reinterpret_cast<float4*>(g + (4 * i / MP) * C::LDM + 4 * i % MP) = v;
     }
     __syncthreads();
@@ -499,12 +502,20 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (done + n < sc.steps) {
       for (int n0 = first; n0 < last; n0 += C::NC) mul_tile<MP>(q, u + (n0 - first), ld);
     } else {
+      // (with 64 rows the products are long enough for the next tile's p to be worth its registers)
+      constexpr bool kAhead = MP == 64;
+      float pv[C::PER], next[C::PER];
+      auto fetch = [&](int n0, float (&to)[C::PER]) {
+        const Elements<MP> x(e, n0, end);
+#pragma unroll
+        for (int k = 0; k < C::PER; ++k) to[k] = pp[x.where(k)];
+      };
+      if (kAhead && first < last) fetch(first, pv);
       for (int n0 = first; n0 < last; n0 += C::NC) {
         const Elements<MP> x(e, n0, end);
-        float pv[C::PER];
-#pragma unroll
-        for (int k = 0; k < C::PER; ++k) pv[k] = pp[x.where(k)];
+        if (!kAhead) fetch(n0, pv);
         mul_tile<MP>(q, u + (n0 - first), ld);
+        if (kAhead && n0 + C::NC < last) fetch(n0 + C::NC, next);
 #pragma unroll
         for (int k = 0; k < C::PER; ++k) {
           const float v = fmaf(-e.step, u[x.in_tile(k, ld) + n0 - first], t.decay * pv[k]);
@@ -512,6 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             pp[x.where(k)] = v;
             if (e.copy) copy[x.where(k)] = __float2bfloat16_rn(v);
           }
+          if (kAhead) pv[k] = next[k];
         }
       }
     }
@@ -562,23 +574,77 @@ bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Ba
   return b->count > 0;
 }
 
-// CTAs of a cluster, and their shared memory: as few as leave two CTAs an SM
-// (or one, where eight need more), more where there are few matrices.  0: u does
-// not fit into eight CTAs.
+// How many clusters of 1 .. 8 CTAs are resident at once, with half of an SM's
+// memory a CTA and with all of it; asked once per kernel and device.
+constexpr int kHalfSm = 113 * 1024, kWholeSm = 227 * 1024;
+template <int MP, bool BF16>
+cudaError_t resident_clusters(int ranks, bool whole, int* n) {
+  static DeviceOnce table[16];
+  cudaError_t e;
+  std::atomic<int>* at = device_entry(table[2 * (ranks - 1) + whole], &e);
+  if (!at) return e;
+  *n = at->load(std::memory_order_acquire);
+  if (*n) return cudaSuccess;
+  auto kern = muon_cluster_kernel<MP, BF16>;
+  static DeviceOnce once;
+  if ((e = set_smem_limit_once(kern, kWholeSm, once)) != cudaSuccess) return e;
+  cudaLaunchConfig_t q = {};
+  q.gridDim = dim3(static_cast<unsigned>(ranks));
+  q.blockDim = dim3(kThreads);
+  q.dynamicSmemBytes = whole ? kWholeSm : kHalfSm;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  q.attrs = attr;
+  q.numAttrs = 1;
+  if ((e = cudaOccupancyMaxActiveClusters(n, kern, &q)) != cudaSuccess) return e;
+  if (*n < 1) return cudaErrorInvalidConfiguration;
+  at->store(*n, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// CTAs of a cluster, and their shared memory: the number that takes the least
+// time, by the rounds of resident clusters, each as long as its longest matrix
+// (measured: 10, 14 or 40 us for the m x m steps and the exchanges, 5, 7 or 12 us a
+// tile).  0 ranks: u does not fit into eight CTAs.
 struct ClusterPlan {
   int ranks, smem;
 };
-template <int MP>
-ClusterPlan cluster_plan(const Batch& b, int64_t most_tiles) {
-  auto smem = [&](int ranks) {
-    const int64_t ld = (most_tiles + ranks - 1) / ranks * Cfg<MP>::NC + 4;
-    return 4 * (cluster_scratch<MP>() + MP * ld);
-  };
-  if (smem(8) > 227 * 1024) return {0, 0};
-  int ranks = 1;
-  while (ranks < 8 && smem(ranks) > 113 * 1024) ranks *= 2;
-  while (ranks < 8 && b.matrices * ranks * 2 <= kTargetBlocks && 2 * ranks <= most_tiles) ranks *= 2;
-  return {ranks, static_cast<int>(smem(ranks))};
+template <int MP, bool BF16>
+cudaError_t cluster_plan(const moe_muon_tensor* t, const Batch& b, int64_t most_tiles, ClusterPlan* best) {
+  constexpr int64_t kOwn = MP == 16 ? 10 : MP == 32 ? 14 : 40, kTile = MP == 16 ? 5 : MP == 32 ? 7 : 12;
+  *best = {0, 0};
+  int64_t least = 0;
+  for (int ranks = 1; ranks <= 8; ++ranks) {
+    auto tiles = [&](int64_t all) { return (all + ranks - 1) / ranks; };
+    const int64_t smem = 4 * (cluster_scratch<MP>() + MP * (tiles(most_tiles) * Cfg<MP>::NC + 4));
+    if (smem > kWholeSm || (ranks > 1 && ranks > most_tiles)) continue;
+    int n;
+    const cudaError_t e = resident_clusters<MP, BF16>(ranks, smem > kHalfSm, &n);
+    if (e != cudaSuccess) return e;
+    int64_t time = 0, left = 0;   // left: places of the round in the making, whose longest is `longest`
+    int64_t longest = 0;
+    for (int i = 0; i < b.count; ++i) {
+      const int64_t each = kOwn + kTile * tiles(tiles_of(t[b.index[i]]));
+      int64_t count = t[b.index[i]].count;
+      const int64_t joined = std::min(count, left);
+      if (joined) longest = std::max(longest, each);
+      count -= joined;
+      left -= joined;
+      if (count) {
+        const int64_t rounds = (count + n - 1) / n;
+        time += longest + (rounds - 1) * each;
+        longest = each;
+        left = rounds * n - count;
+      }
+    }
+    time += longest;
+    if (best->ranks && time >= least) continue;
+    *best = {ranks, static_cast<int>(smem)};
+    least = time;
+  }
+  return cudaSuccess;
 }
 
 struct SmallWs {
@@ -622,12 +688,11 @@ int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_optio
   }
   int64_t most_tiles = 1;
   for (int i = 0; i < b.count; ++i) most_tiles = std::max(most_tiles, tiles_of(t[b.index[i]]));
-  const ClusterPlan plan = cluster_plan<MP>(b, most_tiles);
+  ClusterPlan plan;
+  MOE_CUDA((cluster_plan<MP, BF16>(t, b, most_tiles, &plan)));
   const float a = static_cast<float>(o->coefficients[0]), c1 = static_cast<float>(o->coefficients[1]),
               c2 = static_cast<float>(o->coefficients[2]), eps = static_cast<float>(o->eps);
   if (plan.ranks) {
-    static DeviceOnce once;
-    MOE_CUDA(set_smem_limit_once(muon_cluster_kernel<MP, BF16>, 227 * 1024, once));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(b.matrices * plan.ranks));
     cfg.blockDim = dim3(kThreads);
