@@ -502,20 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (done + n < sc.steps) {
       for (int n0 = first; n0 < last; n0 += C::NC) mul_tile<MP>(q, u + (n0 - first), ld);
     } else {
-      // (with 64 rows the products are long enough for the next tile's p to be worth its registers)
-      constexpr bool kAhead = MP == 64;
-      float pv[C::PER], next[C::PER];
-      auto fetch = [&](int n0, float (&to)[C::PER]) {
-        const Elements<MP> x(e, n0, end);
-#pragma unroll
-        for (int k = 0; k < C::PER; ++k) to[k] = pp[x.where(k)];
-      };
-      if (kAhead && first < last) fetch(first, pv);
-      for (int n0 = first; n0 < last; n0 += C::NC) {
-        const Elements<MP> x(e, n0, end);
-        if (!kAhead) fetch(n0, pv);
-        mul_tile<MP>(q, u + (n0 - first), ld);
-        if (kAhead && n0 + C::NC < last) fetch(n0 + C::NC, next);
+      auto store = [&](const Elements<MP>& x, int n0, const float (&pv)[C::PER]) {
 #pragma unroll
         for (int k = 0; k < C::PER; ++k) {
           const float v = fmaf(-e.step, u[x.in_tile(k, ld) + n0 - first], t.decay * pv[k]);
@@ -523,7 +510,29 @@ __global__ void __launch_bounds__(kThreads, 2)
             pp[x.where(k)] = v;
             if (e.copy) copy[x.where(k)] = __float2bfloat16_rn(v);
           }
-          if (kAhead) pv[k] = next[k];
+        }
+      };
+      if constexpr (MP < 64) {
+        for (int n0 = first; n0 < last; n0 += C::NC) {
+          const Elements<MP> x(e, n0, end);
+          float pv[C::PER];
+#pragma unroll
+          for (int k = 0; k < C::PER; ++k) pv[k] = pp[x.where(k)];
+          mul_tile<MP>(q, u + (n0 - first), ld);
+          store(x, n0, pv);
+        }
+      } else {   // the products are long enough for the next tile's p to be worth its registers
+        float pv[C::PER], next[C::PER];
+        for (int n0 = first - C::NC; n0 < last; n0 += C::NC) {
+          const Elements<MP> x(e, n0, end), y(e, n0 + C::NC, end);
+          if (n0 >= first) mul_tile<MP>(q, u + (n0 - first), ld);
+          if (n0 + C::NC < last) {
+#pragma unroll
+            for (int k = 0; k < C::PER; ++k) next[k] = pp[y.where(k)];
+          }
+          if (n0 >= first) store(x, n0, pv);
+#pragma unroll
+          for (int k = 0; k < C::PER; ++k) pv[k] = next[k];
         }
       }
     }
