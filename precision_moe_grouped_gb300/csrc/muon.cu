@@ -286,24 +286,31 @@ struct EpiShare {
   }
 };
 
+constexpr int kJoinThreads = 64;
 // The shares joined in order: G's planes (and its diagonal blocks + h I), as
 // EpiPlanes stores them.  Four columns a thread.
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kJoinThreads)
     muon_join_kernel(const float* shares, int splits, int64_t batch, int mp, int m, float c, float h, __half* g,
                      __half* diag) {
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
   const int64_t row = i / (mp / 4);   // of all matrices
   if (row >= batch * mp) return;
   const int col = static_cast<int>(i - row * (mp / 4)) * 4, r = static_cast<int>(row % mp);
   const int side = (col >> 8) - (r >> 8);
   if (side < 0) return;
+  const float* at = shares + row * mp + col;
+  const int64_t step = batch * mp * mp;
   float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-  for (int s = 0; s < splits; ++s) {
-    const float4 x = *reinterpret_cast<const float4*>(shares + (s * batch * mp + row) * mp + col);
-    v = make_float4(v.x + x.x, v.y + x.y, v.z + x.z, v.w + x.w);
+  for (int s0 = 0; s0 < splits; s0 += 8) {   // eight shares' loads in flight
+    float4 x[8];
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < splits) x[s] = *reinterpret_cast<const float4*>(at + (s0 + s) * step);
+#pragma unroll
+    for (int s = 0; s < 8; ++s)
+      if (s0 + s < splits) v = make_float4(v.x + x[s].x, v.y + x[s].y, v.z + x[s].z, v.w + x[s].w);
   }
   float d[4] = {v.x * c, v.y * c, v.z * c, v.w * c};
   put_terms(d, g + row * mp + col, batch * mp * mp);
@@ -625,8 +632,8 @@ int32_t gram(const Call& c, Group* gs, int n, float ratio) {
   for (Group* g = gs; g < gs + n; ++g) {
     const Shape& s = g->s;
     if (gram_splits(s) == 1) continue;
-    const int64_t blocks = dense::cdiv(rows_of(s) * (s.mp / 4), kThreads);
-    MOE_CUDA(launch_pdl(muon_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, c.st,
+    const int64_t blocks = dense::cdiv(rows_of(s) * (s.mp / 4), kJoinThreads);
+    MOE_CUDA(launch_pdl(muon_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(kJoinThreads), 0, c.st,
                         reinterpret_cast<const float*>(g->ws + g->w.shares), static_cast<int>(b.l.p[i++].splits),
                         s.batch, s.mp, s.m, g->g.scale / (g->x.scale * g->x.scale), ratio * g->g.scale, g->g.at,
                         g->g.diag));
