@@ -482,6 +482,7 @@ int32_t moe_adamw_step(const moe_adamw_tensor* tensors, int32_t count,
 
 /* Limits of the gated feed-forward block. */
 #define MOE_FFN_MAX_TOKENS (1 << 24)
+#define MOE_FFN_MAX_SUMMED (1 << 16)   /* tokens of a call with weights' gradients */
 #define MOE_FFN_MAX_FEATURES (1 << 17)
 
 /* A gated feed-forward block in bf16 (a shared expert, or a dense layer, beside
@@ -525,7 +526,10 @@ int32_t moe_ffn_forward(const moe_ffn_shape* shape, const void* x, int64_t ld_x,
  *   dw_gate_up  bf16 [2 I, H] = [dg^T x; du^T x]
  *   dw_down     bf16 [H, I] = dout^T (silu(g) u)
  * The weights' gradients are written in full (zero without tokens); both or
- * neither may be NULL.  Sums are float and rounded once; dg, du and silu(g) u
+ * neither may be NULL, and with them num_tokens is at most MOE_FFN_MAX_SUMMED:: a
+ * tensor core cuts its float sums off instead of rounding them, and a sum of n
+ * terms of one sign comes out about n 2^-27.3 of itself short, there 2^-11.
+ * Sums are float and rounded once; dg, du and silu(g) u
  * are rounded to bf16 once, ahead of the products that they enter. */
 int32_t moe_ffn_backward(const moe_ffn_shape* shape, const void* dout, int64_t ld_dout,
                          const void* x, int64_t ld_x, const void* w_gate_up, const void* w_down,
@@ -553,7 +557,7 @@ typedef struct {
 
 typedef struct {
   double lr, momentum, weight_decay;
-  double eps;                /* at least 1e-30 */
+  double eps;                /* at least 1e-16 */
   double coefficients[3];    /* a, b, c */
   int32_t ns_steps;          /* 1 .. 12 */
   int32_t nesterov;          /* 0 or 1 */

@@ -121,7 +121,7 @@ class GatedFFN(_Status):
                  need_dx: bool = True, need_weights: bool = True):
         """(dx, dw_gate_up, dw_down), all bf16, for dout bf16 [T, H]: dx [T, H]
         with dx_base added, the weights' gradients in the weights' shapes (zero
-        without tokens).  The activations are computed again from x.  What is
+        without tokens; of at most 65536 tokens a call).  The activations are computed again from x.  What is
         not needed comes back as None.  `dx` may be `dx_base`, not x or dout."""
         dev, (wgu, wd) = self._start()
         T, H = _rows(x, "x"), self.hidden
@@ -200,8 +200,9 @@ class Muon(_Status):
             state = [torch.zeros_like(p) for p in bound]
         self._state = self._bound(state, "state", torch.float32)
         self._copies = None if copies is None else self._bound(copies, "copies", torch.bfloat16)
-        written = [t for t in (*bound, *self._state, *(self._copies or ())) if t.numel()]
-        if len({t.data_ptr() for t in written}) < len(written):
+        written = [t.data_ptr() for t in (*bound, *self._state, *(self._copies or ())) if t.numel()]
+        self._written = frozenset(written)
+        if len(self._written) < len(written):
             _bad("params, state and copies must be distinct")   # all written, side by side
         self._table = (_lib.MuonTensor * max(1, len(bound)))()
         for i, (e, p, m) in enumerate(zip(self._table, bound, self._state)):
@@ -247,7 +248,10 @@ class Muon(_Status):
         kind = grads[0].dtype if grads else torch.float32
         if kind not in (torch.float32, torch.bfloat16):
             _bad(f"grads must be float32 or bfloat16, got {kind}")
-        self._grads = self._bound(grads, "grads", kind)
+        grads = self._bound(grads, "grads", kind)
+        if not self._written.isdisjoint(t.data_ptr() for t in grads):   # read again after a momentum is written
+            _bad("grads must not be params, state or copies")
+        self._grads = grads
         for e, t in zip(self._table, self._grads):
             e.grad = t.data_ptr()
         self._options.grad_dtype = _lib.MOE_DTYPE_F32 if kind == torch.float32 else _lib.MOE_DTYPE_BF16

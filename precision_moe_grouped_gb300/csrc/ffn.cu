@@ -903,6 +903,8 @@ extern "C" int32_t moe_ffn_backward(const moe_ffn_shape* s, const void* dout, in
   MOE_TRY(check_shape(s));
   if (!dw_gate_up != !dw_down)
     return entry_fail(MOE_ERR_INVALID_ARG, "dw_gate_up and dw_down go together");
+  if (dw_gate_up && s->num_tokens > MOE_FFN_MAX_SUMMED)
+    return entry_fail(MOE_ERR_UNSUPPORTED, "weights' gradients of at most %d tokens a call", MOE_FFN_MAX_SUMMED);
   if (!ptr_aligned(dw_gate_up, 16) || !ptr_aligned(dw_down, 16))
     return entry_fail(MOE_ERR_MISALIGNED, "dw_gate_up and dw_down must be 16-byte aligned");
   cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -813,8 +813,9 @@ int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_optio
     return entry_fail(MOE_ERR_INVALID_ARG, "update_scale %d unknown", o->update_scale);
   if (!(o->momentum >= 0 && o->momentum < 1))
     return entry_fail(MOE_ERR_INVALID_ARG, "momentum must be in [0, 1)");
-  if (!(o->eps >= 1e-30) || !std::isfinite(o->eps) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay))
-    return entry_fail(MOE_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite, eps at least 1e-30");
+  // (with the sum of u^2 in float: a norm that underflows leaves X bounded)
+  if (!(o->eps >= 1e-16) || !std::isfinite(o->eps) || !std::isfinite(o->lr) || !std::isfinite(o->weight_decay))
+    return entry_fail(MOE_ERR_INVALID_ARG, "lr, eps and weight_decay must be finite, eps at least 1e-16");
   if (o->ns_steps < 1 || o->ns_steps > kMaxSteps)
     return entry_fail(MOE_ERR_INVALID_ARG, "ns_steps must be in [1, %d]", kMaxSteps);
   if (o->reserved[0] || o->reserved[1]) return entry_fail(MOE_ERR_INVALID_ARG, "reserved must be zero");

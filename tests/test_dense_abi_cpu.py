@@ -64,6 +64,13 @@ def backward(lib, s, dout=0x100000, ld_dout=64, x=0x200000, ld_x=64, wgu=0x30000
                                 status, None)
 
 
+def test_ffn_tokens_of_weights_gradients(lib):
+    """Sums over the tokens are refused beyond their limit, dx alone is not."""
+    for T, code in ((1 << 16, L.MOE_ERR_WORKSPACE_TOO_SMALL), ((1 << 16) + 1, L.MOE_ERR_UNSUPPORTED)):
+        assert backward(lib, L.FfnShape(T, 64, 32), n=0) == code
+        assert backward(lib, L.FfnShape(T, 64, 32), n=0, dwgu=None, dwd=None) == L.MOE_ERR_WORKSPACE_TOO_SMALL
+
+
 @pytest.mark.parametrize("T", [3, 100, 1000])
 def test_ffn_refusals(lib, T):
     s = L.FfnShape(T, 64, 32)
@@ -129,7 +136,7 @@ def step(lib, t, o, ws=0x400000, n=1 << 50, status=0x500000):
 @pytest.mark.parametrize("bad,code", [
     (dict(lr=float("nan")), L.MOE_ERR_INVALID_ARG), (dict(weight_decay=float("inf")), L.MOE_ERR_INVALID_ARG),
     (dict(momentum=1.0), L.MOE_ERR_INVALID_ARG), (dict(momentum=-0.1), L.MOE_ERR_INVALID_ARG),
-    (dict(eps=0.0), L.MOE_ERR_INVALID_ARG), (dict(eps=1e-31), L.MOE_ERR_INVALID_ARG),
+    (dict(eps=0.0), L.MOE_ERR_INVALID_ARG), (dict(eps=0.9e-16), L.MOE_ERR_INVALID_ARG),
     (dict(ns_steps=0), L.MOE_ERR_INVALID_ARG), (dict(ns_steps=13), L.MOE_ERR_INVALID_ARG),
     (dict(grad_dtype=2), L.MOE_ERR_INVALID_ARG), (dict(update_scale=2), L.MOE_ERR_INVALID_ARG),
     (dict(reserved=0), L.MOE_ERR_INVALID_ARG), (dict(reserved=1), L.MOE_ERR_INVALID_ARG),
@@ -244,7 +251,7 @@ def test_early_operands_are_never_of_a_first_kernel():
     text = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, "ffn.cu")).read())
     assert text.count("l.early = ") == 2
     turned = text.index("l.early = dense::kEarlyA;")
-    assert text.rindex("join_gate_kernel,", 0, turned) > 0 and "w.down, wd" in text[turned:turned + 200]
+    assert text.rindex("join_gate_kernel,", 0, turned) > 0 and "w.t_down, wd" in text[turned:turned + 200]
     whole = text.index("l.early = dense::kEarlyB;")
     assert text.rindex("dense::launch<EpiGate>", 0, whole) > 0 and "w.down" in text[whole:whole + 200]
     up = body("ffn.cu", "decode_kernel")

@@ -155,6 +155,19 @@ def muon(shapes=((3, 20, 30), (40, 16)), grads=torch.float32, copies=True, **kw)
     return P.Muon(z(torch.float32), z(grads), copies=z(BF16) if copies else None, state=z(torch.float32), **kw)
 
 
+def test_muon_gradients_are_memory_of_their_own(lib):
+    """Gradients are read again after the first momentum is written."""
+    op = muon(grads=BF16)
+    for held, kind in ((op.params, torch.float32), (op.state, torch.float32), (op.copies, BF16)):
+        grads = [zeros(3, 20, 30, dtype=kind), held[1]]
+        with pytest.raises(P.MoeError):
+            op.bind_grads(grads)
+        with pytest.raises(P.MoeError):
+            op.step(grads=grads)
+    assert op.grads[0].dtype is BF16 and not any(name == "moe_muon_step" for name, *_ in lib.calls)
+    op.step()
+
+
 def test_muon_arguments(lib):
     op = muon(lr=0.5, momentum=0.25, weight_decay=0.125, eps=1e-3, ns_steps=3, nesterov=False,
               ns_coefficients=(2.0, -1.5, 0.5), update_scale="spectral")
