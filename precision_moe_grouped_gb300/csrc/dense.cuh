@@ -1,24 +1,31 @@
-// dense.cuh -- dense products of bf16 or fp16 matrices on CTA pairs, the core
-// of the gated feed-forward block (ffn.cu) and of the orthogonalised update
-// (muon.cu).
+// dense.cuh -- dense products of bf16 matrices on CTA pairs, the core of the
+// gated feed-forward block (ffn.cu); terms.cuh, on which the orthogonalised update
+// (muon.cu) runs, takes its tiles and its building blocks from here.
 //
-// One persistent launch runs a list of problems D = sum over segments of
-// A_s B_s, each D cut into tiles of 256 x BN (BN = 64 to 256): a CTA pair
-// takes a tile, rank r holds its rows 128 r .. 128 r + 127 in its tensor
-// memory (tcgen05.mma.cta_group::2, M = 256, both operands from shared
-// memory, float accumulators).  A segment is one pair of operands; products
-// of numbers held as two fp16 terms are three segments into one accumulator.
+// One persistent launch runs a list of problems D = A B, each D cut into tiles
+// of 256 x BN (BN = 64 to 256): a CTA pair takes a tile, rank r holds its rows
+// 128 r .. 128 r + 127 in its tensor memory (tcgen05.mma.cta_group::2, M = 256,
+// both operands from shared memory, float accumulators).
 // Operands are K-major ([rows, K], K contiguous) or MN-major ([K, rows], rows
 // contiguous); the TMA boxes and the descriptors differ, the loop does not, so
 // no operand is ever transposed in memory.
 //
 // Per K block of 64 a CTA stages its 128 rows of A and its half of B (16 +
 // 16 KB at BN = 256); six stages, or up to nine smaller ones, keep 192 KB in
-// flight.  Two accumulators of
-// 256 columns let the epilogue of a tile run under the next one's products.
+// flight.  Two accumulators of 256 columns let the epilogue of a tile run under
+// the next one's products.
 //   warps 0, 2: TMA producers of A, B   warp 1: MMA issuer (rank 0), TMEM
 //   warps 4-11: epilogue, two per lane quarter, each with half of the columns
-// All waits are bounded (ptx.cuh).
+// One warp an operand: a single producer's instructions for both stood between a
+// freed slot and its refill (8192 tokens of 7168 x 2048: 521 us against 463).
+// All waits are bounded (ptx.cuh); they sleep, as polling ones cost the issuer
+// slots (489 against 481).
+//
+// Large products are bound by the tensor pipe and, for more than a few hundred
+// us, the power cap: 8192 x 4096 x 7168 runs with the pipe 0.88 busy (250 us, 122
+// registers a thread), 8192 x 7168 x 2048 0.75 (144 us); both in turn at
+// 1.57-1.60 PFLOP/s, 0.92-0.94 of the library's sustained 1.71.  Small ones by the
+// kernel's fixed time: some 7 us of launch, first loads, one tile's epilogue.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -34,13 +41,12 @@ namespace dense {
 constexpr int kTile = 256;     // rows of a tile (128 per CTA)
 constexpr int kBK = 64;        // K elements of a stage: one 128-byte swizzle row
 constexpr int kMaxStages = 9;
-constexpr int kMaxMaps = 12;
-constexpr int kMaxProblems = 4;
+constexpr int kMaxMaps = 9;
+constexpr int kMaxProblems = 3;
 template <int N>
 struct MapList {
   CUtensorMap m[N];
 };
-constexpr int kMaxSegments = 3;
 constexpr int kThreads = 384;
 constexpr int kEpiWarp0 = 4, kNumEpiWarps = 8;
 constexpr int kABytes = 128 * 128, kBBytes = 128 * 128;   // of a stage, B's at most
@@ -55,21 +61,18 @@ static_assert(kSmemBytes <= 232448, "shared memory budget exceeded");
 
 using Maps = MapList<kMaxMaps>;
 
-// Tile t of a problem -> (batch z, split s, tile row i, tile column j).
+// Tile t of a problem -> (matrix z, split s, tile row i, tile column j).
 struct Problem {
-  int32_t segs;
-  int32_t a_map[kMaxSegments], b_map[kMaxSegments];   // index into Maps
-  int32_t a_off[kMaxSegments], b_off[kMaxSegments];   // added to the operand's row coordinate
+  static constexpr int32_t batch = 1, upper = 0;   // (terms.cuh's have several, and symmetric ones)
+  int32_t a_map, b_map;        // index into Maps
   int32_t a_mn, b_mn;          // 1: the operand is MN-major
-  int32_t a_batch, b_batch;    // row coordinates between matrices of the batch
   int32_t bn;                  // 64, 128, 192 or 256
   int32_t b_step;              // columns of D between tiles (bn, or bn / 2 for two halves)
   int32_t b_rank;              // where rank 1's half of B begins, from rank 0's
   int32_t tiles_m, tiles_n;
-  int32_t upper;               // symmetric D: only tiles on and above the diagonal
-  int32_t per_matrix;          // tiles of one matrix
-  int32_t batch, splits;
-  int32_t kb, kb_split;        // K blocks of a segment, of a split's share
+  int32_t per_matrix;          // tiles of a split
+  int32_t splits;
+  int32_t kb, kb_split;        // K blocks, of a split's share
   int32_t idesc;
   int32_t first_tile;          // of the launch's list
 };
@@ -265,26 +268,23 @@ __device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* s
     const int dx = mn ? 0 : kBK, dy = mn ? kBK : 0;
     const bool two = mn && (IS_A || p.bn == 256);   // boxes of 64 columns
     const uint32_t bytes = IS_A ? 2u * kABytes : 128u * static_cast<uint32_t>(p.bn);   // both CTAs'
-    for (int s = 0; ok && s < p.segs; ++s) {
-      const CUtensorMap* m = &maps.m[IS_A ? p.a_map[s] : p.b_map[s]];
-      const int row = IS_A ? p.a_off[s] + o.z * p.a_batch : p.b_off[s] + o.z * p.b_batch;
-      int x = mn ? at : k0 * kBK, y = (mn ? k0 * kBK : at) + row;
-      for (int k = 0; k < n; ++k, x += dx, y += dy) {
-        if (!mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) {
-          uint8_t* dst = slots + stage * static_cast<uint32_t>(l.slot);
-          if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
-          tma_load_2d_pair(dst, m, x, y, full0 + 8 * stage);
-          if (two) tma_load_2d_pair(dst + 8192, m, x + 64, y, full0 + 8 * stage);
-        }
-        issued = true;
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+    const CUtensorMap* m = &maps.m[IS_A ? p.a_map : p.b_map];
+    int x = mn ? at : k0 * kBK, y = mn ? k0 * kBK : at;
+    for (int k = 0; k < n; ++k, x += dx, y += dy) {
+      if (!mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+        ok = false;
+        break;
+      }
+      if (lane == 0) {
+        uint8_t* dst = slots + stage * static_cast<uint32_t>(l.slot);
+        if (rank == 0) mbar_arrive_expect_tx(full + stage, bytes);
+        tma_load_2d_pair(dst, m, x, y, full0 + 8 * stage);
+        if (two) tma_load_2d_pair(dst + 8192, m, x + 64, y, full0 + 8 * stage);
+      }
+      issued = true;
+      if (++stage == stages) {
+        stage = 0;
+        phase ^= 1u;
       }
     }
   }
@@ -362,8 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = pair; ok && t < l.tiles; t += pairs, ++it) {
         const Tile o = find_tile(l, t);
         const Problem& p = l.p[o.p];
-        const int k0 = o.s * p.kb_split, k1 = min(p.kb, k0 + p.kb_split);
-        const int steps = (k1 - k0) * p.segs;
+        const int k0 = o.s * p.kb_split, steps = min(p.kb, k0 + p.kb_split) - k0;
         // MN-major: 64 x 64 boxes of 8 KB side by side, 8 K rows 1024 bytes
         // apart; K-major: rows of 128 bytes, 8 rows 1024 bytes apart.
         const uint64_t ad0 = smem_desc(a0, p.a_mn ? 8192 : 0, 1024, 2);
@@ -463,11 +462,10 @@ inline Plan make_plan(int64_t tiles_m, int64_t cols, int64_t kb) {
 // One operand pair, tiles over rows x cols (cols counts D's columns, or the
 // columns of each half).
 inline Problem make_problem(const Plan& plan, int64_t rows, int64_t cols, int64_t kb, int a_map,
-                            bool a_mn, int b_map, bool b_mn, bool bf16) {
+                            bool a_mn, int b_map, bool b_mn) {
   Problem p = {};
-  p.segs = 1;
-  p.a_map[0] = a_map;
-  p.b_map[0] = b_map;
+  p.a_map = a_map;
+  p.b_map = b_map;
   p.a_mn = a_mn;
   p.b_mn = b_mn;
   p.bn = p.b_step = plan.bn;
@@ -475,11 +473,10 @@ inline Problem make_problem(const Plan& plan, int64_t rows, int64_t cols, int64_
   p.tiles_m = static_cast<int32_t>(cdiv(rows, kTile));
   p.tiles_n = static_cast<int32_t>(cdiv(cols, plan.bn));
   p.per_matrix = p.tiles_m * p.tiles_n;
-  p.batch = 1;
   p.splits = plan.splits;
   p.kb = static_cast<int32_t>(kb);
   p.kb_split = plan.kb_split;
-  p.idesc = static_cast<int32_t>(idesc_f16(bf16, a_mn, b_mn, plan.bn));
+  p.idesc = static_cast<int32_t>(idesc_f16(true, a_mn, b_mn, plan.bn));
   return p;
 }
 

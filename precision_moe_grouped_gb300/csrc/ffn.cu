@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kJoinThreads)
 // one's weights when their own are loaded, so that HBM works through the change
 // of kernels.
 constexpr int kDecodeThreads = 256, kDecodeWarps = 8;
+constexpr int64_t kAheadBytes = 32 << 20;   // of the next weights that L2 is asked for
 
 __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -397,8 +398,9 @@ struct DecodeArgs {
   __nv_bfloat16* out;
   int64_t ld_in, ld_base, ld_out;
   int32_t tokens, units, k;    // units: features (two weight rows each), or rows
-  const uint8_t* next;         // the next product's weights
-  int64_t next_bytes;          // a multiple of 16
+  const uint8_t* next;         // the next product's weights, [next_rows] of next_row bytes
+  int32_t next_rows, next_row;
+  int64_t next_most;           // of them, bytes a CTA asks for at most
 };
 
 // MT: tiles of 16 weight rows at once; NT: of eight tokens; U: K steps of 32
@@ -454,7 +456,8 @@ struct DecodeStep {
 template <bool DOWN, int MT, int NT, int U>
 __global__ void __launch_bounds__(kDecodeThreads)
     decode_kernel(const DecodeArgs a) {
-  __shared__ float sums[kDecodeWarps][MT * NT * 4][32];
+  constexpr int MS = MT * NT > 12 ? MT / 2 : MT;   // tiles whose sums are joined together
+  __shared__ float sums[kDecodeWarps][MS * NT * 4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
   const int K = a.k, steps = (K + 31) >> 5;
@@ -502,51 +505,73 @@ __global__ void __launch_bounds__(kDecodeThreads)
       if (s + U < s1) odd.multiply(acc, s + U, s1, t, K);
     }
     if (!DOWN && u + MT * kPer >= u1) {
-      // this CTA's share of the next weights, 4 KB a request
-      const int64_t n0 = a.next_bytes / 16 * blockIdx.x / gridDim.x * 16;
-      const int64_t n1 = a.next_bytes / 16 * (blockIdx.x + 1) / gridDim.x * 16;
+      // this CTA's rows of the next weights, 4 KB a request
+      const int64_t n0 = static_cast<int64_t>(a.next_rows) * blockIdx.x / gridDim.x * a.next_row;
+      const int64_t n1 = min(static_cast<int64_t>(a.next_rows) * (blockIdx.x + 1) / gridDim.x * a.next_row,
+                             n0 + a.next_most);
       for (int64_t at = n0 + 4096 * threadIdx.x; at < n1; at += 4096 * kDecodeThreads)
         bulk_prefetch_l2(a.next + at, static_cast<uint32_t>(n1 - at < 4096 ? n1 - at : 4096));
     }
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+    for (int m0 = 0; m0 < MT; m0 += MS) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int m = 0; m < MS; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) sums[warp][(m * NT + n) * 4 + i][lane] = acc[m][n][i];
-    __syncthreads();
-    // value i of (tile m, token tile n): row g + 8 (i >> 1), token 2 t + (i & 1)
-    for (int at = threadIdx.x; at < MT * NT * (DOWN ? 4 : 2) * 32; at += kDecodeThreads) {
-      const int l = at & 31, v = at >> 5;
-      const int i = DOWN ? v & 3 : v & 1, mn = DOWN ? v >> 2 : v >> 1;
-      const int n = mn % NT, m = mn / NT;
-      const int token = 8 * n + 2 * (l & 3) + (i & 1);
-      const int unit = u + m * kPer + (l >> 2) + (DOWN ? 8 * (i >> 1) : 0);
-      if (token >= a.tokens || unit >= u1) continue;
-      float x = 0.f, y = 0.f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int j = 0; j < kDecodeWarps; ++j) {
-        x += sums[j][mn * 4 + i][l];
-        if constexpr (!DOWN) y += sums[j][mn * 4 + i + 2][l];
+          for (int i = 0; i < 4; ++i) sums[warp][(m * NT + n) * 4 + i][lane] = acc[m0 + m][n][i];
+      __syncthreads();
+      // value i of (tile m, token tile n): row g + 8 (i >> 1), token 2 t + (i & 1)
+      for (int at = threadIdx.x; at < MS * NT * (DOWN ? 4 : 2) * 32; at += kDecodeThreads) {
+        const int l = at & 31, v = at >> 5;
+        const int i = DOWN ? v & 3 : v & 1, mn = DOWN ? v >> 2 : v >> 1;
+        const int n = mn % NT, m = m0 + mn / NT;
+        const int token = 8 * n + 2 * (l & 3) + (i & 1);
+        const int unit = u + m * kPer + (l >> 2) + (DOWN ? 8 * (i >> 1) : 0);
+        if (token >= a.tokens || unit >= u1) continue;
+        float x = 0.f, y = 0.f;
+#pragma unroll
+        for (int j = 0; j < kDecodeWarps; ++j) {
+          x += sums[j][mn * 4 + i][l];
+          if constexpr (!DOWN) y += sums[j][mn * 4 + i + 2][l];
+        }
+        if constexpr (DOWN) {
+          if (a.base) x += __bfloat162float(a.base[token * a.ld_base + unit]);
+          a.out[token * a.ld_out + unit] = __float2bfloat16_rn(x);
+        } else {
+          a.out[token * a.ld_out + unit] = __float2bfloat16_rn(swiglu(x, y));
+        }
       }
-      if constexpr (DOWN) {
-        if (a.base) x += __bfloat162float(a.base[token * a.ld_base + unit]);
-        a.out[token * a.ld_out + unit] = __float2bfloat16_rn(x);
-      } else {
-        a.out[token * a.ld_out + unit] = __float2bfloat16_rn(swiglu(x, y));
-      }
+      __syncthreads();
     }
-    __syncthreads();
   }
   if (DOWN && !waited) griddep_wait();
 }
 
+template <bool DOWN, int MT, int NT>
+cudaError_t launch_decode(const DecodeArgs& a, int grid, cudaStream_t s) {
+  // about as many bytes in flight whatever the rows, as far as the registers go
+  constexpr int U = (NT == 1 ? 2 : 1) * (MT == 1 ? 4 : MT == 4 ? 1 : 2);
+  return launch_pdl(decode_kernel<DOWN, MT, NT, U>, dim3(static_cast<unsigned>(grid)), dim3(kDecodeThreads), 0, s, a);
+}
+// The tiles of weight rows at once with which a CTA loads the least: each pass
+// over its rows reads MT KB of them and NT / 2 KB of x a step of K, rows beyond
+// its own included.
 template <bool DOWN, int NT>
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
-  constexpr int MT = DOWN ? 3 : 2, U = NT == 1 ? 4 : 2;
   const int grid = static_cast<int>(std::min<int64_t>(sms, (a.units + 7) / 8));
-  return launch_pdl(decode_kernel<DOWN, MT, NT, U>, dim3(static_cast<unsigned>(grid)),
-                    dim3(kDecodeThreads), 0, s, a);
+  const int tiles = static_cast<int>(dense::cdiv(dense::cdiv(a.units, grid), DOWN ? 16 : 8));
+  int best = 0, least = 0;
+  for (int mt = 1; mt <= 4; ++mt) {
+    const int loads = static_cast<int>(dense::cdiv(tiles, mt)) * (2 * mt + NT);
+    if (best && loads >= least) continue;
+    best = mt;
+    least = loads;
+  }
+  return best == 1   ? launch_decode<DOWN, 1, NT>(a, grid, s)
+         : best == 2 ? launch_decode<DOWN, 2, NT>(a, grid, s)
+         : best == 3 ? launch_decode<DOWN, 3, NT>(a, grid, s)
+                     : launch_decode<DOWN, 4, NT>(a, grid, s);
 }
 template <bool DOWN>
 cudaError_t launch_decode(const DecodeArgs& a, int sms, cudaStream_t s) {
@@ -709,7 +734,7 @@ int32_t add_turned(Maps* m, dense::Launch<EpiSum::Args>* l, const TurnPlan& plan
   else MOE_TRY(dense::make_map(&m->m[at], w, Elem::kBf16, rows, k, k, dense::kBK, 128));
   MOE_TRY(dense::make_map(&m->m[at + 1], x, Elem::kBf16, tokens, k, ld_x, dense::kBK, plan.bn / 2));
   MOE_TRY(dense::make_map(&m->m[at + 2], sums, Elem::kF32, plan.splits * up32(rows), plan.tp, plan.tp, 32, 32));
-  l->p[i] = dense::make_problem(plan, rows, plan.tp, dense::cdiv(k, dense::kBK), at, mn, at + 1, false, true);
+  l->p[i] = dense::make_problem(plan, rows, plan.tp, dense::cdiv(k, dense::kBK), at, mn, at + 1, false);
   l->e[i] = {at + 2, static_cast<int32_t>(up32(rows)), plan.tp};
   *out = {sums, plan.splits, static_cast<int32_t>(up32(rows)), plan.tp};
   return MOE_OK;
@@ -718,7 +743,7 @@ int32_t add_turned(Maps* m, dense::Launch<EpiSum::Args>* l, const TurnPlan& plan
 // The launch of D = x [Wg; Wu]^T whose tiles hold both projections of a feature:
 // gate rows in rank 0's half of B, up rows in rank 1's.
 Problem gate_problem(const dense::Plan& plan, int64_t tokens, int64_t inter, int64_t kb) {
-  Problem p = dense::make_problem(plan, tokens, 2 * inter, kb, 0, false, 1, false, true);
+  Problem p = dense::make_problem(plan, tokens, 2 * inter, kb, 0, false, 1, false);
   p.b_step = plan.bn / 2;
   p.b_rank = static_cast<int32_t>(inter);
   p.tiles_n = static_cast<int32_t>(dense::cdiv(inter, plan.bn / 2));
@@ -736,10 +761,11 @@ int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const v
   __nv_bfloat16* to = static_cast<__nv_bfloat16*>(out);
   if (T <= kDecodeTokens) {
     DecodeArgs a = {static_cast<const __nv_bfloat16*>(wgu), static_cast<const __nv_bfloat16*>(x), nullptr, h,
-                    ld_x, 0, I, s->num_tokens, s->inter, s->hidden, static_cast<const uint8_t*>(wd), 2 * H * I};
+                    ld_x, 0, I, s->num_tokens, s->inter, s->hidden, static_cast<const uint8_t*>(wd), s->hidden,
+                    2 * s->inter, kAheadBytes / sms / 16 * 16};
     MOE_CUDA(launch_decode<false>(a, sms, st));
     DecodeArgs b = {static_cast<const __nv_bfloat16*>(wd), h, add, to, I, ld_base, ld_out, s->num_tokens, s->hidden,
-                    s->inter, nullptr, 0};
+                    s->inter, nullptr, 0, 0, 0};
     MOE_CUDA(launch_decode<true>(b, sms, st));
     return MOE_OK;
   }
@@ -780,7 +806,7 @@ int32_t ffn_forward(const moe_ffn_shape* s, const void* x, int64_t ld_x, const v
   l.problems = 1;
   l.maps = 3;
   l.early = dense::kEarlyB;
-  l.p[0] = dense::make_problem(w.down, T, H, dense::cdiv(I, dense::kBK), 0, false, 1, false, true);
+  l.p[0] = dense::make_problem(w.down, T, H, dense::cdiv(I, dense::kBK), 0, false, 1, false);
   l.e[0] = {add, ld_base, 2, s->num_tokens, s->hidden};
   MOE_CUDA(dense::resident_pairs<EpiOut>(sms, &pairs));
   MOE_CUDA(dense::launch<EpiOut>(m, l, pairs, st));
@@ -817,7 +843,7 @@ int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, 
       MOE_TRY(dense::make_map(&m.m[1], wd, Elem::kBf16, H, I, I, kSquare, kSquare));
       MOE_TRY(dense::make_map(&m.m[2], dh, Elem::kF32, rp, I, I, 32, 32));
       l.maps = 3;
-      l.p[0] = dense::make_problem(w.dh, T, I, kh, 0, false, 1, true, true);
+      l.p[0] = dense::make_problem(w.dh, T, I, kh, 0, false, 1, true);
       l.e[0] = {2, static_cast<int32_t>(rp), s->inter};
       l.problems = 1;
       MOE_CUDA(dense::launch<EpiSum>(m, l, pairs, st));
@@ -841,7 +867,7 @@ int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, 
     MOE_TRY(dense::make_map(&m.m[k], dgu, Elem::kBf16, T, 2 * I, 2 * I, dense::kBK, 128));
     MOE_TRY(dense::make_map(&m.m[k + 1], wgu, Elem::kBf16, 2 * I, H, H, kSquare, kSquare));
     MOE_TRY(dense::make_map(&m.m[k + 2], dx, Elem::kBf16, T, H, ld_dx, 64, 32));
-    l.p[i] = dense::make_problem(w.dx, T, H, ki2, k, false, k + 1, true, true);
+    l.p[i] = dense::make_problem(w.dx, T, H, ki2, k, false, k + 1, true);
     l.e[i] = {static_cast<const __nv_bfloat16*>(dx_base), ld_base, k + 2, static_cast<int32_t>(T),
               static_cast<int32_t>(H)};
   }
@@ -853,14 +879,14 @@ int32_t ffn_backward(const moe_ffn_shape* s, const void* dout, int64_t ld_dout, 
     MOE_TRY(dense::make_map(&m.m[k], dgu, Elem::kBf16, T, 2 * I, 2 * I, kSquare, kSquare));
     MOE_TRY(dense::make_map(&m.m[k + 1], x, Elem::kBf16, T, H, ld_x, kSquare, kSquare));
     MOE_TRY(dense::make_map(&m.m[k + 2], dw_gate_up, Elem::kBf16, 2 * I, H, H, 64, 32));
-    l.p[i] = dense::make_problem(g, 2 * I, H, kt, k, true, k + 1, true, true);
+    l.p[i] = dense::make_problem(g, 2 * I, H, kt, k, true, k + 1, true);
     l.e[i] = {nullptr, 0, k + 2, static_cast<int32_t>(2 * I), static_cast<int32_t>(H)};
     i = l.problems++, k = l.maps;
     l.maps += 3;
     MOE_TRY(dense::make_map(&m.m[k], dout, Elem::kBf16, T, H, ld_dout, kSquare, kSquare));
     MOE_TRY(dense::make_map(&m.m[k + 1], h, Elem::kBf16, T, I, I, kSquare, kSquare));
     MOE_TRY(dense::make_map(&m.m[k + 2], dw_down, Elem::kBf16, H, I, I, 64, 32));
-    l.p[i] = dense::make_problem(d, H, I, kt, k, true, k + 1, true, true);
+    l.p[i] = dense::make_problem(d, H, I, kt, k, true, k + 1, true);
     l.e[i] = {nullptr, 0, k + 2, static_cast<int32_t>(H), static_cast<int32_t>(I)};
   }
   MOE_CUDA(dense::resident_pairs<EpiOut>(sms, &pairs));

@@ -6,7 +6,7 @@
 //   at BN = 256, three stages) and feeds three products, so that each term
 //   is loaded once.
 // - An MMA aligns its 16 products and the accumulator to the largest of them
-//   and cuts each off at 24 bits: a long sum of squares shrinks by about n 2^-25
+//   and cuts each off at 24 bits: a sum of n terms of one sign shrinks by about n 2^-27
 //   of itself.  So sums run in pieces of two K blocks, which alternate between
 //   the two accumulators; the epilogue warps add the pieces up in registers
 //   (rounded to nearest) while the next one runs.

@@ -79,6 +79,15 @@ def test_forward(cuda_ok, T, H, I):
         assert op.device_status() == 0
 
 
+@pytest.mark.parametrize("T", [1, 9, 20, 32])
+@pytest.mark.parametrize("H,I", [(64, 3000), (64, 4000), (64, 9000), (5000, 40), (8200, 72), (9608, 64), (20008, 64)])
+def test_long_sides_of_small_batches(cuda_ok, T, H, I):
+    """One to many tiles of weight rows a block, whole and in part, in either product."""
+    s = make(T, H, I, seed=T + H + I)
+    out = P.GatedFFN(s["wgu"], s["wd"])(s["x"], base=s["base"])
+    close(out, reference(s)[0], "out")
+
+
 @pytest.mark.parametrize("T,H,I", SIZES)
 def test_backward(cuda_ok, T, H, I):
     for base in (True, False):
