@@ -24,6 +24,8 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
+#include <utility>
 
 #include "dense.cuh"
 #include "entry.h"
@@ -40,6 +42,7 @@ using dense::Tile;
 
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr int kPartSteps = kMuonPartSteps;
+constexpr int kChainSide = 384;   // of the m x m products that one launch carries out
 constexpr int kThreads = 256;
 
 // ------------------------------------------------------------ elementwise
@@ -202,8 +205,9 @@ struct EpiPlanes {
     int32_t m, rows, cols;   // rows of I; stored rows (a multiple of 64) and columns
   };
   static __device__ __forceinline__ void ahead(const Args&, const Tile&, const EpiWarp&, int, int) {}
+  template <class M>
   static __device__ __forceinline__ void run(const Args& a, const Tile& o, const EpiWarp& w, int col0, int n,
-                                             const Maps& maps, float (&d)[128]) {
+                                             const M& maps, float (&d)[128]) {
     if (w.row >= a.rows) return;
     const int row = o.z * a.rows + w.row;
 #pragma unroll
@@ -522,14 +526,16 @@ struct Group {
   __half* planes(size_t off) const { return reinterpret_cast<__half*>(ws + off); }
   Planes square(size_t off, float scale) const { return {planes(off), scale, s.mp, true, nullptr}; }
 };
-constexpr int kMostGroups = 4;   // that share their launches: two products each in terms::Launch
+constexpr int kMostGroups = terms::kChainGroups;   // that share their launches: two products each in terms::Launch
 int64_t rows_of(const Shape& s) { return s.batch * s.mp; }
 
-// A launch in the making.
-template <class Epi>
+// A launch in the making, of one phase or (terms::Chain) of several.
+template <class Epi, class L = terms::Launch<typename Epi::Args>, class M = Maps>
 struct Build {
-  Maps m;
-  terms::Launch<typename Epi::Args> l;
+  static constexpr bool kChain = !std::is_same<M, Maps>::value;
+  M m;
+  L l;
+  std::pair<const __half*, int> made[kChain ? terms::kChainMaps : 1];   // a chain's maps, which its phases share
 
   explicit Build(const Call& c) : l{} {
     l.status = c.status;
@@ -539,6 +545,15 @@ struct Build {
   }
   int32_t map(const Shape& s, const __half* at, int64_t cols, int box_cols, int box_rows, dense::Swizzle sw,
               int32_t* index) {
+    if (kChain) {
+      for (int32_t i = 1; i < l.maps; ++i) {
+        if (made[i] == std::make_pair(at, box_cols)) {
+          *index = i;
+          return MOE_OK;
+        }
+      }
+      made[l.maps] = {at, box_cols};
+    }
     *index = l.maps++;
     return dense::make_map(&m.m[*index], at, Elem::kF16, 2 * rows_of(s), cols, cols, box_cols, box_rows, sw);
   }
@@ -567,10 +582,12 @@ struct Build {
 };
 
 using BuildPlanes = Build<EpiPlanes>;
+using BuildChain = Build<EpiPlanes, terms::Chain<EpiPlanes::Args>, terms::ChainMaps>;
 
 // out = c A B^T + a I, symmetric [mp, mp]; A and B [mp, k], B's second copy of the
 // diagonal blocks used when use_diag.
-int32_t add_symmetric(BuildPlanes& b, const Shape& s, const Planes& x, Planes y, bool use_diag, const Planes& out, float c,
+template <class B>
+int32_t add_symmetric(B& b, const Shape& s, const Planes& x, Planes y, bool use_diag, const Planes& out, float c,
                       float a, float ratio) {
   if (!use_diag) y.diag = nullptr;
   Planes left = x;
@@ -732,11 +749,74 @@ int32_t first_planes(const Call& c, const Group& g) {
   return MOE_OK;
 }
 
+// CTAs of a cluster that carries out the steps' m x m products in one launch, or 0:
+// each in a launch of its own.  One launch is faster while a phase has a unit of 64
+// columns or two a pair and all matrices are resident (256 x 7168: 140 against 167 us,
+// 384 x 4096 163 / 190, 3 of 333 x 1001 and 2 of 777 x 129 179 / 213, 12 of 200 x 1000
+// 169 / 204); beyond, the whole GPU is (448 x 1000: 223 / 186, 512 x 512 233 / 189).  A
+// cluster of 16 takes 2 us off for short sides of up to 256, too, but holds half as many.
+int chain_size(const Group* gs, int n, int* error) {
+  *error = MOE_OK;
+  int mp = 0;
+  int64_t matrices = 0;
+  for (const Group* g = gs; g < gs + n; ++g) {
+    mp = std::max(mp, g->s.mp);
+    matrices += g->s.batch;
+  }
+  if (mp > kChainSide) return 0;
+  const int size = mp <= dense::kTile ? 8 : 16;
+  int clusters;
+  const cudaError_t e = terms::resident_chains<EpiPlanes>(size, &clusters);
+  if (e != cudaSuccess) *error = entry_launched(e);
+  return e == cudaSuccess && matrices <= clusters ? size : 0;
+}
+
+// `steps` steps on G: Q from G, the products of a phase added to b and ended by
+// flush().
+template <class B, class F>
+int32_t add_steps(const Call& c, Group* gs, int n, const StepScales* sc, int steps, B& b, F flush) {
+  const float fa = static_cast<float>(c.o->coefficients[0]), fc = static_cast<float>(c.o->coefficients[2]);
+  const float ratio = static_cast<float>(c.o->coefficients[1] / c.o->coefficients[2]);
+  Group* const end = gs + n;
+  for (int k = 0; k < steps; ++k) {
+    const bool last = k == steps - 1;
+    for (Group* g = gs; g < end; ++g) {   // P = c G (G + (b / c) I) + a I
+      g->p = g->square(k == 0 ? g->w.qa : g->w.p, sc[k].p);
+      MOE_TRY(add_symmetric(b, g->s, g->g, g->g, true, g->p, fc, fa, 0.f));
+    }
+    MOE_TRY(flush());
+    for (Group* g = gs; g < end; ++g) {   // S = P G, Q <- P Q
+      if (!last)
+        MOE_TRY(add_symmetric(b, g->s, g->p, g->g, false, g->square(g->w.s, sc[k].s), 1.0f, 0.f, 0.f));
+      if (k == 0) {
+        g->q = g->p;
+      } else {
+        const Planes next = g->square(k & 1 ? g->w.qb : g->w.qa, sc[k].q);
+        MOE_TRY(add_symmetric(b, g->s, g->p, g->q, false, next, 1.0f, 0.f, 0.f));
+        // P Q and not P Q^T: what is left of Q's asymmetry belongs to the X that the
+        // next Gram matrix is taken of
+        b.l.p[b.l.problems - 1].b.turned = 1;
+        g->q = next;
+      }
+    }
+    MOE_TRY(flush());
+    if (last) return MOE_OK;
+    for (Group* g = gs; g < end; ++g) {   // G <- S P
+      g->g.scale = sc[k + 1].g;
+      MOE_TRY(add_symmetric(b, g->s, g->square(g->w.s, sc[k].s), g->p, false, g->g, 1.0f, 0.f, ratio));
+    }
+    MOE_TRY(flush());
+  }
+  return MOE_OK;
+}
+
 // All steps of up to kMostGroups groups, whose products share their launches.
 int32_t run_groups(const Call& c, Group* gs, int n) {
-  const double ca = c.o->coefficients[0], cb = c.o->coefficients[1], cc = c.o->coefficients[2];
-  const float fa = static_cast<float>(ca), fc = static_cast<float>(cc), ratio = static_cast<float>(cb / cc);
+  const float ratio = static_cast<float>(c.o->coefficients[1] / c.o->coefficients[2]);
   Group* const end = gs + n;
+  int error;
+  const int chain = chain_size(gs, n, &error);
+  if (error != MOE_OK) return error;
   for (Group* g = gs; g < end; ++g) {
     MOE_TRY(first_planes(c, *g));
     g->x = {g->planes(g->w.x), c.sc.x[0], g->s.np, false, nullptr};
@@ -750,37 +830,26 @@ int32_t run_groups(const Call& c, Group* gs, int n) {
       g->g.diag = g->planes(g->w.h);
     }
     MOE_TRY(gram(c, gs, n, ratio));
-    for (int k = 0; k < steps; ++k) {
-      const bool last = k == steps - 1;
-      BuildPlanes poly(c);   // P = c G (G + (b / c) I) + a I
+    if (chain) {
+      BuildChain b(c);
+      MOE_TRY(add_steps(c, gs, n, sc, steps, b, [&]() -> int32_t {
+        if (b.l.problems > (b.l.phases ? b.l.end[b.l.phases - 1] : 0)) b.l.end[b.l.phases++] = b.l.problems;
+        return MOE_OK;
+      }));
+      int matrices = 0;
       for (Group* g = gs; g < end; ++g) {
-        g->p = g->square(k == 0 ? g->w.qa : g->w.p, sc[k].p);
-        MOE_TRY(add_symmetric(poly, g->s, g->g, g->g, true, g->p, fc, fa, 0.f));
+        b.l.mp[b.l.groups] = g->s.mp;
+        b.l.first[b.l.groups++] = matrices;
+        matrices += static_cast<int>(g->s.batch);
       }
-      MOE_TRY(run(c, poly));
-      BuildPlanes both(c);   // S = P G, Q <- P Q
-      for (Group* g = gs; g < end; ++g) {
-        if (!last)
-          MOE_TRY(add_symmetric(both, g->s, g->p, g->g, false, g->square(g->w.s, sc[k].s), 1.0f, 0.f, 0.f));
-        if (k == 0) {
-          g->q = g->p;
-        } else {
-          const Planes next = g->square(k & 1 ? g->w.qb : g->w.qa, sc[k].q);
-          MOE_TRY(add_symmetric(both, g->s, g->p, g->q, false, next, 1.0f, 0.f, 0.f));
-          // P Q and not P Q^T: what is left of Q's asymmetry belongs to the X that the
-          // next Gram matrix is taken of
-          both.l.p[both.l.problems - 1].b.turned = 1;
-          g->q = next;
-        }
-      }
-      MOE_TRY(run(c, both));
-      if (last) break;
-      BuildPlanes next(c);   // G <- S P
-      for (Group* g = gs; g < end; ++g) {
-        g->g.scale = sc[k + 1].g;
-        MOE_TRY(add_symmetric(next, g->s, g->square(g->w.s, sc[k].s), g->p, false, g->g, 1.0f, 0.f, ratio));
-      }
-      MOE_TRY(run(c, next));
+      MOE_CUDA(terms::launch_chain<EpiPlanes>(b.m, b.l, chain, matrices, c.st));
+    } else {
+      BuildPlanes b(c);
+      MOE_TRY(add_steps(c, gs, n, sc, steps, b, [&]() -> int32_t {
+        MOE_TRY(run(c, b));
+        b = BuildPlanes(c);
+        return MOE_OK;
+      }));
     }
     if (done + steps < c.o->ns_steps) MOE_TRY(apply(c, gs, n, c.sc.x[part + 1]));
   }

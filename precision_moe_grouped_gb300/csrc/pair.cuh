@@ -37,15 +37,15 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
                : "memory");
 }
 
-// Arrive once on the barrier at `bar`'s offset in both CTAs of the pair when
-// the issuing thread's earlier tcgen05 operations have completed.
-__device__ __forceinline__ void tc2_commit_both_warp(uint64_t* bar) {
+// Arrive once on the barrier at `bar`'s offset in both CTAs of the pair (their
+// ranks' bits) when the issuing thread's earlier tcgen05 operations have completed.
+__device__ __forceinline__ void tc2_commit_both_warp(uint64_t* bar, uint16_t both = 3) {
   asm volatile(
       "{\n\t.reg .pred e;\n\t"
       "elect.sync _|e, 0xffffffff;\n\t"
       "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
       " [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(both)
       : "memory");
 }
 
