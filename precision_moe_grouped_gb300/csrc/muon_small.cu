@@ -116,66 +116,123 @@ __device__ __forceinline__ Work find_block(const Table& t, int b) {
   return w;
 }
 
-// This thread's 16 elements of the tile at column n0: element k at row i + k di
-// and column j + k dj of X, `at + k step` in the matrix.  Elements outside of the
-// matrix read its first one: loads without branches stay in flight together.
-template <int MP>
+// V neighbours in memory, met in one access.
+template <class T, int V>
+struct alignas(V * sizeof(T)) Pack {
+  T v[V];
+};
+
+// This thread's 16 elements of the tile at column n0, in packs of V along the
+// memory's rows: pack k at row i + k di and column j + k dj of X, `at + k step` in
+// the matrix.  Packs outside of the matrix read its first one: loads without
+// branches stay in flight together.  (V = 4: the rows in memory are multiples of
+// 4, so that a pack is inside or outside as a whole.)
+template <int MP, int V>
 struct Elements {
+  static constexpr int kPacks = Cfg<MP>::PER / V;
   int i, j, di, dj, m, cols;
   int at, step;   // below 2^26: m <= 64, n <= 2^20
+  bool tall;
 
-  __device__ __forceinline__ Elements(const Entry& e, int n0, int n1) : m(e.m), cols(n1 - n0) {
+  __device__ __forceinline__ Elements(const Entry& e, int n0, int n1) : m(e.m), cols(n1 - n0), tall(e.tall) {
     constexpr int NC = Cfg<MP>::NC;
     const int t = threadIdx.x;
-    if (e.tall) {
-      i = t % MP, j = t / MP, di = 0, dj = kThreads / MP;
+    if (tall) {
+      i = t % (MP / V) * V, j = t / (MP / V), di = 0, dj = kThreads / (MP / V);
       at = (n0 + j) * e.m + i;
       step = dj * e.m;
     } else {
-      i = t / NC, j = t % NC, di = kThreads / NC, dj = 0;
+      i = t / (NC / V), j = t % (NC / V) * V, di = kThreads / (NC / V), dj = 0;
       at = i * e.n + n0 + j;
       step = di * e.n;
     }
   }
   __device__ __forceinline__ bool in(int k) const { return i + k * di < m && j + k * dj < cols; }
   __device__ __forceinline__ int where(int k) const { return in(k) ? at + k * step : 0; }
-  __device__ __forceinline__ int in_tile(int k, int ld = Cfg<MP>::LD) const { return (i + k * di) * ld + j + k * dj; }
+  template <class T>
+  __device__ __forceinline__ Pack<T, V> load(const T* p, int k) const {
+    return *reinterpret_cast<const Pack<T, V>*>(p + where(k));
+  }
+  template <class T>
+  __device__ __forceinline__ void store(T* p, int k, const Pack<T, V>& v) const {
+    if (in(k)) *reinterpret_cast<Pack<T, V>*>(p + where(k)) = v;
+  }
+  // the pack's place in the tile: a run of a row, or of a column of a tall matrix
+  __device__ __forceinline__ void to_tile(float* u, int k, const Pack<float, V>& v, int ld) const {
+    float* to = u + (i + k * di) * ld + j + k * dj;
+    if (V == 1 || !tall) {
+      *reinterpret_cast<Pack<float, V>*>(to) = v;
+    } else {
+#pragma unroll
+      for (int c = 0; c < V; ++c) to[c * ld] = v.v[c];
+    }
+  }
+  __device__ __forceinline__ Pack<float, V> from_tile(const float* u, int k, int ld) const {
+    const float* from = u + (i + k * di) * ld + j + k * dj;
+    if (V == 1 || !tall) return *reinterpret_cast<const Pack<float, V>*>(from);
+    Pack<float, V> v;
+#pragma unroll
+    for (int c = 0; c < V; ++c) v.v[c] = from[c * ld];
+    return v;
+  }
 };
 
 template <bool BF16>
 using Grad = typename std::conditional<BF16, __nv_bfloat16, float>::type;
 
 // A tile's momentum and gradient, from memory to registers ...
-template <int MP, bool BF16>
+template <int MP, bool BF16, int V>
 struct Fetched {
-  float m[Cfg<MP>::PER];
-  Grad<BF16> g[Cfg<MP>::PER];
+  using X = Elements<MP, V>;
+  Pack<float, V> m[X::kPacks];
+  Pack<Grad<BF16>, V> g[X::kPacks];
 
-  __device__ __forceinline__ void fetch(const Elements<MP>& x, const float* mp, const Grad<BF16>* gp, bool need_g) {
+  __device__ __forceinline__ void fetch(const X& x, const float* mp, const Grad<BF16>* gp, bool need_g) {
 #pragma unroll
-    for (int k = 0; k < Cfg<MP>::PER; ++k) m[k] = mp[x.where(k)];
+    for (int k = 0; k < X::kPacks; ++k) m[k] = x.load(mp, k);
     if (need_g) {
 #pragma unroll
-      for (int k = 0; k < Cfg<MP>::PER; ++k) g[k] = gp[x.where(k)];
+      for (int k = 0; k < X::kPacks; ++k) g[k] = x.load(gp, k);
     }
   }
   // ... and u from there to shared memory, zero outside of the matrix; FIRST:
   // with the momentum's update.
   template <bool FIRST>
-  __device__ __forceinline__ void put(const Elements<MP>& x, const Momentum& mo, float* mp, float gs, float* u,
+  __device__ __forceinline__ void put(const X& x, const Momentum& mo, float* mp, float gs, float* u,
                                       int ld = Cfg<MP>::LD) const {
 #pragma unroll
-    for (int k = 0; k < Cfg<MP>::PER; ++k) {
-      float mv = m[k];
-      const float gv = FIRST || mo.nesterov ? static_cast<float>(g[k]) * gs : 0.f;
-      if (FIRST) {
-        mv = fmaf(mo.mu, mv, mo.rest * gv);
-        if (x.in(k)) mp[x.where(k)] = mv;
+    for (int k = 0; k < X::kPacks; ++k) {
+      Pack<float, V> mv = m[k], uv;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        const float gv = FIRST || mo.nesterov ? static_cast<float>(g[k].v[c]) * gs : 0.f;
+        if (FIRST) mv.v[c] = fmaf(mo.mu, mv.v[c], mo.rest * gv);
+        uv.v[c] = x.in(k) ? update_of(mo, mv.v[c], gv) : 0.f;
       }
-      u[x.in_tile(k, ld)] = x.in(k) ? update_of(mo, mv, gv) : 0.f;
+      if (FIRST) x.store(mp, k, mv);
+      x.to_tile(u, k, uv, ld);
     }
   }
 };
+
+// p <- decay p - step Y and the copy, for the tile's Y = Q u.
+template <int MP, int V>
+__device__ __forceinline__ void put_params(const Elements<MP, V>& x, const Pack<float, V> (&pv)[Elements<MP, V>::kPacks],
+                                           const Entry& e, float decay, const float* y, int ld, float* p,
+                                           __nv_bfloat16* copy) {
+#pragma unroll
+  for (int k = 0; k < Elements<MP, V>::kPacks; ++k) {
+    Pack<float, V> v = x.from_tile(y, k, ld);
+    Pack<__nv_bfloat16, V> c;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      v.v[i] = fmaf(-e.step, v.v[i], decay * pv[k].v[i]);
+      c.v[i] = __float2bfloat16_rn(v.v[i]);
+    }
+    x.store(p, k, v);
+    if (e.copy) x.store(copy, k, c);
+  }
+}
 
 // c[r][s] += sum over this group's columns of u[i][k] u[j][k] for the thread's
 // rows i = ti + MP/4 r and j = tj + MP/4 s.
@@ -246,6 +303,42 @@ __device__ __forceinline__ void mul_tile(const float* q, float* u, int ld) {
   for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(u + (i + r) * ld + j) = y[r];
   __syncthreads();
 }
+// The same for two tiles side by side, or one: eight rows and four columns a
+// thread, half of the threads a tile.  A 16-byte load costs shared memory four
+// cycles whatever its lanes share: three for 32 multiply-adds, above two for 16.
+// Faster for 64 rows (64 of 2000 x 33: 245 against 259 us), where it pays for its registers.
+template <int MP>
+__device__ __forceinline__ void mul_tiles(const float* q, float* u, int ld, bool two) {
+  using C = Cfg<MP>;
+  const int half = threadIdx.x / (kThreads / 2), t = threadIdx.x % (kThreads / 2);
+  const int j = half * C::NC + (t % (C::NC / 4)) * 4, i = (t / (C::NC / 4)) * 8;
+  const bool mine = two || half == 0;
+  float4 y[8];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) y[r] = make_float4(0, 0, 0, 0);
+  if (mine) {
+#pragma unroll 4
+    for (int k = 0; k < MP; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(u + k * ld + j);
+      const float4 a = *reinterpret_cast<const float4*>(q + k * C::LDM + i);
+      const float4 b = *reinterpret_cast<const float4*>(q + k * C::LDM + i + 4);
+      const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        y[r].x = fmaf(w[r], v.x, y[r].x);
+        y[r].y = fmaf(w[r], v.y, y[r].y);
+        y[r].z = fmaf(w[r], v.z, y[r].z);
+        y[r].w = fmaf(w[r], v.w, y[r].w);
+      }
+    }
+  }
+  __syncthreads();
+  if (mine) {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) *reinterpret_cast<float4*>(u + (i + r) * ld + j) = y[r];
+  }
+  __syncthreads();
+}
 template <int MP>
 __device__ __forceinline__ void load_q(const float* from, float* q) {
   for (int k = threadIdx.x; k < MP * MP; k += kThreads) q[(k / MP) * Cfg<MP>::LDM + k % MP] = from[k];
@@ -259,7 +352,7 @@ __device__ __forceinline__ void columns_of(const Entry& e, int part, int* n0, in
 }
 
 // Each block's share of u u^T (FIRST) or of Y Y^T, Y = Q u.
-template <int MP, bool FIRST, bool BF16>
+template <int MP, bool FIRST, bool BF16, int V>
 __global__ void __launch_bounds__(kThreads, 2)
     muon_small_gram_kernel(const __grid_constant__ Table t, const float* qs, float* shares) {
   using C = Cfg<MP>;
@@ -278,12 +371,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   int n0, n1;
   columns_of<MP>(e, w.part, &n0, &n1);
   float c[4][4] = {};
-  Fetched<MP, BF16> f;
-  f.fetch(Elements<MP>(e, n0, n1), mp, gp, need_g);
+  Fetched<MP, BF16, V> f;
+  f.fetch(Elements<MP, V>(e, n0, n1), mp, gp, need_g);
   for (; n0 < n1; n0 += C::NC) {
-    f.template put<FIRST>(Elements<MP>(e, n0, n1), e.mo, mp, gs, u);
+    f.template put<FIRST>(Elements<MP, V>(e, n0, n1), e.mo, mp, gs, u);
     __syncthreads();
-    if (n0 + C::NC < n1) f.fetch(Elements<MP>(e, n0 + C::NC, n1), mp, gp, need_g);   // under the products
+    if (n0 + C::NC < n1) f.fetch(Elements<MP, V>(e, n0 + C::NC, n1), mp, gp, need_g);   // under the products
     if (!FIRST) mul_tile<MP>(q, u, C::LD);
     gram_tile<MP>(u, C::LD, c);
     __syncthreads();
@@ -382,7 +475,7 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // p <- decay p - step Q u, and the copy.
-template <int MP, bool BF16>
+template <int MP, bool BF16, int V>
 __global__ void __launch_bounds__(kThreads, 2)
     muon_small_apply_kernel(const __grid_constant__ Table t, const float* qs) {
   using C = Cfg<MP>;
@@ -400,25 +493,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   __nv_bfloat16* copy = e.copy + base;
   int n0, n1;
   columns_of<MP>(e, w.part, &n0, &n1);
-  Fetched<MP, BF16> f;
-  f.fetch(Elements<MP>(e, n0, n1), mp, gp, e.mo.nesterov);
+  Fetched<MP, BF16, V> f;
+  f.fetch(Elements<MP, V>(e, n0, n1), mp, gp, e.mo.nesterov);
   for (; n0 < n1; n0 += C::NC) {
-    const Elements<MP> x(e, n0, n1);
+    const Elements<MP, V> x(e, n0, n1);
     f.template put<false>(x, e.mo, mp, gs, u);
-    float pv[C::PER];
+    Pack<float, V> pv[x.kPacks];
 #pragma unroll
-    for (int k = 0; k < C::PER; ++k) pv[k] = p[x.where(k)];
+    for (int k = 0; k < x.kPacks; ++k) pv[k] = x.load(p, k);
     __syncthreads();
     mul_tile<MP>(q, u, C::LD);
-    if (n0 + C::NC < n1) f.fetch(Elements<MP>(e, n0 + C::NC, n1), mp, gp, e.mo.nesterov);
-#pragma unroll
-    for (int k = 0; k < C::PER; ++k) {
-      const float v = fmaf(-e.step, u[x.in_tile(k)], t.decay * pv[k]);
-      if (x.in(k)) {
-        p[x.where(k)] = v;
-        if (e.copy) copy[x.where(k)] = __float2bfloat16_rn(v);
-      }
-    }
+    if (n0 + C::NC < n1) f.fetch(Elements<MP, V>(e, n0 + C::NC, n1), mp, gp, e.mo.nesterov);
+    put_params(x, pv, e, t.decay, u, C::LD, p, copy);
     __syncthreads();
   }
 }
@@ -437,7 +523,7 @@ __host__ __device__ constexpr int cluster_scratch() {   // floats beside u: G, P
   return 3 * MP * Cfg<MP>::LDM + MP * MP + (Cfg<MP>::kGroups > 1 ? Cfg<MP>::kGroups * MP * MP : 0);
 }
 
-template <int MP, bool BF16>
+template <int MP, bool BF16, int V>
 __global__ void __launch_bounds__(kThreads, 2)
     muon_cluster_kernel(const __grid_constant__ Table t, const Schedule sc) {
   using C = Cfg<MP>;
@@ -460,11 +546,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   const int tiles = (e.n + C::NC - 1) / C::NC;
   const int first = tiles * rank / ranks * C::NC, last = tiles * (rank + 1) / ranks * C::NC;
   const int end = min(e.n, last), ld = (tiles + ranks - 1) / ranks * C::NC + 4;
-  for (int n0 = first; n0 < last; n0 += C::NC) {
-    Fetched<MP, BF16> f;
-    const Elements<MP> x(e, n0, end);
-    f.fetch(x, mp, gp, true);
-    f.template put<true>(x, e.mo, mp, gs, u + (n0 - first), ld);
+  {
+    Fetched<MP, BF16, V> f, next;
+    f.fetch(Elements<MP, V>(e, first, end), mp, gp, true);
+    for (int n0 = first; n0 < last; n0 += C::NC) {
+      if (n0 + C::NC < last) next.fetch(Elements<MP, V>(e, n0 + C::NC, end), mp, gp, true);
+      f.template put<true>(Elements<MP, V>(e, n0, end), e.mo, mp, gs, u + (n0 - first), ld);
+      f = next;
+    }
   }
   __syncthreads();
   for (int done = 0; done < sc.steps; done += kMuonPartSteps) {
@@ -500,39 +589,32 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n = min(kMuonPartSteps, sc.steps - done);
     newton_schulz<MP>(g, p, q, n, true, inv, e.m, sc.a, sc.b, sc.c);
     if (done + n < sc.steps) {
-      for (int n0 = first; n0 < last; n0 += C::NC) mul_tile<MP>(q, u + (n0 - first), ld);
+      for (int n0 = first; n0 < last; n0 += (MP < 64 ? 1 : 2) * C::NC) {
+        if constexpr (MP < 64) mul_tile<MP>(q, u + (n0 - first), ld);
+        else mul_tiles<MP>(q, u + (n0 - first), ld, n0 + C::NC < last);
+      }
     } else {
-      auto store = [&](const Elements<MP>& x, int n0, const float (&pv)[C::PER]) {
-#pragma unroll
-        for (int k = 0; k < C::PER; ++k) {
-          const float v = fmaf(-e.step, u[x.in_tile(k, ld) + n0 - first], t.decay * pv[k]);
-          if (x.in(k)) {
-            pp[x.where(k)] = v;
-            if (e.copy) copy[x.where(k)] = __float2bfloat16_rn(v);
-          }
-        }
-      };
-      if constexpr (MP < 64) {
+      if constexpr (MP < 64 && V == 4) {
         for (int n0 = first; n0 < last; n0 += C::NC) {
-          const Elements<MP> x(e, n0, end);
-          float pv[C::PER];
+          const Elements<MP, V> x(e, n0, end);
+          Pack<float, V> pv[x.kPacks];
 #pragma unroll
-          for (int k = 0; k < C::PER; ++k) pv[k] = pp[x.where(k)];
+          for (int k = 0; k < x.kPacks; ++k) pv[k] = x.load(pp, k);
           mul_tile<MP>(q, u + (n0 - first), ld);
-          store(x, n0, pv);
+          put_params(x, pv, e, t.decay, u + (n0 - first), ld, pp, copy);
         }
-      } else {   // the products are long enough for the next tile's p to be worth its registers
-        float pv[C::PER], next[C::PER];
+      } else {   // the products, or the single loads, are long enough for the next tile's p to be worth its registers
+        Pack<float, V> pv[Elements<MP, V>::kPacks], next[Elements<MP, V>::kPacks];
         for (int n0 = first - C::NC; n0 < last; n0 += C::NC) {
-          const Elements<MP> x(e, n0, end), y(e, n0 + C::NC, end);
+          const Elements<MP, V> x(e, n0, end), y(e, n0 + C::NC, end);
           if (n0 >= first) mul_tile<MP>(q, u + (n0 - first), ld);
           if (n0 + C::NC < last) {
 #pragma unroll
-            for (int k = 0; k < C::PER; ++k) next[k] = pp[y.where(k)];
+            for (int k = 0; k < x.kPacks; ++k) next[k] = y.load(pp, k);
           }
-          if (n0 >= first) store(x, n0, pv);
+          if (n0 >= first) put_params(x, pv, e, t.decay, u + (n0 - first), ld, pp, copy);
 #pragma unroll
-          for (int k = 0; k < C::PER; ++k) pv[k] = next[k];
+          for (int k = 0; k < x.kPacks; ++k) pv[k] = next[k];
         }
       }
     }
@@ -583,10 +665,21 @@ bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Ba
   return b->count > 0;
 }
 
+// Whether all of a batch's tensors can be met in packs of four.
+bool in_fours(const moe_muon_tensor* t, const Batch& b, bool bf16) {
+  for (int i = 0; i < b.count; ++i) {
+    const moe_muon_tensor& x = t[b.index[i]];
+    if (x.cols % 4 || !ptr_aligned(x.param, 16) || !ptr_aligned(x.momentum, 16) ||
+        !ptr_aligned(x.grad, bf16 ? 8 : 16) || !ptr_aligned(x.param_bf16, 8))
+      return false;
+  }
+  return true;
+}
+
 // How many clusters of 1 .. 8 CTAs are resident at once, with half of an SM's
 // memory a CTA and with all of it; asked once per kernel and device.
 constexpr int kHalfSm = 113 * 1024, kWholeSm = 227 * 1024;
-template <int MP, bool BF16>
+template <int MP, bool BF16, int V>
 cudaError_t resident_clusters(int ranks, bool whole, int* n) {
   static DeviceOnce table[16];
   cudaError_t e;
@@ -594,7 +687,7 @@ cudaError_t resident_clusters(int ranks, bool whole, int* n) {
   if (!at) return e;
   *n = at->load(std::memory_order_acquire);
   if (*n) return cudaSuccess;
-  auto kern = muon_cluster_kernel<MP, BF16>;
+  auto kern = muon_cluster_kernel<MP, BF16, V>;
   static DeviceOnce once;
   if ((e = set_smem_limit_once(kern, kWholeSm, once)) != cudaSuccess) return e;
   cudaLaunchConfig_t q = {};
@@ -620,7 +713,7 @@ cudaError_t resident_clusters(int ranks, bool whole, int* n) {
 struct ClusterPlan {
   int ranks, smem;
 };
-template <int MP, bool BF16>
+template <int MP, bool BF16, int V>
 cudaError_t cluster_plan(const moe_muon_tensor* t, const Batch& b, int64_t most_tiles, ClusterPlan* best) {
   constexpr int64_t kOwn = MP == 16 ? 10 : MP == 32 ? 14 : 40, kTile = MP == 16 ? 5 : MP == 32 ? 7 : 12;
   *best = {0, 0};
@@ -630,7 +723,7 @@ cudaError_t cluster_plan(const moe_muon_tensor* t, const Batch& b, int64_t most_
     const int64_t smem = 4 * (cluster_scratch<MP>() + MP * (tiles(most_tiles) * Cfg<MP>::NC + 4));
     if (smem > kWholeSm || (ranks > 1 && ranks > most_tiles)) continue;
     int n;
-    const cudaError_t e = resident_clusters<MP, BF16>(ranks, smem > kHalfSm, &n);
+    const cudaError_t e = resident_clusters<MP, BF16, V>(ranks, smem > kHalfSm, &n);
     if (e != cudaSuccess) return e;
     int64_t time = 0, left = 0;   // left: places of the round in the making, whose longest is `longest`
     int64_t longest = 0;
@@ -667,7 +760,7 @@ SmallWs small_ws(const Batch& b, int mp) {
   return w;
 }
 
-template <int MP, bool BF16>
+template <int MP, bool BF16, int V>
 int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_options* o, uint8_t* ws,
                   cudaStream_t st) {
   const SmallWs w = small_ws(b, MP);
@@ -698,7 +791,7 @@ int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_optio
   int64_t most_tiles = 1;
   for (int i = 0; i < b.count; ++i) most_tiles = std::max(most_tiles, tiles_of(t[b.index[i]]));
   ClusterPlan plan;
-  MOE_CUDA((cluster_plan<MP, BF16>(t, b, most_tiles, &plan)));
+  MOE_CUDA((cluster_plan<MP, BF16, V>(t, b, most_tiles, &plan)));
   const float a = static_cast<float>(o->coefficients[0]), c1 = static_cast<float>(o->coefficients[1]),
               c2 = static_cast<float>(o->coefficients[2]), eps = static_cast<float>(o->eps);
   if (plan.ranks) {
@@ -716,7 +809,7 @@ int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_optio
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     const Schedule sc = {o->ns_steps, a, c1, c2, eps};
-    MOE_CUDA(cudaLaunchKernelEx(&cfg, muon_cluster_kernel<MP, BF16>, tab, sc));
+    MOE_CUDA(cudaLaunchKernelEx(&cfg, muon_cluster_kernel<MP, BF16, V>, tab, sc));
     return MOE_OK;
   }
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
@@ -728,18 +821,18 @@ int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_optio
     const int n = std::min(kMuonPartSteps, o->ns_steps - done);
     const dim3 each(static_cast<unsigned>(matrices));
     if (done == 0) {
-      MOE_CUDA(launch_pdl(muon_small_gram_kernel<MP, true, BF16>, grid, block, 0, st, tab,
+      MOE_CUDA(launch_pdl(muon_small_gram_kernel<MP, true, BF16, V>, grid, block, 0, st, tab,
                           static_cast<const float*>(qs), shares));
       MOE_CUDA(launch_pdl(muon_small_steps_kernel<MP, true>, each, block, kSteps, st, tab,
                           static_cast<const float*>(shares), qs, n, a, c1, c2, eps));
     } else {
-      MOE_CUDA(launch_pdl(muon_small_gram_kernel<MP, false, BF16>, grid, block, 0, st, tab,
+      MOE_CUDA(launch_pdl(muon_small_gram_kernel<MP, false, BF16, V>, grid, block, 0, st, tab,
                           static_cast<const float*>(qs), shares));
       MOE_CUDA(launch_pdl(muon_small_steps_kernel<MP, false>, each, block, kSteps, st, tab,
                           static_cast<const float*>(shares), qs, n, a, c1, c2, eps));
     }
   }
-  MOE_CUDA(launch_pdl(muon_small_apply_kernel<MP, BF16>, grid, block, 0, st, tab, static_cast<const float*>(qs)));
+  MOE_CUDA(launch_pdl(muon_small_apply_kernel<MP, BF16, V>, grid, block, 0, st, tab, static_cast<const float*>(qs)));
   return MOE_OK;
 }
 
@@ -759,12 +852,17 @@ int32_t muon_small_step(const moe_muon_tensor* t, int32_t count, const moe_muon_
                         cudaStream_t st) {
   Batch b;
   const bool bf16 = o->grad_dtype == MOE_DTYPE_BF16;
-  auto run = [&](auto f, auto g) { return bf16 ? g(t, b, o, ws, st) : f(t, b, o, ws, st); };
+  auto run = [&](auto size) -> int32_t {
+    constexpr int MP = decltype(size)::value;
+    const bool four = in_fours(t, b, bf16);
+    return bf16 ? (four ? run_batch<MP, true, 4>(t, b, o, ws, st) : run_batch<MP, true, 1>(t, b, o, ws, st))
+                : (four ? run_batch<MP, false, 4>(t, b, o, ws, st) : run_batch<MP, false, 1>(t, b, o, ws, st));
+  };
   for (int mp : {16, 32, 64})
     for (int32_t at = 0; next_batch(t, count, mp, &at, &b);)
-      MOE_TRY(mp == 16   ? run(run_batch<16, false>, run_batch<16, true>)
-              : mp == 32 ? run(run_batch<32, false>, run_batch<32, true>)
-                         : run(run_batch<64, false>, run_batch<64, true>));
+      MOE_TRY(mp == 16   ? run(std::integral_constant<int, 16>())
+              : mp == 32 ? run(std::integral_constant<int, 32>())
+                         : run(std::integral_constant<int, 64>()));
   return MOE_OK;
 }
 

@@ -1,0 +1,63 @@
+"""Orthogonalised steps of matrices with a short side of up to 64, in packs of four
+elements where the memory allows it and element by element elsewhere: the same
+arithmetic in the same order, so the same bits."""
+import pytest
+import torch
+
+import precision_moe_grouped_gb300 as P
+import test_gpu_muon as M
+
+pytestmark = pytest.mark.gpu
+
+
+def off_by(t, n):
+    """The same values n elements behind a 256-byte boundary."""
+    room = torch.zeros(t.numel() + n, dtype=t.dtype, device="cuda")
+    room[n:].copy_(t.flatten())
+    return room[n:].view(t.shape)
+
+
+def steps(shape, bf16, nesterov, offset):
+    kind = torch.bfloat16 if bf16 else torch.float32
+    grad = off_by(M.inputs("strong", shape, 3).to(kind), offset)
+    param = off_by(M.inputs("noise", shape, 4), offset)
+    copy = off_by(torch.zeros(shape, device="cuda", dtype=torch.bfloat16), offset)
+    state = off_by(M.inputs("noise", shape, 6) * 1e-2, offset)
+    op = P.Muon([param], [grad], copies=[copy], state=[state], lr=0.02, nesterov=nesterov)
+    for _ in range(2):
+        op.step()
+    assert op.device_status() == 0
+    return param, state, copy
+
+
+# wide and tall, the last pack of a tile's and of the matrix's, one pack in all, rows that fill their class or not;
+# (8, 70000) and (64, 20000) do not fit into a cluster's shared memory
+SHAPES = [(1, 4), (16, 4), (5, 8), (3, 16, 260), (2, 260, 16), (2, 300, 12), (3, 20, 516), (2, 1001, 32), (1001, 28), (40, 132), (4, 64, 200),
+          (3, 333, 64), (257, 60), (8, 70000), (70001, 8), (64, 20000), (9999, 36)]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("nesterov", [False, True])
+def test_packs_and_single_elements(cuda_ok, shape, bf16, nesterov):
+    packs = steps(shape, bf16, nesterov, 0)
+    for offset in (1, 2, 4):   # (two and four elements: aligned for some of the types)
+        for x, y in zip(packs, steps(shape, bf16, nesterov, offset)):
+            assert torch.equal(x, y), offset
+
+
+def test_tensors_of_both_kinds(cuda_ok):
+    """A launch holds several tensors; one that is met element by element takes the others with it."""
+    shapes = [(3, 16, 400), (16, 333), (4, 900, 12), (7, 30)]
+    grads = [M.inputs("strong", s, 5) for s in shapes]
+
+    def run(which):
+        params = [torch.zeros(shapes[i], device="cuda") for i in which]
+        op = P.Muon(params, [grads[i] for i in which], lr=1.0, weight_decay=0.0)
+        op.step()
+        assert op.device_status() == 0
+        return params
+
+    together = run(range(len(shapes)))
+    for i, p in enumerate(together):
+        assert torch.equal(p, run([i])[0]), shapes[i]
