@@ -121,6 +121,10 @@ template <class T, int V>
 struct alignas(V * sizeof(T)) Pack {
   T v[V];
 };
+template <int V, class T>
+__device__ __forceinline__ Pack<T, V> load_pack(const T* p) {
+  return *reinterpret_cast<const Pack<T, V>*>(p);
+}
 
 // This thread's 16 elements of the tile at column n0, in packs of V along the
 // memory's rows: pack k at row i + k di and column j + k dj of X, `at + k step` in
@@ -149,10 +153,6 @@ struct Elements {
   }
   __device__ __forceinline__ bool in(int k) const { return i + k * di < m && j + k * dj < cols; }
   __device__ __forceinline__ int where(int k) const { return in(k) ? at + k * step : 0; }
-  template <class T>
-  __device__ __forceinline__ Pack<T, V> load(const T* p, int k) const {
-    return *reinterpret_cast<const Pack<T, V>*>(p + where(k));
-  }
   template <class T>
   __device__ __forceinline__ void store(T* p, int k, const Pack<T, V>& v) const {
     if (in(k)) *reinterpret_cast<Pack<T, V>*>(p + where(k)) = v;
@@ -189,10 +189,10 @@ struct Fetched {
 
   __device__ __forceinline__ void fetch(const X& x, const float* mp, const Grad<BF16>* gp, bool need_g) {
 #pragma unroll
-    for (int k = 0; k < X::kPacks; ++k) m[k] = x.load(mp, k);
+    for (int k = 0; k < X::kPacks; ++k) m[k] = load_pack<V>(mp + x.where(k));
     if (need_g) {
 #pragma unroll
-      for (int k = 0; k < X::kPacks; ++k) g[k] = x.load(gp, k);
+      for (int k = 0; k < X::kPacks; ++k) g[k] = load_pack<V>(gp + x.where(k));
     }
   }
   // ... and u from there to shared memory, zero outside of the matrix; FIRST:
@@ -500,7 +500,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     f.template put<false>(x, e.mo, mp, gs, u);
     Pack<float, V> pv[x.kPacks];
 #pragma unroll
-    for (int k = 0; k < x.kPacks; ++k) pv[k] = x.load(p, k);
+    for (int k = 0; k < x.kPacks; ++k) pv[k] = load_pack<V>(&p[x.where(k)]);
     __syncthreads();
     mul_tile<MP>(q, u, C::LD);
     if (n0 + C::NC < n1) f.fetch(Elements<MP, V>(e, n0 + C::NC, n1), mp, gp, e.mo.nesterov);
@@ -599,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           const Elements<MP, V> x(e, n0, end);
           Pack<float, V> pv[x.kPacks];
 #pragma unroll
-          for (int k = 0; k < x.kPacks; ++k) pv[k] = x.load(pp, k);
+          for (int k = 0; k < x.kPacks; ++k) pv[k] = load_pack<V>(&pp[x.where(k)]);
           mul_tile<MP>(q, u + (n0 - first), ld);
           put_params(x, pv, e, t.decay, u + (n0 - first), ld, pp, copy);
         }
@@ -610,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (n0 >= first) mul_tile<MP>(q, u + (n0 - first), ld);
           if (n0 + C::NC < last) {
 #pragma unroll
-            for (int k = 0; k < x.kPacks; ++k) next[k] = y.load(pp, k);
+            for (int k = 0; k < x.kPacks; ++k) next[k] = load_pack<V>(&pp[y.where(k)]);
           }
           if (n0 >= first) put_params(x, pv, e, t.decay, u + (n0 - first), ld, pp, copy);
 #pragma unroll
