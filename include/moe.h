@@ -525,8 +525,8 @@ int32_t moe_ffn_forward(const moe_ffn_shape* shape, const void* x, int64_t ld_x,
  *               x or dout
  *   dw_gate_up  bf16 [2 I, H] = [dg^T x; du^T x]
  *   dw_down     bf16 [H, I] = dout^T (silu(g) u)
- * The weights' gradients are written in full (zero without tokens); both or
- * neither may be NULL, and with them num_tokens is at most MOE_FFN_MAX_SUMMED: a
+ * The weights' gradients are written in full (zero without tokens), to memory that
+ * no other tensor of the call has a part of; both or neither may be NULL, and with them num_tokens is at most MOE_FFN_MAX_SUMMED: a
  * tensor core cuts its float sums off instead of rounding them, and a sum of n
  * terms of one sign comes out about n 2^-27.3 of itself short, there 2^-11.
  * Sums are float and rounded once; dg, du and silu(g) u

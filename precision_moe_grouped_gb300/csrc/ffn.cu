@@ -933,6 +933,13 @@ extern "C" int32_t moe_ffn_backward(const moe_ffn_shape* s, const void* dout, in
     return entry_fail(MOE_ERR_UNSUPPORTED, "weights' gradients of at most %d tokens a call", MOE_FFN_MAX_SUMMED);
   if (!ptr_aligned(dw_gate_up, 16) || !ptr_aligned(dw_down, 16))
     return entry_fail(MOE_ERR_MISALIGNED, "dw_gate_up and dw_down must be 16-byte aligned");
+  if (dw_gate_up) {   // tiles of one are stored while others are still to be read
+    for (const void* g : {dw_gate_up, dw_down})
+      if (g == w_gate_up || g == w_down || g == x || g == dout || g == dx)
+        return entry_fail(MOE_ERR_INVALID_ARG, "dw_gate_up and dw_down must be memory of their own");
+    if (dw_gate_up == dw_down)
+      return entry_fail(MOE_ERR_INVALID_ARG, "dw_gate_up and dw_down must be memory of their own");
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (s->num_tokens == 0) {   // sums over no tokens
     if (!dw_gate_up) return MOE_OK;
