@@ -526,11 +526,13 @@ int32_t moe_ffn_forward(const moe_ffn_shape* shape, const void* x, int64_t ld_x,
  *   dw_gate_up  bf16 [2 I, H] = [dg^T x; du^T x]
  *   dw_down     bf16 [H, I] = dout^T (silu(g) u)
  * The weights' gradients are written in full (zero without tokens), to memory that
- * no other tensor of the call has a part of; both or neither may be NULL, and with them num_tokens is at most MOE_FFN_MAX_SUMMED: a
- * tensor core cuts its float sums off instead of rounding them, and a sum of n
- * terms of one sign comes out about n 2^-27.3 of itself short, there 2^-11.
- * Sums are float and rounded once; dg, du and silu(g) u
- * are rounded to bf16 once, ahead of the products that they enter. */
+ * no other tensor of the call has a part of; both or neither may be NULL, and with
+ * them num_tokens is at most MOE_FFN_MAX_SUMMED: a tensor core cuts its float sums
+ * off instead of rounding them, and a sum of n terms of one sign comes out about
+ * n 2^-27.3 of itself short, there 2^-11.  (Sums over features, here and in the
+ * forward, do so too: with 131072 features of one sign 2^-10, dx's over both
+ * projections 2^-9.)  Sums are float and rounded once; dg, du and silu(g) u are
+ * rounded to bf16 once, ahead of the products that they enter. */
 int32_t moe_ffn_backward(const moe_ffn_shape* shape, const void* dout, int64_t ld_dout,
                          const void* x, int64_t ld_x, const void* w_gate_up, const void* w_down,
                          const void* dx_base, int64_t ld_dx_base, void* dx, int64_t ld_dx,

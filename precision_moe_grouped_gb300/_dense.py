@@ -121,8 +121,10 @@ class GatedFFN(_Status):
                  need_dx: bool = True, need_weights: bool = True):
         """(dx, dw_gate_up, dw_down), all bf16, for dout bf16 [T, H]: dx [T, H]
         with dx_base added, the weights' gradients in the weights' shapes (zero
-        without tokens; of at most 65536 tokens a call).  The activations are computed again from x.  What is
-        not needed comes back as None.  `dx` may be `dx_base`, not x or dout."""
+        without tokens; of at most 65536 tokens a call).  The activations are
+        computed again from x.  What is not needed comes back as None.  `dx` may
+        be `dx_base`, not x or dout; dw_gate_up and dw_down are memory of their
+        own."""
         dev, (wgu, wd) = self._start()
         T, H = _rows(x, "x"), self.hidden
         shape, bf16 = (T, H), torch.bfloat16

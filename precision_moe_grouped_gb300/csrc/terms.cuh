@@ -377,9 +377,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 // Phases of symmetric products [mp, mp], mp <= 512, each of which reads what the
 // one before stored: a cluster takes a matrix, its pairs units of 64 columns of
 // the tiles on and above the diagonal, and the cluster's barrier stands between
-// two phases.  A phase of one 256 x 256 product takes some 4 us (first loads, 48
-// MMAs, the stores' completion), 6 to 7 as a launch of its own, whose exit and
-// the next one's grid wait come on top.
+// two phases.  A phase of one 256 x 256 product takes some 6 us (2 until the last of
+// its 128 KB a CTA has come from L2, 1 of MMAs, 2 of epilogue and stores, the
+// barrier), 7.6 as a launch of its own, whose exit and the next one's grid wait
+// come on top.
 constexpr int kMaxPhases = 8, kChainGroups = 4;   // three steps; a group's six matrices, read and stored
 constexpr int kChainMaps = 12 * kChainGroups + 1, kChainProblems = 9 * kChainGroups;
 using ChainMaps = dense::MapList<kChainMaps>;
