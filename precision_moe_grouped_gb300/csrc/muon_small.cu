@@ -1,11 +1,13 @@
 // muon_small.cu -- the orthogonalised step for matrices with a short side m of up
 // to 64 (pools of adapters, small heads): muon.cu's steps on m x m matrices, in
-// float on the CUDA cores.
+// float on the CUDA cores, and the products with the long side on mma.sync.
 //
-// Tensor cores would compute tiles of 128 x 256 for matrices of 16 x 16.  Here a
+// tcgen05 would compute tiles of 128 x 256 for matrices of 16 x 16.  Here a
 // matrix is a stream: a block takes a run of its columns (its long side), tile
-// by tile through shared memory, and m multiply-adds an element (m / 2 for a
-// Gram matrix) keep below the stream's time for m up to about 32.
+// by tile through shared memory, whose loads bound multiply-adds from there
+// (48 of 16 x 7168 and 48 of 4096 x 16: 86 us, 80 on mma.sync; 300 of 16 x 4096 156 / 140;
+// 96 of 32 x 4096 189 / 181; 40 of 64 x 4096, which the m x m steps and the legacy
+// pipe's rate bound, 363 / 369, 64 of 2000 x 33 246 / 231).
 //   gram:  m <- mu m + (1 - mu) g, u; or u again and Y = Q u; each block's
 //          share of u u^T (whose trace is |u|^2) or Y Y^T
 //   steps: one block a matrix joins the shares in order and carries out up to
@@ -62,9 +64,15 @@ struct Cfg {
   static constexpr int LD = NC + 4;    // rows 16 bytes apart modulo the banks
   static constexpr int LDM = MP + 4;
   static constexpr int PER = 16;
-  static constexpr int kGroup = MP * MP / 16;          // threads that hold one MP x MP sum
-  static constexpr int kGroups = kThreads / kGroup;    // each over its own columns
-  static_assert(kGroups * MP * MP <= MP * LD || kGroups == 1, "the groups' sums are joined in the tile's memory");
+  // Warps in products with a tile: one of the MP / 16 strips of 16 rows each, one
+  // of kStrips runs of 32 columns of the tile.  In a Gram matrix a warp sums over
+  // its run, and covers all of a strip, or (64 rows) half of it.
+  static constexpr int kRows = MP / 16, kRuns = 8 / kRows;
+  static constexpr int kSums = MP == 64 ? 1 : kRuns;        // Gram matrices of a tile
+  static constexpr int kGramTiles = MP == 16 ? 2 : 4;       // of 16 x 8, a warp's
+  static constexpr int kGramCols = NC / kSums;              // columns that a warp sums over
+  static_assert(NC == 32 * kRuns, "a run has 32 columns");
+  static_assert(kSums * MP * MP <= MP * LD || kSums == 1, "the sums are joined in the tile's memory");
 };
 
 template <int MP>
@@ -237,109 +245,112 @@ __device__ __forceinline__ void put_params(const Elements<MP, V>& x, const Pack<
   }
 }
 
-// c[r][s] += sum over this group's columns of u[i][k] u[j][k] for the thread's
-// rows i = ti + MP/4 r and j = tj + MP/4 s.
+// Products with a tile run on mma.sync with each number as two tf32 terms of 11
+// bits, hi + lo, and three products, lo hi + hi lo + hi hi: 22 bits, and sums in
+// float.  Multiply-adds from shared memory would be bound by its 16-byte loads, which cost
+// four cycles each whatever their lanes share.
+struct Terms {
+  uint32_t hi, lo;
+  __device__ __forceinline__ Terms() {}
+  __device__ __forceinline__ Terms(float x) {
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(hi) : "f"(x));
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(lo) : "f"(x - __uint_as_float(hi)));
+  }
+};
+__device__ __forceinline__ void mma_tf32(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d += a b: a's rows g and g + 8 at columns t and t + 4, b's rows t and t + 4 at column g.
+__device__ __forceinline__ void mma_terms(float (&d)[4], const Terms (&a)[4], const Terms& b0, const Terms& b1) {
+  mma_tf32(d, a[0].lo, a[1].lo, a[2].lo, a[3].lo, b0.hi, b1.hi);
+  mma_tf32(d, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.lo, b1.lo);
+  mma_tf32(d, a[0].hi, a[1].hi, a[2].hi, a[3].hi, b0.hi, b1.hi);
+}
+
+// c += sum over this warp's columns of u[i][k] u[j][k], i of its strip, j of its
+// kGramTiles blocks of 8: c[n] is an MMA's result.  The MMA cuts its sums off, so
+// a tile's are added in float.
 template <int MP>
 __device__ __forceinline__ void gram_tile(const float* u, int ld, float (&c)[4][4]) {
   using C = Cfg<MP>;
-  const int t = threadIdx.x % C::kGroup, g = threadIdx.x / C::kGroup;
-  const float* a = u + (t / (MP / 4)) * ld + g * (C::NC / C::kGroups);
-  const float* b = u + (t % (MP / 4)) * ld + g * (C::NC / C::kGroups);
-#pragma unroll 4
-  for (int k = 0; k < C::NC / C::kGroups; k += 4) {
-    float4 x[4], y[4];
+  const int warp = threadIdx.x >> 5, g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int strip = warp % C::kRows, part = warp / C::kRows;
+  const int j0 = MP == 64 ? part * 32 : 0, k0 = MP == 64 ? 0 : part * C::kGramCols;
+  float d[C::kGramTiles][4] = {};
+#pragma unroll 2
+  for (int k = k0; k < k0 + C::kGramCols; k += 8) {
+    const float* at = u + k + t;
+    Terms a[4];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      x[r] = *reinterpret_cast<const float4*>(a + r * (MP / 4) * ld + k);
-      y[r] = *reinterpret_cast<const float4*>(b + r * (MP / 4) * ld + k);
+    for (int i = 0; i < 4; ++i) a[i] = Terms(at[(strip * 16 + g + 8 * (i & 1)) * ld + 4 * (i >> 1)]);
+#pragma unroll
+    for (int n = 0; n < C::kGramTiles; ++n) {
+      // (16 rows: what a holds already)
+      const float* row = at + (j0 + 8 * n + g) * ld;
+      const Terms b0 = MP == 16 ? a[n & 1] : Terms(row[0]), b1 = MP == 16 ? a[2 + (n & 1)] : Terms(row[4]);
+      mma_terms(d[n], a, b0, b1);
     }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int s = 0; s < 4; ++s)
-        c[r][s] = fmaf(x[r].x, y[s].x, fmaf(x[r].y, y[s].y, fmaf(x[r].z, y[s].z, fmaf(x[r].w, y[s].w, c[r][s]))));
   }
+#pragma unroll
+  for (int n = 0; n < C::kGramTiles; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[n][i] += d[n][i];
 }
-// The groups' sums joined in order, through the tile's memory, to `to`.
+// The parts' sums joined in order, through the tile's memory, to `to`.  What lies
+// below the diagonal is taken from above, so that the matrix is symmetric.
 template <int MP>
 __device__ __forceinline__ void put_gram(float (&c)[4][4], float* u, float* to) {
   using C = Cfg<MP>;
-  const int t = threadIdx.x % C::kGroup, g = threadIdx.x / C::kGroup;
-  float* at = C::kGroups == 1 ? to : u + g * MP * MP;
+  const int warp = threadIdx.x >> 5, g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int strip = warp % C::kRows, part = warp / C::kRows;
+  float* at = C::kSums == 1 ? to : u + part * MP * MP;
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+  for (int n = 0; n < C::kGramTiles; ++n)
 #pragma unroll
-    for (int s = 0; s < 4; ++s) at[(t / (MP / 4) + MP / 4 * r) * MP + t % (MP / 4) + MP / 4 * s] = c[r][s];
-  if (C::kGroups == 1) return;
+    for (int i = 0; i < 4; ++i) {
+      const int row = strip * 16 + g + 8 * (i >> 1), col = (MP == 64 ? part * 32 : 0) + 8 * n + 2 * t + (i & 1);
+      if (row > col) continue;
+      at[row * MP + col] = c[n][i];
+      at[col * MP + row] = c[n][i];
+    }
+  if (C::kSums == 1) return;
   __syncthreads();
   for (int i = threadIdx.x; i < MP * MP; i += kThreads) {
     float v = 0.f;
 #pragma unroll
-    for (int j = 0; j < C::kGroups; ++j) v += u[j * MP * MP + i];
+    for (int j = 0; j < C::kSums; ++j) v += u[j * MP * MP + i];
     to[i] = v;
   }
 }
 
-// u <- Q u for the tile, four rows and columns a thread; q holds Q^T.
+// u <- Q u for the tile, a strip of rows and a run of columns a warp; q holds Q^T.
 template <int MP>
 __device__ __forceinline__ void mul_tile(const float* q, float* u, int ld) {
   using C = Cfg<MP>;
-  const int j = (threadIdx.x % (C::NC / 4)) * 4, i = (threadIdx.x / (C::NC / 4)) * 4;
-  float4 y[4];
+  const int warp = threadIdx.x >> 5, g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  const int row = (warp % C::kRows) * 16 + g, col = warp / C::kRows * 32;
+  float y[4][4] = {};
+#pragma unroll 2
+  for (int k = 0; k < MP; k += 8) {
+    Terms a[4];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) y[r] = make_float4(0, 0, 0, 0);
-#pragma unroll 4
-  for (int k = 0; k < MP; ++k) {
-    const float4 v = *reinterpret_cast<const float4*>(u + k * ld + j);
-    const float4 w4 = *reinterpret_cast<const float4*>(q + k * C::LDM + i);
-    const float w[4] = {w4.x, w4.y, w4.z, w4.w};
+    for (int i = 0; i < 4; ++i) a[i] = Terms(q[(k + t + 4 * (i >> 1)) * C::LDM + row + 8 * (i & 1)]);
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      y[r].x = fmaf(w[r], v.x, y[r].x);
-      y[r].y = fmaf(w[r], v.y, y[r].y);
-      y[r].z = fmaf(w[r], v.z, y[r].z);
-      y[r].w = fmaf(w[r], v.w, y[r].w);
+    for (int n = 0; n < 4; ++n) {
+      const float* at = u + (k + t) * ld + col + 8 * n + g;
+      mma_terms(y[n], a, Terms(at[0]), Terms(at[4 * ld]));
     }
   }
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < 4; ++r) *reinterpret_cast<float4*>(u + (i + r) * ld + j) = y[r];
-  __syncthreads();
-}
-// The same for two tiles side by side, or one: eight rows and four columns a
-// thread, half of the threads a tile.  A 16-byte load costs shared memory four
-// cycles whatever its lanes share: three for 32 multiply-adds, above two for 16.
-// Faster for 64 rows (64 of 2000 x 33: 245 against 259 us), where it pays for its registers.
-template <int MP>
-__device__ __forceinline__ void mul_tiles(const float* q, float* u, int ld, bool two) {
-  using C = Cfg<MP>;
-  const int half = threadIdx.x / (kThreads / 2), t = threadIdx.x % (kThreads / 2);
-  const int j = half * C::NC + (t % (C::NC / 4)) * 4, i = (t / (C::NC / 4)) * 8;
-  const bool mine = two || half == 0;
-  float4 y[8];
+  for (int n = 0; n < 4; ++n)
 #pragma unroll
-  for (int r = 0; r < 8; ++r) y[r] = make_float4(0, 0, 0, 0);
-  if (mine) {
-#pragma unroll 4
-    for (int k = 0; k < MP; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(u + k * ld + j);
-      const float4 a = *reinterpret_cast<const float4*>(q + k * C::LDM + i);
-      const float4 b = *reinterpret_cast<const float4*>(q + k * C::LDM + i + 4);
-      const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        y[r].x = fmaf(w[r], v.x, y[r].x);
-        y[r].y = fmaf(w[r], v.y, y[r].y);
-        y[r].z = fmaf(w[r], v.z, y[r].z);
-        y[r].w = fmaf(w[r], v.w, y[r].w);
-      }
-    }
-  }
-  __syncthreads();
-  if (mine) {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) *reinterpret_cast<float4*>(u + (i + r) * ld + j) = y[r];
-  }
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<float2*>(u + (row + 8 * i) * ld + col + 8 * n + 2 * t) = make_float2(y[n][2 * i], y[n][2 * i + 1]);
   __syncthreads();
 }
 template <int MP>
@@ -523,7 +534,7 @@ struct Schedule {
 };
 template <int MP>
 __host__ __device__ constexpr int cluster_scratch() {   // floats beside u: G, P, Q, this CTA's share, the groups' sums
-  return 3 * MP * Cfg<MP>::LDM + MP * MP + (Cfg<MP>::kGroups > 1 ? Cfg<MP>::kGroups * MP * MP : 0);
+  return 3 * MP * Cfg<MP>::LDM + MP * MP + (Cfg<MP>::kSums > 1 ? Cfg<MP>::kSums * MP * MP : 0);
 }
 
 template <int MP, bool BF16, int V>
@@ -592,10 +603,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n = min(kMuonPartSteps, sc.steps - done);
     newton_schulz<MP>(g, p, q, n, true, inv, e.m, sc.a, sc.b, sc.c);
     if (done + n < sc.steps) {
-      for (int n0 = first; n0 < last; n0 += (MP < 64 ? 1 : 2) * C::NC) {
-        if constexpr (MP < 64) mul_tile<MP>(q, u + (n0 - first), ld);
-        else mul_tiles<MP>(q, u + (n0 - first), ld, n0 + C::NC < last);
-      }
+      for (int n0 = first; n0 < last; n0 += C::NC) mul_tile<MP>(q, u + (n0 - first), ld);
     } else {
       if constexpr (MP < 64 && V == 4) {
         for (int n0 = first; n0 < last; n0 += C::NC) {
