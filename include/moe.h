@@ -503,13 +503,17 @@ size_t moe_ffn_workspace_size(const moe_ffn_shape* shape, int32_t backward);
  *   w_gate_up  bf16 [2 I, H]: rows 0 .. I - 1 Wg, I .. 2 I - 1 Wu
  *   w_down     bf16 [H, I]
  *   base       bf16 [T, H], rows ld_base apart; NULL for zero; may be out itself
+ *              (the same stride)
  *   out        bf16 [T, H], rows ld_out apart; may be x itself (the same
- *              stride), otherwise no part of x or of the weights
+ *              stride)
  *   status     device int32, zeroed by the caller when it is made: the first
  *              device-side error (MOE_ERR_DEVICE_TIMEOUT: a bounded wait ran
  *              out) is recorded there, and stays; the results are then undefined
  * x, base, out and the weights 16-byte aligned, row strides multiples of 8
- * elements and at least the row's length.  Sums are float; silu(g) u is
+ * elements and at least the row's length.  What the call writes (out, the workspace,
+ * status) is otherwise memory that no other tensor of the call has a byte of: a call
+ * where one does is refused with MOE_ERR_INVALID_ARG (rows that lie between the rows of
+ * another tensor are apart from it).  Sums are float; silu(g) u is
  * rounded to bf16 once, between the two products.  Up to 32 tokens stream the
  * weights once from HBM; larger batches run on the tensor cores. */
 int32_t moe_ffn_forward(const moe_ffn_shape* shape, const void* x, int64_t ld_x,
@@ -521,13 +525,14 @@ int32_t moe_ffn_forward(const moe_ffn_shape* shape, const void* x, int64_t ld_x,
  * activations are computed again from x, so that nothing of the forward is kept:
  *   dh = dout Wd, s = sigmoid(g): du = dh g s, dg = dh u s (1 + g (1 - s))
  *   dx          bf16 [T, H] = dx_base + dg Wg + du Wu; dx_base bf16 or NULL for
- *               zero, may be dx itself; NULL: not computed.  Not the memory of
- *               x or dout
+ *               zero, may be dx itself (the same stride); NULL: not computed
  *   dw_gate_up  bf16 [2 I, H] = [dg^T x; du^T x]
  *   dw_down     bf16 [H, I] = dout^T (silu(g) u)
- * The weights' gradients are written in full (zero without tokens), to memory that
- * no other tensor of the call has a part of; both or neither may be NULL, and with
- * them num_tokens is at most MOE_FFN_MAX_SUMMED: a tensor core cuts its float sums
+ * What the call writes (dx, the weights' gradients, the workspace, status) is otherwise
+ * memory that no other tensor of the call has a byte of, or the call is refused as the
+ * forward is.
+ * The weights' gradients are written in full (zero without tokens); both or neither may
+ * be NULL, and with them num_tokens is at most MOE_FFN_MAX_SUMMED: a tensor core cuts its float sums
  * off instead of rounding them, and a sum of n terms of one sign comes out about
  * n 2^-27.3 of itself short, there 2^-11.  (Sums over features, here and in the
  * forward, do so too: with 131072 features of one sign 2^-10, dx's over both

@@ -96,7 +96,8 @@ class GatedFFN(_Status):
 
     def forward(self, x, base=None, out=None):
         """base + the block's output: bf16 [T, H].  x and base bf16 [T, H], rows
-        may be strided; `out` may be `base` itself, or x."""
+        may be strided; `out` may be `base` itself, or x, and shares no memory with
+        the call's tensors otherwise (a call where it does is refused)."""
         dev, (wgu, wd) = self._start()
         T, H = _rows(x, "x"), self.hidden
         shape, bf16 = (T, H), torch.bfloat16
@@ -123,8 +124,8 @@ class GatedFFN(_Status):
         with dx_base added, the weights' gradients in the weights' shapes (zero
         without tokens; of at most 65536 tokens a call).  The activations are
         computed again from x.  What is not needed comes back as None.  `dx` may
-        be `dx_base`, not x or dout; dw_gate_up and dw_down are memory of their
-        own."""
+        be `dx_base`; what is written shares no memory with the call's tensors
+        otherwise (a call where it does is refused)."""
         dev, (wgu, wd) = self._start()
         T, H = _rows(x, "x"), self.hidden
         shape, bf16 = (T, H), torch.bfloat16

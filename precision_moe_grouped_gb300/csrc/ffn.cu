@@ -707,6 +707,47 @@ int32_t check_weights(const void* w_gate_up, const void* w_down, const void* ws,
   return MOE_OK;
 }
 
+// A tensor's bytes: rows of `width`, `step` apart; no rows: none.
+struct Span {
+  const char* name;
+  int64_t at, rows, step, width;
+};
+Span span(const char* name, const void* p, int64_t rows, int64_t ld, int64_t cols) {
+  return {name, static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)), p ? rows : 0, 2 * ld, 2 * cols};
+}
+Span span(const char* name, const void* p, size_t bytes) {
+  return {name, static_cast<int64_t>(reinterpret_cast<uintptr_t>(p)), p ? 1 : 0, 0, static_cast<int64_t>(bytes)};
+}
+// Rows and columns of one buffer may be shared out to several tensors, so that
+// ranges from the first byte to the last may meet where the tensors do not.
+bool meet(const Span& a, const Span& b) {
+  if (!a.rows || !b.rows) return false;
+  if (a.rows > b.rows) return meet(b, a);
+  const int64_t d = b.at - a.at;
+  if (d >= (a.rows - 1) * a.step + a.width || -d >= (b.rows - 1) * b.step + b.width) return false;
+  // the first k from `from` on with -b.width < d + k step; whether it is below `to`, and d + k step below a.width
+  auto hits = [&](int64_t d, int64_t step, int64_t from, int64_t to) {
+    const int64_t need = -b.width - d;   // k step > need
+    int64_t k = step == 0 ? from : need < 0 ? -((-need + step - 1) / step) + 1 : need / step + 1;
+    k = std::max(k, from);
+    return k < to && d + k * step > -b.width && d + k * step < a.width;
+  };
+  // with equal strides only the rows' difference counts
+  if (a.step == b.step) return hits(d, a.step, 1 - a.rows, b.rows);
+  for (int64_t i = 0; i < a.rows; ++i)
+    if (hits(d - i * a.step, b.step, 0, b.rows)) return true;
+  return false;
+}
+int32_t check_apart(const Span& a, const Span& b) {
+  if (!meet(a, b)) return MOE_OK;
+  return entry_fail(MOE_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+}
+// ... unless they are the same rows.
+int32_t check_apart_or_same(const Span& a, const Span& b) {
+  const bool same = a.at == b.at && (a.rows <= 1 || a.step == b.step);
+  return same ? MOE_OK : check_apart(a, b);
+}
+
 template <class Epi>
 dense::Launch<typename Epi::Args> new_launch(int32_t* status) {
   dense::Launch<typename Epi::Args> l = {};
@@ -913,7 +954,20 @@ extern "C" int32_t moe_ffn_forward(const moe_ffn_shape* s, const void* x, int64_
   MOE_TRY(check_matrix(x, "x", ld_x, s->hidden));
   if (base) MOE_TRY(check_matrix(base, "base", ld_base, s->hidden));
   MOE_TRY(check_matrix(out, "out", ld_out, s->hidden));
-  MOE_TRY(check_weights(w_gate_up, w_down, workspace, workspace_bytes, ffn_ws(s, false).total, status));
+  const size_t need = ffn_ws(s, false).total;
+  MOE_TRY(check_weights(w_gate_up, w_down, workspace, workspace_bytes, need, status));
+  {
+    const int64_t T = s->num_tokens, H = s->hidden, I = s->inter;
+    const Span to = span("out", out, T, ld_out, H), ws = span("workspace", workspace, need);
+    const Span from[] = {span("x", x, T, ld_x, H), span("base", base, T, ld_base, H),
+                         span("w_gate_up", w_gate_up, 1, 0, 2 * I * H), span("w_down", w_down, 1, 0, H * I),
+                         span("status", status, 4)};
+    for (int i = 0; i < 5; ++i) {
+      MOE_TRY(i < 2 ? check_apart_or_same(to, from[i]) : check_apart(to, from[i]));
+      MOE_TRY(check_apart(ws, from[i]));
+    }
+    MOE_TRY(check_apart(ws, to));
+  }
   int sms = 0;
   MOE_TRY(check_device(&sms));
   return ffn_forward(s, x, ld_x, w_gate_up, w_down, base, ld_base, out, ld_out,
@@ -940,9 +994,14 @@ extern "C" int32_t moe_ffn_backward(const moe_ffn_shape* s, const void* dout, in
     if (dw_gate_up == dw_down)
       return entry_fail(MOE_ERR_INVALID_ARG, "dw_gate_up and dw_down must be memory of their own");
   }
+  const int64_t T = s->num_tokens, H = s->hidden, I = s->inter;
+  const Span dw[2] = {span("dw_gate_up", dw_gate_up, 1, 0, 2 * I * H), span("dw_down", dw_down, 1, 0, H * I)};
+  const Span w[2] = {span("w_gate_up", w_gate_up, 1, 0, 2 * I * H), span("w_down", w_down, 1, 0, H * I)};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (s->num_tokens == 0) {   // sums over no tokens
+  if (T == 0) {   // sums over no tokens
     if (!dw_gate_up) return MOE_OK;
+    MOE_TRY(check_apart(dw[0], dw[1]));
+    for (int i = 0; i < 4; ++i) MOE_TRY(check_apart(dw[i & 1], w[i >> 1]));
     MOE_TRY(check_device(nullptr));
     const size_t n = static_cast<size_t>(s->hidden) * s->inter * 2;
     MOE_CUDA(cudaMemsetAsync(dw_gate_up, 0, 2 * n, st));
@@ -952,12 +1011,25 @@ extern "C" int32_t moe_ffn_backward(const moe_ffn_shape* s, const void* dout, in
   MOE_TRY(check_matrix(dout, "dout", ld_dout, s->hidden));
   MOE_TRY(check_matrix(x, "x", ld_x, s->hidden));
   if (dx_base) MOE_TRY(check_matrix(dx_base, "dx_base", ld_dx_base, s->hidden));
-  if (dx) {
-    MOE_TRY(check_matrix(dx, "dx", ld_dx, s->hidden));
-    if (dx == x || dx == dout)
-      return entry_fail(MOE_ERR_INVALID_ARG, "dx must not be the memory of x or dout");
+  if (dx) MOE_TRY(check_matrix(dx, "dx", ld_dx, s->hidden));
+  const size_t need = ffn_ws(s, true).total;
+  MOE_TRY(check_weights(w_gate_up, w_down, workspace, workspace_bytes, need, status));
+  {
+    const Span to = span("dx", dx, T, ld_dx, H), add = span("dx_base", dx ? dx_base : nullptr, T, ld_dx_base, H);
+    const Span ws = span("workspace", workspace, need);
+    const Span from[] = {span("x", x, T, ld_x, H), span("dout", dout, T, ld_dout, H), w[0], w[1],
+                         span("status", status, 4)};
+    for (const Span& t : from) {
+      for (const Span& written : {to, dw[0], dw[1], ws}) MOE_TRY(check_apart(written, t));
+    }
+    MOE_TRY(check_apart_or_same(to, add));
+    for (const Span& t : {to, add, ws}) {
+      for (const Span& g : dw) MOE_TRY(check_apart(g, t));
+    }
+    MOE_TRY(check_apart(dw[0], dw[1]));
+    MOE_TRY(check_apart(ws, to));
+    MOE_TRY(check_apart(ws, add));
   }
-  MOE_TRY(check_weights(w_gate_up, w_down, workspace, workspace_bytes, ffn_ws(s, true).total, status));
   if (!dx && !dw_gate_up) return MOE_OK;
   int sms = 0;
   MOE_TRY(check_device(&sms));
