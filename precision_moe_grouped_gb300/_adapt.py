@@ -90,6 +90,11 @@ def _check_flat(t, name: str, dtype, shape: tuple, device) -> None:
         _check_tensor(t, name, cuda=True, dtype=dtype, shape=shape, device=device)
 
 
+def _same_layout(t, dtype, shape: tuple) -> bool:
+    """What tells a tensor at a known address from a view of the same memory."""
+    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+
+
 def _same_device(device, made_on) -> None:
     if device != made_on:
         _bad(f"the current device is cuda:{device}, this object's tensors are on cuda:{made_on}")

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 from . import _adapt as A
 from . import _lib
-from ._adapt import _check_flat, _check_rows, _int32, _ptr, _rows, _same_device, _scratch
+from ._adapt import _check_flat, _check_rows, _int32, _ptr, _rows, _same_device, _same_layout, _scratch
 from ._lib import FfnShape, _bad, check
 
 torch = None   # bound when the first object is made: the build imports this package without it
@@ -43,7 +43,8 @@ class GatedFFN(_Status):
     up projection), w_down bf16 [H, I]; H and I multiples of 8.  The weights
     are read at every call, so that an update in place takes effect with the
     next one.  So does another tensor in their place, by assignment here or to
-    a tensor's .data: a call that finds other memory checks it.
+    a tensor's .data: a call that finds other memory, another shape, type or
+    layout checks it, and refuses what is not as at the start.
 
     Nothing here is recorded for autograd: outputs require no gradient whatever
     the inputs do, and backward() is called by hand."""
@@ -62,9 +63,9 @@ class GatedFFN(_Status):
         self._new_status(self.device)
 
     def _check_weights(self, *at) -> None:
-        """Checks the weights, whose addresses are not the last call's.  That one's
+        """Checks the weights, which are not as in the last call.  That one's
         memory is held (detached): while it was the last call's, no other tensor
-        could get its addresses."""
+        but its views could get its addresses."""
         for t, name, shape in zip((self.w_gate_up, self.w_down), ("w_gate_up", "w_down"), self._shapes):
             _check_flat(t, name, torch.bfloat16, shape, self._dev)
         self._held = [self.w_gate_up.detach(), self.w_down.detach()]
@@ -89,8 +90,10 @@ class GatedFFN(_Status):
         dev = A._device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        at = _ptr(self.w_gate_up), _ptr(self.w_down)
-        if at != self._at:
+        w, d, (w_shape, d_shape) = self.w_gate_up, self.w_down, self._shapes
+        at = _ptr(w), _ptr(d)
+        if (at != self._at or not _same_layout(w, torch.bfloat16, w_shape)
+                or not _same_layout(d, torch.bfloat16, d_shape)):
             self._check_weights(*at)
         return dev, at
 

@@ -150,6 +150,38 @@ def test_ffn_weights_are_checked_at_every_call(lib):
     assert len(op._held) == 2
 
 
+def test_ffn_weights_in_the_same_memory(lib):
+    """Another tensor at the old address, by assignment or to .data: one of another layout, type or size is refused,
+    as it is at an address of its own."""
+    x = zeros(4, 64)
+    for name, others in (("w_down", [lambda t: t.t(), lambda t: t.view(torch.float16), lambda t: t.view(32, 128),
+                                     lambda t: t[:, :32], lambda t: t.view(-1), lambda t: t[:32]]),
+                         ("w_gate_up", [lambda t: t.view(torch.int16), lambda t: t[:64], lambda t: t.view(64, 128)])):
+        for other in others:
+            for assign in (True, False):
+                op = ffn(64, 64)
+                old = getattr(op, name)
+                new = other(old)
+                assert new.data_ptr() == old.data_ptr()
+                if assign:
+                    setattr(op, name, new)
+                elif new.dtype is BF16:
+                    old.data = other(old.data)
+                else:
+                    continue
+                for call in (lambda: op(x), lambda: op.backward(x, x)):
+                    with pytest.raises(P.MoeError, match=name):
+                        call()
+                setattr(op, name, zeros(64, 64) if name == "w_down" else zeros(128, 64))
+                op(x)
+    assert all(name == "moe_ffn_forward" for name, _ in lib.calls)
+    # the same rows again are no other tensor
+    op, calls = ffn(), len(lib.calls)
+    op.w_down = op.w_down[:]
+    op(x)
+    assert len(lib.calls) == calls + 1
+
+
 def muon(shapes=((3, 20, 30), (40, 16)), grads=torch.float32, copies=True, **kw):
     z = lambda kind: [zeros(*s, dtype=kind) for s in shapes]                       # noqa: E731
     return P.Muon(z(torch.float32), z(grads), copies=z(BF16) if copies else None, state=z(torch.float32), **kw)
