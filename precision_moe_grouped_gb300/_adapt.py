@@ -124,8 +124,9 @@ class LowRankAdapters:
     r, H and N multiples of 8, r <= 128, NA <= 1024.  The pools are read at
     every call, so that an update in place takes effect with the next one.  So
     does another tensor in their place, by assignment here or to a tensor's
-    .data: a call that finds other memory checks it, and refuses what is not as
-    at the start (a module moved to the host or to another type).
+    .data: a call that finds other memory, another shape, type or layout checks
+    it, and refuses what is not as at the start (a module moved to the host or to
+    another type).
 
     Nothing here is recorded for autograd: outputs require no gradient whatever
     the inputs do, and backward() is called by hand."""
@@ -149,9 +150,9 @@ class LowRankAdapters:
             self._call(0, kind, 0)
 
     def _check_pools(self, *at) -> None:
-        """Checks a, b and scale, whose addresses are not the last call's.  That
-        one's memory is held (detached): while it was the last call's, no other
-        tensor could get its addresses."""
+        """Checks a, b and scale, which are not as in the last call.  That one's
+        memory is held (detached): while it was the last call's, no other tensor
+        but its views could get its addresses."""
         shapes = self._shapes
         _check_flat(self.a, "a", torch.bfloat16, shapes[0], self._dev)
         _check_flat(self.b, "b", torch.bfloat16, shapes[1], self._dev)
@@ -159,6 +160,17 @@ class LowRankAdapters:
             _check_flat(self.scale, "scale", torch.float32, shapes[2], self._dev)
         self._held = [t.detach() for t in (self.a, self.b, self.scale) if t is not None]
         self._at_a, self._at_b, self._at_scale = at
+
+    def _addresses(self):
+        """(a, b, scale) of the pools, checked."""
+        pa, pb, ps, shapes = self.a, self.b, self.scale, self._shapes
+        a, b, scale = _ptr(pa), _ptr(pb), _ptr(ps)
+        if (a != self._at_a or b != self._at_b or scale != self._at_scale
+                or not _same_layout(pa, torch.bfloat16, shapes[0])
+                or not _same_layout(pb, torch.bfloat16, shapes[1])
+                or ps is not None and not _same_layout(ps, torch.float32, shapes[2])):
+            self._check_pools(a, b, scale)
+        return a, b, scale
 
     def _call(self, T: int, kind: int, backward: int):
         """(shape, workspace bytes) of a call with T tokens."""
@@ -192,9 +204,7 @@ class LowRankAdapters:
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        a, b, scale = _ptr(self.a), _ptr(self.b), _ptr(self.scale)
-        if a != self._at_a or b != self._at_b or scale != self._at_scale:
-            self._check_pools(a, b, scale)
+        a, b, scale = self._addresses()
         T, H, N = _rows(x, "x"), self._H, self._N
         ld_x = _check_rows(x, "x", torch.bfloat16, (T, H), dev)
         _check_flat(ids, "ids", torch.int32, (T,), dev)
@@ -228,9 +238,7 @@ class LowRankAdapters:
         dev = _device()
         if dev != self._dev:
             _same_device(dev, self._dev)
-        a, b, scale = _ptr(self.a), _ptr(self.b), _ptr(self.scale)
-        if a != self._at_a or b != self._at_b or scale != self._at_scale:
-            self._check_pools(a, b, scale)
+        a, b, scale = self._addresses()
         T, H, N = _rows(x, "x"), self._H, self._N
         if dout is None:
             _bad("dout is None")

@@ -108,6 +108,36 @@ def adapters(NA=3, r=8, H=64, N=32):
     return P.LowRankAdapters(a, b, on(torch.ones(NA)))
 
 
+def test_views_of_the_pools_own_memory_are_checked(lib):
+    """Another tensor at the old address, by assignment or to .data: one of another layout, type or size is refused,
+    as it is at an address of its own."""
+    x, ids = on(torch.zeros(4, 64, dtype=torch.bfloat16)), on(torch.zeros(4, dtype=torch.int32))
+    changes = {"a": [lambda t: t.transpose(1, 2), lambda t: t.view(torch.float16), lambda t: t[:2], lambda t: t.view(3, 32, 128)],
+               "b": [lambda t: t.transpose(1, 2), lambda t: t.view(torch.int16), lambda t: t[:, :16]],
+               "scale": [lambda t: t.view(torch.int32), lambda t: t[:2]]}
+    for name, others in changes.items():
+        for other in others:
+            for assign in (True, False):
+                op = adapters(r=64, N=64)
+                old = getattr(op, name)
+                new = other(old)
+                assert new.data_ptr() == old.data_ptr()
+                if assign:
+                    setattr(op, name, new)
+                elif new.dtype is old.dtype:
+                    old.data = other(old.data)
+                else:
+                    continue
+                for call in (lambda: op.forward(x, ids), lambda: op.backward(x, x, ids)):
+                    with pytest.raises(P.MoeError, match=name):
+                        call()
+    assert not lib.calls
+    op = adapters()
+    op.a = op.a[:]                                          # the same rows again
+    op.forward(x, ids)
+    assert len(lib.calls) == 1
+
+
 def test_pools_are_checked_at_every_call(lib):
     """A pool whose memory, type, size, layout or place changed after the
     construction: the library sees the new one or the call is refused."""
