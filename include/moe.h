@@ -552,7 +552,9 @@ int32_t moe_ffn_backward(const moe_ffn_shape* shape, const void* dout, int64_t l
 #define MOE_MUON_RMS 0        /* 0.2 sqrt(max(rows, cols)): a root mean square of about 0.2 */
 #define MOE_MUON_SPECTRAL 1   /* sqrt(max(1, rows / cols)) */
 
-/* `count` matrices [rows, cols] one after another; all updated in place. */
+/* `count` matrices [rows, cols] one after another; all updated in place.  param,
+ * momentum and param_bf16 are written, side by side with all reads: the caller sees
+ * to it that no other tensor of the call (nor grad_scale) has a byte of them. */
 typedef struct {
   float* param;        /* [count, rows, cols] */
   const void* grad;    /* the same, of grad_dtype */

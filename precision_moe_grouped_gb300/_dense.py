@@ -7,6 +7,8 @@ device, and a call's workspace comes from torch's allocator for that stream.
 """
 from __future__ import annotations
 
+import bisect
+
 from . import _adapt as A
 from . import _lib
 from ._adapt import _check_flat, _check_rows, _int32, _ptr, _rows, _same_device, _same_layout, _scratch
@@ -20,6 +22,12 @@ def _bind_torch() -> None:
     if torch is None:
         A._bind_torch()
         torch = A.torch
+
+
+def _bytes(t) -> tuple:
+    """(first, behind the last) of a contiguous tensor's bytes."""
+    at = t.data_ptr()
+    return at, at + t.numel() * t.element_size()
 
 
 class _Status:
@@ -175,7 +183,9 @@ class Muon(_Status):
     in place; grads: tensors of the same shapes, all float32 or all bfloat16;
     copies: bfloat16 tensors of the same shapes that receive the rounded
     parameters, or None.  `state`: the momenta, float32 of the same shapes, to
-    resume from; by default they start at zero.  update_scale "rms" makes an
+    resume from; by default they start at zero.  What is written (params, state,
+    copies) shares no memory with another tensor: calls where it does are refused.
+    update_scale "rms" makes an
     update's root mean square about 0.2 whatever the shape, "spectral" its
     largest singular value about sqrt(max(1, rows / cols)).  The tensors are
     bound and held here (params, grads, copies and state name them and cannot be
@@ -206,10 +216,10 @@ class Muon(_Status):
             state = [torch.zeros_like(p) for p in bound]
         self._state = self._bound(state, "state", torch.float32)
         self._copies = None if copies is None else self._bound(copies, "copies", torch.bfloat16)
-        written = [t.data_ptr() for t in (*bound, *self._state, *(self._copies or ())) if t.numel()]
-        self._written = frozenset(written)
-        if len(self._written) < len(written):
-            _bad("params, state and copies must be distinct")   # all written, side by side
+        written = sorted(_bytes(t) for t in (*bound, *self._state, *(self._copies or ())) if t.numel())
+        if any(a[1] > b[0] for a, b in zip(written, written[1:])):
+            _bad("params, state and copies must be distinct memory")   # all written, side by side
+        self._written = [a for a, _ in written], [b for _, b in written]
         self._table = (_lib.MuonTensor * max(1, len(bound)))()
         for i, (e, p, m) in enumerate(zip(self._table, bound, self._state)):
             e.param, e.momentum = p.data_ptr(), m.data_ptr()
@@ -230,6 +240,12 @@ class Muon(_Status):
         for i, (t, p) in enumerate(zip(held, self._params)):
             _check_flat(t, f"{name}[{i}]", dtype, p.shape, self._dev)
         return held
+
+    def _is_written(self, t) -> bool:
+        """Whether a step writes any byte of t."""
+        begin, end = _bytes(t)
+        i = bisect.bisect_left(self._written[0], end)
+        return begin < end and i > 0 and self._written[1][i - 1] > begin
 
     @property
     def params(self) -> tuple:
@@ -255,8 +271,8 @@ class Muon(_Status):
         if kind not in (torch.float32, torch.bfloat16):
             _bad(f"grads must be float32 or bfloat16, got {kind}")
         grads = self._bound(grads, "grads", kind)
-        if not self._written.isdisjoint(t.data_ptr() for t in grads):   # read again after a momentum is written
-            _bad("grads must not be params, state or copies")
+        if any(map(self._is_written, grads)):   # read again after a momentum is written
+            _bad("grads must not share memory with params, state or copies")
         self._grads = grads
         for e, t in zip(self._table, self._grads):
             e.grad = t.data_ptr()
@@ -291,6 +307,8 @@ class Muon(_Status):
         _same_device(dev, self._dev)
         o.grad_scale = None if grad_scale is None else A._check_numel(
             grad_scale, "grad_scale", 0, torch.float32, 1, dev)
+        if grad_scale is not None and self._is_written(grad_scale):
+            _bad("grad_scale must not share memory with params, state or copies")
         n = self._workspace_size()
         ws = _scratch(n, self._status)
         check(self._lib.moe_muon_step(self._table, len(self._params), o, ws.data_ptr(), n,

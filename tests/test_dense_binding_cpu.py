@@ -200,6 +200,36 @@ def test_muon_gradients_are_memory_of_their_own(lib):
     op.step()
 
 
+def test_muon_tensors_share_no_memory(lib):
+    """Slices of one buffer: end to end they are accepted; what is written may not begin or end inside another tensor,
+    nor lie in one."""
+    f32 = torch.float32
+    room, half = zeros(400, dtype=f32), zeros(400)
+    part = lambda at, of=room: of[at:at + 48].view(8, 6)                          # noqa: E731
+    good = dict(params=[part(0), part(48)], grads=[part(192), part(192)], state=[part(96), part(144)],
+                copies=[part(0, half), part(48, half)])
+    op = P.Muon(**good)
+    op.step()
+    assert len(lib.calls) == 1
+    for bad in (dict(params=[part(0), part(47)]), dict(state=[part(49), part(144)]), dict(state=[part(96), part(97)]),
+                dict(copies=[part(0, half), part(47, half)]), dict(copies=[part(0, half), room[50:74].view(BF16).view(8, 6)]),
+                dict(params=[part(0), room[20:26].view(1, 6)], state=[part(96), part(144)[:1]], grads=[part(192), part(192)[:1]],
+                     copies=None)):
+        with pytest.raises(P.MoeError, match="distinct"):
+            P.Muon(**{**good, **bad})
+    for grads in ([part(192), part(1)], [part(145), part(300)], [part(191), part(300)], [part(192), part(47)]):
+        for call in (lambda: P.Muon(**{**good, "grads": grads}), lambda: op.bind_grads(grads), lambda: op.step(grads)):
+            with pytest.raises(P.MoeError, match="grads must not"):
+                call()
+    for at in (0, 191):
+        with pytest.raises(P.MoeError, match="grad_scale must not"):
+            op.step(grad_scale=room[at])
+    assert len(lib.calls) == 1
+    op.step(grad_scale=room[192])
+    # a tensor without elements has no bytes
+    P.Muon([part(0), room[20:20].view(0, 6)], [part(192), room[0:0].view(0, 6)], state=[part(96), room[100:100].view(0, 6)]).step()
+
+
 def test_muon_arguments(lib):
     op = muon(lr=0.5, momentum=0.25, weight_decay=0.125, eps=1e-3, ns_steps=3, nesterov=False,
               ns_coefficients=(2.0, -1.5, 0.5), update_scale="spectral")
