@@ -83,7 +83,9 @@ struct Tile {
 
 // An operand that no kernel of the call writes is copied ahead of the grid wait,
 // as far as the slots go: the kernel before has passed its own, behind which the
-// call's inputs are complete.
+// call's inputs are complete.  Its producer comes to the grid wait before its first
+// bounded one, whose limit so covers this kernel's progress alone, however long the
+// kernel before still runs.
 constexpr int kEarlyA = 1, kEarlyB = 2;
 
 template <typename Args>
@@ -251,13 +253,14 @@ struct EpiWarp {
 // followed by the next tile's first without a pause.
 template <bool IS_A, class L>
 __device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* smem, uint64_t* full, uint64_t* empty,
-                                        uint32_t rank, int pair, int pairs, volatile int32_t* abort_flag) {
+                                        uint32_t rank, int pair, int pairs, bool early,
+                                        volatile int32_t* abort_flag) {
   const int lane = threadIdx.x & 31;
   const uint32_t full0 = cluster_addr(full, 0), stages = static_cast<uint32_t>(l.stages);
   uint8_t* const slots = smem + (IS_A ? 0 : kABytes);
   asm volatile("fence.proxy.async.global;" ::: "memory");   // the kernel before used plain stores
   uint32_t stage = 0, phase = 0;
-  bool ok = true, issued = false;
+  bool ok = true, issued = false, ahead = early;   // ahead: of the grid wait, in slots that are free from the start
   for (int t = pair; ok && t < l.tiles; t += pairs) {
     const Tile o = find_tile(l, t);
     const Problem& p = l.p[o.p];
@@ -271,7 +274,11 @@ __device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* s
     const CUtensorMap* m = &maps.m[IS_A ? p.a_map : p.b_map];
     int x = mn ? at : k0 * kBK, y = mn ? k0 * kBK : at;
     for (int k = 0; k < n; ++k, x += dx, y += dy) {
-      if (!mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
+      if (ahead && phase) {
+        griddep_wait();
+        ahead = false;
+      }
+      if (!ahead && !mbar_wait_warp(empty + stage, phase ^ 1u, l.timeout_ns, l.status, kDevTimeout, abort_flag)) {
         ok = false;
         break;
       }
@@ -288,6 +295,7 @@ __device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* s
       }
     }
   }
+  if (ahead) griddep_wait();
   // Rank 0: every copy of both CTAs has landed before either may leave
   // (bounded, whatever the abort flag says): the last fill of each slot.
   if (rank == 0 && issued) {
@@ -343,15 +351,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   // (a producer of an early operand reads nothing that a kernel of the call writes)
-  if (!(warp == 0 && l.early == kEarlyA) && !(warp == 2 && l.early == kEarlyB)) {
+  const bool early = (warp == 0 && l.early == kEarlyA) || (warp == 2 && l.early == kEarlyB);
+  if (!early) {
     griddep_wait();
     griddep_launch_dependents();
   }
 
   if (warp == 0) {
-    produce<true>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
+    produce<true>(maps, l, smem, full, empty, rank, pair, pairs, early, abort_flag);
   } else if (warp == 2) {
-    produce<false>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
+    produce<false>(maps, l, smem, full, empty, rank, pair, pairs, early, abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {
