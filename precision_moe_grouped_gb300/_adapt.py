@@ -90,9 +90,10 @@ def _check_flat(t, name: str, dtype, shape: tuple, device) -> None:
         _check_tensor(t, name, cuda=True, dtype=dtype, shape=shape, device=device)
 
 
-def _same_layout(t, dtype, shape: tuple) -> bool:
-    """What tells a tensor at a known address from a view of the same memory."""
-    return t.dtype is dtype and t.shape == shape and t.is_contiguous()
+def _same_layout(t, dtype, shape) -> bool:
+    """What tells a tensor at a known address from a view of the same memory.
+    (shape: torch.Size, which size() is compared with the quickest.)"""
+    return t.dtype is dtype and t.size() == shape and t.is_contiguous()
 
 
 def _same_device(device, made_on) -> None:
@@ -141,7 +142,7 @@ class LowRankAdapters:
             _bad("b must be [adapters, out_features, rank]")
         N = self.out_features = b.shape[1]
         self._dims, self._H, self._N = (NA, r, H, N), H, N
-        self._shapes = (NA, r, H), (NA, N, r), (NA,)
+        self._shapes = torch.Size((NA, r, H)), torch.Size((NA, N, r)), torch.Size((NA,))
         self.a, self.b, self.scale, self.device, self._dev = a, b, scale, a.device, dev
         self._check_pools(a.data_ptr(), b.data_ptr(), _ptr(scale))
         self._lib = load()

@@ -63,7 +63,7 @@ class GatedFFN(_Status):
         if w_gate_up is None or w_gate_up.dim() != 2 or w_gate_up.shape[0] % 2:
             _bad("w_gate_up must be [2 * features, hidden]")
         I, H = self.inter, self.hidden = w_gate_up.shape[0] // 2, w_gate_up.shape[1]
-        self._shapes = (2 * I, H), (H, I)
+        self._shapes = torch.Size((2 * I, H)), torch.Size((H, I))
         self.w_gate_up, self.w_down, self.device, self._dev = w_gate_up, w_down, w_gate_up.device, dev
         self._check_weights(_ptr(w_gate_up), _ptr(w_down))
         self._lib, self._sizes = A.load(), {}
