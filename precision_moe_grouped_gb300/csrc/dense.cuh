@@ -251,16 +251,15 @@ struct EpiWarp {
 // B's, so that neither's instructions stand between a freed slot and its
 // refill.  The whole warp runs the loop, one lane issues; a tile's last slot is
 // followed by the next tile's first without a pause.
-template <bool IS_A, class L>
+template <bool IS_A, bool EARLY, class L>
 __device__ __forceinline__ void produce(const Maps& maps, const L& l, uint8_t* smem, uint64_t* full, uint64_t* empty,
-                                        uint32_t rank, int pair, int pairs, bool early,
-                                        volatile int32_t* abort_flag) {
+                                        uint32_t rank, int pair, int pairs, volatile int32_t* abort_flag) {
   const int lane = threadIdx.x & 31;
   const uint32_t full0 = cluster_addr(full, 0), stages = static_cast<uint32_t>(l.stages);
   uint8_t* const slots = smem + (IS_A ? 0 : kABytes);
   asm volatile("fence.proxy.async.global;" ::: "memory");   // the kernel before used plain stores
   uint32_t stage = 0, phase = 0;
-  bool ok = true, issued = false, ahead = early;   // ahead: of the grid wait, in slots that are free from the start
+  bool ok = true, issued = false, ahead = EARLY;   // ahead: of the grid wait, in slots that are free from the start
   for (int t = pair; ok && t < l.tiles; t += pairs) {
     const Tile o = find_tile(l, t);
     const Problem& p = l.p[o.p];
@@ -358,9 +357,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp == 0) {
-    produce<true>(maps, l, smem, full, empty, rank, pair, pairs, early, abort_flag);
+    if (early) produce<true, true>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
+    else produce<true, false>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
   } else if (warp == 2) {
-    produce<false>(maps, l, smem, full, empty, rank, pair, pairs, early, abort_flag);
+    if (early) produce<false, true>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
+    else produce<false, false>(maps, l, smem, full, empty, rank, pair, pairs, abort_flag);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (rank == 0) {

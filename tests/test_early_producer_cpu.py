@@ -47,7 +47,8 @@ int main(int, char** v) {
   p.bn = p.b_step = 256; p.b_rank = 128; p.tiles_m = 1; p.tiles_n = tiles; p.per_matrix = tiles; p.splits = 1;
   p.kb = p.kb_split = kb;
   int32_t none = 0;
-  produce<true>(maps, l, mem, bar, bar + kMaxStages, rank, 0, 1, CALL &none);
+  if (early) produce<true, true>(maps, l, mem, bar, bar + kMaxStages, rank, 0, 1, &none);
+  else produce<true, false>(maps, l, mem, bar, bar + kMaxStages, rank, 0, 1, &none);
 }
 """
 
@@ -69,15 +70,13 @@ def program(tmp_path_factory):
     constants = "\n".join(re.findall(r"^constexpr int \w+ = [^;]*;", text, re.M))
     parts = [cut(text, s) for s in ("template <int N>\nstruct MapList", "struct Problem {", "struct Tile {",
                                     "template <typename Args>\nstruct Launch {", "template <typename L>\n__device__ __forceinline__ Tile",
-                                    "template <bool IS_A, class L>\n__device__ __forceinline__ void produce")]
+                                    "template <bool IS_A, bool EARLY, class L>\n__device__ __forceinline__ void produce")]
     parts.insert(1, "using Maps = MapList<kMaxMaps>;")
     source = HEAD + re.sub(r"asm volatile\(.*?\);", "", constants + "\n" + "\n".join(parts))
     source = re.sub(r"#pragma unroll[^\n]*", "", source)
     d = tmp_path_factory.mktemp("producer")
     exe = str(d / "a")
-    call = "early," if re.search(r"bool early,", source) else ""
-    subprocess.run(["g++", "-std=c++17", "-x", "c++", "-", "-o", exe], input=source + MAIN.replace("CALL", call), text=True,
-                   check=True)
+    subprocess.run(["g++", "-std=c++17", "-x", "c++", "-", "-o", exe], input=source + MAIN, text=True, check=True)
 
     def run(*args):
         out = subprocess.run([exe, *map(str, args)], capture_output=True, text=True, check=True).stdout
