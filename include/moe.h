@@ -576,7 +576,10 @@ typedef struct {
   const float* grad_scale;   /* device scalar every gradient is multiplied by, or NULL */
 } moe_muon_options;
 
-/* Workspace bytes of moe_muon_step for these tensors; 0 for invalid arguments. */
+/* Workspace bytes of moe_muon_step for these tensors; 0 for invalid arguments.  At
+ * most some 4 GiB however many matrices there are, unless one alone takes more (8 bytes
+ * an element and 20 for each of the square of its shorter side): matrices of one shape
+ * run in slices of as many as that holds. */
 size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count,
                                const moe_muon_options* options);
 

@@ -435,10 +435,12 @@ bool make_scales(const moe_muon_options* o, Scales* out) {
   return true;
 }
 
-// One group: the tensors whose matrices are m x n (or n x m).
+// One group: the tensors whose matrices are m x n (or n x m), `all` of them in the
+// tensors' order; it runs in equal slices of up to `each`, of which this one has
+// `batch` matrices from number `first` on.
 struct Shape {
   int32_t m, n, mp, np;
-  int64_t batch;
+  int64_t all, each, first, batch;
 };
 Shape shape_of(const moe_muon_tensor& t) {
   Shape s;
@@ -446,7 +448,7 @@ Shape shape_of(const moe_muon_tensor& t) {
   s.n = std::max(t.rows, t.cols);
   s.mp = (s.m + 63) / 64 * 64;
   s.np = (s.n + 63) / 64 * 64;
-  s.batch = 0;
+  s.all = s.each = s.first = s.batch = 0;
   return s;
 }
 bool same(const moe_muon_tensor& t, const Shape& s) {
@@ -454,7 +456,7 @@ bool same(const moe_muon_tensor& t, const Shape& s) {
 }
 // Blocks' shares: long ones, unless they would leave SMs idle.
 int chunk_of(const Shape& s) {
-  return static_cast<int64_t>(s.m) * s.n * s.batch >= int64_t(600) * kChunk ? kChunk : kChunkSmall;
+  return static_cast<int64_t>(s.m) * s.n * s.each >= int64_t(600) * kChunk ? kChunk : kChunkSmall;
 }
 int chunks_of(const Shape& s) {
   return static_cast<int>(dense::cdiv(static_cast<int64_t>(s.m) * s.n, chunk_of(s)));
@@ -468,7 +470,7 @@ int64_t upper_tiles(int64_t mp) {
 // Shares of the sum over the long side, of at least four K blocks, where the
 // halves of X X^T's tiles leave half of the pairs without one.
 int gram_splits(const Shape& s) {
-  const int64_t units = 2 * upper_tiles(s.mp) * s.batch, kb = s.np / dense::kBK;
+  const int64_t units = 2 * upper_tiles(s.mp) * s.each, kb = s.np / dense::kBK;
   return static_cast<int>(std::max<int64_t>(1, std::min(dense::kPlanPairs / units, kb / 4)));
 }
 
@@ -681,6 +683,27 @@ int32_t apply(const Call& c, Group* gs, int n, float scale) {
   return run(c, b);
 }
 
+// What a slice has of a tensor: `count` matrices from number `at` on.
+struct Part {
+  int32_t tensor;
+  int64_t at, count, before;   // before: the group's matrices in the tensors ahead
+};
+// The slice's next part, beginning with {}; false: none.
+bool next_part(const Call& c, const Shape& s, Part* part) {
+  for (int32_t& i = part->tensor; i < c.count; ++i) {
+    if (!same(c.t[i], s)) continue;
+    const int64_t n = c.t[i].count, from = std::max(s.first, part->before), to = std::min(s.first + s.batch, part->before + n);
+    if (part->count == 0 && from < to) {
+      part->at = from - part->before;
+      part->count = to - from;
+      return true;
+    }
+    part->count = 0;
+    part->before += n;
+  }
+  return false;
+}
+
 // p <- decay p - lr s Q X for the groups' tensors, as many in a launch as it
 // holds.
 int32_t update(const Call& c, Group* gs, int n) {
@@ -692,22 +715,22 @@ int32_t update(const Call& c, Group* gs, int n) {
   };
   for (Group* g = gs; g < gs + n; ++g) {
     const Shape& s = g->s;
+    const int64_t size = static_cast<int64_t>(s.m) * s.n;
     int64_t z = 0;
-    for (int i = 0; i < c.count; ++i) {
-      const moe_muon_tensor& t = c.t[i];
-      if (!same(t, s)) continue;
+    for (Part part = {}; next_part(c, s, &part);) {
+      const moe_muon_tensor& t = c.t[part.tensor];
       const bool tall = t.rows > t.cols;
       EpiUpdate::Args& e = b.l.e[b.l.problems];
-      terms::Problem& p = b.problem(tall ? s.m : s.n, tall ? s.n : s.m, t.count, s.mp / dense::kBK);
+      terms::Problem& p = b.problem(tall ? s.m : s.n, tall ? s.n : s.m, part.count, s.mp / dense::kBK);
       MOE_TRY(b.operand(s, tall ? g->q : g->x, !tall, z, &p.a));
       MOE_TRY(b.operand(s, tall ? g->x : g->q, tall, z, &p.b));
-      e.p = t.param;
-      e.copy = static_cast<__nv_bfloat16*>(t.param_bf16);
+      e.p = t.param + part.at * size;
+      e.copy = t.param_bf16 ? static_cast<__nv_bfloat16*>(t.param_bf16) + part.at * size : nullptr;
       e.decay = muon_decay(c.o);
       e.step = static_cast<float>(muon_step(c.o, t) / (static_cast<double>(g->q.scale) * g->x.scale));
       e.rows = tall ? s.m : s.n;
       e.cols = tall ? s.n : s.m;
-      z += t.count;
+      z += part.count;
       if (b.l.problems == terms::kMaxProblems) MOE_TRY(send());
     }
   }
@@ -725,17 +748,16 @@ int32_t first_planes(const Call& c, const Group& g) {
   // that the second reading finds them there; as many small ones at once as do.
   const int64_t at_once = std::min<int64_t>(65535, std::max<int64_t>(1, kL2Bytes / (size * (bf16 ? 6 : 8))));
   int64_t z = 0;
-  for (int i = 0; i < c.count; ++i) {
-    const moe_muon_tensor& t = c.t[i];
-    if (!same(t, s)) continue;
+  for (Part p = {}; next_part(c, s, &p);) {
+    const moe_muon_tensor& t = c.t[p.tensor];
     Momentum a = {t.grad, t.momentum, c.o->grad_scale, static_cast<float>(c.o->momentum),
                   static_cast<float>(1.0 - c.o->momentum), bf16, c.o->nesterov};
     const int vec = size % 4 == 0 && ptr_aligned(t.momentum, 16) && ptr_aligned(t.grad, bf16 ? 8 : 16);
     const int vec_rows = vec && t.cols % 4 == 0;
-    for (int64_t at = 0; at < t.count; at += at_once) {
-      const unsigned n = static_cast<unsigned>(std::min<int64_t>(t.count - at, at_once));
-      a.m = t.momentum + at * size;
-      a.grad = static_cast<const uint8_t*>(t.grad) + at * size * (bf16 ? 2 : 4);
+    for (int64_t at = 0; at < p.count; at += at_once) {
+      const unsigned n = static_cast<unsigned>(std::min<int64_t>(p.count - at, at_once));
+      a.m = t.momentum + (p.at + at) * size;
+      a.grad = static_cast<const uint8_t*>(t.grad) + (p.at + at) * size * (bf16 ? 2 : 4);
       float* part = sums + (z + at) * chunks;
       MOE_CUDA(launch_pdl(muon_momentum_kernel, dim3(chunks, n), dim3(kThreads), 0, c.st, a, size, chunk_of(s), vec,
                           part));
@@ -744,7 +766,7 @@ int32_t first_planes(const Call& c, const Group& g) {
                           static_cast<float>(c.o->eps), c.sc.x[0], g.planes(g.w.x) + (z + at) * s.mp * s.np,
                           rows_of(s) * s.np, s.mp, s.np));
     }
-    z += t.count;
+    z += p.count;
   }
   return MOE_OK;
 }
@@ -901,11 +923,34 @@ int32_t check_call(const moe_muon_tensor* t, int32_t count, const moe_muon_optio
   return MOE_OK;
 }
 
+// (More matrices than any GPU holds: a slice's indices stay within 32 bits.)
 int32_t check_group(const Shape& s) {
-  if (2 * s.batch * s.mp >= (int64_t(1) << 31) || s.batch * chunks_of(s) >= (int64_t(1) << 31) ||
-      s.batch * dense::cdiv(s.mp, 128) * dense::cdiv(s.np, 128) >= (int64_t(1) << 31))
+  if (2 * s.all * s.mp >= (int64_t(1) << 31) || s.all * chunks_of(s) >= (int64_t(1) << 31) ||
+      s.all * dense::cdiv(s.mp, 128) * dense::cdiv(s.np, 128) >= (int64_t(1) << 31))
     return entry_fail(MOE_ERR_UNSUPPORTED, "too many matrices of %d x %d", s.m, s.n);
   return MOE_OK;
+}
+
+// A slice is as many matrices as this much workspace holds, and one at least.  All at once
+// take as much as they are many (256 experts' 768 of 2048 x 1024: 27.8 GiB) and gain what a
+// slice's last rounds of tiles leave idle: 768 of 2048 x 1024 62.6 ms at once, in slices of 4 GiB
+// 63.5, of 2 65.4, of 1 68.9; 96 of 2048 x 7168 67.2 / 68.2 / 69.7 / 72.3; 1600 of 512 x 512
+// 18.3 / 18.8 / 19.6 / 20.9.
+constexpr size_t kSliceBytes = size_t(4) << 30;
+// The slice that follows `s` (batch 0: the first); false: none.
+bool next_slice(Shape* s) {
+  if (s->batch == 0) {
+    Shape one = *s;
+    one.batch = 1;
+    one.each = dense::kPlanPairs;   // (without the shares that few matrices' sums are split into, some MB)
+    const int64_t most = std::max<int64_t>(1, kSliceBytes / group_ws(one).total);
+    s->each = dense::cdiv(s->all, dense::cdiv(s->all, most));
+    s->first = 0;
+  } else {
+    s->first += s->batch;
+  }
+  s->batch = std::min(s->each, s->all - s->first);
+  return s->batch > 0;
 }
 
 // The next group at or after tensor *i, whose first tensor it is; false: none.
@@ -917,16 +962,16 @@ bool next_shape(const moe_muon_tensor* t, int32_t count, int32_t* i, Shape* s) {
     for (int j = 0; j < *i && !seen; ++j) seen = same(t[j], *s);
     if (seen) continue;
     for (int j = *i; j < count; ++j)
-      if (same(t[j], *s)) s->batch += t[j].count;
+      if (same(t[j], *s)) s->all += t[j].count;
     ++*i;
     return true;
   }
   return false;
 }
 
-// Calls f with each set of groups that share their launches (and the bytes that
-// they need), in the order of their first tensors: as many as kMostGroups and
-// the memory of the largest group, or kSharedBytes, hold.  Stops at the first
+// Calls f with each set of slices that share their launches (and the bytes that
+// they need), in the order of their groups' first tensors: as many as kMostGroups and
+// the memory of the largest slice, or kSharedBytes, hold.  Stops at the first
 // error.
 constexpr size_t kSharedBytes = size_t(256) << 20;
 template <class F>
@@ -934,6 +979,7 @@ int32_t each_set(const moe_muon_tensor* t, int32_t count, F f) {
   size_t most = kSharedBytes;
   Shape s;
   for (int32_t i = 0; next_shape(t, count, &i, &s);) {
+    next_slice(&s);   // the others have no more matrices
     MOE_TRY(check_group(s));
     most = std::max(most, group_ws(s).total);
   }
@@ -941,15 +987,17 @@ int32_t each_set(const moe_muon_tensor* t, int32_t count, F f) {
   int n = 0;
   size_t bytes = 0;
   for (int32_t i = 0; next_shape(t, count, &i, &s);) {
-    const GroupWs w = group_ws(s);
-    if (n == kMostGroups || (n && bytes + w.total > most)) {
-      MOE_TRY(f(set, n, bytes));
-      n = 0;
-      bytes = 0;
+    while (next_slice(&s)) {
+      const GroupWs w = group_ws(s);
+      if (n == kMostGroups || (n && bytes + w.total > most)) {
+        MOE_TRY(f(set, n, bytes));
+        n = 0;
+        bytes = 0;
+      }
+      set[n].s = s;
+      set[n++].w = w;
+      bytes += w.total;
     }
-    set[n].s = s;
-    set[n++].w = w;
-    bytes += w.total;
   }
   return n ? f(set, n, bytes) : MOE_OK;
 }

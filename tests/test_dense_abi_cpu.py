@@ -197,6 +197,32 @@ def test_muon_workspace_is_shared(lib):
     assert size(tensor(count=5, rows=8, cols=1 << 20)) < 1 << 27
 
 
+GIB = 1 << 30
+
+
+@pytest.mark.parametrize("rows,cols", [(2048, 7168), (7168, 2048), (100, 1000), (65, 65), (512, 512), (384, 1 << 17)])
+def test_muon_workspace_does_not_grow_with_the_matrices(lib, rows, cols):
+    """Matrices of one shape run in slices of up to 4 GiB of workspace (one matrix at least), but for the shares of
+    few long sums (up to 38 of 256 x 256 floats a tile of the Gram matrix: 13 MB)."""
+    o = options()
+    size = lambda *t: step(lib, list(t), o, ws=None)[1]                          # noqa: E731
+    one = size(tensor(rows=rows, cols=cols))
+    sizes = [size(tensor(rows=rows, cols=cols, count=n)) for n in (2, 5, 30, 1000, 20000)]
+    assert all(0 < n <= max(one, 4 * GIB) + (16 << 20) for n in sizes)
+    assert max(sizes) > 2 * GIB
+    # several tensors of the shape, turned or not, are one group
+    assert size(*(tensor(rows=rows, cols=cols, count=400), tensor(rows=cols, cols=rows, count=600))) == sizes[3]
+
+
+def test_muon_workspace_of_a_model(lib):
+    """Shared experts of 61 layers, and the matrices of 256 experts."""
+    o = options()
+    layers = [tensor(rows=2048, cols=7168, count=2), tensor(rows=7168, cols=2048)] * 61
+    experts = [tensor(rows=2048, cols=7168, count=512), tensor(rows=7168, cols=2048, count=256)]
+    for t in (layers, experts):
+        assert 0 < step(lib, t, o, ws=None)[1] <= 4 * GIB + (16 << 20)
+
+
 def test_structures_match_the_header():
     """Sizes and offsets of the C structures, as a C compiler lays them out."""
     fields = {"moe_ffn_shape": L.FfnShape, "moe_muon_tensor": L.MuonTensor, "moe_muon_options": L.MuonOptions}
