@@ -655,7 +655,9 @@ struct Batch {
 int64_t blocks_of(const moe_muon_tensor& t, const Batch& b) { return (tiles_of(t) + b.tiles - 1) / b.tiles; }
 
 // The next batch of class mp at or after *at (a tensor's index); false: none.
-// Its blocks take as few tiles each as leaves all of them resident at once.
+// Its blocks take as few tiles each as leaves all of them resident at once; where
+// that would be more than twice their fair share (many matrices beside a longer one),
+// they take that, and the blocks that have no place at first follow the others.
 bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Batch* b) {
   b->count = 0;
   b->matrices = 0;
@@ -668,11 +670,16 @@ bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Ba
     all += t[*at].count * tiles_of(t[*at]);
     most = std::max(most, tiles_of(t[*at]));
   }
-  for (b->tiles = std::min(most, std::max<int64_t>(1, (all + kTargetBlocks - 1) / kTargetBlocks));; ++b->tiles) {
+  const int64_t fair = std::min(most, std::max<int64_t>(1, (all + kTargetBlocks - 1) / kTargetBlocks));
+  auto cut = [&](int64_t tiles) {
+    b->tiles = tiles;
     b->blocks = 0;
     for (int i = 0; i < b->count; ++i) b->blocks += t[b->index[i]].count * blocks_of(t[b->index[i]], *b);
-    if (b->blocks <= kTargetBlocks || b->tiles >= most) break;
-  }
+    return b->blocks <= kTargetBlocks;
+  };
+  int64_t tiles = fair;
+  while (!cut(tiles) && tiles < std::min(most, 2 * fair)) ++tiles;
+  if (b->blocks > kTargetBlocks) cut(fair);
   return b->count > 0;
 }
 

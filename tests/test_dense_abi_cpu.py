@@ -197,6 +197,17 @@ def test_muon_workspace_is_shared(lib):
     assert size(tensor(count=5, rows=8, cols=1 << 20)) < 1 << 27
 
 
+@pytest.mark.parametrize("count", [300, 304, 400, 3000])
+def test_muon_long_matrix_among_many(lib, count):
+    """A matrix of 2^20 columns is shared out to blocks by its length, however many matrices there are besides: each
+    block's sum of u u^T has a place in the workspace, beside a matrix's Q."""
+    o, place = options(), 4 * 64 * 64
+    size = lambda *t: step(lib, list(t), o, ws=None)[1]                          # noqa: E731
+    tiles = count * 112 + 16384                                                  # of 64 columns
+    blocks = count + 16384 * 304 // tiles // 2                                   # half of its fair share at least
+    assert size(tensor(rows=64, cols=7168, count=count), tensor(rows=64, cols=1 << 20)) >= place * (blocks + count + 1)
+
+
 GIB = 1 << 30
 
 
