@@ -50,7 +50,7 @@ struct Entry {
 };
 struct Table {
   Entry e[kCap];
-  int32_t count, matrices;
+  int32_t count;
   float decay;
 };
 
@@ -638,34 +638,64 @@ int size_class(const moe_muon_tensor& t) {
   return m <= 16 ? 16 : m <= 32 ? 32 : 64;
 }
 
-// A launch's tensors: those of one class from `at` on, as many as fit.  Returns
-// the blocks.
+bool of_class(const moe_muon_tensor& t, int mp) {
+  return !muon_empty(t) && muon_is_small(t) && size_class(t) == mp;
+}
+
 constexpr int64_t kMaxBlocks = int64_t(1) << 22;
 int64_t tiles_of(const moe_muon_tensor& t) {
   const int nc = 4096 / size_class(t);
   return (std::max(t.rows, t.cols) + nc - 1) / nc;
 }
 
+// Shared memory of a cluster's CTA that holds `tiles` of a matrix; a CTA has at most kWholeSm.
+constexpr int kHalfSm = 113 * 1024, kWholeSm = 227 * 1024;
+constexpr int kMaxRanks = 8;
+template <int MP>
+constexpr int64_t cluster_smem(int64_t tiles) {
+  return 4 * (cluster_scratch<MP>() + MP * (tiles * Cfg<MP>::NC + 4));
+}
+// Whether a cluster holds the tensor's matrices.
+bool is_resident(const moe_muon_tensor& t) {
+  const int64_t each = (tiles_of(t) + kMaxRanks - 1) / kMaxRanks;
+  const int mp = size_class(t);
+  return (mp == 16 ? cluster_smem<16>(each) : mp == 32 ? cluster_smem<32>(each) : cluster_smem<64>(each)) <= kWholeSm;
+}
+
+// A launch's tensors, of one class.
 struct Batch {
   int32_t index[kCap];
   int32_t count;
   int64_t matrices, blocks;
   int64_t tiles;   // of a block, at most
+  bool resident;   // clusters hold all of them
 };
+// Tensors that a cluster holds go with longer ones of their class through the three kernels,
+// which saves the cluster kernel's launch, unless they are more matrices than this.  Beside 8 x 70000,
+// together and apart: 48 of 16 x 4096 61 and 89 us, 300 265 / 196, 1000 744 / 467; 30 x 20000: 48 of 32 x 4096
+// 158 / 184, 300 515 / 565, 1000 1767 / 1662; 64 x 20000: 48 of 64 x 4096 351 / 650, 1000 5096 / 8327, 1000 of
+// 64 x 400 893 / 905.  (They also take no workspace apart: Q and the shares of many small matrices are
+// larger than these.)
+constexpr int64_t joined_matrices(int mp) { return mp == 16 ? 128 : mp == 32 ? 512 : INT64_MAX; }
+enum class Pick { kAll, kResident, kLonger };
 int64_t blocks_of(const moe_muon_tensor& t, const Batch& b) { return (tiles_of(t) + b.tiles - 1) / b.tiles; }
 
 // The next batch of class mp at or after *at (a tensor's index); false: none.
 // Its blocks take as few tiles each as leaves all of them resident at once; where
 // that would be more than twice their fair share (many matrices beside a longer one),
 // they take that, and the blocks that have no place at first follow the others.
-bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Batch* b) {
+bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, Pick pick, int32_t* at, Batch* b) {
   b->count = 0;
+  b->resident = true;
   b->matrices = 0;
   int64_t all = 0, most = 1;
   for (; *at < count && b->count < kCap; ++*at) {
-    if (muon_empty(t[*at]) || !muon_is_small(t[*at]) || size_class(t[*at]) != mp) continue;
+    if (!of_class(t[*at], mp)) continue;
+    const bool resident = is_resident(t[*at]);
+    if (pick != Pick::kAll && (pick == Pick::kResident) != resident) continue;
     if (b->count && b->matrices + t[*at].count > kMaxBlocks) break;
     b->index[b->count++] = *at;
+    b->resident = b->resident && resident;
     b->matrices += t[*at].count;
     all += t[*at].count * tiles_of(t[*at]);
     most = std::max(most, tiles_of(t[*at]));
@@ -682,6 +712,26 @@ bool next_batch(const moe_muon_tensor* t, int32_t count, int mp, int32_t* at, Ba
   if (b->blocks > kTargetBlocks) cut(fair);
   return b->count > 0;
 }
+// Calls f(class, batch) with all batches.  Stops at the first error.
+template <class F>
+int32_t each_batch(const moe_muon_tensor* t, int32_t count, F f) {
+  Batch b;
+  for (int mp : {16, 32, 64}) {
+    int64_t held = 0;
+    bool longer = false;
+    for (int i = 0; i < count; ++i) {
+      if (!of_class(t[i], mp)) continue;
+      if (is_resident(t[i])) held += t[i].count;
+      else longer = true;
+    }
+    const bool apart = longer && held > joined_matrices(mp);
+    for (Pick pick : {apart ? Pick::kResident : Pick::kAll, Pick::kLonger}) {
+      if (pick == Pick::kLonger && !apart) break;
+      for (int32_t at = 0; next_batch(t, count, mp, pick, &at, &b);) MOE_TRY(f(mp, b));
+    }
+  }
+  return MOE_OK;
+}
 
 // Whether all of a batch's tensors can be met in packs of four.
 bool in_fours(const moe_muon_tensor* t, const Batch& b, bool bf16) {
@@ -696,7 +746,6 @@ bool in_fours(const moe_muon_tensor* t, const Batch& b, bool bf16) {
 
 // How many clusters of 1 .. 8 CTAs are resident at once, with half of an SM's
 // memory a CTA and with all of it; asked once per kernel and device.
-constexpr int kHalfSm = 113 * 1024, kWholeSm = 227 * 1024;
 template <int MP, bool BF16, int V>
 cudaError_t resident_clusters(int ranks, bool whole, int* n) {
   static DeviceOnce table[16];
@@ -728,7 +777,6 @@ cudaError_t resident_clusters(int ranks, bool whole, int* n) {
 // time, by the rounds of resident clusters, each as long as its longest matrix
 // (measured element by element: 10, 14 or 40 us for the m x m steps and the
 // exchanges, 5, 7 or 12 us a tile; packs of four take about a tenth less of all).
-// 0 ranks: u does not fit into eight CTAs.
 struct ClusterPlan {
   int ranks, smem;
 };
@@ -737,9 +785,9 @@ cudaError_t cluster_plan(const moe_muon_tensor* t, const Batch& b, int64_t most_
   constexpr int64_t kOwn = MP == 16 ? 10 : MP == 32 ? 14 : 40, kTile = MP == 16 ? 5 : MP == 32 ? 7 : 12;
   *best = {0, 0};
   int64_t least = 0;
-  for (int ranks = 1; ranks <= 8; ++ranks) {
+  for (int ranks = 1; ranks <= kMaxRanks; ++ranks) {
     auto tiles = [&](int64_t all) { return (all + ranks - 1) / ranks; };
-    const int64_t smem = 4 * (cluster_scratch<MP>() + MP * (tiles(most_tiles) * Cfg<MP>::NC + 4));
+    const int64_t smem = cluster_smem<MP>(tiles(most_tiles));
     if (smem > kWholeSm || (ranks > 1 && ranks > most_tiles)) continue;
     int n;
     const cudaError_t e = resident_clusters<MP, BF16, V>(ranks, smem > kHalfSm, &n);
@@ -782,12 +830,8 @@ SmallWs small_ws(const Batch& b, int mp) {
 template <int MP, bool BF16, int V>
 int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_options* o, uint8_t* ws,
                   cudaStream_t st) {
-  const SmallWs w = small_ws(b, MP);
-  float* shares = reinterpret_cast<float*>(ws + w.shares);
-  float* qs = reinterpret_cast<float*>(ws + w.q);
   Table tab = {};
   tab.count = b.count;
-  tab.matrices = static_cast<int32_t>(b.matrices);
   tab.decay = muon_decay(o);
   int64_t blocks = 0, matrices = 0;
   for (int i = 0; i < b.count; ++i) {
@@ -807,13 +851,13 @@ int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_optio
     blocks += x.count * static_cast<int64_t>(e.blocks);
     matrices += x.count;
   }
-  int64_t most_tiles = 1;
-  for (int i = 0; i < b.count; ++i) most_tiles = std::max(most_tiles, tiles_of(t[b.index[i]]));
-  ClusterPlan plan;
-  MOE_CUDA((cluster_plan<MP, BF16, V>(t, b, most_tiles, &plan)));
   const float a = static_cast<float>(o->coefficients[0]), c1 = static_cast<float>(o->coefficients[1]),
               c2 = static_cast<float>(o->coefficients[2]), eps = static_cast<float>(o->eps);
-  if (plan.ranks) {
+  if (b.resident) {
+    int64_t most_tiles = 1;
+    for (int i = 0; i < b.count; ++i) most_tiles = std::max(most_tiles, tiles_of(t[b.index[i]]));
+    ClusterPlan plan;
+    MOE_CUDA((cluster_plan<MP, BF16, V>(t, b, most_tiles, &plan)));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(b.matrices * plan.ranks));
     cfg.blockDim = dim3(kThreads);
@@ -831,6 +875,9 @@ int32_t run_batch(const moe_muon_tensor* t, const Batch& b, const moe_muon_optio
     MOE_CUDA(cudaLaunchKernelEx(&cfg, muon_cluster_kernel<MP, BF16, V>, tab, sc));
     return MOE_OK;
   }
+  const SmallWs w = small_ws(b, MP);
+  float* shares = reinterpret_cast<float*>(ws + w.shares);
+  float* qs = reinterpret_cast<float*>(ws + w.q);
   const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   constexpr int kSteps = 3 * MP * Cfg<MP>::LDM * 4;
   static DeviceOnce once_first, once_next;
@@ -861,28 +908,27 @@ bool muon_is_small(const moe_muon_tensor& t) { return std::min(t.rows, t.cols) <
 
 size_t muon_small_ws(const moe_muon_tensor* t, int32_t count) {
   size_t need = 0;
-  Batch b;
-  for (int mp : {16, 32, 64})
-    for (int32_t at = 0; next_batch(t, count, mp, &at, &b);) need = std::max(need, small_ws(b, mp).total);
+  each_batch(t, count, [&](int mp, const Batch& b) -> int32_t {
+    if (!b.resident) need = std::max(need, small_ws(b, mp).total);
+    return MOE_OK;
+  });
   return need;
 }
 
 int32_t muon_small_step(const moe_muon_tensor* t, int32_t count, const moe_muon_options* o, uint8_t* ws,
                         cudaStream_t st) {
-  Batch b;
   const bool bf16 = o->grad_dtype == MOE_DTYPE_BF16;
-  auto run = [&](auto size) -> int32_t {
-    constexpr int MP = decltype(size)::value;
-    const bool four = in_fours(t, b, bf16);
-    return bf16 ? (four ? run_batch<MP, true, 4>(t, b, o, ws, st) : run_batch<MP, true, 1>(t, b, o, ws, st))
-                : (four ? run_batch<MP, false, 4>(t, b, o, ws, st) : run_batch<MP, false, 1>(t, b, o, ws, st));
-  };
-  for (int mp : {16, 32, 64})
-    for (int32_t at = 0; next_batch(t, count, mp, &at, &b);)
-      MOE_TRY(mp == 16   ? run(std::integral_constant<int, 16>())
-              : mp == 32 ? run(std::integral_constant<int, 32>())
-                         : run(std::integral_constant<int, 64>()));
-  return MOE_OK;
+  return each_batch(t, count, [&](int mp, const Batch& b) -> int32_t {
+    auto run = [&](auto size) -> int32_t {
+      constexpr int MP = decltype(size)::value;
+      const bool four = in_fours(t, b, bf16);
+      return bf16 ? (four ? run_batch<MP, true, 4>(t, b, o, ws, st) : run_batch<MP, true, 1>(t, b, o, ws, st))
+                  : (four ? run_batch<MP, false, 4>(t, b, o, ws, st) : run_batch<MP, false, 1>(t, b, o, ws, st));
+    };
+    return mp == 16   ? run(std::integral_constant<int, 16>())
+           : mp == 32 ? run(std::integral_constant<int, 32>())
+                      : run(std::integral_constant<int, 64>());
+  });
 }
 
 }  // namespace moe

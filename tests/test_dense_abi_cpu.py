@@ -208,6 +208,21 @@ def test_muon_long_matrix_among_many(lib, count):
     assert size(tensor(rows=64, cols=7168, count=count), tensor(rows=64, cols=1 << 20)) >= place * (blocks + count + 1)
 
 
+def test_muon_resident_matrices_take_no_workspace(lib):
+    """What stays in a cluster's shared memory has no sums in the workspace, whatever it stands beside."""
+    o = options()
+    size = lambda *t: step(lib, list(t), o, ws=None)[1]                          # noqa: E731
+    pools = [tensor(count=1 << 22, rows=1, cols=1), tensor(count=48, rows=16, cols=7168), tensor(count=48, rows=4096, cols=16),
+             tensor(count=500, rows=64, cols=4096), tensor(rows=8, cols=20000), tensor(count=70, rows=300, cols=33)]
+    for t in pools:
+        assert size(t) == 256
+    # ... but for few matrices that go with a longer one of their size
+    long = tensor(rows=8, cols=70000), tensor(rows=20, cols=40000)
+    assert size(*pools, *long) == size(*long) > 256
+    assert size(long[1], tensor(count=600, rows=300, cols=17)) == size(long[1])
+    assert size(long[0], tensor(count=9, rows=300, cols=16)) > size(long[0])
+
+
 GIB = 1 << 30
 
 

@@ -93,3 +93,41 @@ def test_long_matrix_among_many(cuda_ok):
         ref = M.orthogonal(grad.double(), 5, 1e-7)
         e32 = M.relative(M.orthogonal(grad, 5, 1e-7), ref)
         assert M.relative(got / M.factor("spectral", *s[-2:]), ref) <= 8 * e32 + s[-1] / 4 * 2.0 ** -24 + 2.0 ** -18
+
+
+@pytest.mark.parametrize("shapes", [[(150, 16, 400), (8, 70000), (5, 1000, 12), (16, 200)],
+                                    [(400, 32, 200), (2, 20, 40000), (150, 100, 20)]], ids=str)
+def test_many_short_beside_long(cuda_ok, shapes):
+    """Many matrices that stay in a cluster's shared memory, and one that is too long for it: neither changes a bit of
+    the other's step."""
+    grads = [M.inputs("strong", s, 5 + i) for i, s in enumerate(shapes)]
+
+    def run(which):
+        params = [M.inputs("noise", shapes[i], 3) for i in which]
+        op = P.Muon(params, [grads[i] for i in which], lr=0.02)
+        for _ in range(2):
+            op.step()
+        assert op.device_status() == 0
+        return {(i, k): t for k, group in enumerate((params, op.state)) for i, t in zip(which, group)}
+
+    every = range(len(shapes))
+    together = run(every)
+    for which in ([i for i in every if i != 1], [1]):
+        for at, got in run(which).items():
+            assert torch.equal(together[at], got), at
+
+
+@pytest.mark.parametrize("mp,long", [(16, (8, 70000)), (32, (2, 24, 20000)), (64, (64, 20000))])
+def test_few_short_beside_long(cuda_ok, mp, long):
+    """Few of them go with the long one: by the formula."""
+    shapes = [(3, mp, 400), long, (5, 1000, mp - 4), (mp, 200)]
+    grads = [M.inputs("strong", s, 5 + i) for i, s in enumerate(shapes)]
+    params = [torch.zeros(s, device="cuda") for s in shapes]
+    op = P.Muon(params, grads, lr=1.0, weight_decay=0.0, momentum=0.0, nesterov=False, update_scale="spectral")
+    op.step()
+    assert op.device_status() == 0
+    for p, grad, s in zip(params, grads, shapes):
+        ref = M.orthogonal(grad.double(), 5, 1e-7)
+        e32 = M.relative(M.orthogonal(grad, 5, 1e-7), ref)
+        bound = 8 * e32 + max(s[-2:]) / 4 * 2.0 ** -24 + 2.0 ** -18
+        assert M.relative(-p / M.factor("spectral", *s[-2:]), ref) <= bound, s
