@@ -733,16 +733,18 @@ int32_t each_batch(const moe_muon_tensor* t, int32_t count, F f) {
   return MOE_OK;
 }
 
-// Whether all of a batch's tensors can be met in packs of four.
-bool in_fours(const moe_muon_tensor* t, const Batch& b, bool bf16) {
-  for (int i = 0; i < b.count; ++i) {
-    const moe_muon_tensor& x = t[b.index[i]];
-    if (x.cols % 4 || !ptr_aligned(x.param, 16) || !ptr_aligned(x.momentum, 16) ||
-        !ptr_aligned(x.grad, bf16 ? 8 : 16) || !ptr_aligned(x.param_bf16, 8))
-      return false;
-  }
-  return true;
+// Whether the tensor can be met in packs of four.
+bool in_fours(const moe_muon_tensor& x, bool bf16) {
+  return x.cols % 4 == 0 && ptr_aligned(x.param, 16) && ptr_aligned(x.momentum, 16) &&
+         ptr_aligned(x.grad, bf16 ? 8 : 16) && ptr_aligned(x.param_bf16, 8);
 }
+// A launch meets its tensors in packs if it can all of them.  Beside ones that cannot be, matrices
+// of up to 16 rows in clusters have a launch of their own from this many tiles on (with 1 of 16 x 333,
+// one launch and two: 48 of 16 x 4096, 768 tiles, 41 and 46 us; 96 60 / 64; 48 of 16 x 7168 and 48 of
+// 4096 x 16, 2112 tiles, 97 / 91; 600 of 16 x 4096 325 / 267).  Those of up to 32 rows gain less: 48 of
+// 32 x 4096 113 / 127, 96 202 / 200.  (Both ways in one kernel, by tensor, cost registers: 81 -> 83 us for
+// the pools without an odd one, 40 of 64 x 4096 370 -> 425.)
+constexpr int64_t kPackedTiles = 2000;
 
 // How many clusters of 1 .. 8 CTAs are resident at once, with half of an SM's
 // memory a CTA and with all of it; asked once per kernel and device.
@@ -919,15 +921,31 @@ int32_t muon_small_step(const moe_muon_tensor* t, int32_t count, const moe_muon_
                         cudaStream_t st) {
   const bool bf16 = o->grad_dtype == MOE_DTYPE_BF16;
   return each_batch(t, count, [&](int mp, const Batch& b) -> int32_t {
-    auto run = [&](auto size) -> int32_t {
+    Batch part[2] = {b, b};   // element by element, in packs
+    part[0].count = part[1].count = 0;
+    part[0].matrices = part[1].matrices = 0;
+    int64_t packed = 0;
+    for (int i = 0; i < b.count; ++i) {
+      const moe_muon_tensor& x = t[b.index[i]];
+      const bool fours = in_fours(x, bf16);
+      Batch& to = part[fours];
+      to.index[to.count++] = b.index[i];
+      to.matrices += x.count;
+      if (fours) packed += x.count * tiles_of(x);
+    }
+    auto run = [&](auto size, const Batch& b, bool four) -> int32_t {
       constexpr int MP = decltype(size)::value;
-      const bool four = in_fours(t, b, bf16);
       return bf16 ? (four ? run_batch<MP, true, 4>(t, b, o, ws, st) : run_batch<MP, true, 1>(t, b, o, ws, st))
                   : (four ? run_batch<MP, false, 4>(t, b, o, ws, st) : run_batch<MP, false, 1>(t, b, o, ws, st));
     };
-    return mp == 16   ? run(std::integral_constant<int, 16>())
-           : mp == 32 ? run(std::integral_constant<int, 32>())
-                      : run(std::integral_constant<int, 64>());
+    auto send = [&](const Batch& b, bool four) -> int32_t {
+      return mp == 16   ? run(std::integral_constant<int, 16>(), b, four)
+             : mp == 32 ? run(std::integral_constant<int, 32>(), b, four)
+                        : run(std::integral_constant<int, 64>(), b, four);
+    };
+    if (!part[0].count || !part[1].count || !b.resident || mp > 16 || packed < kPackedTiles) return send(b, !part[0].count);
+    MOE_TRY(send(part[1], true));
+    return send(part[0], false);
   });
 }
 

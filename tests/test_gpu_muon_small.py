@@ -131,3 +131,32 @@ def test_few_short_beside_long(cuda_ok, mp, long):
         e32 = M.relative(M.orthogonal(grad, 5, 1e-7), ref)
         bound = 8 * e32 + max(s[-2:]) / 4 * 2.0 ** -24 + 2.0 ** -18
         assert M.relative(-p / M.factor("spectral", *s[-2:]), ref) <= bound, s
+
+
+def test_an_odd_tensor_beside_many(cuda_ok):
+    """One that cannot be met in packs: the others' step is the same to the bit, and takes no longer for it but for one
+    more launch (a quarter, when all went by single elements)."""
+    shapes = [(600, 16, 4096), (16, 333)]
+    grads = [M.inputs("strong", s, 5 + i) for i, s in enumerate(shapes)]
+
+    def run(which):
+        params = [M.inputs("noise", shapes[i], 3) for i in which]
+        op = P.Muon(params, [grads[i] for i in which], lr=0.02)
+        op.step()
+        first = [p.clone() for p in params]
+        times = []
+        for _ in range(5):
+            a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            a.record()
+            for _ in range(10):
+                op.step()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        assert op.device_status() == 0
+        return min(times), first
+
+    together, x = run([0, 1])
+    alone, pool = run([0])
+    assert torch.equal(x[0], pool[0]) and torch.equal(x[1], run([1])[1][0])
+    assert together <= 1.12 * alone, (together, alone)
