@@ -776,9 +776,13 @@ cudaError_t resident_clusters(int ranks, bool whole, int* n) {
 }
 
 // CTAs of a cluster, and their shared memory: the number that takes the least
-// time, by the rounds of resident clusters, each as long as its longest matrix
-// (measured element by element: 10, 14 or 40 us for the m x m steps and the
-// exchanges, 5, 7 or 12 us a tile; packs of four take about a tenth less of all).
+// time, by the rounds of resident clusters, each as long as its longest matrix:
+// 10, 14 or 40 us for the m x m steps and the exchanges, 5, 7 or 12 us a tile.  (These were
+// measured element by element on the CUDA cores; the present kernels take 7.5, 17 or 47 and 3.3, 4.9
+// or 8.  Of 28 batches of 1 to 1000 matrices, the sizes chosen so are within 3 % of the best of
+// all eight.)  The steps of 64 rows fill an SM's pipes, so that two CTAs on one take half
+// as long again: 100 of 64 x 1000 237 us in clusters of four, 325 in clusters of eight, two an SM; 18 of them
+// in clusters of six 69, of eight 98.
 struct ClusterPlan {
   int ranks, smem;
 };
@@ -791,9 +795,11 @@ cudaError_t cluster_plan(const moe_muon_tensor* t, const Batch& b, int64_t most_
     auto tiles = [&](int64_t all) { return (all + ranks - 1) / ranks; };
     const int64_t smem = cluster_smem<MP>(tiles(most_tiles));
     if (smem > kWholeSm || (ranks > 1 && ranks > most_tiles)) continue;
-    int n;
-    const cudaError_t e = resident_clusters<MP, BF16, V>(ranks, smem > kHalfSm, &n);
+    int n, apart;   // apart: with an SM to each CTA
+    cudaError_t e = resident_clusters<MP, BF16, V>(ranks, smem > kHalfSm, &n);
+    if (e == cudaSuccess) e = resident_clusters<MP, BF16, V>(ranks, true, &apart);
     if (e != cudaSuccess) return e;
+    const bool crowded = MP == 64 && smem <= kHalfSm && b.matrices > apart;
     int64_t time = 0, left = 0;   // left: places of the round in the making, whose longest is `longest`
     int64_t longest = 0;
     for (int i = 0; i < b.count; ++i) {
@@ -811,6 +817,7 @@ cudaError_t cluster_plan(const moe_muon_tensor* t, const Batch& b, int64_t most_
       }
     }
     time += longest;
+    if (crowded) time += time / 2;
     if (best->ranks && time >= least) continue;
     *best = {ranks, static_cast<int>(smem)};
     least = time;
