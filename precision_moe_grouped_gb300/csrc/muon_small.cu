@@ -21,7 +21,8 @@
 // 4096 x 16: 97 -> 86 us; 96 of 32 x 4096 212 -> 189).
 // All tensors of a size class go in one launch of each kernel.  Matrices that fit
 // into the shared memory of a cluster go through all of it in one kernel, which
-// reads and writes every tensor once; the three kernels are for longer ones.
+// reads and writes every tensor once; the three kernels are for longer ones, and for
+// few others beside them.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
