@@ -1,5 +1,6 @@
-"""The orthogonalised step's stated precision: X "as near to the formula as 32-bit
-arithmetic brings it, to a small factor", for long sums as for short ones.
+"""The orthogonalised step's precision for long sums as for short ones, on well spread,
+decaying and low-rank spectra.  (Nearly singular matrices of a few rows can be further off
+than this bound, whose e32 is one sample of the plain form's roundings.)
 
 test_gpu_muon.py's bound has a term that grows with n, the loss of an MMA that cuts
 off its sum over n terms.  The sums run in pieces instead, 128 terms in the large
