@@ -103,7 +103,7 @@ def test_rows_between_rows():
     """Against the set of bytes: two matrices of 16-byte pieces with any strides and distances."""
     rng = random.Random(0)
     said = [0, 0]
-    for _ in range(4000):
+    for _ in range(1000):
         T, width = rng.randint(1, 7), rng.randint(1, 4)
         ld_x, ld_out = (width + rng.choice([0, 0, 1, 2, 3, 5, 9]) for _ in range(2))
         if rng.random() < 0.5:
@@ -115,4 +115,4 @@ def test_rows_between_rows():
         rc = forward(T, x=X, ld_x=8 * ld_x, out=X + 16 * d, ld_out=8 * ld_out, hidden=8 * width)
         assert (refused(rc) if meet else passed(rc)), (T, width, ld_x, ld_out, d)
         said[meet] += 1
-    assert min(said) > 500
+    assert min(said) > 150
